@@ -21,7 +21,7 @@ __all__ = [
     "CB_ERR_TIMEOUT", "CB_ERR_CUDA", "CbDims", "CbOptions", "library", "library_path",
     "kv_append", "ragged_paged_attention", "workspace_size", "get_device_error",
     "check_device_error", "status_string", "copy_blocks", "kv_offload", "kv_restore",
-    "append_attention", "selftest_wait_timeout",
+    "append_attention", "selftest_wait_timeout", "CbRope", "rope_append",
 ]
 
 CB_OK = 0
@@ -56,6 +56,14 @@ class CbOptions(ctypes.Structure):
                 ("reserved", ctypes.c_int64 * 3)]
 
 
+class CbRope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_positions", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("reserved32", ctypes.c_int32), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("reserved", ctypes.c_int64 * 2)]
+
+
 class CbError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str = ""):
         self.status = status
@@ -83,6 +91,9 @@ def _declare(lib: ctypes.CDLL) -> None:
                                  ctypes.POINTER(CbDims), _P]
     attn = [_P, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_float, _P, _P, _P, ctypes.c_size_t,
             ctypes.POINTER(CbDims)]
+    lib.cb_rope_append.restype = ctypes.c_int
+    lib.cb_rope_append.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int32,
+                                   ctypes.POINTER(CbRope), ctypes.POINTER(CbDims), _P]
     lib.cb_ragged_paged_attention.restype = ctypes.c_int
     lib.cb_ragged_paged_attention.argtypes = attn + [_P]
     lib.cb_ragged_paged_attention_ex.restype = ctypes.c_int
@@ -255,6 +266,93 @@ def kv_append(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens
                                 _ptr(block_table), _ptr(cu_seqlens_q), _ptr(kv_lens),
                                 int(block_size), ctypes.byref(dims), _stream(stream))
     _check(st, "cb_kv_append")
+
+
+def _rows_stride(name, t) -> int:
+    """Elements between the token rows of a bf16 [T, H, D] tensor whose rows are contiguous (a
+    view of a wider projection's output, for instance)."""
+    import torch
+    _require(t.dtype == torch.bfloat16, f"{name} must be bfloat16")
+    _require(t.is_cuda, f"{name} must be a CUDA tensor")
+    _require(t.dim() == 3, f"{name} must have 3 dimensions")
+    T, H, D = t.shape
+    step, head, elem = t.stride()
+    _require(T == 0 or (elem == 1 and (head == D or H == 1)),
+             f"{name} must have contiguous token rows")
+    return step if T > 1 else H * D
+
+
+def _on_current_device(*tensors) -> None:
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        _require(t is None or t.get_device() == dev,
+                 "every tensor must be on the current CUDA device")
+
+
+def _on_stream(stream):
+    """Context that makes `stream` (None: the current one) the stream of allocations made in it, so
+    that memory the call allocates is reused only after the work queued there."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(_stream(stream)))
+
+
+def _rope(q, k_new, v_new, cos_sin, interleaved) -> CbRope:
+    """cb_rope of the given tensors (the shapes of q, k_new and v_new are checked by the caller)."""
+    import torch
+    _require(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_cuda
+             and cos_sin.is_contiguous(),
+             "cos_sin must be a contiguous fp32 CUDA tensor [max_positions, rot_dim]")
+    return CbRope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), 0,
+                  0 if q is None else _rows_stride("q", q), _rows_stride("k_new", k_new),
+                  _rows_stride("v_new", v_new))
+
+
+def rope_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
+                cos_sin, interleaved: bool = False, q_out=None, stream=None):
+    """kv_append with the rotary position embedding applied on the way (cb_rope_append): rotates
+    q [T, Hq, D] and k_new [T, Hkv, D] by their positions' rows of cos_sin fp32 [max_positions,
+    rot_dim] (rot_dim / 2 cosines, then the sines), writes k_new rotated and v_new to their cache
+    slots and returns q rotated, [T, Hq, D] contiguous (q_out; q itself rotates in place).  q,
+    k_new and v_new may be views with other token strides; q None: keys and values only.
+
+        pos = torch.arange(max_positions, dtype=torch.float64, device="cuda")
+        freq = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device="cuda") / rot_dim)
+        ang = pos[:, None] * freq
+        cos_sin = torch.cat((ang.cos(), ang.sin()), 1).float()
+    """
+    import torch
+    rope = _rope(q, k_new, v_new, cos_sin, interleaved)
+    _check_bf16("k_pages", k_pages, 4)
+    _check_bf16("v_pages", v_pages, 4)
+    S = _check_meta(block_table, cu_seqlens_q, kv_lens)
+    T, Hkv, D = k_new.shape
+    Hq = Hkv
+    _require(v_new.shape == k_new.shape, "v_new must match k_new")
+    _require(k_pages.shape[1:] == (block_size, Hkv, D), "k_pages must be [P, block_size, Hkv, D]")
+    _require(k_pages.shape == v_pages.shape, "v_pages must match k_pages")
+    if q is not None:
+        Hq = q.shape[1]
+        _require(q.shape == (T, Hq, D), "q must be [T, Hq, D]")
+        if q_out is None:
+            with _on_stream(stream):
+                q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        _check_bf16("q_out", q_out, 3)
+        _require(q_out.shape == (T, Hq, D), "q_out must be [T, Hq, D]")
+    else:
+        _require(q_out is None, "q_out without q")
+    _on_current_device(q, k_new, v_new, q_out, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                       cos_sin)
+    dims = CbDims(S, T, Hq, Hkv, D, k_pages.shape[0], block_table.shape[1])
+    _check(library().cb_rope_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(q_out), _ptr(k_pages),
+                                    _ptr(v_pages), _ptr(block_table), _ptr(cu_seqlens_q),
+                                    _ptr(kv_lens), int(block_size), ctypes.byref(rope),
+                                    ctypes.byref(dims), _stream(stream)), "cb_rope_append")
+    return q_out
 
 
 def workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, num_tokens) -> int:

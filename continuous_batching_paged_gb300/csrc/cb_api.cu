@@ -148,6 +148,72 @@ cb_status check_dims(const cb_dims* d, int32_t block_size) {
   return CB_OK;
 }
 
+cb::AppendArgs append_args(const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                           const int32_t* block_table, const int32_t* cu_seqlens_q,
+                           const int32_t* kv_lens, int32_t block_size, const cb_dims* dims) {
+  cb::AppendArgs a;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.block_table = block_table;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.kv_lens = kv_lens;
+  a.S = dims->num_seqs;
+  a.T = dims->num_tokens;
+  a.Hkv = dims->num_kv_heads;
+  a.D = dims->head_dim;
+  a.bs = block_size;
+  a.max_blocks = dims->max_blocks_per_seq;
+  a.P = dims->num_pages;
+  a.err = nullptr;  // set to the device's error word at launch
+  return a;
+}
+
+// Checks of cb_rope and of the tensors it applies to (non-empty batch), and the kernel's arguments.
+cb_status rope_args(const void* q, void* q_out, const cb_rope* rope, const cb::AppendArgs& ap,
+                    int Hq, cb::RopeArgs* out) {
+  if (rope == nullptr) return fail(CB_ERR_INVALID_ARG, "rope is NULL");
+  if ((q == nullptr) != (q_out == nullptr) || !ap.k_new || !ap.v_new || !ap.k_pages ||
+      !ap.v_pages || !ap.block_table || !ap.cu_seqlens_q || !ap.kv_lens || !rope->cos_sin)
+    return fail(CB_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(ap.k_new) || !aligned16(ap.v_new) ||
+      !aligned16(ap.k_pages) || !aligned16(ap.v_pages) || !aligned16(rope->cos_sin))
+    return fail(CB_ERR_INVALID_ARG, "q, K/V tensors and cos_sin must be 16-byte aligned");
+  if (rope->max_positions < 1) return fail(CB_ERR_INVALID_ARG, "max_positions must be >= 1");
+  if (rope->rot_dim < 16 || rope->rot_dim > ap.D || rope->rot_dim % 16 != 0)
+    return fail(CB_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [16, %d], got %d", ap.D,
+                rope->rot_dim);
+  if (rope->interleaved != 0 && rope->interleaved != 1)
+    return fail(CB_ERR_INVALID_ARG, "interleaved must be 0 or 1, got %d", rope->interleaved);
+  cb::RopeArgs r;
+  r.ap = ap;
+  r.q = q;
+  r.q_out = q_out;
+  r.cos_sin = rope->cos_sin;
+  r.Hq = Hq;
+  r.max_positions = rope->max_positions;
+  r.rot_dim = rope->rot_dim;
+  r.interleaved = rope->interleaved;
+  r.parts = 1;
+  const long long row_q = (long long)Hq * ap.D, row_kv = (long long)ap.Hkv * ap.D;
+  r.q_stride = rope->q_stride == 0 ? row_q : rope->q_stride;
+  r.k_stride = rope->k_stride == 0 ? row_kv : rope->k_stride;
+  r.v_stride = rope->v_stride == 0 ? row_kv : rope->v_stride;
+  if ((q != nullptr && (r.q_stride < row_q || r.q_stride % 8 != 0)) || r.k_stride < row_kv ||
+      r.k_stride % 8 != 0 || r.v_stride < row_kv || r.v_stride % 8 != 0)
+    return fail(CB_ERR_INVALID_ARG,
+                "token strides must be multiples of 8 elements and at least one row");
+  if (q != nullptr && !(q == q_out && (r.q_stride == row_q || ap.T == 1))) {
+    const char* q0 = static_cast<const char*>(q);
+    const char* o0 = static_cast<const char*>(q_out);
+    if (q0 < o0 + 2 * row_q * ap.T && o0 < q0 + 2 * (r.q_stride * (ap.T - 1) + row_q))
+      return fail(CB_ERR_INVALID_ARG, "q_out overlaps q (allowed: q_out == q, q contiguous)");
+  }
+  *out = r;
+  return CB_OK;
+}
+
 // 3-D bf16 tensor map with 128-byte swizzle and a box of 64 x box1 x box2 elements.
 cb_status encode_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                      uint64_t s1_bytes, uint64_t s2_bytes, uint32_t box1, uint32_t box2) {
@@ -221,24 +287,34 @@ cb_status cb_kv_append(const void* k_new, const void* v_new, void* k_pages, void
   DeviceState* ds = nullptr;
   st = device_state(&ds);
   if (st != CB_OK) return st;
-  cb::AppendArgs a;
-  a.k_new = k_new;
-  a.v_new = v_new;
-  a.k_pages = k_pages;
-  a.v_pages = v_pages;
-  a.block_table = block_table;
-  a.cu_seqlens_q = cu_seqlens_q;
-  a.kv_lens = kv_lens;
-  a.S = dims->num_seqs;
-  a.T = dims->num_tokens;
-  a.Hkv = dims->num_kv_heads;
-  a.D = dims->head_dim;
-  a.bs = block_size;
-  a.max_blocks = dims->max_blocks_per_seq;
-  a.P = dims->num_pages;
+  cb::AppendArgs a = append_args(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                                 block_size, dims);
   a.err = ds->err;
   cudaError_t e = cb::launch_kv_append(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
+  return CB_OK;
+}
+
+cb_status cb_rope_append(const void* q, const void* k_new, const void* v_new, void* q_out,
+                         void* k_pages, void* v_pages, const int32_t* block_table,
+                         const int32_t* cu_seqlens_q, const int32_t* kv_lens, int32_t block_size,
+                         const cb_rope* rope, const cb_dims* dims, void* stream) {
+  t_last_error.clear();
+  cb_status st = check_dims(dims, block_size);
+  if (st != CB_OK) return st;
+  if (dims->num_tokens == 0 || dims->num_seqs == 0) return CB_OK;  // no token but padding rows
+  cb::RopeArgs r;
+  st = rope_args(q, q_out, rope,
+                 append_args(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                             block_size, dims),
+                 dims->num_q_heads, &r);
+  if (st != CB_OK) return st;
+  DeviceState* ds = nullptr;
+  st = device_state(&ds);
+  if (st != CB_OK) return st;
+  r.ap.err = ds->err;
+  cudaError_t e = cb::launch_rope_append(r, ds->sm_count, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope_append launch");
   return CB_OK;
 }
 
@@ -409,22 +485,8 @@ cb_status cb_append_attention(const void* k_new, const void* v_new, void* k_page
   if (!k_new || !v_new) return fail(CB_ERR_INVALID_ARG, "null pointer argument");
   if (!aligned16(k_new) || !aligned16(v_new))
     return fail(CB_ERR_INVALID_ARG, "K/V tensors must be 16-byte aligned");
-  cb::AppendArgs ap;
-  ap.k_new = k_new;
-  ap.v_new = v_new;
-  ap.k_pages = k_pages;
-  ap.v_pages = v_pages;
-  ap.block_table = block_table;
-  ap.cu_seqlens_q = cu_seqlens_q;
-  ap.kv_lens = kv_lens;
-  ap.S = dims->num_seqs;
-  ap.T = dims->num_tokens;
-  ap.Hkv = dims->num_kv_heads;
-  ap.D = dims->head_dim;
-  ap.bs = block_size;
-  ap.max_blocks = dims->max_blocks_per_seq;
-  ap.P = dims->num_pages;
-  ap.err = nullptr;  // set to the device's error word at launch
+  const cb::AppendArgs ap = append_args(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q,
+                                        kv_lens, block_size, dims);
   return attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, scale,
                    out, lse, workspace, workspace_bytes, dims, options, &ap, stream);
 }

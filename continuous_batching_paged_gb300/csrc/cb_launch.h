@@ -19,6 +19,18 @@ struct AppendArgs {
   uint32_t* err;
 };
 
+// The rotary append: what the plain append takes, plus q, its rotation, and the angles' table.
+// Token rows of q / k_new / v_new are q_stride / k_stride / v_stride elements apart.
+struct RopeArgs {
+  AppendArgs ap;
+  const void* q;     // NULL: keys are rotated and appended only
+  void* q_out;       // [T, Hq, D]; may be q itself where q is contiguous
+  const float* cos_sin;
+  int Hq, max_positions, rot_dim, interleaved;
+  long long q_stride, k_stride, v_stride;
+  int parts;         // warps that share one token's heads
+};
+
 struct AttnArgs {
   const void* q;
   void* out;
@@ -58,6 +70,7 @@ struct BlockMoveArgs {
 unsigned long long launch_context_id();
 
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_append(RopeArgs r, int sm_count, cudaStream_t stream);
 cudaError_t launch_block_move(const BlockMoveArgs& a, int sm_count, cudaStream_t stream);
 cudaError_t launch_wait_selftest(uint32_t* err, uint64_t limit_ns, uint64_t* waited_ns,
                                  cudaStream_t stream);

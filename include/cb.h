@@ -95,6 +95,48 @@ cb_status cb_kv_append(const void* k_new, const void* v_new, void* k_pages, void
                        void* stream);
 
 /*
+ * cb_rope_append -- cb_kv_append with the rotary position embedding applied on the way: the query
+ * and key rows of this step are rotated by their positions' angles, the keys (rotated) and the
+ * values (as they are) go to their cache slots, and the rotated queries to q_out, ready for the
+ * attention call.  One launch; nothing is rotated in the cache later.
+ *
+ * Token i of sequence s has position pos = ctx_s + i.  The first rot_dim elements of each query and
+ * key head are rot_dim / 2 pairs (x, y): elements (j, j + rot_dim / 2), or (2j, 2j + 1) when
+ * `interleaved`; with c = cos_sin[pos][j] and s = cos_sin[pos][rot_dim / 2 + j]
+ *     x' = x c - y s,   y' = y c + x s
+ * in fp32 (each product and sum rounded by itself), rounded once to bf16.  Elements rot_dim .. D-1
+ * are copied.  The table holds whatever angles (and factors on them) the model uses, so scaled and
+ * stretched variants need no other call.  (An addition of this library; the pages that describe
+ * the method leave the position embedding to the model.)
+ *
+ *   q, k_new, v_new  bf16, heads contiguous (Hq x D, Hkv x D); the rows of successive tokens
+ *                    q_stride / k_stride / v_stride elements apart, so that the three may be
+ *                    views of one projection's output.  q and q_out NULL: keys and values only.
+ *   q_out            bf16 [T, Hq, D] contiguous.  May be q itself where q is contiguous too;
+ *                    otherwise the two must not overlap (CB_ERR_INVALID_ARG).
+ * The other arguments, the padding rows and the errors are those of cb_kv_append; in addition a
+ * position >= max_positions is a device error (CB_ERR_OUT_OF_RANGE).  A token with a device error
+ * is skipped: neither its cache slot nor its row of q_out is written.
+ */
+typedef struct {
+  const float* cos_sin;    /* device fp32 [max_positions, rot_dim]: row p holds the rot_dim / 2
+                              cosines, then the rot_dim / 2 sines, of position p; 16-byte aligned */
+  int32_t max_positions;   /* rows of cos_sin, >= 1                                     */
+  int32_t rot_dim;         /* rotated elements of a head: a multiple of 16, 16 .. D     */
+  int32_t interleaved;     /* 0: pairs (j, j + rot_dim / 2); 1: pairs (2j, 2j + 1)      */
+  int32_t reserved32;
+  int64_t q_stride;        /* elements from one token's row to the next: a multiple of 8, at   */
+  int64_t k_stride;        /* least Hq * D (q) or Hkv * D (k_new, v_new); 0 = contiguous        */
+  int64_t v_stride;
+  int64_t reserved[2];
+} cb_rope;
+
+cb_status cb_rope_append(const void* q, const void* k_new, const void* v_new, void* q_out,
+                         void* k_pages, void* v_pages, const int32_t* block_table,
+                         const int32_t* cu_seqlens_q, const int32_t* kv_lens, int32_t block_size,
+                         const cb_rope* rope, const cb_dims* dims, void* stream);
+
+/*
  * cb_attention_workspace_size -- bytes of device scratch cb_ragged_paged_attention needs.
  * Pure host arithmetic on num_seqs, num_tokens, num_q_heads, num_kv_heads and head_dim (the
  * other fields of dims do not change the size and are not checked here); 0 when dims is NULL
