@@ -22,6 +22,7 @@ __all__ = [
     "kv_append", "ragged_paged_attention", "workspace_size", "get_device_error",
     "check_device_error", "status_string", "copy_blocks", "kv_offload", "kv_restore",
     "append_attention", "selftest_wait_timeout", "CbRope", "rope_append",
+    "CbPrefix", "shared_prefix_attention", "rope_append_attention", "prefix_workspace_size",
 ]
 
 CB_OK = 0
@@ -64,6 +65,12 @@ class CbRope(ctypes.Structure):
                 ("reserved", ctypes.c_int64 * 2)]
 
 
+class CbPrefix(ctypes.Structure):
+    _fields_ = [("prefix_group", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+                ("num_groups", ctypes.c_int32), ("reserved32", ctypes.c_int32),
+                ("reserved", ctypes.c_int64 * 2)]
+
+
 class CbError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str = ""):
         self.status = status
@@ -94,6 +101,15 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.cb_rope_append.restype = ctypes.c_int
     lib.cb_rope_append.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int32,
                                    ctypes.POINTER(CbRope), ctypes.POINTER(CbDims), _P]
+    lib.cb_prefix_workspace_size.restype = ctypes.c_size_t
+    lib.cb_prefix_workspace_size.argtypes = [ctypes.POINTER(CbDims), ctypes.c_int32]
+    lib.cb_shared_prefix_attention.restype = ctypes.c_int
+    lib.cb_shared_prefix_attention.argtypes = attn[:8] + [ctypes.POINTER(CbPrefix)] + attn[8:] + [
+        ctypes.POINTER(CbOptions), _P]
+    lib.cb_rope_append_attention.restype = ctypes.c_int
+    lib.cb_rope_append_attention.argtypes = [_P] * 9 + [
+        ctypes.c_int32, ctypes.c_float, ctypes.POINTER(CbRope), ctypes.POINTER(CbPrefix)] + attn[8:] + [
+        ctypes.POINTER(CbOptions), _P]
     lib.cb_ragged_paged_attention.restype = ctypes.c_int
     lib.cb_ragged_paged_attention.argtypes = attn + [_P]
     lib.cb_ragged_paged_attention_ex.restype = ctypes.c_int
@@ -157,8 +173,8 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # without the Stream object that torch.cuda.current_stream() makes (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -272,39 +288,84 @@ def _rows_stride(name, t) -> int:
     """Elements between the token rows of a bf16 [T, H, D] tensor whose rows are contiguous (a
     view of a wider projection's output, for instance)."""
     import torch
-    _require(t.dtype == torch.bfloat16, f"{name} must be bfloat16")
-    _require(t.is_cuda, f"{name} must be a CUDA tensor")
-    _require(t.dim() == 3, f"{name} must have 3 dimensions")
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.dim() != 3:
+        _require(t.dtype == torch.bfloat16, f"{name} must be bfloat16")
+        _require(t.is_cuda, f"{name} must be a CUDA tensor")
+        _require(False, f"{name} must have 3 dimensions")
     T, H, D = t.shape
     step, head, elem = t.stride()
-    _require(T == 0 or (elem == 1 and (head == D or H == 1)),
-             f"{name} must have contiguous token rows")
+    if T > 0 and (elem != 1 or (head != D and H > 1)):
+        _require(False, f"{name} must have contiguous token rows")
     return step if T > 1 else H * D
 
 
-def _on_current_device(*tensors) -> None:
-    import torch
-    dev = torch.cuda.current_device()
+def _plain(dtype, dev, *tensors) -> bool:
+    """Whether every tensor is contiguous, of the dtype and on CUDA device dev: the quick form of
+    the checks whose messages the functions above give (a call's checks cost as much host time as
+    its launch)."""
     for t in tensors:
-        _require(t is None or t.get_device() == dev,
-                 "every tensor must be on the current CUDA device")
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return True
+
+
+def _check_step(k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, Hkv, D):
+    """Checks of a step's pools and metadata; the number of sequences."""
+    import torch
+    dev = k_pages.get_device()
+    if not (dev >= 0 and _plain(torch.bfloat16, dev, k_pages, v_pages)
+            and _plain(torch.int32, dev, block_table, cu_seqlens_q, kv_lens)
+            and k_pages.dim() == 4 and block_table.dim() == 2):
+        _check_bf16("k_pages", k_pages, 4)
+        _check_bf16("v_pages", v_pages, 4)
+        _check_meta(block_table, cu_seqlens_q, kv_lens)
+    _require(dev == torch.cuda.current_device(), "every tensor must be on the current CUDA device")
+    S = kv_lens.numel()
+    if cu_seqlens_q.numel() != S + 1 or block_table.shape[0] != S:
+        _check_meta(block_table, cu_seqlens_q, kv_lens)
+    shape = k_pages.shape
+    _require(shape[1] == block_size and shape[2] == Hkv and shape[3] == D,
+             "k_pages must be [P, block_size, Hkv, D]")
+    _require(shape == v_pages.shape, "v_pages must match k_pages")
+    return S
+
+
+def _on_device(dev, *tensors) -> None:
+    for t in tensors:
+        _require(t is None or t.get_device() == dev, "every tensor must be on the same device")
 
 
 def _on_stream(stream):
-    """Context that makes `stream` (None: the current one) the stream of allocations made in it, so
-    that memory the call allocates is reused only after the work queued there."""
-    import contextlib
+    """Context that makes `stream` the stream of the allocations made in it, so that memory the call
+    allocates is reused only after the work queued there."""
     import torch
-    if stream is None:
-        return contextlib.nullcontext()
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
                              else torch.cuda.ExternalStream(_stream(stream)))
+
+
+def _new(shape, dtype, like, stream):
+    """A tensor beside `like`, its memory reused only after the work queued on `stream`."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with _on_stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _output(t, name, shape, like, stream):
+    """The caller's bf16 output tensor, checked, or a new one beside `like`."""
+    import torch
+    if t is None:
+        return _new(shape, torch.bfloat16, like, stream)
+    _check_bf16(name, t, len(shape))
+    _require(tuple(t.shape) == shape, f"{name} must be {list(shape)}")
+    return t
 
 
 def _rope(q, k_new, v_new, cos_sin, interleaved) -> CbRope:
     """cb_rope of the given tensors (the shapes of q, k_new and v_new are checked by the caller)."""
     import torch
-    _require(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_cuda
+    _require(cos_sin.dtype is torch.float32 and cos_sin.dim() == 2 and cos_sin.is_cuda
              and cos_sin.is_contiguous(),
              "cos_sin must be a contiguous fp32 CUDA tensor [max_positions, rot_dim]")
     return CbRope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), 0,
@@ -325,33 +386,25 @@ def rope_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv
         ang = pos[:, None] * freq
         cos_sin = torch.cat((ang.cos(), ang.sin()), 1).float()
     """
-    import torch
     rope = _rope(q, k_new, v_new, cos_sin, interleaved)
-    _check_bf16("k_pages", k_pages, 4)
-    _check_bf16("v_pages", v_pages, 4)
-    S = _check_meta(block_table, cu_seqlens_q, kv_lens)
     T, Hkv, D = k_new.shape
-    Hq = Hkv
+    S = _check_step(k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, Hkv, D)
     _require(v_new.shape == k_new.shape, "v_new must match k_new")
-    _require(k_pages.shape[1:] == (block_size, Hkv, D), "k_pages must be [P, block_size, Hkv, D]")
-    _require(k_pages.shape == v_pages.shape, "v_pages must match k_pages")
+    Hq = Hkv
     if q is not None:
         Hq = q.shape[1]
-        _require(q.shape == (T, Hq, D), "q must be [T, Hq, D]")
-        if q_out is None:
-            with _on_stream(stream):
-                q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-        _check_bf16("q_out", q_out, 3)
-        _require(q_out.shape == (T, Hq, D), "q_out must be [T, Hq, D]")
+        _require(q.shape[0] == T and q.shape[2] == D, "q must be [T, Hq, D]")
+        q_out = _output(q_out, "q_out", (T, Hq, D), q, stream)
     else:
         _require(q_out is None, "q_out without q")
-    _on_current_device(q, k_new, v_new, q_out, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
-                       cos_sin)
+    _on_device(k_pages.get_device(), q, k_new, v_new, q_out, block_table, cu_seqlens_q, kv_lens,
+               cos_sin)
     dims = CbDims(S, T, Hq, Hkv, D, k_pages.shape[0], block_table.shape[1])
-    _check(library().cb_rope_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(q_out), _ptr(k_pages),
-                                    _ptr(v_pages), _ptr(block_table), _ptr(cu_seqlens_q),
-                                    _ptr(kv_lens), int(block_size), ctypes.byref(rope),
-                                    ctypes.byref(dims), _stream(stream)), "cb_rope_append")
+    _check(library().cb_rope_append(_ptr(q), k_new.data_ptr(), v_new.data_ptr(), _ptr(q_out),
+                                    k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                                    cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), int(block_size),
+                                    ctypes.byref(rope), ctypes.byref(dims), _stream(stream)),
+           "cb_rope_append")
     return q_out
 
 
@@ -435,6 +488,118 @@ def append_attention(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_
     ragged_paged_attention."""
     return ragged_paged_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
                                   block_size, scale, k_new=k_new, v_new=v_new, **kwargs)
+
+
+def prefix_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, num_tokens,
+                          num_groups) -> int:
+    """Bytes of device workspace a call with shared prefixes on this batch shape needs
+    (cb_prefix_workspace_size; 0 for an invalid shape)."""
+    dims = _dims(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, 1, 1)
+    return int(library().cb_prefix_workspace_size(ctypes.byref(dims), int(num_groups)))
+
+
+def _step_tensors(q, dims, prefix_group, prefix_lens, out, lse, workspace, decode_ctas, serial,
+                  window, phase_events, stream):
+    """What an attention call with shared prefixes needs beside its inputs: cb_prefix (or None),
+    out, lse, workspace and cb_options, checked or made."""
+    import torch
+    T, S, Hq, D = dims.num_tokens, dims.num_seqs, dims.num_q_heads, dims.head_dim
+    dev = q.get_device()
+    prefix, NG = None, 0
+    if prefix_group is not None or prefix_lens is not None:
+        _require(prefix_group is not None and prefix_lens is not None,
+                 "prefix_group and prefix_lens go together")
+        _require(_plain(torch.int32, dev, prefix_group, prefix_lens),
+                 "prefix_group and prefix_lens must be contiguous int32 CUDA tensors on q's device")
+        _require(prefix_group.numel() == S, "prefix_group must have num_seqs entries")
+        NG = prefix_lens.numel()
+        prefix = CbPrefix(prefix_group.data_ptr(), prefix_lens.data_ptr(), NG)
+    out = _output(out, "out", (T, Hq, D), q, stream)
+    if lse is True:
+        lse = _new((T, Hq), torch.float32, q, stream)
+    elif lse is False:
+        lse = None
+    elif lse is not None:
+        _require(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (T, Hq),
+                 "lse must be a contiguous fp32 [T, Hq] tensor")
+    if workspace is None:
+        need = int(library().cb_prefix_workspace_size(ctypes.byref(dims), NG))
+        workspace = _new((max(need, 256),), torch.uint8, q, stream)
+    _require(workspace.dtype is torch.uint8 and workspace.is_contiguous(), "workspace must be uint8")
+    _on_device(dev, out, lse, workspace)
+    opts = CbOptions(int(decode_ctas), OPT_SERIAL if serial else 0)
+    opts.window = int(window)
+    if phase_events is not None:
+        _require(len(phase_events) == NUM_PHASE_EVENTS, f"need {NUM_PHASE_EVENTS} phase events")
+        handles = (ctypes.c_void_p * NUM_PHASE_EVENTS)(*[int(e.cuda_event) for e in phase_events])
+        _require(all(handles), "phase events must have been recorded once (created) before use")
+        opts.phase_events = ctypes.cast(handles, ctypes.POINTER(ctypes.c_void_p))
+    return prefix, out, lse, workspace, opts
+
+
+def shared_prefix_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
+                            scale, prefix_group, prefix_lens, out=None, lse=None, workspace=None,
+                            decode_ctas: int = 0, phase_events=None, serial: bool = False,
+                            stream=None):
+    """ragged_paged_attention for a batch whose sequences share prefixes: the attention over a
+    group's shared keys is computed once for the whole group (cb_shared_prefix_attention).
+
+    prefix_group int32 [num_seqs]: each sequence's group, or -1; prefix_lens int32 [num_groups]:
+    how many leading keys the members of a group have in common (the same blocks in their tables,
+    or blocks with the same content), at most each member's prior context.  Results are
+    ragged_paged_attention's within rounding; the other arguments are its.
+    """
+    import torch
+    if not (q.dtype is torch.bfloat16 and q.is_cuda and q.is_contiguous() and q.dim() == 3):
+        _check_bf16("q", q, 3)
+    T, Hq, D = q.shape
+    Hkv = k_pages.shape[2] if k_pages.dim() == 4 else 0
+    S = _check_step(k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, Hkv, D)
+    _on_device(k_pages.get_device(), q, block_table, cu_seqlens_q, kv_lens)
+    dims = CbDims(S, T, Hq, Hkv, D, k_pages.shape[0], block_table.shape[1])
+    _require(prefix_group is not None, "prefix_group must be given")
+    want_lse = lse is not None and lse is not False
+    prefix, out, lse, workspace, opts = _step_tensors(
+        q, dims, prefix_group, prefix_lens, out, lse, workspace, decode_ctas, serial, 0,
+        phase_events, stream)
+    _check(library().cb_shared_prefix_attention(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+        cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), int(block_size), float(scale),
+        ctypes.byref(prefix), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(),
+        ctypes.byref(dims), ctypes.byref(opts), _stream(stream)), "cb_shared_prefix_attention")
+    return (out, lse) if want_lse else out
+
+
+def rope_append_attention(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                          block_size, scale, cos_sin, interleaved: bool = False, prefix_group=None,
+                          prefix_lens=None, q_out=None, out=None, lse=None, workspace=None,
+                          decode_ctas: int = 0, phase_events=None, serial: bool = False,
+                          window: int = 0, stream=None):
+    """One layer's attention step (cb_rope_append_attention): rope_append, then
+    shared_prefix_attention on the rotated queries (ragged_paged_attention without groups), same
+    results, in two launches.  q_out: where the rotated queries go (default: a temporary)."""
+    rope = _rope(q, k_new, v_new, cos_sin, interleaved)
+    T, Hkv, D = k_new.shape
+    Hq = q.shape[1]
+    S = _check_step(k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, Hkv, D)
+    _require(q.shape[0] == T and q.shape[2] == D, "q must be [T, Hq, D]")
+    _require(v_new.shape == k_new.shape, "v_new must match k_new")
+    q_out = _output(q_out, "q_out", (T, Hq, D), q, stream)
+    _on_device(k_pages.get_device(), q, k_new, v_new, q_out, block_table, cu_seqlens_q, kv_lens,
+               cos_sin)
+    dims = CbDims(S, T, Hq, Hkv, D, k_pages.shape[0], block_table.shape[1])
+    want_lse = lse is not None and lse is not False
+    prefix, out, lse, workspace, opts = _step_tensors(
+        q_out, dims, prefix_group, prefix_lens, out, lse, workspace, decode_ctas, serial, window,
+        phase_events, stream)
+    _check(library().cb_rope_append_attention(
+        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
+        v_pages.data_ptr(), block_table.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
+        int(block_size), float(scale), ctypes.byref(rope),
+        None if prefix is None else ctypes.byref(prefix), out.data_ptr(), _ptr(lse),
+        workspace.data_ptr(), workspace.numel(), ctypes.byref(dims), ctypes.byref(opts),
+        _stream(stream)), "cb_rope_append_attention")
+    return (out, lse) if want_lse else out
 
 
 def get_device_error(stream=None) -> int:

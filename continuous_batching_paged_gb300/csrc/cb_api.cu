@@ -319,20 +319,28 @@ cb_status cb_rope_append(const void* q, const void* k_new, const void* v_new, vo
 }
 
 // The attention pass on `stream`: the planner, then the attention kernel (decode and chunk
-// passes in one launch); with `app` non-NULL the KV-append of the same step shares the
-// planner's launch.
+// passes in one launch); with `app` (or `rope`) non-NULL the KV-append (rotary append) of the same
+// step shares the planner's launch; with `prefix` non-NULL and groups in it, shared prefixes are
+// computed once.
 static cb_status attention(const void* q, const void* k_pages, const void* v_pages,
                            const int32_t* block_table, const int32_t* cu_seqlens_q,
                            const int32_t* kv_lens, int32_t block_size, float scale, void* out,
                            float* lse, void* workspace, size_t workspace_bytes,
                            const cb_dims* dims, const cb_options* options,
-                           const cb::AppendArgs* app, void* stream) {
+                           const cb::AppendArgs* app, const cb::RopeArgs* rope,
+                           const cb_prefix* prefix, void* stream) {
   cb_status st = check_dims(dims, block_size);
   if (st != CB_OK) return st;
   if (dims->num_tokens == 0) return CB_OK;
   if (dims->num_seqs == 0) return CB_OK;  // every token row is padding
   if (!q || !k_pages || !v_pages || !block_table || !cu_seqlens_q || !kv_lens || !out || !workspace)
     return fail(CB_ERR_INVALID_ARG, "null pointer argument");
+  const int NG = prefix != nullptr ? prefix->num_groups : 0;
+  if (NG < 0) return fail(CB_ERR_INVALID_ARG, "num_groups must be >= 0, got %d", NG);
+  if (NG > 0 && (!prefix->prefix_group || !prefix->prefix_lens))
+    return fail(CB_ERR_INVALID_ARG, "null pointer argument");
+  if (NG > 0 && options != nullptr && options->window > 0)
+    return fail(CB_ERR_UNSUPPORTED, "shared prefixes with a sliding window");
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
     return fail(CB_ERR_INVALID_ARG, "q, pages and out must be 16-byte aligned");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
@@ -341,7 +349,11 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
     return fail(CB_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   if (!(scale > 0.f) || scale != scale)
     return fail(CB_ERR_INVALID_ARG, "scale must be a positive finite number");
-  const size_t need = cb::ws_layout(dims->num_seqs, dims->num_tokens, dims->num_q_heads, dims->head_dim).total;
+  const int R = NG > 0 ? cb::pre_records(dims->num_seqs, dims->num_tokens) : dims->num_seqs;
+  const size_t need =
+      NG > 0 ? cb::pre_layout(R, dims->num_tokens, dims->num_q_heads, dims->num_kv_heads,
+                              dims->head_dim, NG).total
+             : cb::ws_layout(R, dims->num_tokens, dims->num_q_heads, dims->head_dim).total;
   if (workspace_bytes < need)
     return fail(CB_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
   const int Hq = dims->num_q_heads, Hkv = dims->num_kv_heads, G = Hq / Hkv;
@@ -384,6 +396,10 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   if (dctas > CB_MAX_DECODE_CTAS) dctas = CB_MAX_DECODE_CTAS;
   a.decode_ctas = dctas;
   a.prefill_ctas = ds->sm_count;
+  a.R = R;
+  a.prefix_group = NG > 0 ? prefix->prefix_group : nullptr;
+  a.prefix_lens = NG > 0 ? prefix->prefix_lens : nullptr;
+  a.NG = NG;
   a.window = options != nullptr ? options->window : 0;
   if (a.window < 0) return fail(CB_ERR_INVALID_ARG, "window must be >= 0, got %d", a.window);
   a.scale_log2 = scale * 1.4426950408889634f;
@@ -399,6 +415,11 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   if ((st = encode_map(&maps.k_chunk, k_pages, D, Hkv, rows, D * 2, D * 2 * Hkv, 1, a.KBp)) != CB_OK) return st;
   if ((st = encode_map(&maps.v_chunk, v_pages, D, Hkv, rows, D * 2, D * 2 * Hkv, 1, a.KBp)) != CB_OK) return st;
   if ((st = encode_map(&maps.q, q, D, Hq, (uint64_t)a.T, D * 2, D * 2 * Hq, 1, 128)) != CB_OK) return st;
+  CUtensorMap q_tok;  // one token's query heads of one KV head
+  if (NG > 0 && (st = encode_map(&q_tok, q, D, Hq, (uint64_t)a.T, D * 2, D * 2 * Hq, G, 1)) != CB_OK) return st;
+  auto launch_pass = [&](const cb::AttnArgs& x, cudaStream_t on) {
+    return NG > 0 ? cb::launch_prefix_attention(x, maps, q_tok, on) : cb::launch_attention(x, maps, on);
+  };
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* const* ev = options != nullptr ? options->phase_events : nullptr;
@@ -412,7 +433,17 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
     ap = *app;
     ap.err = ds->err;
   }
-  if (app != nullptr && !serial) {
+  cb::RopeArgs ra;
+  if (rope != nullptr) {
+    ra = *rope;
+    ra.ap.err = ds->err;
+  }
+  if (rope != nullptr && !serial) {
+    // One launch rotates, appends and plans, as below.
+    if ((e = mark(0)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord(phase event)");
+    if ((e = cb::launch_rope_plan(ra, a, ds->sm_count, s)) != cudaSuccess)
+      return cuda_fail(e, "rope append + plan launch");
+  } else if (app != nullptr && !serial) {
     // One launch appends the step's K/V rows and plans the attention pass (which reads only
     // the metadata, not the pages).
     if ((e = mark(0)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord(phase event)");
@@ -420,25 +451,27 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   } else {
     if (app != nullptr && (e = cb::launch_kv_append(ap, s)) != cudaSuccess)
       return cuda_fail(e, "kv_append launch");
+    if (rope != nullptr && (e = cb::launch_rope_append(ra, ds->sm_count, s)) != cudaSuccess)
+      return cuda_fail(e, "rope_append launch");
     if ((e = mark(0)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord(phase event)");
-    if ((e = cb::launch_plan(a, s)) != cudaSuccess) return cuda_fail(e, "plan launch");
+    if ((e = NG > 0 ? cb::launch_prefix_plan(a, s) : cb::launch_plan(a, s)) != cudaSuccess) return cuda_fail(e, "plan launch");
   }
   if ((e = mark(1)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord(phase event)");
   if (serial) {
     cb::AttnArgs d = a;
     d.decode_grid = a.decode_ctas * head_groups;
     d.prefill_ctas = 0;
-    if ((e = cb::launch_attention(d, maps, s)) != cudaSuccess) return cuda_fail(e, "attention launch");
+    if ((e = launch_pass(d, s)) != cudaSuccess) return cuda_fail(e, "attention launch");
     if ((e = mark(2)) != cudaSuccess || (e = mark(3)) != cudaSuccess)
       return cuda_fail(e, "cudaEventRecord(phase event)");
     cb::AttnArgs c = a;
     c.decode_grid = 0;
-    if ((e = cb::launch_attention(c, maps, s)) != cudaSuccess) return cuda_fail(e, "attention launch");
+    if ((e = launch_pass(c, s)) != cudaSuccess) return cuda_fail(e, "attention launch");
     if ((e = mark(4)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord(phase event)");
   } else {
     a.decode_grid = a.decode_ctas * head_groups;
     if ((e = mark(3)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord(phase event)");
-    if ((e = cb::launch_attention(a, maps, s)) != cudaSuccess) return cuda_fail(e, "attention launch");
+    if ((e = launch_pass(a, s)) != cudaSuccess) return cuda_fail(e, "attention launch");
     if ((e = mark(2)) != cudaSuccess || (e = mark(4)) != cudaSuccess)
       return cuda_fail(e, "cudaEventRecord(phase event)");
   }
@@ -469,7 +502,7 @@ cb_status cb_ragged_paged_attention_ex(const void* q, const void* k_pages, const
                                        const cb_options* options, void* stream) {
   t_last_error.clear();
   return attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, scale,
-                   out, lse, workspace, workspace_bytes, dims, options, nullptr, stream);
+                   out, lse, workspace, workspace_bytes, dims, options, nullptr, nullptr, nullptr, stream);
 }
 
 cb_status cb_append_attention(const void* k_new, const void* v_new, void* k_pages, void* v_pages,
@@ -488,7 +521,49 @@ cb_status cb_append_attention(const void* k_new, const void* v_new, void* k_page
   const cb::AppendArgs ap = append_args(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q,
                                         kv_lens, block_size, dims);
   return attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, scale,
-                   out, lse, workspace, workspace_bytes, dims, options, &ap, stream);
+                   out, lse, workspace, workspace_bytes, dims, options, &ap, nullptr, nullptr, stream);
+}
+
+size_t cb_prefix_workspace_size(const cb_dims* dims, int32_t num_groups) {
+  if (num_groups <= 0) return num_groups == 0 ? cb_attention_workspace_size(dims) : 0;
+  if (cb_attention_workspace_size(dims) == 0 || dims->num_q_heads / dims->num_kv_heads > 16) return 0;
+  return cb::pre_layout(cb::pre_records(dims->num_seqs, dims->num_tokens), dims->num_tokens,
+                        dims->num_q_heads, dims->num_kv_heads, dims->head_dim, num_groups).total;
+}
+
+cb_status cb_shared_prefix_attention(const void* q, const void* k_pages, const void* v_pages,
+                                     const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                     const int32_t* kv_lens, int32_t block_size, float scale,
+                                     const cb_prefix* prefix, void* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, const cb_dims* dims,
+                                     const cb_options* options, void* stream) {
+  t_last_error.clear();
+  if (prefix == nullptr) return fail(CB_ERR_INVALID_ARG, "prefix is NULL");
+  return attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, scale,
+                   out, lse, workspace, workspace_bytes, dims, options, nullptr, nullptr, prefix,
+                   stream);
+}
+
+cb_status cb_rope_append_attention(const void* q, const void* k_new, const void* v_new, void* q_out,
+                                   void* k_pages, void* v_pages, const int32_t* block_table,
+                                   const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                                   int32_t block_size, float scale, const cb_rope* rope,
+                                   const cb_prefix* prefix, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, const cb_dims* dims,
+                                   const cb_options* options, void* stream) {
+  t_last_error.clear();
+  cb_status st = check_dims(dims, block_size);
+  if (st != CB_OK) return st;
+  if (dims->num_tokens == 0 || dims->num_seqs == 0) return CB_OK;
+  if (!q || !q_out) return fail(CB_ERR_INVALID_ARG, "null pointer argument");
+  cb::RopeArgs r;
+  st = rope_args(q, q_out, rope,
+                 append_args(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                             block_size, dims),
+                 dims->num_q_heads, &r);
+  if (st != CB_OK) return st;
+  return attention(q_out, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, scale,
+                   out, lse, workspace, workspace_bytes, dims, options, nullptr, &r, prefix, stream);
 }
 
 cb_status cb_ragged_paged_attention(const void* q, const void* k_pages, const void* v_pages,

@@ -28,7 +28,7 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
 
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(AttnArgs a) {
   allow_dependent_launch();
-  plan_cta(a);
+  plan_cta<false>(a);
 }
 
 cudaError_t launch_plan(const AttnArgs& a, cudaStream_t stream) {
@@ -42,7 +42,7 @@ constexpr int kAppendPlanMaxChunks = 4;  // fits the 64 registers of a 1024-thre
 __global__ void __launch_bounds__(kPlanThreads, 1) append_plan_kernel(AppendArgs ap, AttnArgs a) {
   allow_dependent_launch();
   if (blockIdx.x == 0) {
-    plan_cta(a);
+    plan_cta<false>(a);
   } else {
     constexpr int kWarps = kPlanThreads / 32;
     append_tokens<kAppendPlanMaxChunks>(ap, (blockIdx.x - 1) * kWarps + (threadIdx.x >> 5),

@@ -8,21 +8,9 @@
 // planner's counter, so however many of them start early, every item runs once.  In one launch
 // the order of the two passes on the SMs is fixed by construction, where two kernels on two
 // streams would race for them: a chunk kernel dispatched first holds every SM until it ends.
-#include "cb_decode.cuh"
-#include "cb_prefill.cuh"
+#include "cb_attention.cuh"
 
 namespace cb {
-
-constexpr int kAttnThreads = kPrefillThreads;
-static_assert(32 * (kMaxDecodeHeadsPerCta + 1) <= kAttnThreads,
-              "the decode role fits in the chunk role's CTA");
-
-template <int D, int QS>
-struct AttnSmem {
-  static constexpr int kTotal = DecodeSmem<D, QS>::kTotal > PrefillSmem<D>::kTotal
-                                    ? DecodeSmem<D, QS>::kTotal
-                                    : PrefillSmem<D>::kTotal;
-};
 
 template <int D, int QS, bool kWin>
 __global__ void __launch_bounds__(kAttnThreads, 1)
@@ -32,22 +20,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                      const __grid_constant__ CUtensorMap kmap_chunk,
                      const __grid_constant__ CUtensorMap vmap_chunk) {
   extern __shared__ uint8_t smem_raw[];
-  // Launched as a programmatic dependent of the planner: CTAs may start while the planner's
-  // launch still runs; everything below reads the plan (and the appended K/V), so wait here
-  // for that launch to complete and its writes to be visible.  A no-op without the attribute.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int b = (int)blockIdx.x;
-  if (b < a.decode_grid) {
-    // Span of the decode role: first start and last end of any warp of a CTA with work (the
-    // chunk role stamps its own span inside prefill_cta).
-    PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.S, a.T, a.Hq, a.D).header);
-    const bool busy = hdr->dec_tiles > 0;
-    if (threadIdx.x == 0 && busy) atomicMin(&hdr->t_dec_start, global_ns());
-    decode_cta<D, QS>(a, &kmap_dec, &vmap_dec, smem_raw, b % a.decode_ctas, b / a.decode_ctas);
-    if ((threadIdx.x & 31) == 0 && busy) atomicMax(&hdr->t_dec_end, global_ns());
-    return;
-  }
-  prefill_cta<D, kWin>(a, &qmap, &kmap_chunk, &vmap_chunk, smem_raw);
+  attention_cta<D, QS, kWin, false>(a, &qmap, nullptr, &kmap_dec, &vmap_dec, &kmap_chunk,
+                                    &vmap_chunk, smem_raw);
 }
 
 template <int D, int QS, bool kWin>

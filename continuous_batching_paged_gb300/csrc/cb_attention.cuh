@@ -1,0 +1,48 @@
+// One CTA of an attention kernel: a decode-role CTA or a chunk-role CTA, by its index in the grid
+// (cb_attention.cu says how the two share the GPU).
+#pragma once
+
+#include "cb_decode.cuh"
+#include "cb_prefill.cuh"
+
+namespace cb {
+
+constexpr int kAttnThreads = kPrefillThreads;
+static_assert(32 * (kMaxDecodeHeadsPerCta + 1) <= kAttnThreads,
+              "the decode role fits in the chunk role's CTA");
+
+template <int D, int QS>
+struct AttnSmem {
+  static constexpr int kTotal = DecodeSmem<D, QS>::kTotal > PrefillSmem<D>::kTotal
+                                    ? DecodeSmem<D, QS>::kTotal
+                                    : PrefillSmem<D>::kTotal;
+};
+
+// kPre: the batch's shared prefixes are computed once per group (cb_prefix.cu); qmap_tok is the
+// tensor map that gathers a group's query rows (unused otherwise).
+template <int D, int QS, bool kWin, bool kPre>
+__device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorMap* qmap,
+                                              const CUtensorMap* qmap_tok,
+                                              const CUtensorMap* kmap_dec,
+                                              const CUtensorMap* vmap_dec,
+                                              const CUtensorMap* kmap_chunk,
+                                              const CUtensorMap* vmap_chunk, uint8_t* smem_raw) {
+  // Launched as a programmatic dependent of the planner: CTAs may start while the planner's
+  // launch still runs; everything below reads the plan (and the appended K/V), so wait here
+  // for that launch to complete and its writes to be visible.  A no-op without the attribute.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = (int)blockIdx.x;
+  if (b < a.decode_grid) {
+    // Span of the decode role: first start and last end of any warp of a CTA with work (the
+    // chunk role stamps its own span inside prefill_cta).
+    PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D).header);
+    const bool busy = hdr->dec_tiles > 0;
+    if (threadIdx.x == 0 && busy) atomicMin(&hdr->t_dec_start, global_ns());
+    decode_cta<D, QS, kPre>(a, kmap_dec, vmap_dec, smem_raw, b % a.decode_ctas, b / a.decode_ctas);
+    if ((threadIdx.x & 31) == 0 && busy) atomicMax(&hdr->t_dec_end, global_ns());
+    return;
+  }
+  prefill_cta<D, QS, kWin, kPre>(a, qmap, qmap_tok, kmap_chunk, vmap_chunk, smem_raw);
+}
+
+}  // namespace cb

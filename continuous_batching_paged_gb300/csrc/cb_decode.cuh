@@ -25,6 +25,8 @@
 // then add 2^(x_j - m') and 2^(x_j - m') v_j; x_j = scale * log2(e) * q.k_j.
 #pragma once
 
+#include <type_traits>
+
 #include "cb_common.cuh"
 #include "cb_launch.h"
 
@@ -42,7 +44,7 @@ template <int D, int QS>
 constexpr int decode_stages() { return 3 * QS * (128 / D); }
 constexpr uint32_t kInfoFirst = 1u, kInfoLast = 2u, kInfoComplete = 4u;
 
-struct StageInfo {
+struct StageInfoBase {
   int seq;       // sequence id
   int dec;       // index among decode sequences (partial-result slot = cta + dec)
   int tok;       // packed token index of the sequence's query
@@ -52,6 +54,12 @@ struct StageInfo {
   uint32_t flags;
   int p0, p1;    // the sequence's tile range [p0, p1) in the concatenated tile order
 };
+struct StageInfoPre : StageInfoBase {  // with shared prefixes
+  int pre_slot, pre_stride, pre_n;  // the prefix's partial results: first slot, slots between
+                                    // parts, parts (0: no prefix computed apart)
+};
+template <bool kPre>
+using StageInfo = std::conditional_t<kPre, StageInfoPre, StageInfoBase>;
 
 template <int D, int QS>
 struct DecodeSmem {
@@ -62,7 +70,7 @@ struct DecodeSmem {
   static constexpr int kStages = decode_stages<D, QS>();
   static constexpr int kBarOffset = kStages * kStageBytes;
   static constexpr int kInfoOffset = kBarOffset + 2 * kStages * 8;
-  static constexpr int kTotal = kInfoOffset + kStages * (int)sizeof(StageInfo) + 1024;
+  static constexpr int kTotal = kInfoOffset + kStages * (int)sizeof(StageInfoPre) + 1024;
 };
 
 // Largest CTA index c in [0, N) whose range start floor(c * n / N) is <= t.
@@ -75,22 +83,34 @@ __device__ __forceinline__ int cta_of_tile(long long t, long long n, int N) {
   return lo;
 }
 
-// One warp combines the partial (m, l, o) that CTAs cf..cl wrote for decode sequence `dec`
-// and query heads h0 .. h1 - 1 of KV head `kvh`'s group: M = max m_c, w_c = 2^(m_c - M),
+// Partial results of a sequence: the parts that decode CTAs wrote (slot first CTA + record, then one
+// further per CTA), and the parts of its prefix where the group's prefix was computed apart.
+struct Parts {
+  const float2* ml;
+  const float* o;
+  int cf, cl;               // decode CTAs cf .. cl hold a part
+  const float2* pre_ml;
+  const float* pre_o;
+  int pre_slot, pre_stride, pre_n;
+};
+
+// One warp combines the partial (m, l, o) of decode record `dec` (packed token `tok`) for query
+// heads h0 .. h1 - 1 of KV head `kvh`'s group, the prefix's parts first:
+// M = max m_c, w_c = 2^(m_c - M),
 // out = sum_c w_c o_c / sum_c w_c l_c, lse = (M + log2 sum_c w_c l_c) * ln 2.
 // Other CTAs wrote these parts: they are read through L2 (ld.global.cg), never from a stale L1
 // line.  Parts are taken kC at a time for kH heads at once, every (m, l) and o row of such a
 // batch loaded before any is used (lane i holds output columns PER i .. PER i + PER - 1), and
 // folded in with a running maximum: one L2 round trip per batch, so a sequence cut in two
 // merges 4 heads in one round trip.
-template <int D>
-__device__ __forceinline__ void merge_parts(const AttnArgs& a, const float2* part_ml,
-                                            const float* part_o, int dec, int tok, int kvh,
-                                            int cf, int cl, int h0, int h1, int lane) {
+template <int D, bool kPre>
+__device__ __forceinline__ void merge_parts(const AttnArgs& a, const Parts& p, int dec, int tok,
+                                            int kvh, int h0, int h1, int lane) {
   constexpr int PER = D / 32;  // output columns per lane: 4 (D = 128) or 2 (D = 64)
   constexpr int kH = 4, kC = 2;  // heads and parts in flight
   __nv_bfloat16* outg = static_cast<__nv_bfloat16*>(a.out);
-  const int nparts = cl - cf + 1;
+  const int pre_n = kPre ? p.pre_n : 0;
+  const int nparts = pre_n + p.cl - p.cf + 1;
   for (int r0 = h0; r0 < h1; r0 += kH) {
     float M[kH], Lsum[kH], acc[kH][PER];
 #pragma unroll
@@ -108,13 +128,15 @@ __device__ __forceinline__ void merge_parts(const AttnArgs& a, const float2* par
 #pragma unroll
         for (int cc = 0; cc < kC; ++cc) {
           const int head = kvh * a.G + r0 + hh;
-          const size_t slot = (size_t)(cf + c0 + cc) + dec;
+          const bool pre = kPre && c0 + cc < pre_n;
+          const size_t slot = pre ? (size_t)p.pre_slot + (size_t)(c0 + cc) * p.pre_stride
+                                  : (size_t)(p.cf + c0 + cc - pre_n) + dec;
           ml[hh][cc] = make_float2(-INFINITY, 0.f);
 #pragma unroll
           for (int i = 0; i < PER; ++i) v[hh][cc][i] = 0.f;
           if (r0 + hh < h1 && c0 + cc < nparts) {
-            ml[hh][cc] = __ldcg(part_ml + slot * a.Hq + head);
-            const float* po = part_o + (slot * a.Hq + head) * D + lane * PER;
+            ml[hh][cc] = __ldcg((pre ? p.pre_ml : p.ml) + slot * a.Hq + head);
+            const float* po = (pre ? p.pre_o : p.o) + (slot * a.Hq + head) * D + lane * PER;
             if constexpr (PER == 4) {
               const float4 x = __ldcg(reinterpret_cast<const float4*>(po));
               v[hh][cc][0] = x.x; v[hh][cc][1] = x.y; v[hh][cc][2] = x.z; v[hh][cc][3] = x.w;
@@ -162,9 +184,9 @@ __device__ __forceinline__ void merge_parts(const AttnArgs& a, const float2* par
 // P^T is moved from the S^T accumulator layout to the B-operand layout with movmatrix.  The warp
 // first loads every K and V fragment of the stage into registers and releases the stage before
 // computing, so the producer refills it sooner.
-template <int D, int QS>
+template <int D, int QS, bool kPre>
 __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase, uint32_t bar_full,
-                                               uint32_t bar_empty, const StageInfo* info, int c,
+                                               uint32_t bar_empty, const StageInfo<kPre>* info, int c,
                                                int hg, int warp, long long n_my, long long ntiles,
                                                int N, const WsLayout& L, int lane) {
   using SM = DecodeSmem<D, QS>;
@@ -201,7 +223,7 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
       report(a.err, kErrTimeout);
       break;
     }
-    const StageInfo si = info[stage];
+    const StageInfo<kPre> si = info[stage];
     if (si.flags & kInfoFirst) {
 #pragma unroll
       for (int ht = 0; ht < NTH; ++ht) {
@@ -401,8 +423,11 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
         // one counter per (sequence, KV head, group of 8 query heads): with QS warps per KV
         // head, the last warp of each group merges that group's heads, the groups in parallel.
         // Counts only grow, so a counter already at parts - 1 leaves this warp the last (the
-        // fence makes its own part, read back through L2, visible to all its lanes).
-        int last = __shfl_sync(0xffffffffu, peek, 0) == cl - cf ? 1 : 0;
+        // fence makes its own part, read back through L2, visible to all its lanes).  A prefix
+        // computed apart counts once per part too (cb_prefill.cuh).
+        int others = cl - cf;  // parts besides this one
+        if constexpr (kPre) others += si.pre_n;
+        int last = __shfl_sync(0xffffffffu, peek, 0) == others ? 1 : 0;
         if (last) {
           __threadfence();
           __syncwarp();
@@ -411,13 +436,23 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
           __syncwarp();
           if (lane == 0)
             last = atomicAdd(merge_cnt + ((size_t)si.dec * a.Hkv + kvh) * QS + warp % QS, 1) ==
-                   cl - cf;
+                   others;
           last = __shfl_sync(0xffffffffu, last, 0);
           if (last) __threadfence();
         }
-        if (last)
-          merge_parts<D>(a, part_ml, part_o, si.dec, si.tok, kvh, cf, cl, qoff,
-                         qoff + 8 < a.G ? qoff + 8 : a.G, lane);
+        if (last) {
+          Parts p = {part_ml, part_o, cf, cl, nullptr, nullptr, 0, 0, 0};
+          if constexpr (kPre) {
+            const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.Hkv, a.D, a.NG);
+            p.pre_ml = reinterpret_cast<const float2*>(a.ws + PL.part_ml);
+            p.pre_o = reinterpret_cast<const float*>(a.ws + PL.part_o);
+            p.pre_slot = si.pre_slot;
+            p.pre_stride = si.pre_stride;
+            p.pre_n = si.pre_n;
+          }
+          merge_parts<D, kPre>(a, p, si.dec, si.tok, kvh, qoff, qoff + 8 < a.G ? qoff + 8 : a.G,
+                               lane);
+        }
       }
     }
   }
@@ -425,11 +460,11 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
 
 // The producer warp of a decode CTA (see decode_cta): walks the CTA's tile range and issues
 // the TMA copies of every tile's page runs into the stage ring.
-template <int D, int QS>
+template <int D, int QS, bool kPre>
 __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensorMap* kmap,
                                                const CUtensorMap* vmap, uint32_t sbase,
                                                uint32_t bar_full, uint32_t bar_empty,
-                                               StageInfo* info, const PlanHeader* hdr,
+                                               StageInfo<kPre>* info, const PlanHeader* hdr,
                                                const int4* dec_rec, int d_first, int c, int hg,
                                                int HB, long long t0, long long t1, int lane) {
   using SM = DecodeSmem<D, QS>;
@@ -453,11 +488,17 @@ __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensor
     const long long p0 = rec.w, p1 = dec_rec[d + 1].w;
     const int s = rec.x, tok = rec.y, kv = rec.z;
     // with a sliding window the sequence's tiles start at the one holding its first key
-    const int lo_key = window_first_key(kv - 1, a.window);
+    int lo_key = window_first_key(kv - 1, a.window);
+    int4 pre = make_int4(0, 0, 0, 0);
+    if constexpr (kPre) {  // and with a prefix computed apart, at the one holding its end
+      pre = reinterpret_cast<const int4*>(
+          a.ws + pre_layout(a.R, a.T, a.Hq, a.Hkv, a.D, a.NG).rec)[d];
+      lo_key = pre.x;
+    }
     const int first_tile_key = lo_key / kDecodeTileKeys * kDecodeTileKeys;
     const long long lo = t > p0 ? t : p0;
     const long long hi = t1 < p1 ? t1 : p1;
-    const bool complete = p0 >= t0 && p1 <= t1;
+    const bool complete = p0 >= t0 && p1 <= t1 && (!kPre || pre.w == 0);
     const int32_t* row = a.block_table + (size_t)s * a.max_blocks;
     // The consumers read this sequence's query rows (the CTA's head group) at its first tile,
     // a few stages from now: pull them into L2 so that the read does not wait on HBM.
@@ -497,7 +538,7 @@ __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensor
         if (want && !valid) report(a.err, kErrOutOfRange);
         const uint32_t nvalid = __popc(__ballot_sync(0xffffffffu, valid));
         if (lane == 0) {
-          StageInfo& si = info[stage];
+          StageInfo<kPre>& si = info[stage];
           si.seq = s;
           si.dec = d;
           si.tok = tok;
@@ -506,6 +547,11 @@ __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensor
           si.key0 = key0;
           si.p0 = (int)p0;
           si.p1 = (int)p1;
+          if constexpr (kPre) {
+            si.pre_slot = pre.y;
+            si.pre_stride = pre.z;
+            si.pre_n = pre.w;
+          }
           si.flags = (tile == lo ? kInfoFirst : 0u) | (tile == hi - 1 ? kInfoLast : 0u) |
                      (complete ? kInfoComplete : 0u);
           mbar_arrive_expect_tx(bar_full + 8 * stage,
@@ -535,7 +581,7 @@ __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensor
 // One CTA of the decode pass: CTA `bx` of the a.decode_ctas CTAs of KV-head group `hg`
 // (decode_kv_heads<QS>() KV heads per group).  Runs in the attention kernel (cb_attention.cu)
 // with that kernel's dynamic shared memory; uses 32 * (QS * HB + 1) of its threads.
-template <int D, int QS>
+template <int D, int QS, bool kPre>
 __device__ __forceinline__ void decode_cta(const AttnArgs& a, const CUtensorMap* kmap,
                                            const CUtensorMap* vmap, uint8_t* smem_raw, int bx,
                                            int hg) {
@@ -545,12 +591,12 @@ __device__ __forceinline__ void decode_cta(const AttnArgs& a, const CUtensorMap*
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar_full = sbase + SM::kBarOffset;              // kStages x 8 B
   const uint32_t bar_empty = bar_full + SM::kStages * 8;         // kStages x 8 B
-  StageInfo* info = reinterpret_cast<StageInfo*>(smem + SM::kInfoOffset);
+  StageInfo<kPre>* info = reinterpret_cast<StageInfo<kPre>*>(smem + SM::kInfoOffset);
 
   const int HB = a.Hkv < decode_kv_heads<QS>() ? a.Hkv : decode_kv_heads<QS>();
   const int n_cons = QS * HB;  // consumer warps; the producer is warp n_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const WsLayout L = ws_layout(a.S, a.T, a.Hq, a.D);
+  const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D);
   const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.ws + L.header);
   const int4* dec_rec = reinterpret_cast<const int4*>(a.ws + L.dec_rec);
   const int32_t* cta_first = reinterpret_cast<const int32_t*>(a.ws + L.cta_first);
@@ -575,11 +621,11 @@ __device__ __forceinline__ void decode_cta(const AttnArgs& a, const CUtensorMap*
   __syncthreads();
 
   auto produce = [&]() {
-    decode_produce<D, QS>(a, kmap, vmap, sbase, bar_full, bar_empty, info, hdr, dec_rec, d_first,
+    decode_produce<D, QS, kPre>(a, kmap, vmap, sbase, bar_full, bar_empty, info, hdr, dec_rec, d_first,
                           c, hg, HB, t0, t1, lane);
   };
   auto consume = [&]() {
-    decode_consume<D, QS>(a, sbase, bar_full, bar_empty, info, c, hg, warp, t1 - t0, ntiles, N,
+    decode_consume<D, QS, kPre>(a, sbase, bar_full, bar_empty, info, c, hg, warp, t1 - t0, ntiles, N,
                            L, lane);
   };
   if (warp == n_cons) produce();

@@ -48,6 +48,11 @@ struct AttnArgs {
                        // 0 when the launch runs the chunk pass only)
   int decode_auto;     // 1: the planner picks how many of them work (decode / chunk balance)
   int prefill_ctas;    // persistent CTAs of the chunk pass (0 when the launch runs decode only)
+  int R;               // decode records the workspace is laid out for (S; pre_records(S, T) with
+                       // shared prefixes)
+  const int32_t* prefix_group;  // [S]: the group whose prefix a sequence shares, or -1
+  const int32_t* prefix_lens;   // [NG]: keys of each group's prefix
+  int NG;                       // groups (0 without shared prefixes)
   int window;          // > 0: query at position p sees keys (p - window, p]; 0: all <= p
   float scale_log2;    // softmax scale * log2(e)
 };
@@ -83,7 +88,14 @@ cudaError_t launch_append_plan(const AppendArgs& ap, const AttnArgs& a, cudaStre
 struct AttnMaps {
   CUtensorMap q, k_dec, v_dec, k_chunk, v_chunk;
 };
+// The rotary append and the planner in one launch (with shared prefixes where a.NG > 0).
+cudaError_t launch_rope_plan(RopeArgs r, const AttnArgs& a, int sm_count, cudaStream_t stream);
 // The attention kernel: a.decode_grid decode-role CTAs, then a.prefill_ctas chunk-role CTAs.
 cudaError_t launch_attention(const AttnArgs& a, const AttnMaps& maps, cudaStream_t stream);
+// The planner and the attention kernel for a batch with shared prefixes (a.NG > 0); q_tok: Q as boxes of one token's query
+// heads of one KV head.
+cudaError_t launch_prefix_plan(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_prefix_attention(const AttnArgs& a, const AttnMaps& maps,
+                                    const CUtensorMap& q_tok, cudaStream_t stream);
 
 }  // namespace cb

@@ -71,7 +71,7 @@ __device__ __forceinline__ void block_scan4(int v[4], int ex[4], int tot[4], int
 // full warp; candidates
 // N = 4, 8, ... are spread over the lanes, in fp32 (the fp64 rate of this part is far too low
 // for even this much arithmetic on one thread).
-__device__ int choose_decode_ctas(float dec_bytes, float chunk_flops, int chunk_items,
+__device__ __forceinline__ int choose_decode_ctas(float dec_bytes, float chunk_flops, int chunk_items,
                                   int max_ctas, long long tiles) {
   const int lane = threadIdx.x & 31;
   if (tiles <= 0) return 1;
@@ -128,7 +128,7 @@ __device__ int choose_decode_ctas(float dec_bytes, float chunk_flops, int chunk_
 // more K/V tiles get lower bins, so an ascending walk over the bins is longest first.
 // With `lens` (shared memory: q_len and prior context of the i-th chunk sequence, interleaved)
 // the lengths need no global loads.
-__device__ int pf_unit_bin(const AttnArgs& a, const int32_t* pf_seq, const int32_t* pf_prefix,
+__device__ inline int pf_unit_bin(const AttnArgs& a, const int32_t* pf_seq, const int32_t* pf_prefix,
                            const int2* lens, int n_pf, int g) {
   int lo = 0, hi = n_pf - 1;  // largest i with pf_prefix[i] <= g
   while (lo < hi) {
@@ -151,17 +151,120 @@ __device__ int pf_unit_bin(const AttnArgs& a, const int32_t* pf_seq, const int32
   return kCostBins - 1 - min(tiles, kCostBins - 1);
 }
 
+// With shared prefixes: which groups' prefixes are computed once, as which work items.  Fills the
+// group list, the map from group number to it (-1: every member's own pass does it all) and zeroes
+// the count of tokens listed so far.  *pairs: the items' (query token, key) pairs, tile by tile.
+// Returns the number of items (the same in every thread).
+//
+// A group takes part when it has at least two query tokens (from members with at most kPreMaxQ
+// each) and kPreMinKeys keys; after bad metadata none does, and each sequence is computed alone.
+// Long prefixes are split into parts of equal K/V tiles so that all items together come to about
+// kPreItems; the bound on the partial results (pre_layout) rests on the rule len >= W / kPreItems.
+__device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], float* pairs) {
+  const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.Hkv, a.D, a.NG);
+  int32_t* cnt = reinterpret_cast<int32_t*>(a.ws + PL.cnt);
+  int32_t* first = reinterpret_cast<int32_t*>(a.ws + PL.first);
+  int32_t* map = reinterpret_cast<int32_t*>(a.ws + PL.map);
+  PreGroup* groups = reinterpret_cast<PreGroup*>(a.ws + PL.group);
+  PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D).header);
+  const int tid = threadIdx.x;
+  const long long max_kv = (long long)a.max_blocks * a.bs;
+  __shared__ unsigned long long s_work, s_items;
+  if (tid == 0) s_work = s_items = 0;
+  for (int g = tid; g < a.NG; g += kPlanThreads) {
+    cnt[g] = 0;
+    first[g] = 0x7fffffff;
+  }
+  __syncthreads();
+  bool bad = false;
+  for (int s = tid; s < a.S; s += kPlanThreads) {
+    const int c0 = a.cu_seqlens_q[s], c1 = a.cu_seqlens_q[s + 1], kv = a.kv_lens[s];
+    const int q_len = c1 - c0;
+    if (c0 < 0 || c1 > a.T || (s == 0 && c0 != 0) || q_len < 0 || kv < q_len || kv > max_kv) {
+      bad = true;  // reported with the lengths
+      continue;
+    }
+    const int g = a.prefix_group[s];
+    if (q_len == 0 || g == -1) continue;
+    const int keys = g >= 0 && g < a.NG ? a.prefix_lens[g] : -1;
+    if (keys < 0 || keys > kv - q_len) {
+      report(a.err, kErrOutOfRange);
+      bad = true;
+    } else if (q_len <= kPreMaxQ) {
+      atomicAdd(&cnt[g], q_len);
+      atomicMin(&first[g], s);
+    }
+  }
+  bad = __syncthreads_or(bad) != 0;
+  const int per_tile = pre_tile_tokens(a.G);
+  auto units_of = [&](int n_tok) { return (n_tok + 2 * per_tile - 1) / (2 * per_tile); };
+  auto shared_tokens = [&](int g) -> int {  // tokens of group g if its prefix is computed once
+    if (bad || g >= a.NG || cnt[g] < 2 || a.prefix_lens[g] < kPreMinKeys) return 0;
+    return cnt[g];
+  };
+  auto tiles_of = [&](int g) { return (a.prefix_lens[g] + kChunkKeys - 1) / kChunkKeys; };
+  float my_pairs = 0.f;
+  for (int g = tid; g < a.NG; g += kPlanThreads) {
+    const int n = shared_tokens(g);
+    if (n > 0) {
+      const unsigned long long items = (unsigned long long)units_of(n) * a.Hkv;
+      atomicAdd(&s_items, items);
+      atomicAdd(&s_work, items * tiles_of(g));
+      my_pairs += (float)(units_of(n) * 2 * per_tile) * (float)a.prefix_lens[g];
+    }
+  }
+  __syncthreads();
+  long long len = (long long)((s_work + kPreItems - 1) / kPreItems);
+  if (len < kPreMinTiles) len = kPreMinTiles;
+  if (s_items >= kPreItems || len > 0x7fffffff) len = 0x7fffffff;
+  int carry[4] = {0, 0, 0, 0};  // groups, tokens, items, slots
+  for (int base = 0; base < a.NG; base += kPlanThreads) {
+    const int g = base + tid;
+    const int n = shared_tokens(g);
+    int v[4] = {0, 0, 0, 0}, ex[4], tot[4], nsplit = 0, part = 0;
+    if (n > 0) {
+      const int nt = tiles_of(g);
+      nsplit = (int)((nt + len - 1) / len);
+      part = (nt + nsplit - 1) / nsplit;
+      nsplit = (nt + part - 1) / part;
+      v[0] = 1;
+      v[1] = n;
+      v[2] = units_of(n) * a.Hkv * nsplit;
+      v[3] = n * nsplit;
+    }
+    block_scan4(v, ex, tot, sw);  // (its barriers also part the reads of cnt from the writes)
+    if (g < a.NG) {
+      map[g] = n > 0 ? carry[0] + ex[0] : -1;
+      cnt[g] = 0;
+    }
+    if (n > 0)
+      groups[carry[0] + ex[0]] = {carry[2] + ex[2], n, carry[1] + ex[1], a.prefix_lens[g],
+                                  first[g], nsplit, part, carry[3] + ex[3]};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) carry[k] += tot[k];
+  }
+  if (tid == 0) {
+    hdr->pre_groups = carry[0];
+    hdr->pre_items = carry[2];
+  }
+  __syncthreads();
+  *pairs = my_pairs;
+  return carry[2];
+}
+
 // Batches of up to this many decode (or chunk) sequences keep the planner's prefix arrays in
 // shared memory as well, so its binary searches cost no global round trips.
 constexpr int kPlanSmemSeqs = 2048;
 
+// kPre: with shared prefixes (a.NG > 0).
+template <bool kPre>
 __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   static_assert(kCostBins == kPlanThreads, "one histogram bin per planner thread");
   __shared__ int sw[32][4];
   __shared__ int32_t s_dec_prefix[kPlanSmemSeqs + 1], s_pf_prefix[kPlanSmemSeqs + 1];
   __shared__ int32_t s_pf_seq[kPlanSmemSeqs];
   __shared__ int2 s_pf_lens[kPlanSmemSeqs];  // (q_len, prior context) of each chunk sequence
-  const WsLayout L = ws_layout(a.S, a.T, a.Hq, a.D);
+  const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D);
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + L.header);
   int32_t* dec_seq = reinterpret_cast<int32_t*>(a.ws + L.dec_seq);
   int32_t* dec_prefix = reinterpret_cast<int32_t*>(a.ws + L.dec_prefix);
@@ -173,6 +276,9 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   const long long max_kv = (long long)a.max_blocks * a.bs;
 
   float my_keys = 0.f, my_pairs = 0.f;  // work estimates for the decode / chunk balance
+  int n_pre = 0;                        // items of the shared prefixes
+  const PreLayout PL = kPre ? pre_layout(a.R, a.T, a.Hq, a.Hkv, a.D, a.NG) : PreLayout{};
+  if constexpr (kPre) n_pre = plan_prefixes(a, sw, &my_pairs);
   bool bad = false;
   const int unit_rows = pf_unit_tiles(a.G) * kPrefillTileM;
   int carry[4] = {0, 0, 0, 0};
@@ -180,6 +286,8 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     const int s = base + tid;
     int v[4] = {0, 0, 0, 0};
     int tok = 0, kv = 0;
+    PreGroup grp = {};   // kPre: the group that computes this sequence's prefix (n_tok 0: none)
+    int grp_no = -1;
     if (s < a.S) {
       const int c0 = a.cu_seqlens_q[s], c1 = a.cu_seqlens_q[s + 1];
       const int q_len = c1 - c0;
@@ -190,6 +298,17 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       if (!ok) {
         report(a.err, kErrOutOfRange);
         bad = true;
+      } else if (kPre && q_len > 0 && q_len <= kPreMaxQ && n_pre > 0 && a.prefix_group[s] >= 0 &&
+                 reinterpret_cast<const int32_t*>(a.ws + PL.map)[a.prefix_group[s]] >= 0) {
+        // one record per token: the tiles from the one holding the prefix's end to its last key
+        grp_no = a.prefix_group[s];
+        grp = reinterpret_cast<const PreGroup*>(
+            a.ws + PL.group)[reinterpret_cast<const int32_t*>(a.ws + PL.map)[grp_no]];
+        const int first = grp.keys / kDecodeTileKeys * kDecodeTileKeys;
+        v[0] = q_len;
+        for (int i = 0; i < q_len; ++i)
+          v[1] += (kv - q_len + i + 1 - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
+        my_keys += (float)(kv - grp.keys) * (float)q_len;
       } else if (q_len == 1) {
         // tiles from the one holding the window's first key (every key without a window)
         const int first = window_first_key(kv - 1, a.window) / kDecodeTileKeys * kDecodeTileKeys;
@@ -213,8 +332,26 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     }
     int ex[4], tot[4];
     block_scan4(v, ex, tot, sw);
-    if (v[0]) {
+    if (kPre && grp.n_tok > 0) {
+      // The tokens' places in the group's list come in any order: a row's result does not depend
+      // on the tile it is computed in.
+      const int q_len = v[0], first = grp.keys / kDecodeTileKeys * kDecodeTileKeys;
+      const int at = atomicAdd(reinterpret_cast<int32_t*>(a.ws + PL.cnt) + grp_no, q_len);
+      int tile = carry[1] + ex[1];
+      for (int j = 0; j < q_len; ++j) {
+        const int i = carry[0] + ex[0] + j, keys = kv - q_len + j + 1;
+        dec_seq[i] = s;
+        dec_prefix[i] = tile;
+        dec_rec[i] = make_int4(s, tok + j, keys, tile);
+        if (i < kPlanSmemSeqs) s_dec_prefix[i] = tile;
+        reinterpret_cast<int4*>(a.ws + PL.rec)[i] =
+            make_int4(grp.keys, grp.slot0 + at + j, grp.n_tok, grp.nsplit);
+        reinterpret_cast<int2*>(a.ws + PL.tok)[grp.tok0 + at + j] = make_int2(tok + j, i);
+        tile += (keys - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
+      }
+    } else if (v[0]) {
       const int i = carry[0] + ex[0];
+      if constexpr (kPre) reinterpret_cast<int4*>(a.ws + PL.rec)[i] = make_int4(0, 0, 0, 0);
       dec_seq[i] = s;
       dec_prefix[i] = carry[1] + ex[1];
       dec_rec[i] = make_int4(s, tok, kv, carry[1] + ex[1]);
@@ -304,7 +441,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     int n = (int)(ntiles < a.decode_ctas ? (ntiles > 0 ? ntiles : 1) : a.decode_ctas);
     if (a.decode_auto)
       n = choose_decode_ctas(keys * (float)(a.Hkv * a.D * 4), pairs * (float)(4 * a.D * a.Hq),
-                             n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq), a.decode_ctas,
+                             n_pre + n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq), a.decode_ctas,
                              ntiles);
     if (tid == 0) {
       s_N = n;

@@ -1,4 +1,6 @@
-// The rotary KV-append as a launch of its own (the arithmetic and the lane layout: cb_rope.cuh).
+// The rotary KV-append as a launch of its own, and with the attention planner beside it (the
+// arithmetic and the lane layout: cb_rope.cuh).
+#include "cb_plan.cuh"
 #include "cb_rope.cuh"
 
 namespace cb {
@@ -12,19 +14,49 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
                            (long long)gridDim.x * (kRopeThreads / 32));
 }
 
-cudaError_t launch_rope_append(RopeArgs r, int sm_count, cudaStream_t stream) {
-  const AppendArgs& a = r.ap;
-  if (a.T == 0) return cudaSuccess;
-  const int per_warp = 32 / (a.D / 16);
-  const int heads = (r.q != nullptr ? r.Hq : 0) + 2 * a.Hkv;
+// Warps per token: enough that the step's warps fill the SMs (32 warps each), at most one per group
+// of heads.
+static int rope_parts(const RopeArgs& r, int sm_count) {
+  const int per_warp = 32 / (r.ap.D / 16);
+  const int heads = (r.q != nullptr ? r.Hq : 0) + 2 * r.ap.Hkv;
   const int groups = (heads + per_warp - 1) / per_warp;
-  // Warps per token: enough that the step's warps fill the SMs (32 warps each).
-  const long long want = ((long long)sm_count * 32 + a.T - 1) / a.T;
-  r.parts = (int)(want < groups ? want : groups);
+  const long long want = ((long long)sm_count * 32 + r.ap.T - 1) / r.ap.T;
+  return (int)(want < groups ? want : groups);
+}
+
+cudaError_t launch_rope_append(RopeArgs r, int sm_count, cudaStream_t stream) {
+  if (r.ap.T == 0) return cudaSuccess;
+  r.parts = rope_parts(r, sm_count);
   const int warps = kRopeThreads / 32;
-  long long blocks = ((long long)a.T * r.parts + warps - 1) / warps;
+  long long blocks = ((long long)r.ap.T * r.parts + warps - 1) / warps;
   if (blocks > (long long)sm_count * 64) blocks = (long long)sm_count * 64;
   rope_append_kernel<<<(unsigned)blocks, kRopeThreads, 0, stream>>>(r);
+  return cudaGetLastError();
+}
+
+// CTA 0 plans the attention pass (it reads only the metadata); CTAs 1.. rotate and append.
+constexpr int kRopePlanUnroll = 2;  // fits the 64 registers of a 1024-thread CTA
+template <bool kPre>
+__global__ void __launch_bounds__(kPlanThreads, 1) rope_plan_kernel(const RopeArgs r, AttnArgs a) {
+  allow_dependent_launch();
+  if (blockIdx.x == 0) {
+    plan_cta<kPre>(a);
+  } else {
+    constexpr int kWarps = kPlanThreads / 32;
+    rope_tokens<kRopePlanUnroll>(r, (long long)(blockIdx.x - 1) * kWarps + (threadIdx.x >> 5),
+                                 (long long)(gridDim.x - 1) * kWarps);
+  }
+}
+
+cudaError_t launch_rope_plan(RopeArgs r, const AttnArgs& a, int sm_count, cudaStream_t stream) {
+  constexpr int kWarps = kPlanThreads / 32;
+  r.parts = rope_parts(r, sm_count);
+  long long blocks = ((long long)r.ap.T * r.parts + kWarps - 1) / kWarps;
+  if (blocks > (long long)sm_count * 16) blocks = (long long)sm_count * 16;
+  if (a.NG > 0)
+    rope_plan_kernel<true><<<(unsigned)(1 + blocks), kPlanThreads, 0, stream>>>(r, a);
+  else
+    rope_plan_kernel<false><<<(unsigned)(1 + blocks), kPlanThreads, 0, stream>>>(r, a);
   return cudaGetLastError();
 }
 

@@ -238,6 +238,71 @@ cb_status cb_append_attention(const void* k_new, const void* v_new, void* k_page
                               const cb_options* options, void* stream);
 
 /*
+ * cb_shared_prefix_attention -- cb_ragged_paged_attention for a batch in which sequences share
+ * prefixes (a system prompt, samples of one prompt, questions about one document): the attention
+ * of a group's query tokens over the keys they share is computed once for the whole group, from
+ * one read of those keys, and merged with each sequence's attention over its own keys.
+ *
+ * Sequence s belongs to group prefix_group[s] (or to none: -1); the first prefix_lens[g] keys of
+ * every member of group g are the same: the members' block tables name the same blocks for them
+ * (cb_alloc_fork and the prefix cache make such tables), or blocks with the same content.  Any
+ * length is allowed, not only whole blocks.  The result is cb_ragged_paged_attention's within
+ * rounding, whatever the grouping: the groups say what may be computed once, not what is attended
+ * to.  Where sharing does not pay the members are computed alone: groups of one query token,
+ * prefixes below 128 keys, members with more than 8 query tokens (prompt chunks; members with 2
+ * to 8, as in speculative decoding, do share).  Several levels of sharing (a tree) are given as
+ * the one level that saves most.  (An addition of this library: the pages share prefix blocks in
+ * the cache, "LLM learning path 3.3", section "PagedAttention: block tables", and leave the
+ * attention over them to each sequence.)
+ *
+ * prefix: the groups, see below; with num_groups == 0 the call is cb_ragged_paged_attention_ex.
+ * workspace: at least cb_prefix_workspace_size(dims, num_groups) bytes.
+ * options: as in cb_ragged_paged_attention_ex, but window must be 0 (CB_ERR_UNSUPPORTED).
+ * Device errors: those of cb_ragged_paged_attention; also, for a sequence with query tokens, a
+ * group outside [-1, num_groups) and a prefix length below 0 or above the sequence's prior context
+ * kv_len - q_len (the prefix must be visible to its first query): CB_ERR_OUT_OF_RANGE.
+ */
+typedef struct {
+  const int32_t* prefix_group;  /* device int32 [num_seqs]   */
+  const int32_t* prefix_lens;   /* device int32 [num_groups] */
+  int32_t num_groups;           /* >= 0                      */
+  int32_t reserved32;
+  int64_t reserved[2];
+} cb_prefix;
+
+/*
+ * cb_prefix_workspace_size -- bytes of device scratch for num_groups groups; pure host arithmetic
+ * on what cb_attention_workspace_size uses, num_kv_heads and num_groups; 0 when dims is NULL or
+ * invalid or num_groups is negative.  Beside the plan and the partial results of the decode pass
+ * it holds the prefixes' partial results: fp32 output rows of up to min(8 num_seqs, num_tokens)
+ * query tokens, and 20 MB (head_dim 128) or less for the parts of split prefixes.
+ */
+size_t cb_prefix_workspace_size(const cb_dims* dims, int32_t num_groups);
+
+cb_status cb_shared_prefix_attention(const void* q, const void* k_pages, const void* v_pages,
+                                     const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                     const int32_t* kv_lens, int32_t block_size, float scale,
+                                     const cb_prefix* prefix, void* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, const cb_dims* dims,
+                                     const cb_options* options, void* stream);
+
+/*
+ * cb_rope_append_attention -- one layer's attention step in one call: cb_rope_append, then
+ * cb_shared_prefix_attention on the rotated queries (with prefix NULL,
+ * cb_ragged_paged_attention_ex), with the same arguments and the same results (bit for bit).  Two
+ * launches: the rotary append with the attention planner beside it, and the attention kernel.
+ * q_out (required) receives the rotated queries and is what the attention reads; out must not
+ * overlap it.  Phase events as in cb_append_attention.
+ */
+cb_status cb_rope_append_attention(const void* q, const void* k_new, const void* v_new, void* q_out,
+                                   void* k_pages, void* v_pages, const int32_t* block_table,
+                                   const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                                   int32_t block_size, float scale, const cb_rope* rope,
+                                   const cb_prefix* prefix, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, const cb_dims* dims,
+                                   const cb_options* options, void* stream);
+
+/*
  * cb_pass_timestamps -- device time stamps (%globaltimer, ns) of the two passes of the last
  * attention call that used `workspace`: ts_ns[0] / [1] the first start and the last end of the
  * decode CTAs that had work, ts_ns[2] / [3] the same for the chunk CTAs (the end is the last
