@@ -467,11 +467,15 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
     cb::AttnArgs c = a;
     c.decode_grid = 0;
     if ((e = launch_pass(c, s)) != cudaSuccess) return cuda_fail(e, "attention launch");
+    if (NG > 0 && (e = cb::launch_prefix_merge(a, ds->sm_count, s)) != cudaSuccess)
+      return cuda_fail(e, "prefix merge launch");
     if ((e = mark(4)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord(phase event)");
   } else {
     a.decode_grid = a.decode_ctas * head_groups;
     if ((e = mark(3)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord(phase event)");
     if ((e = launch_pass(a, s)) != cudaSuccess) return cuda_fail(e, "attention launch");
+    if (NG > 0 && (e = cb::launch_prefix_merge(a, ds->sm_count, s)) != cudaSuccess)
+      return cuda_fail(e, "prefix merge launch");
     if ((e = mark(2)) != cudaSuccess || (e = mark(4)) != cudaSuccess)
       return cuda_fail(e, "cudaEventRecord(phase event)");
   }

@@ -31,6 +31,8 @@ __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorM
   // launch still runs; everything below reads the plan (and the appended K/V), so wait here
   // for that launch to complete and its writes to be visible.  A no-op without the attribute.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the merge of the prefixes' parts may start once every CTA of this kernel has (it waits itself)
+  if constexpr (kPre) asm volatile("griddepcontrol.launch_dependents;");
   const int b = (int)blockIdx.x;
   if (b < a.decode_grid) {
     // Span of the decode role: first start and last end of any warp of a CTA with work (the
@@ -42,7 +44,7 @@ __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorM
     if ((threadIdx.x & 31) == 0 && busy) atomicMax(&hdr->t_dec_end, global_ns());
     return;
   }
-  prefill_cta<D, QS, kWin, kPre>(a, qmap, qmap_tok, kmap_chunk, vmap_chunk, smem_raw);
+  prefill_cta<D, kWin, kPre>(a, qmap, qmap_tok, kmap_chunk, vmap_chunk, smem_raw);
 }
 
 }  // namespace cb

@@ -57,6 +57,7 @@ struct PlanHeader {
   // %globaltimer stamps (ns) of the attention kernel's roles, reset by the planner: first
   // start and last end of the decode CTAs that had work, and of the chunk CTAs.
   unsigned long long t_dec_start, t_dec_end, t_pf_start, t_pf_end;
+  int32_t pre_tokens, pad;  // entries of the groups' token list (only with prefixes)
 };
 
 // Byte offsets of the workspace sections (all 256-byte aligned).

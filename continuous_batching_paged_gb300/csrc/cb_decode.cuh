@@ -55,8 +55,7 @@ struct StageInfoBase {
   int p0, p1;    // the sequence's tile range [p0, p1) in the concatenated tile order
 };
 struct StageInfoPre : StageInfoBase {  // with shared prefixes
-  int pre_slot, pre_stride, pre_n;  // the prefix's partial results: first slot, slots between
-                                    // parts, parts (0: no prefix computed apart)
+  int pre;  // 1: its prefix is computed apart, so its own keys' results stay parts
 };
 template <bool kPre>
 using StageInfo = std::conditional_t<kPre, StageInfoPre, StageInfoBase>;
@@ -73,44 +72,28 @@ struct DecodeSmem {
   static constexpr int kTotal = kInfoOffset + kStages * (int)sizeof(StageInfoPre) + 1024;
 };
 
-// Largest CTA index c in [0, N) whose range start floor(c * n / N) is <= t.
+// Largest CTA index c in [0, N) whose range start floor(c * n / N) is <= t (t < n):
+// floor(c n / N) <= t  <=>  c n < (t + 1) N.
 __device__ __forceinline__ int cta_of_tile(long long t, long long n, int N) {
-  int lo = 0, hi = N - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (n * mid / N <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
+  return (int)(((t + 1) * N - 1) / n);
 }
 
-// Partial results of a sequence: the parts that decode CTAs wrote (slot first CTA + record, then one
-// further per CTA), and the parts of its prefix where the group's prefix was computed apart.
-struct Parts {
-  const float2* ml;
-  const float* o;
-  int cf, cl;               // decode CTAs cf .. cl hold a part
-  const float2* pre_ml;
-  const float* pre_o;
-  int pre_slot, pre_stride, pre_n;
-};
-
-// One warp combines the partial (m, l, o) of decode record `dec` (packed token `tok`) for query
-// heads h0 .. h1 - 1 of KV head `kvh`'s group, the prefix's parts first:
-// M = max m_c, w_c = 2^(m_c - M),
+// One warp combines the partial (m, l, o) that CTAs cf..cl wrote for decode sequence `dec`
+// and query heads h0 .. h1 - 1 of KV head `kvh`'s group: M = max m_c, w_c = 2^(m_c - M),
 // out = sum_c w_c o_c / sum_c w_c l_c, lse = (M + log2 sum_c w_c l_c) * ln 2.
 // Other CTAs wrote these parts: they are read through L2 (ld.global.cg), never from a stale L1
 // line.  Parts are taken kC at a time for kH heads at once, every (m, l) and o row of such a
 // batch loaded before any is used (lane i holds output columns PER i .. PER i + PER - 1), and
 // folded in with a running maximum: one L2 round trip per batch, so a sequence cut in two
 // merges 4 heads in one round trip.
-template <int D, bool kPre>
-__device__ __forceinline__ void merge_parts(const AttnArgs& a, const Parts& p, int dec, int tok,
-                                            int kvh, int h0, int h1, int lane) {
+template <int D>
+__device__ __forceinline__ void merge_parts(const AttnArgs& a, const float2* part_ml,
+                                            const float* part_o, int dec, int tok, int kvh,
+                                            int cf, int cl, int h0, int h1, int lane) {
   constexpr int PER = D / 32;  // output columns per lane: 4 (D = 128) or 2 (D = 64)
   constexpr int kH = 4, kC = 2;  // heads and parts in flight
   __nv_bfloat16* outg = static_cast<__nv_bfloat16*>(a.out);
-  const int pre_n = kPre ? p.pre_n : 0;
-  const int nparts = pre_n + p.cl - p.cf + 1;
+  const int nparts = cl - cf + 1;
   for (int r0 = h0; r0 < h1; r0 += kH) {
     float M[kH], Lsum[kH], acc[kH][PER];
 #pragma unroll
@@ -128,15 +111,13 @@ __device__ __forceinline__ void merge_parts(const AttnArgs& a, const Parts& p, i
 #pragma unroll
         for (int cc = 0; cc < kC; ++cc) {
           const int head = kvh * a.G + r0 + hh;
-          const bool pre = kPre && c0 + cc < pre_n;
-          const size_t slot = pre ? (size_t)p.pre_slot + (size_t)(c0 + cc) * p.pre_stride
-                                  : (size_t)(p.cf + c0 + cc - pre_n) + dec;
+          const size_t slot = (size_t)(cf + c0 + cc) + dec;
           ml[hh][cc] = make_float2(-INFINITY, 0.f);
 #pragma unroll
           for (int i = 0; i < PER; ++i) v[hh][cc][i] = 0.f;
           if (r0 + hh < h1 && c0 + cc < nparts) {
-            ml[hh][cc] = __ldcg((pre ? p.pre_ml : p.ml) + slot * a.Hq + head);
-            const float* po = (pre ? p.pre_o : p.o) + (slot * a.Hq + head) * D + lane * PER;
+            ml[hh][cc] = __ldcg(part_ml + slot * a.Hq + head);
+            const float* po = part_o + (slot * a.Hq + head) * D + lane * PER;
             if constexpr (PER == 4) {
               const float4 x = __ldcg(reinterpret_cast<const float4*>(po));
               v[hh][cc][0] = x.x; v[hh][cc][1] = x.y; v[hh][cc][2] = x.z; v[hh][cc][3] = x.w;
@@ -363,7 +344,10 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
       // part is written.  If every other part has counted already, this warp is the last and
       // merges without an atomic of its own.
       int peek = -1;
-      if (!(si.flags & kInfoComplete) && lane == 0)
+      // (a part of a sequence whose prefix is computed apart is merged later, with the prefix's)
+      bool counted = !(si.flags & kInfoComplete);
+      if constexpr (kPre) counted = counted && !si.pre;
+      if (counted && lane == 0)
         asm volatile("ld.acquire.gpu.global.s32 %0, [%1];"
                      : "=r"(peek)
                      : "l"(merge_cnt + ((size_t)si.dec * a.Hkv + kvh) * QS + warp % QS)
@@ -416,18 +400,15 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
           }
         }
       }
-      if (!(si.flags & kInfoComplete)) {
+      if (counted) {
         // Split sequence: the last warp to finish this (sequence, KV head, group of 8 query
         // heads) merges the group's parts.
         const int cf = cta_of_tile(si.p0, ntiles, N), cl = cta_of_tile(si.p1 - 1, ntiles, N);
         // one counter per (sequence, KV head, group of 8 query heads): with QS warps per KV
         // head, the last warp of each group merges that group's heads, the groups in parallel.
         // Counts only grow, so a counter already at parts - 1 leaves this warp the last (the
-        // fence makes its own part, read back through L2, visible to all its lanes).  A prefix
-        // computed apart counts once per part too (cb_prefill.cuh).
-        int others = cl - cf;  // parts besides this one
-        if constexpr (kPre) others += si.pre_n;
-        int last = __shfl_sync(0xffffffffu, peek, 0) == others ? 1 : 0;
+        // fence makes its own part, read back through L2, visible to all its lanes).
+        int last = __shfl_sync(0xffffffffu, peek, 0) == cl - cf ? 1 : 0;
         if (last) {
           __threadfence();
           __syncwarp();
@@ -436,23 +417,13 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
           __syncwarp();
           if (lane == 0)
             last = atomicAdd(merge_cnt + ((size_t)si.dec * a.Hkv + kvh) * QS + warp % QS, 1) ==
-                   others;
+                   cl - cf;
           last = __shfl_sync(0xffffffffu, last, 0);
           if (last) __threadfence();
         }
-        if (last) {
-          Parts p = {part_ml, part_o, cf, cl, nullptr, nullptr, 0, 0, 0};
-          if constexpr (kPre) {
-            const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.Hkv, a.D, a.NG);
-            p.pre_ml = reinterpret_cast<const float2*>(a.ws + PL.part_ml);
-            p.pre_o = reinterpret_cast<const float*>(a.ws + PL.part_o);
-            p.pre_slot = si.pre_slot;
-            p.pre_stride = si.pre_stride;
-            p.pre_n = si.pre_n;
-          }
-          merge_parts<D, kPre>(a, p, si.dec, si.tok, kvh, qoff, qoff + 8 < a.G ? qoff + 8 : a.G,
-                               lane);
-        }
+        if (last)
+          merge_parts<D>(a, part_ml, part_o, si.dec, si.tok, kvh, cf, cl, qoff,
+                         qoff + 8 < a.G ? qoff + 8 : a.G, lane);
       }
     }
   }
@@ -547,11 +518,7 @@ __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensor
           si.key0 = key0;
           si.p0 = (int)p0;
           si.p1 = (int)p1;
-          if constexpr (kPre) {
-            si.pre_slot = pre.y;
-            si.pre_stride = pre.z;
-            si.pre_n = pre.w;
-          }
+          if constexpr (kPre) si.pre = pre.w > 0;
           si.flags = (tile == lo ? kInfoFirst : 0u) | (tile == hi - 1 ? kInfoLast : 0u) |
                      (complete ? kInfoComplete : 0u);
           mbar_arrive_expect_tx(bar_full + 8 * stage,

@@ -97,5 +97,7 @@ cudaError_t launch_attention(const AttnArgs& a, const AttnMaps& maps, cudaStream
 cudaError_t launch_prefix_plan(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_attention(const AttnArgs& a, const AttnMaps& maps,
                                     const CUtensorMap& q_tok, cudaStream_t stream);
+// After it: merges the parts of the shared prefixes' rows.
+cudaError_t launch_prefix_merge(const AttnArgs& a, int sm_count, cudaStream_t stream);
 
 }  // namespace cb

@@ -246,6 +246,7 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], fl
   if (tid == 0) {
     hdr->pre_groups = carry[0];
     hdr->pre_items = carry[2];
+    hdr->pre_tokens = carry[1];
   }
   __syncthreads();
   *pairs = my_pairs;

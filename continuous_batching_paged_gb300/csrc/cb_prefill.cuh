@@ -37,7 +37,10 @@
 // TMEM columns: [0,128) S/P of A, [128,256) S/P of B, [256,256+D) O of A, then O of B.
 #pragma once
 
-#include "cb_decode.cuh"
+#include <type_traits>
+
+#include "cb_common.cuh"
+#include "cb_launch.h"
 
 namespace cb {
 
@@ -63,7 +66,7 @@ struct PrefillSmem {
   static constexpr int bQFull = 0, bQEmpty = 1, bFull = 2, bEmpty = bFull + kStages,
                        bSFull = bEmpty + kStages, bPFull = bSFull + 2, bOFinal = bPFull + 2,
                        bOFree = bOFinal + 2, bItemFull = bOFree + 2, bItemEmpty = bItemFull + 2,
-                       bClaim = bItemEmpty + 2, bRows = bClaim + 1, kNumBars = bRows + 2;
+                       bClaim = bItemEmpty + 2, kNumBars = bClaim + 1;
   static constexpr int kMisc = (kBar + kNumBars * 8 + 127) / 128 * 128;  // tmem base
   static constexpr int kItems = kMisc + 64;                 // two slots of decoded items
   static constexpr int kItemSlot = 128;
@@ -207,7 +210,7 @@ __device__ __forceinline__ PfItemPre pre_decode_item(int item, const AttnArgs& a
 // the window's bookkeeping, so it runs exactly the code it ran before windows existed.
 // One persistent CTA of the chunk pass (all kPrefillThreads threads).  Runs in the attention
 // kernel (cb_attention.cu) with that kernel's dynamic shared memory.
-template <int D, int QS, bool kWin, bool kPre>
+template <int D, bool kWin, bool kPre>
 __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap* qmap,
                                             const CUtensorMap* qmap_tok,
                                             const CUtensorMap* kmap, const CUtensorMap* vmap,
@@ -253,7 +256,6 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
       mbar_init(bar(SM::bOFree + i), 4);
       mbar_init(bar(SM::bItemFull + i), 1);
       mbar_init(bar(SM::bItemEmpty + i), kItemConsumers);
-      if constexpr (kPre) mbar_init(bar(SM::bRows + i), 4);    // (prefix parts) rows of the tile written, per warp
     }
     mbar_init(bar(SM::bClaim), 1);
     fence_barrier_init();
@@ -565,7 +567,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
     const uint32_t o_col = 256 + t * D;
     const float sl2 = a.scale_log2;
     __nv_bfloat16* outg = static_cast<__nv_bfloat16*>(a.out);
-    uint32_t g = 0, gx = 0, kx = 0, px = 0;
+    uint32_t g = 0, gx = 0, kx = 0;
     for (uint32_t k = 0;; ++k) {
       const int slot = k & 1;
       if (!mbar_wait(bar(SM::bItemFull + slot), (k >> 1) & 1)) { report(a.err, kErrTimeout); break; }
@@ -701,8 +703,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
       __syncwarp();
       tc_fence_after();
       if constexpr (kPre) if (pre) {
-        // ---- epilogue of a prefix part: (m, l) and O as they are, to the token's slot; then one
-        // count per token, and the merge of those whose last part this was
+        // ---- epilogue of a prefix part: (m, l) and O as they are, to the token's slot
         float2* part_ml = reinterpret_cast<float2*>(a.ws + PL.part_ml);
         float* part_o = reinterpret_cast<float*>(a.ws + PL.part_o);
         const int i_tok = r / a.G;
@@ -726,60 +727,6 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         gx += nt - it.j0;
         kx += 1;
         if (r < rows) part_ml[row] = make_float2(m_run, l_run);
-        // The tile's rows are out once its four warps have arrived; the fences before the arrival
-        // and before the counts below make them visible to whoever merges.
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(SM::bRows + t));
-        if (!mbar_wait(bar(SM::bRows + t), px & 1)) { report(a.err, kErrTimeout); break; }
-        px += 1;
-        __threadfence();
-        const int ntok = t ? it.ntok[1] : it.ntok[0];
-        const int i_mine = lane * 4 + quad;  // the group's 128 threads count one token each
-        int2 tr = make_int2(0, 0);
-        int4 rec = make_int4(0, 0, 0, 0);
-        int cf = 0, cl = 0;
-        unsigned last_of[QS];
-#pragma unroll
-        for (int hg = 0; hg < QS; ++hg) last_of[hg] = 0;
-        if (i_mine < ntok) {
-          tr = pre_tok[tok + i_mine];
-          rec = reinterpret_cast<const int4*>(a.ws + PL.rec)[tr.y];
-          const int4* dec_rec = reinterpret_cast<const int4*>(a.ws + L.dec_rec);
-          const long long ntiles = hdr->dec_tiles;
-          cf = cta_of_tile(dec_rec[tr.y].w, ntiles, hdr->decode_ctas);
-          cl = cta_of_tile(dec_rec[tr.y + 1].w - 1, ntiles, hdr->decode_ctas);
-        }
-#pragma unroll
-        for (int hg = 0; hg < QS; ++hg) {
-          bool last = false;
-          if (i_mine < ntok) {
-            int32_t* cnt = reinterpret_cast<int32_t*>(a.ws + L.merge_cnt) +
-                           ((size_t)tr.y * a.Hkv + it.kvh) * QS + hg;
-            last = atomicAdd(cnt, 1) == cl - cf + rec.w;
-          }
-          last_of[hg] = __ballot_sync(0xffffffffu, last);
-          if (last_of[hg]) __threadfence();
-        }
-#pragma unroll
-        for (int hg = 0; hg < QS; ++hg) {
-          for (unsigned m = last_of[hg]; m != 0; m &= m - 1) {
-            const int src = __ffs(m) - 1;
-            Parts p;
-            p.ml = reinterpret_cast<const float2*>(a.ws + L.part_ml);
-            p.o = reinterpret_cast<const float*>(a.ws + L.part_o);
-            p.cf = __shfl_sync(0xffffffffu, cf, src);
-            p.cl = __shfl_sync(0xffffffffu, cl, src);
-            p.pre_ml = part_ml;
-            p.pre_o = part_o;
-            p.pre_slot = __shfl_sync(0xffffffffu, rec.y, src);
-            p.pre_stride = __shfl_sync(0xffffffffu, rec.z, src);
-            p.pre_n = __shfl_sync(0xffffffffu, rec.w, src);
-            merge_parts<D, true>(a, p, __shfl_sync(0xffffffffu, tr.y, src),
-                                 __shfl_sync(0xffffffffu, tr.x, src), it.kvh, hg * 8,
-                                 min(hg * 8 + 8, a.G), lane);
-          }
-        }
         if (r == 0) atomicMax(&hdr->t_pf_end, global_ns());
         continue;
       }
