@@ -351,8 +351,7 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
     return fail(CB_ERR_INVALID_ARG, "scale must be a positive finite number");
   const int R = NG > 0 ? cb::pre_records(dims->num_seqs, dims->num_tokens) : dims->num_seqs;
   const size_t need =
-      NG > 0 ? cb::pre_layout(R, dims->num_tokens, dims->num_q_heads, dims->num_kv_heads,
-                              dims->head_dim, NG).total
+      NG > 0 ? cb::pre_layout(R, dims->num_tokens, dims->num_q_heads, dims->head_dim, NG).total
              : cb::ws_layout(R, dims->num_tokens, dims->num_q_heads, dims->head_dim).total;
   if (workspace_bytes < need)
     return fail(CB_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
@@ -396,6 +395,7 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   if (dctas > CB_MAX_DECODE_CTAS) dctas = CB_MAX_DECODE_CTAS;
   a.decode_ctas = dctas;
   a.prefill_ctas = ds->sm_count;
+  a.pre_ctas = NG == 0 ? 0 : ds->sm_count < cb::kMaxPreCtas ? ds->sm_count : cb::kMaxPreCtas;
   a.R = R;
   a.prefix_group = NG > 0 ? prefix->prefix_group : nullptr;
   a.prefix_lens = NG > 0 ? prefix->prefix_lens : nullptr;
@@ -460,7 +460,7 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   if (serial) {
     cb::AttnArgs d = a;
     d.decode_grid = a.decode_ctas * head_groups;
-    d.prefill_ctas = 0;
+    d.prefill_ctas = d.pre_ctas = 0;
     if ((e = launch_pass(d, s)) != cudaSuccess) return cuda_fail(e, "attention launch");
     if ((e = mark(2)) != cudaSuccess || (e = mark(3)) != cudaSuccess)
       return cuda_fail(e, "cudaEventRecord(phase event)");
@@ -532,7 +532,7 @@ size_t cb_prefix_workspace_size(const cb_dims* dims, int32_t num_groups) {
   if (num_groups <= 0) return num_groups == 0 ? cb_attention_workspace_size(dims) : 0;
   if (cb_attention_workspace_size(dims) == 0 || dims->num_q_heads / dims->num_kv_heads > 16) return 0;
   return cb::pre_layout(cb::pre_records(dims->num_seqs, dims->num_tokens), dims->num_tokens,
-                        dims->num_q_heads, dims->num_kv_heads, dims->head_dim, num_groups).total;
+                        dims->num_q_heads, dims->head_dim, num_groups).total;
 }
 
 cb_status cb_shared_prefix_attention(const void* q, const void* k_pages, const void* v_pages,

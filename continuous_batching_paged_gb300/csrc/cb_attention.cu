@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
 template <int D, int QS, bool kWin>
 static cudaError_t launch_instance(const AttnArgs& a, const AttnMaps& m, cudaStream_t stream) {
-  constexpr int kSmem = AttnSmem<D, QS>::kTotal;
+  constexpr int kSmem = AttnSmem<D, QS, false>::kTotal;
   // The shared-memory opt-in is a setting of the context: made again whenever the launch
   // goes to another context than the last one configured.
   static unsigned long long configured_ctx = 0;

@@ -1,9 +1,10 @@
-// One CTA of an attention kernel: a decode-role CTA or a chunk-role CTA, by its index in the grid
-// (cb_attention.cu says how the two share the GPU).
+// One CTA of an attention kernel: a decode-role CTA, with shared prefixes a prefix-role CTA, or a
+// chunk-role CTA, by its index in the grid (cb_attention.cu says how they share the GPU).
 #pragma once
 
 #include "cb_decode.cuh"
 #include "cb_prefill.cuh"
+#include "cb_prefix.cuh"
 
 namespace cb {
 
@@ -11,11 +12,12 @@ constexpr int kAttnThreads = kPrefillThreads;
 static_assert(32 * (kMaxDecodeHeadsPerCta + 1) <= kAttnThreads,
               "the decode role fits in the chunk role's CTA");
 
-template <int D, int QS>
+template <int D, int QS, bool kPre>
 struct AttnSmem {
-  static constexpr int kTotal = DecodeSmem<D, QS>::kTotal > PrefillSmem<D>::kTotal
-                                    ? DecodeSmem<D, QS>::kTotal
-                                    : PrefillSmem<D>::kTotal;
+  static constexpr int kBoth = DecodeSmem<D, QS>::kTotal > PrefillSmem<D>::kTotal
+                                   ? DecodeSmem<D, QS>::kTotal
+                                   : PrefillSmem<D>::kTotal;
+  static constexpr int kTotal = kPre && PreSmem<D>::kTotal > kBoth ? PreSmem<D>::kTotal : kBoth;
 };
 
 // kPre: the batch's shared prefixes are computed once per group (cb_prefix.cu); qmap_tok is the
@@ -44,7 +46,13 @@ __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorM
     if ((threadIdx.x & 31) == 0 && busy) atomicMax(&hdr->t_dec_end, global_ns());
     return;
   }
-  prefill_cta<D, kWin, kPre>(a, qmap, qmap_tok, kmap_chunk, vmap_chunk, smem_raw);
+  if constexpr (kPre) {
+    if (b < a.decode_grid + a.pre_ctas) {
+      prefix_cta<D>(a, qmap_tok, kmap_chunk, vmap_chunk, smem_raw, b - a.decode_grid);
+      return;
+    }
+  }
+  prefill_cta<D, kWin>(a, qmap, kmap_chunk, vmap_chunk, smem_raw);
 }
 
 }  // namespace cb

@@ -52,12 +52,13 @@ struct PlanHeader {
   int32_t pf_qtiles;      // total work units over all chunk sequences (pf_unit_tiles)
   int32_t pf_counter;     // dynamic work counter of the prefill pass (reset by the planner)
   int32_t decode_ctas;    // CTAs the decode pass was planned for
-  int32_t pre_groups;     // shared-prefix pass: groups whose prefix is computed once ...
-  int32_t pre_items;      // ... and its work items (both only with prefixes)
+  int32_t pre_groups;     // shared prefixes (only with them): groups whose prefix is computed once,
+  int32_t pre_ctas;       // CTAs that do it (0: no such group),
   // %globaltimer stamps (ns) of the attention kernel's roles, reset by the planner: first
   // start and last end of the decode CTAs that had work, and of the chunk CTAs.
   unsigned long long t_dec_start, t_dec_end, t_pf_start, t_pf_end;
-  int32_t pre_tokens, pad;  // entries of the groups' token list (only with prefixes)
+  long long pre_cost;       // their work, in cost units (PreGroup),
+  int32_t pre_tokens, pad;  // and entries of the groups' token list
 };
 
 // Byte offsets of the workspace sections (all 256-byte aligned).
@@ -94,16 +95,15 @@ __host__ __device__ inline WsLayout ws_layout(int S, int T, int Hq, int D) {
 }
 
 // ------------------------------------------------------------------------------------------
-// Shared prefixes (cb_prefix.cu).  A sequence of a group with at most kPreMaxQ query tokens gets
+// Shared prefixes (cb_prefix.cuh).  A sequence of a group with at most kPreMaxQ query tokens gets
 // one decode record per token for its own keys, and its tokens' rows go into the group's tiles of
 // kPrefillTileM rows for the prefix; longer chunks run the chunk pass over all their keys (it is
 // bound by arithmetic, which sharing does not save).
 constexpr int kPreMaxQ = 8;
 // Prefixes shorter than one K/V tile are left to each sequence's own pass.
 constexpr int kPreMinKeys = kChunkKeys;
-// Work items that long prefixes are split into (about one per SM), and the shortest split.
-constexpr int kPreItems = 152;
-constexpr int kPreMinTiles = 4;
+constexpr int kMaxPreCtas = 160;   // CTAs of the prefix pass (at most one per SM)
+constexpr int kPreMinSteps = 3;    // K/V tiles per CTA at least
 
 // Query tokens per tile: all G query heads of a KV head, token by token.
 __host__ __device__ inline int pre_tile_tokens(int G) { return kPrefillTileM / G; }
@@ -113,40 +113,43 @@ __host__ __device__ inline int pre_records(int S, int T) {
   return most > S ? (int)most : S;
 }
 
-// One group whose prefix is computed once, in the order of the group numbers.
+// One group whose prefix is computed once.  Its query tokens make tiles, two tiles (the last time
+// maybe one) make a unit, and a chain is one unit under one KV head against all K/V tiles of the
+// prefix.  A step (one K/V tile) of a chain costs kPreCost2 units with two tiles of rows, kPreCost1
+// with one.  All chains of all groups are laid end to end, KV head by KV head and unit by unit, and
+// cut into equal ranges of cost, one per CTA.
+constexpr int kPreCost2 = 3, kPreCost1 = 2;
 struct PreGroup {
-  int32_t item0;    // its first work item
+  long long cost0;  // where its first chain starts
   int32_t n_tok;    // query tokens
   int32_t tok0;     // its first entry of the token list
   int32_t keys;     // prefix length
   int32_t seq;      // the sequence whose block table is read (the first member)
-  int32_t nsplit;   // parts that the prefix is split into
-  int32_t tiles;    // K/V tiles per part
-  int32_t slot0;    // partial results: slot0 + part * n_tok + token
 };
 
 // Sections of the workspace behind ws_layout's (all 256-byte aligned).
 struct PreLayout {
-  size_t rec, cnt, first, map, group, tok, part_ml, part_o, total;
+  size_t rec, cnt, first, map, group, tok, base_ml, base_o, cut_ml, cut_o, total;
 };
-__host__ __device__ inline PreLayout pre_layout(int R, int T, int Hq, int Hkv, int D, int NG) {
+__host__ __device__ inline PreLayout pre_layout(int R, int T, int Hq, int D, int NG) {
   PreLayout L;
   size_t off = ws_layout(R, T, Hq, D).total;
-  // per decode record (prefix length, first partial-result slot, slots between parts, parts)
+  // per decode record (prefix length, index in the group list, token of the group, 1), or zeros
   L.rec = off;     off = align_up(off + sizeof(int32_t) * 4 * (size_t)(R + 1), 256);
-  // per group number: query tokens (then: tokens listed so far), first member, index below
+  // per group number: query tokens (then: tokens listed so far), first member, index in the list
   L.cnt = off;     off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.first = off;   off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.map = off;     off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.group = off;   off = align_up(off + sizeof(PreGroup) * (size_t)(NG + 1), 256);
   // per query token of a group: (packed token, decode record)
   L.tok = off;     off = align_up(off + sizeof(int32_t) * 2 * (size_t)(R + 1), 256);
-  // One slot per token and part.  Splitting adds less than kPreItems items (the planner splits
-  // into parts of at least all items' tiles / kPreItems), each of at most two tiles of tokens.
-  const size_t slots =
-      (size_t)R + ((size_t)kPreItems * 2 * pre_tile_tokens(Hq / Hkv) + Hkv - 1) / Hkv;
-  L.part_ml = off; off = align_up(off + sizeof(float2) * slots * (size_t)Hq, 256);
-  L.part_o = off;  off = align_up(off + sizeof(float) * slots * (size_t)Hq * (size_t)D, 256);
+  // Partial results of a chain: the part with its first K/V tile in a row per (token list entry,
+  // query head), and a part that a CTA's range begins with in the CTA's own 2 x 128 rows.
+  L.base_ml = off; off = align_up(off + sizeof(float2) * (size_t)R * (size_t)Hq, 256);
+  L.base_o = off;  off = align_up(off + sizeof(float) * (size_t)R * (size_t)Hq * (size_t)D, 256);
+  const size_t cut_rows = (size_t)kMaxPreCtas * 2 * kPrefillTileM;
+  L.cut_ml = off;  off = align_up(off + sizeof(float2) * cut_rows, 256);
+  L.cut_o = off;   off = align_up(off + sizeof(float) * cut_rows * (size_t)D, 256);
   L.total = off;
   return L;
 }

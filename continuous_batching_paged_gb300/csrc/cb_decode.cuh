@@ -463,7 +463,7 @@ __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensor
     int4 pre = make_int4(0, 0, 0, 0);
     if constexpr (kPre) {  // and with a prefix computed apart, at the one holding its end
       pre = reinterpret_cast<const int4*>(
-          a.ws + pre_layout(a.R, a.T, a.Hq, a.Hkv, a.D, a.NG).rec)[d];
+          a.ws + pre_layout(a.R, a.T, a.Hq, a.D, a.NG).rec)[d];
       lo_key = pre.x;
     }
     const int first_tile_key = lo_key / kDecodeTileKeys * kDecodeTileKeys;

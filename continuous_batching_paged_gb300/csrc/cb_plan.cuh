@@ -3,6 +3,7 @@
 
 #include "cb_common.cuh"
 #include "cb_launch.h"
+#include "cb_pre_parts.cuh"
 
 namespace cb {
 
@@ -151,17 +152,15 @@ __device__ inline int pf_unit_bin(const AttnArgs& a, const int32_t* pf_seq, cons
   return kCostBins - 1 - min(tiles, kCostBins - 1);
 }
 
-// With shared prefixes: which groups' prefixes are computed once, as which work items.  Fills the
-// group list, the map from group number to it (-1: every member's own pass does it all) and zeroes
-// the count of tokens listed so far.  *pairs: the items' (query token, key) pairs, tile by tile.
-// Returns the number of items (the same in every thread).
+// With shared prefixes: which groups' prefixes are computed once.  Fills the group list, the map
+// from group number to it (-1: every member's own pass does it all) and zeroes the count of tokens
+// listed so far.  Returns the work of the prefixes in cost units (0: no group takes part; the same
+// in every thread).
 //
 // A group takes part when it has at least two query tokens (from members with at most kPreMaxQ
 // each) and kPreMinKeys keys; after bad metadata none does, and each sequence is computed alone.
-// Long prefixes are split into parts of equal K/V tiles so that all items together come to about
-// kPreItems; the bound on the partial results (pre_layout) rests on the rule len >= W / kPreItems.
-__device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], float* pairs) {
-  const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.Hkv, a.D, a.NG);
+__device__ __forceinline__ long long plan_prefixes(const AttnArgs& a, int (*sw)[4]) {
+  const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG);
   int32_t* cnt = reinterpret_cast<int32_t*>(a.ws + PL.cnt);
   int32_t* first = reinterpret_cast<int32_t*>(a.ws + PL.first);
   int32_t* map = reinterpret_cast<int32_t*>(a.ws + PL.map);
@@ -169,8 +168,7 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], fl
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D).header);
   const int tid = threadIdx.x;
   const long long max_kv = (long long)a.max_blocks * a.bs;
-  __shared__ unsigned long long s_work, s_items;
-  if (tid == 0) s_work = s_items = 0;
+  __shared__ long long s_scan[kPlanThreads / 32 + 1];
   for (int g = tid; g < a.NG; g += kPlanThreads) {
     cnt[g] = 0;
     first[g] = 0x7fffffff;
@@ -196,61 +194,85 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], fl
     }
   }
   bad = __syncthreads_or(bad) != 0;
-  const int per_tile = pre_tile_tokens(a.G);
-  auto units_of = [&](int n_tok) { return (n_tok + 2 * per_tile - 1) / (2 * per_tile); };
-  auto shared_tokens = [&](int g) -> int {  // tokens of group g if its prefix is computed once
-    if (bad || g >= a.NG || cnt[g] < 2 || a.prefix_lens[g] < kPreMinKeys) return 0;
-    return cnt[g];
-  };
-  auto tiles_of = [&](int g) { return (a.prefix_lens[g] + kChunkKeys - 1) / kChunkKeys; };
-  float my_pairs = 0.f;
-  for (int g = tid; g < a.NG; g += kPlanThreads) {
-    const int n = shared_tokens(g);
-    if (n > 0) {
-      const unsigned long long items = (unsigned long long)units_of(n) * a.Hkv;
-      atomicAdd(&s_items, items);
-      atomicAdd(&s_work, items * tiles_of(g));
-      my_pairs += (float)(units_of(n) * 2 * per_tile) * (float)a.prefix_lens[g];
-    }
-  }
-  __syncthreads();
-  long long len = (long long)((s_work + kPreItems - 1) / kPreItems);
-  if (len < kPreMinTiles) len = kPreMinTiles;
-  if (s_items >= kPreItems || len > 0x7fffffff) len = 0x7fffffff;
-  int carry[4] = {0, 0, 0, 0};  // groups, tokens, items, slots
+  int carry[4] = {0, 0, 0, 0};  // groups, tokens
+  long long cost_carry = 0;
   for (int base = 0; base < a.NG; base += kPlanThreads) {
     const int g = base + tid;
-    const int n = shared_tokens(g);
-    int v[4] = {0, 0, 0, 0}, ex[4], tot[4], nsplit = 0, part = 0;
-    if (n > 0) {
-      const int nt = tiles_of(g);
-      nsplit = (int)((nt + len - 1) / len);
-      part = (nt + nsplit - 1) / nsplit;
-      nsplit = (nt + part - 1) / part;
-      v[0] = 1;
-      v[1] = n;
-      v[2] = units_of(n) * a.Hkv * nsplit;
-      v[3] = n * nsplit;
-    }
+    const int n = bad || g >= a.NG || cnt[g] < 2 || a.prefix_lens[g] < kPreMinKeys ? 0 : cnt[g];
+    int v[4] = {n > 0, n, 0, 0}, ex[4], tot[4];
+    long long cost = n > 0 ? pre_cost_per_head(n, a.prefix_lens[g], a.G) * a.Hkv : 0;
     block_scan4(v, ex, tot, sw);  // (its barriers also part the reads of cnt from the writes)
+    // the same scan of the costs, in 64 bits
+    const long long own = cost;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, cost, o);
+      if ((tid & 31) >= o) cost += y;
+    }
+    if ((tid & 31) == 31) s_scan[tid >> 5] = cost;
+    __syncthreads();
+    if (tid < 32) {
+      long long x = s_scan[tid];
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (tid >= o) x += y;
+      }
+      s_scan[tid] = x;
+    }
+    __syncthreads();
+    const long long before = cost - own + (tid >= 32 ? s_scan[(tid >> 5) - 1] : 0);
     if (g < a.NG) {
       map[g] = n > 0 ? carry[0] + ex[0] : -1;
       cnt[g] = 0;
     }
     if (n > 0)
-      groups[carry[0] + ex[0]] = {carry[2] + ex[2], n, carry[1] + ex[1], a.prefix_lens[g],
-                                  first[g], nsplit, part, carry[3] + ex[3]};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) carry[k] += tot[k];
+      groups[carry[0] + ex[0]] = {cost_carry + before, n, carry[1] + ex[1], a.prefix_lens[g], first[g]};
+    carry[0] += tot[0];
+    carry[1] += tot[1];
+    cost_carry += s_scan[kPlanThreads / 32 - 1];
+    __syncthreads();
   }
   if (tid == 0) {
     hdr->pre_groups = carry[0];
-    hdr->pre_items = carry[2];
     hdr->pre_tokens = carry[1];
+    hdr->pre_cost = cost_carry;
   }
   __syncthreads();
-  *pairs = my_pairs;
-  return carry[2];
+  return cost_carry;
+}
+
+// Decode and prefix CTA counts where prefixes are computed apart.  Called by one full warp.
+// Model, fitted to GB300 measurements: decode on n SMs streams as in choose_decode_ctas; a cost
+// unit of the prefixes takes 0.7 us of an SM (a step with one tile of rows 1.4, with two 2.1); chunk
+// work follows on the SMs that the prefixes leave, so it is counted with them.  The two sides run at
+// once, so the choice is the n with the least max(decode, prefix + chunk), the smallest such n.
+__device__ __forceinline__ int choose_prefix_split(float dec_bytes, float cost, float chunk_flops,
+                                                   int head_groups, int max_ctas, int sms,
+                                                   long long tiles) {
+  const int lane = threadIdx.x & 31;
+  const int cap = (int)(tiles < max_ctas ? tiles : max_ctas);
+  const float w_us = cost * 0.7f + chunk_flops * (1.f / 6.4e6f);
+  const float b_mb = dec_bytes * 1e-6f;
+  float best = 3.4e38f;
+  int best_n = cap < 1 ? 1 : cap;
+  for (int i = lane; 2 * (i + 1) * head_groups < sms && 2 * (i + 1) <= cap; i += 32) {
+    const int n = 2 * (i + 1), m = sms - n * head_groups;
+    const float lin = 0.11f * n * head_groups, sat = 6.8f;
+    const float bw = rcbrtf(1.f / (lin * lin * lin) + 1.f / (sat * sat * sat));
+    const float t = fmaxf(b_mb / bw, w_us / (float)m);
+    if (t < best) {
+      best = t;
+      best_n = n;
+    }
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    const float t = __shfl_xor_sync(0xffffffffu, best, o);
+    const int n = __shfl_xor_sync(0xffffffffu, best_n, o);
+    if (t < best || (t == best && n < best_n)) {
+      best = t;
+      best_n = n;
+    }
+  }
+  return best_n;
 }
 
 // Batches of up to this many decode (or chunk) sequences keep the planner's prefix arrays in
@@ -277,9 +299,9 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   const long long max_kv = (long long)a.max_blocks * a.bs;
 
   float my_keys = 0.f, my_pairs = 0.f;  // work estimates for the decode / chunk balance
-  int n_pre = 0;                        // items of the shared prefixes
-  const PreLayout PL = kPre ? pre_layout(a.R, a.T, a.Hq, a.Hkv, a.D, a.NG) : PreLayout{};
-  if constexpr (kPre) n_pre = plan_prefixes(a, sw, &my_pairs);
+  long long pre_cost = 0;               // work of the shared prefixes
+  const PreLayout PL = kPre ? pre_layout(a.R, a.T, a.Hq, a.D, a.NG) : PreLayout{};
+  if constexpr (kPre) pre_cost = plan_prefixes(a, sw);
   bool bad = false;
   const int unit_rows = pf_unit_tiles(a.G) * kPrefillTileM;
   int carry[4] = {0, 0, 0, 0};
@@ -288,7 +310,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     int v[4] = {0, 0, 0, 0};
     int tok = 0, kv = 0;
     PreGroup grp = {};   // kPre: the group that computes this sequence's prefix (n_tok 0: none)
-    int grp_no = -1;
+    int grp_no = -1, grp_at = 0;
     if (s < a.S) {
       const int c0 = a.cu_seqlens_q[s], c1 = a.cu_seqlens_q[s + 1];
       const int q_len = c1 - c0;
@@ -299,12 +321,12 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       if (!ok) {
         report(a.err, kErrOutOfRange);
         bad = true;
-      } else if (kPre && q_len > 0 && q_len <= kPreMaxQ && n_pre > 0 && a.prefix_group[s] >= 0 &&
+      } else if (kPre && q_len > 0 && q_len <= kPreMaxQ && pre_cost > 0 && a.prefix_group[s] >= 0 &&
                  reinterpret_cast<const int32_t*>(a.ws + PL.map)[a.prefix_group[s]] >= 0) {
         // one record per token: the tiles from the one holding the prefix's end to its last key
         grp_no = a.prefix_group[s];
-        grp = reinterpret_cast<const PreGroup*>(
-            a.ws + PL.group)[reinterpret_cast<const int32_t*>(a.ws + PL.map)[grp_no]];
+        grp_at = reinterpret_cast<const int32_t*>(a.ws + PL.map)[grp_no];
+        grp = reinterpret_cast<const PreGroup*>(a.ws + PL.group)[grp_at];
         const int first = grp.keys / kDecodeTileKeys * kDecodeTileKeys;
         v[0] = q_len;
         for (int i = 0; i < q_len; ++i)
@@ -346,7 +368,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
         dec_rec[i] = make_int4(s, tok + j, keys, tile);
         if (i < kPlanSmemSeqs) s_dec_prefix[i] = tile;
         reinterpret_cast<int4*>(a.ws + PL.rec)[i] =
-            make_int4(grp.keys, grp.slot0 + at + j, grp.n_tok, grp.nsplit);
+            make_int4(grp.keys, grp_at, at + j, 1);
         reinterpret_cast<int2*>(a.ws + PL.tok)[grp.tok0 + at + j] = make_int2(tok + j, i);
         tile += (keys - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
       }
@@ -440,10 +462,23 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       pairs += s_red[1][w];
     }
     int n = (int)(ntiles < a.decode_ctas ? (ntiles > 0 ? ntiles : 1) : a.decode_ctas);
-    if (a.decode_auto)
+    if (kPre && pre_cost > 0) {
+      const int hg = (a.Hkv + (a.G > 8 ? 4 : 8) - 1) / (a.G > 8 ? 4 : 8);
+      if (a.decode_auto)
+        n = choose_prefix_split(keys * (float)(a.Hkv * a.D * 4), (float)pre_cost,
+                                pairs * (float)(4 * a.D * a.Hq), hg, a.decode_ctas, a.prefill_ctas,
+                                ntiles);
+      const int left = a.prefill_ctas - n * hg;  // SMs beside the decode CTAs
+      long long np = left > a.prefill_ctas / 8 ? left : a.prefill_ctas / 8;
+      const long long most = pre_cost / (kPreMinSteps * kPreCost1);
+      np = np < most ? np : most;
+      if (tid == 0) hdr->pre_ctas = np < 1 ? 1 : np < a.pre_ctas ? (int)np : a.pre_ctas;
+    } else if (a.decode_auto) {
       n = choose_decode_ctas(keys * (float)(a.Hkv * a.D * 4), pairs * (float)(4 * a.D * a.Hq),
-                             n_pre + n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq), a.decode_ctas,
+                             n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq), a.decode_ctas,
                              ntiles);
+    }
+    if (kPre && pre_cost == 0 && tid == 0) hdr->pre_ctas = 0;
     if (tid == 0) {
       s_N = n;
       hdr->decode_ctas = n;

@@ -37,8 +37,6 @@
 // TMEM columns: [0,128) S/P of A, [128,256) S/P of B, [256,256+D) O of A, then O of B.
 #pragma once
 
-#include <type_traits>
-
 #include "cb_common.cuh"
 #include "cb_launch.h"
 
@@ -89,7 +87,7 @@ constexpr int kRegsSoftmax = 200;  // warpgroups 1 and 2
 static_assert(kRegsIssue + 2 * kRegsSoftmax <= 3 * 168, "register split exceeds the launch");
 constexpr int kItemConsumers = 10;  // producer, MMA warp, 4 warps of each softmax group
 
-struct PfItemBase {
+struct PfItem {
   int item;                                    // claimed item index, -1: no more work
   int s, kvh, ctx;
   int head[2], tok[2], rows[2], nk[2], nt[2];  // per tile: query head, first token, valid rows,
@@ -99,16 +97,7 @@ struct PfItemBase {
   int j0;                                      // first K/V tile (a sliding window skips older)
   int hasB;
 };
-// With kPre also a part of a group's prefix (pre_n > 0): tok[] index the group's token list, rows[]
-// are ntok[] tokens x G heads from head[0] on, every row sees the same keys, and the tiles' results
-// are partial ones, from slot[] on; ctx is the prefix length.
-struct PfItemPre : PfItemBase {
-  int pre_n;                                   // parts the prefix is split into
-  int ntok[2], slot[2];
-};
-template <bool kPre>
-using PfItem = std::conditional_t<kPre, PfItemPre, PfItemBase>;
-static_assert(sizeof(PfItemPre) <= 128, "a decoded item fits its shared-memory slot");
+static_assert(sizeof(PfItem) <= 128, "a decoded item fits its shared-memory slot");
 
 // Query heads (pairs) per unit: items are unit-major with the head (pair) fastest, so the
 // CTAs on the heads of one KV group at the same time share its K/V tiles through L2.
@@ -117,10 +106,10 @@ __device__ __forceinline__ int pf_heads_per_unit(const AttnArgs& a) {
 }
 
 template <bool kWin>
-__device__ __forceinline__ PfItemBase pf_decode_item(int item, const AttnArgs& a,
+__device__ __forceinline__ PfItem pf_decode_item(int item, const AttnArgs& a,
                                                  const int32_t* pf_seq, const int32_t* pf_prefix,
                                                  const int32_t* pf_order, int n_pf) {
-  PfItemBase it;
+  PfItem it;
   it.item = item;
   const int hu_n = pf_heads_per_unit(a);
   const int pos = item / hu_n;  // position in the longest-first unit order
@@ -165,58 +154,15 @@ __device__ __forceinline__ PfItemBase pf_decode_item(int item, const AttnArgs& a
   return it;
 }
 
-// Work item `item` of the shared prefixes: rows of one group (two tiles of tokens with all query
-// heads of one KV head) against one part of the group's prefix.  Items of a group go tiles
-// fastest, then KV head, then part, so that CTAs running at the same time share K/V through L2.
-__device__ __forceinline__ PfItemPre pre_decode_item(int item, const AttnArgs& a,
-                                                  const PreGroup* groups, int n_groups) {
-  int lo = 0, hi = n_groups - 1;  // largest i with groups[i].item0 <= item
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (groups[mid].item0 <= item) lo = mid; else hi = mid - 1;
-  }
-  const PreGroup g = groups[lo];
-  PfItemPre it;
-  it.item = item;
-  const int per_tile = pre_tile_tokens(a.G);
-  const int units = (g.n_tok + 2 * per_tile - 1) / (2 * per_tile);
-  const int rel = item - g.item0, rest = rel / units;
-  const int u = rel - rest * units, part = rest / a.Hkv;
-  it.kvh = rest - part * a.Hkv;
-  it.s = g.seq;
-  it.ctx = g.keys;
-  it.pre_n = g.nsplit;
-  it.j0 = part * g.tiles;
-  it.nt_all = min((g.keys + kChunkKeys - 1) / kChunkKeys, it.j0 + g.tiles);
-  it.nk_all = min(g.keys, it.nt_all * kChunkKeys);
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int first = (2 * u + t) * per_tile;
-    it.ntok[t] = max(0, min(per_tile, g.n_tok - first));
-    it.rows[t] = it.ntok[t] * a.G;
-    it.tok[t] = g.tok0 + first;
-    it.slot[t] = g.slot0 + part * g.n_tok + first;
-    it.head[t] = it.kvh * a.G;
-    it.nk[t] = it.nk_all;
-    it.nt[t] = it.nt_all;
-    it.qoff[t] = 0;
-  }
-  it.hasB = it.ntok[1] > 0;
-  return it;
-}
-
-// kPre: the items of the shared prefixes come before the chunk items.
 // kWin: sliding-window attention (a.window > 0).  The full causal pass is compiled without
 // the window's bookkeeping, so it runs exactly the code it ran before windows existed.
 // One persistent CTA of the chunk pass (all kPrefillThreads threads).  Runs in the attention
 // kernel (cb_attention.cu) with that kernel's dynamic shared memory.
-template <int D, bool kWin, bool kPre>
+template <int D, bool kWin>
 __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap* qmap,
-                                            const CUtensorMap* qmap_tok,
                                             const CUtensorMap* kmap, const CUtensorMap* vmap,
                                             uint8_t* smem_raw) {
   using SM = PrefillSmem<D>;
-  using Item = PfItem<kPre>;
   constexpr int NS = SM::kStages;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -225,7 +171,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + SM::kMisc);
   // Decoded items, two slots: the scheduler warp claims and decodes the next item while the
   // current one runs; every role reads it from here (no global-memory chain at an item's start).
-  auto item_slot = [&](int slot) { return reinterpret_cast<Item*>(smem + SM::kItems + slot * SM::kItemSlot); };
+  auto item_slot = [&](int slot) { return reinterpret_cast<PfItem*>(smem + SM::kItems + slot * SM::kItemSlot); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D);
@@ -234,12 +180,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
   const int32_t* pf_prefix = reinterpret_cast<const int32_t*>(a.ws + L.pf_prefix);
   const int32_t* pf_order = reinterpret_cast<const int32_t*>(a.ws + L.pf_order);
   const int n_pf = hdr->n_pf;
-  // with shared prefixes: their items, groups and token list
-  const int n_pre = kPre ? hdr->pre_items : 0, n_groups = kPre ? hdr->pre_groups : 0;
-  const PreLayout PL = kPre ? pre_layout(a.R, a.T, a.Hq, a.Hkv, a.D, a.NG) : PreLayout{};
-  const PreGroup* groups = reinterpret_cast<const PreGroup*>(a.ws + PL.group);
-  const int2* pre_tok = reinterpret_cast<const int2*>(a.ws + PL.tok);
-  const int n_items = n_pre + hdr->pf_qtiles * pf_heads_per_unit(a);
+  const int n_items = hdr->pf_qtiles * pf_heads_per_unit(a);
   if (n_items == 0) return;
 
   if (threadIdx.x == 0) {
@@ -286,33 +227,13 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
       for (uint32_t k = 0;; ++k) {
         const int slot = k & 1;
         if (!mbar_wait(bar(SM::bItemFull + slot), (k >> 1) & 1)) { report(a.err, kErrTimeout); break; }
-        const Item it = *item_slot(slot);
+        const PfItem it = *item_slot(slot);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
         if (it.item < 0) break;
         // stage at which the scheduler warp is told to claim the next item
         const int m_claim = max(0, it.nt_all - it.j0 - 3);
-        bool pre = false;
-        if constexpr (kPre) pre = it.pre_n > 0;
-        if constexpr (kPre) if (pre) {
-          // a box per token and half: its G query heads of this KV head, G rows of the tile
-          if (lane == 0) {
-            if (!mbar_wait(bar(SM::bQEmpty), (k & 1) ^ 1)) report(a.err, kErrTimeout);
-            mbar_arrive_expect_tx(bar(SM::bQFull),
-                                  (uint32_t)((it.ntok[0] + it.ntok[1]) * a.G * SM::kHalves * 128));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            for (int i = lane; i < it.ntok[t]; i += 32) {
-              const int tok = pre_tok[it.tok[t] + i].x;
-#pragma unroll
-              for (int half = 0; half < SM::kHalves; ++half)
-                tma_load_3d(sbase + SM::kQ0 + t * SM::kQTile + half * SM::kQHalf + i * a.G * 128,
-                            qmap_tok, bar(SM::bQFull), half * 64, it.head[0], tok);
-            }
-        }
-        if (!pre && lane == 0) {
+        if (lane == 0) {
           if (!mbar_wait(bar(SM::bQEmpty), (k & 1) ^ 1)) report(a.err, kErrTimeout);
           mbar_arrive_expect_tx(bar(SM::bQFull), (it.hasB ? 2 : 1) * SM::kQTile);
 #pragma unroll
@@ -422,14 +343,8 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
           if (kc == 0 && item >= 0) atomicMin(&hdr->t_pf_start, global_ns());  // role span
         }
         item = __shfl_sync(0xffffffffu, item, 0);
-        Item it;
-        if constexpr (kPre) {
-          it.pre_n = 0;
-          if (item >= 0 && item < n_pre) it = pre_decode_item(item, a, groups, n_groups);
-        }
-        if (item >= n_pre)
-          static_cast<PfItemBase&>(it) =
-              pf_decode_item<kWin>(item - n_pre, a, pf_seq, pf_prefix, pf_order, n_pf);
+        PfItem it;
+        if (item >= 0) it = pf_decode_item<kWin>(item, a, pf_seq, pf_prefix, pf_order, n_pf);
         it.item = item;
         if (lane == 0) {
           *item_slot(slot) = it;
@@ -509,7 +424,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         const int slot = k & 1;
         wait(bar(SM::bItemFull + slot), (k >> 1) & 1);
         if (!ok) break;
-        const Item it = *item_slot(slot);
+        const PfItem it = *item_slot(slot);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
         if (it.item < 0) break;
@@ -571,7 +486,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
     for (uint32_t k = 0;; ++k) {
       const int slot = k & 1;
       if (!mbar_wait(bar(SM::bItemFull + slot), (k >> 1) & 1)) { report(a.err, kErrTimeout); break; }
-      const Item it = *item_slot(slot);
+      const PfItem it = *item_slot(slot);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
       if (it.item < 0) break;
@@ -582,11 +497,8 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
       const int tok = t ? it.tok[1] : it.tok[0];
       const int rows = t ? it.rows[1] : it.rows[0];
       const int head = t ? it.head[1] : it.head[0];
-      bool pre = false;
-      if constexpr (kPre) pre = it.pre_n > 0;
-      // row 0's and row r's last key (in a prefix, its last one for every row)
-      const int diag0 = pre ? it.ctx - 1 : it.ctx + (t ? it.qoff[1] : it.qoff[0]);
-      const int limit = pre ? diag0 : diag0 + r;
+      const int diag0 = it.ctx + (t ? it.qoff[1] : it.qoff[0]);  // row 0's last key
+      const int limit = diag0 + r;                                     // row r's last key
       float m_run = -INFINITY, l_run = 0.f;
       bool ok = true;
       const int W = kWin ? a.window : 0;
@@ -702,34 +614,6 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
       if (!mbar_wait(bar(SM::bOFinal + t), kx & 1)) { report(a.err, kErrTimeout); break; }
       __syncwarp();
       tc_fence_after();
-      if constexpr (kPre) if (pre) {
-        // ---- epilogue of a prefix part: (m, l) and O as they are, to the token's slot
-        float2* part_ml = reinterpret_cast<float2*>(a.ws + PL.part_ml);
-        float* part_o = reinterpret_cast<float*>(a.ws + PL.part_o);
-        const int i_tok = r / a.G;
-        const size_t row = ((size_t)(t ? it.slot[1] : it.slot[0]) + i_tok) * a.Hq + head +
-                           (r - i_tok * a.G);
-#pragma unroll
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t ov[32];
-          tmem_ld32(t_lane + o_col + ch * 32, ov);
-          tc_wait_ld();
-          if (r < rows) {
-            uint4* dst = reinterpret_cast<uint4*>(part_o + row * D + ch * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(SM::bOFree + t));
-        gx += nt - it.j0;
-        kx += 1;
-        if (r < rows) part_ml[row] = make_float2(m_run, l_run);
-        if (r == 0) atomicMax(&hdr->t_pf_end, global_ns());
-        continue;
-      }
       const float inv = 1.f / l_run;
       const bool store = r < rows;
       // Each 32-column slice of the warp's 32 rows goes through shared memory: lane = row on

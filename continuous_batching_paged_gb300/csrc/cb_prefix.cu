@@ -8,15 +8,14 @@
 //
 // Own keys are streamed by the decode pass (cb_decode.cuh), as ever, from the prefix's end on; a
 // member with up to kPreMaxQ query tokens has one record per token.  The prefix is a dense
-// contraction (all rows of the group see all its keys), so it runs on the 5th-generation tensor
-// cores, in the chunk pass (cb_prefill.cuh): tiles of 128 rows = 128 / G query tokens with the G
-// heads of one KV head, gathered by TMA, two tiles per work item against the same K/V tiles, no
-// mask but the prefix's end, O and (m, l) left unnormalised in fp32.  K/V of the prefix are read
-// once per 2 x 128 rows (by L2 at most once from HBM) instead of once per query token, which is
-// what bounds the batch otherwise.  The two passes run side by side in one launch, no part waits
-// for another, and a last small launch merges the parts, a warp per (token, query head).  (Merged by
-// whoever counted last, as the decode pass merges its own splits, the prefix's few warps merged
-// a tile's tokens one after the other: 64 sequences sharing 1024 keys took 96 us.)
+// contraction (all rows of the group see all its keys) and runs on the 5th-generation tensor cores
+// (cb_prefix.cuh): its K/V are read once per 2 x 128 rows (from HBM at most once) instead of once
+// per query token, which is what bounds the batch otherwise.  The passes run side by side in one
+// launch, each on the SMs that the planner gives it, no part of either waits for another, and a
+// last small launch merges the parts, a warp per (token, query head).  (Merged by whoever counted
+// last, as the decode pass merges its own splits, a tile's tokens were merged one after the other
+// by the few warps that finished last: 64 sequences sharing 1024 keys took 96 us, now see
+// launch_prefix_attention.)
 #include "cb_attention.cuh"
 #include "cb_plan.cuh"
 
@@ -48,7 +47,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 template <int D, int QS>
 static cudaError_t launch_instance(const AttnArgs& a, const AttnMaps& m, const CUtensorMap& q_tok,
                                    cudaStream_t stream) {
-  constexpr int kSmem = AttnSmem<D, QS>::kTotal;
+  constexpr int kSmem = AttnSmem<D, QS, true>::kTotal;
   // a setting of the context, as for the attention kernel without prefixes
   static unsigned long long configured_ctx = 0;
   const unsigned long long ctx = launch_context_id();
@@ -63,7 +62,7 @@ static cudaError_t launch_instance(const AttnArgs& a, const AttnMaps& m, const C
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.decode_grid + a.prefill_ctas);
+  cfg.gridDim = dim3(a.decode_grid + a.pre_ctas + a.prefill_ctas);
   cfg.blockDim = dim3(kAttnThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
@@ -74,80 +73,112 @@ static cudaError_t launch_instance(const AttnArgs& a, const AttnMaps& m, const C
 }
 
 // One warp per (query token, query head) of the shared prefixes: M = max m_c, w_c = 2^(m_c - M),
-// out = sum_c w_c o_c / sum_c w_c l_c, lse = (M + log2 sum_c w_c l_c) ln 2 over the prefix's parts,
-// then the parts of the own keys that decode CTAs cf .. cl left.  Every part holds at least one
-// key, so its m is finite.  Bound by the latency of its loads: kC parts at a time, all loaded
-// before any is used.
+// out = sum_c w_c o_c / sum_c w_c l_c, lse = (M + log2 sum_c w_c l_c) ln 2 over the parts c of the
+// prefix's chain and of the own keys.  Every part that exists holds at least one key, so its m is
+// finite.  Bound by latency: a lane finds a part and loads its (m, l), so all are there after one
+// trip to L2, and the rows of O follow kC at a time.
 constexpr int kMergeThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnArgs a) {
-  constexpr int PER = D / 32, kC = 4;
+  constexpr int PER = D / 32, kC = 8;  // columns per lane, rows of O in flight
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D);
-  const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.Hkv, a.D, a.NG);
+  const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG);
   const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.ws + L.header);
-  const int2* pre_tok = reinterpret_cast<const int2*>(a.ws + PL.tok);
+  const int2* list = reinterpret_cast<const int2*>(a.ws + PL.tok);
   const int4* pre_rec = reinterpret_cast<const int4*>(a.ws + PL.rec);
   const int4* dec_rec = reinterpret_cast<const int4*>(a.ws + L.dec_rec);
-  const float2* pre_ml = reinterpret_cast<const float2*>(a.ws + PL.part_ml);
-  const float* pre_o = reinterpret_cast<const float*>(a.ws + PL.part_o);
-  const float2* own_ml = reinterpret_cast<const float2*>(a.ws + L.part_ml);
-  const float* own_o = reinterpret_cast<const float*>(a.ws + L.part_o);
+  const PreGroup* groups = reinterpret_cast<const PreGroup*>(a.ws + PL.group);
   __nv_bfloat16* outg = static_cast<__nv_bfloat16*>(a.out);
   const long long rows = (long long)hdr->pre_tokens * a.Hq;
-  const long long ntiles = hdr->dec_tiles;
-  const int N = hdr->decode_ctas;
+  const long long ntiles = hdr->dec_tiles, W = hdr->pre_cost;
+  const int N = hdr->decode_ctas, NP = hdr->pre_ctas;
+  const int per_tile = pre_tile_tokens(a.G);
   for (long long row = (long long)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5); row < rows;
        row += (long long)gridDim.x * (kMergeThreads / 32)) {
     const int i = (int)(row / a.Hq), head = (int)(row - (long long)i * a.Hq);
-    const int2 tr = pre_tok[i];
-    const int4 rec = pre_rec[tr.y];  // prefix length, first slot, slots between parts, parts
-    const int cf = cta_of_tile(dec_rec[tr.y].w, ntiles, N);
-    const int cl = cta_of_tile(dec_rec[tr.y + 1].w - 1, ntiles, N);
-    const int nparts = rec.w + cl - cf + 1;
+    const int kvh = head / a.G;
+    const int2 tr = list[i];
+    const int4 rec = pre_rec[tr.y];
+    const PreGroup g = groups[rec.y];
+    // own keys: decode CTAs df .. dl
+    const int df = cta_of_tile(dec_rec[tr.y].w, ntiles, N);
+    const int dl = cta_of_tile(dec_rec[tr.y + 1].w - 1, ntiles, N);
+    // the prefix: the chain of this token's unit, prefix CTAs pf .. pl
+    const PreShape sh = pre_shape(g.n_tok, g.keys, a.G);
+    const int tile = rec.z / per_tile, u = tile >> 1;
+    const int w = u < sh.full ? kPreCost2 : kPreCost1;
+    const long long cs = g.cost0 + kvh * sh.per + (long long)u * kPreCost2 * sh.nt;
+    const int pf = cta_of_tile(cs, W, NP), pl = cta_of_tile(cs + (long long)w * sh.nt - 1, W, NP);
+    const int n_pre = pl - pf + 1, nparts = n_pre + dl - df + 1;
+    // row of this (token, head) in its tile, for the parts in a CTA's own rows
+    const int in_tile = (rec.z - tile * per_tile) * a.G + head - kvh * a.G;
     float M = -INFINITY, l = 0.f, acc[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) acc[k] = 0.f;
-    for (int c0 = 0; c0 < nparts; c0 += kC) {
-      float2 ml[kC];
-      float v[kC][PER];
-#pragma unroll
-      for (int cc = 0; cc < kC; ++cc) {
-        const int c = c0 + cc;
-        ml[cc] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int k = 0; k < PER; ++k) v[cc][k] = 0.f;
-        if (c < nparts) {
-          const bool pre = c < rec.w;
-          const size_t at = (pre ? (size_t)rec.y + (size_t)c * rec.z
-                                 : (size_t)(cf + c - rec.w) + tr.y) * a.Hq + head;
-          ml[cc] = (pre ? pre_ml : own_ml)[at];
-          const float* po = (pre ? pre_o : own_o) + at * D + lane * PER;
-          if constexpr (PER == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(po);
-            v[cc][0] = x.x; v[cc][1] = x.y; v[cc][2] = x.z; v[cc][3] = x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(po);
-            v[cc][0] = x.x; v[cc][1] = x.y;
-          }
-        }
+    for (int p0 = 0; p0 < nparts; p0 += 32) {
+      const int p = p0 + lane;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      unsigned long long po = 0;
+      bool have = false;
+      if (p < n_pre) {
+        const int c = pf + p;
+        const int j0 = pre_step(cs, w, sh.nt, pre_bound(W, c, NP));
+        const int j1 = pre_step(cs, w, sh.nt, pre_bound(W, c + 1, NP));
+        have = j0 < j1;  // (a range may end before the step that its last unit of cost lies in)
+        const bool cut = j0 > 0;
+        const size_t at = cut ? ((size_t)c * 2 + (tile & 1)) * kPrefillTileM + in_tile
+                              : (size_t)i * a.Hq + head;
+        if (have) ml = reinterpret_cast<const float2*>(a.ws + (cut ? PL.cut_ml : PL.base_ml))[at];
+        po = (unsigned long long)(reinterpret_cast<const float*>(a.ws + (cut ? PL.cut_o : PL.base_o)) +
+                                  at * D);
+      } else if (p < nparts) {
+        const size_t at = ((size_t)(df + p - n_pre) + tr.y) * a.Hq + head;
+        have = true;
+        ml = reinterpret_cast<const float2*>(a.ws + L.part_ml)[at];
+        po = (unsigned long long)(reinterpret_cast<const float*>(a.ws + L.part_o) + at * D);
       }
-      float mn = M;
+      float mn = ml.x;
 #pragma unroll
-      for (int cc = 0; cc < kC; ++cc) mn = fmaxf(mn, ml[cc].x);
-      const float sc = fast_exp2(M - mn);
-      l *= sc;
+      for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      mn = fmaxf(mn, M);
+      const float sc = fast_exp2(M - mn), wt = have ? fast_exp2(ml.x - mn) : 0.f;
+      float ls = wt * ml.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+      l = l * sc + ls;
+      M = mn;
 #pragma unroll
       for (int k = 0; k < PER; ++k) acc[k] *= sc;
+      unsigned left = __ballot_sync(0xffffffffu, have);
+      while (left) {
+        float v[kC][PER], wc[kC];
 #pragma unroll
-      for (int cc = 0; cc < kC; ++cc) {
-        const float w = fast_exp2(ml[cc].x - mn);  // 0 past the last part
-        l += w * ml[cc].y;
+        for (int cc = 0; cc < kC; ++cc) {
+          const int src = left ? __ffs(left) - 1 : -1;
+          left &= left - 1;  // (0 stays 0)
+          wc[cc] = __shfl_sync(0xffffffffu, wt, src & 31);
+          const float* o = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, po, src & 31)) +
+                           lane * PER;
+          if (src < 0) wc[cc] = 0.f;
 #pragma unroll
-        for (int k = 0; k < PER; ++k) acc[k] += w * v[cc][k];
+          for (int k = 0; k < PER; ++k) v[cc][k] = 0.f;
+          if (src >= 0) {
+            if constexpr (PER == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(o);
+              v[cc][0] = x.x; v[cc][1] = x.y; v[cc][2] = x.z; v[cc][3] = x.w;
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(o);
+              v[cc][0] = x.x; v[cc][1] = x.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int cc = 0; cc < kC; ++cc)
+#pragma unroll
+          for (int k = 0; k < PER; ++k) acc[k] += wc[cc] * v[cc][k];
       }
-      M = mn;
     }
     const float inv = 1.f / l;
     uint32_t* dst = reinterpret_cast<uint32_t*>(outg + ((size_t)tr.x * a.Hq + head) * D + lane * PER);
