@@ -394,8 +394,7 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   if (dctas <= 0) dctas = ds->sm_count / head_groups > 0 ? ds->sm_count / head_groups : 1;
   if (dctas > CB_MAX_DECODE_CTAS) dctas = CB_MAX_DECODE_CTAS;
   a.decode_ctas = dctas;
-  a.prefill_ctas = ds->sm_count;
-  a.pre_ctas = NG == 0 ? 0 : ds->sm_count < cb::kMaxPreCtas ? ds->sm_count : cb::kMaxPreCtas;
+  a.prefill_ctas = a.chunk_ctas = ds->sm_count;
   a.R = R;
   a.prefix_group = NG > 0 ? prefix->prefix_group : nullptr;
   a.prefix_lens = NG > 0 ? prefix->prefix_lens : nullptr;
@@ -460,7 +459,7 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   if (serial) {
     cb::AttnArgs d = a;
     d.decode_grid = a.decode_ctas * head_groups;
-    d.prefill_ctas = d.pre_ctas = 0;
+    d.prefill_ctas = 0;
     if ((e = launch_pass(d, s)) != cudaSuccess) return cuda_fail(e, "attention launch");
     if ((e = mark(2)) != cudaSuccess || (e = mark(3)) != cudaSuccess)
       return cuda_fail(e, "cudaEventRecord(phase event)");

@@ -36,21 +36,28 @@ __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorM
   // the merge of the prefixes' parts may start once every CTA of this kernel has (it waits itself)
   if constexpr (kPre) asm volatile("griddepcontrol.launch_dependents;");
   const int b = (int)blockIdx.x;
+  PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D).header);
+  if constexpr (kPre) {
+    // The decode CTAs that the planner leaves without work are the first prefix CTAs; where those
+    // are too few, some of the chunk CTAs are the others.
+    const int N = hdr->decode_ctas;
+    const int c = b < a.decode_grid
+                      ? pre_idle_index(b % a.decode_ctas, b / a.decode_ctas, N, a.decode_ctas)
+                      : pre_idle_count(pre_head_groups(a.Hkv, a.G), N, a.decode_ctas) + b -
+                            a.decode_grid;
+    if (c >= 0 && c < hdr->pre_ctas) {
+      prefix_cta<D>(a, qmap_tok, kmap_chunk, vmap_chunk, smem_raw, c);
+      return;
+    }
+  }
   if (b < a.decode_grid) {
     // Span of the decode role: first start and last end of any warp of a CTA with work (the
     // chunk role stamps its own span inside prefill_cta).
-    PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D).header);
     const bool busy = hdr->dec_tiles > 0;
     if (threadIdx.x == 0 && busy) atomicMin(&hdr->t_dec_start, global_ns());
     decode_cta<D, QS, kPre>(a, kmap_dec, vmap_dec, smem_raw, b % a.decode_ctas, b / a.decode_ctas);
     if ((threadIdx.x & 31) == 0 && busy) atomicMax(&hdr->t_dec_end, global_ns());
     return;
-  }
-  if constexpr (kPre) {
-    if (b < a.decode_grid + a.pre_ctas) {
-      prefix_cta<D>(a, qmap_tok, kmap_chunk, vmap_chunk, smem_raw, b - a.decode_grid);
-      return;
-    }
   }
   prefill_cta<D, kWin>(a, qmap, kmap_chunk, vmap_chunk, smem_raw);
 }

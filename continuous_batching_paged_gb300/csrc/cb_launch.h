@@ -48,7 +48,7 @@ struct AttnArgs {
                        // 0 when the launch runs the chunk pass only)
   int decode_auto;     // 1: the planner picks how many of them work (decode / chunk balance)
   int prefill_ctas;    // persistent CTAs of the chunk pass (0 when the launch runs decode only)
-  int pre_ctas;        // CTAs of the shared prefixes' pass of this launch (<= kMaxPreCtas)
+  int chunk_ctas;      // the same, whatever this launch runs (for the planner)
   int R;               // decode records the workspace is laid out for (S; pre_records(S, T) with
                        // shared prefixes)
   const int32_t* prefix_group;  // [S]: the group whose prefix a sequence shares, or -1

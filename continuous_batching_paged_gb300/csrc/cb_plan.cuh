@@ -152,114 +152,123 @@ __device__ inline int pf_unit_bin(const AttnArgs& a, const int32_t* pf_seq, cons
   return kCostBins - 1 - min(tiles, kCostBins - 1);
 }
 
-// With shared prefixes: which groups' prefixes are computed once.  Fills the group list, the map
-// from group number to it (-1: every member's own pass does it all) and zeroes the count of tokens
-// listed so far.  Returns the work of the prefixes in cost units (0: no group takes part; the same
-// in every thread).
+// Up to this many groups the planner keeps in shared memory.
+constexpr int kPlanSmemGroups = 1024;
+
+// What the first look at a sequence finds (kept for the second where one round covers the batch).
+struct PreSeq {
+  int c0, c1, kv, group, keys;
+};
+
+// With shared prefixes: which groups' prefixes are computed once.  Fills the group list, and per
+// group number: map (index in the list, -1: every member's own pass does it all), tok0 (its first
+// entry of the token list) and cnt (the tokens listed so far: 0).  Returns the work of the prefixes
+// per KV head in cost units (0: no group takes part; the same in every thread).
 //
 // A group takes part when it has at least two query tokens (from members with at most kPreMaxQ
 // each) and kPreMinKeys keys; after bad metadata none does, and each sequence is computed alone.
-__device__ __forceinline__ long long plan_prefixes(const AttnArgs& a, int (*sw)[4]) {
+__device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], int32_t* cnt,
+                                             int32_t* first, int32_t* map, PreSeq& mine) {
   const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG);
-  int32_t* cnt = reinterpret_cast<int32_t*>(a.ws + PL.cnt);
-  int32_t* first = reinterpret_cast<int32_t*>(a.ws + PL.first);
-  int32_t* map = reinterpret_cast<int32_t*>(a.ws + PL.map);
   PreGroup* groups = reinterpret_cast<PreGroup*>(a.ws + PL.group);
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D).header);
   const int tid = threadIdx.x;
   const long long max_kv = (long long)a.max_blocks * a.bs;
-  __shared__ long long s_scan[kPlanThreads / 32 + 1];
+  __shared__ unsigned long long s_total;
+  if (tid == 0) s_total = 0;
   for (int g = tid; g < a.NG; g += kPlanThreads) {
     cnt[g] = 0;
     first[g] = 0x7fffffff;
   }
-  __syncthreads();
+  const int my_keys = tid < a.NG ? a.prefix_lens[tid] : 0;  // (first round of the loops over groups)
   bool bad = false;
-  for (int s = tid; s < a.S; s += kPlanThreads) {
-    const int c0 = a.cu_seqlens_q[s], c1 = a.cu_seqlens_q[s + 1], kv = a.kv_lens[s];
-    const int q_len = c1 - c0;
-    if (c0 < 0 || c1 > a.T || (s == 0 && c0 != 0) || q_len < 0 || kv < q_len || kv > max_kv) {
-      bad = true;  // reported with the lengths
-      continue;
+  for (int base = 0; base < a.S; base += kPlanThreads) {
+    const int s = base + tid;
+    PreSeq q = {0, 0, 0, -1, 0};
+    if (s < a.S) {
+      q.c0 = a.cu_seqlens_q[s];
+      q.c1 = a.cu_seqlens_q[s + 1];
+      q.kv = a.kv_lens[s];
+      q.group = a.prefix_group[s];
     }
-    const int g = a.prefix_group[s];
-    if (q_len == 0 || g == -1) continue;
-    const int keys = g >= 0 && g < a.NG ? a.prefix_lens[g] : -1;
-    if (keys < 0 || keys > kv - q_len) {
-      report(a.err, kErrOutOfRange);
-      bad = true;
-    } else if (q_len <= kPreMaxQ) {
-      atomicAdd(&cnt[g], q_len);
-      atomicMin(&first[g], s);
+    const int q_len = q.c1 - q.c0;
+    const bool lens_ok = !(q.c0 < 0 || q.c1 > a.T || (s == 0 && q.c0 != 0) || q_len < 0 ||
+                           q.kv < q_len || q.kv > max_kv);
+    bool group_ok = true, member = lens_ok && s < a.S && q_len > 0 && q.group != -1;
+    if (member) {
+      q.keys = q.group >= 0 && q.group < a.NG ? a.prefix_lens[q.group] : -1;
+      group_ok = q.keys >= 0 && q.keys <= q.kv - q_len;
+      if (!group_ok) report(a.err, kErrOutOfRange);
+      member = group_ok && q_len <= kPreMaxQ;
+    }
+    bad |= !lens_ok || !group_ok;  // (bad lengths are reported by the caller)
+    if (base == 0) {
+      __syncthreads();  // cnt and first are set
+      mine = q;
+    }
+    if (member) {
+      atomicAdd(&cnt[q.group], q_len);
+      atomicMin(&first[q.group], s);
     }
   }
   bad = __syncthreads_or(bad) != 0;
-  int carry[4] = {0, 0, 0, 0};  // groups, tokens
-  long long cost_carry = 0;
+  auto shared_tokens = [&](int g, int keys) {  // tokens of group g if its prefix is computed once
+    return bad || g >= a.NG || cnt[g] < 2 || keys < kPreMinKeys ? 0 : cnt[g];
+  };
+  for (int g = tid; g < a.NG; g += kPlanThreads) {
+    const int keys = g == tid ? my_keys : a.prefix_lens[g], n = shared_tokens(g, keys);
+    if (n > 0) atomicAdd(&s_total, (unsigned long long)pre_shape(n, keys, a.G).per);
+  }
+  __syncthreads();
+  if (s_total > kPreMaxCost) bad = true;  // (32 bits hold every cost below)
+  int carry[4] = {0, 0, 0, 0};  // groups, tokens, cost
   for (int base = 0; base < a.NG; base += kPlanThreads) {
     const int g = base + tid;
-    const int n = bad || g >= a.NG || cnt[g] < 2 || a.prefix_lens[g] < kPreMinKeys ? 0 : cnt[g];
-    int v[4] = {n > 0, n, 0, 0}, ex[4], tot[4];
-    long long cost = n > 0 ? pre_cost_per_head(n, a.prefix_lens[g], a.G) * a.Hkv : 0;
+    const int keys = base == 0 ? my_keys : g < a.NG ? a.prefix_lens[g] : 0;
+    const int n = shared_tokens(g, keys);
+    int v[4] = {n > 0, n, n > 0 ? (int)pre_shape(n, keys, a.G).per : 0, 0}, ex[4], tot[4];
     block_scan4(v, ex, tot, sw);  // (its barriers also part the reads of cnt from the writes)
-    // the same scan of the costs, in 64 bits
-    const long long own = cost;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, cost, o);
-      if ((tid & 31) >= o) cost += y;
-    }
-    if ((tid & 31) == 31) s_scan[tid >> 5] = cost;
-    __syncthreads();
-    if (tid < 32) {
-      long long x = s_scan[tid];
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (tid >= o) x += y;
-      }
-      s_scan[tid] = x;
-    }
-    __syncthreads();
-    const long long before = cost - own + (tid >= 32 ? s_scan[(tid >> 5) - 1] : 0);
+    if (n > 0)
+      groups[carry[0] + ex[0]] = {carry[2] + ex[2], n, carry[1] + ex[1], keys, first[g]};
     if (g < a.NG) {
       map[g] = n > 0 ? carry[0] + ex[0] : -1;
       cnt[g] = 0;
+      first[g] = carry[1] + ex[1];  // from here on: tok0
     }
-    if (n > 0)
-      groups[carry[0] + ex[0]] = {cost_carry + before, n, carry[1] + ex[1], a.prefix_lens[g], first[g]};
-    carry[0] += tot[0];
-    carry[1] += tot[1];
-    cost_carry += s_scan[kPlanThreads / 32 - 1];
-    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) carry[k] += tot[k];
   }
   if (tid == 0) {
     hdr->pre_groups = carry[0];
     hdr->pre_tokens = carry[1];
-    hdr->pre_cost = cost_carry;
+    hdr->pre_cost = carry[2];
   }
   __syncthreads();
-  return cost_carry;
+  return carry[2];
 }
 
-// Decode and prefix CTA counts where prefixes are computed apart.  Called by one full warp.
-// Model, fitted to GB300 measurements: decode on n SMs streams as in choose_decode_ctas; a cost
-// unit of the prefixes takes 0.7 us of an SM (a step with one tile of rows 1.4, with two 2.1); chunk
-// work follows on the SMs that the prefixes leave, so it is counted with them.  The two sides run at
-// once, so the choice is the n with the least max(decode, prefix + chunk), the smallest such n.
-__device__ __forceinline__ int choose_prefix_split(float dec_bytes, float cost, float chunk_flops,
-                                                   int head_groups, int max_ctas, int sms,
-                                                   long long tiles) {
+// Decode CTAs per head group where prefixes are computed apart; the other SMs are the prefixes'.
+// Called by one full warp.  Model, fitted to GB300 measurements of the two passes side by side: n
+// decode CTAs stream as in choose_decode_ctas, or take 1.1 us per 64 KB stage (0.8 at least) and 1
+// us per record, 4 us to start; a cost unit of the prefixes takes 0.95 us of an SM, 8 us to start
+// and end; chunk work follows on the prefixes' SMs, so it is counted with them.  The choice is the
+// n with the least max(decode, prefix + chunk), the largest such n.
+__device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes, float cost,
+                                                   float chunk_flops, long long tiles, int records) {
   const int lane = threadIdx.x & 31;
-  const int cap = (int)(tiles < max_ctas ? tiles : max_ctas);
-  const float w_us = cost * 0.7f + chunk_flops * (1.f / 6.4e6f);
+  const int hg = pre_head_groups(a.Hkv, a.G), sms = a.chunk_ctas;
+  const int cap = (int)(tiles < a.decode_ctas ? tiles : a.decode_ctas);
+  const float w_us = cost * 0.95f + chunk_flops * (1.f / 6.4e6f);
   const float b_mb = dec_bytes * 1e-6f;
+  const float stage_kb = (float)(a.Hkv < 8 ? a.Hkv : 8) * (float)a.D * (1.f / 16.f);
+  const float tile_us = (float)tiles * fmaxf(0.8f, stage_kb * (1.1f / 64.f)) + (float)records;
   float best = 3.4e38f;
-  int best_n = cap < 1 ? 1 : cap;
-  for (int i = lane; 2 * (i + 1) * head_groups < sms && 2 * (i + 1) <= cap; i += 32) {
-    const int n = 2 * (i + 1), m = sms - n * head_groups;
-    const float lin = 0.11f * n * head_groups, sat = 6.8f;
+  int best_n = 1;
+  for (int n = 2 * (lane + 1); n <= (cap > 2 ? cap : 2) && n * hg < sms; n += 64) {
+    const float lin = 0.11f * n * hg, sat = 6.8f;
     const float bw = rcbrtf(1.f / (lin * lin * lin) + 1.f / (sat * sat * sat));
-    const float t = fmaxf(b_mb / bw, w_us / (float)m);
-    if (t < best) {
+    const float t = fmaxf(4.f + fmaxf(b_mb / bw, tile_us / (float)n), 8.f + w_us / (float)(sms - n * hg));
+    if (t <= best) {
       best = t;
       best_n = n;
     }
@@ -267,26 +276,31 @@ __device__ __forceinline__ int choose_prefix_split(float dec_bytes, float cost, 
   for (int o = 16; o > 0; o >>= 1) {
     const float t = __shfl_xor_sync(0xffffffffu, best, o);
     const int n = __shfl_xor_sync(0xffffffffu, best_n, o);
-    if (t < best || (t == best && n < best_n)) {
+    if (t < best || (t == best && n > best_n)) {
       best = t;
       best_n = n;
     }
   }
-  return best_n;
+  return best_n < cap ? best_n : cap;
 }
 
 // Batches of up to this many decode (or chunk) sequences keep the planner's prefix arrays in
 // shared memory as well, so its binary searches cost no global round trips.
 constexpr int kPlanSmemSeqs = 2048;
+// (with shared prefixes half as many, beside kPlanSmemGroups groups)
+template <bool kPre>
+constexpr int plan_smem_seqs() { return kPre ? kPlanSmemSeqs / 2 : kPlanSmemSeqs; }
 
 // kPre: with shared prefixes (a.NG > 0).
 template <bool kPre>
 __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   static_assert(kCostBins == kPlanThreads, "one histogram bin per planner thread");
+  constexpr int kSeqs = plan_smem_seqs<kPre>();
   __shared__ int sw[32][4];
-  __shared__ int32_t s_dec_prefix[kPlanSmemSeqs + 1], s_pf_prefix[kPlanSmemSeqs + 1];
-  __shared__ int32_t s_pf_seq[kPlanSmemSeqs];
-  __shared__ int2 s_pf_lens[kPlanSmemSeqs];  // (q_len, prior context) of each chunk sequence
+  __shared__ int32_t s_dec_prefix[kSeqs + 1], s_pf_prefix[kSeqs + 1];
+  __shared__ int32_t s_pf_seq[kSeqs];
+  __shared__ int2 s_pf_lens[kSeqs];  // (q_len, prior context) of each chunk sequence
+  __shared__ int32_t s_groups[kPre ? 3 * kPlanSmemGroups : 1];
   const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D);
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + L.header);
   int32_t* dec_seq = reinterpret_cast<int32_t*>(a.ws + L.dec_seq);
@@ -299,9 +313,15 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   const long long max_kv = (long long)a.max_blocks * a.bs;
 
   float my_keys = 0.f, my_pairs = 0.f;  // work estimates for the decode / chunk balance
-  long long pre_cost = 0;               // work of the shared prefixes
+  // shared prefixes: their work per KV head, and per group number cnt, tok0 and map
+  int pre_cost = 0;
   const PreLayout PL = kPre ? pre_layout(a.R, a.T, a.Hq, a.D, a.NG) : PreLayout{};
-  if constexpr (kPre) pre_cost = plan_prefixes(a, sw);
+  const bool few = a.NG <= kPlanSmemGroups;
+  int32_t* grp_cnt = few ? s_groups : reinterpret_cast<int32_t*>(a.ws + PL.cnt);
+  int32_t* grp_tok0 = few ? s_groups + kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.first);
+  int32_t* grp_map = few ? s_groups + 2 * kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.map);
+  PreSeq mine = {};
+  if constexpr (kPre) pre_cost = plan_prefixes(a, sw, grp_cnt, grp_tok0, grp_map, mine);
   bool bad = false;
   const int unit_rows = pf_unit_tiles(a.G) * kPrefillTileM;
   int carry[4] = {0, 0, 0, 0};
@@ -309,36 +329,43 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     const int s = base + tid;
     int v[4] = {0, 0, 0, 0};
     int tok = 0, kv = 0;
-    PreGroup grp = {};   // kPre: the group that computes this sequence's prefix (n_tok 0: none)
-    int grp_no = -1, grp_at = 0;
+    int grp = -1, keys = 0;  // kPre: the group that computes this sequence's prefix, its length
     if (s < a.S) {
-      const int c0 = a.cu_seqlens_q[s], c1 = a.cu_seqlens_q[s + 1];
+      int c0, c1;
+      if (kPre && base == 0) {
+        c0 = mine.c0;
+        c1 = mine.c1;
+        kv = mine.kv;
+      } else {
+        c0 = a.cu_seqlens_q[s];
+        c1 = a.cu_seqlens_q[s + 1];
+        kv = a.kv_lens[s];
+      }
       const int q_len = c1 - c0;
-      kv = a.kv_lens[s];
       tok = c0;
       if (s == 0 && c0 != 0) report(a.err, kErrOutOfRange);  // cu_seqlens_q[0] must be 0
       const bool ok = c0 >= 0 && c1 <= a.T && q_len >= 0 && kv >= q_len && kv <= max_kv;
       if (!ok) {
         report(a.err, kErrOutOfRange);
         bad = true;
-      } else if (kPre && q_len > 0 && q_len <= kPreMaxQ && pre_cost > 0 && a.prefix_group[s] >= 0 &&
-                 reinterpret_cast<const int32_t*>(a.ws + PL.map)[a.prefix_group[s]] >= 0) {
+      } else if (kPre && pre_cost > 0 && q_len > 0 && q_len <= kPreMaxQ &&
+                 (grp = base == 0 ? mine.group : a.prefix_group[s]) >= 0 && grp_map[grp] >= 0) {
         // one record per token: the tiles from the one holding the prefix's end to its last key
-        grp_no = a.prefix_group[s];
-        grp_at = reinterpret_cast<const int32_t*>(a.ws + PL.map)[grp_no];
-        grp = reinterpret_cast<const PreGroup*>(a.ws + PL.group)[grp_at];
-        const int first = grp.keys / kDecodeTileKeys * kDecodeTileKeys;
+        keys = base == 0 ? mine.keys : a.prefix_lens[grp];
+        const int first = keys / kDecodeTileKeys * kDecodeTileKeys;
         v[0] = q_len;
         for (int i = 0; i < q_len; ++i)
           v[1] += (kv - q_len + i + 1 - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
-        my_keys += (float)(kv - grp.keys) * (float)q_len;
+        my_keys += (float)(kv - keys) * (float)q_len;
       } else if (q_len == 1) {
+        grp = -1;
         // tiles from the one holding the window's first key (every key without a window)
         const int first = window_first_key(kv - 1, a.window) / kDecodeTileKeys * kDecodeTileKeys;
         v[0] = 1;
         v[1] = (kv - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
         my_keys += (float)(kv - window_first_key(kv - 1, a.window));
       } else if (q_len > 1) {
+        grp = -1;
         v[2] = 1;
         if (a.window > 0) {  // sum over the chunk's rows of min(position + 1, window)
           const float W = (float)a.window;
@@ -355,22 +382,21 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     }
     int ex[4], tot[4];
     block_scan4(v, ex, tot, sw);
-    if (kPre && grp.n_tok > 0) {
+    if (kPre && grp >= 0 && v[0]) {
       // The tokens' places in the group's list come in any order: a row's result does not depend
       // on the tile it is computed in.
-      const int q_len = v[0], first = grp.keys / kDecodeTileKeys * kDecodeTileKeys;
-      const int at = atomicAdd(reinterpret_cast<int32_t*>(a.ws + PL.cnt) + grp_no, q_len);
+      const int q_len = v[0], first = keys / kDecodeTileKeys * kDecodeTileKeys;
+      const int at = atomicAdd(&grp_cnt[grp], q_len);
       int tile = carry[1] + ex[1];
       for (int j = 0; j < q_len; ++j) {
-        const int i = carry[0] + ex[0] + j, keys = kv - q_len + j + 1;
+        const int i = carry[0] + ex[0] + j, n_keys = kv - q_len + j + 1;
         dec_seq[i] = s;
         dec_prefix[i] = tile;
-        dec_rec[i] = make_int4(s, tok + j, keys, tile);
-        if (i < kPlanSmemSeqs) s_dec_prefix[i] = tile;
-        reinterpret_cast<int4*>(a.ws + PL.rec)[i] =
-            make_int4(grp.keys, grp_at, at + j, 1);
-        reinterpret_cast<int2*>(a.ws + PL.tok)[grp.tok0 + at + j] = make_int2(tok + j, i);
-        tile += (keys - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
+        dec_rec[i] = make_int4(s, tok + j, n_keys, tile);
+        if (i < kSeqs) s_dec_prefix[i] = tile;
+        reinterpret_cast<int4*>(a.ws + PL.rec)[i] = make_int4(keys, grp_map[grp], at + j, 1);
+        reinterpret_cast<int2*>(a.ws + PL.tok)[grp_tok0[grp] + at + j] = make_int2(tok + j, i);
+        tile += (n_keys - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
       }
     } else if (v[0]) {
       const int i = carry[0] + ex[0];
@@ -378,13 +404,13 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       dec_seq[i] = s;
       dec_prefix[i] = carry[1] + ex[1];
       dec_rec[i] = make_int4(s, tok, kv, carry[1] + ex[1]);
-      if (i < kPlanSmemSeqs) s_dec_prefix[i] = carry[1] + ex[1];
+      if (i < kSeqs) s_dec_prefix[i] = carry[1] + ex[1];
     }
     if (v[2]) {
       const int i = carry[2] + ex[2];
       pf_seq[i] = s;
       pf_prefix[i] = carry[3] + ex[3];
-      if (i < kPlanSmemSeqs) {
+      if (i < kSeqs) {
         s_pf_seq[i] = s;
         s_pf_prefix[i] = carry[3] + ex[3];
         const int q_len = a.cu_seqlens_q[s + 1] - a.cu_seqlens_q[s];
@@ -403,8 +429,8 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     dec_prefix[carry[0]] = carry[1];
     dec_rec[carry[0]] = make_int4(-1, 0, 0, carry[1]);
     pf_prefix[carry[2]] = carry[3];
-    if (carry[0] <= kPlanSmemSeqs) s_dec_prefix[carry[0]] = carry[1];
-    if (carry[2] <= kPlanSmemSeqs) s_pf_prefix[carry[2]] = carry[3];
+    if (carry[0] <= kSeqs) s_dec_prefix[carry[0]] = carry[1];
+    if (carry[2] <= kSeqs) s_pf_prefix[carry[2]] = carry[3];
     hdr->n_dec = carry[0];
     hdr->dec_tiles = carry[1];
     hdr->n_pf = n_pf;
@@ -424,7 +450,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     int32_t* pf_order = reinterpret_cast<int32_t*>(a.ws + L.pf_order);
     hist[tid] = 0;
     __syncthreads();
-    const bool pf_local = n_pf <= kPlanSmemSeqs;
+    const bool pf_local = n_pf <= kSeqs;
     const int32_t* ps = pf_local ? s_pf_seq : pf_seq;
     const int32_t* pp = pf_local ? s_pf_prefix : pf_prefix;
     const int2* lens = pf_local ? s_pf_lens : nullptr;
@@ -463,16 +489,17 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     }
     int n = (int)(ntiles < a.decode_ctas ? (ntiles > 0 ? ntiles : 1) : a.decode_ctas);
     if (kPre && pre_cost > 0) {
-      const int hg = (a.Hkv + (a.G > 8 ? 4 : 8) - 1) / (a.G > 8 ? 4 : 8);
       if (a.decode_auto)
-        n = choose_prefix_split(keys * (float)(a.Hkv * a.D * 4), (float)pre_cost,
-                                pairs * (float)(4 * a.D * a.Hq), hg, a.decode_ctas, a.prefill_ctas,
-                                ntiles);
-      const int left = a.prefill_ctas - n * hg;  // SMs beside the decode CTAs
-      long long np = left > a.prefill_ctas / 8 ? left : a.prefill_ctas / 8;
-      const long long most = pre_cost / (kPreMinSteps * kPreCost1);
-      np = np < most ? np : most;
-      if (tid == 0) hdr->pre_ctas = np < 1 ? 1 : np < a.pre_ctas ? (int)np : a.pre_ctas;
+        n = choose_prefix_split(a, keys * (float)(a.Hkv * a.D * 4), (float)pre_cost * (float)a.Hkv,
+                                pairs * (float)(4 * a.D * a.Hq), ntiles, n_dec);
+      // the decode CTAs without work; where a given number leaves none, an eighth of the chunk CTAs
+      const int idle = pre_idle_count(pre_head_groups(a.Hkv, a.G), n, a.decode_ctas);
+      int np = idle > 0 ? idle : a.chunk_ctas / 8;
+      const long long most = (long long)pre_cost * a.Hkv / (kPreMinSteps * kPreCost1);
+      if (np > most) np = (int)most;
+      if (np > kMaxPreCtas) np = kMaxPreCtas;
+      if (np > a.Hkv) np -= np % a.Hkv;  // as many for each KV head (PreGroup)
+      if (tid == 0) hdr->pre_ctas = np < 1 ? 1 : np;
     } else if (a.decode_auto) {
       n = choose_decode_ctas(keys * (float)(a.Hkv * a.D * 4), pairs * (float)(4 * a.D * a.Hq),
                              n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq), a.decode_ctas,
@@ -493,7 +520,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   for (int i = tid; i < n_dec * a.Hkv * head_groups; i += kPlanThreads) merge_cnt[i] = 0;
   // Indexed by the grid's decode CTA, so that a CTA reads its first sequence in the same round
   // trip as the plan header.
-  const int32_t* dp = n_dec <= kPlanSmemSeqs ? s_dec_prefix : dec_prefix;
+  const int32_t* dp = n_dec <= kSeqs ? s_dec_prefix : dec_prefix;
   for (int bx = tid; bx < a.decode_ctas; bx += kPlanThreads) {
     const int c = decode_cta_index(bx, N, a.decode_ctas);
     int lo = -1;

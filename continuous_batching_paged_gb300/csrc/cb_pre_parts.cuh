@@ -6,12 +6,32 @@
 
 namespace cb {
 
+// Groups of KV heads that the decode CTAs are divided into (8 KV heads, or 4 with more than 8 query
+// heads each).
+__device__ __forceinline__ int pre_head_groups(int Hkv, int G) {
+  const int heads = G > 8 ? kMaxDecodeHeadsPerCta / 2 : kMaxDecodeHeadsPerCta;
+  return (Hkv + heads - 1) / heads;
+}
+// Decode CTAs without work when n of `grid` per head group work, and the index among them of CTA bx
+// of head group hg (-1 if it has work): see decode_cta_index.
+__device__ __forceinline__ int pre_idle_count(int head_groups, int n, int grid) {
+  return head_groups * (grid - n);
+}
+__device__ __forceinline__ int pre_idle_index(int bx, int hg, int n, int grid) {
+  if (decode_cta_index(bx, n, grid) >= 0) return -1;
+  const bool pairs = ((n | grid) & 1) == 0;
+  const int units = pairs ? grid / 2 : grid, wanted = pairs ? n / 2 : n;
+  const int u = pairs ? bx >> 1 : bx;  // (unit 0 always works)
+  const int rank = u - ((int)((long long)(u - 1) * wanted / units) + 1);
+  return hg * (grid - n) + (pairs ? 2 * rank + (bx & 1) : rank);
+}
+
 // Shape of a group's chains.
 struct PreShape {
   int nt;         // K/V tiles of the prefix
   int full;       // units with two tiles of rows (the units before the last, at least)
   int units;      // units in all
-  long long per;  // cost of all units under one KV head
+  long long per;  // cost of all units under one KV head (kPreMaxCost at most, once planned)
 };
 __device__ __forceinline__ PreShape pre_shape(int n_tok, int keys, int G) {
   PreShape s;
@@ -34,8 +54,8 @@ __device__ __forceinline__ long long pre_bound(long long W, int c, int N) { retu
 // belongs to the range that its start lies in.
 __device__ __forceinline__ int pre_step(long long cs, int w, int nt, long long b) {
   if (b <= cs) return 0;
-  const long long j = (b - cs + w - 1) / w;
-  return j < nt ? (int)j : nt;
+  if (b - cs >= (long long)w * nt) return nt;
+  return ((int)(b - cs) + w - 1) / w;
 }
 
 // Part of a chain that one CTA does: K/V tiles [j0, j1) of the prefix of `seq` (keys long) under KV
@@ -49,32 +69,37 @@ struct PreSeg {
 // Walks the parts of one CTA's range, in order.
 struct PreWalk {
   const PreGroup* groups;
-  int n_groups, gi, G;
+  int n_groups, gi, G, head_cost;
   long long b0, b1, pos;
 
-  __device__ __forceinline__ PreWalk(const PreGroup* list, int n, int G_, long long W, int c, int N)
-      : groups(list), n_groups(n), gi(0), G(G_), b0(pre_bound(W, c, N)), b1(pre_bound(W, c + 1, N)),
-        pos(b0) {
-    int hi = n - 1;  // largest index with cost0 <= b0
-    while (gi < hi) {
-      const int mid = (gi + hi + 1) >> 1;
-      if (groups[mid].cost0 <= b0) gi = mid; else hi = mid - 1;
-    }
-  }
+  // W: cost per KV head, of Hkv heads.
+  __device__ __forceinline__ PreWalk(const PreGroup* list, int n, int G_, int Hkv, int W, int c, int N)
+      : groups(list), n_groups(n), gi(-1), G(G_), head_cost(W),
+        b0(pre_bound((long long)W * Hkv, c, N)), b1(pre_bound((long long)W * Hkv, c + 1, N)), pos(b0) {}
 
   __device__ __forceinline__ bool next(PreSeg& s) {
     while (pos < b1) {
-      while (gi + 1 < n_groups && groups[gi + 1].cost0 <= pos) ++gi;
+      const int kvh = (int)(pos / head_cost);
+      const long long head0 = (long long)kvh * head_cost;
+      const int rel = (int)(pos - head0);
+      if (gi < 0) {  // the range's first group: the last one with cost0 <= rel
+        int hi = n_groups - 1;
+        gi = 0;
+        while (gi < hi) {
+          const int mid = (gi + hi + 1) >> 1;
+          if (groups[mid].cost0 <= rel) gi = mid; else hi = mid - 1;
+        }
+      } else if (rel == 0) {
+        gi = 0;
+      } else if (gi + 1 < n_groups && groups[gi + 1].cost0 <= rel) {
+        ++gi;
+      }
       const PreGroup g = groups[gi];
       const PreShape sh = pre_shape(g.n_tok, g.keys, G);
-      const long long rel = pos - g.cost0;
-      const int kvh = (int)(rel / sh.per);
-      const long long unit_cost = (long long)kPreCost2 * sh.nt;
-      const long long in_head = rel - kvh * sh.per;
-      const int u = (int)(in_head / unit_cost);  // (the last unit may be a cheaper one: same index)
+      const int u = (rel - g.cost0) / (kPreCost2 * sh.nt);  // (a cheaper last unit: same index)
       const int w = u < sh.full ? kPreCost2 : kPreCost1;
-      const long long cs = g.cost0 + kvh * sh.per + u * unit_cost;
-      pos = cs + (long long)w * sh.nt;
+      const long long cs = head0 + g.cost0 + u * kPreCost2 * sh.nt;
+      pos = cs + w * sh.nt;
       s.j0 = pre_step(cs, w, sh.nt, b0);
       s.j1 = pre_step(cs, w, sh.nt, b1);
       if (s.j0 >= s.j1) continue;

@@ -62,7 +62,7 @@ static cudaError_t launch_instance(const AttnArgs& a, const AttnMaps& m, const C
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.decode_grid + a.pre_ctas + a.prefill_ctas);
+  cfg.gridDim = dim3(a.decode_grid + a.prefill_ctas);
   cfg.blockDim = dim3(kAttnThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnA
   const PreGroup* groups = reinterpret_cast<const PreGroup*>(a.ws + PL.group);
   __nv_bfloat16* outg = static_cast<__nv_bfloat16*>(a.out);
   const long long rows = (long long)hdr->pre_tokens * a.Hq;
-  const long long ntiles = hdr->dec_tiles, W = hdr->pre_cost;
+  const long long ntiles = hdr->dec_tiles, Wh = hdr->pre_cost, W = Wh * a.Hkv;
   const int N = hdr->decode_ctas, NP = hdr->pre_ctas;
   const int per_tile = pre_tile_tokens(a.G);
   for (long long row = (long long)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5); row < rows;
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnA
     const PreShape sh = pre_shape(g.n_tok, g.keys, a.G);
     const int tile = rec.z / per_tile, u = tile >> 1;
     const int w = u < sh.full ? kPreCost2 : kPreCost1;
-    const long long cs = g.cost0 + kvh * sh.per + (long long)u * kPreCost2 * sh.nt;
+    const long long cs = kvh * Wh + g.cost0 + u * kPreCost2 * sh.nt;
     const int pf = cta_of_tile(cs, W, NP), pl = cta_of_tile(cs + (long long)w * sh.nt - 1, W, NP);
     const int n_pre = pl - pf + 1, nparts = n_pre + dl - df + 1;
     // row of this (token, head) in its tile, for the parts in a CTA's own rows

@@ -43,7 +43,7 @@ struct PreSmem {
 };
 static_assert(PreSmem<128>::kTotal <= 232448 && PreSmem<64>::kTotal <= 232448, "shared memory");
 
-// CTA `c` of the prefix role (all kPrefillThreads threads).
+// CTA `c` < hdr->pre_ctas of the prefix role (all kPrefillThreads threads).
 template <int D>
 __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap* qmap,
                                            const CUtensorMap* kmap, const CUtensorMap* vmap,
@@ -52,7 +52,6 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
   constexpr int NS = SM::kSlots;
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D).header);
   const int N = hdr->pre_ctas;
-  if (c >= N) return;
   const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG);
   const int2* list = reinterpret_cast<const int2*>(a.ws + PL.tok);
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -84,7 +83,7 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
     tmem_relinquish();
   }
   PreWalk walk(reinterpret_cast<const PreGroup*>(a.ws + PL.group), hdr->pre_groups, a.G,
-               hdr->pre_cost, c, N);
+               a.Hkv, hdr->pre_cost, c, N);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -100,7 +99,11 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
         tma_prefetch_desc(kmap);
         tma_prefetch_desc(vmap);
       }
-      const int KB = a.KBp, nsb = kChunkKeys / KB;  // page-run boxes per tile (<= 128)
+      // A tile is nsb page runs of KB keys (a power of two; a box each per half of D).  Each lane
+      // keeps the pool row of one run, 32 / nsb tiles at a time, so block-table loads and divisions
+      // are one per 32 runs, and the next 32 are loaded a batch ahead.
+      const int KB = a.KBp, nsb = kChunkKeys / KB;  // 1 .. 128
+      const int per_batch = nsb < 32 ? 32 / nsb : 1, batches = nsb < 32 ? 1 : nsb / 32;
       uint32_t g = 0;
       bool ok = true;
       auto wait = [&](uint32_t b, uint32_t parity) {  // by lane 0, for the warp
@@ -114,16 +117,22 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
         const int n = s.j1 - s.j0;
         const int n_keys = min(s.keys, s.j1 * kChunkKeys);
         const int32_t* row = a.block_table + (size_t)s.seq * a.max_blocks;
-        // block ids of tile j's page runs (lane = run index mod 32)
-        auto entries = [&](int j, int (&ent)[4]) {
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const int sb = p * 32 + lane, pos = j * kChunkKeys + sb * KB;
-            ent[p] = sb < nsb && pos < n_keys ? __ldg(row + pos / a.bs) : -1;
-          }
+        // Block id of run `run` of the part (-1 behind its keys).
+        auto entry = [&](int run) {
+          const int pos = s.j0 * kChunkKeys + run * KB;
+          return pos < n_keys ? __ldg(row + pos / a.bs) : -1;
         };
-        int e_prev[4] = {-1, -1, -1, -1}, e_cur[4], e_next[4];
-        entries(s.j0, e_cur);
+        // Its pool row (-1: none, or a bad block id, which is reported).
+        auto pool_row = [&](int run, int blk) {
+          const int pos = s.j0 * kChunkKeys + run * KB;
+          if (pos >= n_keys) return -1;
+          if (blk < 0 || blk >= a.P) {
+            report(a.err, kErrOutOfRange);
+            return -1;
+          }
+          return blk * a.bs + pos % a.bs;
+        };
+        int blk_next = entry(lane);
         wait(bar(SM::bQEmpty), (k & 1) ^ 1);
         if (!ok) break;
         if (lane == 0)
@@ -139,47 +148,78 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
               tma_load_3d(sbase + t * SM::kTile + half * SM::kHalf + i * a.G * 128, qmap,
                           bar(SM::bQFull), half * 64, s.kvh * a.G, tok);
           }
-        // K or V tile j into the next slot (a run with a bad block id is skipped and reported)
-        auto load = [&](int j, const int (&ent)[4], const CUtensorMap* map, bool report_bad) {
+        // K or V tile into the next slot: the runs whose pool rows the lanes of `lanes` hold
+        auto load = [&](int token, uint32_t lanes, const CUtensorMap* map) {
           const uint32_t slot = g % NS, full = bar(SM::bFull + slot);
           wait(bar(SM::bEmpty + slot), ((g / NS) & 1) ^ 1);
           if (!ok) return;
-          uint32_t runs = 0;
-          bool valid[4];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const int sb = p * 32 + lane;
-            const bool want = sb < nsb && j * kChunkKeys + sb * KB < n_keys;
-            valid[p] = want && ent[p] >= 0 && ent[p] < a.P;
-            if (report_bad && want && !valid[p]) report(a.err, kErrOutOfRange);
-            runs += __popc(__ballot_sync(0xffffffffu, valid[p]));
-          }
-          if (lane == 0) mbar_arrive_expect_tx(full, runs * (uint32_t)(SM::kHalves * KB * 128));
+          lanes &= __ballot_sync(0xffffffffu, token >= 0);
+          if (lane == 0)
+            mbar_arrive_expect_tx(full, __popc(lanes) * (uint32_t)(SM::kHalves * KB * 128));
           __syncwarp();
-          const uint32_t dst = sbase + SM::kRing + slot * SM::kTile;
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            if (!valid[p]) continue;
-            const int sb = p * 32 + lane, pos = j * kChunkKeys + sb * KB;
-            const int token = ent[p] * a.bs + (pos % a.bs);
+          if ((lanes >> lane) & 1) {
+            const uint32_t dst = sbase + SM::kRing + slot * SM::kTile + (lane & (nsb - 1)) * KB * 128;
 #pragma unroll
             for (int half = 0; half < SM::kHalves; ++half)
-              tma_load_3d(dst + half * SM::kHalf + sb * KB * 128, map, full, half * 64, s.kvh, token);
+              tma_load_3d(dst + half * SM::kHalf, map, full, half * 64, s.kvh, token);
           }
           ++g;
         };
-        for (int i = 0; i <= n && ok; ++i) {
-          if (i + 1 < n) entries(s.j0 + i + 1, e_next);
-          if (i < n) load(s.j0 + i, e_cur, kmap, true);
-          if (s.two) {
-            if (i < n) load(s.j0 + i, e_cur, vmap, false);
-          } else if (i > 0) {
-            load(s.j0 + i - 1, e_prev, vmap, false);
+        if (batches == 1) {
+          const uint32_t tile_lanes = nsb == 32 ? 0xffffffffu : (1u << nsb) - 1u;
+          int t_cur = -1, t_prev = -1;  // this batch's pool rows, and the batch's before it
+          for (int i = 0; i <= n && ok; ++i) {
+            const int in_batch = i & (per_batch - 1);
+            if (in_batch == 0) {
+              t_prev = t_cur;
+              t_cur = pool_row(i * nsb + lane, blk_next);
+              blk_next = entry((i + per_batch) * nsb + lane);
+            }
+            if (i < n) {
+              load(t_cur, tile_lanes << (in_batch * nsb), kmap);
+              if (s.two) load(t_cur, tile_lanes << (in_batch * nsb), vmap);
+            }
+            if (!s.two && i > 0) {
+              if (in_batch == 0)
+                load(t_prev, tile_lanes << ((per_batch - 1) * nsb), vmap);
+              else
+                load(t_cur, tile_lanes << ((in_batch - 1) * nsb), vmap);
+            }
           }
+        } else {
+          // Runs of one or two keys (block sizes that share no larger power of two with a tile):
+          // several batches per tile, looked up as they are needed.
+          auto load_runs = [&](int j, const CUtensorMap* map) {
+            const uint32_t slot = g % NS, full = bar(SM::bFull + slot);
+            wait(bar(SM::bEmpty + slot), ((g / NS) & 1) ^ 1);
+            if (!ok) return;
+            int token[4];
+            uint32_t runs = 0;
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            e_prev[p] = e_cur[p];
-            e_cur[p] = e_next[p];
+            for (int p = 0; p < 4; ++p) {
+              token[p] = -1;
+              if (p >= batches) continue;
+              const int run = j * nsb + p * 32 + lane;
+              token[p] = pool_row(run, entry(run));
+              runs += __popc(__ballot_sync(0xffffffffu, token[p] >= 0));
+            }
+            if (lane == 0) mbar_arrive_expect_tx(full, runs * (uint32_t)(SM::kHalves * KB * 128));
+            __syncwarp();
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              if (token[p] < 0) continue;
+#pragma unroll
+              for (int half = 0; half < SM::kHalves; ++half)
+                tma_load_3d(sbase + SM::kRing + slot * SM::kTile + half * SM::kHalf +
+                                (p * 32 + lane) * KB * 128,
+                            map, full, half * 64, s.kvh, token[p]);
+            }
+            ++g;
+          };
+          for (int i = 0; i <= n && ok; ++i) {
+            if (i < n) load_runs(i, kmap);
+            if (s.two && i < n) load_runs(i, vmap);
+            if (!s.two && i > 0) load_runs(i - 1, vmap);
           }
         }
       }
