@@ -131,6 +131,16 @@ struct PreGroup {
   int32_t seq;      // the sequence whose block table is read (the first member)
 };
 
+// Entry of the groups' token list: a query token whose prefix is computed apart, with all that the
+// merge needs to find its parts, in two 16-byte loads.
+struct PreToken {
+  int32_t token;         // packed token
+  int32_t rec;           // its decode record
+  int32_t tile0, tile1;  // that record's tiles among all decode tiles
+  int32_t at;            // its place among the group's tokens
+  int32_t n_tok, keys, cost0;  // of the group (PreGroup)
+};
+
 // Sections of the workspace behind ws_layout's (all 256-byte aligned).
 struct PreLayout {
   size_t rec, cnt, first, map, group, tok, base_ml, base_o, cut_ml, cut_o, total;
@@ -138,15 +148,14 @@ struct PreLayout {
 __host__ __device__ inline PreLayout pre_layout(int R, int T, int Hq, int D, int NG) {
   PreLayout L;
   size_t off = ws_layout(R, T, Hq, D).total;
-  // per decode record (prefix length, index in the group list, token of the group, 1), or zeros
-  L.rec = off;     off = align_up(off + sizeof(int32_t) * 4 * (size_t)(R + 1), 256);
+  // per decode record: keys of the prefix computed apart, or 0
+  L.rec = off;     off = align_up(off + sizeof(int32_t) * (size_t)(R + 1), 256);
   // per group number: query tokens (then: tokens listed so far), first member, index in the list
   L.cnt = off;     off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.first = off;   off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.map = off;     off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.group = off;   off = align_up(off + sizeof(PreGroup) * (size_t)(NG + 1), 256);
-  // per query token of a group: (packed token, decode record)
-  L.tok = off;     off = align_up(off + sizeof(int32_t) * 2 * (size_t)(R + 1), 256);
+  L.tok = off;     off = align_up(off + sizeof(PreToken) * (size_t)(R + 1), 256);
   // Partial results of a chain: the part with its first K/V tile in a row per (token list entry,
   // query head), and a part that a CTA's range begins with in the CTA's own 2 x 128 rows.
   L.base_ml = off; off = align_up(off + sizeof(float2) * (size_t)R * (size_t)Hq, 256);

@@ -460,16 +460,16 @@ __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensor
     const int s = rec.x, tok = rec.y, kv = rec.z;
     // with a sliding window the sequence's tiles start at the one holding its first key
     int lo_key = window_first_key(kv - 1, a.window);
-    int4 pre = make_int4(0, 0, 0, 0);
+    int pre = 0;
     if constexpr (kPre) {  // and with a prefix computed apart, at the one holding its end
-      pre = reinterpret_cast<const int4*>(
+      pre = reinterpret_cast<const int32_t*>(
           a.ws + pre_layout(a.R, a.T, a.Hq, a.D, a.NG).rec)[d];
-      lo_key = pre.x;
+      lo_key = pre;
     }
     const int first_tile_key = lo_key / kDecodeTileKeys * kDecodeTileKeys;
     const long long lo = t > p0 ? t : p0;
     const long long hi = t1 < p1 ? t1 : p1;
-    const bool complete = p0 >= t0 && p1 <= t1 && (!kPre || pre.w == 0);
+    const bool complete = p0 >= t0 && p1 <= t1 && (!kPre || pre == 0);
     const int32_t* row = a.block_table + (size_t)s * a.max_blocks;
     // The consumers read this sequence's query rows (the CTA's head group) at its first tile,
     // a few stages from now: pull them into L2 so that the read does not wait on HBM.
@@ -518,7 +518,7 @@ __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensor
           si.key0 = key0;
           si.p0 = (int)p0;
           si.p1 = (int)p1;
-          if constexpr (kPre) si.pre = pre.w > 0;
+          if constexpr (kPre) si.pre = pre > 0;
           si.flags = (tile == lo ? kInfoFirst : 0u) | (tile == hi - 1 ? kInfoLast : 0u) |
                      (complete ? kInfoComplete : 0u);
           mbar_arrive_expect_tx(bar_full + 8 * stage,

@@ -161,8 +161,8 @@ struct PreSeq {
 };
 
 // With shared prefixes: which groups' prefixes are computed once.  Fills the group list, and per
-// group number: map (index in the list, -1: every member's own pass does it all), tok0 (its first
-// entry of the token list) and cnt (the tokens listed so far: 0).  Returns the work of the prefixes
+// group number map (index in the list, -1: every member's own pass does it all) and cnt (the tokens
+// listed so far: 0).  Returns the work of the prefixes
 // per KV head in cost units (0: no group takes part; the same in every thread).
 //
 // A group takes part when it has at least two query tokens (from members with at most kPreMaxQ
@@ -233,7 +233,6 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
     if (g < a.NG) {
       map[g] = n > 0 ? carry[0] + ex[0] : -1;
       cnt[g] = 0;
-      first[g] = carry[1] + ex[1];  // from here on: tok0
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) carry[k] += tot[k];
@@ -248,26 +247,25 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
 }
 
 // Decode CTAs per head group where prefixes are computed apart; the other SMs are the prefixes'.
-// Called by one full warp.  Model, fitted to GB300 measurements of the two passes side by side: n
-// decode CTAs stream as in choose_decode_ctas, or take 1.1 us per 64 KB stage (0.8 at least) and 1
-// us per record, 4 us to start; a cost unit of the prefixes takes 0.95 us of an SM, 8 us to start
-// and end; chunk work follows on the prefixes' SMs, so it is counted with them.  The choice is the
-// n with the least max(decode, prefix + chunk), the largest such n.
+// Called by one full warp.  Model, fitted to GB300 measurements of the two passes side by side: a
+// decode CTA takes 1.3 us per 64 KB stage (0.8 us at least) and 1.5 us per record, all of them no less
+// than their bytes at 6.2 TB/s, 4 us to start; a cost unit of the prefixes takes 0.95 us of an SM,
+// 8 us to start and end; chunk work follows on the prefixes' SMs, so it is counted with them.  The
+// choice is the n with the least max(decode, prefix + chunk), the largest such n.
 __device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes, float cost,
                                                    float chunk_flops, long long tiles, int records) {
   const int lane = threadIdx.x & 31;
   const int hg = pre_head_groups(a.Hkv, a.G), sms = a.chunk_ctas;
   const int cap = (int)(tiles < a.decode_ctas ? tiles : a.decode_ctas);
   const float w_us = cost * 0.95f + chunk_flops * (1.f / 6.4e6f);
-  const float b_mb = dec_bytes * 1e-6f;
   const float stage_kb = (float)(a.Hkv < 8 ? a.Hkv : 8) * (float)a.D * (1.f / 16.f);
-  const float tile_us = (float)tiles * fmaxf(0.8f, stage_kb * (1.1f / 64.f)) + (float)records;
+  const float tile_us = (float)tiles * fmaxf(0.8f, stage_kb * (1.3f / 64.f)) + 1.5f * (float)records;
+  const float least = dec_bytes * (1e-6f / 6.2f);
   float best = 3.4e38f;
   int best_n = 1;
   for (int n = 2 * (lane + 1); n <= (cap > 2 ? cap : 2) && n * hg < sms; n += 64) {
-    const float lin = 0.11f * n * hg, sat = 6.8f;
-    const float bw = rcbrtf(1.f / (lin * lin * lin) + 1.f / (sat * sat * sat));
-    const float t = fmaxf(4.f + fmaxf(b_mb / bw, tile_us / (float)n), 8.f + w_us / (float)(sms - n * hg));
+    const float t = fmaxf(4.f + fmaxf(least, __fdividef(tile_us, (float)n)),
+                          8.f + __fdividef(w_us, (float)(sms - n * hg)));
     if (t <= best) {
       best = t;
       best_n = n;
@@ -313,15 +311,15 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   const long long max_kv = (long long)a.max_blocks * a.bs;
 
   float my_keys = 0.f, my_pairs = 0.f;  // work estimates for the decode / chunk balance
-  // shared prefixes: their work per KV head, and per group number cnt, tok0 and map
+  // shared prefixes: their work per KV head, and per group number cnt, first member and map
   int pre_cost = 0;
   const PreLayout PL = kPre ? pre_layout(a.R, a.T, a.Hq, a.D, a.NG) : PreLayout{};
   const bool few = a.NG <= kPlanSmemGroups;
   int32_t* grp_cnt = few ? s_groups : reinterpret_cast<int32_t*>(a.ws + PL.cnt);
-  int32_t* grp_tok0 = few ? s_groups + kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.first);
+  int32_t* grp_first = few ? s_groups + kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.first);
   int32_t* grp_map = few ? s_groups + 2 * kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.map);
   PreSeq mine = {};
-  if constexpr (kPre) pre_cost = plan_prefixes(a, sw, grp_cnt, grp_tok0, grp_map, mine);
+  if constexpr (kPre) pre_cost = plan_prefixes(a, sw, grp_cnt, grp_first, grp_map, mine);
   bool bad = false;
   const int unit_rows = pf_unit_tiles(a.G) * kPrefillTileM;
   int carry[4] = {0, 0, 0, 0};
@@ -387,6 +385,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       // on the tile it is computed in.
       const int q_len = v[0], first = keys / kDecodeTileKeys * kDecodeTileKeys;
       const int at = atomicAdd(&grp_cnt[grp], q_len);
+      const PreGroup group = reinterpret_cast<const PreGroup*>(a.ws + PL.group)[grp_map[grp]];
       int tile = carry[1] + ex[1];
       for (int j = 0; j < q_len; ++j) {
         const int i = carry[0] + ex[0] + j, n_keys = kv - q_len + j + 1;
@@ -394,13 +393,16 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
         dec_prefix[i] = tile;
         dec_rec[i] = make_int4(s, tok + j, n_keys, tile);
         if (i < kSeqs) s_dec_prefix[i] = tile;
-        reinterpret_cast<int4*>(a.ws + PL.rec)[i] = make_int4(keys, grp_map[grp], at + j, 1);
-        reinterpret_cast<int2*>(a.ws + PL.tok)[grp_tok0[grp] + at + j] = make_int2(tok + j, i);
-        tile += (n_keys - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
+        reinterpret_cast<int32_t*>(a.ws + PL.rec)[i] = keys;
+        const int n_tiles = (n_keys - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
+        int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 2 * (size_t)(group.tok0 + at + j);
+        entry[0] = make_int4(tok + j, i, tile, tile + n_tiles);
+        entry[1] = make_int4(at + j, group.n_tok, keys, group.cost0);
+        tile += n_tiles;
       }
     } else if (v[0]) {
       const int i = carry[0] + ex[0];
-      if constexpr (kPre) reinterpret_cast<int4*>(a.ws + PL.rec)[i] = make_int4(0, 0, 0, 0);
+      if constexpr (kPre) reinterpret_cast<int32_t*>(a.ws + PL.rec)[i] = 0;
       dec_seq[i] = s;
       dec_prefix[i] = carry[1] + ex[1];
       dec_rec[i] = make_int4(s, tok, kv, carry[1] + ex[1]);

@@ -72,128 +72,171 @@ static cudaError_t launch_instance(const AttnArgs& a, const AttnMaps& m, const C
                             m.k_chunk, m.v_chunk);
 }
 
-// One warp per (query token, query head) of the shared prefixes: M = max m_c, w_c = 2^(m_c - M),
-// out = sum_c w_c o_c / sum_c w_c l_c, lse = (M + log2 sum_c w_c l_c) ln 2 over the parts c of the
-// prefix's chain and of the own keys.  Every part that exists holds at least one key, so its m is
-// finite.  Bound by latency: a lane finds a part and loads its (m, l), so all are there after one
-// trip to L2, and the rows of O follow kC at a time.
+// One warp per (query token, HP query heads of one KV head) of the shared prefixes:
+// M = max m_c, w_c = 2^(m_c - M), out = sum_c w_c o_c / sum_c w_c l_c,
+// lse = (M + log2 sum_c w_c l_c) ln 2 over the parts c of the prefix's chain and of the own keys.
+// Every part that exists holds at least one key, so its m is finite.  A lane finds a part and loads
+// its (m, l), so all are there after one trip to L2, and the rows of O follow kC at a time.  Finding
+// the parts is what costs instructions, so with many rows a warp does HP = 4 heads; with few, where
+// only the latency of its loads counts, one.
 constexpr int kMergeThreads = 256;
-template <int D>
+template <int D, int HP>
 __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnArgs a) {
-  constexpr int PER = D / 32, kC = 8;  // columns per lane, rows of O in flight
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int PER = D / 32, kC = 8 / HP;  // columns per lane, parts' rows of O in flight
   const int lane = threadIdx.x & 31;
   const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D);
   const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG);
   const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.ws + L.header);
-  const int2* list = reinterpret_cast<const int2*>(a.ws + PL.tok);
-  const int4* pre_rec = reinterpret_cast<const int4*>(a.ws + PL.rec);
-  const int4* dec_rec = reinterpret_cast<const int4*>(a.ws + L.dec_rec);
-  const PreGroup* groups = reinterpret_cast<const PreGroup*>(a.ws + PL.group);
+  const int4* list = reinterpret_cast<const int4*>(a.ws + PL.tok);
   __nv_bfloat16* outg = static_cast<__nv_bfloat16*>(a.out);
-  const long long rows = (long long)hdr->pre_tokens * a.Hq;
-  const long long ntiles = hdr->dec_tiles, Wh = hdr->pre_cost, W = Wh * a.Hkv;
-  const int N = hdr->decode_ctas, NP = hdr->pre_ctas;
+  // The plan is read before the wait for the attention kernel: that kernel's CTAs let this one
+  // start only after their own wait for the planner, so the plan is complete and in L2 (ld.cg).
+  // (An entry behind the list's end is read before the end is known, inside the workspace.)
+  const int per_kvh = (a.G + HP - 1) / HP, per_tok = per_kvh * a.Hkv;
+  long long job = (long long)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  const int i0 = (int)(job / per_tok);
+  int4 ta = make_int4(0, 0, 0, 0), tb = ta;
+  if (i0 < a.R) {
+    ta = __ldcg(list + 2 * (size_t)i0);
+    tb = __ldcg(list + 2 * (size_t)i0 + 1);
+  }
+  const long long jobs = (long long)__ldcg(&hdr->pre_tokens) * per_tok;
+  const long long ntiles = __ldcg(&hdr->dec_tiles), Wh = __ldcg(&hdr->pre_cost), W = Wh * a.Hkv;
+  const int N = __ldcg(&hdr->decode_ctas), NP = __ldcg(&hdr->pre_ctas);
   const int per_tile = pre_tile_tokens(a.G);
-  for (long long row = (long long)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5); row < rows;
-       row += (long long)gridDim.x * (kMergeThreads / 32)) {
-    const int i = (int)(row / a.Hq), head = (int)(row - (long long)i * a.Hq);
-    const int kvh = head / a.G;
-    const int2 tr = list[i];
-    const int4 rec = pre_rec[tr.y];
-    const PreGroup g = groups[rec.y];
+  bool waited = false;
+  for (; job < jobs; job += (long long)gridDim.x * (kMergeThreads / 32)) {
+    const int i = (int)(job / per_tok), in_tok = (int)(job - (long long)i * per_tok);
+    const int kvh = in_tok / per_kvh, h0 = (in_tok - kvh * per_kvh) * HP;
+    const int nh = a.G - h0 < HP ? a.G - h0 : HP, head0 = kvh * a.G + h0;
+    if (waited) {
+      ta = __ldcg(list + 2 * (size_t)i);
+      tb = __ldcg(list + 2 * (size_t)i + 1);
+    }
+    const PreToken t = {ta.x, ta.y, ta.z, ta.w, tb.x, tb.y, tb.z, tb.w};
     // own keys: decode CTAs df .. dl
-    const int df = cta_of_tile(dec_rec[tr.y].w, ntiles, N);
-    const int dl = cta_of_tile(dec_rec[tr.y + 1].w - 1, ntiles, N);
+    const int df = cta_of_tile(t.tile0, ntiles, N), dl = cta_of_tile(t.tile1 - 1, ntiles, N);
     // the prefix: the chain of this token's unit, prefix CTAs pf .. pl
-    const PreShape sh = pre_shape(g.n_tok, g.keys, a.G);
-    const int tile = rec.z / per_tile, u = tile >> 1;
+    const PreShape sh = pre_shape(t.n_tok, t.keys, a.G);
+    const int tile = t.at / per_tile, u = tile >> 1;
     const int w = u < sh.full ? kPreCost2 : kPreCost1;
-    const long long cs = kvh * Wh + g.cost0 + u * kPreCost2 * sh.nt;
+    const long long cs = kvh * Wh + t.cost0 + u * kPreCost2 * sh.nt;
     const int pf = cta_of_tile(cs, W, NP), pl = cta_of_tile(cs + (long long)w * sh.nt - 1, W, NP);
     const int n_pre = pl - pf + 1, nparts = n_pre + dl - df + 1;
-    // row of this (token, head) in its tile, for the parts in a CTA's own rows
-    const int in_tile = (rec.z - tile * per_tile) * a.G + head - kvh * a.G;
-    float M = -INFINITY, l = 0.f, acc[PER];
+    // row of this token's first head in its tile, for the parts in a CTA's own rows
+    const int in_tile = (t.at - tile * per_tile) * a.G + h0;
+    float M[HP], l[HP], acc[HP][PER];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) acc[k] = 0.f;
+    for (int h = 0; h < HP; ++h) {
+      M[h] = -INFINITY;
+      l[h] = 0.f;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) acc[h][k] = 0.f;
+    }
     for (int p0 = 0; p0 < nparts; p0 += 32) {
+      // this lane's part: its first head's row of (m, l) and of O (the heads' rows follow it)
       const int p = p0 + lane;
-      float2 ml = make_float2(-INFINITY, 0.f);
+      const float2* pml = nullptr;
       unsigned long long po = 0;
-      bool have = false;
       if (p < n_pre) {
         const int c = pf + p;
         const int j0 = pre_step(cs, w, sh.nt, pre_bound(W, c, NP));
         const int j1 = pre_step(cs, w, sh.nt, pre_bound(W, c + 1, NP));
-        have = j0 < j1;  // (a range may end before the step that its last unit of cost lies in)
         const bool cut = j0 > 0;
         const size_t at = cut ? ((size_t)c * 2 + (tile & 1)) * kPrefillTileM + in_tile
-                              : (size_t)i * a.Hq + head;
-        if (have) ml = reinterpret_cast<const float2*>(a.ws + (cut ? PL.cut_ml : PL.base_ml))[at];
-        po = (unsigned long long)(reinterpret_cast<const float*>(a.ws + (cut ? PL.cut_o : PL.base_o)) +
-                                  at * D);
+                              : (size_t)i * a.Hq + head0;
+        if (j0 < j1) {  // (a range may end before the step that its last unit of cost lies in)
+          pml = reinterpret_cast<const float2*>(a.ws + (cut ? PL.cut_ml : PL.base_ml)) + at;
+          po = (unsigned long long)(reinterpret_cast<const float*>(
+                                        a.ws + (cut ? PL.cut_o : PL.base_o)) + at * D);
+        }
       } else if (p < nparts) {
-        const size_t at = ((size_t)(df + p - n_pre) + tr.y) * a.Hq + head;
-        have = true;
-        ml = reinterpret_cast<const float2*>(a.ws + L.part_ml)[at];
+        const size_t at = ((size_t)(df + p - n_pre) + t.rec) * a.Hq + head0;
+        pml = reinterpret_cast<const float2*>(a.ws + L.part_ml) + at;
         po = (unsigned long long)(reinterpret_cast<const float*>(a.ws + L.part_o) + at * D);
       }
-      float mn = ml.x;
+      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+      waited = true;
+      float2 ml[HP];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      mn = fmaxf(mn, M);
-      const float sc = fast_exp2(M - mn), wt = have ? fast_exp2(ml.x - mn) : 0.f;
-      float ls = wt * ml.y;
+      for (int h = 0; h < HP; ++h) {
+        ml[h] = make_float2(-INFINITY, 0.f);
+        if (pml != nullptr && h < nh) ml[h] = pml[h];
+      }
+      float wt[HP];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-      l = l * sc + ls;
-      M = mn;
+      for (int h = 0; h < HP; ++h) {
+        float mn = ml[h].x;
 #pragma unroll
-      for (int k = 0; k < PER; ++k) acc[k] *= sc;
-      unsigned left = __ballot_sync(0xffffffffu, have);
+        for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mn = fmaxf(mn, M[h]);
+        if (h >= nh) mn = 0.f;  // (no such head: every weight 0)
+        const float sc = fast_exp2(M[h] - mn);
+        wt[h] = fast_exp2(ml[h].x - mn);
+        float ls = wt[h] * ml[h].y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+        l[h] = l[h] * sc + ls;
+        M[h] = mn;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) acc[h][k] *= sc;
+      }
+      unsigned left = __ballot_sync(0xffffffffu, pml != nullptr);
       while (left) {
-        float v[kC][PER], wc[kC];
+        float v[kC][HP][PER], wc[kC][HP];
 #pragma unroll
         for (int cc = 0; cc < kC; ++cc) {
           const int src = left ? __ffs(left) - 1 : -1;
           left &= left - 1;  // (0 stays 0)
-          wc[cc] = __shfl_sync(0xffffffffu, wt, src & 31);
           const float* o = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, po, src & 31)) +
                            lane * PER;
-          if (src < 0) wc[cc] = 0.f;
 #pragma unroll
-          for (int k = 0; k < PER; ++k) v[cc][k] = 0.f;
-          if (src >= 0) {
-            if constexpr (PER == 4) {
-              const float4 x = *reinterpret_cast<const float4*>(o);
-              v[cc][0] = x.x; v[cc][1] = x.y; v[cc][2] = x.z; v[cc][3] = x.w;
-            } else {
-              const float2 x = *reinterpret_cast<const float2*>(o);
-              v[cc][0] = x.x; v[cc][1] = x.y;
+          for (int h = 0; h < HP; ++h) {
+            const float wx = __shfl_sync(0xffffffffu, wt[h], src & 31);
+            wc[cc][h] = src < 0 ? 0.f : wx;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) v[cc][h][k] = 0.f;
+            if (src >= 0 && h < nh) {
+              if constexpr (PER == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(o + h * D);
+                v[cc][h][0] = x.x; v[cc][h][1] = x.y; v[cc][h][2] = x.z; v[cc][h][3] = x.w;
+              } else {
+                const float2 x = *reinterpret_cast<const float2*>(o + h * D);
+                v[cc][h][0] = x.x; v[cc][h][1] = x.y;
+              }
             }
           }
         }
 #pragma unroll
         for (int cc = 0; cc < kC; ++cc)
 #pragma unroll
-          for (int k = 0; k < PER; ++k) acc[k] += wc[cc] * v[cc][k];
+          for (int h = 0; h < HP; ++h)
+#pragma unroll
+            for (int k = 0; k < PER; ++k) acc[h][k] += wc[cc][h] * v[cc][h][k];
       }
     }
-    const float inv = 1.f / l;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(outg + ((size_t)tr.x * a.Hq + head) * D + lane * PER);
-    if constexpr (PER == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
-                                                  pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    else
-      dst[0] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    if (lane == 0 && a.lse != nullptr)
-      a.lse[(size_t)tr.x * a.Hq + head] = (M + __log2f(l)) * 0.6931471805599453f;
+#pragma unroll
+    for (int h = 0; h < HP; ++h) {
+      if (h >= nh) continue;
+      const float inv = 1.f / l[h];
+      const size_t row = (size_t)t.token * a.Hq + head0 + h;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(outg + row * D + lane * PER);
+      if constexpr (PER == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[h][0] * inv, acc[h][1] * inv),
+                                                    pack_bf16x2(acc[h][2] * inv, acc[h][3] * inv));
+      else
+        dst[0] = pack_bf16x2(acc[h][0] * inv, acc[h][1] * inv);
+      if (lane == 0 && a.lse != nullptr) a.lse[row] = (M[h] + __log2f(l[h])) * 0.6931471805599453f;
+    }
   }
+  // (without a row too: work behind this launch on the stream must not overtake the attention)
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 cudaError_t launch_prefix_merge(const AttnArgs& a, int sm_count, cudaStream_t stream) {
-  const long long warps = (long long)a.R * a.Hq;
+  // four heads per warp where that leaves every SM several warps
+  const bool four = (long long)a.R * a.Hkv >= (long long)sm_count * 4 && a.G >= 4;
+  const long long warps = (long long)a.R * a.Hkv * (four ? (a.G + 3) / 4 : a.G);
   long long blocks = (warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
   if (blocks > (long long)sm_count * 8) blocks = (long long)sm_count * 8;
   cudaLaunchAttribute attr[1];
@@ -205,8 +248,11 @@ cudaError_t launch_prefix_merge(const AttnArgs& a, int sm_count, cudaStream_t st
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return a.D == 128 ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<128>, a)
-                    : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<64>, a);
+  if (a.D == 128)
+    return four ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<128, 4>, a)
+                : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<128, 1>, a);
+  return four ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<64, 4>, a)
+              : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<64, 1>, a);
 }
 
 cudaError_t launch_prefix_attention(const AttnArgs& a, const AttnMaps& m, const CUtensorMap& q_tok,

@@ -53,7 +53,7 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D).header);
   const int N = hdr->pre_ctas;
   const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG);
-  const int2* list = reinterpret_cast<const int2*>(a.ws + PL.tok);
+  const PreToken* list = reinterpret_cast<const PreToken*>(a.ws + PL.tok);
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -142,7 +142,7 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           for (int i = lane; i < s.ntok[t]; i += 32) {
-            const int tok = list[s.tok0 + t * pre_tile_tokens(a.G) + i].x;
+            const int tok = list[s.tok0 + t * pre_tile_tokens(a.G) + i].token;
 #pragma unroll
             for (int half = 0; half < SM::kHalves; ++half)
               tma_load_3d(sbase + t * SM::kTile + half * SM::kHalf + i * a.G * 128, qmap,
