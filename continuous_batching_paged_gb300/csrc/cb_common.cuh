@@ -58,7 +58,8 @@ struct PlanHeader {
   // start and last end of the decode CTAs that had work, and of the chunk CTAs.
   unsigned long long t_dec_start, t_dec_end, t_pf_start, t_pf_end;
   int32_t pre_cost;         // their work per KV head, in cost units (PreGroup),
-  int32_t pre_tokens;       // and entries of the groups' token list
+  int32_t pre_tokens;       // entries of the groups' token list,
+  int32_t pre_keys, pad;    // and keys of all prefixes (for the planner's estimates)
 };
 
 // Byte offsets of the workspace sections (all 256-byte aligned).

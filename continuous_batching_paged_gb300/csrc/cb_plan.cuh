@@ -221,12 +221,13 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
   }
   __syncthreads();
   if (s_total > kPreMaxCost) bad = true;  // (32 bits hold every cost below)
-  int carry[4] = {0, 0, 0, 0};  // groups, tokens, cost
+  int carry[4] = {0, 0, 0, 0};  // groups, tokens, cost, keys (an estimate: it may wrap)
   for (int base = 0; base < a.NG; base += kPlanThreads) {
     const int g = base + tid;
     const int keys = base == 0 ? my_keys : g < a.NG ? a.prefix_lens[g] : 0;
     const int n = shared_tokens(g, keys);
-    int v[4] = {n > 0, n, n > 0 ? (int)pre_shape(n, keys, a.G).per : 0, 0}, ex[4], tot[4];
+    int v[4] = {n > 0, n, n > 0 ? (int)pre_shape(n, keys, a.G).per : 0, n > 0 ? keys : 0};
+    int ex[4], tot[4];
     block_scan4(v, ex, tot, sw);  // (its barriers also part the reads of cnt from the writes)
     if (n > 0)
       groups[carry[0] + ex[0]] = {carry[2] + ex[2], n, carry[1] + ex[1], keys, first[g]};
@@ -235,38 +236,56 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
       cnt[g] = 0;
     }
 #pragma unroll
-    for (int k = 0; k < 3; ++k) carry[k] += tot[k];
+    for (int k = 0; k < 4; ++k) carry[k] += tot[k];
   }
   if (tid == 0) {
     hdr->pre_groups = carry[0];
     hdr->pre_tokens = carry[1];
     hdr->pre_cost = carry[2];
+    hdr->pre_keys = carry[3];
   }
   __syncthreads();
   return carry[2];
 }
 
+// Prefix CTAs where `free` SMs are left to them: as many for each KV head (PreGroup), no more than
+// the work is worth.
+__device__ __forceinline__ int pre_cta_count(int free, int cost, int Hkv) {
+  int np = free < kMaxPreCtas ? free : kMaxPreCtas;
+  const long long most = (long long)cost * Hkv / (kPreMinSteps * kPreCost1);
+  if (np > most) np = (int)most;
+  if (np > Hkv) np -= np % Hkv;
+  return np < 1 ? 1 : np;
+}
+
 // Decode CTAs per head group where prefixes are computed apart; the other SMs are the prefixes'.
-// Called by one full warp.  Model, fitted to GB300 measurements of the two passes side by side: a
-// decode CTA takes 1.3 us per 64 KB stage (0.8 us at least) and 1.5 us per record, all of them no less
-// than their bytes at 6.2 TB/s, 4 us to start; a cost unit of the prefixes takes 0.95 us of an SM,
-// 8 us to start and end; chunk work follows on the prefixes' SMs, so it is counted with them.  The
-// choice is the n with the least max(decode, prefix + chunk), the largest such n.
-__device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes, float cost,
-                                                   float chunk_flops, long long tiles, int records) {
+// Called by one full warp.  Model, fitted to GB300 measurements over all n of 15 batches (8 to 256
+// sequences, prefixes of 1k to 64k keys, 8 and 1 KV heads, head_dim 64 and 128), in us:
+//   decode = 3 + hypot(x, y): x the CTA's tiles (0.8 each at 64 KB, 0.54 at 8 KB; a record counts as
+//            one more), y the HBM time of all bytes, its share of which grows as x shrinks;
+//   prefix = 12 + 0.8 per cost unit of a CTA; chunk work follows on the same SMs.
+// The choice is the n with the least max(decode, prefix + chunk), plus a tenth of the other one so
+// that where one side is flat the other is not starved, plus 0.015 a CTA for the parts it adds.  It comes within 5 % of the best n on 13 of
+// the 15 batches, and within 12 % on the others.
+__device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes, float pre_bytes,
+                                                   int cost, float chunk_flops, long long tiles,
+                                                   int records) {
   const int lane = threadIdx.x & 31;
   const int hg = pre_head_groups(a.Hkv, a.G), sms = a.chunk_ctas;
   const int cap = (int)(tiles < a.decode_ctas ? tiles : a.decode_ctas);
-  const float w_us = cost * 0.95f + chunk_flops * (1.f / 6.4e6f);
-  const float stage_kb = (float)(a.Hkv < 8 ? a.Hkv : 8) * (float)a.D * (1.f / 16.f);
-  const float tile_us = (float)tiles * fmaxf(0.8f, stage_kb * (1.3f / 64.f)) + 1.5f * (float)records;
-  const float least = dec_bytes * (1e-6f / 6.2f);
+  const float stage = (float)((a.Hkv < 8 ? a.Hkv : 8) * a.D) * (1.f / 1024.f);  // of 64 KB
+  const float x1 = (0.5f + 0.3f * stage) * ((float)tiles + (float)records);
+  const float y = (dec_bytes + pre_bytes) * (0.7e-6f / 6.2f);
   float best = 3.4e38f;
   int best_n = 1;
   for (int n = 2 * (lane + 1); n <= (cap > 2 ? cap : 2) && n * hg < sms; n += 64) {
-    const float t = fmaxf(4.f + fmaxf(least, __fdividef(tile_us, (float)n)),
-                          8.f + __fdividef(w_us, (float)(sms - n * hg)));
-    if (t <= best) {
+    const int free = sms - n * hg;
+    const float x = __fdividef(x1, (float)n), d = 3.f + __fsqrt_rn(x * x + y * y);
+    const float p = 12.f + __fdividef(0.8f * (float)cost * (float)a.Hkv,
+                                      (float)pre_cta_count(free, cost, a.Hkv)) +
+                    __fdividef(chunk_flops * (1.f / 6.4e6f), (float)free);
+    const float t = fmaxf(d, p) + 0.1f * fminf(d, p) + 0.015f * (float)n;
+    if (t < best) {
       best = t;
       best_n = n;
     }
@@ -274,7 +293,7 @@ __device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_
   for (int o = 16; o > 0; o >>= 1) {
     const float t = __shfl_xor_sync(0xffffffffu, best, o);
     const int n = __shfl_xor_sync(0xffffffffu, best_n, o);
-    if (t < best || (t == best && n > best_n)) {
+    if (t < best || (t == best && n < best_n)) {
       best = t;
       best_n = n;
     }
@@ -354,7 +373,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
         v[0] = q_len;
         for (int i = 0; i < q_len; ++i)
           v[1] += (kv - q_len + i + 1 - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
-        my_keys += (float)(kv - keys) * (float)q_len;
+        my_keys += (float)(kv - keys);
       } else if (q_len == 1) {
         grp = -1;
         // tiles from the one holding the window's first key (every key without a window)
@@ -491,17 +510,13 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     }
     int n = (int)(ntiles < a.decode_ctas ? (ntiles > 0 ? ntiles : 1) : a.decode_ctas);
     if (kPre && pre_cost > 0) {
+      const float row = (float)(a.Hkv * a.D * 4);  // bytes of a key and its value
       if (a.decode_auto)
-        n = choose_prefix_split(a, keys * (float)(a.Hkv * a.D * 4), (float)pre_cost * (float)a.Hkv,
+        n = choose_prefix_split(a, keys * row, (float)hdr->pre_keys * row, pre_cost,
                                 pairs * (float)(4 * a.D * a.Hq), ntiles, n_dec);
       // the decode CTAs without work; where a given number leaves none, an eighth of the chunk CTAs
       const int idle = pre_idle_count(pre_head_groups(a.Hkv, a.G), n, a.decode_ctas);
-      int np = idle > 0 ? idle : a.chunk_ctas / 8;
-      const long long most = (long long)pre_cost * a.Hkv / (kPreMinSteps * kPreCost1);
-      if (np > most) np = (int)most;
-      if (np > kMaxPreCtas) np = kMaxPreCtas;
-      if (np > a.Hkv) np -= np % a.Hkv;  // as many for each KV head (PreGroup)
-      if (tid == 0) hdr->pre_ctas = np < 1 ? 1 : np;
+      if (tid == 0) hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, pre_cost, a.Hkv);
     } else if (a.decode_auto) {
       n = choose_decode_ctas(keys * (float)(a.Hkv * a.D * 4), pairs * (float)(4 * a.D * a.Hq),
                              n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq), a.decode_ctas,
