@@ -64,6 +64,7 @@ struct PreSeg {
   int kvh, seq, keys, j0, j1, tok0;
   int ntok[2];
   bool two;
+  bool once;  // the group has this unit alone: its keys are read once per KV head
 };
 
 // Walks the parts of one CTA's range, in order.
@@ -111,6 +112,7 @@ struct PreWalk {
       s.ntok[0] = min(per_tile, g.n_tok - first);
       s.ntok[1] = max(0, min(per_tile, g.n_tok - first - per_tile));
       s.two = s.ntok[1] > 0;
+      s.once = sh.units == 1;
       return true;
     }
     return false;
