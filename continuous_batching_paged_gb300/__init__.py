@@ -174,7 +174,7 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     import torch
     if stream is None:  # without the Stream object that torch.cuda.current_stream() makes (3 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -284,55 +284,99 @@ def kv_append(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens
     _check(st, "cb_kv_append")
 
 
-def _rows_stride(name, t) -> int:
-    """Elements between the token rows of a bf16 [T, H, D] tensor whose rows are contiguous (a
-    view of a wider projection's output, for instance)."""
+# The calls below are made once per layer and step, often on a few tokens, where the host time of
+# their checks is most of their cost: each makes all its checks in one expression, and asks the
+# _explain functions for the message only when that fails.
+
+def _rows_ok(T, H, D, strides) -> bool:
+    """Whether a [T, H, D] tensor of these strides has contiguous token rows (as a view of a wider
+    projection's output has)."""
+    return T == 0 or (strides[2] == 1 and (strides[1] == D or H == 1))
+
+
+def _explain_rows(name, t) -> None:
     import torch
-    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.dim() != 3:
-        _require(t.dtype == torch.bfloat16, f"{name} must be bfloat16")
-        _require(t.is_cuda, f"{name} must be a CUDA tensor")
-        _require(False, f"{name} must have 3 dimensions")
-    T, H, D = t.shape
-    step, head, elem = t.stride()
-    if T > 0 and (elem != 1 or (head != D and H > 1)):
-        _require(False, f"{name} must have contiguous token rows")
-    return step if T > 1 else H * D
+    _require(t.dtype == torch.bfloat16, f"{name} must be bfloat16")
+    _require(t.is_cuda, f"{name} must be a CUDA tensor")
+    _require(t.dim() == 3, f"{name} must have 3 dimensions")
+    _require(_rows_ok(*t.shape, t.stride()), f"{name} must have contiguous token rows")
 
 
-def _plain(dtype, dev, *tensors) -> bool:
-    """Whether every tensor is contiguous, of the dtype and on CUDA device dev: the quick form of
-    the checks whose messages the functions above give (a call's checks cost as much host time as
-    its launch)."""
-    for t in tensors:
-        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-            return False
-    return True
-
-
-def _check_step(k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, Hkv, D):
-    """Checks of a step's pools and metadata; the number of sequences."""
+def _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
+                  cos_sin) -> None:
+    """Raise the error of a step's inputs that failed their check (k_new, v_new and cos_sin: None
+    where the call takes none; q: None where it may be left out)."""
     import torch
-    dev = k_pages.get_device()
-    if not (dev >= 0 and _plain(torch.bfloat16, dev, k_pages, v_pages)
-            and _plain(torch.int32, dev, block_table, cu_seqlens_q, kv_lens)
-            and k_pages.dim() == 4 and block_table.dim() == 2):
-        _check_bf16("k_pages", k_pages, 4)
-        _check_bf16("v_pages", v_pages, 4)
-        _check_meta(block_table, cu_seqlens_q, kv_lens)
-    _require(dev == torch.cuda.current_device(), "every tensor must be on the current CUDA device")
-    S = kv_lens.numel()
-    if cu_seqlens_q.numel() != S + 1 or block_table.shape[0] != S:
-        _check_meta(block_table, cu_seqlens_q, kv_lens)
-    shape = k_pages.shape
-    _require(shape[1] == block_size and shape[2] == Hkv and shape[3] == D,
-             "k_pages must be [P, block_size, Hkv, D]")
-    _require(shape == v_pages.shape, "v_pages must match k_pages")
-    return S
+    if cos_sin is not None:
+        _require(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_cuda
+                 and cos_sin.is_contiguous(),
+                 "cos_sin must be a contiguous fp32 CUDA tensor [max_positions, rot_dim]")
+        for name, t in (("q", q), ("k_new", k_new), ("v_new", v_new)):
+            if t is not None:
+                _explain_rows(name, t)
+    else:
+        _check_bf16("q", q, 3)
+    _check_bf16("k_pages", k_pages, 4)
+    _check_bf16("v_pages", v_pages, 4)
+    _check_meta(block_table, cu_seqlens_q, kv_lens)
+    P, bs, Hkv, D = k_pages.shape
+    _require(bs == block_size, "k_pages must be [P, block_size, Hkv, D]")
+    _require(k_pages.shape == v_pages.shape, "v_pages must match k_pages")
+    if k_new is not None:
+        _require(k_new.shape[1:] == (Hkv, D), "k_new must be [T, Hkv, D]")
+        _require(v_new.shape == k_new.shape, "v_new must match k_new")
+        _require(q is None or (q.shape[0], q.shape[2]) == (k_new.shape[0], D), "q must be [T, Hq, D]")
+    else:
+        _require(q.shape[2] == D, "q must be [T, Hq, D]")
+    dev = torch.cuda.current_device()
+    for t in (q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, cos_sin):
+        _require(t is None or t.get_device() == dev, "every tensor must be on the current CUDA device")
+    raise ValueError("inconsistent arguments")
 
 
-def _on_device(dev, *tensors) -> None:
-    for t in tensors:
-        _require(t is None or t.get_device() == dev, "every tensor must be on the same device")
+def _meta_ok(dev, i32, block_table, cu_seqlens_q, kv_lens) -> bool:
+    return (block_table.dtype is i32 and cu_seqlens_q.dtype is i32 and kv_lens.dtype is i32
+            and block_table.get_device() == dev and cu_seqlens_q.get_device() == dev
+            and kv_lens.get_device() == dev and block_table.is_contiguous()
+            and cu_seqlens_q.is_contiguous() and kv_lens.is_contiguous()
+            and block_table.dim() == 2 and cu_seqlens_q.numel() == kv_lens.numel() + 1
+            and block_table.shape[0] == kv_lens.numel())
+
+
+def _rope_inputs(torch, q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                 block_size, cos_sin, interleaved):
+    """cb_dims and cb_rope of a rotary append, its inputs checked."""
+    bf16, dev = torch.bfloat16, k_new.get_device()
+    ks, vs, shape, pool = k_new.stride(), v_new.stride(), k_new.shape, k_pages.shape
+    ok = (dev >= 0 and len(shape) == 3 and len(pool) == 4 and len(cos_sin.shape) == 2
+          and dev == torch._C._cuda_getDevice())
+    if ok:
+        T, Hkv, D = shape
+        Hq, qs = Hkv, None
+        ok = (k_new.dtype is bf16 and v_new.dtype is bf16 and k_pages.dtype is bf16
+              and v_pages.dtype is bf16 and cos_sin.dtype is torch.float32
+              and v_new.get_device() == dev and k_pages.get_device() == dev
+              and v_pages.get_device() == dev and cos_sin.get_device() == dev
+              and k_pages.is_contiguous() and v_pages.is_contiguous() and cos_sin.is_contiguous()
+              and v_new.shape == shape and v_pages.shape == pool
+              and pool[1] == block_size and pool[2] == Hkv and pool[3] == D
+              and _rows_ok(T, Hkv, D, ks) and _rows_ok(T, Hkv, D, vs)
+              and _meta_ok(dev, torch.int32, block_table, cu_seqlens_q, kv_lens))
+        if ok and q is not None:
+            qs = q.stride()
+            ok = q.dtype is bf16 and q.get_device() == dev and len(qs) == 3
+            if ok:
+                Tq, Hq, Dq = q.shape
+                ok = Tq == T and Dq == D and _rows_ok(T, Hq, D, qs)
+    if not ok:
+        _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                      block_size, cos_sin)
+    many = T > 1  # (one token's row is contiguous whatever its stride says)
+    rows, rot = cos_sin.shape
+    return (CbDims(kv_lens.numel(), T, Hq, Hkv, D, pool[0], block_table.shape[1]),
+            CbRope(cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, 0,
+                   qs[0] if many and qs is not None else 0, ks[0] if many else 0,
+                   vs[0] if many else 0))
 
 
 def _on_stream(stream):
@@ -345,32 +389,17 @@ def _on_stream(stream):
 
 def _new(shape, dtype, like, stream):
     """A tensor beside `like`, its memory reused only after the work queued on `stream`."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with _on_stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _output(t, name, shape, like, stream):
-    """The caller's bf16 output tensor, checked, or a new one beside `like`."""
-    import torch
-    if t is None:
-        return _new(shape, torch.bfloat16, like, stream)
+def _check_output(t, name, shape, dev) -> None:
+    """Checks of a bf16 output tensor that the caller gave."""
     _check_bf16(name, t, len(shape))
     _require(tuple(t.shape) == shape, f"{name} must be {list(shape)}")
-    return t
-
-
-def _rope(q, k_new, v_new, cos_sin, interleaved) -> CbRope:
-    """cb_rope of the given tensors (the shapes of q, k_new and v_new are checked by the caller)."""
-    import torch
-    _require(cos_sin.dtype is torch.float32 and cos_sin.dim() == 2 and cos_sin.is_cuda
-             and cos_sin.is_contiguous(),
-             "cos_sin must be a contiguous fp32 CUDA tensor [max_positions, rot_dim]")
-    return CbRope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), 0,
-                  0 if q is None else _rows_stride("q", q), _rows_stride("k_new", k_new),
-                  _rows_stride("v_new", v_new))
+    _require(t.get_device() == dev, f"{name} must be on the inputs' device")
 
 
 def rope_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
@@ -386,25 +415,23 @@ def rope_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv
         ang = pos[:, None] * freq
         cos_sin = torch.cat((ang.cos(), ang.sin()), 1).float()
     """
-    rope = _rope(q, k_new, v_new, cos_sin, interleaved)
-    T, Hkv, D = k_new.shape
-    S = _check_step(k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, Hkv, D)
-    _require(v_new.shape == k_new.shape, "v_new must match k_new")
-    Hq = Hkv
+    import torch
+    dims, rope = _rope_inputs(torch, q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q,
+                              kv_lens, block_size, cos_sin, interleaved)
     if q is not None:
-        Hq = q.shape[1]
-        _require(q.shape[0] == T and q.shape[2] == D, "q must be [T, Hq, D]")
-        q_out = _output(q_out, "q_out", (T, Hq, D), q, stream)
+        if q_out is None:
+            q_out = q.new_empty(q.shape) if stream is None else _new(q.shape, q.dtype, q, stream)
+        else:
+            _check_output(q_out, "q_out", tuple(q.shape), q.get_device())
     else:
         _require(q_out is None, "q_out without q")
-    _on_device(k_pages.get_device(), q, k_new, v_new, q_out, block_table, cu_seqlens_q, kv_lens,
-               cos_sin)
-    dims = CbDims(S, T, Hq, Hkv, D, k_pages.shape[0], block_table.shape[1])
-    _check(library().cb_rope_append(_ptr(q), k_new.data_ptr(), v_new.data_ptr(), _ptr(q_out),
-                                    k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-                                    cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), int(block_size),
-                                    ctypes.byref(rope), ctypes.byref(dims), _stream(stream)),
-           "cb_rope_append")
+    st = (_lib or library()).cb_rope_append(
+        None if q is None else q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+        None if q is None else q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        block_table.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_size,
+        ctypes.byref(rope), ctypes.byref(dims), _stream(stream))
+    if st:
+        _check(st, "cb_rope_append")
     return q_out
 
 
@@ -498,37 +525,42 @@ def prefix_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, num_tok
     return int(library().cb_prefix_workspace_size(ctypes.byref(dims), int(num_groups)))
 
 
-def _step_tensors(q, dims, prefix_group, prefix_lens, out, lse, workspace, decode_ctas, serial,
-                  window, phase_events, stream):
+def _step_tensors(torch, q, dims, prefix_group, prefix_lens, out, lse, workspace, decode_ctas,
+                  serial, window, phase_events, stream):
     """What an attention call with shared prefixes needs beside its inputs: cb_prefix (or None),
     out, lse, workspace and cb_options, checked or made."""
-    import torch
-    T, S, Hq, D = dims.num_tokens, dims.num_seqs, dims.num_q_heads, dims.head_dim
-    dev = q.get_device()
+    shape, dev = q.shape, q.get_device()
     prefix, NG = None, 0
     if prefix_group is not None or prefix_lens is not None:
         _require(prefix_group is not None and prefix_lens is not None,
                  "prefix_group and prefix_lens go together")
-        _require(_plain(torch.int32, dev, prefix_group, prefix_lens),
+        i32 = torch.int32
+        _require(prefix_group.dtype is i32 and prefix_lens.dtype is i32
+                 and prefix_group.get_device() == dev and prefix_lens.get_device() == dev
+                 and prefix_group.is_contiguous() and prefix_lens.is_contiguous(),
                  "prefix_group and prefix_lens must be contiguous int32 CUDA tensors on q's device")
-        _require(prefix_group.numel() == S, "prefix_group must have num_seqs entries")
+        _require(prefix_group.numel() == dims.num_seqs, "prefix_group must have num_seqs entries")
         NG = prefix_lens.numel()
-        prefix = CbPrefix(prefix_group.data_ptr(), prefix_lens.data_ptr(), NG)
-    out = _output(out, "out", (T, Hq, D), q, stream)
+        prefix = ctypes.byref(CbPrefix(prefix_group.data_ptr(), prefix_lens.data_ptr(), NG))
+    if out is None:
+        out = _new(shape, q.dtype, q, stream)
+    else:
+        _check_output(out, "out", tuple(shape), dev)
     if lse is True:
-        lse = _new((T, Hq), torch.float32, q, stream)
+        lse = _new(shape[:2], torch.float32, q, stream)
     elif lse is False:
         lse = None
     elif lse is not None:
-        _require(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (T, Hq),
-                 "lse must be a contiguous fp32 [T, Hq] tensor")
+        _require(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == shape[:2]
+                 and lse.get_device() == dev, "lse must be a contiguous fp32 [T, Hq] tensor")
     if workspace is None:
-        need = int(library().cb_prefix_workspace_size(ctypes.byref(dims), NG))
-        workspace = _new((max(need, 256),), torch.uint8, q, stream)
-    _require(workspace.dtype is torch.uint8 and workspace.is_contiguous(), "workspace must be uint8")
-    _on_device(dev, out, lse, workspace)
-    opts = CbOptions(int(decode_ctas), OPT_SERIAL if serial else 0)
-    opts.window = int(window)
+        need = (_lib or library()).cb_prefix_workspace_size(ctypes.byref(dims), NG)
+        workspace = _new(max(need, 256), torch.uint8, q, stream)
+    else:
+        _require(workspace.dtype is torch.uint8 and workspace.is_contiguous()
+                 and workspace.get_device() == dev, "workspace must be uint8")
+    opts = CbOptions(decode_ctas, OPT_SERIAL if serial else 0)
+    opts.window = window
     if phase_events is not None:
         _require(len(phase_events) == NUM_PHASE_EVENTS, f"need {NUM_PHASE_EVENTS} phase events")
         handles = (ctypes.c_void_p * NUM_PHASE_EVENTS)(*[int(e.cuda_event) for e in phase_events])
@@ -550,23 +582,28 @@ def shared_prefix_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_l
     ragged_paged_attention's within rounding; the other arguments are its.
     """
     import torch
-    if not (q.dtype is torch.bfloat16 and q.is_cuda and q.is_contiguous() and q.dim() == 3):
-        _check_bf16("q", q, 3)
-    T, Hq, D = q.shape
-    Hkv = k_pages.shape[2] if k_pages.dim() == 4 else 0
-    S = _check_step(k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, Hkv, D)
-    _on_device(k_pages.get_device(), q, block_table, cu_seqlens_q, kv_lens)
-    dims = CbDims(S, T, Hq, Hkv, D, k_pages.shape[0], block_table.shape[1])
+    bf16, dev, pool, shape = torch.bfloat16, q.get_device(), k_pages.shape, q.shape
+    if not (dev >= 0 and len(shape) == 3 and len(pool) == 4 and q.dtype is bf16
+            and dev == torch._C._cuda_getDevice() and q.is_contiguous()
+            and k_pages.dtype is bf16 and v_pages.dtype is bf16 and k_pages.get_device() == dev
+            and v_pages.get_device() == dev and k_pages.is_contiguous() and v_pages.is_contiguous()
+            and v_pages.shape == pool and pool[1] == block_size and pool[3] == shape[2]
+            and _meta_ok(dev, torch.int32, block_table, cu_seqlens_q, kv_lens)):
+        _explain_step(q, None, None, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
+                      None)
     _require(prefix_group is not None, "prefix_group must be given")
+    dims = CbDims(kv_lens.numel(), *shape[:2], pool[2], pool[3], pool[0], block_table.shape[1])
     want_lse = lse is not None and lse is not False
     prefix, out, lse, workspace, opts = _step_tensors(
-        q, dims, prefix_group, prefix_lens, out, lse, workspace, decode_ctas, serial, 0,
+        torch, q, dims, prefix_group, prefix_lens, out, lse, workspace, decode_ctas, serial, 0,
         phase_events, stream)
-    _check(library().cb_shared_prefix_attention(
+    st = (_lib or library()).cb_shared_prefix_attention(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-        cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), int(block_size), float(scale),
-        ctypes.byref(prefix), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(),
-        ctypes.byref(dims), ctypes.byref(opts), _stream(stream)), "cb_shared_prefix_attention")
+        cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_size, scale, prefix, out.data_ptr(),
+        _ptr(lse), workspace.data_ptr(), workspace.numel(), ctypes.byref(dims), ctypes.byref(opts),
+        _stream(stream))
+    if st:
+        _check(st, "cb_shared_prefix_attention")
     return (out, lse) if want_lse else out
 
 
@@ -578,27 +615,26 @@ def rope_append_attention(q, k_new, v_new, k_pages, v_pages, block_table, cu_seq
     """One layer's attention step (cb_rope_append_attention): rope_append, then
     shared_prefix_attention on the rotated queries (ragged_paged_attention without groups), same
     results, in two launches.  q_out: where the rotated queries go (default: a temporary)."""
-    rope = _rope(q, k_new, v_new, cos_sin, interleaved)
-    T, Hkv, D = k_new.shape
-    Hq = q.shape[1]
-    S = _check_step(k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, Hkv, D)
-    _require(q.shape[0] == T and q.shape[2] == D, "q must be [T, Hq, D]")
-    _require(v_new.shape == k_new.shape, "v_new must match k_new")
-    q_out = _output(q_out, "q_out", (T, Hq, D), q, stream)
-    _on_device(k_pages.get_device(), q, k_new, v_new, q_out, block_table, cu_seqlens_q, kv_lens,
-               cos_sin)
-    dims = CbDims(S, T, Hq, Hkv, D, k_pages.shape[0], block_table.shape[1])
+    import torch
+    _require(q is not None, "q must be given")
+    dims, rope = _rope_inputs(torch, q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q,
+                              kv_lens, block_size, cos_sin, interleaved)
+    if q_out is None:
+        q_out = _new(q.shape, q.dtype, q, stream)
+    else:
+        _check_output(q_out, "q_out", tuple(q.shape), q.get_device())
     want_lse = lse is not None and lse is not False
     prefix, out, lse, workspace, opts = _step_tensors(
-        q_out, dims, prefix_group, prefix_lens, out, lse, workspace, decode_ctas, serial, window,
-        phase_events, stream)
-    _check(library().cb_rope_append_attention(
+        torch, q_out, dims, prefix_group, prefix_lens, out, lse, workspace, decode_ctas, serial,
+        window, phase_events, stream)
+    st = (_lib or library()).cb_rope_append_attention(
         q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
         v_pages.data_ptr(), block_table.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
-        int(block_size), float(scale), ctypes.byref(rope),
-        None if prefix is None else ctypes.byref(prefix), out.data_ptr(), _ptr(lse),
+        block_size, scale, ctypes.byref(rope), prefix, out.data_ptr(), _ptr(lse),
         workspace.data_ptr(), workspace.numel(), ctypes.byref(dims), ctypes.byref(opts),
-        _stream(stream)), "cb_rope_append_attention")
+        _stream(stream))
+    if st:
+        _check(st, "cb_rope_append_attention")
     return (out, lse) if want_lse else out
 
 

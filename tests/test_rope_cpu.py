@@ -83,7 +83,7 @@ def test_binding_refuses_host_tensors_and_bad_rows():
     with pytest.raises(ValueError, match="cos_sin"):
         cb.rope_append(q, kn, kn, kp, kp, *meta, 16, t(32, 64))
     with pytest.raises(ValueError, match="contiguous token rows"):
-        cb._rows_stride("q", _FakeCuda(t(3, 64, 4).transpose(1, 2)))
+        cb._explain_rows("q", _FakeCuda(t(3, 64, 4).transpose(1, 2)))
 
 
 class _FakeCuda:
@@ -97,9 +97,10 @@ class _FakeCuda:
         return getattr(self._t, name)
 
 
-def test_rows_stride_of_views():
+def test_rows_of_views():
     qkv = torch.zeros(5, 8, 64, dtype=torch.bfloat16)
-    f = lambda t: cb._rows_stride("q", _FakeCuda(t))
-    assert f(qkv[:, :4]) == 512 and f(qkv) == 512 and f(qkv[:, 4:6]) == 512
-    assert f(qkv[:1, :4]) == 256                       # one token: its row alone
-    assert f(qkv[:, 3:4]) == 512
+    for rows in (qkv, qkv[:, :4], qkv[:, 4:6], qkv[:1, :4], qkv[:, 3:4], qkv[:0]):
+        assert cb._rows_ok(*rows.shape, rows.stride())
+        cb._explain_rows("q", _FakeCuda(rows))
+    for rows in (qkv.transpose(0, 1), qkv[:, ::2], qkv[:, :, ::2]):
+        assert not cb._rows_ok(*rows.shape, rows.stride()) or rows.shape[0] == 0
