@@ -350,8 +350,9 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   if (!(scale > 0.f) || scale != scale)
     return fail(CB_ERR_INVALID_ARG, "scale must be a positive finite number");
   const int R = NG > 0 ? cb::pre_records(dims->num_seqs, dims->num_tokens) : dims->num_seqs;
+  const int pack = NG > 0 ? cb::pre_pack(dims->num_q_heads / dims->num_kv_heads) : 1;
   const size_t need =
-      NG > 0 ? cb::pre_layout(R, dims->num_tokens, dims->num_q_heads, dims->head_dim, NG).total
+      NG > 0 ? cb::pre_layout(R, dims->num_tokens, dims->num_q_heads, dims->head_dim, NG, pack).total
              : cb::ws_layout(R, dims->num_tokens, dims->num_q_heads, dims->head_dim).total;
   if (workspace_bytes < need)
     return fail(CB_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
@@ -396,6 +397,7 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   a.decode_ctas = dctas;
   a.prefill_ctas = a.chunk_ctas = ds->sm_count;
   a.R = R;
+  a.pack = pack;
   a.prefix_group = NG > 0 ? prefix->prefix_group : nullptr;
   a.prefix_lens = NG > 0 ? prefix->prefix_lens : nullptr;
   a.NG = NG;
@@ -531,7 +533,8 @@ size_t cb_prefix_workspace_size(const cb_dims* dims, int32_t num_groups) {
   if (num_groups <= 0) return num_groups == 0 ? cb_attention_workspace_size(dims) : 0;
   if (cb_attention_workspace_size(dims) == 0 || dims->num_q_heads / dims->num_kv_heads > 16) return 0;
   return cb::pre_layout(cb::pre_records(dims->num_seqs, dims->num_tokens), dims->num_tokens,
-                        dims->num_q_heads, dims->head_dim, num_groups).total;
+                        dims->num_q_heads, dims->head_dim, num_groups,
+                        cb::pre_pack(dims->num_q_heads / dims->num_kv_heads)).total;
 }
 
 cb_status cb_shared_prefix_attention(const void* q, const void* k_pages, const void* v_pages,

@@ -36,7 +36,7 @@ __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorM
   // the merge of the prefixes' parts may start once every CTA of this kernel has (it waits itself)
   if constexpr (kPre) asm volatile("griddepcontrol.launch_dependents;");
   const int b = (int)blockIdx.x;
-  PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D).header);
+  PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D, a.pack).header);
   if constexpr (kPre) {
     // The decode CTAs that the planner leaves without work are the first prefix CTAs; where those
     // are too few, some of the chunk CTAs are the others.

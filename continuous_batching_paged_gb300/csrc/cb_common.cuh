@@ -71,8 +71,8 @@ struct WsLayout {
 __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // S: the most decode records and the most chunk sequences (the sequences; with shared prefixes,
-// pre_records).
-__host__ __device__ inline WsLayout ws_layout(int S, int T, int Hq, int D) {
+// pre_records).  pack: query tokens of a decode record at most (1; with shared prefixes, pre_pack).
+__host__ __device__ inline WsLayout ws_layout(int S, int T, int Hq, int D, int pack = 1) {
   WsLayout L;
   size_t off = 0;
   L.header = off;     off = align_up(off + sizeof(PlanHeader), 256);
@@ -89,18 +89,21 @@ __host__ __device__ inline WsLayout ws_layout(int S, int T, int Hq, int D) {
   L.pf_order = off;   off = align_up(off + sizeof(int32_t) * ((size_t)S + (size_t)T / kPrefillTileM + 1), 256);
   L.merge_cnt = off;  off = align_up(off + sizeof(int32_t) * (size_t)S * (size_t)Hq, 256);
   const size_t slots = (size_t)CB_MAX_DECODE_CTAS + (size_t)S;
-  L.part_ml = off;    off = align_up(off + sizeof(float2) * slots * (size_t)Hq, 256);
-  L.part_o = off;     off = align_up(off + sizeof(float) * slots * (size_t)Hq * (size_t)D, 256);
+  const size_t part_rows = slots * (size_t)pack * (size_t)Hq;
+  L.part_ml = off;    off = align_up(off + sizeof(float2) * part_rows, 256);
+  L.part_o = off;     off = align_up(off + sizeof(float) * part_rows * (size_t)D, 256);
   L.total = off;
   return L;
 }
 
 // ------------------------------------------------------------------------------------------
 // Shared prefixes (cb_prefix.cuh).  A sequence of a group with at most kPreMaxQ query tokens gets
-// one decode record per token for its own keys, and its tokens' rows go into the group's tiles of
-// kPrefillTileM rows for the prefix; longer chunks run the chunk pass over all their keys (it is
-// bound by arithmetic, which sharing does not save).
+// decode records of up to pre_pack tokens for its own keys, and its tokens' rows go into the group's
+// tiles of kPrefillTileM rows for the prefix; longer chunks run the chunk pass over all their keys
+// (it is bound by arithmetic, which sharing does not save).
 constexpr int kPreMaxQ = 8;
+// Tokens of one sequence that a decode warp's 8 columns hold with G query heads each.
+__host__ __device__ inline int pre_pack(int G) { return G <= 8 ? 8 / G : 1; }
 // Prefixes shorter than one K/V tile are left to each sequence's own pass.
 constexpr int kPreMinKeys = kChunkKeys;
 constexpr int kMaxPreCtas = 160;   // CTAs of the prefix pass (at most one per SM)
@@ -136,7 +139,7 @@ struct PreGroup {
 // merge needs to find its parts, in two 16-byte loads.
 struct PreToken {
   int32_t token;         // packed token
-  int32_t rec;           // its decode record
+  int32_t rec;           // 8 x its decode record + its place among the record's tokens
   int32_t tile0, tile1;  // that record's tiles among all decode tiles
   int32_t at;            // its place among the group's tokens
   int32_t n_tok, keys, cost0;  // of the group (PreGroup)
@@ -146,11 +149,11 @@ struct PreToken {
 struct PreLayout {
   size_t rec, cnt, first, map, group, tok, base_ml, base_o, cut_ml, cut_o, total;
 };
-__host__ __device__ inline PreLayout pre_layout(int R, int T, int Hq, int D, int NG) {
+__host__ __device__ inline PreLayout pre_layout(int R, int T, int Hq, int D, int NG, int pack) {
   PreLayout L;
-  size_t off = ws_layout(R, T, Hq, D).total;
-  // per decode record: keys of the prefix computed apart, or 0
-  L.rec = off;     off = align_up(off + sizeof(int32_t) * (size_t)(R + 1), 256);
+  size_t off = ws_layout(R, T, Hq, D, pack).total;
+  // per decode record: keys of the prefix computed apart and query tokens, or zeros
+  L.rec = off;     off = align_up(off + sizeof(int32_t) * 2 * (size_t)(R + 1), 256);
   // per group number: query tokens (then: tokens listed so far), first member, index in the list
   L.cnt = off;     off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.first = off;   off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);

@@ -55,7 +55,8 @@ struct StageInfoBase {
   int p0, p1;    // the sequence's tile range [p0, p1) in the concatenated tile order
 };
 struct StageInfoPre : StageInfoBase {  // with shared prefixes
-  int pre;  // 1: its prefix is computed apart, so its own keys' results stay parts
+  int pre;  // query tokens of a record whose prefix is computed apart: its own keys' results stay
+            // parts (0: a sequence as without prefixes)
 };
 template <bool kPre>
 using StageInfo = std::conditional_t<kPre, StageInfoPre, StageInfoBase>;
@@ -86,7 +87,7 @@ __device__ __forceinline__ int cta_of_tile(long long t, long long n, int N) {
 // batch loaded before any is used (lane i holds output columns PER i .. PER i + PER - 1), and
 // folded in with a running maximum: one L2 round trip per batch, so a sequence cut in two
 // merges 4 heads in one round trip.
-template <int D>
+template <int D, bool kPre>
 __device__ __forceinline__ void merge_parts(const AttnArgs& a, const float2* part_ml,
                                             const float* part_o, int dec, int tok, int kvh,
                                             int cf, int cl, int h0, int h1, int lane) {
@@ -111,7 +112,8 @@ __device__ __forceinline__ void merge_parts(const AttnArgs& a, const float2* par
 #pragma unroll
         for (int cc = 0; cc < kC; ++cc) {
           const int head = kvh * a.G + r0 + hh;
-          const size_t slot = (size_t)(cf + c0 + cc) + dec;
+          size_t slot = (size_t)(cf + c0 + cc) + dec;
+          if constexpr (kPre) slot *= a.pack;
           ml[hh][cc] = make_float2(-INFINITY, 0.f);
 #pragma unroll
           for (int i = 0; i < PER; ++i) v[hh][cc][i] = 0.f;
@@ -210,8 +212,17 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
       for (int ht = 0; ht < NTH; ++ht) {
         mrun[ht][0] = mrun[ht][1] = -INFINITY;
         lrun[ht][0] = lrun[ht][1] = 0.f;
-        const int hl = qoff + ht * 8 + g;  // query head within the group, column g of Q^T
-        const uint32_t* qrow = q32 + (((size_t)si.tok * a.Hq + kvh * a.G + hl) * D) / 2;
+        // query head within the group, column g of Q^T (kPre: the columns of a record's tokens one
+        // after the other; hl < a.G stands for a column in use)
+        int hl = qoff + ht * 8 + g, col_tok = si.tok;
+        if constexpr (kPre && QS == 1) {
+          const int j = hl / a.G;
+          if (j < si.pre) {
+            hl -= j * a.G;
+            col_tok += j;
+          }
+        }
+        const uint32_t* qrow = q32 + (((size_t)col_tok * a.Hq + kvh * a.G + hl) * D) / 2;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           qb[ht][ks][0] = hl < a.G ? __ldg(qrow + ks * 8 + tq) : 0u;
@@ -224,6 +235,17 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
     const uint32_t kst = sbase + stage * SM::kStageBytes;
     const uint32_t vst = kst + SM::kKVBytes;
     const bool tail = si.key0 + kDecodeTileKeys > si.kv;
+    // kPre: the record's tokens before its last see fewer keys; kv_a and kv_b are how many the tokens
+    // of this thread's two columns see
+    int kv_a = si.kv, kv_b = si.kv;
+    bool edge = tail;
+    if constexpr (kPre && QS == 1) {
+      if (si.pre > 1) {
+        kv_a = min(si.kv, si.kv - si.pre + 1 + 2 * tq / a.G);
+        kv_b = min(si.kv, si.kv - si.pre + 1 + (2 * tq + 1) / a.G);
+        edge = si.key0 + kDecodeTileKeys > si.kv - si.pre + 1;
+      }
+    }
 
     const bool head = si.key0 < si.lo;  // keys before the sliding window in this tile
 
@@ -270,7 +292,18 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) mma_bf16_16816(s[ht], kf[ks], qb[ht][ks][0], qb[ht][ks][1]);
     }
-    if (tail || head) {
+    if constexpr (kPre && QS == 1) {
+      if (edge || head) {
+        const int k0 = si.key0 + g, k1 = k0 + 8;
+#pragma unroll
+        for (int ht = 0; ht < NTH; ++ht) {
+          if (k0 >= kv_a || k0 < si.lo) s[ht][0] = -INFINITY;
+          if (k0 >= kv_b || k0 < si.lo) s[ht][1] = -INFINITY;
+          if (k1 >= kv_a || k1 < si.lo) s[ht][2] = -INFINITY;
+          if (k1 >= kv_b || k1 < si.lo) s[ht][3] = -INFINITY;
+        }
+      }
+    } else if (tail || head) {
       const bool dead0 = si.key0 + g >= si.kv || si.key0 + g < si.lo;
       const bool dead1 = si.key0 + g + 8 >= si.kv || si.key0 + g + 8 < si.lo;
 #pragma unroll
@@ -292,12 +325,15 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
         mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
       }
       const float na = fmaxf(mrun[ht][0], ma * sl2), nb = fmaxf(mrun[ht][1], mb * sl2);
-      al[ht][0] = fast_exp2(mrun[ht][0] - na);
-      al[ht][1] = fast_exp2(mrun[ht][1] - nb);
+      // (kPre: a token of a record may see no key of a part's first tile; its m is then -inf, and 0
+      // is subtracted so that no -inf - (-inf) appears)
+      const float sa = kPre && na == -INFINITY ? 0.f : na, sb = kPre && nb == -INFINITY ? 0.f : nb;
+      al[ht][0] = fast_exp2(mrun[ht][0] - sa);
+      al[ht][1] = fast_exp2(mrun[ht][1] - sb);
       mrun[ht][0] = na;
       mrun[ht][1] = nb;
-      const float p0 = fast_exp2(fmaf(s[ht][0], sl2, -na)), p1 = fast_exp2(fmaf(s[ht][1], sl2, -nb));
-      const float p2 = fast_exp2(fmaf(s[ht][2], sl2, -na)), p3 = fast_exp2(fmaf(s[ht][3], sl2, -nb));
+      const float p0 = fast_exp2(fmaf(s[ht][0], sl2, -sa)), p1 = fast_exp2(fmaf(s[ht][1], sl2, -sb));
+      const float p2 = fast_exp2(fmaf(s[ht][2], sl2, -sa)), p3 = fast_exp2(fmaf(s[ht][3], sl2, -sb));
       lrun[ht][0] = lrun[ht][0] * al[ht][0] + (p0 + p2);
       lrun[ht][1] = lrun[ht][1] * al[ht][1] + (p1 + p3);
       resc |= (al[ht][0] != 1.f) || (al[ht][1] != 1.f);
@@ -380,23 +416,36 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
             if (hb < a.G) a.lse[(size_t)si.tok * a.Hq + kvh * a.G + hb] = (mrun[ht][1] + __log2f(lb)) * 0.6931471805599453f;
           }
         } else {
+          // this thread's two columns: their rows of the part, and whether they are in use
           const size_t slot = (size_t)c + si.dec;
+          size_t row_a = slot * a.Hq + kvh * a.G + ha, row_b = slot * a.Hq + kvh * a.G + hb;
+          bool use_a = ha < a.G, use_b = hb < a.G;
+          if constexpr (kPre) {
+            const int ja = QS == 1 ? ha / a.G : 0, jb = QS == 1 ? hb / a.G : 0;  // token of the record
+            if constexpr (QS == 1) {
+              const int n = si.pre > 1 ? si.pre : 1;
+              use_a = ja < n;
+              use_b = jb < n;
+            }
+            row_a = (slot * a.pack + ja) * a.Hq + kvh * a.G + (ha - ja * a.G);
+            row_b = (slot * a.pack + jb) * a.Hq + kvh * a.G + (hb - jb * a.G);
+          }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            if (ha < a.G) {
-              float* po = part_o + (slot * a.Hq + kvh * a.G + ha) * D + 16 * mt + g;
+            if (use_a) {
+              float* po = part_o + row_a * D + 16 * mt + g;
               po[0] = o[mt][ht][0];
               po[8] = o[mt][ht][2];
             }
-            if (hb < a.G) {
-              float* po = part_o + (slot * a.Hq + kvh * a.G + hb) * D + 16 * mt + g;
+            if (use_b) {
+              float* po = part_o + row_b * D + 16 * mt + g;
               po[0] = o[mt][ht][1];
               po[8] = o[mt][ht][3];
             }
           }
           if (g == 0) {
-            if (ha < a.G) part_ml[slot * a.Hq + kvh * a.G + ha] = make_float2(mrun[ht][0], la);
-            if (hb < a.G) part_ml[slot * a.Hq + kvh * a.G + hb] = make_float2(mrun[ht][1], lb);
+            if (use_a) part_ml[row_a] = make_float2(mrun[ht][0], la);
+            if (use_b) part_ml[row_b] = make_float2(mrun[ht][1], lb);
           }
         }
       }
@@ -422,7 +471,7 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
           if (last) __threadfence();
         }
         if (last)
-          merge_parts<D>(a, part_ml, part_o, si.dec, si.tok, kvh, cf, cl, qoff,
+          merge_parts<D, kPre>(a, part_ml, part_o, si.dec, si.tok, kvh, cf, cl, qoff,
                          qoff + 8 < a.G ? qoff + 8 : a.G, lane);
       }
     }
@@ -460,16 +509,16 @@ __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensor
     const int s = rec.x, tok = rec.y, kv = rec.z;
     // with a sliding window the sequence's tiles start at the one holding its first key
     int lo_key = window_first_key(kv - 1, a.window);
-    int pre = 0;
+    int2 pre = make_int2(0, 0);
     if constexpr (kPre) {  // and with a prefix computed apart, at the one holding its end
-      pre = reinterpret_cast<const int32_t*>(
-          a.ws + pre_layout(a.R, a.T, a.Hq, a.D, a.NG).rec)[d];
-      lo_key = pre;
+      pre = reinterpret_cast<const int2*>(
+          a.ws + pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack).rec)[d];
+      lo_key = pre.x;
     }
     const int first_tile_key = lo_key / kDecodeTileKeys * kDecodeTileKeys;
     const long long lo = t > p0 ? t : p0;
     const long long hi = t1 < p1 ? t1 : p1;
-    const bool complete = p0 >= t0 && p1 <= t1 && (!kPre || pre == 0);
+    const bool complete = p0 >= t0 && p1 <= t1 && (!kPre || pre.y == 0);
     const int32_t* row = a.block_table + (size_t)s * a.max_blocks;
     // The consumers read this sequence's query rows (the CTA's head group) at its first tile,
     // a few stages from now: pull them into L2 so that the read does not wait on HBM.
@@ -518,7 +567,7 @@ __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensor
           si.key0 = key0;
           si.p0 = (int)p0;
           si.p1 = (int)p1;
-          if constexpr (kPre) si.pre = pre > 0;
+          if constexpr (kPre) si.pre = pre.y;
           si.flags = (tile == lo ? kInfoFirst : 0u) | (tile == hi - 1 ? kInfoLast : 0u) |
                      (complete ? kInfoComplete : 0u);
           mbar_arrive_expect_tx(bar_full + 8 * stage,
@@ -563,7 +612,7 @@ __device__ __forceinline__ void decode_cta(const AttnArgs& a, const CUtensorMap*
   const int HB = a.Hkv < decode_kv_heads<QS>() ? a.Hkv : decode_kv_heads<QS>();
   const int n_cons = QS * HB;  // consumer warps; the producer is warp n_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D);
+  const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, a.pack);
   const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.ws + L.header);
   const int4* dec_rec = reinterpret_cast<const int4*>(a.ws + L.dec_rec);
   const int32_t* cta_first = reinterpret_cast<const int32_t*>(a.ws + L.cta_first);

@@ -51,6 +51,7 @@ struct AttnArgs {
   int chunk_ctas;      // the same, whatever this launch runs (for the planner)
   int R;               // decode records the workspace is laid out for (S; pre_records(S, T) with
                        // shared prefixes)
+  int pack;            // most query tokens of a decode record (1; pre_pack(G) with shared prefixes)
   const int32_t* prefix_group;  // [S]: the group whose prefix a sequence shares, or -1
   const int32_t* prefix_lens;   // [NG]: keys of each group's prefix
   int NG;                       // groups (0 without shared prefixes)

@@ -169,9 +169,9 @@ struct PreSeq {
 // each) and kPreMinKeys keys; after bad metadata none does, and each sequence is computed alone.
 __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], int32_t* cnt,
                                              int32_t* first, int32_t* map, PreSeq& mine) {
-  const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG);
+  const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack);
   PreGroup* groups = reinterpret_cast<PreGroup*>(a.ws + PL.group);
-  PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D).header);
+  PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D, a.pack).header);
   const int tid = threadIdx.x;
   const long long max_kv = (long long)a.max_blocks * a.bs;
   __shared__ unsigned long long s_total;
@@ -318,7 +318,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   __shared__ int32_t s_pf_seq[kSeqs];
   __shared__ int2 s_pf_lens[kSeqs];  // (q_len, prior context) of each chunk sequence
   __shared__ int32_t s_groups[kPre ? 3 * kPlanSmemGroups : 1];
-  const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D);
+  const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, a.pack);
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + L.header);
   int32_t* dec_seq = reinterpret_cast<int32_t*>(a.ws + L.dec_seq);
   int32_t* dec_prefix = reinterpret_cast<int32_t*>(a.ws + L.dec_prefix);
@@ -332,7 +332,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   float my_keys = 0.f, my_pairs = 0.f;  // work estimates for the decode / chunk balance
   // shared prefixes: their work per KV head, and per group number cnt, first member and map
   int pre_cost = 0;
-  const PreLayout PL = kPre ? pre_layout(a.R, a.T, a.Hq, a.D, a.NG) : PreLayout{};
+  const PreLayout PL = kPre ? pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack) : PreLayout{};
   const bool few = a.NG <= kPlanSmemGroups;
   int32_t* grp_cnt = few ? s_groups : reinterpret_cast<int32_t*>(a.ws + PL.cnt);
   int32_t* grp_first = few ? s_groups + kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.first);
@@ -367,12 +367,14 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
         bad = true;
       } else if (kPre && pre_cost > 0 && q_len > 0 && q_len <= kPreMaxQ &&
                  (grp = base == 0 ? mine.group : a.prefix_group[s]) >= 0 && grp_map[grp] >= 0) {
-        // one record per token: the tiles from the one holding the prefix's end to its last key
+        // records of a.pack tokens: the tiles from the one holding the prefix's end to the one
+        // holding the last key that the record's last token sees
         keys = base == 0 ? mine.keys : a.prefix_lens[grp];
         const int first = keys / kDecodeTileKeys * kDecodeTileKeys;
-        v[0] = q_len;
-        for (int i = 0; i < q_len; ++i)
-          v[1] += (kv - q_len + i + 1 - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
+        for (int i = 0; i < q_len; i += a.pack) {
+          v[0] += 1;
+          v[1] += (kv - max(q_len - i - a.pack, 0) - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
+        }
         my_keys += (float)(kv - keys);
       } else if (q_len == 1) {
         grp = -1;
@@ -402,26 +404,29 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     if (kPre && grp >= 0 && v[0]) {
       // The tokens' places in the group's list come in any order: a row's result does not depend
       // on the tile it is computed in.
-      const int q_len = v[0], first = keys / kDecodeTileKeys * kDecodeTileKeys;
+      const int q_len = base == 0 ? mine.c1 - mine.c0 : a.cu_seqlens_q[s + 1] - tok;
+      const int first = keys / kDecodeTileKeys * kDecodeTileKeys;
       const int at = atomicAdd(&grp_cnt[grp], q_len);
       const PreGroup group = reinterpret_cast<const PreGroup*>(a.ws + PL.group)[grp_map[grp]];
-      int tile = carry[1] + ex[1];
-      for (int j = 0; j < q_len; ++j) {
-        const int i = carry[0] + ex[0] + j, n_keys = kv - q_len + j + 1;
+      int tile = carry[1] + ex[1], i = carry[0] + ex[0];
+      for (int j = 0; j < q_len; j += a.pack, ++i) {
+        const int n = min(a.pack, q_len - j), n_keys = kv - (q_len - j - n);
+        const int n_tiles = (n_keys - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
         dec_seq[i] = s;
         dec_prefix[i] = tile;
         dec_rec[i] = make_int4(s, tok + j, n_keys, tile);
         if (i < kSeqs) s_dec_prefix[i] = tile;
-        reinterpret_cast<int32_t*>(a.ws + PL.rec)[i] = keys;
-        const int n_tiles = (n_keys - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
-        int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 2 * (size_t)(group.tok0 + at + j);
-        entry[0] = make_int4(tok + j, i, tile, tile + n_tiles);
-        entry[1] = make_int4(at + j, group.n_tok, keys, group.cost0);
+        reinterpret_cast<int2*>(a.ws + PL.rec)[i] = make_int2(keys, n);
+        for (int t = 0; t < n; ++t) {
+          int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 2 * (size_t)(group.tok0 + at + j + t);
+          entry[0] = make_int4(tok + j + t, 8 * i + t, tile, tile + n_tiles);
+          entry[1] = make_int4(at + j + t, group.n_tok, keys, group.cost0);
+        }
         tile += n_tiles;
       }
     } else if (v[0]) {
       const int i = carry[0] + ex[0];
-      if constexpr (kPre) reinterpret_cast<int32_t*>(a.ws + PL.rec)[i] = 0;
+      if constexpr (kPre) reinterpret_cast<int2*>(a.ws + PL.rec)[i] = make_int2(0, 0);
       dec_seq[i] = s;
       dec_prefix[i] = carry[1] + ex[1];
       dec_rec[i] = make_int4(s, tok, kv, carry[1] + ex[1]);

@@ -84,8 +84,8 @@ template <int D, int HP>
 __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnArgs a) {
   constexpr int PER = D / 32, kC = 8 / HP;  // columns per lane, parts' rows of O in flight
   const int lane = threadIdx.x & 31;
-  const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D);
-  const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG);
+  const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, a.pack);
+  const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack);
   const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.ws + L.header);
   const int4* list = reinterpret_cast<const int4*>(a.ws + PL.tok);
   __nv_bfloat16* outg = static_cast<__nv_bfloat16*>(a.out);
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnA
                                         a.ws + (cut ? PL.cut_o : PL.base_o)) + at * D);
         }
       } else if (p < nparts) {
-        const size_t at = ((size_t)(df + p - n_pre) + t.rec) * a.Hq + head0;
+        const size_t at = (((size_t)(df + p - n_pre) + (t.rec >> 3)) * a.pack + (t.rec & 7)) * a.Hq + head0;
         pml = reinterpret_cast<const float2*>(a.ws + L.part_ml) + at;
         po = (unsigned long long)(reinterpret_cast<const float*>(a.ws + L.part_o) + at * D);
       }

@@ -404,3 +404,22 @@ def test_empty_batches(cuda_lib):
     out, lse = d.attend()
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
     assert cb.get_device_error() == cb.CB_OK
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 1), (3, 1), (4, 1), (8, 2), (5, 1), (8, 1), (12, 1)])
+def test_verified_tokens_share_records(cuda_lib, Hq, Hkv):
+    # up to 8 query tokens of a member: 8 / G of them in one record of the decode pass, whose tokens
+    # see different numbers of own keys; own lengths put those edges inside a 16-key tile, at its
+    # border, and into a tile of which the first tokens see nothing
+    rng = np.random.default_rng(Hq)
+    q = [1 + i % 8 for i in range(48)]
+    own = [n + int(x) for n, x in zip(q, rng.integers(0, 40, 48))]
+    own[:8] = [1, 2, 3, 4, 5, 6, 7, 8]                       # nothing but this step's tokens
+    group = [i % 2 for i in range(48)]
+    # prefix ends at tile borders and beside them
+    for prefix in ([256, 144], [131, 271]):
+        for ctas in (0, 40):
+            b = grouped_batch(q, own, group, prefix, Hq, Hkv, 64, 16, seed=910 + Hq)
+            check(b, decode_ctas=ctas)
+    # (slots behind kv_len are NaN)
+    check(grouped_batch([8, 7, 8], [8, 39, 41], [0, 0, 0], [144], Hq, Hkv, 128, 16, seed=911))
