@@ -349,7 +349,8 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
     return fail(CB_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   if (!(scale > 0.f) || scale != scale)
     return fail(CB_ERR_INVALID_ARG, "scale must be a positive finite number");
-  const int R = NG > 0 ? cb::pre_records(dims->num_seqs, dims->num_tokens) : dims->num_seqs;
+  const int R = NG > 0 ? cb::pre_records(dims->num_seqs, dims->num_tokens, dims->num_q_heads)
+                       : dims->num_seqs;
   const int pack = NG > 0 ? cb::pre_pack(dims->num_q_heads / dims->num_kv_heads) : 1;
   const size_t need =
       NG > 0 ? cb::pre_layout(R, dims->num_tokens, dims->num_q_heads, dims->head_dim, NG, pack).total
@@ -532,7 +533,8 @@ cb_status cb_append_attention(const void* k_new, const void* v_new, void* k_page
 size_t cb_prefix_workspace_size(const cb_dims* dims, int32_t num_groups) {
   if (num_groups <= 0) return num_groups == 0 ? cb_attention_workspace_size(dims) : 0;
   if (cb_attention_workspace_size(dims) == 0 || dims->num_q_heads / dims->num_kv_heads > 16) return 0;
-  return cb::pre_layout(cb::pre_records(dims->num_seqs, dims->num_tokens), dims->num_tokens,
+  return cb::pre_layout(cb::pre_records(dims->num_seqs, dims->num_tokens, dims->num_q_heads),
+                        dims->num_tokens,
                         dims->num_q_heads, dims->head_dim, num_groups,
                         cb::pre_pack(dims->num_q_heads / dims->num_kv_heads)).total;
 }

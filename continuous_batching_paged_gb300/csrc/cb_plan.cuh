@@ -158,6 +158,7 @@ constexpr int kPlanSmemGroups = 1024;
 // What the first look at a sequence finds (kept for the second where one round covers the batch).
 struct PreSeq {
   int c0, c1, kv, group, keys;
+  int tok0, cost0;  // a chunk that is a group of its own: its first list entry (else -1), PreGroup
 };
 
 // With shared prefixes: which groups' prefixes are computed once.  Fills the group list, and per
@@ -167,6 +168,8 @@ struct PreSeq {
 //
 // A group takes part when it has at least two query tokens (from members with at most kPreMaxQ
 // each) and kPreMinKeys keys; after bad metadata none does, and each sequence is computed alone.
+// Chunks that are groups of their own (kPreChunkItems; in batches of one round) follow the others in
+// the list.
 __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], int32_t* cnt,
                                              int32_t* first, int32_t* map, PreSeq& mine) {
   const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack);
@@ -174,8 +177,8 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D, a.pack).header);
   const int tid = threadIdx.x;
   const long long max_kv = (long long)a.max_blocks * a.bs;
-  __shared__ unsigned long long s_total;
-  if (tid == 0) s_total = 0;
+  __shared__ unsigned long long s_total, s_units;
+  if (tid == 0) s_total = s_units = 0;
   for (int g = tid; g < a.NG; g += kPlanThreads) {
     cnt[g] = 0;
     first[g] = 0x7fffffff;
@@ -184,7 +187,7 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
   bool bad = false;
   for (int base = 0; base < a.S; base += kPlanThreads) {
     const int s = base + tid;
-    PreSeq q = {0, 0, 0, -1, 0};
+    PreSeq q = {0, 0, 0, -1, 0, -1, 0};
     if (s < a.S) {
       q.c0 = a.cu_seqlens_q[s];
       q.c1 = a.cu_seqlens_q[s + 1];
@@ -210,8 +213,20 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
       atomicAdd(&cnt[q.group], q_len);
       atomicMin(&first[q.group], s);
     }
+    if (lens_ok && s < a.S && q_len > 1) {
+      const int rows = pf_unit_tiles(a.G) * kPrefillTileM;
+      if (!member)
+        atomicAdd(&s_units, (unsigned long long)((q_len + rows - 1) / rows));
+    }
   }
   bad = __syncthreads_or(bad) != 0;
+  // this thread's sequence as a group of its own: its query tokens, or 0
+  const int my_q = mine.c1 - mine.c0, my_ctx = mine.kv - my_q;
+  const int own_tokens =
+      !bad && a.S <= kPlanThreads && my_q > kPreMaxQ && my_ctx >= kPreMinKeys &&
+              s_units * (unsigned long long)(pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq) < kPreChunkItems
+          ? my_q
+          : 0;
   auto shared_tokens = [&](int g, int keys) {  // tokens of group g if its prefix is computed once
     return bad || g >= a.NG || cnt[g] < 2 || keys < kPreMinKeys ? 0 : cnt[g];
   };
@@ -219,8 +234,12 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
     const int keys = g == tid ? my_keys : a.prefix_lens[g], n = shared_tokens(g, keys);
     if (n > 0) atomicAdd(&s_total, (unsigned long long)pre_shape(n, keys, a.G).per);
   }
-  __syncthreads();
-  if (s_total > kPreMaxCost) bad = true;  // (32 bits hold every cost below)
+  const int own_cost = own_tokens > 0 ? (int)min((long long)kPreMaxCost + 1,
+                                                 pre_shape(own_tokens, my_ctx, a.G).per) : 0;
+  if (own_cost > 0) atomicAdd(&s_total, (unsigned long long)own_cost);
+  const bool any_own = __syncthreads_or(own_tokens) != 0;
+  const bool too_much = s_total > kPreMaxCost;  // (32 bits hold every cost below)
+  bad |= too_much;
   int carry[4] = {0, 0, 0, 0};  // groups, tokens, cost, keys (an estimate: it may wrap)
   for (int base = 0; base < a.NG; base += kPlanThreads) {
     const int g = base + tid;
@@ -234,6 +253,17 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
     if (g < a.NG) {
       map[g] = n > 0 ? carry[0] + ex[0] : -1;
       cnt[g] = 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) carry[k] += tot[k];
+  }
+  if (any_own && !too_much) {
+    int v[4] = {own_tokens > 0, own_tokens, own_cost, own_tokens > 0 ? my_ctx : 0}, ex[4], tot[4];
+    block_scan4(v, ex, tot, sw);
+    if (own_tokens > 0) {
+      mine.tok0 = carry[1] + ex[1];
+      mine.cost0 = carry[2] + ex[2];
+      groups[carry[0] + ex[0]] = {mine.cost0, own_tokens, mine.tok0, my_ctx, tid};
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) carry[k] += tot[k];
@@ -337,8 +367,12 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   int32_t* grp_cnt = few ? s_groups : reinterpret_cast<int32_t*>(a.ws + PL.cnt);
   int32_t* grp_first = few ? s_groups + kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.first);
   int32_t* grp_map = few ? s_groups + 2 * kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.map);
-  PreSeq mine = {};
+  PreSeq mine = {0, 0, 0, -1, 0, -1, 0};
   if constexpr (kPre) pre_cost = plan_prefixes(a, sw, grp_cnt, grp_first, grp_map, mine);
+  // kPre: chunks that are groups of their own: (first token, tokens, first list entry, keys), cost0
+  __shared__ int s_chunks;
+  __shared__ int4 s_chunk[kPre ? kPreChunkItems : 1][2];
+  if (kPre && tid == 0) s_chunks = 0;  // (the loop's barriers follow)
   bool bad = false;
   const int unit_rows = pf_unit_tiles(a.G) * kPrefillTileM;
   int carry[4] = {0, 0, 0, 0};
@@ -376,6 +410,12 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
           v[1] += (kv - max(q_len - i - a.pack, 0) - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
         }
         my_keys += (float)(kv - keys);
+      } else if (kPre && base == 0 && mine.tok0 >= 0) {
+        // a chunk whose context is computed apart: its own keys
+        keys = kv - q_len;
+        v[2] = 1;
+        v[3] = (q_len + unit_rows - 1) / unit_rows;
+        my_pairs += 0.5f * (float)q_len * (float)(q_len + 1);
       } else if (q_len == 1) {
         grp = -1;
         // tiles from the one holding the window's first key (every key without a window)
@@ -434,6 +474,16 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     }
     if (v[2]) {
       const int i = carry[2] + ex[2];
+      if constexpr (kPre) {
+        int2 pre = make_int2(0, 0);
+        if (base == 0 && mine.tok0 >= 0) {  // its tokens' list entries are written below, by all
+          pre = make_int2(keys, mine.tok0);
+          const int x = atomicAdd(&s_chunks, 1);  // (fewer than kPreChunkItems)
+          s_chunk[x][0] = make_int4(tok, mine.c1 - mine.c0, mine.tok0, keys);
+          s_chunk[x][1] = make_int4(mine.cost0, 0, 0, 0);
+        }
+        reinterpret_cast<int2*>(a.ws + PL.pf)[i] = pre;
+      }
       pf_seq[i] = s;
       pf_prefix[i] = carry[3] + ex[3];
       if (i < kSeqs) {
@@ -445,6 +495,18 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) carry[k] += tot[k];
+  }
+  if constexpr (kPre) {
+    __syncthreads();
+    for (int x = 0; x < s_chunks; ++x) {
+      const int4 ch = s_chunk[x][0];
+      const int cost0 = s_chunk[x][1].x;
+      for (int t = tid; t < ch.y; t += kPlanThreads) {
+        int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 2 * (size_t)(ch.z + t);
+        entry[0] = make_int4(ch.x + t, -1, 0, 0);
+        entry[1] = make_int4(t, ch.y, ch.w, cost0);
+      }
+    }
   }
   // With every length valid the query ranges are disjoint, so the units fit pf_order (at most
   // S + T / 128); after an invalid length the chunk pass is given no work.
@@ -520,7 +582,8 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
         n = choose_prefix_split(a, keys * row, (float)hdr->pre_keys * row, pre_cost,
                                 pairs * (float)(4 * a.D * a.Hq), ntiles, n_dec);
       // the decode CTAs without work; where a given number leaves none, an eighth of the chunk CTAs
-      const int idle = pre_idle_count(pre_head_groups(a.Hkv, a.G), n, a.decode_ctas);
+      int idle = pre_idle_count(pre_head_groups(a.Hkv, a.G), n, a.decode_ctas);
+      if (n_units > 0) idle -= idle / 8;  // (chunk CTAs take those at once)
       if (tid == 0) hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, pre_cost, a.Hkv);
     } else if (a.decode_auto) {
       n = choose_decode_ctas(keys * (float)(a.Hkv * a.D * 4), pairs * (float)(4 * a.D * a.Hq),

@@ -6,8 +6,8 @@
 // the same sum in another order, so a row's result is that of cb_ragged_paged_attention within
 // rounding.
 //
-// Own keys are streamed by the decode pass (cb_decode.cuh), as ever, from the prefix's end on; a
-// member with up to kPreMaxQ query tokens has one record per token.  The prefix is a dense
+// Own keys are streamed by the decode pass (cb_decode.cuh), as ever, from the prefix's end on, or by
+// the chunk pass for a member with more than kPreMaxQ query tokens.  The prefix is a dense
 // contraction (all rows of the group see all its keys) and runs on the 5th-generation tensor cores
 // (cb_prefix.cuh): its K/V are read once per 2 x 128 rows (from HBM at most once) instead of once
 // per query token, which is what bounds the batch otherwise.  The passes run side by side in one
@@ -114,8 +114,9 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnA
       tb = __ldcg(list + 2 * (size_t)i + 1);
     }
     const PreToken t = {ta.x, ta.y, ta.z, ta.w, tb.x, tb.y, tb.z, tb.w};
-    // own keys: decode CTAs df .. dl
-    const int df = cta_of_tile(t.tile0, ntiles, N), dl = cta_of_tile(t.tile1 - 1, ntiles, N);
+    // own keys: decode CTAs df .. dl, or the one part of a chunk's token
+    const int df = t.rec < 0 ? 0 : cta_of_tile(t.tile0, ntiles, N);
+    const int dl = t.rec < 0 ? 0 : cta_of_tile(t.tile1 - 1, ntiles, N);
     // the prefix: the chain of this token's unit, prefix CTAs pf .. pl
     const PreShape sh = pre_shape(t.n_tok, t.keys, a.G);
     const int tile = t.at / per_tile, u = tile >> 1;
@@ -150,8 +151,13 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnA
           po = (unsigned long long)(reinterpret_cast<const float*>(
                                         a.ws + (cut ? PL.cut_o : PL.base_o)) + at * D);
         }
+      } else if (p < nparts && t.rec < 0) {
+        const size_t at = (size_t)i * a.Hq + head0;
+        pml = reinterpret_cast<const float2*>(a.ws + PL.own_ml) + at;
+        po = (unsigned long long)(reinterpret_cast<const float*>(a.ws + PL.own_o) + at * D);
       } else if (p < nparts) {
-        const size_t at = (((size_t)(df + p - n_pre) + (t.rec >> 3)) * a.pack + (t.rec & 7)) * a.Hq + head0;
+        const size_t at =
+            (((size_t)(df + p - n_pre) + (t.rec >> 3)) * a.pack + (t.rec & 7)) * a.Hq + head0;
         pml = reinterpret_cast<const float2*>(a.ws + L.part_ml) + at;
         po = (unsigned long long)(reinterpret_cast<const float*>(a.ws + L.part_o) + at * D);
       }

@@ -249,8 +249,8 @@ cb_status cb_append_attention(const void* k_new, const void* v_new, void* k_page
  * length is allowed, not only whole blocks.  The result is cb_ragged_paged_attention's within
  * rounding, whatever the grouping: the groups say what may be computed once, not what is attended
  * to.  Where sharing does not pay the members are computed alone: groups of one query token,
- * prefixes below 128 keys, members with more than 8 query tokens (prompt chunks; members with 2
- * to 8, as in speculative decoding, do share).  Several levels of sharing (a tree) are given as
+ * prefixes below 128 keys, members with more than 8 query tokens (prompt chunks) in batches with
+ * enough chunk tokens to fill the GPU.  Several levels of sharing (a tree) are given as
  * the one level that saves most.  (An addition of this library: the pages share prefix blocks in
  * the cache, "LLM learning path 3.3", section "PagedAttention: block tables", and leave the
  * attention over them to each sequence.)
@@ -274,8 +274,8 @@ typedef struct {
  * cb_prefix_workspace_size -- bytes of device scratch for num_groups groups; pure host arithmetic
  * on what cb_attention_workspace_size uses, num_kv_heads and num_groups; 0 when dims is NULL or
  * invalid or num_groups is negative.  Beside the plan and the partial results of the decode pass
- * it holds the prefixes' partial results: fp32 output rows of up to min(8 num_seqs, num_tokens)
- * query tokens, and 20 MB (head_dim 128) or less for the parts of split prefixes.
+ * it holds partial results: two fp32 output rows per query head of up to min(num_tokens,
+ * 8 num_seqs + 38912 / num_q_heads) query tokens, and 21 MB (head_dim 128) for split prefixes.
  */
 size_t cb_prefix_workspace_size(const cb_dims* dims, int32_t num_groups);
 

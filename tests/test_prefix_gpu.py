@@ -423,3 +423,25 @@ def test_verified_tokens_share_records(cuda_lib, Hq, Hkv):
             check(b, decode_ctas=ctas)
     # (slots behind kv_len are NaN)
     check(grouped_batch([8, 7, 8], [8, 39, 41], [0, 0, 0], [144], Hq, Hkv, 128, 16, seed=911))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (3, 1, 64), (16, 1, 64), (5, 5, 128)])
+@pytest.mark.parametrize("prefix", [128, 200, 384, 1000])
+def test_chunks_of_a_group(cuda_lib, Hq, Hkv, D, prefix):
+    # members with more than 8 query tokens: the prefix with the group's other tokens, the own keys in
+    # the chunk pass from the prefix's end on; own lengths from the chunk itself to several tiles more
+    q = [9, 1, 128, 129, 300, 1, 40, 8]
+    own = [9, 4, 128, 400, 300, 30, 41, 8]
+    b = grouped_batch(q, own, [0, 0, 0, 0, 0, -1, -1, 0], [prefix], Hq, Hkv, D, 16, seed=920 + prefix)
+    check(b)
+    check(b, serial=True)
+
+
+def test_chunks_too_many_to_share(cuda_lib):
+    # enough chunk items to fill the GPU: the chunks are computed alone, the other members share
+    b = grouped_batch([700, 1, 600, 3, 1], [800, 4, 600, 9, 70], [0, 0, 0, 0, 0], [300], 64, 8, 64, 32,
+                      seed=930)
+    check(b)
+    # one chunk alone in its group, and a group of nothing but chunks
+    check(grouped_batch([200, 1, 30, 45], [201, 9, 30, 60], [0, -1, 1, 1], [260, 400], 8, 2, 64, 16,
+                        seed=931))
