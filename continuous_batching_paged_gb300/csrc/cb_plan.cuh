@@ -1,4 +1,4 @@
-// Batch planner of the attention pass (device code; run by one CTA of kPlanThreads threads).
+// Batch planner of the attention pass (device code; run by one CTA).
 #pragma once
 
 #include "cb_common.cuh"
@@ -13,8 +13,15 @@ namespace cb {
 // read.  Nothing returns to the host.
 
 constexpr int kPlanThreads = 1024;
+// With shared prefixes the planner has more to compute per sequence and its time is instructions: a
+// batch of one round (a sequence per thread) takes 5 us with 256 threads and 8 us with 1024, whose
+// idle warps run through every step too.
+constexpr int kPrePlanThreads = 256;
+template <bool kPre>
+constexpr int plan_threads() { return kPre ? kPrePlanThreads : kPlanThreads; }
 
-// Exclusive block-wide scan of four counters at once; returns the block totals in tot[].
+// Exclusive block-wide scan of four counters at once (NT threads); returns the block totals in tot[].
+template <int NT>
 __device__ __forceinline__ void block_scan4(int v[4], int ex[4], int tot[4], int (*sw)[4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc[4];
@@ -36,7 +43,7 @@ __device__ __forceinline__ void block_scan4(int v[4], int ex[4], int tot[4], int
   if (warp == 0) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      int x = sw[lane][k];
+      int x = NT == 1024 || lane < NT / 32 ? sw[lane][k] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -170,8 +177,10 @@ struct PreSeq {
 // each) and kPreMinKeys keys; after bad metadata none does, and each sequence is computed alone.
 // Chunks that are groups of their own (kPreChunkItems; in batches of one round) follow the others in
 // the list.
+// lens: the groups' prefix lengths (in shared memory where all of them fit, else a.prefix_lens).
 __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], int32_t* cnt,
-                                             int32_t* first, int32_t* map, PreSeq& mine) {
+                                             int32_t* first, int32_t* map, const int32_t* lens,
+                                             PreSeq& mine) {
   const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack);
   PreGroup* groups = reinterpret_cast<PreGroup*>(a.ws + PL.group);
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D, a.pack).header);
@@ -179,13 +188,12 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
   const long long max_kv = (long long)a.max_blocks * a.bs;
   __shared__ unsigned long long s_total, s_units;
   if (tid == 0) s_total = s_units = 0;
-  for (int g = tid; g < a.NG; g += kPlanThreads) {
+  for (int g = tid; g < a.NG; g += kPrePlanThreads) {
     cnt[g] = 0;
     first[g] = 0x7fffffff;
   }
-  const int my_keys = tid < a.NG ? a.prefix_lens[tid] : 0;  // (first round of the loops over groups)
   bool bad = false;
-  for (int base = 0; base < a.S; base += kPlanThreads) {
+  for (int base = 0; base < a.S; base += kPrePlanThreads) {
     const int s = base + tid;
     PreSeq q = {0, 0, 0, -1, 0, -1, 0};
     if (s < a.S) {
@@ -197,57 +205,60 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
     const int q_len = q.c1 - q.c0;
     const bool lens_ok = !(q.c0 < 0 || q.c1 > a.T || (s == 0 && q.c0 != 0) || q_len < 0 ||
                            q.kv < q_len || q.kv > max_kv);
+    if (base == 0) __syncthreads();  // cnt, first and lens are set
     bool group_ok = true, member = lens_ok && s < a.S && q_len > 0 && q.group != -1;
     if (member) {
-      q.keys = q.group >= 0 && q.group < a.NG ? a.prefix_lens[q.group] : -1;
+      q.keys = q.group >= 0 && q.group < a.NG ? lens[q.group] : -1;
       group_ok = q.keys >= 0 && q.keys <= q.kv - q_len;
       if (!group_ok) report(a.err, kErrOutOfRange);
       member = group_ok && q_len <= kPreMaxQ;
     }
     bad |= !lens_ok || !group_ok;  // (bad lengths are reported by the caller)
-    if (base == 0) {
-      __syncthreads();  // cnt and first are set
-      mine = q;
-    }
+    if (base == 0) mine = q;
     if (member) {
       atomicAdd(&cnt[q.group], q_len);
       atomicMin(&first[q.group], s);
     }
-    if (lens_ok && s < a.S && q_len > 1) {
-      const int rows = pf_unit_tiles(a.G) * kPrefillTileM;
-      if (!member)
-        atomicAdd(&s_units, (unsigned long long)((q_len + rows - 1) / rows));
+    // units of the chunk pass (a warp's sum first: 64-bit atomics on shared memory are slow)
+    const int rows = pf_unit_tiles(a.G) * kPrefillTileM;
+    const bool chunk = lens_ok && s < a.S && q_len > 1 && !member;
+    if (__any_sync(0xffffffffu, chunk)) {
+      unsigned long long n = chunk ? (unsigned long long)((q_len + rows - 1) / rows) : 0ull;
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if ((tid & 31) == 0) atomicAdd(&s_units, n);
     }
   }
   bad = __syncthreads_or(bad) != 0;
   // this thread's sequence as a group of its own: its query tokens, or 0
   const int my_q = mine.c1 - mine.c0, my_ctx = mine.kv - my_q;
   const int own_tokens =
-      !bad && a.S <= kPlanThreads && my_q > kPreMaxQ && my_ctx >= kPreMinKeys &&
+      !bad && a.S <= kPrePlanThreads && my_q > kPreMaxQ && my_ctx >= kPreMinKeys &&
               s_units * (unsigned long long)(pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq) < kPreChunkItems
           ? my_q
           : 0;
   auto shared_tokens = [&](int g, int keys) {  // tokens of group g if its prefix is computed once
     return bad || g >= a.NG || cnt[g] < 2 || keys < kPreMinKeys ? 0 : cnt[g];
   };
-  for (int g = tid; g < a.NG; g += kPlanThreads) {
-    const int keys = g == tid ? my_keys : a.prefix_lens[g], n = shared_tokens(g, keys);
-    if (n > 0) atomicAdd(&s_total, (unsigned long long)pre_shape(n, keys, a.G).per);
-  }
   const int own_cost = own_tokens > 0 ? (int)min((long long)kPreMaxCost + 1,
                                                  pre_shape(own_tokens, my_ctx, a.G).per) : 0;
-  if (own_cost > 0) atomicAdd(&s_total, (unsigned long long)own_cost);
+  unsigned long long total = own_cost;
+  for (int g = tid; g < a.NG; g += kPrePlanThreads) {
+    const int n = shared_tokens(g, lens[g]);
+    if (n > 0) total += (unsigned long long)pre_shape(n, lens[g], a.G).per;
+  }
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if ((tid & 31) == 0 && total > 0) atomicAdd(&s_total, total);
   const bool any_own = __syncthreads_or(own_tokens) != 0;
   const bool too_much = s_total > kPreMaxCost;  // (32 bits hold every cost below)
   bad |= too_much;
   int carry[4] = {0, 0, 0, 0};  // groups, tokens, cost, keys (an estimate: it may wrap)
-  for (int base = 0; base < a.NG; base += kPlanThreads) {
+  for (int base = 0; base < a.NG; base += kPrePlanThreads) {
     const int g = base + tid;
-    const int keys = base == 0 ? my_keys : g < a.NG ? a.prefix_lens[g] : 0;
+    const int keys = g < a.NG ? lens[g] : 0;
     const int n = shared_tokens(g, keys);
     int v[4] = {n > 0, n, n > 0 ? (int)pre_shape(n, keys, a.G).per : 0, n > 0 ? keys : 0};
     int ex[4], tot[4];
-    block_scan4(v, ex, tot, sw);  // (its barriers also part the reads of cnt from the writes)
+    block_scan4<kPrePlanThreads>(v, ex, tot, sw);  // (its barriers also part the reads of cnt from the writes)
     if (n > 0)
       groups[carry[0] + ex[0]] = {carry[2] + ex[2], n, carry[1] + ex[1], keys, first[g]};
     if (g < a.NG) {
@@ -259,7 +270,7 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
   }
   if (any_own && !too_much) {
     int v[4] = {own_tokens > 0, own_tokens, own_cost, own_tokens > 0 ? my_ctx : 0}, ex[4], tot[4];
-    block_scan4(v, ex, tot, sw);
+    block_scan4<kPrePlanThreads>(v, ex, tot, sw);
     if (own_tokens > 0) {
       mine.tok0 = carry[1] + ex[1];
       mine.cost0 = carry[2] + ex[2];
@@ -343,13 +354,14 @@ constexpr int plan_smem_seqs() { return kPre ? kPlanSmemSeqs / 2 : kPlanSmemSeqs
 // kPre: with shared prefixes (a.NG > 0).
 template <bool kPre>
 __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
-  static_assert(kCostBins == kPlanThreads, "one histogram bin per planner thread");
+  constexpr int NT = plan_threads<kPre>();  // threads
+  constexpr int kBins = kCostBins / NT;      // histogram bins per thread
   constexpr int kSeqs = plan_smem_seqs<kPre>();
   __shared__ int sw[32][4];
   __shared__ int32_t s_dec_prefix[kSeqs + 1], s_pf_prefix[kSeqs + 1];
   __shared__ int32_t s_pf_seq[kSeqs];
   __shared__ int2 s_pf_lens[kSeqs];  // (q_len, prior context) of each chunk sequence
-  __shared__ int32_t s_groups[kPre ? 3 * kPlanSmemGroups : 1];
+  __shared__ int32_t s_groups[kPre ? 4 * kPlanSmemGroups : 1];
   const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, a.pack);
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + L.header);
   int32_t* dec_seq = reinterpret_cast<int32_t*>(a.ws + L.dec_seq);
@@ -369,8 +381,13 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   int32_t* grp_cnt = few ? s_groups : reinterpret_cast<int32_t*>(a.ws + PL.cnt);
   int32_t* grp_first = few ? s_groups + kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.first);
   int32_t* grp_map = few ? s_groups + 2 * kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.map);
+  const int32_t* grp_lens = few ? s_groups + 3 * kPlanSmemGroups : a.prefix_lens;
   PreSeq mine = {0, 0, 0, -1, 0, -1, 0};
-  if constexpr (kPre) pre_cost = plan_prefixes(a, sw, grp_cnt, grp_first, grp_map, mine);
+  if constexpr (kPre) {
+    if (few)  // (the function's first barrier follows)
+      for (int g = tid; g < a.NG; g += NT) s_groups[3 * kPlanSmemGroups + g] = a.prefix_lens[g];
+    pre_cost = plan_prefixes(a, sw, grp_cnt, grp_first, grp_map, grp_lens, mine);
+  }
   // kPre: chunks that are groups of their own: (first token, tokens, first list entry, keys), cost0
   __shared__ int s_chunks;
   __shared__ int4 s_chunk[kPre ? kPreChunkItems : 1][2];
@@ -378,7 +395,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   bool bad = false;
   const int unit_rows = pf_unit_tiles(a.G) * kPrefillTileM;
   int carry[4] = {0, 0, 0, 0};
-  for (int base = 0; base < a.S; base += kPlanThreads) {
+  for (int base = 0; base < a.S; base += NT) {
     const int s = base + tid;
     int v[4] = {0, 0, 0, 0};
     int tok = 0, kv = 0;
@@ -405,7 +422,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
                  (grp = base == 0 ? mine.group : a.prefix_group[s]) >= 0 && grp_map[grp] >= 0) {
         // records of a.pack tokens: the tiles from the one holding the prefix's end to the one
         // holding the last key that the record's last token sees
-        keys = base == 0 ? mine.keys : a.prefix_lens[grp];
+        keys = grp_lens[grp];
         const int first = keys / kDecodeTileKeys * kDecodeTileKeys;
         for (int i = 0; i < q_len; i += a.pack) {
           v[0] += 1;
@@ -442,7 +459,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       }
     }
     int ex[4], tot[4];
-    block_scan4(v, ex, tot, sw);
+    block_scan4<NT>(v, ex, tot, sw);
     if (kPre && grp >= 0 && v[0]) {
       // The tokens' places in the group's list come in any order: a row's result does not depend
       // on the tile it is computed in.
@@ -503,7 +520,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     for (int x = 0; x < s_chunks; ++x) {
       const int4 ch = s_chunk[x][0];
       const int cost0 = s_chunk[x][1].x;
-      for (int t = tid; t < ch.y; t += kPlanThreads) {
+      for (int t = tid; t < ch.y; t += NT) {
         int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 2 * (size_t)(ch.z + t);
         entry[0] = make_int4(ch.x + t, -1, 0, 0);
         entry[1] = make_int4(t, ch.y, ch.w, cost0);
@@ -538,20 +555,25 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   if (n_units > 0) {
     __shared__ int hist[kCostBins];
     int32_t* pf_order = reinterpret_cast<int32_t*>(a.ws + L.pf_order);
-    hist[tid] = 0;
+    for (int i = 0; i < kBins; ++i) hist[kBins * tid + i] = 0;
     __syncthreads();
     const bool pf_local = n_pf <= kSeqs;
     const int32_t* ps = pf_local ? s_pf_seq : pf_seq;
     const int32_t* pp = pf_local ? s_pf_prefix : pf_prefix;
     const int2* lens = pf_local ? s_pf_lens : nullptr;
-    for (int g = tid; g < n_units; g += kPlanThreads)
+    for (int g = tid; g < n_units; g += NT)
       atomicAdd(&hist[pf_unit_bin(a, ps, pp, lens, n_pf, g)], 1);
     __syncthreads();
-    int v[4] = {hist[tid], 0, 0, 0}, ex[4], tot[4];
-    block_scan4(v, ex, tot, sw);
-    hist[tid] = ex[0];
+    int v[4] = {0, 0, 0, 0}, ex[4], tot[4];
+    for (int i = 0; i < kBins; ++i) v[0] += hist[kBins * tid + i];
+    block_scan4<NT>(v, ex, tot, sw);
+    for (int i = 0; i < kBins; ++i) {
+      const int n = hist[kBins * tid + i];
+      hist[kBins * tid + i] = ex[0];
+      ex[0] += n;
+    }
     __syncthreads();
-    for (int g = tid; g < n_units; g += kPlanThreads)
+    for (int g = tid; g < n_units; g += NT)
       pf_order[atomicAdd(&hist[pf_unit_bin(a, ps, pp, lens, n_pf, g)], 1)] = g;
   }
   // First decode sequence of each decode CTA: CTA c owns tiles [c*n/N, (c+1)*n/N), with N
@@ -559,7 +581,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   const int n_dec = carry[0];
   const long long ntiles = carry[1];
   __shared__ int s_N;
-  __shared__ float s_red[2][kPlanThreads / 32];
+  __shared__ float s_red[2][NT / 32];
   // fixed-order reduction, so that the CTA count (and with it the rounding of the split-KV
   // merge) is the same on every call with the same lengths
   for (int o = 16; o > 0; o >>= 1) {
@@ -573,9 +595,18 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   __syncthreads();
   if (tid < 32) {
     float keys = 0.f, pairs = 0.f;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-      keys += s_red[0][w];
-      pairs += s_red[1][w];
+    if constexpr (kPre) {
+      keys = tid < NT / 32 ? s_red[0][tid] : 0.f;
+      pairs = tid < NT / 32 ? s_red[1][tid] : 0.f;
+      for (int o = 16; o > 0; o >>= 1) {
+        keys += __shfl_xor_sync(0xffffffffu, keys, o);
+        pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
+      }
+    } else {
+      for (int w = 0; w < NT / 32; ++w) {
+        keys += s_red[0][w];
+        pairs += s_red[1][w];
+      }
     }
     int n = (int)(ntiles < a.decode_ctas ? (ntiles > 0 ? ntiles : 1) : a.decode_ctas);
     if (kPre && pre_cost > 0) {
@@ -604,11 +635,11 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   int32_t* merge_cnt = reinterpret_cast<int32_t*>(a.ws + L.merge_cnt);
   // (one per decode sequence, KV head and group of 8 query heads: two groups when G > 8)
   const int head_groups = a.G > 8 ? 2 : 1;
-  for (int i = tid; i < n_dec * a.Hkv * head_groups; i += kPlanThreads) merge_cnt[i] = 0;
+  for (int i = tid; i < n_dec * a.Hkv * head_groups; i += NT) merge_cnt[i] = 0;
   // Indexed by the grid's decode CTA, so that a CTA reads its first sequence in the same round
   // trip as the plan header.
   const int32_t* dp = n_dec <= kSeqs ? s_dec_prefix : dec_prefix;
-  for (int bx = tid; bx < a.decode_ctas; bx += kPlanThreads) {
+  for (int bx = tid; bx < a.decode_ctas; bx += NT) {
     const int c = decode_cta_index(bx, N, a.decode_ctas);
     int lo = -1;
     if (c >= 0 && c < N) {

@@ -21,13 +21,13 @@
 
 namespace cb {
 
-__global__ void __launch_bounds__(kPlanThreads, 1) prefix_plan_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kPrePlanThreads, 1) prefix_plan_kernel(AttnArgs a) {
   allow_dependent_launch();
   plan_cta<true>(a);
 }
 
 cudaError_t launch_prefix_plan(const AttnArgs& a, cudaStream_t stream) {
-  prefix_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  prefix_plan_kernel<<<1, kPrePlanThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

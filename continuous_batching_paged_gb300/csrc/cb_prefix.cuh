@@ -137,21 +137,29 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
           return blk * a.bs + pos % a.bs;
         };
         int blk_next = entry(lane);
-        wait(bar(SM::bQEmpty), (k & 1) ^ 1);
-        if (!ok) break;
-        if (lane == 0)
-          mbar_arrive_expect_tx(bar(SM::bQFull),
-                                (uint32_t)((s.ntok[0] + s.ntok[1]) * a.G * SM::kHalves * 128));
-        __syncwarp();
+        // The part's query rows, behind its first K tile: their addresses are a load away, K's are here.
+        int q_tok[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          for (int i = lane; i < s.ntok[t]; i += 32) {
-            const int tok = list[s.tok0 + t * pre_tile_tokens(a.G) + i].token;
+          q_tok[t] = lane < s.ntok[t] ? list[s.tok0 + t * pre_tile_tokens(a.G) + lane].token : 0;
+        auto load_q = [&]() {
+          wait(bar(SM::bQEmpty), (k & 1) ^ 1);
+          if (!ok) return;
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar(SM::bQFull),
+                                  (uint32_t)((s.ntok[0] + s.ntok[1]) * a.G * SM::kHalves * 128));
+          __syncwarp();
 #pragma unroll
-            for (int half = 0; half < SM::kHalves; ++half)
-              tma_load_3d(sbase + t * SM::kTile + half * SM::kHalf + i * a.G * 128, qmap,
-                          bar(SM::bQFull), half * 64, s.kvh * a.G, tok);
-          }
+          for (int t = 0; t < 2; ++t)
+            for (int i = lane; i < s.ntok[t]; i += 32) {
+              const int tok =
+                  i < 32 ? q_tok[t] : list[s.tok0 + t * pre_tile_tokens(a.G) + i].token;
+#pragma unroll
+              for (int half = 0; half < SM::kHalves; ++half)
+                tma_load_3d(sbase + t * SM::kTile + half * SM::kHalf + i * a.G * 128, qmap,
+                            bar(SM::bQFull), half * 64, s.kvh * a.G, tok);
+            }
+        };
         // K or V tile into the next slot: the runs whose pool rows the lanes of `lanes` hold
         auto load = [&](int token, uint32_t lanes, const CUtensorMap* map) {
           const uint32_t slot = g % NS, full = bar(SM::bFull + slot);
@@ -181,9 +189,10 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
             }
             if (i < n) {
               load(t_cur, tile_lanes << (in_batch * nsb), kmap);
-              if (s.two) load(t_cur, tile_lanes << (in_batch * nsb), vmap);
+              if (i == 0 && ok) load_q();
+              if (s.two && ok) load(t_cur, tile_lanes << (in_batch * nsb), vmap);
             }
-            if (!s.two && i > 0) {
+            if (!s.two && i > 0 && ok) {
               if (in_batch == 0)
                 load(t_prev, tile_lanes << ((per_batch - 1) * nsb), vmap);
               else
@@ -222,8 +231,9 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
           };
           for (int i = 0; i <= n && ok; ++i) {
             if (i < n) load_runs(i, kmap);
-            if (s.two && i < n) load_runs(i, vmap);
-            if (!s.two && i > 0) load_runs(i - 1, vmap);
+            if (i == 0 && ok) load_q();
+            if (s.two && i < n && ok) load_runs(i, vmap);
+            if (!s.two && i > 0 && ok) load_runs(i - 1, vmap);
           }
         }
       }

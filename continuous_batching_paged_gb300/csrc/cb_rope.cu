@@ -35,28 +35,36 @@ cudaError_t launch_rope_append(RopeArgs r, int sm_count, cudaStream_t stream) {
 }
 
 // CTA 0 plans the attention pass (it reads only the metadata); CTAs 1.. rotate and append.
-constexpr int kRopePlanUnroll = 2;  // fits the 64 registers of a 1024-thread CTA
 template <bool kPre>
-__global__ void __launch_bounds__(kPlanThreads, 1) rope_plan_kernel(const RopeArgs r, AttnArgs a) {
+__global__ void __launch_bounds__(plan_threads<kPre>(), 1) rope_plan_kernel(const RopeArgs r,
+                                                                            AttnArgs a) {
   allow_dependent_launch();
   if (blockIdx.x == 0) {
     plan_cta<kPre>(a);
   } else {
-    constexpr int kWarps = kPlanThreads / 32;
-    rope_tokens<kRopePlanUnroll>(r, (long long)(blockIdx.x - 1) * kWarps + (threadIdx.x >> 5),
-                                 (long long)(gridDim.x - 1) * kWarps);
+    constexpr int kWarps = plan_threads<kPre>() / 32;
+    constexpr int kUnroll = kPre ? kRopeUnroll : 2;  // (2 fits the 64 registers of 1024 threads)
+    rope_tokens<kUnroll>(r, (long long)(blockIdx.x - 1) * kWarps + (threadIdx.x >> 5),
+                         (long long)(gridDim.x - 1) * kWarps);
   }
 }
 
-cudaError_t launch_rope_plan(RopeArgs r, const AttnArgs& a, int sm_count, cudaStream_t stream) {
-  constexpr int kWarps = kPlanThreads / 32;
-  r.parts = rope_parts(r, sm_count);
+template <bool kPre>
+static void launch_rope_plan_t(const RopeArgs& r, const AttnArgs& a, int sm_count,
+                               cudaStream_t stream) {
+  constexpr int kWarps = plan_threads<kPre>() / 32;
   long long blocks = ((long long)r.ap.T * r.parts + kWarps - 1) / kWarps;
-  if (blocks > (long long)sm_count * 16) blocks = (long long)sm_count * 16;
+  const long long most = (long long)sm_count * 512 / kWarps;
+  if (blocks > most) blocks = most;
+  rope_plan_kernel<kPre><<<(unsigned)(1 + blocks), kWarps * 32, 0, stream>>>(r, a);
+}
+
+cudaError_t launch_rope_plan(RopeArgs r, const AttnArgs& a, int sm_count, cudaStream_t stream) {
+  r.parts = rope_parts(r, sm_count);
   if (a.NG > 0)
-    rope_plan_kernel<true><<<(unsigned)(1 + blocks), kPlanThreads, 0, stream>>>(r, a);
+    launch_rope_plan_t<true>(r, a, sm_count, stream);
   else
-    rope_plan_kernel<false><<<(unsigned)(1 + blocks), kPlanThreads, 0, stream>>>(r, a);
+    launch_rope_plan_t<false>(r, a, sm_count, stream);
   return cudaGetLastError();
 }
 
