@@ -1,8 +1,9 @@
 """Ragged paged attention and paged KV-append for GB300 (sm_103a).
 
-Thin ctypes binding of libcb (include/cb.h).  It only marshals arguments: every step of the
-path runs in the library's CUDA kernels, and PyTorch supplies device memory and streams.  There
-is no fallback: if the library is missing or cannot be built, every call raises.
+Thin binding of libcb (include/cb.h), by ctypes and, for the calls that a serving loop makes per layer
+and step, a C++ extension.  It only marshals arguments: every step of the path runs in the library's
+CUDA kernels, and PyTorch supplies device memory and streams.  There is no fallback: if the library
+is missing or cannot be built, every call raises.
 
     import continuous_batching_paged_gb300 as cb
     cb.kv_append(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size)
@@ -79,6 +80,7 @@ class CbError(RuntimeError):
 
 _lock = threading.Lock()
 _lib: ctypes.CDLL | None = None
+_ext = None  # the C++ extension of the per-step calls
 
 _P = ctypes.c_void_p
 _I32P = ctypes.POINTER(ctypes.c_int32)
@@ -284,9 +286,19 @@ def kv_append(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens
     _check(st, "cb_kv_append")
 
 
-# The calls below are made once per layer and step, often on a few tokens, where the host time of
-# their checks is most of their cost: each makes all its checks in one expression, and asks the
-# _explain functions for the message only when that fails.
+# The calls below are made once per layer and step, often on a few tokens, where their host time is
+# most of their cost.  They go through the package's C++ extension (csrc/cb_torch.cpp), which checks
+# the tensors; the _explain functions find the message for what it refused.
+
+def _native():
+    """The extension (built with the library, which it links to)."""
+    global _ext
+    if _ext is None:
+        library()
+        from . import _cb_torch
+        _ext = _cb_torch
+    return _ext
+
 
 def _rows_ok(T, H, D, strides) -> bool:
     """Whether a [T, H, D] tensor of these strides has contiguous token rows (as a view of a wider
@@ -331,52 +343,6 @@ def _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, 
     dev = torch.cuda.current_device()
     for t in (q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, cos_sin):
         _require(t is None or t.get_device() == dev, "every tensor must be on the current CUDA device")
-    raise ValueError("inconsistent arguments")
-
-
-def _meta_ok(dev, i32, block_table, cu_seqlens_q, kv_lens) -> bool:
-    return (block_table.dtype is i32 and cu_seqlens_q.dtype is i32 and kv_lens.dtype is i32
-            and block_table.get_device() == dev and cu_seqlens_q.get_device() == dev
-            and kv_lens.get_device() == dev and block_table.is_contiguous()
-            and cu_seqlens_q.is_contiguous() and kv_lens.is_contiguous()
-            and block_table.dim() == 2 and cu_seqlens_q.numel() == kv_lens.numel() + 1
-            and block_table.shape[0] == kv_lens.numel())
-
-
-def _rope_inputs(torch, q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
-                 block_size, cos_sin, interleaved):
-    """cb_dims and cb_rope of a rotary append, its inputs checked."""
-    bf16, dev = torch.bfloat16, k_new.get_device()
-    ks, vs, shape, pool = k_new.stride(), v_new.stride(), k_new.shape, k_pages.shape
-    ok = (dev >= 0 and len(shape) == 3 and len(pool) == 4 and len(cos_sin.shape) == 2
-          and dev == torch._C._cuda_getDevice())
-    if ok:
-        T, Hkv, D = shape
-        Hq, qs = Hkv, None
-        ok = (k_new.dtype is bf16 and v_new.dtype is bf16 and k_pages.dtype is bf16
-              and v_pages.dtype is bf16 and cos_sin.dtype is torch.float32
-              and v_new.get_device() == dev and k_pages.get_device() == dev
-              and v_pages.get_device() == dev and cos_sin.get_device() == dev
-              and k_pages.is_contiguous() and v_pages.is_contiguous() and cos_sin.is_contiguous()
-              and v_new.shape == shape and v_pages.shape == pool
-              and pool[1] == block_size and pool[2] == Hkv and pool[3] == D
-              and _rows_ok(T, Hkv, D, ks) and _rows_ok(T, Hkv, D, vs)
-              and _meta_ok(dev, torch.int32, block_table, cu_seqlens_q, kv_lens))
-        if ok and q is not None:
-            qs = q.stride()
-            ok = q.dtype is bf16 and q.get_device() == dev and len(qs) == 3
-            if ok:
-                Tq, Hq, Dq = q.shape
-                ok = Tq == T and Dq == D and _rows_ok(T, Hq, D, qs)
-    if not ok:
-        _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
-                      block_size, cos_sin)
-    many = T > 1  # (one token's row is contiguous whatever its stride says)
-    rows, rot = cos_sin.shape
-    return (CbDims(kv_lens.numel(), T, Hq, Hkv, D, pool[0], block_table.shape[1]),
-            CbRope(cos_sin.data_ptr(), rows, rot, 1 if interleaved else 0, 0,
-                   qs[0] if many and qs is not None else 0, ks[0] if many else 0,
-                   vs[0] if many else 0))
 
 
 def _on_stream(stream):
@@ -385,14 +351,6 @@ def _on_stream(stream):
     import torch
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
                              else torch.cuda.ExternalStream(_stream(stream)))
-
-
-def _new(shape, dtype, like, stream):
-    """A tensor beside `like`, its memory reused only after the work queued on `stream`."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    with _on_stream(stream):
-        return like.new_empty(shape, dtype=dtype)
 
 
 def _check_output(t, name, shape, dev) -> None:
@@ -415,24 +373,22 @@ def rope_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv
         ang = pos[:, None] * freq
         cos_sin = torch.cat((ang.cos(), ang.sin()), 1).float()
     """
-    import torch
-    dims, rope = _rope_inputs(torch, q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q,
-                              kv_lens, block_size, cos_sin, interleaved)
-    if q is not None:
-        if q_out is None:
-            q_out = q.new_empty(q.shape) if stream is None else _new(q.shape, q.dtype, q, stream)
-        else:
+    if stream is not None:
+        with _on_stream(stream):
+            return rope_append(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                               block_size, cos_sin, interleaved, q_out)
+    r = (_ext or _native()).rope_append(k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                                        block_size, q, k_new, v_new, cos_sin, interleaved, q_out)
+    if r is NotImplemented:
+        _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                      block_size, cos_sin)
+        _require(q is not None or q_out is None, "q_out without q")
+        if q_out is not None:
             _check_output(q_out, "q_out", tuple(q.shape), q.get_device())
-    else:
-        _require(q_out is None, "q_out without q")
-    st = (_lib or library()).cb_rope_append(
-        None if q is None else q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-        None if q is None else q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-        block_table.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_size,
-        ctypes.byref(rope), ctypes.byref(dims), _stream(stream))
-    if st:
-        _check(st, "cb_rope_append")
-    return q_out
+        raise ValueError("rope_append: bad argument")
+    if r.__class__ is int:
+        _check(r, "cb_rope_append")
+    return r
 
 
 def workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, num_tokens) -> int:
@@ -525,48 +481,34 @@ def prefix_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, num_tok
     return int(library().cb_prefix_workspace_size(ctypes.byref(dims), int(num_groups)))
 
 
-def _step_tensors(torch, q, dims, prefix_group, prefix_lens, out, lse, workspace, decode_ctas,
-                  serial, window, phase_events, stream):
-    """What an attention call with shared prefixes needs beside its inputs: cb_prefix (or None),
-    out, lse, workspace and cb_options, checked or made."""
-    shape, dev = q.shape, q.get_device()
-    prefix, NG = None, 0
+def _explain_tail(q, num_seqs, prefix_group, prefix_lens, out, lse, workspace, phase_events) -> None:
+    """Raise the error of an attention call's other arguments (q: the tensor that it attends with)."""
+    import torch
+    dev = q.get_device()
     if prefix_group is not None or prefix_lens is not None:
         _require(prefix_group is not None and prefix_lens is not None,
                  "prefix_group and prefix_lens go together")
-        i32 = torch.int32
-        _require(prefix_group.dtype is i32 and prefix_lens.dtype is i32
-                 and prefix_group.get_device() == dev and prefix_lens.get_device() == dev
-                 and prefix_group.is_contiguous() and prefix_lens.is_contiguous(),
-                 "prefix_group and prefix_lens must be contiguous int32 CUDA tensors on q's device")
-        _require(prefix_group.numel() == dims.num_seqs, "prefix_group must have num_seqs entries")
-        NG = prefix_lens.numel()
-        prefix = ctypes.byref(CbPrefix(prefix_group.data_ptr(), prefix_lens.data_ptr(), NG))
-    if out is None:
-        out = _new(shape, q.dtype, q, stream)
-    else:
-        _check_output(out, "out", tuple(shape), dev)
-    if lse is True:
-        lse = _new(shape[:2], torch.float32, q, stream)
-    elif lse is False:
-        lse = None
-    elif lse is not None:
-        _require(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == shape[:2]
-                 and lse.get_device() == dev, "lse must be a contiguous fp32 [T, Hq] tensor")
-    if workspace is None:
-        need = (_lib or library()).cb_prefix_workspace_size(ctypes.byref(dims), NG)
-        workspace = _new(max(need, 256), torch.uint8, q, stream)
-    else:
-        _require(workspace.dtype is torch.uint8 and workspace.is_contiguous()
+        for name, t in (("prefix_group", prefix_group), ("prefix_lens", prefix_lens)):
+            _check_ids(name, t)
+            _require(t.get_device() == dev, f"{name} must be on q's device")
+        _require(prefix_group.numel() == num_seqs, "prefix_group must have num_seqs entries")
+    if out is not None:
+        _check_output(out, "out", tuple(q.shape), dev)
+    if lse is not None and not isinstance(lse, bool):
+        _require(lse.dtype == torch.float32 and lse.is_contiguous() and lse.get_device() == dev
+                 and lse.shape == q.shape[:2], "lse must be a contiguous fp32 [T, Hq] tensor")
+    if workspace is not None:
+        _require(workspace.dtype == torch.uint8 and workspace.is_contiguous()
                  and workspace.get_device() == dev, "workspace must be uint8")
-    opts = CbOptions(decode_ctas, OPT_SERIAL if serial else 0)
-    opts.window = window
-    if phase_events is not None:
-        _require(len(phase_events) == NUM_PHASE_EVENTS, f"need {NUM_PHASE_EVENTS} phase events")
-        handles = (ctypes.c_void_p * NUM_PHASE_EVENTS)(*[int(e.cuda_event) for e in phase_events])
-        _require(all(handles), "phase events must have been recorded once (created) before use")
-        opts.phase_events = ctypes.cast(handles, ctypes.POINTER(ctypes.c_void_p))
-    return prefix, out, lse, workspace, opts
+
+
+def _event_handles(phase_events):
+    if phase_events is None:
+        return None
+    _require(len(phase_events) == NUM_PHASE_EVENTS, f"need {NUM_PHASE_EVENTS} phase events")
+    handles = tuple(int(e.cuda_event) for e in phase_events)
+    _require(all(handles), "phase events must have been recorded once (created) before use")
+    return handles
 
 
 def shared_prefix_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
@@ -581,30 +523,23 @@ def shared_prefix_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_l
     or blocks with the same content), at most each member's prior context.  Results are
     ragged_paged_attention's within rounding; the other arguments are its.
     """
-    import torch
-    bf16, dev, pool, shape = torch.bfloat16, q.get_device(), k_pages.shape, q.shape
-    if not (dev >= 0 and len(shape) == 3 and len(pool) == 4 and q.dtype is bf16
-            and dev == torch._C._cuda_getDevice() and q.is_contiguous()
-            and k_pages.dtype is bf16 and v_pages.dtype is bf16 and k_pages.get_device() == dev
-            and v_pages.get_device() == dev and k_pages.is_contiguous() and v_pages.is_contiguous()
-            and v_pages.shape == pool and pool[1] == block_size and pool[3] == shape[2]
-            and _meta_ok(dev, torch.int32, block_table, cu_seqlens_q, kv_lens)):
+    if stream is not None:
+        with _on_stream(stream):
+            return shared_prefix_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                                           block_size, scale, prefix_group, prefix_lens, out, lse,
+                                           workspace, decode_ctas, phase_events, serial)
+    r = (_ext or _native()).shared_prefix_attention(
+        k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, q, scale, prefix_group,
+        prefix_lens, out, lse, workspace, decode_ctas, serial, 0, _event_handles(phase_events))
+    if r is NotImplemented:
         _explain_step(q, None, None, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
                       None)
-    _require(prefix_group is not None, "prefix_group must be given")
-    dims = CbDims(kv_lens.numel(), *shape[:2], pool[2], pool[3], pool[0], block_table.shape[1])
-    want_lse = lse is not None and lse is not False
-    prefix, out, lse, workspace, opts = _step_tensors(
-        torch, q, dims, prefix_group, prefix_lens, out, lse, workspace, decode_ctas, serial, 0,
-        phase_events, stream)
-    st = (_lib or library()).cb_shared_prefix_attention(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-        cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_size, scale, prefix, out.data_ptr(),
-        _ptr(lse), workspace.data_ptr(), workspace.numel(), ctypes.byref(dims), ctypes.byref(opts),
-        _stream(stream))
-    if st:
-        _check(st, "cb_shared_prefix_attention")
-    return (out, lse) if want_lse else out
+        _require(prefix_group is not None, "prefix_group must be given")
+        _explain_tail(q, kv_lens.numel(), prefix_group, prefix_lens, out, lse, workspace, phase_events)
+        raise ValueError("shared_prefix_attention: bad argument")
+    if r.__class__ is int:
+        _check(r, "cb_shared_prefix_attention")
+    return r
 
 
 def rope_append_attention(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
@@ -615,27 +550,27 @@ def rope_append_attention(q, k_new, v_new, k_pages, v_pages, block_table, cu_seq
     """One layer's attention step (cb_rope_append_attention): rope_append, then
     shared_prefix_attention on the rotated queries (ragged_paged_attention without groups), same
     results, in two launches.  q_out: where the rotated queries go (default: a temporary)."""
-    import torch
-    _require(q is not None, "q must be given")
-    dims, rope = _rope_inputs(torch, q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q,
-                              kv_lens, block_size, cos_sin, interleaved)
-    if q_out is None:
-        q_out = _new(q.shape, q.dtype, q, stream)
-    else:
-        _check_output(q_out, "q_out", tuple(q.shape), q.get_device())
-    want_lse = lse is not None and lse is not False
-    prefix, out, lse, workspace, opts = _step_tensors(
-        torch, q_out, dims, prefix_group, prefix_lens, out, lse, workspace, decode_ctas, serial,
-        window, phase_events, stream)
-    st = (_lib or library()).cb_rope_append_attention(
-        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
-        v_pages.data_ptr(), block_table.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
-        block_size, scale, ctypes.byref(rope), prefix, out.data_ptr(), _ptr(lse),
-        workspace.data_ptr(), workspace.numel(), ctypes.byref(dims), ctypes.byref(opts),
-        _stream(stream))
-    if st:
-        _check(st, "cb_rope_append_attention")
-    return (out, lse) if want_lse else out
+    if stream is not None:
+        with _on_stream(stream):
+            return rope_append_attention(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q,
+                                         kv_lens, block_size, scale, cos_sin, interleaved,
+                                         prefix_group, prefix_lens, q_out, out, lse, workspace,
+                                         decode_ctas, phase_events, serial, window)
+    r = (_ext or _native()).rope_append_attention(
+        k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, q, k_new, v_new, cos_sin,
+        interleaved, q_out, scale, prefix_group, prefix_lens, out, lse, workspace, decode_ctas, serial,
+        window, _event_handles(phase_events))
+    if r is NotImplemented:
+        _require(q is not None, "q must be given")
+        _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                      block_size, cos_sin)
+        if q_out is not None:
+            _check_output(q_out, "q_out", tuple(q.shape), q.get_device())
+        _explain_tail(q, kv_lens.numel(), prefix_group, prefix_lens, out, lse, workspace, phase_events)
+        raise ValueError("rope_append_attention: bad argument")
+    if r.__class__ is int:
+        _check(r, "cb_rope_append_attention")
+    return r
 
 
 def get_device_error(stream=None) -> int:
