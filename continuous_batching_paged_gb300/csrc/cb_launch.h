@@ -7,6 +7,25 @@
 
 namespace cb {
 
+// Launch `kernel` as a programmatic dependent of the launch before it on the stream: it may start
+// before that one ends (once all of its CTAs have allowed that, or ended), and waits for it with
+// griddepcontrol.wait before it touches memory, so its launch latency overlaps.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), unsigned blocks, unsigned threads,
+                             size_t smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct AppendArgs {
   const void* k_new;
   const void* v_new;

@@ -292,10 +292,10 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
 // Prefix CTAs where `free` SMs are left to them and to `items` chunk items (up to a third of them for
 // those, an SM per item: an item is mostly latency): as many for each KV head (PreGroup), no more
 // than the work is worth.
-__device__ __forceinline__ int pre_cta_count(int free, int items, int cost, int Hkv) {
+__device__ __forceinline__ int pre_cta_count(int free, int items, int cost, int Hkv, int min_steps) {
   free -= items < free / 3 ? items : free / 3;
   int np = free < kMaxPreCtas ? free : kMaxPreCtas;
-  const long long most = (long long)cost * Hkv / (kPreMinSteps * kPreCost1);
+  const long long most = (long long)cost * Hkv / (min_steps * kPreCost1);
   if (np > most) np = (int)most;
   if (np > Hkv) np -= np % Hkv;
   return np < 1 ? 1 : np;
@@ -312,7 +312,7 @@ __device__ __forceinline__ int pre_cta_count(int free, int items, int cost, int 
 // the 15 batches, and within 12 % on the others.
 __device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes, float pre_bytes,
                                                    int cost, float chunk_flops, int items,
-                                                   long long tiles, int records) {
+                                                   long long tiles, int records, int min_steps) {
   const int lane = threadIdx.x & 31;
   const int hg = pre_head_groups(a.Hkv, a.G), sms = a.chunk_ctas;
   const int cap = (int)(tiles < a.decode_ctas ? tiles : a.decode_ctas);
@@ -325,7 +325,7 @@ __device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_
     const int free = sms - n * hg;
     const float x = __fdividef(x1, (float)n), d = 3.f + __fsqrt_rn(x * x + y * y);
     const float p = 12.f + __fdividef(0.8f * (float)cost * (float)a.Hkv,
-                                      (float)pre_cta_count(free, items, cost, a.Hkv)) +
+                                      (float)pre_cta_count(free, items, cost, a.Hkv, min_steps)) +
                     __fdividef(chunk_flops * (1.f / 6.4e6f), (float)free);
     const float t = fmaxf(d, p) + 0.1f * fminf(d, p) + 0.015f * (float)n;
     if (t < best) {
@@ -612,12 +612,15 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     if (kPre && pre_cost > 0) {
       const float row = (float)(a.Hkv * a.D * 4);  // bytes of a key and its value
       const int items = n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq);
+      const int min_steps = pre_min_steps((long long)hdr->pre_tokens * a.Hq);
       if (a.decode_auto)
         n = choose_prefix_split(a, keys * row, (float)hdr->pre_keys * row, pre_cost,
-                                pairs * (float)(4 * a.D * a.Hq), items, ntiles, n_dec);
+                                pairs * (float)(4 * a.D * a.Hq), items, ntiles, n_dec, min_steps);
       // the decode CTAs without work; where a given number leaves none, an eighth of the chunk CTAs
       const int idle = pre_idle_count(pre_head_groups(a.Hkv, a.G), n, a.decode_ctas);
-      if (tid == 0) hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, items, pre_cost, a.Hkv);
+      if (tid == 0)
+        hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, items, pre_cost, a.Hkv,
+                                      min_steps);
     } else if (a.decode_auto) {
       n = choose_decode_ctas(keys * (float)(a.Hkv * a.D * 4), pairs * (float)(4 * a.D * a.Hq),
                              n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq), a.decode_ctas,

@@ -23,12 +23,12 @@ namespace cb {
 
 __global__ void __launch_bounds__(kPrePlanThreads, 1) prefix_plan_kernel(AttnArgs a) {
   allow_dependent_launch();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (the workspace may still be in use)
   plan_cta<true>(a);
 }
 
 cudaError_t launch_prefix_plan(const AttnArgs& a, cudaStream_t stream) {
-  prefix_plan_kernel<<<1, kPrePlanThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(prefix_plan_kernel, 1, kPrePlanThreads, 0, stream, a);
 }
 
 template <int D, int QS>
@@ -57,19 +57,8 @@ static cudaError_t launch_instance(const AttnArgs& a, const AttnMaps& m, const C
     if (e != cudaSuccess) return e;
     configured_ctx = ctx;
   }
-  // may start before the planner ends, and waits for it (griddepcontrol.wait)
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.decode_grid + a.prefill_ctas);
-  cfg.blockDim = dim3(kAttnThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefix_attention_kernel<D, QS>, a, m.q, q_tok, m.k_dec, m.v_dec,
-                            m.k_chunk, m.v_chunk);
+  return launch_dependent(prefix_attention_kernel<D, QS>, a.decode_grid + a.prefill_ctas, kAttnThreads,
+                          kSmem, stream, a, m.q, q_tok, m.k_dec, m.v_dec, m.k_chunk, m.v_chunk);
 }
 
 // One warp per (query token, HP query heads of one KV head) of the shared prefixes:
@@ -83,6 +72,7 @@ constexpr int kMergeThreads = 256;
 template <int D, int HP>
 __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnArgs a) {
   constexpr int PER = D / 32, kC = 8 / HP;  // columns per lane, parts' rows of O in flight
+  allow_dependent_launch();
   const int lane = threadIdx.x & 31;
   const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, a.pack);
   const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack);
@@ -245,20 +235,9 @@ cudaError_t launch_prefix_merge(const AttnArgs& a, int sm_count, cudaStream_t st
   const long long warps = (long long)a.R * a.Hkv * (four ? (a.G + 3) / 4 : a.G);
   long long blocks = (warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
   if (blocks > (long long)sm_count * 8) blocks = (long long)sm_count * 8;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (a.D == 128)
-    return four ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<128, 4>, a)
-                : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<128, 1>, a);
-  return four ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<64, 4>, a)
-              : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<64, 1>, a);
+  auto* kernel = a.D == 128 ? (four ? prefix_merge_kernel<128, 4> : prefix_merge_kernel<128, 1>)
+                            : (four ? prefix_merge_kernel<64, 4> : prefix_merge_kernel<64, 1>);
+  return launch_dependent(kernel, (unsigned)blocks, kMergeThreads, 0, stream, a);
 }
 
 cudaError_t launch_prefix_attention(const AttnArgs& a, const AttnMaps& m, const CUtensorMap& q_tok,

@@ -12,6 +12,10 @@ constexpr int kRopeThreads = 128;
 constexpr int kRopeUnroll = 4;
 
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs r) {
+  // Launched as a programmatic dependent of whatever precedes it on the stream, and lets such a
+  // launch behind it start early: the launch latency of calls in a row overlaps.
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   check_cu_seqlens(r.ap);
   rope_tokens<kRopeUnroll>(r, (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5),
                            (long long)gridDim.x * (kRopeThreads / 32));
@@ -34,8 +38,7 @@ cudaError_t launch_rope_append(RopeArgs r, int sm_count, cudaStream_t stream) {
   const int warps = kRopeThreads / 32;
   long long blocks = ((long long)r.ap.T * r.parts + warps - 1) / warps;
   if (blocks > (long long)sm_count * 64) blocks = (long long)sm_count * 64;
-  rope_append_kernel<<<(unsigned)blocks, kRopeThreads, 0, stream>>>(r);
-  return cudaGetLastError();
+  return launch_dependent(rope_append_kernel, (unsigned)blocks, kRopeThreads, 0, stream, r);
 }
 
 // CTA 0 plans the attention pass (it reads only the metadata); CTAs 1.. rotate and append.
@@ -43,6 +46,7 @@ template <bool kPre>
 __global__ void __launch_bounds__(plan_threads<kPre>(), 1) rope_plan_kernel(const RopeArgs r,
                                                                             AttnArgs a) {
   allow_dependent_launch();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (blockIdx.x == 0) {
     plan_cta<kPre>(a);
   } else {
@@ -54,22 +58,19 @@ __global__ void __launch_bounds__(plan_threads<kPre>(), 1) rope_plan_kernel(cons
 }
 
 template <bool kPre>
-static void launch_rope_plan_t(const RopeArgs& r, const AttnArgs& a, int sm_count,
-                               cudaStream_t stream) {
+static cudaError_t launch_rope_plan_t(const RopeArgs& r, const AttnArgs& a, int sm_count,
+                                      cudaStream_t stream) {
   constexpr int kWarps = plan_threads<kPre>() / 32;
   long long blocks = ((long long)r.ap.T * r.parts + kWarps - 1) / kWarps;
   const long long most = (long long)sm_count * 512 / kWarps;
   if (blocks > most) blocks = most;
-  rope_plan_kernel<kPre><<<(unsigned)(1 + blocks), kWarps * 32, 0, stream>>>(r, a);
+  return launch_dependent(rope_plan_kernel<kPre>, (unsigned)(1 + blocks), kWarps * 32, 0, stream, r, a);
 }
 
 cudaError_t launch_rope_plan(RopeArgs r, const AttnArgs& a, int sm_count, cudaStream_t stream) {
   r.parts = rope_parts(r, sm_count);
-  if (a.NG > 0)
-    launch_rope_plan_t<true>(r, a, sm_count, stream);
-  else
-    launch_rope_plan_t<false>(r, a, sm_count, stream);
-  return cudaGetLastError();
+  return a.NG > 0 ? launch_rope_plan_t<true>(r, a, sm_count, stream)
+                  : launch_rope_plan_t<false>(r, a, sm_count, stream);
 }
 
 }  // namespace cb
