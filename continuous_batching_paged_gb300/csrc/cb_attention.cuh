@@ -59,7 +59,7 @@ __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorM
     if ((threadIdx.x & 31) == 0 && busy) atomicMax(&hdr->t_dec_end, global_ns());
     return;
   }
-  prefill_cta<D, kWin, kPre>(a, qmap, kmap_chunk, vmap_chunk, smem_raw);
+  prefill_cta<D, kWin>(a, qmap, kmap_chunk, vmap_chunk, smem_raw);
 }
 
 }  // namespace cb

@@ -98,13 +98,16 @@ __host__ __device__ inline WsLayout ws_layout(int S, int T, int Hq, int D, int p
 
 // ------------------------------------------------------------------------------------------
 // Shared prefixes (cb_prefix.cuh).  The query tokens of a group's members with at most kPreMaxQ each
-// go into the group's tiles of kPrefillTileM rows for the prefix, and for its own keys such a member
-// gets decode records of up to pre_pack tokens.  Longer ones (chunks) are computed alone: their
-// arithmetic is the same either way.  But where the batch's chunk pass has fewer than kPreChunkItems
-// work items, so that it would leave SMs idle, a chunk is a group of its own: the keys before it
-// (which all its rows see) are its prefix, cut to equal shares like any other, and the chunk pass
-// does only the chunk's own keys.
+// go into the group's tiles of kPrefillTileM rows for the prefix.  For its own keys a member gets one
+// decode record where the record holds all its tokens (pre_pack); one with more is a group of its
+// own for them, with a causal edge at their end: a K/V tile of 128 keys costs the tensor cores 0.9 us
+// for one KV head and all its rows, the decode pass 0.8 us per 16 keys, 8 KV heads and record, so
+// from two records on the tiles are cheaper.  So is a sequence outside the groups with 2 to kPreMaxQ
+// tokens.  Longer ones (chunks) run the chunk pass, which sharing saves nothing: but where its work
+// items are fewer than kPreChunkItems, so that it would leave SMs idle, a chunk after at least its
+// own length of keys is such a group too, cut to equal shares like the others.
 constexpr int kPreMaxQ = 8;
+constexpr int kPrePlanThreads = 256;  // of the planner (cb_plan.cuh); sequences it sees at once
 constexpr int kPreChunkItems = 152;
 // Tokens of one sequence that a decode warp's 8 columns hold with G query heads each.
 __host__ __device__ inline int pre_pack(int G) { return G <= 8 ? 8 / G : 1; }
@@ -119,7 +122,6 @@ __host__ __device__ inline int pre_min_steps(long long rows) { return rows <= 51
 __host__ __device__ inline int pre_tile_tokens(int G) { return kPrefillTileM / G; }
 // Most query tokens whose prefix is computed apart (and most decode records) of a batch: kPreMaxQ
 // per sequence, and what fewer than kPreChunkItems chunk items hold (an item is 2 x 128 rows).
-// Chunks, at least an item each, are fewer than kPreChunkItems, too.
 __host__ __device__ inline int pre_records(int S, int T, int Hq) {
   const long long most = (long long)S * kPreMaxQ + kPreChunkItems * 2 * kPrefillTileM / Hq;
   return most > T ? (T > S ? T : S) : (int)most;
@@ -139,25 +141,28 @@ struct PreGroup {
   int32_t cost0;    // where its first chain under a KV head starts, from the head's start
   int32_t n_tok;    // query tokens
   int32_t tok0;     // its first entry of the token list
-  int32_t keys;     // prefix length
+  int32_t first;    // its keys: first .. keys - 1
+  int32_t keys;
   int32_t seq;      // the sequence whose block table is read (the first member)
+  int32_t ctx;      // -1: every token sees all the keys; else token i sees those up to ctx + i
+  int32_t second;   // 1: its tokens have another chain, so its parts' rows are the second ones
 };
 
-// Entry of the groups' token list: a query token whose prefix is computed apart, with all that the
-// merge needs to find its parts, in two 16-byte loads.
+// Entry of the token list: a query token whose keys are (in part) computed apart, with all that the
+// merge needs to find its parts, in three 16-byte loads.
 struct PreToken {
   int32_t token;         // packed token
-  int32_t rec;           // 8 x its decode record + its place among the record's tokens; -1: a
-                         // chunk's token, whose own keys' part is in the list entry's row of own_o
+  int32_t rec;           // 8 x its decode record + its place among the record's tokens; -1: none
   int32_t tile0, tile1;  // that record's tiles among all decode tiles
-  int32_t at;            // its place among the group's tokens
-  int32_t n_tok, keys, cost0;  // of the group (PreGroup)
+  struct {               // its chains (the second: nt 0 if there is none)
+    int32_t at;          // its place among the group's tokens
+    int32_t n_tok, nt, cost0;  // of the group (nt: K/V tiles)
+  } chain[2];
 };
 
 // Sections of the workspace behind ws_layout's (all 256-byte aligned).
 struct PreLayout {
-  size_t rec, cnt, first, map, group, tok, pf, base_ml, base_o, own_ml, own_o, cut_ml, cut_o,
-      total;
+  size_t rec, cnt, first, map, group, tok, base_ml, base_o, cut_ml, cut_o, total;
 };
 __host__ __device__ inline PreLayout pre_layout(int R, int T, int Hq, int D, int NG, int pack) {
   PreLayout L;
@@ -168,17 +173,13 @@ __host__ __device__ inline PreLayout pre_layout(int R, int T, int Hq, int D, int
   L.cnt = off;     off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.first = off;   off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.map = off;     off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
-  L.group = off;   off = align_up(off + sizeof(PreGroup) * (size_t)(NG + kPreChunkItems + 1), 256);
+  L.group = off;   off = align_up(off + sizeof(PreGroup) * (size_t)(NG + kPrePlanThreads + 1), 256);
   L.tok = off;     off = align_up(off + sizeof(PreToken) * (size_t)(R + 1), 256);
-  // per chunk sequence: keys of the prefix computed apart and its first list entry, or zeros
-  L.pf = off;      off = align_up(off + sizeof(int32_t) * 2 * (size_t)(R + 1), 256);
   // Partial results of a chain: the part with its first K/V tile in a row per (token list entry,
-  // query head), and a part that a CTA's range begins with in the CTA's own 2 x 128 rows.
-  L.base_ml = off; off = align_up(off + sizeof(float2) * (size_t)R * (size_t)Hq, 256);
-  L.base_o = off;  off = align_up(off + sizeof(float) * (size_t)R * (size_t)Hq * (size_t)D, 256);
-  // (and the own keys' part of a chunk's tokens in such a row too)
-  L.own_ml = off;  off = align_up(off + sizeof(float2) * (size_t)R * (size_t)Hq, 256);
-  L.own_o = off;   off = align_up(off + sizeof(float) * (size_t)R * (size_t)Hq * (size_t)D, 256);
+  // first or second chain, query head), and a part that a CTA's range begins with in the CTA's own
+  // 2 x 128 rows.
+  L.base_ml = off; off = align_up(off + sizeof(float2) * 2 * (size_t)R * (size_t)Hq, 256);
+  L.base_o = off;  off = align_up(off + sizeof(float) * 2 * (size_t)R * (size_t)Hq * (size_t)D, 256);
   const size_t cut_rows = (size_t)kMaxPreCtas * 2 * kPrefillTileM;
   L.cut_ml = off;  off = align_up(off + sizeof(float2) * cut_rows, 256);
   L.cut_o = off;   off = align_up(off + sizeof(float) * cut_rows * (size_t)D, 256);

@@ -14,9 +14,8 @@ namespace cb {
 
 constexpr int kPlanThreads = 1024;
 // With shared prefixes the planner has more to compute per sequence and its time is instructions: a
-// batch of one round (a sequence per thread) takes 5 us with 256 threads and 8 us with 1024, whose
-// idle warps run through every step too.
-constexpr int kPrePlanThreads = 256;
+// batch of one round (a sequence per thread) takes 5 us with kPrePlanThreads = 256 threads and 8 us
+// with 1024, whose idle warps run through every step too.
 template <bool kPre>
 constexpr int plan_threads() { return kPre ? kPrePlanThreads : kPlanThreads; }
 
@@ -165,18 +164,21 @@ constexpr int kPlanSmemGroups = 1024;
 // What the first look at a sequence finds (kept for the second where one round covers the batch).
 struct PreSeq {
   int c0, c1, kv, group, keys;
-  int tok0, cost0;  // a chunk that is a group of its own: its first list entry (else -1), PreGroup
+  // in batches of one round, for a sequence with a place in the token list:
+  int list, at;     // its first entry (else -1), and that entry's place in the group's chain
+  int chain;        // its own keys' group: PreGroup's cost0 (else -1)
+  int own_first;    // and that group's first key (0: it is the sequence's only chain)
 };
 
 // With shared prefixes: which groups' prefixes are computed once.  Fills the group list, and per
 // group number map (index in the list, -1: every member's own pass does it all) and cnt (the tokens
-// listed so far: 0).  Returns the work of the prefixes
-// per KV head in cost units (0: no group takes part; the same in every thread).
+// listed so far).  Returns the work of the prefixes per KV head in cost units (0: no group takes
+// part; the same in every thread).
 //
 // A group takes part when it has at least two query tokens (from members with at most kPreMaxQ
 // each) and kPreMinKeys keys; after bad metadata none does, and each sequence is computed alone.
-// Chunks that are groups of their own (kPreChunkItems; in batches of one round) follow the others in
-// the list.
+// Sequences that are groups of their own (PreGroup; in batches of one round) follow the others in the
+// list.
 // lens: the groups' prefix lengths (in shared memory where all of them fit, else a.prefix_lens).
 __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], int32_t* cnt,
                                              int32_t* first, int32_t* map, const int32_t* lens,
@@ -195,7 +197,7 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
   bool bad = false;
   for (int base = 0; base < a.S; base += kPrePlanThreads) {
     const int s = base + tid;
-    PreSeq q = {0, 0, 0, -1, 0, -1, 0};
+    PreSeq q = {0, 0, 0, -1, 0, -1, 0, -1, 0};
     if (s < a.S) {
       q.c0 = a.cu_seqlens_q[s];
       q.c1 = a.cu_seqlens_q[s + 1];
@@ -221,7 +223,7 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
     }
     // units of the chunk pass (a warp's sum first: 64-bit atomics on shared memory are slow)
     const int rows = pf_unit_tiles(a.G) * kPrefillTileM;
-    const bool chunk = lens_ok && s < a.S && q_len > 1 && !member;
+    const bool chunk = lens_ok && s < a.S && q_len > kPreMaxQ;
     if (__any_sync(0xffffffffu, chunk)) {
       unsigned long long n = chunk ? (unsigned long long)((q_len + rows - 1) / rows) : 0ull;
       for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -229,26 +231,33 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
     }
   }
   bad = __syncthreads_or(bad) != 0;
-  // this thread's sequence as a group of its own: its query tokens, or 0
-  const int my_q = mine.c1 - mine.c0, my_ctx = mine.kv - my_q;
-  const int own_tokens =
-      !bad && a.S <= kPrePlanThreads && my_q > kPreMaxQ && my_ctx >= kPreMinKeys &&
-              s_units * (unsigned long long)(pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq) < kPreChunkItems
-          ? my_q
-          : 0;
   auto shared_tokens = [&](int g, int keys) {  // tokens of group g if its prefix is computed once
     return bad || g >= a.NG || cnt[g] < 2 || keys < kPreMinKeys ? 0 : cnt[g];
   };
-  const int own_cost = own_tokens > 0 ? (int)min((long long)kPreMaxCost + 1,
-                                                 pre_shape(own_tokens, my_ctx, a.G).per) : 0;
+  // This thread's sequence: a member, and its keys as a group of their own (0: not).
+  const int my_q = mine.c1 - mine.c0, my_ctx = mine.kv - my_q;
+  const bool one_round = !bad && a.S <= kPrePlanThreads;
+  const bool my_member = one_round && my_q > 0 && my_q <= kPreMaxQ && mine.group >= 0 &&
+                         shared_tokens(mine.group, mine.keys) > 0;
+  const bool few_chunks =
+      s_units * (unsigned long long)(pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq) < kPreChunkItems;
+  int own_nt = 0;
+  if (my_member) {
+    if (my_q > a.pack) own_nt = pre_tiles(mine.keys, mine.kv);
+  } else if (one_round && my_q > 1 && mine.kv >= kPreMinKeys &&
+             (my_q <= kPreMaxQ || (few_chunks && my_ctx >= my_q))) {
+    own_nt = pre_tiles(0, mine.kv);
+  }
+  const int own_cost = own_nt > 0 ? (int)min((long long)kPreMaxCost + 1,
+                                             pre_shape(my_q, own_nt, a.G).per) : 0;
   unsigned long long total = own_cost;
   for (int g = tid; g < a.NG; g += kPrePlanThreads) {
     const int n = shared_tokens(g, lens[g]);
-    if (n > 0) total += (unsigned long long)pre_shape(n, lens[g], a.G).per;
+    if (n > 0) total += (unsigned long long)pre_shape(n, pre_tiles(0, lens[g]), a.G).per;
   }
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if ((tid & 31) == 0 && total > 0) atomicAdd(&s_total, total);
-  const bool any_own = __syncthreads_or(own_tokens) != 0;
+  const bool any_own = __syncthreads_or(own_nt) != 0;
   const bool too_much = s_total > kPreMaxCost;  // (32 bits hold every cost below)
   bad |= too_much;
   int carry[4] = {0, 0, 0, 0};  // groups, tokens, cost, keys (an estimate: it may wrap)
@@ -256,11 +265,12 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
     const int g = base + tid;
     const int keys = g < a.NG ? lens[g] : 0;
     const int n = shared_tokens(g, keys);
-    int v[4] = {n > 0, n, n > 0 ? (int)pre_shape(n, keys, a.G).per : 0, n > 0 ? keys : 0};
+    int v[4] = {n > 0, n, n > 0 ? (int)pre_shape(n, pre_tiles(0, keys), a.G).per : 0, n > 0 ? keys : 0};
     int ex[4], tot[4];
     block_scan4<kPrePlanThreads>(v, ex, tot, sw);  // (its barriers also part the reads of cnt from the writes)
     if (n > 0)
-      groups[carry[0] + ex[0]] = {carry[2] + ex[2], n, carry[1] + ex[1], keys, first[g]};
+      groups[carry[0] + ex[0]] =
+          {carry[2] + ex[2], n, carry[1] + ex[1], 0, keys, first[g], -1, 0};
     if (g < a.NG) {
       map[g] = n > 0 ? carry[0] + ex[0] : -1;
       cnt[g] = 0;
@@ -268,16 +278,30 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
 #pragma unroll
     for (int k = 0; k < 4; ++k) carry[k] += tot[k];
   }
-  if (any_own && !too_much) {
-    int v[4] = {own_tokens > 0, own_tokens, own_cost, own_tokens > 0 ? my_ctx : 0}, ex[4], tot[4];
-    block_scan4<kPrePlanThreads>(v, ex, tot, sw);
-    if (own_tokens > 0) {
-      mine.tok0 = carry[1] + ex[1];
-      mine.cost0 = carry[2] + ex[2];
-      groups[carry[0] + ex[0]] = {mine.cost0, own_tokens, mine.tok0, my_ctx, tid};
+  if (!too_much && one_round) {
+    __syncthreads();  // the groups and map are written, cnt is 0
+    if (my_member) {
+      mine.at = atomicAdd(&cnt[mine.group], my_q);
+      mine.list = groups[map[mine.group]].tok0 + mine.at;
+      mine.own_first = mine.keys;
     }
+    if (any_own) {
+      int v[4] = {own_nt > 0, own_nt > 0 && !my_member ? my_q : 0, own_nt > 0 ? own_cost : 0,
+                  own_nt > 0 ? mine.kv - mine.own_first : 0};
+      int ex[4], tot[4];
+      block_scan4<kPrePlanThreads>(v, ex, tot, sw);
+      if (own_nt > 0) {
+        mine.chain = carry[2] + ex[2];
+        if (!my_member) {
+          mine.list = carry[1] + ex[1];
+          mine.at = 0;
+        }
+        groups[carry[0] + ex[0]] = {mine.chain, my_q,   mine.list, mine.own_first,
+                                    mine.kv,    tid,    my_ctx,    my_member};
+      }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) carry[k] += tot[k];
+      for (int k = 0; k < 4; ++k) carry[k] += tot[k];
+    }
   }
   if (tid == 0) {
     hdr->pre_groups = carry[0];
@@ -341,7 +365,7 @@ __device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_
       best_n = n;
     }
   }
-  return best_n < cap ? best_n : cap;
+  return cap < 1 ? 1 : best_n < cap ? best_n : cap;
 }
 
 // Batches of up to this many decode (or chunk) sequences keep the planner's prefix arrays in
@@ -382,13 +406,13 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   int32_t* grp_first = few ? s_groups + kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.first);
   int32_t* grp_map = few ? s_groups + 2 * kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.map);
   const int32_t* grp_lens = few ? s_groups + 3 * kPlanSmemGroups : a.prefix_lens;
-  PreSeq mine = {0, 0, 0, -1, 0, -1, 0};
+  PreSeq mine = {0, 0, 0, -1, 0, -1, 0, -1, 0};
   if constexpr (kPre) {
     if (few)  // (the function's first barrier follows)
       for (int g = tid; g < a.NG; g += NT) s_groups[3 * kPlanSmemGroups + g] = a.prefix_lens[g];
     pre_cost = plan_prefixes(a, sw, grp_cnt, grp_first, grp_map, grp_lens, mine);
   }
-  // kPre: chunks that are groups of their own: (first token, tokens, first list entry, keys), cost0
+  // kPre: chunks that are groups of their own: (first token, tokens, first list entry, K/V tiles), cost0
   __shared__ int s_chunks;
   __shared__ int4 s_chunk[kPre ? kPreChunkItems : 1][2];
   if (kPre && tid == 0) s_chunks = 0;  // (the loop's barriers follow)
@@ -418,6 +442,8 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       if (!ok) {
         report(a.err, kErrOutOfRange);
         bad = true;
+      } else if (kPre && base == 0 && mine.chain >= 0) {
+        // all its own keys are a group of their own
       } else if (kPre && pre_cost > 0 && q_len > 0 && q_len <= kPreMaxQ &&
                  (grp = base == 0 ? mine.group : a.prefix_group[s]) >= 0 && grp_map[grp] >= 0) {
         // records of a.pack tokens: the tiles from the one holding the prefix's end to the one
@@ -429,12 +455,6 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
           v[1] += (kv - max(q_len - i - a.pack, 0) - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
         }
         my_keys += (float)(kv - keys);
-      } else if (kPre && base == 0 && mine.tok0 >= 0) {
-        // a chunk whose context is computed apart: its own keys
-        keys = kv - q_len;
-        v[2] = 1;
-        v[3] = (q_len + unit_rows - 1) / unit_rows;
-        my_pairs += 0.5f * (float)q_len * (float)(q_len + 1);
       } else if (q_len == 1) {
         grp = -1;
         // tiles from the one holding the window's first key (every key without a window)
@@ -460,13 +480,34 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     }
     int ex[4], tot[4];
     block_scan4<NT>(v, ex, tot, sw);
-    if (kPre && grp >= 0 && v[0]) {
+    if (kPre && base == 0 && mine.chain >= 0) {
+      const int q_len = mine.c1 - mine.c0, own_nt = pre_tiles(mine.own_first, mine.kv);
+      if (q_len > kPreMaxQ) {  // a chunk's list entries are written below, by all threads
+        const int x = atomicAdd(&s_chunks, 1);  // (fewer than kPreChunkItems)
+        s_chunk[x][0] = make_int4(tok, q_len, mine.list, own_nt);
+        s_chunk[x][1] = make_int4(mine.chain, 0, 0, 0);
+      } else {
+        int4 shared = make_int4(0, 0, 0, 0);  // the prefix's chain
+        if (mine.own_first > 0) {
+          const PreGroup g = reinterpret_cast<const PreGroup*>(a.ws + PL.group)[grp_map[mine.group]];
+          shared = make_int4(mine.at, g.n_tok, pre_tiles(0, g.keys), g.cost0);
+        }
+        for (int t = 0; t < q_len; ++t) {
+          int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 3 * (size_t)(mine.list + t);
+          const int4 own = make_int4(t, q_len, own_nt, mine.chain);
+          entry[0] = make_int4(tok + t, -1, 0, 0);
+          entry[1] = mine.own_first > 0 ? shared : own;
+          entry[2] = mine.own_first > 0 ? own : make_int4(0, 0, 0, 0);
+          ++shared.x;
+        }
+      }
+    } else if (kPre && grp >= 0 && v[0]) {
       // The tokens' places in the group's list come in any order: a row's result does not depend
       // on the tile it is computed in.
       const int q_len = base == 0 ? mine.c1 - mine.c0 : a.cu_seqlens_q[s + 1] - tok;
       const int first = keys / kDecodeTileKeys * kDecodeTileKeys;
-      const int at = atomicAdd(&grp_cnt[grp], q_len);
       const PreGroup group = reinterpret_cast<const PreGroup*>(a.ws + PL.group)[grp_map[grp]];
+      const int at = base == 0 && mine.list >= 0 ? mine.at : atomicAdd(&grp_cnt[grp], q_len);
       int tile = carry[1] + ex[1], i = carry[0] + ex[0];
       for (int j = 0; j < q_len; j += a.pack, ++i) {
         const int n = min(a.pack, q_len - j), n_keys = kv - (q_len - j - n);
@@ -477,9 +518,10 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
         if (i < kSeqs) s_dec_prefix[i] = tile;
         reinterpret_cast<int2*>(a.ws + PL.rec)[i] = make_int2(keys, n);
         for (int t = 0; t < n; ++t) {
-          int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 2 * (size_t)(group.tok0 + at + j + t);
+          int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 3 * (size_t)(group.tok0 + at + j + t);
           entry[0] = make_int4(tok + j + t, 8 * i + t, tile, tile + n_tiles);
-          entry[1] = make_int4(at + j + t, group.n_tok, keys, group.cost0);
+          entry[1] = make_int4(at + j + t, group.n_tok, pre_tiles(0, keys), group.cost0);
+          entry[2] = make_int4(0, 0, 0, 0);
         }
         tile += n_tiles;
       }
@@ -493,16 +535,6 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     }
     if (v[2]) {
       const int i = carry[2] + ex[2];
-      if constexpr (kPre) {
-        int2 pre = make_int2(0, 0);
-        if (base == 0 && mine.tok0 >= 0) {  // its tokens' list entries are written below, by all
-          pre = make_int2(keys, mine.tok0);
-          const int x = atomicAdd(&s_chunks, 1);  // (fewer than kPreChunkItems)
-          s_chunk[x][0] = make_int4(tok, mine.c1 - mine.c0, mine.tok0, keys);
-          s_chunk[x][1] = make_int4(mine.cost0, 0, 0, 0);
-        }
-        reinterpret_cast<int2*>(a.ws + PL.pf)[i] = pre;
-      }
       pf_seq[i] = s;
       pf_prefix[i] = carry[3] + ex[3];
       if (i < kSeqs) {
@@ -521,9 +553,10 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       const int4 ch = s_chunk[x][0];
       const int cost0 = s_chunk[x][1].x;
       for (int t = tid; t < ch.y; t += NT) {
-        int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 2 * (size_t)(ch.z + t);
+        int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 3 * (size_t)(ch.z + t);
         entry[0] = make_int4(ch.x + t, -1, 0, 0);
         entry[1] = make_int4(t, ch.y, ch.w, cost0);
+        entry[2] = make_int4(0, 0, 0, 0);
       }
     }
   }

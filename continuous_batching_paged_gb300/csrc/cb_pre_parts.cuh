@@ -28,23 +28,24 @@ __device__ __forceinline__ int pre_idle_index(int bx, int hg, int n, int grid) {
 
 // Shape of a group's chains.
 struct PreShape {
-  int nt;         // K/V tiles of the prefix
+  int nt;         // K/V tiles
   int full;       // units with two tiles of rows (the units before the last, at least)
   int units;      // units in all
   long long per;  // cost of all units under one KV head (kPreMaxCost at most, once planned)
 };
-__device__ __forceinline__ PreShape pre_shape(int n_tok, int keys, int G) {
+__device__ __forceinline__ PreShape pre_shape(int n_tok, int nt, int G) {
   PreShape s;
   const int per_tile = pre_tile_tokens(G);
   const int tiles = (n_tok + per_tile - 1) / per_tile;
-  s.nt = (keys + kChunkKeys - 1) / kChunkKeys;
+  s.nt = nt;
   s.full = tiles >> 1;
   s.units = (tiles + 1) >> 1;
-  s.per = (long long)s.nt * (kPreCost2 * s.full + kPreCost1 * (tiles & 1));
+  s.per = (long long)nt * (kPreCost2 * s.full + kPreCost1 * (tiles & 1));
   return s;
 }
-__device__ __forceinline__ long long pre_cost_per_head(int n_tok, int keys, int G) {
-  return pre_shape(n_tok, keys, G).per;
+// K/V tiles that keys first .. keys - 1 lie in.
+__device__ __forceinline__ int pre_tiles(int first, int keys) {
+  return (keys + kChunkKeys - 1) / kChunkKeys - first / kChunkKeys;
 }
 
 // CTA c of N does the cost range [pre_bound(W, c, N), pre_bound(W, c + 1, N)) of the W units.
@@ -58,13 +59,15 @@ __device__ __forceinline__ int pre_step(long long cs, int w, int nt, long long b
   return ((int)(b - cs) + w - 1) / w;
 }
 
-// Part of a chain that one CTA does: K/V tiles [j0, j1) of the prefix of `seq` (keys long) under KV
-// head kvh, for `two` tiles of rows (or one): ntok[] query tokens from token list entry tok0 on.
+// Part of a chain that one CTA does: K/V tiles [j0, j1) of `seq` under KV head kvh, as far as keys
+// first .. keys - 1 lie in them, for `two` tiles of rows (or one): ntok[] query tokens from token list
+// entry tok0 on, the first of them token `at` of the group (see PreGroup for ctx and second).
 struct PreSeg {
-  int kvh, seq, keys, j0, j1, tok0;
+  int kvh, seq, first, keys, ctx, second, j0, j1, tok0, at;
   int ntok[2];
   bool two;
   bool once;  // the group has this unit alone: its keys are read once per KV head
+  bool cut;   // not the chain's first part
 };
 
 // Walks the parts of one CTA's range, in order.
@@ -96,21 +99,28 @@ struct PreWalk {
         ++gi;
       }
       const PreGroup g = groups[gi];
-      const PreShape sh = pre_shape(g.n_tok, g.keys, G);
+      const int tile0 = g.first / kChunkKeys;
+      const PreShape sh = pre_shape(g.n_tok, pre_tiles(g.first, g.keys), G);
       const int u = (rel - g.cost0) / (kPreCost2 * sh.nt);  // (a cheaper last unit: same index)
       const int w = u < sh.full ? kPreCost2 : kPreCost1;
       const long long cs = head0 + g.cost0 + u * kPreCost2 * sh.nt;
       pos = cs + w * sh.nt;
-      s.j0 = pre_step(cs, w, sh.nt, b0);
-      s.j1 = pre_step(cs, w, sh.nt, b1);
-      if (s.j0 >= s.j1) continue;
-      const int per_tile = pre_tile_tokens(G), first = u * 2 * per_tile;
+      const int r0 = pre_step(cs, w, sh.nt, b0), r1 = pre_step(cs, w, sh.nt, b1);
+      if (r0 >= r1) continue;
+      const int per_tile = pre_tile_tokens(G);
+      s.j0 = tile0 + r0;
+      s.j1 = tile0 + r1;
+      s.cut = r0 > 0;
+      s.at = u * 2 * per_tile;
       s.kvh = kvh;
       s.seq = g.seq;
+      s.first = g.first;
       s.keys = g.keys;
-      s.tok0 = g.tok0 + first;
-      s.ntok[0] = min(per_tile, g.n_tok - first);
-      s.ntok[1] = max(0, min(per_tile, g.n_tok - first - per_tile));
+      s.ctx = g.ctx;
+      s.second = g.second;
+      s.tok0 = g.tok0 + s.at;
+      s.ntok[0] = min(per_tile, g.n_tok - s.at);
+      s.ntok[1] = max(0, min(per_tile, g.n_tok - s.at - per_tile));
       s.two = s.ntok[1] > 0;
       s.once = sh.units == 1;
       return true;

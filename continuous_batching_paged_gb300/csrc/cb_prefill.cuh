@@ -37,8 +37,6 @@
 // TMEM columns: [0,128) S/P of A, [128,256) S/P of B, [256,256+D) O of A, then O of B.
 #pragma once
 
-#include <type_traits>
-
 #include "cb_common.cuh"
 #include "cb_launch.h"
 
@@ -89,7 +87,7 @@ constexpr int kRegsSoftmax = 200;  // warpgroups 1 and 2
 static_assert(kRegsIssue + 2 * kRegsSoftmax <= 3 * 168, "register split exceeds the launch");
 constexpr int kItemConsumers = 10;  // producer, MMA warp, 4 warps of each softmax group
 
-struct PfItemBase {
+struct PfItem {
   int item;                                    // claimed item index, -1: no more work
   int s, kvh, ctx;
   int head[2], tok[2], rows[2], nk[2], nt[2];  // per tile: query head, first token, valid rows,
@@ -99,14 +97,7 @@ struct PfItemBase {
   int j0;                                      // first K/V tile (a sliding window skips older)
   int hasB;
 };
-// With shared prefixes: a chunk whose prefix is computed apart starts at key `lo` > 0, and its tiles'
-// results are parts, in the rows of the token list's entries from list[] on.
-struct PfItemPre : PfItemBase {
-  int lo, list[2];
-};
-template <bool kPre>
-using PfItem = std::conditional_t<kPre, PfItemPre, PfItemBase>;
-static_assert(sizeof(PfItemPre) <= 128, "a decoded item fits its shared-memory slot");
+static_assert(sizeof(PfItem) <= 128, "a decoded item fits its shared-memory slot");
 
 // Query heads (pairs) per unit: items are unit-major with the head (pair) fastest, so the
 // CTAs on the heads of one KV group at the same time share its K/V tiles through L2.
@@ -114,12 +105,11 @@ __device__ __forceinline__ int pf_heads_per_unit(const AttnArgs& a) {
   return pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq;
 }
 
-template <bool kWin, bool kPre>
-__device__ __forceinline__ PfItem<kPre> pf_decode_item(int item, const AttnArgs& a,
-                                                       const int32_t* pf_seq,
-                                                       const int32_t* pf_prefix,
-                                                       const int32_t* pf_order, int n_pf) {
-  PfItem<kPre> it;
+template <bool kWin>
+__device__ __forceinline__ PfItem pf_decode_item(int item, const AttnArgs& a,
+                                                 const int32_t* pf_seq, const int32_t* pf_prefix,
+                                                 const int32_t* pf_order, int n_pf) {
+  PfItem it;
   it.item = item;
   const int hu_n = pf_heads_per_unit(a);
   const int pos = item / hu_n;  // position in the longest-first unit order
@@ -161,28 +151,18 @@ __device__ __forceinline__ PfItem<kPre> pf_decode_item(int item, const AttnArgs&
   it.nt_all = max(it.nt[0], it.nt[1]);
   // tile A's first row is the item's earliest query; keys before its window are not needed
   it.j0 = kWin ? window_first_key(it.ctx + qt[0] * kPrefillTileM, a.window) / kChunkKeys : 0;
-  if constexpr (kPre) {
-    const int2 pre = reinterpret_cast<const int2*>(
-        a.ws + pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack).pf)[lo];
-    it.lo = pre.x;
-    it.j0 = pre.x / kChunkKeys;
-    it.list[0] = pre.y + it.qoff[0];
-    it.list[1] = pre.y + it.qoff[1];
-  }
   return it;
 }
 
-// kPre: with shared prefixes.
 // kWin: sliding-window attention (a.window > 0).  The full causal pass is compiled without
 // the window's bookkeeping, so it runs exactly the code it ran before windows existed.
 // One persistent CTA of the chunk pass (all kPrefillThreads threads).  Runs in the attention
 // kernel (cb_attention.cu) with that kernel's dynamic shared memory.
-template <int D, bool kWin, bool kPre>
+template <int D, bool kWin>
 __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap* qmap,
                                             const CUtensorMap* kmap, const CUtensorMap* vmap,
                                             uint8_t* smem_raw) {
   using SM = PrefillSmem<D>;
-  using Item = PfItem<kPre>;
   constexpr int NS = SM::kStages;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -191,10 +171,10 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + SM::kMisc);
   // Decoded items, two slots: the scheduler warp claims and decodes the next item while the
   // current one runs; every role reads it from here (no global-memory chain at an item's start).
-  auto item_slot = [&](int slot) { return reinterpret_cast<Item*>(smem + SM::kItems + slot * SM::kItemSlot); };
+  auto item_slot = [&](int slot) { return reinterpret_cast<PfItem*>(smem + SM::kItems + slot * SM::kItemSlot); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, kPre ? a.pack : 1);
+  const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, a.pack);
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + L.header);
   const int32_t* pf_seq = reinterpret_cast<const int32_t*>(a.ws + L.pf_seq);
   const int32_t* pf_prefix = reinterpret_cast<const int32_t*>(a.ws + L.pf_prefix);
@@ -247,7 +227,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
       for (uint32_t k = 0;; ++k) {
         const int slot = k & 1;
         if (!mbar_wait(bar(SM::bItemFull + slot), (k >> 1) & 1)) { report(a.err, kErrTimeout); break; }
-        const Item it = *item_slot(slot);
+        const PfItem it = *item_slot(slot);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
         if (it.item < 0) break;
@@ -363,8 +343,8 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
           if (kc == 0 && item >= 0) atomicMin(&hdr->t_pf_start, global_ns());  // role span
         }
         item = __shfl_sync(0xffffffffu, item, 0);
-        Item it;
-        if (item >= 0) it = pf_decode_item<kWin, kPre>(item, a, pf_seq, pf_prefix, pf_order, n_pf);
+        PfItem it;
+        if (item >= 0) it = pf_decode_item<kWin>(item, a, pf_seq, pf_prefix, pf_order, n_pf);
         it.item = item;
         if (lane == 0) {
           *item_slot(slot) = it;
@@ -444,7 +424,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         const int slot = k & 1;
         wait(bar(SM::bItemFull + slot), (k >> 1) & 1);
         if (!ok) break;
-        const Item it = *item_slot(slot);
+        const PfItem it = *item_slot(slot);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
         if (it.item < 0) break;
@@ -506,7 +486,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
     for (uint32_t k = 0;; ++k) {
       const int slot = k & 1;
       if (!mbar_wait(bar(SM::bItemFull + slot), (k >> 1) & 1)) { report(a.err, kErrTimeout); break; }
-      const Item it = *item_slot(slot);
+      const PfItem it = *item_slot(slot);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
       if (it.item < 0) break;
@@ -535,12 +515,11 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         const int key0 = j * kChunkKeys;
         // causal edge (keys past the row's position) and, with a sliding window, its lower
         // edge (keys at or before position - W)
-        int lo_r = kWin ? limit - W + 1 : 0;
-        if constexpr (kPre) lo_r = it.lo;  // keys before it are the prefix's
-        if (key0 + kChunkKeys - 1 > diag0 || ((kWin || kPre) && key0 < lo_r)) {
+        const int lo_r = kWin ? limit - W + 1 : 0;
+        if (key0 + kChunkKeys - 1 > diag0 || (kWin && key0 < lo_r)) {
 #pragma unroll
           for (int c = 0; c < 128; ++c)
-            if (key0 + c > limit || ((kWin || kPre) && key0 + c < lo_r)) sr[c] = __float_as_uint(-INFINITY);
+            if (key0 + c > limit || (kWin && key0 + c < lo_r)) sr[c] = __float_as_uint(-INFINITY);
         }
         // row max: 8 independent chains of three-input max over the 128 columns
         float mx8[8];
@@ -635,33 +614,6 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
       if (!mbar_wait(bar(SM::bOFinal + t), kx & 1)) { report(a.err, kErrTimeout); break; }
       __syncwarp();
       tc_fence_after();
-      if constexpr (kPre) if (it.lo > 0) {
-        // ---- epilogue of a part: (m, l) and O as they are, to the list entry's row
-        const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack);
-        const size_t row = (size_t)((t ? it.list[1] : it.list[0]) + r) * a.Hq + head;
-#pragma unroll
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t ov[32];
-          tmem_ld32(t_lane + o_col + ch * 32, ov);
-          tc_wait_ld();
-          if (r < rows) {
-            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<float*>(a.ws + PL.own_o) + row * D +
-                                                  ch * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
-          }
-        }
-        if (r < rows)
-          reinterpret_cast<float2*>(a.ws + PL.own_ml)[row] = make_float2(m_run, l_run);
-        if (r == 0) atomicMax(&hdr->t_pf_end, global_ns());
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(SM::bOFree + t));
-        gx += nt - it.j0;
-        kx += 1;
-        continue;
-      }
       const float inv = 1.f / l_run;
       const bool store = r < rows;
       // Each 32-column slice of the warp's 32 rows goes through shared memory: lane = row on

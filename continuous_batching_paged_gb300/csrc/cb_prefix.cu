@@ -6,8 +6,8 @@
 // the same sum in another order, so a row's result is that of cb_ragged_paged_attention within
 // rounding.
 //
-// Own keys are streamed by the decode pass (cb_decode.cuh), as ever, from the prefix's end on, or by
-// the chunk pass for a member with more than kPreMaxQ query tokens.  The prefix is a dense
+// Own keys are streamed by the decode pass (cb_decode.cuh), as ever, from the prefix's end on (or,
+// for several query tokens, are a group of their own: PreGroup).  The prefix is a dense
 // contraction (all rows of the group see all its keys) and runs on the 5th-generation tensor cores
 // (cb_prefix.cuh): its K/V are read once per 2 x 128 rows (from HBM at most once) instead of once
 // per query token, which is what bounds the batch otherwise.  The passes run side by side in one
@@ -63,8 +63,8 @@ static cudaError_t launch_instance(const AttnArgs& a, const AttnMaps& m, const C
 
 // One warp per (query token, HP query heads of one KV head) of the shared prefixes:
 // M = max m_c, w_c = 2^(m_c - M), out = sum_c w_c o_c / sum_c w_c l_c,
-// lse = (M + log2 sum_c w_c l_c) ln 2 over the parts c of the prefix's chain and of the own keys.
-// Every part that exists holds at least one key, so its m is finite.  A lane finds a part and loads
+// lse = (M + log2 sum_c w_c l_c) ln 2 over the parts c of its chains and of its decode record.  Some
+// part holds a key that the token sees, so M is finite (a part without one has m = -inf, w = 0).  A lane finds a part and loads
 // its (m, l), so all are there after one trip to L2, and the rows of O follow kC at a time.  Finding
 // the parts is what costs instructions, so with many rows a warp does HP = 4 heads; with few, where
 // only the latency of its loads counts, one.
@@ -85,11 +85,12 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnA
   const int per_kvh = (a.G + HP - 1) / HP, per_tok = per_kvh * a.Hkv;
   long long job = (long long)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
   const int i0 = (int)(job / per_tok);
-  int4 ta = make_int4(0, 0, 0, 0), tb = ta;
-  if (i0 < a.R) {
-    ta = __ldcg(list + 2 * (size_t)i0);
-    tb = __ldcg(list + 2 * (size_t)i0 + 1);
-  }
+  int4 e[3] = {};
+  auto entry = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) e[k] = __ldcg(list + 3 * (size_t)i + k);
+  };
+  if (i0 < a.R) entry(i0);
   const long long jobs = (long long)__ldcg(&hdr->pre_tokens) * per_tok;
   const long long ntiles = __ldcg(&hdr->dec_tiles), Wh = __ldcg(&hdr->pre_cost), W = Wh * a.Hkv;
   const int N = __ldcg(&hdr->decode_ctas), NP = __ldcg(&hdr->pre_ctas);
@@ -99,23 +100,32 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnA
     const int i = (int)(job / per_tok), in_tok = (int)(job - (long long)i * per_tok);
     const int kvh = in_tok / per_kvh, h0 = (in_tok - kvh * per_kvh) * HP;
     const int nh = a.G - h0 < HP ? a.G - h0 : HP, head0 = kvh * a.G + h0;
-    if (waited) {
-      ta = __ldcg(list + 2 * (size_t)i);
-      tb = __ldcg(list + 2 * (size_t)i + 1);
+    if (waited) entry(i);
+    const int token = e[0].x, rec = e[0].y;
+    // own keys' parts: decode CTAs df .. dl of the record
+    const int df = rec < 0 ? 0 : cta_of_tile(e[0].z, ntiles, N);
+    const int n_own = rec < 0 ? 0 : cta_of_tile(e[0].w - 1, ntiles, N) - df + 1;
+    // a chain's parts: prefix CTAs pf ..., its place, and this token's first head's row in its tile
+    struct Chain {
+      long long cs;
+      int w, nt, pf, n, tile, row;
+    } ch[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int4 c = e[1 + k];  // place, tokens, tiles, cost0
+      ch[k] = {0, 1, 0, 0, 0, 0, 0};
+      if (c.z > 0) {
+        const PreShape sh = pre_shape(c.y, c.z, a.G);
+        ch[k].tile = c.x / per_tile;
+        ch[k].w = (ch[k].tile >> 1) < sh.full ? kPreCost2 : kPreCost1;
+        ch[k].nt = c.z;
+        ch[k].cs = kvh * Wh + c.w + (ch[k].tile >> 1) * kPreCost2 * c.z;
+        ch[k].pf = cta_of_tile(ch[k].cs, W, NP);
+        ch[k].n = cta_of_tile(ch[k].cs + (long long)ch[k].w * c.z - 1, W, NP) - ch[k].pf + 1;
+        ch[k].row = (c.x - ch[k].tile * per_tile) * a.G + h0;
+      }
     }
-    const PreToken t = {ta.x, ta.y, ta.z, ta.w, tb.x, tb.y, tb.z, tb.w};
-    // own keys: decode CTAs df .. dl, or the one part of a chunk's token
-    const int df = t.rec < 0 ? 0 : cta_of_tile(t.tile0, ntiles, N);
-    const int dl = t.rec < 0 ? 0 : cta_of_tile(t.tile1 - 1, ntiles, N);
-    // the prefix: the chain of this token's unit, prefix CTAs pf .. pl
-    const PreShape sh = pre_shape(t.n_tok, t.keys, a.G);
-    const int tile = t.at / per_tile, u = tile >> 1;
-    const int w = u < sh.full ? kPreCost2 : kPreCost1;
-    const long long cs = kvh * Wh + t.cost0 + u * kPreCost2 * sh.nt;
-    const int pf = cta_of_tile(cs, W, NP), pl = cta_of_tile(cs + (long long)w * sh.nt - 1, W, NP);
-    const int n_pre = pl - pf + 1, nparts = n_pre + dl - df + 1;
-    // row of this token's first head in its tile, for the parts in a CTA's own rows
-    const int in_tile = (t.at - tile * per_tile) * a.G + h0;
+    const int n_pre = ch[0].n + ch[1].n, nparts = n_pre + n_own;
     float M[HP], l[HP], acc[HP][PER];
 #pragma unroll
     for (int h = 0; h < HP; ++h) {
@@ -130,24 +140,21 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnA
       const float2* pml = nullptr;
       unsigned long long po = 0;
       if (p < n_pre) {
-        const int c = pf + p;
-        const int j0 = pre_step(cs, w, sh.nt, pre_bound(W, c, NP));
-        const int j1 = pre_step(cs, w, sh.nt, pre_bound(W, c + 1, NP));
+        const int k = p < ch[0].n ? 0 : 1;
+        const Chain x = k ? ch[1] : ch[0];
+        const int c = x.pf + (k ? p - ch[0].n : p);
+        const int j0 = pre_step(x.cs, x.w, x.nt, pre_bound(W, c, NP));
+        const int j1 = pre_step(x.cs, x.w, x.nt, pre_bound(W, c + 1, NP));
         const bool cut = j0 > 0;
-        const size_t at = cut ? ((size_t)c * 2 + (tile & 1)) * kPrefillTileM + in_tile
-                              : (size_t)i * a.Hq + head0;
+        const size_t at = cut ? ((size_t)c * 2 + (x.tile & 1)) * kPrefillTileM + x.row
+                              : ((size_t)i * 2 + k) * a.Hq + head0;
         if (j0 < j1) {  // (a range may end before the step that its last unit of cost lies in)
           pml = reinterpret_cast<const float2*>(a.ws + (cut ? PL.cut_ml : PL.base_ml)) + at;
           po = (unsigned long long)(reinterpret_cast<const float*>(
                                         a.ws + (cut ? PL.cut_o : PL.base_o)) + at * D);
         }
-      } else if (p < nparts && t.rec < 0) {
-        const size_t at = (size_t)i * a.Hq + head0;
-        pml = reinterpret_cast<const float2*>(a.ws + PL.own_ml) + at;
-        po = (unsigned long long)(reinterpret_cast<const float*>(a.ws + PL.own_o) + at * D);
       } else if (p < nparts) {
-        const size_t at =
-            (((size_t)(df + p - n_pre) + (t.rec >> 3)) * a.pack + (t.rec & 7)) * a.Hq + head0;
+        const size_t at = (((size_t)(df + p - n_pre) + (rec >> 3)) * a.pack + (rec & 7)) * a.Hq + head0;
         pml = reinterpret_cast<const float2*>(a.ws + L.part_ml) + at;
         po = (unsigned long long)(reinterpret_cast<const float*>(a.ws + L.part_o) + at * D);
       }
@@ -166,14 +173,15 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnA
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
         mn = fmaxf(mn, M[h]);
-        if (h >= nh) mn = 0.f;  // (no such head: every weight 0)
+        const float mx = mn;
+        if (h >= nh || mn == -INFINITY) mn = 0.f;  // (no such head, or no key yet: every weight 0)
         const float sc = fast_exp2(M[h] - mn);
         wt[h] = fast_exp2(ml[h].x - mn);
         float ls = wt[h] * ml[h].y;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
         l[h] = l[h] * sc + ls;
-        M[h] = mn;
+        M[h] = mx;
 #pragma unroll
         for (int k = 0; k < PER; ++k) acc[h][k] *= sc;
       }
@@ -215,7 +223,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnA
     for (int h = 0; h < HP; ++h) {
       if (h >= nh) continue;
       const float inv = 1.f / l[h];
-      const size_t row = (size_t)t.token * a.Hq + head0 + h;
+      const size_t row = (size_t)token * a.Hq + head0 + h;
       uint32_t* dst = reinterpret_cast<uint32_t*>(outg + row * D + lane * PER);
       if constexpr (PER == 4)
         *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[h][0] * inv, acc[h][1] * inv),

@@ -2,8 +2,9 @@
 // share (tcgen05 tensor cores, K/V streamed by TMA).
 //
 // Rows are query tokens x the G query heads of one KV head, 128 to a tile, gathered by TMA (a box
-// of G rows per token, from the group's token list); every row sees every key, so there is no mask
-// but the prefix's end.  A CTA does an equal share of all prefixes' work: a contiguous range of the
+// of G rows per token, from the group's token list); every row sees every key of a shared prefix, so
+// there is no mask but at the keys' ends and, for groups that are one sequence's own keys, its causal
+// edge.  A CTA does an equal share of all prefixes' work: a contiguous range of the
 // chains (PreGroup) laid end to end, whose parts of chains it takes one after the other.  With two
 // tiles of rows both read the same K/V tiles (as in the chunk pass) and the softmax bounds the step
 // (16 K exponentials a tile and SM); with one tile a step is bound by the K/V bytes (64 KB a step,
@@ -378,6 +379,11 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
       const int rows = (s.two && t ? s.ntok[1] : s.ntok[0]) * a.G;
       const bool active = quad * 32 < rows;
       const int first = s.two ? 0 : t, stride = s.two ? 1 : 2;
+      // keys that this row sees (its token's, where the group has a causal edge)
+      const int i_tok = r / a.G;
+      const int sees = s.ctx < 0 ? s.keys
+                                 : min(s.keys, s.ctx + s.at + (s.two && t ? pre_tile_tokens(a.G) : 0) +
+                                                   i_tok + 1);
       float m_run = -INFINITY, l_run = 0.f;
       for (int i = first; i < n; i += stride) {
         wait(bar(SM::bSFull + t), rx++ & 1);
@@ -404,10 +410,13 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
 #pragma unroll
           for (int x = 0; x < 4; ++x) tmem_ld32(t_lane + s_col + x * 32, sr + x * 32);
           tc_wait_ld();
-          if (left < kChunkKeys) {
+          // the keys' end (or causal edge) and their start inside this tile
+          const int key0 = (s.j0 + i) * kChunkKeys;
+          const int hi = sees - key0, lo = s.first - key0;
+          if (__any_sync(0xffffffffu, hi < kChunkKeys || lo > 0)) {
 #pragma unroll
             for (int x = 0; x < 128; ++x)
-              if (x >= left) sr[x] = __float_as_uint(-INFINITY);
+              if (x >= hi || x < lo) sr[x] = __float_as_uint(-INFINITY);
           }
           float mx8[8];
 #pragma unroll
@@ -432,7 +441,9 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
             m_run = mt;
             resc = true;
           }
-          const uint64_t scale2 = f2_pack(sl2, sl2), neg_m2 = f2_pack(-m_run, -m_run);
+          // (a row that sees no key so far: its m is -inf, 0 is subtracted, every p is 0)
+          const float m_sub = m_run == -INFINITY ? 0.f : m_run;
+          const uint64_t scale2 = f2_pack(sl2, sl2), neg_m2 = f2_pack(-m_sub, -m_sub);
           uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
           for (int col = 0; col < 128; col += 2) {
@@ -474,13 +485,13 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
       // ---- the part's end: partial (m, l) and O, unnormalised, to its rows.
       // Destination row of a token's head: the chain's own rows (part with its first tile), or
       // this CTA's.
-      const int per_tile = pre_tile_tokens(a.G), i_tok = r / a.G;
-      const bool cut = s.j0 > 0;
-      const size_t row = cut ? ((size_t)c * 2 + (s.two ? t : 0)) * kPrefillTileM + r
-                             : (size_t)(s.tok0 + (s.two ? t * per_tile : 0) + i_tok) * a.Hq +
-                                   s.kvh * a.G + (r - i_tok * a.G);
-      float2* ml = reinterpret_cast<float2*>(a.ws + (cut ? PL.cut_ml : PL.base_ml)) + row;
-      float* o = reinterpret_cast<float*>(a.ws + (cut ? PL.cut_o : PL.base_o)) + row * D;
+      const int per_tile = pre_tile_tokens(a.G);
+      const size_t row =
+          s.cut ? ((size_t)c * 2 + (s.two ? t : 0)) * kPrefillTileM + r
+                : ((size_t)(s.tok0 + (s.two ? t * per_tile : 0) + i_tok) * 2 + s.second) * a.Hq +
+                      s.kvh * a.G + (r - i_tok * a.G);
+      float2* ml = reinterpret_cast<float2*>(a.ws + (s.cut ? PL.cut_ml : PL.base_ml)) + row;
+      float* o = reinterpret_cast<float*>(a.ws + (s.cut ? PL.cut_o : PL.base_o)) + row * D;
       float w0 = 1.f, w1 = 0.f;  // weights of O_0 and O_1 (one tile of rows)
       if (!s.two) {
         // both groups' (m, l): group 1 hands its own over, group 0 hands the weights back
@@ -494,9 +505,9 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
         float x0, x1;
         asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x0), "=f"(x1) : "r"(xch) : "memory");
         if (t == 0) {
-          const float M = fmaxf(m_run, x0);  // (group 0 has the first tile, so M is finite)
-          w0 = fast_exp2(m_run - M);
-          w1 = fast_exp2(x0 - M);
+          const float M = fmaxf(m_run, x0), m_sub = M == -INFINITY ? 0.f : M;
+          w0 = fast_exp2(m_run - m_sub);
+          w1 = fast_exp2(x0 - m_sub);
           l_run = l_run * w0 + x1 * w1;
           m_run = M;
           __syncwarp();

@@ -445,3 +445,23 @@ def test_chunks_too_many_to_share(cuda_lib):
     # one chunk alone in its group, and a group of nothing but chunks
     check(grouped_batch([200, 1, 30, 45], [201, 9, 30, 60], [0, -1, 1, 1], [260, 400], 8, 2, 64, 16,
                         seed=931))
+
+
+def test_nothing_left_for_the_decode_pass(cuda_lib):
+    # every token is one of several of its sequence: own keys are groups of their own, in and outside
+    # of the groups, and no sequence has a decode record
+    q = [3, 8, 2, 5, 40, 8, 2]
+    own = [3, 30, 200, 129, 300, 8, 500]
+    for Hq, Hkv, D in ((8, 2, 128), (8, 1, 64), (5, 5, 64), (12, 1, 64)):
+        for grp in ([0, 0, 0, 0, 0, -1, -1], [-1] * 7, [0, 1, 0, 1, -1, 0, 1]):
+            check(grouped_batch(q, own, grp, [300, 140], Hq, Hkv, D, 16, seed=940 + Hq))
+
+
+def test_more_sequences_than_the_planner_sees_at_once(cuda_lib):
+    # beyond 256 sequences several tokens of a member take several records
+    rng = np.random.default_rng(9)
+    q = [int(x) for x in rng.integers(1, 9, 300)]
+    own = [n + int(x) for n, x in zip(q, rng.integers(0, 30, 300))]
+    grp = [int(x) for x in rng.integers(-1, 3, 300)]
+    check(grouped_batch(q, own, grp, [200, 150, 400], 4, 1, 64, 16, seed=950))
+    check(grouped_batch(q[:256], own[:256], grp[:256], [200, 150, 400], 4, 1, 64, 16, seed=951))
