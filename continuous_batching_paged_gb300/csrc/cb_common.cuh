@@ -59,7 +59,8 @@ struct PlanHeader {
   unsigned long long t_dec_start, t_dec_end, t_pf_start, t_pf_end;
   int32_t pre_cost;         // their work per KV head, in cost units (PreGroup),
   int32_t pre_tokens;       // entries of the groups' token list,
-  int32_t pre_keys, pad;    // and keys of all prefixes (for the planner's estimates)
+  int32_t pre_keys;         // keys of all groups, and groups of one sequence (for the planner's
+  int32_t pre_own;          // estimates)
 };
 
 // Byte offsets of the workspace sections (all 256-byte aligned).
@@ -98,14 +99,14 @@ __host__ __device__ inline WsLayout ws_layout(int S, int T, int Hq, int D, int p
 
 // ------------------------------------------------------------------------------------------
 // Shared prefixes (cb_prefix.cuh).  The query tokens of a group's members with at most kPreMaxQ each
-// go into the group's tiles of kPrefillTileM rows for the prefix.  For its own keys a member gets one
-// decode record where the record holds all its tokens (pre_pack); one with more is a group of its
-// own for them, with a causal edge at their end: a K/V tile of 128 keys costs the tensor cores 0.9 us
-// for one KV head and all its rows, the decode pass 0.8 us per 16 keys, 8 KV heads and record, so
-// from two records on the tiles are cheaper.  So is a sequence outside the groups with 2 to kPreMaxQ
-// tokens.  Longer ones (chunks) run the chunk pass, which sharing saves nothing: but where its work
-// items are fewer than kPreChunkItems, so that it would leave SMs idle, a chunk after at least its
-// own length of keys is such a group too, cut to equal shares like the others.
+// go into the group's tiles of kPrefillTileM rows for the prefix.  For its own keys a member gets
+// decode records of up to pre_pack tokens; with more than one, where that is estimated to be cheaper
+// (long own keys, few KV heads), it is a group of its own for them, with a causal edge at their end: a
+// K/V tile of 128 keys costs the tensor cores 0.9 us for one KV head and all its rows, the decode pass
+// 0.8 us per 16 keys, 8 KV heads and record.  A sequence outside the groups with 2 to kPreMaxQ tokens
+// is such a group, too.  Longer ones (chunks) run the chunk pass, which sharing saves nothing: but
+// where its work items are fewer than kPreChunkItems, so that it would leave SMs idle, a chunk after
+// at least its own length of keys is such a group too, cut to equal shares like the others.
 constexpr int kPreMaxQ = 8;
 constexpr int kPrePlanThreads = 256;  // of the planner (cb_plan.cuh); sequences it sees at once
 constexpr int kPreChunkItems = 152;

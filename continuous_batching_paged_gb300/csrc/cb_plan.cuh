@@ -158,6 +158,14 @@ __device__ inline int pf_unit_bin(const AttnArgs& a, const int32_t* pf_seq, cons
   return kCostBins - 1 - min(tiles, kCostBins - 1);
 }
 
+// Times that the planner weighs, in us of an SM, fitted to GB300 measurements: a step of a chain with
+// one tile of rows, a chain's start and end, and a decode record's 16-key tile (0.8 at 64 KB: 8 KV
+// heads of 128; 0.54 at 8 KB).
+constexpr float kPreStepUs = 0.9f, kPreChainUs = 7.f;
+__device__ __forceinline__ float pre_decode_tile_us(const AttnArgs& a) {
+  return 0.5f + 0.3f * (float)((a.Hkv < 8 ? a.Hkv : 8) * a.D) * (1.f / 1024.f);
+}
+
 // Up to this many groups the planner keeps in shared memory.
 constexpr int kPlanSmemGroups = 1024;
 
@@ -243,7 +251,12 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
       s_units * (unsigned long long)(pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq) < kPreChunkItems;
   int own_nt = 0;
   if (my_member) {
-    if (my_q > a.pack) own_nt = pre_tiles(mine.keys, mine.kv);
+    // its own keys as a group of their own, or as decode records: whatever takes fewer SM-us
+    const int nt = pre_tiles(mine.keys, mine.kv), records = (my_q + a.pack - 1) / a.pack;
+    const float as_chain = (float)a.Hkv * ((float)nt * kPreStepUs + kPreChainUs);
+    const float as_records = (float)(records * pre_head_groups(a.Hkv, a.G)) *
+                             (pre_decode_tile_us(a) * (float)((mine.kv - mine.keys) / kDecodeTileKeys + 1) + 1.f);
+    if (records > 1 && as_chain < as_records) own_nt = nt;
   } else if (one_round && my_q > 1 && mine.kv >= kPreMinKeys &&
              (my_q <= kPreMaxQ || (few_chunks && my_ctx >= my_q))) {
     own_nt = pre_tiles(0, mine.kv);
@@ -278,6 +291,7 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
 #pragma unroll
     for (int k = 0; k < 4; ++k) carry[k] += tot[k];
   }
+  int n_own = 0;  // sequences that are groups of their own
   if (!too_much && one_round) {
     __syncthreads();  // the groups and map are written, cnt is 0
     if (my_member) {
@@ -299,11 +313,13 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
         groups[carry[0] + ex[0]] = {mine.chain, my_q,   mine.list, mine.own_first,
                                     mine.kv,    tid,    my_ctx,    my_member};
       }
+      n_own = tot[0];
 #pragma unroll
       for (int k = 0; k < 4; ++k) carry[k] += tot[k];
     }
   }
   if (tid == 0) {
+    hdr->pre_own = n_own;
     hdr->pre_groups = carry[0];
     hdr->pre_tokens = carry[1];
     hdr->pre_cost = carry[2];
@@ -330,25 +346,25 @@ __device__ __forceinline__ int pre_cta_count(int free, int items, int cost, int 
 // sequences, prefixes of 1k to 64k keys, 8 and 1 KV heads, head_dim 64 and 128), in us:
 //   decode = 3 + hypot(x, y): x the CTA's tiles (0.8 each at 64 KB, 0.54 at 8 KB; a record counts as
 //            one more), y the HBM time of all bytes, its share of which grows as x shrinks;
-//   prefix = 12 + 0.8 per cost unit of a CTA; chunk work follows on the same SMs.
+//   prefix = 12 + 0.8 per cost unit of a CTA, and kPreChainUs per chain of a single sequence; chunk
+//            work follows on the same SMs.
 // The choice is the n with the least max(decode, prefix + chunk), plus a tenth of the other one so
 // that where one side is flat the other is not starved, plus 0.015 a CTA for the parts it adds.  It comes within 5 % of the best n on 13 of
 // the 15 batches, and within 12 % on the others.
 __device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes, float pre_bytes,
-                                                   int cost, float chunk_flops, int items,
+                                                   int cost, int chains, float chunk_flops, int items,
                                                    long long tiles, int records, int min_steps) {
   const int lane = threadIdx.x & 31;
   const int hg = pre_head_groups(a.Hkv, a.G), sms = a.chunk_ctas;
   const int cap = (int)(tiles < a.decode_ctas ? tiles : a.decode_ctas);
-  const float stage = (float)((a.Hkv < 8 ? a.Hkv : 8) * a.D) * (1.f / 1024.f);  // of 64 KB
-  const float x1 = (0.5f + 0.3f * stage) * ((float)tiles + (float)records);
+  const float x1 = pre_decode_tile_us(a) * ((float)tiles + (float)records);
   const float y = (dec_bytes + pre_bytes) * (0.7e-6f / 6.2f);
   float best = 3.4e38f;
   int best_n = 1;
   for (int n = 2 * (lane + 1); n <= (cap > 2 ? cap : 2) && n * hg < sms; n += 64) {
     const int free = sms - n * hg;
     const float x = __fdividef(x1, (float)n), d = 3.f + __fsqrt_rn(x * x + y * y);
-    const float p = 12.f + __fdividef(0.8f * (float)cost * (float)a.Hkv,
+    const float p = 12.f + __fdividef((0.8f * (float)cost + kPreChainUs * (float)chains) * (float)a.Hkv,
                                       (float)pre_cta_count(free, items, cost, a.Hkv, min_steps)) +
                     __fdividef(chunk_flops * (1.f / 6.4e6f), (float)free);
     const float t = fmaxf(d, p) + 0.1f * fminf(d, p) + 0.015f * (float)n;
@@ -648,6 +664,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       const int min_steps = pre_min_steps((long long)hdr->pre_tokens * a.Hq);
       if (a.decode_auto)
         n = choose_prefix_split(a, keys * row, (float)hdr->pre_keys * row, pre_cost,
+                                hdr->pre_own,
                                 pairs * (float)(4 * a.D * a.Hq), items, ntiles, n_dec, min_steps);
       // the decode CTAs without work; where a given number leaves none, an eighth of the chunk CTAs
       const int idle = pre_idle_count(pre_head_groups(a.Hkv, a.G), n, a.decode_ctas);
