@@ -203,8 +203,8 @@ __device__ __forceinline__ int decode_cta_index(int bx, int N, int grid) {
   const bool pairs = ((N | grid) & 1) == 0;
   const int units = pairs ? grid / 2 : grid, wanted = pairs ? N / 2 : N;
   const int u = pairs ? bx >> 1 : bx;
-  const int cu = (int)((long long)u * wanted / units);
-  if (u > 0 && (long long)(u - 1) * wanted / units == cu) return -1;
+  const int cu = u * wanted / units;  // (both at most CB_MAX_DECODE_CTAS)
+  if (u > 0 && (u - 1) * wanted / units == cu) return -1;
   return pairs ? 2 * cu + (bx & 1) : cu;
 }
 
@@ -360,6 +360,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 // Packed pairs of fp32 values in one 64-bit register, for the paired fp32 instructions

@@ -331,14 +331,16 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
 
 // Prefix CTAs where `free` SMs are left to them and to `items` chunk items (up to a third of them for
 // those, an SM per item: an item is mostly latency): as many for each KV head (PreGroup), no more
-// than the work is worth.
-__device__ __forceinline__ int pre_cta_count(int free, int items, int cost, int Hkv, int min_steps) {
+// than the work is worth (`most`).
+__device__ __forceinline__ int pre_cta_count(int free, int items, int most, int Hkv) {
   free -= items < free / 3 ? items : free / 3;
-  int np = free < kMaxPreCtas ? free : kMaxPreCtas;
-  const long long most = (long long)cost * Hkv / (min_steps * kPreCost1);
-  if (np > most) np = (int)most;
+  int np = free < most ? free : most;
   if (np > Hkv) np -= np % Hkv;
   return np < 1 ? 1 : np;
+}
+__device__ __forceinline__ int pre_cta_most(int cost, int Hkv, int min_steps) {
+  const long long most = (long long)cost * Hkv / (min_steps * kPreCost1);
+  return most < kMaxPreCtas ? (int)most : kMaxPreCtas;
 }
 
 // Decode CTAs per head group where prefixes are computed apart; the other SMs are the prefixes'.
@@ -353,20 +355,22 @@ __device__ __forceinline__ int pre_cta_count(int free, int items, int cost, int 
 // the 15 batches, and within 12 % on the others.
 __device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes, float pre_bytes,
                                                    int cost, int chains, float chunk_flops, int items,
-                                                   long long tiles, int records, int min_steps) {
+                                                   long long tiles, int records, int most) {
   const int lane = threadIdx.x & 31;
   const int hg = pre_head_groups(a.Hkv, a.G), sms = a.chunk_ctas;
   const int cap = (int)(tiles < a.decode_ctas ? tiles : a.decode_ctas);
   const float x1 = pre_decode_tile_us(a) * ((float)tiles + (float)records);
   const float y = (dec_bytes + pre_bytes) * (0.7e-6f / 6.2f);
+  const float pre_us = (0.8f * (float)cost + kPreChainUs * (float)chains) * (float)a.Hkv;
+  const float chunk_us = chunk_flops * (1.f / 6.4e6f);
   float best = 3.4e38f;
   int best_n = 1;
   for (int n = 2 * (lane + 1); n <= (cap > 2 ? cap : 2) && n * hg < sms; n += 64) {
     const int free = sms - n * hg;
-    const float x = __fdividef(x1, (float)n), d = 3.f + __fsqrt_rn(x * x + y * y);
-    const float p = 12.f + __fdividef((0.8f * (float)cost + kPreChainUs * (float)chains) * (float)a.Hkv,
-                                      (float)pre_cta_count(free, items, cost, a.Hkv, min_steps)) +
-                    __fdividef(chunk_flops * (1.f / 6.4e6f), (float)free);
+    const float x = __fdividef(x1, (float)n), d = 3.f + sqrt_approx(x * x + y * y);
+    const float p = 12.f + __fdividef(pre_us,
+                                      (float)pre_cta_count(free, items, most, a.Hkv)) +
+                    __fdividef(chunk_us, (float)free);
     const float t = fmaxf(d, p) + 0.1f * fminf(d, p) + 0.015f * (float)n;
     if (t < best) {
       best = t;
@@ -661,16 +665,15 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     if (kPre && pre_cost > 0) {
       const float row = (float)(a.Hkv * a.D * 4);  // bytes of a key and its value
       const int items = n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq);
-      const int min_steps = pre_min_steps((long long)hdr->pre_tokens * a.Hq);
+      const int most = pre_cta_most(pre_cost, a.Hkv, pre_min_steps((long long)hdr->pre_tokens * a.Hq));
       if (a.decode_auto)
         n = choose_prefix_split(a, keys * row, (float)hdr->pre_keys * row, pre_cost,
                                 hdr->pre_own,
-                                pairs * (float)(4 * a.D * a.Hq), items, ntiles, n_dec, min_steps);
+                                pairs * (float)(4 * a.D * a.Hq), items, ntiles, n_dec, most);
       // the decode CTAs without work; where a given number leaves none, an eighth of the chunk CTAs
       const int idle = pre_idle_count(pre_head_groups(a.Hkv, a.G), n, a.decode_ctas);
       if (tid == 0)
-        hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, items, pre_cost, a.Hkv,
-                                      min_steps);
+        hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, items, most, a.Hkv);
     } else if (a.decode_auto) {
       n = choose_decode_ctas(keys * (float)(a.Hkv * a.D * 4), pairs * (float)(4 * a.D * a.Hq),
                              n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq), a.decode_ctas,

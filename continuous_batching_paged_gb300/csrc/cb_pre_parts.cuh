@@ -22,7 +22,7 @@ __device__ __forceinline__ int pre_idle_index(int bx, int hg, int n, int grid) {
   const bool pairs = ((n | grid) & 1) == 0;
   const int units = pairs ? grid / 2 : grid, wanted = pairs ? n / 2 : n;
   const int u = pairs ? bx >> 1 : bx;  // (unit 0 always works)
-  const int rank = u - ((int)((long long)(u - 1) * wanted / units) + 1);
+  const int rank = u - ((u - 1) * wanted / units + 1);
   return hg * (grid - n) + (pairs ? 2 * rank + (bx & 1) : rank);
 }
 
