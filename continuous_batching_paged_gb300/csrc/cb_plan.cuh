@@ -344,34 +344,36 @@ __device__ __forceinline__ int pre_cta_most(int cost, int Hkv, int min_steps) {
 }
 
 // Decode CTAs per head group where prefixes are computed apart; the other SMs are the prefixes'.
-// Called by one full warp.  Model, fitted to GB300 measurements over all n of 15 batches (8 to 256
-// sequences, prefixes of 1k to 64k keys, 8 and 1 KV heads, head_dim 64 and 128), in us:
-//   decode = 3 + hypot(x, y): x the CTA's tiles (0.8 each at 64 KB, 0.54 at 8 KB; a record counts as
-//            one more), y the HBM time of all bytes, its share of which grows as x shrinks;
-//   prefix = 12 + 0.8 per cost unit of a CTA, and kPreChainUs per chain of a single sequence; chunk
-//            work follows on the same SMs.
-// The choice is the n with the least max(decode, prefix + chunk), plus a tenth of the other one so
-// that where one side is flat the other is not starved, plus 0.015 a CTA for the parts it adds.  It comes within 5 % of the best n on 13 of
-// the 15 batches, and within 12 % on the others.
+// Called by one full warp.  Model, in us:
+//   decode = 5.5 + hypot(x, y): x the CTA's tiles (0.62 each at 64 KB, 0.47 at 8 KB; a record counts
+//            as one more), y the HBM time of all bytes, its share of which grows as x shrinks;
+//   prefix = 11 + 0.73 per cost unit of a CTA, and 6.4 per chain of a single sequence; chunk work
+//            follows on the same SMs.
+// The choice is the n with the least max(decode, prefix + chunk), plus a sixth of the other one so
+// that where one side is flat the other is not starved, plus 0.029 a CTA for the parts it adds.  The
+// constants are those with the least loss over every even n of 18 batches timed on a GB300 (4 to 256
+// sequences, prefixes of 500 to 64k keys, 1, 2 and 8 KV heads, head_dim 64 and 128): the choice is
+// within 4 % of the best n on 17 of them, and within 6.5 % on the other.
 __device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes, float pre_bytes,
                                                    int cost, int chains, float chunk_flops, int items,
                                                    long long tiles, int records, int most) {
   const int lane = threadIdx.x & 31;
   const int hg = pre_head_groups(a.Hkv, a.G), sms = a.chunk_ctas;
   const int cap = (int)(tiles < a.decode_ctas ? tiles : a.decode_ctas);
-  const float x1 = pre_decode_tile_us(a) * ((float)tiles + (float)records);
-  const float y = (dec_bytes + pre_bytes) * (0.7e-6f / 6.2f);
-  const float pre_us = (0.8f * (float)cost + kPreChainUs * (float)chains) * (float)a.Hkv;
+  const float tile_us = 0.45f + 0.17f * (float)((a.Hkv < 8 ? a.Hkv : 8) * a.D) * (1.f / 1024.f);
+  const float x1 = tile_us * ((float)tiles + (float)records);
+  const float y = (dec_bytes + pre_bytes) * 0.16e-6f;
+  const float pre_us = (0.73f * (float)cost + 6.4f * (float)chains) * (float)a.Hkv;
   const float chunk_us = chunk_flops * (1.f / 6.4e6f);
   float best = 3.4e38f;
   int best_n = 1;
   for (int n = 2 * (lane + 1); n <= (cap > 2 ? cap : 2) && n * hg < sms; n += 64) {
     const int free = sms - n * hg;
-    const float x = __fdividef(x1, (float)n), d = 3.f + sqrt_approx(x * x + y * y);
-    const float p = 12.f + __fdividef(pre_us,
+    const float x = __fdividef(x1, (float)n), d = 5.5f + sqrt_approx(x * x + y * y);
+    const float p = 11.f + __fdividef(pre_us,
                                       (float)pre_cta_count(free, items, most, a.Hkv)) +
                     __fdividef(chunk_us, (float)free);
-    const float t = fmaxf(d, p) + 0.1f * fminf(d, p) + 0.015f * (float)n;
+    const float t = fmaxf(d, p) + 0.17f * fminf(d, p) + 0.029f * (float)n;
     if (t < best) {
       best = t;
       best_n = n;
