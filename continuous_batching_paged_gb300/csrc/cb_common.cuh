@@ -115,6 +115,14 @@ __host__ __device__ inline int pre_pack(int G) { return G <= 8 ? 8 / G : 1; }
 // Prefixes shorter than one K/V tile are left to each sequence's own pass.
 constexpr int kPreMinKeys = kChunkKeys;
 constexpr int kMaxPreCtas = 160;   // CTAs of the prefix pass (at most one per SM)
+// A chain's start and end cost 8 us besides its steps (rows and first tiles loaded, the part written),
+// and a CTA whose range holds the end of one chain and the start of another pays them twice: 128
+// sequences on 2000 keys (2 units under each of 8 KV heads) take 59.4 us on 48 CTAs, none of which
+// does, and 70.4 on 40; 40 sequences on 30k keys under one KV head 41.7 us on 96 and 50.4 on 98.  So a
+// lone group of few units gets CTAs in a multiple of kPrePeriod or less: as many for each unit, in
+// proportion to its steps' cost.  (Counting a start as 11 cost units instead, so that such a CTA gets
+// fewer steps, helped several groups by 2 % and cost the rest 1 us of planning.)
+constexpr int kPrePeriod = 32;
 // K/V tiles per CTA at least: more CTAs end sooner but leave the merge more parts per row (16 rows of
 // 500 keys: 20.8 us with at least 3, 17.9 with 1; 1024 rows of 2000 keys: 29.1 and 32.4).
 __host__ __device__ inline int pre_min_steps(long long rows) { return rows <= 512 ? 1 : 3; }

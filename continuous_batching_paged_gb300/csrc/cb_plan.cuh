@@ -188,15 +188,17 @@ struct PreSeq {
 // Sequences that are groups of their own (PreGroup; in batches of one round) follow the others in the
 // list.
 // lens: the groups' prefix lengths (in shared memory where all of them fit, else a.prefix_lens).
+// period: CTAs per KV head that give each unit of a lone group a whole number of them (else 1).
 __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], int32_t* cnt,
                                              int32_t* first, int32_t* map, const int32_t* lens,
-                                             PreSeq& mine) {
+                                             PreSeq& mine, int& period) {
   const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack);
   PreGroup* groups = reinterpret_cast<PreGroup*>(a.ws + PL.group);
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D, a.pack).header);
   const int tid = threadIdx.x;
   const long long max_kv = (long long)a.max_blocks * a.bs;
   __shared__ unsigned long long s_total, s_units;
+  __shared__ int s_period;
   if (tid == 0) s_total = s_units = 0;
   for (int g = tid; g < a.NG; g += kPrePlanThreads) {
     cnt[g] = 0;
@@ -261,12 +263,18 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
              (my_q <= kPreMaxQ || (few_chunks && my_ctx >= my_q))) {
     own_nt = pre_tiles(0, mine.kv);
   }
-  const int own_cost = own_nt > 0 ? (int)min((long long)kPreMaxCost + 1,
-                                             pre_shape(my_q, own_nt, a.G).per) : 0;
+  auto cost = [&](int n, int nt) {
+    const PreShape sh = pre_shape(n, nt, a.G);
+    // (of use where one thread has the only group)
+    s_period = sh.full == 0 ? 1 : sh.units > sh.full ? kPreCost2 * sh.full + kPreCost1 : sh.full;
+    return sh.per;
+  };
+  const int own_cost =
+      own_nt > 0 ? (int)min((long long)kPreMaxCost + 1, cost(my_q, own_nt)) : 0;
   unsigned long long total = own_cost;
   for (int g = tid; g < a.NG; g += kPrePlanThreads) {
     const int n = shared_tokens(g, lens[g]);
-    if (n > 0) total += (unsigned long long)pre_shape(n, pre_tiles(0, lens[g]), a.G).per;
+    if (n > 0) total += (unsigned long long)cost(n, pre_tiles(0, lens[g]));
   }
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if ((tid & 31) == 0 && total > 0) atomicAdd(&s_total, total);
@@ -318,6 +326,7 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
       for (int k = 0; k < 4; ++k) carry[k] += tot[k];
     }
   }
+  period = carry[0] == 1 ? s_period : 1;
   if (tid == 0) {
     hdr->pre_own = n_own;
     hdr->pre_groups = carry[0];
@@ -330,12 +339,13 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
 }
 
 // Prefix CTAs where `free` SMs are left to them and to `items` chunk items (up to a third of them for
-// those, an SM per item: an item is mostly latency): as many for each KV head (PreGroup), no more
-// than the work is worth (`most`).
-__device__ __forceinline__ int pre_cta_count(int free, int items, int most, int Hkv) {
+// those, an SM per item: an item is mostly latency): as many for each KV head (PreGroup), where there
+// are enough a multiple of `per` (Hkv x plan_prefixes' period), no more than the work is worth (`most`).
+__device__ __forceinline__ int pre_cta_count(int free, int items, int most, int Hkv, int per) {
   free -= items < free / 3 ? items : free / 3;
   int np = free < most ? free : most;
-  if (np > Hkv) np -= np % Hkv;
+  const int of = np > per ? per : Hkv;
+  if (np > of) np -= np % of;
   return np < 1 ? 1 : np;
 }
 __device__ __forceinline__ int pre_cta_most(int cost, int Hkv, int min_steps) {
@@ -345,35 +355,34 @@ __device__ __forceinline__ int pre_cta_most(int cost, int Hkv, int min_steps) {
 
 // Decode CTAs per head group where prefixes are computed apart; the other SMs are the prefixes'.
 // Called by one full warp.  Model, in us:
-//   decode = 5.5 + hypot(x, y): x the CTA's tiles (0.62 each at 64 KB, 0.47 at 8 KB; a record counts
-//            as one more), y the HBM time of all bytes, its share of which grows as x shrinks;
-//   prefix = 11 + 0.73 per cost unit of a CTA, and 6.4 per chain of a single sequence; chunk work
+//   decode = 4.8 + hypot(x, y): x the CTA's tiles (1.17 each at 64 KB, 0.86 at 8 KB; a record counts
+//            as one more), y a share of the HBM time of all bytes;
+//   prefix = 12 + 1.1 per cost unit of a CTA, and 3.5 per chain of a single sequence; chunk work
 //            follows on the same SMs.
-// The choice is the n with the least max(decode, prefix + chunk), plus a sixth of the other one so
-// that where one side is flat the other is not starved, plus 0.029 a CTA for the parts it adds.  The
-// constants are those with the least loss over every even n of 18 batches timed on a GB300 (4 to 256
-// sequences, prefixes of 500 to 64k keys, 1, 2 and 8 KV heads, head_dim 64 and 128): the choice is
-// within 4 % of the best n on 17 of them, and within 6.5 % on the other.
+// The choice is the n with the least max(decode, prefix + chunk), plus a little of the other one and
+// 0.019 a CTA for the parts it adds.  The constants are those with the least loss over every even n of
+// 18 batches timed on a GB300 (4 to 256 sequences, prefixes of 500 to 64k keys, 1, 2 and 8 KV heads,
+// head_dim 64 and 128): the choice is within 3.5 % of the best n on 16 of them, and within 6 % on all.
 __device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes, float pre_bytes,
-                                                   int cost, int chains, float chunk_flops, int items,
-                                                   long long tiles, int records, int most) {
+                                                   int cost, int chains, int per, float chunk_flops,
+                                                   int items, long long tiles, int records, int most) {
   const int lane = threadIdx.x & 31;
   const int hg = pre_head_groups(a.Hkv, a.G), sms = a.chunk_ctas;
   const int cap = (int)(tiles < a.decode_ctas ? tiles : a.decode_ctas);
-  const float tile_us = 0.45f + 0.17f * (float)((a.Hkv < 8 ? a.Hkv : 8) * a.D) * (1.f / 1024.f);
+  const float tile_us = 0.82f + 0.35f * (float)((a.Hkv < 8 ? a.Hkv : 8) * a.D) * (1.f / 1024.f);
   const float x1 = tile_us * ((float)tiles + (float)records);
-  const float y = (dec_bytes + pre_bytes) * 0.16e-6f;
-  const float pre_us = (0.73f * (float)cost + 6.4f * (float)chains) * (float)a.Hkv;
+  const float y = (dec_bytes + pre_bytes) * 0.022e-6f;
+  const float pre_us = (1.1f * (float)cost + 3.5f * (float)chains) * (float)a.Hkv;
   const float chunk_us = chunk_flops * (1.f / 6.4e6f);
   float best = 3.4e38f;
   int best_n = 1;
   for (int n = 2 * (lane + 1); n <= (cap > 2 ? cap : 2) && n * hg < sms; n += 64) {
     const int free = sms - n * hg;
-    const float x = __fdividef(x1, (float)n), d = 5.5f + sqrt_approx(x * x + y * y);
-    const float p = 11.f + __fdividef(pre_us,
-                                      (float)pre_cta_count(free, items, most, a.Hkv)) +
+    const float x = __fdividef(x1, (float)n), d = 4.8f + sqrt_approx(x * x + y * y);
+    const float p = 12.f + __fdividef(pre_us,
+                                      (float)pre_cta_count(free, items, most, a.Hkv, per)) +
                     __fdividef(chunk_us, (float)free);
-    const float t = fmaxf(d, p) + 0.17f * fminf(d, p) + 0.029f * (float)n;
+    const float t = fmaxf(d, p) + 0.018f * fminf(d, p) + 0.019f * (float)n;
     if (t < best) {
       best = t;
       best_n = n;
@@ -421,7 +430,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
 
   float my_keys = 0.f, my_pairs = 0.f;  // work estimates for the decode / chunk balance
   // shared prefixes: their work per KV head, and per group number cnt, first member and map
-  int pre_cost = 0;
+  int pre_cost = 0, period = 1;
   const PreLayout PL = kPre ? pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack) : PreLayout{};
   const bool few = a.NG <= kPlanSmemGroups;
   int32_t* grp_cnt = few ? s_groups : reinterpret_cast<int32_t*>(a.ws + PL.cnt);
@@ -432,7 +441,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   if constexpr (kPre) {
     if (few)  // (the function's first barrier follows)
       for (int g = tid; g < a.NG; g += NT) s_groups[3 * kPlanSmemGroups + g] = a.prefix_lens[g];
-    pre_cost = plan_prefixes(a, sw, grp_cnt, grp_first, grp_map, grp_lens, mine);
+    pre_cost = plan_prefixes(a, sw, grp_cnt, grp_first, grp_map, grp_lens, mine, period);
   }
   // kPre: chunks that are groups of their own: (first token, tokens, first list entry, K/V tiles), cost0
   __shared__ int s_chunks;
@@ -665,17 +674,18 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     }
     int n = (int)(ntiles < a.decode_ctas ? (ntiles > 0 ? ntiles : 1) : a.decode_ctas);
     if (kPre && pre_cost > 0) {
+      const int per = a.Hkv * period <= kPrePeriod ? a.Hkv * period : a.Hkv;
       const float row = (float)(a.Hkv * a.D * 4);  // bytes of a key and its value
       const int items = n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq);
       const int most = pre_cta_most(pre_cost, a.Hkv, pre_min_steps((long long)hdr->pre_tokens * a.Hq));
       if (a.decode_auto)
         n = choose_prefix_split(a, keys * row, (float)hdr->pre_keys * row, pre_cost,
-                                hdr->pre_own,
+                                hdr->pre_own, per,
                                 pairs * (float)(4 * a.D * a.Hq), items, ntiles, n_dec, most);
       // the decode CTAs without work; where a given number leaves none, an eighth of the chunk CTAs
       const int idle = pre_idle_count(pre_head_groups(a.Hkv, a.G), n, a.decode_ctas);
       if (tid == 0)
-        hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, items, most, a.Hkv);
+        hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, items, most, a.Hkv, per);
     } else if (a.decode_auto) {
       n = choose_decode_ctas(keys * (float)(a.Hkv * a.D * 4), pairs * (float)(4 * a.D * a.Hq),
                              n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq), a.decode_ctas,
