@@ -119,8 +119,8 @@ constexpr int kMaxPreCtas = 160;   // CTAs of the prefix pass (at most one per S
 // and a CTA whose range holds the end of one chain and the start of another pays them twice: 128
 // sequences on 2000 keys (2 units under each of 8 KV heads) take 59.4 us on 48 CTAs, none of which
 // does, and 70.4 on 40; 40 sequences on 30k keys under one KV head 41.7 us on 96 and 50.4 on 98.  So a
-// lone group of few units gets CTAs in a multiple of kPrePeriod or less: as many for each unit, in
-// proportion to its steps' cost.  (Counting a start as 11 cost units instead, so that such a CTA gets
+// lone group gets a multiple of the CTAs that make up whole ones for every unit, in proportion to its
+// steps' cost, where that is kPrePeriod or less.  (Counting a start as 11 cost units instead, so that such a CTA gets
 // fewer steps, helped several groups by 2 % and cost the rest 1 us of planning.)
 constexpr int kPrePeriod = 32;
 // K/V tiles per CTA at least: more CTAs end sooner but leave the merge more parts per row (16 rows of
