@@ -178,6 +178,32 @@ struct PreSeq {
   int own_first;    // and that group's first key (0: it is the sequence's only chain)
 };
 
+// Places of a round's members among their groups' tokens, in the order of the sequences, so that a
+// token's tile, and with it the rounding of its parts, is the same on every call.  Returns the group's
+// tokens listed before this thread's q (<= kPreMaxQ), and adds the round's to cnt; group -1: no member.
+// Warps take turns, lanes of a group count the tokens of the lanes before them.  All threads call it.
+__device__ __forceinline__ int group_place(int32_t* cnt, int group, int q, int warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned peers = __match_any_sync(0xffffffffu, group), below = peers & ((1u << lane) - 1);
+  int before = 0, total = 0;
+#pragma unroll
+  for (int b = 0; (1 << b) <= kPreMaxQ; ++b) {
+    const unsigned bit = __ballot_sync(0xffffffffu, (q >> b) & 1);
+    before += __popc(bit & below) << b;
+    total += __popc(bit & peers) << b;
+  }
+  int at = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (warp == w) {
+      if (group >= 0) at = cnt[group];
+      __syncwarp();
+      if (group >= 0 && below == 0) cnt[group] = at + total;
+    }
+    __syncthreads();
+  }
+  return at + before;
+}
+
 // With shared prefixes: which groups' prefixes are computed once.  Fills the group list, and per
 // group number map (index in the list, -1: every member's own pass does it all) and cnt (the tokens
 // listed so far).  Returns the work of the prefixes per KV head in cost units (0: no group takes
@@ -302,8 +328,8 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
   int n_own = 0;  // sequences that are groups of their own
   if (!too_much && one_round) {
     __syncthreads();  // the groups and map are written, cnt is 0
+    mine.at = group_place(cnt, my_member ? mine.group : -1, my_q, (a.S + 31) / 32);
     if (my_member) {
-      mine.at = atomicAdd(&cnt[mine.group], my_q);
       mine.list = groups[map[mine.group]].tok0 + mine.at;
       mine.own_first = mine.keys;
     }
@@ -453,7 +479,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   for (int base = 0; base < a.S; base += NT) {
     const int s = base + tid;
     int v[4] = {0, 0, 0, 0};
-    int tok = 0, kv = 0;
+    int tok = 0, kv = 0, q_len = 0;
     int grp = -1, keys = 0;  // kPre: the group that computes this sequence's prefix, its length
     if (s < a.S) {
       int c0, c1;
@@ -466,7 +492,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
         c1 = a.cu_seqlens_q[s + 1];
         kv = a.kv_lens[s];
       }
-      const int q_len = c1 - c0;
+      q_len = c1 - c0;
       tok = c0;
       if (s == 0 && c0 != 0) report(a.err, kErrOutOfRange);  // cu_seqlens_q[0] must be 0
       const bool ok = c0 >= 0 && c1 <= a.T && q_len >= 0 && kv >= q_len && kv <= max_kv;
@@ -511,8 +537,13 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     }
     int ex[4], tot[4];
     block_scan4<NT>(v, ex, tot, sw);
+    int at = mine.at;
+    if constexpr (kPre) {
+      if (a.S > NT && pre_cost > 0)  // (else plan_prefixes has found them)
+        at = group_place(grp_cnt, v[0] ? grp : -1, q_len, (min(a.S - base, NT) + 31) / 32);
+    }
     if (kPre && base == 0 && mine.chain >= 0) {
-      const int q_len = mine.c1 - mine.c0, own_nt = pre_tiles(mine.own_first, mine.kv);
+      const int own_nt = pre_tiles(mine.own_first, mine.kv);
       if (q_len > kPreMaxQ) {  // a chunk's list entries are written below, by all threads
         const int x = atomicAdd(&s_chunks, 1);  // (fewer than kPreChunkItems)
         s_chunk[x][0] = make_int4(tok, q_len, mine.list, own_nt);
@@ -533,12 +564,8 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
         }
       }
     } else if (kPre && grp >= 0 && v[0]) {
-      // The tokens' places in the group's list come in any order: a row's result does not depend
-      // on the tile it is computed in.
-      const int q_len = base == 0 ? mine.c1 - mine.c0 : a.cu_seqlens_q[s + 1] - tok;
       const int first = keys / kDecodeTileKeys * kDecodeTileKeys;
       const PreGroup group = reinterpret_cast<const PreGroup*>(a.ws + PL.group)[grp_map[grp]];
-      const int at = base == 0 && mine.list >= 0 ? mine.at : atomicAdd(&grp_cnt[grp], q_len);
       int tile = carry[1] + ex[1], i = carry[0] + ex[0];
       for (int j = 0; j < q_len; j += a.pack, ++i) {
         const int n = min(a.pack, q_len - j), n_keys = kv - (q_len - j - n);

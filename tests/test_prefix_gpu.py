@@ -465,3 +465,73 @@ def test_more_sequences_than_the_planner_sees_at_once(cuda_lib):
     grp = [int(x) for x in rng.integers(-1, 3, 300)]
     check(grouped_batch(q, own, grp, [200, 150, 400], 4, 1, 64, 16, seed=950))
     check(grouped_batch(q[:256], own[:256], grp[:256], [200, 150, 400], 4, 1, 64, 16, seed=951))
+
+
+@pytest.mark.parametrize("n", [40, 200, 600])
+def test_tiles_of_a_group_are_the_same_on_every_call(cuda_lib, n):
+    # 2 to 19 tiles of a group: were a token now in a unit of two tiles, now in the last one, its
+    # parts would be rounded differently
+    rng = np.random.default_rng(n)
+    q = [int(x) for x in rng.integers(1, 4, n)]
+    own = [k + int(x) for k, x in zip(q, rng.integers(0, 20, n))]
+    b = grouped_batch(q, own, [int(x < 0.8) for x in rng.random(n)], [150, 900], 8, 2, 64, 16, seed=960)
+    d, out, lse = check(b)
+    busy = torch.randn(4096, 4096, device="cuda")
+    for i in range(12):
+        if i % 2:
+            busy @ busy  # (another neighbour on the stream)
+        out2, lse2 = d.attend()
+        assert torch.equal(out.view(torch.int16), out2.view(torch.int16))
+        assert torch.equal(lse, lse2)
+
+
+def test_pages_past_32_bit_offsets(cuda_lib):
+    # the last pages of pools of 2^32 elements and more: same bits as in a small pool
+    b = grouped_batch([1, 3, 1, 1, 40, 1], [30, 9, 200, 1, 45, 17], [0, 0, 0, -1, 0, 0], [300], 8, 8, 128,
+                      64, seed=961)
+    d = Dev(b)
+    out, lse = d.attend()
+    n = d.kp.shape[0]
+    far = 2 ** 32 // (64 * 8 * 128) + n
+    pools = []
+    for near in (d.kp, d.vp):
+        pool = torch.empty((far, 64, 8, 128), dtype=torch.bfloat16, device="cuda")
+        pool[far - n:] = near
+        pools.append(pool)
+    table = torch.where(d.table >= 0, d.table + (far - n), d.table)
+    out2, lse2 = cb.shared_prefix_attention(d.q, *pools, table, d.cu, d.kv, 64, b["scale"], d.group,
+                                            d.prefix, lse=True)
+    assert cb.get_device_error() == cb.CB_OK
+    assert torch.equal(out.view(torch.int16), out2.view(torch.int16)) and torch.equal(lse, lse2)
+    # and the rotary append into them
+    kn = torch.randn(d.q.shape[0], 8, 128, device="cuda").bfloat16()
+    cs = torch.from_numpy(orope.table(int(b["kv"].max()), 128)).cuda()
+    rot = cb.rope_append(d.q, kn, kn.flip(0), d.kp, d.vp, d.table, d.cu, d.kv, 64, cs)
+    rot2 = cb.rope_append(d.q, kn, kn.flip(0), *pools, table, d.cu, d.kv, 64, cs)
+    assert cb.get_device_error() == cb.CB_OK
+    assert torch.equal(rot.view(torch.int16), rot2.view(torch.int16))
+    for near, pool in zip((d.kp, d.vp), pools):
+        assert torch.equal(near.view(torch.int16), pool[far - n:].view(torch.int16))
+
+
+def test_steps_in_a_row_and_the_same_sequence_twice(cuda_lib):
+    # layer after layer without a wait between them, into the same workspace: each call starts early
+    # behind the one before; and two entries of the batch that are the same sequence
+    b = grouped_batch([1] * 30, [1 + 7 * i for i in range(30)], [i % 3 - 1 for i in range(30)],
+                      [400, 333], 8, 2, 128, 16, seed=962)
+    b["table"][5], b["kv"][5] = b["table"][2], b["kv"][2]  # (both of group 1)
+    b["q"][5] = b["q"][2]
+    d = Dev(b)
+    ws = d.workspace()
+    q = [d.q, d.q.flip(0).contiguous()]
+    alone = []
+    for x in q:
+        alone.append(cb.shared_prefix_attention(x, d.kp, d.vp, d.table, d.cu, d.kv, 16, b["scale"], d.group,
+                                                d.prefix))
+        torch.cuda.synchronize()
+    assert_matches(alone[0], None, b)
+    outs = [cb.shared_prefix_attention(q[i % 2], d.kp, d.vp, d.table, d.cu, d.kv, 16, b["scale"], d.group,
+                                       d.prefix, workspace=ws) for i in range(40)]
+    for i, o in enumerate(outs):
+        assert torch.equal(o.view(torch.int16), alone[i % 2].view(torch.int16)), i
+    assert cb.get_device_error() == cb.CB_OK
