@@ -170,6 +170,12 @@ cb::AppendArgs append_args(const void* k_new, const void* v_new, void* k_pages, 
   return a;
 }
 
+// Do two ranges of bf16 elements overlap?
+bool overlap(const void* a, long long na, const void* b, long long nb) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  return x < y + 2 * nb && y < x + 2 * na;
+}
+
 // Checks of cb_rope and of the tensors it applies to (non-empty batch), and the kernel's arguments.
 cb_status rope_args(const void* q, void* q_out, const cb_rope* rope, const cb::AppendArgs& ap,
                     int Hq, cb::RopeArgs* out) {
@@ -204,12 +210,13 @@ cb_status rope_args(const void* q, void* q_out, const cb_rope* rope, const cb::A
       r.k_stride % 8 != 0 || r.v_stride < row_kv || r.v_stride % 8 != 0)
     return fail(CB_ERR_INVALID_ARG,
                 "token strides must be multiples of 8 elements and at least one row");
-  if (q != nullptr && !(q == q_out && (r.q_stride == row_q || ap.T == 1))) {
-    const char* q0 = static_cast<const char*>(q);
-    const char* o0 = static_cast<const char*>(q_out);
-    if (q0 < o0 + 2 * row_q * ap.T && o0 < q0 + 2 * (r.q_stride * (ap.T - 1) + row_q))
-      return fail(CB_ERR_INVALID_ARG, "q_out overlaps q (allowed: q_out == q, q contiguous)");
-  }
+  const long long last = ap.T - 1, n_q = row_q * ap.T;
+  if (q != nullptr && !(q == q_out && (r.q_stride == row_q || last == 0)) &&
+      overlap(q, r.q_stride * last + row_q, q_out, n_q))
+    return fail(CB_ERR_INVALID_ARG, "q_out overlaps q (allowed: q_out == q, q contiguous)");
+  if (q != nullptr && (overlap(ap.k_new, r.k_stride * last + row_kv, q_out, n_q) ||
+                       overlap(ap.v_new, r.v_stride * last + row_kv, q_out, n_q)))
+    return fail(CB_ERR_INVALID_ARG, "q_out overlaps k_new or v_new");
   *out = r;
   return CB_OK;
 }
@@ -365,6 +372,9 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   if (Hkv > dec_heads && Hkv % dec_heads != 0)
     return fail(CB_ERR_UNSUPPORTED, "num_kv_heads > %d must be a multiple of %d", dec_heads,
                 dec_heads);
+  const long long n_q = (long long)dims->num_tokens * Hq * dims->head_dim;
+  if ((rope != nullptr || prefix != nullptr) && overlap(q, n_q, out, n_q))
+    return fail(CB_ERR_INVALID_ARG, "out overlaps the queries that the attention reads");
   DeviceState* ds = nullptr;
   st = device_state(&ds);
   if (st != CB_OK) return st;

@@ -113,7 +113,8 @@ cb_status cb_kv_append(const void* k_new, const void* v_new, void* k_pages, void
  *                    q_stride / k_stride / v_stride elements apart, so that the three may be
  *                    views of one projection's output.  q and q_out NULL: keys and values only.
  *   q_out            bf16 [T, Hq, D] contiguous.  May be q itself where q is contiguous too;
- *                    otherwise the two must not overlap (CB_ERR_INVALID_ARG).
+ *                    otherwise the two must not overlap, nor q_out and k_new or v_new
+ *                    (CB_ERR_INVALID_ARG).
  * The other arguments, the padding rows and the errors are those of cb_kv_append; in addition a
  * position >= max_positions is a device error (CB_ERR_OUT_OF_RANGE).  A token with a device error
  * is skipped: neither its cache slot nor its row of q_out is written.
@@ -258,6 +259,9 @@ cb_status cb_append_attention(const void* k_new, const void* v_new, void* k_page
  * prefix: the groups, see below; with num_groups == 0 the call is cb_ragged_paged_attention_ex.
  * workspace: at least cb_prefix_workspace_size(dims, num_groups) bytes.
  * options: as in cb_ragged_paged_attention_ex, but window must be 0 (CB_ERR_UNSUPPORTED).
+ * out must not overlap q (CB_ERR_INVALID_ARG).
+ * Three launches: the planner, the attention kernel (whose decode CTAs without work do the prefixes),
+ * and a merge of the partial results, which the last phase event follows.
  * Device errors: those of cb_ragged_paged_attention; also, for a sequence with query tokens, a
  * group outside [-1, num_groups) and a prefix length below 0 or above the sequence's prior context
  * kv_len - q_len (the prefix must be visible to its first query): CB_ERR_OUT_OF_RANGE.
@@ -289,10 +293,10 @@ cb_status cb_shared_prefix_attention(const void* q, const void* k_pages, const v
 /*
  * cb_rope_append_attention -- one layer's attention step in one call: cb_rope_append, then
  * cb_shared_prefix_attention on the rotated queries (with prefix NULL,
- * cb_ragged_paged_attention_ex), with the same arguments and the same results (bit for bit).  Two
- * launches: the rotary append with the attention planner beside it, and the attention kernel.
- * q_out (required) receives the rotated queries and is what the attention reads; out must not
- * overlap it.  Phase events as in cb_append_attention.
+ * cb_ragged_paged_attention_ex), with the same arguments and the same results (bit for bit).  The
+ * rotary append and the attention planner share a launch; the attention kernel and, with groups, the
+ * merge follow.  q_out (required) receives the rotated queries and is what the attention reads; out
+ * must not overlap it (CB_ERR_INVALID_ARG).  Phase events as in cb_append_attention.
  */
 cb_status cb_rope_append_attention(const void* q, const void* k_new, const void* v_new, void* q_out,
                                    void* k_pages, void* v_pages, const int32_t* block_table,

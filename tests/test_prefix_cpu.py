@@ -112,3 +112,14 @@ def test_binding_refuses_host_tensors():
                                  prefix_group=grp[0], prefix_lens=grp[1])
     with pytest.raises(ValueError, match="bfloat16"):
         cb.shared_prefix_attention(q.float(), kp, kp, *meta, 16, 0.125, *grp)
+
+
+@pytest.mark.parametrize("out", [P, P + 16, P + 35 * 512 - 16, P - 35 * 512 + 16])
+def test_output_must_not_overlap_the_queries(lib, out):
+    assert _attend(lib, out=out) == cb.CB_ERR_INVALID_ARG
+    assert b"overlaps the queries" in lib.cb_last_error_message()
+    r = cb.CbRope(256, 128, 64, 0, 0, 0, 0, 0)
+    assert lib.cb_rope_append_attention(QO, QO + (1 << 24), QO, P, P, P, 256, 256, 256, 16, 0.1,
+                                        ctypes.byref(r), None, out, None, P, 1 << 40,
+                                        ctypes.byref(_dims()), None, None) == cb.CB_ERR_INVALID_ARG
+    assert b"overlaps the queries" in lib.cb_last_error_message()

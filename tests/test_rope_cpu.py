@@ -104,3 +104,10 @@ def test_rows_of_views():
         cb._explain_rows("q", _FakeCuda(rows))
     for rows in (qkv.transpose(0, 1), qkv[:, ::2], qkv[:, :, ::2]):
         assert not cb._rows_ok(*rows.shape, rows.stride()) or rows.shape[0] == 0
+
+
+@pytest.mark.parametrize("kw", [dict(k=OUT), dict(v=OUT - 16), dict(k=OUT + 35 * 512 - 16),
+                                dict(v=OUT - 34 * 2048 - 16, v_stride=1024)])
+def test_rotated_queries_must_not_overlap_the_new_rows(lib, kw):
+    assert _status(lib, **kw) == cb.CB_ERR_INVALID_ARG
+    assert b"overlaps k_new or v_new" in lib.cb_last_error_message()
