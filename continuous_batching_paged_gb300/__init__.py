@@ -302,8 +302,9 @@ def _native():
 
 def _rows_ok(T, H, D, strides) -> bool:
     """Whether a [T, H, D] tensor of these strides has contiguous token rows (as a view of a wider
-    projection's output has)."""
-    return T == 0 or (strides[2] == 1 and (strides[1] == D or H == 1))
+    projection's output has) that do not overlap (as a broadcast row's do)."""
+    return T == 0 or (strides[2] == 1 and (strides[1] == D or H == 1)
+                      and (T == 1 or strides[0] >= H * D))
 
 
 def _explain_rows(name, t) -> None:
@@ -311,7 +312,7 @@ def _explain_rows(name, t) -> None:
     _require(t.dtype == torch.bfloat16, f"{name} must be bfloat16")
     _require(t.is_cuda, f"{name} must be a CUDA tensor")
     _require(t.dim() == 3, f"{name} must have 3 dimensions")
-    _require(_rows_ok(*t.shape, t.stride()), f"{name} must have contiguous token rows")
+    _require(_rows_ok(*t.shape, t.stride()), f"{name} must have contiguous token rows that do not overlap")
 
 
 def _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,

@@ -29,13 +29,15 @@ bool plain(const at::Tensor* t, at::ScalarType type, int64_t dim, int dev) {
          t->get_device() == dev && t->is_contiguous();
 }
 
-// bf16 [T, H, D] with contiguous token rows (a view of a wider projection's output, for instance).
+// bf16 [T, H, D] with contiguous token rows (a view of a wider projection's output, for instance)
+// that do not overlap (as a broadcast row's would).
 bool rows(const at::Tensor* t, int dev) {
   if (t == nullptr || t->scalar_type() != at::kBFloat16 || t->dim() != 3 || !t->is_cuda() ||
       t->get_device() != dev)
     return false;
   return t->size(0) == 0 ||
-         (t->stride(2) == 1 && (t->stride(1) == t->size(2) || t->size(1) == 1));
+         (t->stride(2) == 1 && (t->stride(1) == t->size(2) || t->size(1) == 1) &&
+          (t->size(0) == 1 || t->stride(0) >= t->size(1) * t->size(2)));
 }
 
 // The row stride that the library is given: 0 (contiguous) for one token, whatever its stride says.

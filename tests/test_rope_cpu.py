@@ -111,3 +111,11 @@ def test_rows_of_views():
 def test_rotated_queries_must_not_overlap_the_new_rows(lib, kw):
     assert _status(lib, **kw) == cb.CB_ERR_INVALID_ARG
     assert b"overlaps k_new or v_new" in lib.cb_last_error_message()
+
+
+def test_binding_refuses_broadcast_rows():
+    # a stride of 0 is the library's word for contiguous rows: a broadcast row would be read past its end
+    row = torch.zeros(1, 2, 64)
+    assert not cb._rows_ok(*row.expand(5, 2, 64).shape, row.expand(5, 2, 64).stride())
+    assert cb._rows_ok(*row.expand(1, 2, 64).shape, row.expand(1, 2, 64).stride())
+    assert not cb._rows_ok(5, 2, 64, (64, 64, 1))

@@ -217,3 +217,20 @@ def test_captured_and_replayed(cuda_lib):
     assert cb.get_device_error() == cb.CB_OK
     pos = orope.positions_of(b2.cu_seqlens_q, b2.kv_lens)
     assert np.array_equal(bits_of(q_out), rotate_fp32(b2.q, pos, cs_np, False))
+
+
+@pytest.mark.parametrize("which", ["q", "k_new", "v_new"])
+def test_broadcast_rows_are_refused(cuda_lib, which):
+    b = workloads.build_batch(*RAGGED, 8, 4, 128, 16, seed=770)
+    db = DeviceBatch(b)
+    rows = dict(q=db.q, k_new=db.k_new, v_new=db.v_new)
+    rows[which] = rows[which][:1].expand_as(rows[which])
+    cs = torch.from_numpy(orope.table(600, 128)).cuda()
+    where = (db.k_pages, db.v_pages, db.block_table, db.cu, db.kv_lens, b.block_size)
+    before = bits_of(db.k_pages)
+    with pytest.raises(ValueError, match=f"{which} must have contiguous token rows"):
+        cb.rope_append(*rows.values(), *where, cs)
+    with pytest.raises(ValueError, match=f"{which} must have contiguous token rows"):
+        cb.rope_append_attention(*rows.values(), *where, b.scale, cs)
+    assert cb.get_device_error() == cb.CB_OK
+    assert np.array_equal(bits_of(db.k_pages), before)
