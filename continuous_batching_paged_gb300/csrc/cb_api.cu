@@ -427,10 +427,14 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   if ((st = encode_map(&maps.k_chunk, k_pages, D, Hkv, rows, D * 2, D * 2 * Hkv, 1, a.KBp)) != CB_OK) return st;
   if ((st = encode_map(&maps.v_chunk, v_pages, D, Hkv, rows, D * 2, D * 2 * Hkv, 1, a.KBp)) != CB_OK) return st;
   if ((st = encode_map(&maps.q, q, D, Hq, (uint64_t)a.T, D * 2, D * 2 * Hq, 1, 128)) != CB_OK) return st;
-  CUtensorMap q_tok;  // one token's query heads of one KV head
-  if (NG > 0 && (st = encode_map(&q_tok, q, D, Hq, (uint64_t)a.T, D * 2, D * 2 * Hq, G, 1)) != CB_OK) return st;
+  cb::PrefixMaps pm;
+  if (NG > 0) {
+    const uint64_t T = (uint64_t)a.T, tok = D * 2 * Hq;
+    if ((st = encode_map(&pm.q_tok, q, D, Hq, T, D * 2, tok, G, 1)) != CB_OK) return st;
+    if ((st = encode_map(&pm.q_run, q, D, Hq, T, D * 2, tok, G, cb::pre_tile_tokens(G))) != CB_OK) return st;
+  }
   auto launch_pass = [&](const cb::AttnArgs& x, cudaStream_t on) {
-    return NG > 0 ? cb::launch_prefix_attention(x, maps, q_tok, on) : cb::launch_attention(x, maps, on);
+    return NG > 0 ? cb::launch_prefix_attention(x, maps, pm, on) : cb::launch_attention(x, maps, on);
   };
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);

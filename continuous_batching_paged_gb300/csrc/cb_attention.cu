@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                      const __grid_constant__ CUtensorMap kmap_chunk,
                      const __grid_constant__ CUtensorMap vmap_chunk) {
   extern __shared__ uint8_t smem_raw[];
-  attention_cta<D, QS, kWin, false>(a, &qmap, nullptr, &kmap_dec, &vmap_dec, &kmap_chunk,
+  attention_cta<D, QS, kWin, false>(a, &qmap, nullptr, nullptr, &kmap_dec, &vmap_dec, &kmap_chunk,
                                     &vmap_chunk, smem_raw);
 }
 

@@ -20,11 +20,13 @@ struct AttnSmem {
   static constexpr int kTotal = kPre && PreSmem<D>::kTotal > kBoth ? PreSmem<D>::kTotal : kBoth;
 };
 
-// kPre: the batch's shared prefixes are computed once per group (cb_prefix.cu); qmap_tok is the
-// tensor map that gathers a group's query rows (unused otherwise).
+// kPre: the batch's shared prefixes are computed once per group (cb_prefix.cu); qmap_tok and
+// qmap_run are the tensor maps of a group's query rows, token by token and a tile of tokens (unused
+// otherwise).
 template <int D, int QS, bool kWin, bool kPre>
 __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorMap* qmap,
                                               const CUtensorMap* qmap_tok,
+                                              const CUtensorMap* qmap_run,
                                               const CUtensorMap* kmap_dec,
                                               const CUtensorMap* vmap_dec,
                                               const CUtensorMap* kmap_chunk,
@@ -46,7 +48,7 @@ __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorM
                       : pre_idle_count(pre_head_groups(a.Hkv, a.G), N, a.decode_ctas) + b -
                             a.decode_grid;
     if (c >= 0 && c < hdr->pre_ctas) {
-      prefix_cta<D>(a, qmap_tok, kmap_chunk, vmap_chunk, smem_raw, c);
+      prefix_cta<D>(a, qmap_tok, qmap_run, kmap_chunk, vmap_chunk, smem_raw, c);
       return;
     }
   }

@@ -113,11 +113,14 @@ struct AttnMaps {
 cudaError_t launch_rope_plan(RopeArgs r, const AttnArgs& a, int sm_count, cudaStream_t stream);
 // The attention kernel: a.decode_grid decode-role CTAs, then a.prefill_ctas chunk-role CTAs.
 cudaError_t launch_attention(const AttnArgs& a, const AttnMaps& maps, cudaStream_t stream);
-// The planner and the attention kernel for a batch with shared prefixes (a.NG > 0); q_tok: Q as boxes of one token's query
-// heads of one KV head.
+// The planner and the attention kernel for a batch with shared prefixes (a.NG > 0).  Q as boxes of the
+// query heads of one KV head: of one token, and of as many tokens as a tile of rows holds.
+struct PrefixMaps {
+  CUtensorMap q_tok, q_run;
+};
 cudaError_t launch_prefix_plan(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_attention(const AttnArgs& a, const AttnMaps& maps,
-                                    const CUtensorMap& q_tok, cudaStream_t stream);
+                                    const PrefixMaps& p, cudaStream_t stream);
 // After it: merges the parts of the shared prefixes' rows.
 cudaError_t launch_prefix_merge(const AttnArgs& a, int sm_count, cudaStream_t stream);
 

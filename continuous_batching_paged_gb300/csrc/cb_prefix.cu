@@ -34,17 +34,18 @@ template <int D, int QS>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     prefix_attention_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap qmap,
                             const __grid_constant__ CUtensorMap qmap_tok,
+                            const __grid_constant__ CUtensorMap qmap_run,
                             const __grid_constant__ CUtensorMap kmap_dec,
                             const __grid_constant__ CUtensorMap vmap_dec,
                             const __grid_constant__ CUtensorMap kmap_chunk,
                             const __grid_constant__ CUtensorMap vmap_chunk) {
   extern __shared__ uint8_t smem_raw[];
-  attention_cta<D, QS, false, true>(a, &qmap, &qmap_tok, &kmap_dec, &vmap_dec, &kmap_chunk,
-                                    &vmap_chunk, smem_raw);
+  attention_cta<D, QS, false, true>(a, &qmap, &qmap_tok, &qmap_run, &kmap_dec, &vmap_dec,
+                                    &kmap_chunk, &vmap_chunk, smem_raw);
 }
 
 template <int D, int QS>
-static cudaError_t launch_instance(const AttnArgs& a, const AttnMaps& m, const CUtensorMap& q_tok,
+static cudaError_t launch_instance(const AttnArgs& a, const AttnMaps& m, const PrefixMaps& p,
                                    cudaStream_t stream) {
   constexpr int kSmem = AttnSmem<D, QS, true>::kTotal;
   // a setting of the context, as for the attention kernel without prefixes
@@ -57,7 +58,8 @@ static cudaError_t launch_instance(const AttnArgs& a, const AttnMaps& m, const C
     configured_ctx = ctx;
   }
   return launch_dependent(prefix_attention_kernel<D, QS>, a.decode_grid + a.prefill_ctas, kAttnThreads,
-                          kSmem, stream, a, m.q, q_tok, m.k_dec, m.v_dec, m.k_chunk, m.v_chunk);
+                          kSmem, stream, a, m.q, p.q_tok, p.q_run, m.k_dec, m.v_dec, m.k_chunk,
+                          m.v_chunk);
 }
 
 // One warp per (query token, HP query heads of one KV head) of the shared prefixes:
@@ -247,13 +249,13 @@ cudaError_t launch_prefix_merge(const AttnArgs& a, int sm_count, cudaStream_t st
   return launch_dependent(kernel, (unsigned)blocks, kMergeThreads, 0, stream, a);
 }
 
-cudaError_t launch_prefix_attention(const AttnArgs& a, const AttnMaps& m, const CUtensorMap& q_tok,
+cudaError_t launch_prefix_attention(const AttnArgs& a, const AttnMaps& m, const PrefixMaps& p,
                                     cudaStream_t stream) {
   if (a.D == 128)
-    return a.G <= 8 ? launch_instance<128, 1>(a, m, q_tok, stream)
-                    : launch_instance<128, 2>(a, m, q_tok, stream);
-  return a.G <= 8 ? launch_instance<64, 1>(a, m, q_tok, stream)
-                  : launch_instance<64, 2>(a, m, q_tok, stream);
+    return a.G <= 8 ? launch_instance<128, 1>(a, m, p, stream)
+                    : launch_instance<128, 2>(a, m, p, stream);
+  return a.G <= 8 ? launch_instance<64, 1>(a, m, p, stream)
+                  : launch_instance<64, 2>(a, m, p, stream);
 }
 
 }  // namespace cb

@@ -47,8 +47,8 @@ static_assert(PreSmem<128>::kTotal <= 232448 && PreSmem<64>::kTotal <= 232448, "
 // CTA `c` < hdr->pre_ctas of the prefix role (all kPrefillThreads threads).
 template <int D>
 __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap* qmap,
-                                           const CUtensorMap* kmap, const CUtensorMap* vmap,
-                                           uint8_t* smem_raw, int c) {
+                                           const CUtensorMap* qmap_run, const CUtensorMap* kmap,
+                                           const CUtensorMap* vmap, uint8_t* smem_raw, int c) {
   using SM = PreSmem<D>;
   constexpr int NS = SM::kSlots;
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D, a.pack).header);
@@ -96,6 +96,7 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
     if (warp == 0) {
       // =================================================================== TMA producer
       if (lane == 0) {
+        tma_prefetch_desc(qmap_run);
         tma_prefetch_desc(qmap);
         tma_prefetch_desc(kmap);
         tma_prefetch_desc(vmap);
@@ -139,19 +140,38 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
         };
         int blk_next = entry(lane);
         // The part's query rows, behind its first K tile: their addresses are a load away, K's are here.
-        int q_tok[2];
+        // A tile's tokens are in ascending order.  Where they follow one another, as a batch of decodes
+        // does, one box per half of D takes the tile (and rows behind its last token, which nobody
+        // uses): token by token 2 x 32 tokens took 3.8 us, and K and V wait behind them, now 0.8.  For
+        // fewer than 8 tokens a box of a whole tile is not worth it.
+        int q_tok[2], q_last[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          q_tok[t] = lane < s.ntok[t] ? list[s.tok0 + t * pre_tile_tokens(a.G) + lane].token : 0;
+        for (int t = 0; t < 2; ++t) {
+          const PreToken* tok = list + s.tok0 + t * pre_tile_tokens(a.G);
+          q_tok[t] = lane < s.ntok[t] ? tok[lane].token : 0;
+          q_last[t] = s.ntok[t] >= 8 ? tok[s.ntok[t] - 1].token : 0;
+        }
         auto load_q = [&]() {
           wait(bar(SM::bQEmpty), (k & 1) ^ 1);
           if (!ok) return;
-          if (lane == 0)
-            mbar_arrive_expect_tx(bar(SM::bQFull),
-                                  (uint32_t)((s.ntok[0] + s.ntok[1]) * a.G * SM::kHalves * 128));
+          bool run[2];
+          int rows = 0;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int first = __shfl_sync(0xffffffffu, q_tok[t], 0);
+            run[t] = s.ntok[t] >= 8 && q_last[t] - first == s.ntok[t] - 1;
+            rows += (run[t] ? pre_tile_tokens(a.G) : s.ntok[t]) * a.G;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(SM::bQFull), (uint32_t)(rows * SM::kHalves * 128));
           __syncwarp();
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2; ++t) {
+            if (run[t]) {
+              if (lane < SM::kHalves)
+                tma_load_3d(sbase + t * SM::kTile + lane * SM::kHalf, qmap_run, bar(SM::bQFull), lane * 64,
+                            s.kvh * a.G, q_last[t] - (s.ntok[t] - 1));
+              continue;
+            }
             for (int i = lane; i < s.ntok[t]; i += 32) {
               const int tok =
                   i < 32 ? q_tok[t] : list[s.tok0 + t * pre_tile_tokens(a.G) + i].token;
@@ -160,6 +180,7 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
                 tma_load_3d(sbase + t * SM::kTile + half * SM::kHalf + i * a.G * 128, qmap,
                             bar(SM::bQFull), half * 64, s.kvh * a.G, tok);
             }
+          }
         };
         // K or V tile into the next slot: the runs whose pool rows the lanes of `lanes` hold
         auto load = [&](int token, uint32_t lanes, const CUtensorMap* map) {
@@ -486,12 +507,12 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
       // Destination row of a token's head: the chain's own rows (part with its first tile), or
       // this CTA's.
       const int per_tile = pre_tile_tokens(a.G);
-      const size_t row =
-          s.cut ? ((size_t)c * 2 + (s.two ? t : 0)) * kPrefillTileM + r
-                : ((size_t)(s.tok0 + (s.two ? t * per_tile : 0) + i_tok) * 2 + s.second) * a.Hq +
+      const uint32_t row =  // (the workspace holds far less than 2^32 of them)
+          s.cut ? (uint32_t)((c * 2 + (s.two ? t : 0)) * kPrefillTileM + r)
+                : (uint32_t)((s.tok0 + (s.two ? t * per_tile : 0) + i_tok) * 2 + s.second) * (uint32_t)a.Hq +
                       s.kvh * a.G + (r - i_tok * a.G);
       float2* ml = reinterpret_cast<float2*>(a.ws + (s.cut ? PL.cut_ml : PL.base_ml)) + row;
-      float* o = reinterpret_cast<float*>(a.ws + (s.cut ? PL.cut_o : PL.base_o)) + row * D;
+      float* o = reinterpret_cast<float*>(a.ws + (s.cut ? PL.cut_o : PL.base_o));
       float w0 = 1.f, w1 = 0.f;  // weights of O_0 and O_1 (one tile of rows)
       if (!s.two) {
         // both groups' (m, l): group 1 hands its own over, group 0 hands the weights back
@@ -528,6 +549,10 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
         const int ch0 = s.two ? 0 : t * (D / 64), ch1 = s.two ? D / 32 : ch0 + D / 64;
         const uint32_t o0 = s.two ? o_col : 256u;
         const bool both = !s.two && n > 1;
+        // A lane holds 32 columns of its row.  With many rows 8 lanes turn their 8 x 8 pieces of 4
+        // columns, so that they write a row's 128 bytes at once: each lane 16 bytes of a row of its
+        // own, 2 x 128 rows took 4.8 us, so 3; with few the turning costs more than it saves.
+        const bool turn = s.two || rows > 64;
         for (int ch = ch0; ch < ch1; ++ch) {
           uint32_t ov[32];
           tmem_ld32(t_lane + o0 + ch * 32, ov);
@@ -541,8 +566,26 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
           } else {
             tc_wait_ld();
           }
-          if (r < rows) {
-            uint4* dst = reinterpret_cast<uint4*>(o + ch * 32);
+          if (turn) {
+#pragma unroll
+            for (int sh = 1; sh < 8; sh *= 2)
+#pragma unroll
+              for (int x = 0; x < 32; ++x) {
+                if (x & (4 * sh)) continue;
+                const bool up = lane & sh;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? ov[x] : ov[x + 4 * sh], sh);
+                if (up) ov[x] = got;
+                else ov[x + 4 * sh] = got;
+              }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const uint32_t to = __shfl_sync(0xffffffffu, row, (lane & 24) + x);
+              if (quad * 32 + (lane & 24) + x < rows)
+                *reinterpret_cast<uint4*>(o + (size_t)to * D + ch * 32 + (lane & 7) * 4) =
+                    make_uint4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
+            }
+          } else if (r < rows) {
+            uint4* dst = reinterpret_cast<uint4*>(o + (size_t)row * D + ch * 32);
 #pragma unroll
             for (int x = 0; x < 8; ++x)
               dst[x] = make_uint4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
