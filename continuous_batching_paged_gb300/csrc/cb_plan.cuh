@@ -367,11 +367,22 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
 // Prefix CTAs where `free` SMs are left to them and to `items` chunk items (up to a third of them for
 // those, an SM per item: an item is mostly latency): as many for each KV head (PreGroup), where there
 // are enough a multiple of `per` (Hkv x plan_prefixes' period), no more than the work is worth (`most`).
-__device__ __forceinline__ int pre_cta_count(int free, int items, int most, int Hkv, int per) {
-  free -= items < free / 3 ? items : free / 3;
+// (Quotients by reciprocals, exact for numbers below 1024: integer divisions cost the
+// planner 0.2 us.)
+struct PreRound {
+  int Hkv, per;
+  float inv_hkv, inv_per;
+};
+__device__ __forceinline__ PreRound pre_round(int Hkv, int per) {
+  return {Hkv, per, __fdividef(1.f, (float)Hkv), __fdividef(1.f, (float)per)};
+}
+__device__ __forceinline__ int pre_cta_count(int free, int items, int most, const PreRound& m) {
+  const int third = (free * 43691) >> 17;  // free / 3
+  free -= items < third ? items : third;
   int np = free < most ? free : most;
-  const int of = np > per ? per : Hkv;
-  if (np > of) np -= np % of;
+  const bool whole = np > m.per;
+  const int of = whole ? m.per : m.Hkv;
+  if (np > of) np = of * (int)(((float)np + 0.5f) * (whole ? m.inv_per : m.inv_hkv));
   return np < 1 ? 1 : np;
 }
 __device__ __forceinline__ int pre_cta_most(int cost, int Hkv, int min_steps) {
@@ -390,7 +401,7 @@ __device__ __forceinline__ int pre_cta_most(int cost, int Hkv, int min_steps) {
 // 18 batches timed on a GB300 (4 to 256 sequences, prefixes of 500 to 64k keys, 1, 2 and 8 KV heads,
 // head_dim 64 and 128): the choice is within 3 % of the best n on 15 of them, and within 6 % on all.
 __device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes, float pre_bytes,
-                                                   int cost, int chains, int per, float chunk_flops,
+                                                   int cost, int chains, const PreRound& m, float chunk_flops,
                                                    int items, long long tiles, int records, int most) {
   const int lane = threadIdx.x & 31;
   const int hg = pre_head_groups(a.Hkv, a.G), sms = a.chunk_ctas;
@@ -406,7 +417,7 @@ __device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_
     const int free = sms - n * hg;
     const float x = __fdividef(x1, (float)n), d = 4.8f + sqrt_approx(x * x + y * y);
     const float p = 12.f + __fdividef(pre_us,
-                                      (float)pre_cta_count(free, items, most, a.Hkv, per)) +
+                                      (float)pre_cta_count(free, items, most, m)) +
                     __fdividef(chunk_us, (float)free);
     const float t = fmaxf(d, p) + 0.018f * fminf(d, p) + 0.019f * (float)n;
     if (t < best) {
@@ -701,18 +712,18 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
     }
     int n = (int)(ntiles < a.decode_ctas ? (ntiles > 0 ? ntiles : 1) : a.decode_ctas);
     if (kPre && pre_cost > 0) {
-      const int per = a.Hkv * period <= kPrePeriod ? a.Hkv * period : a.Hkv;
+      const PreRound m = pre_round(a.Hkv, a.Hkv * period <= kPrePeriod ? a.Hkv * period : a.Hkv);
       const float row = (float)(a.Hkv * a.D * 4);  // bytes of a key and its value
       const int items = n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq);
       const int most = pre_cta_most(pre_cost, a.Hkv, pre_min_steps((long long)hdr->pre_tokens * a.Hq));
       if (a.decode_auto)
         n = choose_prefix_split(a, keys * row, (float)hdr->pre_keys * row, pre_cost,
-                                hdr->pre_own, per,
+                                hdr->pre_own, m,
                                 pairs * (float)(4 * a.D * a.Hq), items, ntiles, n_dec, most);
       // the decode CTAs without work; where a given number leaves none, an eighth of the chunk CTAs
       const int idle = pre_idle_count(pre_head_groups(a.Hkv, a.G), n, a.decode_ctas);
       if (tid == 0)
-        hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, items, most, a.Hkv, per);
+        hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, items, most, m);
     } else if (a.decode_auto) {
       n = choose_decode_ctas(keys * (float)(a.Hkv * a.D * 4), pairs * (float)(4 * a.D * a.Hq),
                              n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq), a.decode_ctas,
