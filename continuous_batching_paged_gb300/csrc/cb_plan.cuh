@@ -399,7 +399,7 @@ __device__ __forceinline__ int pre_cta_most(int cost, int Hkv, int min_steps) {
 // The choice is the n with the least max(decode, prefix + chunk), plus a little of the other one and
 // 0.019 a CTA for the parts it adds.  The constants are those with the least loss over every even n of
 // 18 batches timed on a GB300 (4 to 256 sequences, prefixes of 500 to 64k keys, 1, 2 and 8 KV heads,
-// head_dim 64 and 128): the choice is within 3 % of the best n on 15 of them, and within 6 % on all.
+// head_dim 64 and 128): the choice is within 3 % of the best n on 16 of them, and within 6 % on all.
 __device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes, float pre_bytes,
                                                    int cost, int chains, const PreRound& m, float chunk_flops,
                                                    int items, long long tiles, int records, int most) {
