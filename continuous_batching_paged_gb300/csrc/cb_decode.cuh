@@ -289,8 +289,19 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
 #pragma unroll
     for (int ht = 0; ht < NTH; ++ht) {
       s[ht][0] = s[ht][1] = s[ht][2] = s[ht][3] = 0.f;
+      if constexpr (kPre) {  // (two chains of products, see the softmax)
+        float s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) mma_bf16_16816(s[ht], kf[ks], qb[ht][ks][0], qb[ht][ks][1]);
+        for (int ks = 0; ks < KS; ks += 2) {
+          mma_bf16_16816(s[ht], kf[ks], qb[ht][ks][0], qb[ht][ks][1]);
+          mma_bf16_16816(s1, kf[ks + 1], qb[ht][ks + 1][0], qb[ht][ks + 1][1]);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[ht][x] += s1[x];
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) mma_bf16_16816(s[ht], kf[ks], qb[ht][ks][0], qb[ht][ks][1]);
+      }
     }
     if constexpr (kPre && QS == 1) {
       if (edge || head) {
@@ -316,29 +327,65 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
     uint32_t pb[NTH][2];
     bool resc = false;
     float al[NTH][2];
+    if constexpr (kPre) {
+      // Beside the prefix pass this one has fewer SMs than HBM needs, and a warp's chain through a tile
+      // bounds it, so the chain is kept short: the running maximum follows only where a score exceeds it
+      // by more than 2^8 (as in the chunk pass), and no shuffle is needed elsewhere.
 #pragma unroll
-    for (int ht = 0; ht < NTH; ++ht) {
-      float ma = fmaxf(s[ht][0], s[ht][2]), mb = fmaxf(s[ht][1], s[ht][3]);
+      for (int ht = 0; ht < NTH; ++ht) {
+        float& ra = mrun[ht][0];
+        float& rb = mrun[ht][1];
+        al[ht][0] = al[ht][1] = 1.f;
+        const float ta = fmaxf(s[ht][0], s[ht][2]) * sl2, tb = fmaxf(s[ht][1], s[ht][3]) * sl2;
+        if (__any_sync(0xffffffffu, ta > ra + 8.f || tb > rb + 8.f)) {
+          float ma = ta, mb = tb;
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) {
-        ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, x));
-        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
+          for (int x = 4; x < 32; x <<= 1) {
+            ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, x));
+            mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
+          }
+          if (ma > ra + 8.f) {
+            al[ht][0] = fast_exp2(ra - ma);
+            ra = ma;
+          }
+          if (mb > rb + 8.f) {
+            al[ht][1] = fast_exp2(rb - mb);
+            rb = mb;
+          }
+          resc = true;
+        }
+        // (a token of a record may see no key of a part's first tile; its m is then -inf, and 0 is
+        // subtracted so that no -inf - (-inf) appears)
+        const float sa = ra == -INFINITY ? 0.f : ra, sb = rb == -INFINITY ? 0.f : rb;
+        const float p0 = fast_exp2(fmaf(s[ht][0], sl2, -sa)), p1 = fast_exp2(fmaf(s[ht][1], sl2, -sb));
+        const float p2 = fast_exp2(fmaf(s[ht][2], sl2, -sa)), p3 = fast_exp2(fmaf(s[ht][3], sl2, -sb));
+        lrun[ht][0] = lrun[ht][0] * al[ht][0] + (p0 + p2);
+        lrun[ht][1] = lrun[ht][1] * al[ht][1] + (p1 + p3);
+        pb[ht][0] = movm_trans(pack_bf16x2(p0, p1));  // keys 0-7:  B[k = 2tq, 2tq+1][n = g]
+        pb[ht][1] = movm_trans(pack_bf16x2(p2, p3));  // keys 8-15
       }
-      const float na = fmaxf(mrun[ht][0], ma * sl2), nb = fmaxf(mrun[ht][1], mb * sl2);
-      // (kPre: a token of a record may see no key of a part's first tile; its m is then -inf, and 0
-      // is subtracted so that no -inf - (-inf) appears)
-      const float sa = kPre && na == -INFINITY ? 0.f : na, sb = kPre && nb == -INFINITY ? 0.f : nb;
-      al[ht][0] = fast_exp2(mrun[ht][0] - sa);
-      al[ht][1] = fast_exp2(mrun[ht][1] - sb);
-      mrun[ht][0] = na;
-      mrun[ht][1] = nb;
-      const float p0 = fast_exp2(fmaf(s[ht][0], sl2, -sa)), p1 = fast_exp2(fmaf(s[ht][1], sl2, -sb));
-      const float p2 = fast_exp2(fmaf(s[ht][2], sl2, -sa)), p3 = fast_exp2(fmaf(s[ht][3], sl2, -sb));
-      lrun[ht][0] = lrun[ht][0] * al[ht][0] + (p0 + p2);
-      lrun[ht][1] = lrun[ht][1] * al[ht][1] + (p1 + p3);
-      resc |= (al[ht][0] != 1.f) || (al[ht][1] != 1.f);
-      pb[ht][0] = movm_trans(pack_bf16x2(p0, p1));  // keys 0-7:  B[k = 2tq, 2tq+1][n = g]
-      pb[ht][1] = movm_trans(pack_bf16x2(p2, p3));  // keys 8-15
+    } else {
+#pragma unroll
+      for (int ht = 0; ht < NTH; ++ht) {
+        float ma = fmaxf(s[ht][0], s[ht][2]), mb = fmaxf(s[ht][1], s[ht][3]);
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, x));
+          mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
+        }
+        const float na = fmaxf(mrun[ht][0], ma * sl2), nb = fmaxf(mrun[ht][1], mb * sl2);
+        al[ht][0] = fast_exp2(mrun[ht][0] - na);
+        al[ht][1] = fast_exp2(mrun[ht][1] - nb);
+        mrun[ht][0] = na;
+        mrun[ht][1] = nb;
+        const float p0 = fast_exp2(fmaf(s[ht][0], sl2, -na)), p1 = fast_exp2(fmaf(s[ht][1], sl2, -nb));
+        const float p2 = fast_exp2(fmaf(s[ht][2], sl2, -na)), p3 = fast_exp2(fmaf(s[ht][3], sl2, -nb));
+        lrun[ht][0] = lrun[ht][0] * al[ht][0] + (p0 + p2);
+        lrun[ht][1] = lrun[ht][1] * al[ht][1] + (p1 + p3);
+        resc |= (al[ht][0] != 1.f) || (al[ht][1] != 1.f);
+        pb[ht][0] = movm_trans(pack_bf16x2(p0, p1));  // keys 0-7:  B[k = 2tq, 2tq+1][n = g]
+        pb[ht][1] = movm_trans(pack_bf16x2(p2, p3));  // keys 8-15
+      }
     }
     // alpha is exactly 1 while the running max stands (the common case): skip the rescale then
     if (__any_sync(0xffffffffu, resc)) {
