@@ -66,15 +66,14 @@ static cudaError_t launch_instance(const AttnArgs& a, const AttnMaps& m, const P
 // M = max m_c, w_c = 2^(m_c - M), out = sum_c w_c o_c / sum_c w_c l_c,
 // lse = (M + log2 sum_c w_c l_c) ln 2 over the parts c of its chains and of its decode record.  Some
 // part holds a key that the token sees, so M is finite (a part without one has m = -inf, w = 0).  A lane
-// finds a part and loads
-// its (m, l), so all are there after one trip to L2, and the rows of O follow kC = 8 at a time (2: 1.9 us
-// more for 128 sequences on 4096 keys, 3.5 for a step with a chunk).  Finding the parts is what costs
-// instructions, so with many rows a warp does HP = 4 heads; with few, where only the latency of its
-// loads counts, one.
+// finds a part and loads its (m, l), so all are there after one trip to L2, and the rows of O follow kC
+// at a time.  Finding the parts is what costs instructions, so with many rows a warp does HP = 4 heads;
+// with few, where only the latency of its loads counts, one (launch_prefix_merge).
 constexpr int kMergeThreads = 256;
-template <int D, int HP>
-__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnArgs a) {
-  constexpr int PER = D / 32, kC = 8;  // columns per lane, parts' rows of O in flight
+template <int D, int HP, int kC>
+__global__ void __launch_bounds__(kMergeThreads, HP * kC > 16 ? 1 : 2)
+    prefix_merge_kernel(const AttnArgs a) {
+  constexpr int PER = D / 32;  // columns per lane
   allow_dependent_launch();
   const int lane = threadIdx.x & 31;
   const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, a.pack);
@@ -242,13 +241,20 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const AttnA
 
 cudaError_t launch_prefix_merge(const AttnArgs& a, int sm_count, cudaStream_t stream) {
   // Four heads per warp where that leaves every SM two warps or more (32 sequences under 8 KV heads 27.6
-  // us with one, 30.6 with four; 64 sequences 47.5 and 45.4).
+  // us with one, 30.6 with four; 64 sequences 47.5 and 45.4).  8 parts of four heads in flight take all
+  // registers of an SM for 8 warps, so with more blocks than SMs 4 (128 sequences on 4096 keys 57.4 us
+  // with 4, 56.0 with 8; 256 on 8192 100.2 and 102.7).
   const bool four = (long long)a.R * a.Hkv >= (long long)sm_count * 2 && a.G >= 4;
   const long long warps = (long long)a.R * a.Hkv * (four ? (a.G + 3) / 4 : a.G);
   long long blocks = (warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+  const bool one_each = blocks <= sm_count;
   if (blocks > (long long)sm_count * 8) blocks = (long long)sm_count * 8;
-  auto* kernel = a.D == 128 ? (four ? prefix_merge_kernel<128, 4> : prefix_merge_kernel<128, 1>)
-                            : (four ? prefix_merge_kernel<64, 4> : prefix_merge_kernel<64, 1>);
+  auto* kernel = a.D == 128 ? (!four      ? prefix_merge_kernel<128, 1, 8>
+                               : one_each ? prefix_merge_kernel<128, 4, 8>
+                                          : prefix_merge_kernel<128, 4, 4>)
+                            : (!four      ? prefix_merge_kernel<64, 1, 8>
+                               : one_each ? prefix_merge_kernel<64, 4, 8>
+                                          : prefix_merge_kernel<64, 4, 4>);
   return launch_dependent(kernel, (unsigned)blocks, kMergeThreads, 0, stream, a);
 }
 
