@@ -117,7 +117,7 @@ constexpr int kPreMinKeys = kChunkKeys;
 constexpr int kMaxPreCtas = 160;   // CTAs of the prefix pass (at most one per SM)
 // A chain's start and end cost 8 us besides its steps (rows and first tiles loaded, the part written),
 // and a CTA whose range holds the end of one chain and the start of another pays them twice: 128
-// sequences on 2000 keys (2 units under each of 8 KV heads) take 59.4 us on 48 CTAs, none of which
+// sequences on 4096 keys (2 units under each of 8 KV heads) took 59.4 us on 48 CTAs, none of which
 // does, and 70.4 on 40; 40 sequences on 30k keys under one KV head 41.7 us on 96 and 50.4 on 98.  So a
 // lone group gets a multiple of the CTAs that make up whole ones for every unit, in proportion to its
 // steps' cost, where that is kPrePeriod or less.  (Counting a start as 11 cost units instead, so that such a CTA gets
