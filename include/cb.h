@@ -310,8 +310,8 @@ cb_status cb_rope_append_attention(const void* q, const void* k_new, const void*
  * cb_pass_timestamps -- device time stamps (%globaltimer, ns) of the two passes of the last
  * attention call that used `workspace`: ts_ns[0] / [1] the first start and the last end of the
  * decode CTAs that had work, ts_ns[2] / [3] the same for the chunk CTAs (the end is the last
- * chunk item's output written); 0 / 0 for a pass that had no work.  Waits for `stream`, then
- * reads 64 bytes of the workspace.  For profiling: inside one launch CUDA events cannot separate
+ * chunk item's output written) and those of shared prefixes; 0 / 0 for a pass that had no work.
+ * Waits for `stream`, then reads the plan's header in the workspace.  For profiling: inside one launch CUDA events cannot separate
  * the passes.  Errors: CB_ERR_INVALID_ARG (NULL pointer), CB_ERR_CUDA.
  */
 cb_status cb_pass_timestamps(const void* workspace, uint64_t* ts_ns, void* stream);
