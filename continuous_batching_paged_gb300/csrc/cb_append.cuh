@@ -15,7 +15,9 @@ constexpr int kAppendThreads = 256;
 constexpr int kAppendMaxChunks = 8;  // 16-byte chunks per lane and tensor in flight
 
 // Cache slot (row of the flattened [P * bs, Hkv, D] pool) of packed token t < cu_seqlens_q[S], and
-// its position; -1, after a report, where the metadata is bad.  Called by one full warp.
+// its position; -1, after a report, where the metadata is bad.  Called by one full warp.  kPadding: t
+// may lie behind the last sequence (-1 then, without a report).
+template <bool kPadding = false>
 __device__ __forceinline__ long long token_slot(const AppendArgs& a, int t, int lane, int& pos) {
   // Sequence of token t: the last s with cu[s] <= t (cu is non-decreasing).  Each round
   // probes 32 increasing positions in (lo, hi]; the lanes whose probe is <= t form a prefix.
@@ -36,7 +38,7 @@ __device__ __forceinline__ long long token_slot(const AppendArgs& a, int t, int 
   }
   const int s = lo;
   if (s >= a.S) {
-    if (lane == 0) report(a.err, kErrOutOfRange);
+    if (!kPadding && lane == 0) report(a.err, kErrOutOfRange);
     return -1;
   }
   const int c0 = __ldg(a.cu_seqlens_q + s), c1 = __ldg(a.cu_seqlens_q + s + 1);

@@ -83,8 +83,7 @@ __device__ __forceinline__ void rope_tokens(const RopeArgs& r, long long first_w
   __nv_bfloat16* qo = static_cast<__nv_bfloat16*>(r.q_out);
   __nv_bfloat16* kp = static_cast<__nv_bfloat16*>(a.k_pages);
   __nv_bfloat16* vp = static_cast<__nv_bfloat16*>(a.v_pages);
-  const int t_end = min(a.T, __ldg(a.cu_seqlens_q + a.S));
-  const long long n_items = (long long)t_end * r.parts;
+  const long long n_items = (long long)a.T * r.parts;
   for (long long item = first_warp; item < n_items; item += nwarps) {
     const int t = (int)(item / r.parts), part = (int)(item - (long long)t * r.parts);
     long long slot = 0;
@@ -105,7 +104,7 @@ __device__ __forceinline__ void rope_tokens(const RopeArgs& r, long long first_w
         }
       }
       if (g0 == part) {
-        slot = token_slot(a, t, lane, pos);
+        slot = token_slot<true>(a, t, lane, pos);
         if (slot >= 0 && pos >= r.max_positions) {
           if (lane == 0) report(a.err, kErrOutOfRange);
           slot = -1;
