@@ -5,9 +5,9 @@
 
 namespace cb {
 
-// Blocks of 4 warps and 4 head groups in flight (8 16-byte loads per lane, 101 registers): blocks of 8
+// Blocks of 4 warps and 4 head groups in flight (8 16-byte loads per lane, 96 registers): blocks of 8
 // leave a quarter of the registers unused and were slower at every size (8208 tokens of 64 heads 59
-// us, now 53 us, 5.96 TB/s; 2048 tokens of 32 heads 13.7 us, now 11.7 us), 2 or 6 groups too.
+// us, now 52 us, 6.07 TB/s; 2048 tokens of 32 heads 13.7 us, now 11.5 us), 2 or 6 groups too.
 constexpr int kRopeThreads = 128;
 constexpr int kRopeUnroll = 4;
 
