@@ -535,3 +535,28 @@ def test_steps_in_a_row_and_the_same_sequence_twice(cuda_lib):
     for i, o in enumerate(outs):
         assert torch.equal(o.view(torch.int16), alone[i % 2].view(torch.int16)), i
     assert cb.get_device_error() == cb.CB_OK
+
+
+@pytest.mark.parametrize("first,step", [(0.0, 0.3), (0.0, 0.1), (90.0, -0.3), (-40.0, 0.36), (5.0, 1.0)])
+@pytest.mark.parametrize("decode_ctas", [0, 1])
+def test_own_scores_that_climb_and_fall(cuda_lib, first, step, decode_ctas):
+    # the score of own key j is first + step j: per tile of 16 keys the running maximum grows by less and
+    # by more than the 2^8 at which it is followed (0.3 x 16 log2(e) = 6.9, 0.36: 8.3), or never again
+    b = grouped_batch([1] * 3, [300, 77, 16], [0] * 3, [208], 1, 1, 64, 16, seed=970)
+    q = opa.bf16_bits_to_f64(b["q"])
+    kp = opa.bf16_bits_to_f64(b["kp"])
+    for s in range(3):
+        along = q[s, 0] / (q[s, 0] @ q[s, 0]) / b["scale"]
+        for j in range(208 // 16, int(b["kv"][s] + 15) // 16):
+            n = min(16, int(b["kv"][s]) - j * 16)
+            score = first + step * (j * 16 - 208 + np.arange(n))
+            kp[b["table"][s][j], :n, 0] = score[:, None] * along
+    b["kp"] = workloads.f32_to_bf16_bits(kp.astype(np.float32))
+    # (scores reach 300: the fp32 sums are off by 300 x 2^-20 = 2.9e-4, 7 % of 2^-8)
+    ref, mag, ref_lse = reference(b)
+    out, lse = Dev(b).attend(decode_ctas=decode_ctas)
+    assert cb.get_device_error() == cb.CB_OK
+    got = out.float().cpu().numpy().astype(np.float64)
+    lim = 2.0 ** -8 * np.abs(ref) + 1.1 * 2.0 ** -8 * mag
+    assert np.all(np.abs(got - ref) <= lim), float((np.abs(got - ref) / lim).max())
+    assert np.all(np.abs(lse.cpu().numpy() - ref_lse) <= 3e-4 + 2e-6 * np.abs(ref_lse))
