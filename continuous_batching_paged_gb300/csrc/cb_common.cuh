@@ -171,17 +171,19 @@ struct PreToken {
 
 // Sections of the workspace behind ws_layout's (all 256-byte aligned).
 struct PreLayout {
-  size_t rec, cnt, first, map, group, tok, base_ml, base_o, cut_ml, cut_o, total;
+  size_t rec, cnt, first, map, cost, group, tok, base_ml, base_o, cut_ml, cut_o, total;
 };
 __host__ __device__ inline PreLayout pre_layout(int R, int T, int Hq, int D, int NG, int pack) {
   PreLayout L;
   size_t off = ws_layout(R, T, Hq, D, pack).total;
   // per decode record: keys of the prefix computed apart and query tokens, or zeros
   L.rec = off;     off = align_up(off + sizeof(int32_t) * 2 * (size_t)(R + 1), 256);
-  // per group number: query tokens (then: tokens listed so far), first member, index in the list
+  // per group number: query tokens (then: tokens listed so far), first member (then: its first entry
+  // of the token list), index in the list of groups, cost0
   L.cnt = off;     off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.first = off;   off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.map = off;     off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
+  L.cost = off;    off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.group = off;   off = align_up(off + sizeof(PreGroup) * (size_t)(NG + kPrePlanThreads + 1), 256);
   L.tok = off;     off = align_up(off + sizeof(PreToken) * (size_t)(R + 1), 256);
   // Partial results of a chain: the part with its first K/V tile in a row per (token list entry,

@@ -166,8 +166,8 @@ __device__ __forceinline__ float pre_decode_tile_us(const AttnArgs& a) {
   return 0.5f + 0.3f * (float)((a.Hkv < 8 ? a.Hkv : 8) * a.D) * (1.f / 1024.f);
 }
 
-// Up to this many groups the planner keeps in shared memory.
-constexpr int kPlanSmemGroups = 1024;
+// Up to this many groups the planner keeps in shared memory (five arrays).
+constexpr int kPlanSmemGroups = 768;
 
 // What the first look at a sequence finds (kept for the second where one round covers the batch).
 struct PreSeq {
@@ -205,9 +205,10 @@ __device__ __forceinline__ int group_place(int32_t* cnt, int group, int q, int w
 }
 
 // With shared prefixes: which groups' prefixes are computed once.  Fills the group list, and per
-// group number map (index in the list, -1: every member's own pass does it all) and cnt (the tokens
-// listed so far).  Returns the work of the prefixes per KV head in cost units (0: no group takes
-// part; the same in every thread).
+// group number map (index in the list, -1: every member's own pass does it all), first (its first
+// entry of the token list), cost (cost0) and cnt (the tokens listed so far): in shared memory, since a
+// look at the list itself is a trip to L2 (two of them: 0.3 us).  Returns the work of the prefixes per
+// KV head in cost units (0: no group takes part; the same in every thread).
 //
 // A group takes part when it has at least two query tokens (from members with at most kPreMaxQ
 // each) and kPreMinKeys keys; after bad metadata none does, and each sequence is computed alone.
@@ -216,7 +217,8 @@ __device__ __forceinline__ int group_place(int32_t* cnt, int group, int q, int w
 // lens: the groups' prefix lengths (in shared memory where all of them fit, else a.prefix_lens).
 // period: CTAs per KV head that give each unit of a lone group a whole number of them (else 1).
 __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], int32_t* cnt,
-                                             int32_t* first, int32_t* map, const int32_t* lens,
+                                             int32_t* first, int32_t* map, int32_t* cost,
+                                             const int32_t* lens,
                                              PreSeq& mine, int& period) {
   const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack);
   PreGroup* groups = reinterpret_cast<PreGroup*>(a.ws + PL.group);
@@ -289,18 +291,18 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
              (my_q <= kPreMaxQ || (few_chunks && my_ctx >= my_q))) {
     own_nt = pre_tiles(0, mine.kv);
   }
-  auto cost = [&](int n, int nt) {
+  auto work = [&](int n, int nt) {
     const PreShape sh = pre_shape(n, nt, a.G);
     // (of use where one thread has the only group)
     s_period = sh.full == 0 ? 1 : sh.units > sh.full ? kPreCost2 * sh.full + kPreCost1 : sh.full;
     return sh.per;
   };
   const int own_cost =
-      own_nt > 0 ? (int)min((long long)kPreMaxCost + 1, cost(my_q, own_nt)) : 0;
+      own_nt > 0 ? (int)min((long long)kPreMaxCost + 1, work(my_q, own_nt)) : 0;
   unsigned long long total = own_cost;
   for (int g = tid; g < a.NG; g += kPrePlanThreads) {
     const int n = shared_tokens(g, lens[g]);
-    if (n > 0) total += (unsigned long long)cost(n, pre_tiles(0, lens[g]));
+    if (n > 0) total += (unsigned long long)work(n, pre_tiles(0, lens[g]));
   }
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if ((tid & 31) == 0 && total > 0) atomicAdd(&s_total, total);
@@ -320,6 +322,8 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
           {carry[2] + ex[2], n, carry[1] + ex[1], 0, keys, first[g], -1, 0};
     if (g < a.NG) {
       map[g] = n > 0 ? carry[0] + ex[0] : -1;
+      first[g] = carry[1] + ex[1];
+      cost[g] = carry[2] + ex[2];
       cnt[g] = 0;
     }
 #pragma unroll
@@ -330,7 +334,7 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
     __syncthreads();  // the groups and map are written, cnt is 0
     mine.at = group_place(cnt, my_member ? mine.group : -1, my_q, (a.S + 31) / 32);
     if (my_member) {
-      mine.list = groups[map[mine.group]].tok0 + mine.at;
+      mine.list = first[mine.group] + mine.at;
       mine.own_first = mine.keys;
     }
     if (any_own) {
@@ -453,7 +457,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   __shared__ int32_t s_dec_prefix[kSeqs + 1], s_pf_prefix[kSeqs + 1];
   __shared__ int32_t s_pf_seq[kSeqs];
   __shared__ int2 s_pf_lens[kSeqs];  // (q_len, prior context) of each chunk sequence
-  __shared__ int32_t s_groups[kPre ? 4 * kPlanSmemGroups : 1];
+  __shared__ int32_t s_groups[kPre ? 5 * kPlanSmemGroups : 1];
   const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, a.pack);
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + L.header);
   int32_t* dec_seq = reinterpret_cast<int32_t*>(a.ws + L.dec_seq);
@@ -466,19 +470,20 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   const long long max_kv = (long long)a.max_blocks * a.bs;
 
   float my_keys = 0.f, my_pairs = 0.f;  // work estimates for the decode / chunk balance
-  // shared prefixes: their work per KV head, and per group number cnt, first member and map
+  // shared prefixes: their work per KV head, and per group number what plan_prefixes finds
   int pre_cost = 0, period = 1;
   const PreLayout PL = kPre ? pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack) : PreLayout{};
   const bool few = a.NG <= kPlanSmemGroups;
   int32_t* grp_cnt = few ? s_groups : reinterpret_cast<int32_t*>(a.ws + PL.cnt);
   int32_t* grp_first = few ? s_groups + kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.first);
   int32_t* grp_map = few ? s_groups + 2 * kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.map);
+  int32_t* grp_cost = few ? s_groups + 4 * kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.cost);
   const int32_t* grp_lens = few ? s_groups + 3 * kPlanSmemGroups : a.prefix_lens;
   PreSeq mine = {0, 0, 0, -1, 0, -1, 0, -1, 0};
   if constexpr (kPre) {
     if (few)  // (the function's first barrier follows)
       for (int g = tid; g < a.NG; g += NT) s_groups[3 * kPlanSmemGroups + g] = a.prefix_lens[g];
-    pre_cost = plan_prefixes(a, sw, grp_cnt, grp_first, grp_map, grp_lens, mine, period);
+    pre_cost = plan_prefixes(a, sw, grp_cnt, grp_first, grp_map, grp_cost, grp_lens, mine, period);
   }
   // kPre: chunks that are groups of their own: (first token, tokens, first list entry, K/V tiles), cost0
   __shared__ int s_chunks;
@@ -561,10 +566,8 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
         s_chunk[x][1] = make_int4(mine.chain, 0, 0, 0);
       } else {
         int4 shared = make_int4(0, 0, 0, 0);  // the prefix's chain
-        if (mine.own_first > 0) {
-          const PreGroup g = reinterpret_cast<const PreGroup*>(a.ws + PL.group)[grp_map[mine.group]];
-          shared = make_int4(mine.at, g.n_tok, pre_tiles(0, g.keys), g.cost0);
-        }
+        if (mine.own_first > 0)
+          shared = make_int4(mine.at, grp_cnt[mine.group], pre_tiles(0, mine.keys), grp_cost[mine.group]);
         for (int t = 0; t < q_len; ++t) {
           int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 3 * (size_t)(mine.list + t);
           const int4 own = make_int4(t, q_len, own_nt, mine.chain);
@@ -576,7 +579,10 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       }
     } else if (kPre && grp >= 0 && v[0]) {
       const int first = keys / kDecodeTileKeys * kDecodeTileKeys;
-      const PreGroup group = reinterpret_cast<const PreGroup*>(a.ws + PL.group)[grp_map[grp]];
+      // (all of the group's tokens are listed by now, unless the batch takes several rounds)
+      const int n_tok = a.S <= NT ? grp_cnt[grp]
+                                  : reinterpret_cast<const PreGroup*>(a.ws + PL.group)[grp_map[grp]].n_tok;
+      const int tok0 = grp_first[grp], cost0 = grp_cost[grp];
       int tile = carry[1] + ex[1], i = carry[0] + ex[0];
       for (int j = 0; j < q_len; j += a.pack, ++i) {
         const int n = min(a.pack, q_len - j), n_keys = kv - (q_len - j - n);
@@ -587,9 +593,9 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
         if (i < kSeqs) s_dec_prefix[i] = tile;
         reinterpret_cast<int2*>(a.ws + PL.rec)[i] = make_int2(keys, n);
         for (int t = 0; t < n; ++t) {
-          int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 3 * (size_t)(group.tok0 + at + j + t);
+          int4* entry = reinterpret_cast<int4*>(a.ws + PL.tok) + 3 * (size_t)(tok0 + at + j + t);
           entry[0] = make_int4(tok + j + t, 8 * i + t, tile, tile + n_tiles);
-          entry[1] = make_int4(at + j + t, group.n_tok, pre_tiles(0, keys), group.cost0);
+          entry[1] = make_int4(at + j + t, n_tok, pre_tiles(0, keys), cost0);
           entry[2] = make_int4(0, 0, 0, 0);
         }
         tile += n_tiles;
