@@ -59,8 +59,7 @@ struct PlanHeader {
   unsigned long long t_dec_start, t_dec_end, t_pf_start, t_pf_end;
   int32_t pre_cost;         // their work per KV head, in cost units (PreGroup),
   int32_t pre_tokens;       // entries of the groups' token list,
-  int32_t pre_keys;         // keys of all groups, and groups of one sequence (for the planner's
-  int32_t pre_own;          // estimates)
+  int32_t pre_chains;       // and their chains per KV head
 };
 
 // Byte offsets of the workspace sections (all 256-byte aligned).

@@ -309,12 +309,17 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
   const bool any_own = __syncthreads_or(own_nt) != 0;
   const bool too_much = s_total > kPreMaxCost;  // (32 bits hold every cost below)
   bad |= too_much;
-  int carry[4] = {0, 0, 0, 0};  // groups, tokens, cost, keys (an estimate: it may wrap)
+  int carry[4] = {0, 0, 0, 0};  // groups, tokens, cost, chains
   for (int base = 0; base < a.NG; base += kPrePlanThreads) {
     const int g = base + tid;
     const int keys = g < a.NG ? lens[g] : 0;
     const int n = shared_tokens(g, keys);
-    int v[4] = {n > 0, n, n > 0 ? (int)pre_shape(n, pre_tiles(0, keys), a.G).per : 0, n > 0 ? keys : 0};
+    int v[4] = {n > 0, n, 0, 0};
+    if (n > 0) {
+      const PreShape sh = pre_shape(n, pre_tiles(0, keys), a.G);
+      v[2] = (int)sh.per;
+      v[3] = sh.units;
+    }
     int ex[4], tot[4];
     block_scan4<kPrePlanThreads>(v, ex, tot, sw);  // (its barriers also part the reads of cnt from the writes)
     if (n > 0)
@@ -329,7 +334,6 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
 #pragma unroll
     for (int k = 0; k < 4; ++k) carry[k] += tot[k];
   }
-  int n_own = 0;  // sequences that are groups of their own
   if (!too_much && one_round) {
     __syncthreads();  // the groups and map are written, cnt is 0
     mine.at = group_place(cnt, my_member ? mine.group : -1, my_q, (a.S + 31) / 32);
@@ -339,7 +343,7 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
     }
     if (any_own) {
       int v[4] = {own_nt > 0, own_nt > 0 && !my_member ? my_q : 0, own_nt > 0 ? own_cost : 0,
-                  own_nt > 0 ? mine.kv - mine.own_first : 0};
+                  own_nt > 0 ? pre_shape(my_q, own_nt, a.G).units : 0};
       int ex[4], tot[4];
       block_scan4<kPrePlanThreads>(v, ex, tot, sw);
       if (own_nt > 0) {
@@ -351,18 +355,16 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
         groups[carry[0] + ex[0]] = {mine.chain, my_q,   mine.list, mine.own_first,
                                     mine.kv,    tid,    my_ctx,    my_member};
       }
-      n_own = tot[0];
 #pragma unroll
       for (int k = 0; k < 4; ++k) carry[k] += tot[k];
     }
   }
   period = carry[0] == 1 ? s_period : 1;
   if (tid == 0) {
-    hdr->pre_own = n_own;
     hdr->pre_groups = carry[0];
     hdr->pre_tokens = carry[1];
     hdr->pre_cost = carry[2];
-    hdr->pre_keys = carry[3];
+    hdr->pre_chains = carry[3];
   }
   __syncthreads();
   return carry[2];
@@ -396,30 +398,29 @@ __device__ __forceinline__ int pre_cta_most(int cost, int Hkv, int min_steps) {
 
 // Decode CTAs per head group where prefixes are computed apart; the other SMs are the prefixes'.
 // Called by one full warp.  Model, in us:
-//   decode = 4.8 + hypot(x, y): x the CTA's tiles (1.17 each at 64 KB, 0.86 at 8 KB; a record counts
-//            as one more), y a share of the HBM time of all bytes;
-//   prefix = 12 + 1.1 per cost unit of a CTA, and 3.5 per chain of a single sequence; chunk work
-//            follows on the same SMs.
+//   decode = 7.2 + hypot(x, y): x the CTA's tiles (1.19 each at 64 KB, 0.87 at 8 KB; a record counts
+//            as one more), y a share of the HBM time of their bytes;
+//   prefix = 12 + 1.1 per cost unit of a CTA and 4.9 per chain; chunk work follows on the same SMs.
 // The choice is the n with the least max(decode, prefix + chunk), plus a little of the other one and
 // 0.019 a CTA for the parts it adds.  The constants are those with the least loss over every even n of
-// 18 batches timed on a GB300 (4 to 256 sequences, prefixes of 500 to 64k keys, 1, 2 and 8 KV heads,
-// head_dim 64 and 128): the choice is within 3 % of the best n on 16 of them, and within 6 % on all.
-__device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes, float pre_bytes,
+// 24 batches timed on a GB300 (4 to 256 sequences, 1 to 40 groups, prefixes of 300 to 64k keys, 1 to 8 KV
+// heads, head_dim 64 and 128): the choice is within 3.5 % of the best n on all of them.
+__device__ __forceinline__ int choose_prefix_split(const AttnArgs& a, float dec_bytes,
                                                    int cost, int chains, const PreRound& m, float chunk_flops,
                                                    int items, long long tiles, int records, int most) {
   const int lane = threadIdx.x & 31;
   const int hg = pre_head_groups(a.Hkv, a.G), sms = a.chunk_ctas;
   const int cap = (int)(tiles < a.decode_ctas ? tiles : a.decode_ctas);
-  const float tile_us = 0.82f + 0.35f * (float)((a.Hkv < 8 ? a.Hkv : 8) * a.D) * (1.f / 1024.f);
+  const float tile_us = 0.82f + 0.37f * (float)((a.Hkv < 8 ? a.Hkv : 8) * a.D) * (1.f / 1024.f);
   const float x1 = tile_us * ((float)tiles + (float)records);
-  const float y = (dec_bytes + pre_bytes) * 0.022e-6f;
-  const float pre_us = (1.1f * (float)cost + 3.5f * (float)chains) * (float)a.Hkv;
+  const float y = dec_bytes * 0.013e-6f;
+  const float pre_us = (1.1f * (float)cost + 4.9f * (float)chains) * (float)a.Hkv;
   const float chunk_us = chunk_flops * (1.f / 6.4e6f);
   float best = 3.4e38f;
   int best_n = 1;
   for (int n = 2 * (lane + 1); n <= (cap > 2 ? cap : 2) && n * hg < sms; n += 64) {
     const int free = sms - n * hg;
-    const float x = __fdividef(x1, (float)n), d = 4.8f + sqrt_approx(x * x + y * y);
+    const float x = __fdividef(x1, (float)n), d = 7.2f + sqrt_approx(x * x + y * y);
     const float p = 12.f + __fdividef(pre_us,
                                       (float)pre_cta_count(free, items, most, m)) +
                     __fdividef(chunk_us, (float)free);
@@ -723,8 +724,8 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       const int items = n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq);
       const int most = pre_cta_most(pre_cost, a.Hkv, pre_min_steps((long long)hdr->pre_tokens * a.Hq));
       if (a.decode_auto)
-        n = choose_prefix_split(a, keys * row, (float)hdr->pre_keys * row, pre_cost,
-                                hdr->pre_own, m,
+        n = choose_prefix_split(a, keys * row, pre_cost,
+                                hdr->pre_chains, m,
                                 pairs * (float)(4 * a.D * a.Hq), items, ntiles, n_dec, most);
       // the decode CTAs without work; where a given number leaves none, an eighth of the chunk CTAs
       const int idle = pre_idle_count(pre_head_groups(a.Hkv, a.G), n, a.decode_ctas);
