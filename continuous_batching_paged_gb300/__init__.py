@@ -350,8 +350,10 @@ def _on_stream(stream):
     """Context that makes `stream` the stream of the allocations made in it, so that memory the call
     allocates is reused only after the work queued there."""
     import torch
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                             else torch.cuda.ExternalStream(_stream(stream)))
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)  # (ExternalStream(0) is a new stream, not the default one)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _check_output(t, name, shape, dev) -> None:
