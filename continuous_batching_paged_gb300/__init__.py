@@ -149,8 +149,8 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
         if _lib is None:
             from . import _build
             path = library_path()
-            if build_if_missing and _build.is_stale():
-                _build.build()
+            if build_if_missing and _build.library_is_stale():
+                _build.build_library()
             if not os.path.exists(path):
                 raise RuntimeError(f"libcb is not built ({path}); run the package build first")
             lib = ctypes.CDLL(path)
@@ -291,12 +291,17 @@ def kv_append(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens
 # the tensors; the _explain functions find the message for what it refused.
 
 def _native():
-    """The extension (built with the library, which it links to)."""
+    """The extension (built in-tree first if it is missing or older than its sources), which links to
+    the library."""
     global _ext
     if _ext is None:
         library()
-        from . import _cb_torch
-        _ext = _cb_torch
+        with _lock:
+            from . import _build
+            if _build.extension_is_stale():
+                _build.build_extension()
+            from . import _cb_torch
+            _ext = _cb_torch
     return _ext
 
 

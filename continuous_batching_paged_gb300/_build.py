@@ -4,7 +4,8 @@ Python extension that binds its per-step calls to torch tensors.
 Each .cu file compiles to an object in parallel; the objects link into one shared library
 with the CUDA runtime linked statically, so loading the library needs no GPU or driver.  The
 extension (csrc/cb_torch.cpp) compiles beside them with the host compiler against the headers of the
-installed Python and torch, and links to libcb.so next to it.
+installed Python and torch, and links to libcb.so next to it.  The library builds and loads without
+torch; the extension is built where there is one.
 """
 from __future__ import annotations
 
@@ -40,18 +41,29 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps() -> list[str]:
-    out = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
-    out += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
-    out.append(os.path.abspath(__file__))
-    return out
+def _is_old(path: str, deps: list[str]) -> bool:
+    """Whether `path` is missing or older than one of `deps` (or this file)."""
+    if not os.path.exists(path):
+        return True
+    t = os.path.getmtime(path)
+    return any(os.path.getmtime(p) > t for p in [*deps, os.path.abspath(__file__)])
+
+
+def _in(folder: str, suffixes) -> list[str]:
+    return [os.path.join(folder, f) for f in os.listdir(folder) if f.endswith(suffixes)]
+
+
+def library_is_stale() -> bool:
+    return _is_old(LIB, _in(CSRC, (".cu", ".cuh", ".h")) + _in(INCLUDE, ".h"))
+
+
+def extension_is_stale() -> bool:
+    return _is_old(EXT, [EXT_SOURCE, *_in(INCLUDE, ".h")])
 
 
 def is_stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(EXT)):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
-    return any(os.path.getmtime(p) > t for p in _deps())
+    """Whether build() has something to do (without torch there is no extension to build)."""
+    return library_is_stale() or (_torch_dir() is not None and extension_is_stale())
 
 
 def _compile(src: str) -> tuple[str, str]:
@@ -69,11 +81,10 @@ def _run(cmd: list[str], what: str) -> None:
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
+    """Where torch is installed (None: it is not)."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("torch not found: the Python binding needs its headers")
-    return list(spec.submodule_search_locations)[0]
+    return None if spec is None else list(spec.submodule_search_locations)[0]
 
 
 def _compile_ext() -> str:
@@ -98,16 +109,12 @@ def _link_ext(obj: str) -> None:
     os.replace(tmp, EXT)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every kernel source and link libcb.so; returns its path."""
-    if not force and not is_stale():
-        return LIB
+def build_library(verbose: bool = False) -> str:
+    """Compile every kernel source and link libcb.so; returns its path.  Needs no torch."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        ext = ex.submit(_compile_ext)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
         results = list(ex.map(_compile, srcs))
-        ext_obj = ext.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -116,9 +123,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
            "-ldl", "-lpthread", "-lrt"]
     _run(cmd, "link")
     os.replace(tmp, LIB)
-    _link_ext(ext_obj)
     return LIB
 
 
-if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose=True))
+def build_extension() -> str:
+    """Compile and link the extension against libcb.so, which must be there; returns its path."""
+    if _torch_dir() is None:
+        raise RuntimeError("torch not found: the Python binding needs its headers")
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    _link_ext(_compile_ext())
+    return EXT
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Build what is missing or older than its sources (force: everything): libcb.so and, where
+    torch is installed, the extension.  Returns the library's path.  The library is linked whatever
+    becomes of the extension: the allocator, the scheduler and the C ABI need neither torch nor its
+    headers."""
+    lib = force or library_is_stale()
+    ext = _torch_dir() is not None and (force or extension_is_stale())
+    if ext:
+        os.makedirs(BUILD_DIR, exist_ok=True)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        obj = ex.submit(_compile_ext) if ext else None  # (beside the kernels)
+        if lib:
+            build_library(verbose)
+        if obj is not None:
+            _link_ext(obj.result())
+    return LIB
