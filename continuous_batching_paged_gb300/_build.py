@@ -57,8 +57,29 @@ def library_is_stale() -> bool:
     return _is_old(LIB, _in(CSRC, (".cu", ".cuh", ".h")) + _in(INCLUDE, ".h"))
 
 
+def _ext_stamp() -> str:
+    """What the extension is compiled for, beside its sources: this Python and the installed torch."""
+    torch = _torch_dir()
+    with open(os.path.join(torch, "version.py")) as f:
+        return f"{sys.version}\n{torch}\n{f.read()}"
+
+
+def _ext_stamp_path() -> str:
+    return os.path.join(BUILD_DIR, "cb_torch.stamp")
+
+
 def extension_is_stale() -> bool:
-    return _is_old(EXT, [EXT_SOURCE, *_in(INCLUDE, ".h")])
+    """Whether the extension is missing, older than its sources, or compiled for another Python or
+    torch than those that are here."""
+    if _is_old(EXT, [EXT_SOURCE, *_in(INCLUDE, ".h")]):
+        return True
+    if _torch_dir() is None:
+        return False
+    try:
+        with open(_ext_stamp_path()) as f:
+            return f.read() != _ext_stamp()
+    except FileNotFoundError:
+        return True
 
 
 def is_stale() -> bool:
@@ -107,6 +128,8 @@ def _link_ext(obj: str) -> None:
           "-Wl,-rpath,$ORIGIN", "-L", lib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
           "-lc10_cuda", "-lc10"], "linking _cb_torch.so")
     os.replace(tmp, EXT)
+    with open(_ext_stamp_path(), "w") as f:
+        f.write(_ext_stamp())
 
 
 def build_library(verbose: bool = False) -> str:

@@ -69,3 +69,20 @@ assert cb.workspace_size(1, 4, 2, 64, 20) > 0
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_extension_is_rebuilt_for_another_torch_or_python(here, monkeypatch):
+    torch_dir = here / "torch"
+    torch_dir.mkdir()
+    (torch_dir / "version.py").write_text("__version__ = '1.0'\n")
+    monkeypatch.setattr(_build, "_torch_dir", lambda: str(torch_dir))
+    _build.build()
+    assert not _build.is_stale()
+    old = os.path.getmtime(torch_dir / "version.py")
+    (torch_dir / "version.py").write_text("__version__ = '1.1'\n")
+    os.utime(torch_dir / "version.py", (old - 1000, old - 1000))     # (files of packages keep their dates)
+    assert _build.is_stale() and not _build.library_is_stale()
+    _build.build()
+    assert not _build.is_stale()
+    monkeypatch.setattr(sys, "version", sys.version + " of another build")
+    assert _build.is_stale() and not _build.library_is_stale()
