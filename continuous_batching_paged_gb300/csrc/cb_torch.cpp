@@ -49,6 +49,18 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, int dev) {
 
 bool fits(int64_t x) { return x <= INT_MAX; }
 
+// A Python integer that fits 32 bits; no error is left pending where it does not.
+bool read_int(PyObject* o, int32_t* x) {
+  if (!PyLong_Check(o)) return false;
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) {  // beyond a long
+    PyErr_Clear();
+    return false;
+  }
+  *x = (int32_t)v;
+  return v == *x;
+}
+
 struct Step {
   cb_dims dims;
   int dev;
@@ -63,15 +75,13 @@ bool read_step(PyObject* const* args, int dev, Step* s) {
   if (dev != c10::cuda::current_device() || !plain(t[0], at::kBFloat16, 4, dev) ||
       !plain(t[1], at::kBFloat16, 4, dev) || !plain(t[2], at::kInt, 2, dev) ||
       !plain(t[3], at::kInt, t[3] ? t[3]->dim() : 0, dev) ||
-      !plain(t[4], at::kInt, t[4] ? t[4]->dim() : 0, dev) || !PyLong_Check(args[5]))
+      !plain(t[4], at::kInt, t[4] ? t[4]->dim() : 0, dev) || !read_int(args[5], &s->block_size))
     return false;
   const int64_t S = t[4]->numel();
-  const long bs = PyLong_AsLong(args[5]);
   if (t[3]->numel() != S + 1 || t[2]->size(0) != S || t[0]->sizes() != t[1]->sizes() ||
-      t[0]->size(1) != bs || !fits(S) || !fits(t[0]->size(0)) || !fits(t[2]->size(1)) || !fits(bs))
+      t[0]->size(1) != s->block_size || !fits(S) || !fits(t[0]->size(0)) || !fits(t[2]->size(1)))
     return false;
   s->dev = dev;
-  s->block_size = (int32_t)bs;
   s->k_pages = t[0];
   s->v_pages = t[1];
   s->block_table = t[2];
@@ -198,17 +208,13 @@ bool read_tail(PyObject* const* args, const at::Tensor& q, const Step& s, Tail* 
     if (!plain(w, at::kByte, w ? w->dim() : 0, dev)) return false;
     t->ws = *w;
   }
-  if (!PyLong_Check(args[5]) || !PyLong_Check(args[7])) return false;
-  const long ctas = PyLong_AsLong(args[5]), window = PyLong_AsLong(args[7]);
+  if (!read_int(args[5], &t->options.decode_ctas) || !read_int(args[7], &t->options.window)) return false;
   const int serial = PyObject_IsTrue(args[6]);
-  if (serial < 0 || PyErr_Occurred() || !fits(ctas) || !fits(window) || ctas < INT_MIN ||
-      window < INT_MIN) {
+  if (serial < 0) {
     PyErr_Clear();
     return false;
   }
-  t->options.decode_ctas = (int32_t)ctas;
   t->options.flags = serial ? CB_OPT_SERIAL : 0;
-  t->options.window = (int32_t)window;
   if (args[8] != Py_None) {  // a tuple of event handles, made by the Python side
     if (!PyTuple_Check(args[8]) || PyTuple_GET_SIZE(args[8]) != CB_NUM_PHASE_EVENTS) return false;
     for (int i = 0; i < CB_NUM_PHASE_EVENTS; ++i)

@@ -1,4 +1,4 @@
-"""The C++ binding of the per-step calls: streams by their handles."""
+"""The C++ binding of the per-step calls: streams by their handles, and integers that no length can be."""
 import numpy as np
 import pytest
 import torch
@@ -57,3 +57,13 @@ def test_default_stream_by_its_handle(cuda_lib, name, stream):
     assert np.array_equal(bits_of(got), expect)
     with cb._on_stream(stream):
         assert torch.cuda.current_stream().cuda_stream == 0
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("size", [1 << 70, -(1 << 70), 1 << 40, 1 << 31, -16, 0, 17])
+def test_block_sizes_of_no_pool_are_refused(cuda_lib, name, size):
+    s = Step(1001)
+    with pytest.raises(ValueError, match="block_size"):
+        s.call(name, block_size=size)
+    assert s.call(name) is not None                     # nothing is left behind for the next call
+    assert cb.get_device_error() == cb.CB_OK
