@@ -14,6 +14,7 @@ is missing or cannot be built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 
@@ -320,6 +321,11 @@ def _explain_rows(name, t) -> None:
     _require(_rows_ok(*t.shape, t.stride()), f"{name} must have contiguous token rows that do not overlap")
 
 
+def _explain_int(name, x) -> None:
+    _require(hasattr(x, "__index__"), f"{name} must be an integer")
+    _require(-2**31 <= operator.index(x) < 2**31, f"{name} must be a 32-bit integer")
+
+
 def _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
                   cos_sin) -> None:
     """Raise the error of a step's inputs that failed their check (k_new, v_new and cos_sin: None
@@ -338,6 +344,7 @@ def _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, 
     _check_bf16("v_pages", v_pages, 4)
     _check_meta(block_table, cu_seqlens_q, kv_lens)
     P, bs, Hkv, D = k_pages.shape
+    _explain_int("block_size", block_size)
     _require(bs == block_size, "k_pages must be [P, block_size, Hkv, D]")
     _require(k_pages.shape == v_pages.shape, "v_pages must match k_pages")
     if k_new is not None:
@@ -489,9 +496,12 @@ def prefix_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, num_tok
     return int(library().cb_prefix_workspace_size(ctypes.byref(dims), int(num_groups)))
 
 
-def _explain_tail(q, num_seqs, prefix_group, prefix_lens, out, lse, workspace, phase_events) -> None:
+def _explain_tail(q, num_seqs, prefix_group, prefix_lens, out, lse, workspace, decode_ctas,
+                  window=0) -> None:
     """Raise the error of an attention call's other arguments (q: the tensor that it attends with)."""
     import torch
+    _explain_int("decode_ctas", decode_ctas)
+    _explain_int("window", window)
     dev = q.get_device()
     if prefix_group is not None or prefix_lens is not None:
         _require(prefix_group is not None and prefix_lens is not None,
@@ -543,7 +553,7 @@ def shared_prefix_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_l
         _explain_step(q, None, None, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
                       None)
         _require(prefix_group is not None, "prefix_group must be given")
-        _explain_tail(q, kv_lens.numel(), prefix_group, prefix_lens, out, lse, workspace, phase_events)
+        _explain_tail(q, kv_lens.numel(), prefix_group, prefix_lens, out, lse, workspace, decode_ctas)
         raise ValueError("shared_prefix_attention: bad argument")
     if r.__class__ is int:
         _check(r, "cb_shared_prefix_attention")
@@ -574,7 +584,8 @@ def rope_append_attention(q, k_new, v_new, k_pages, v_pages, block_table, cu_seq
                       block_size, cos_sin)
         if q_out is not None:
             _check_output(q_out, "q_out", tuple(q.shape), q.get_device())
-        _explain_tail(q, kv_lens.numel(), prefix_group, prefix_lens, out, lse, workspace, phase_events)
+        _explain_tail(q, kv_lens.numel(), prefix_group, prefix_lens, out, lse, workspace, decode_ctas,
+                      window)
         raise ValueError("rope_append_attention: bad argument")
     if r.__class__ is int:
         _check(r, "cb_rope_append_attention")

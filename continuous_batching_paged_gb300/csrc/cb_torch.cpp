@@ -49,11 +49,16 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, int dev) {
 
 bool fits(int64_t x) { return x <= INT_MAX; }
 
-// A Python integer that fits 32 bits; no error is left pending where it does not.
+// An integer (Python's, numpy's, ...) that fits 32 bits; no error is left pending where it is none.
 bool read_int(PyObject* o, int32_t* x) {
-  if (!PyLong_Check(o)) return false;
-  const long v = PyLong_AsLong(o);
-  if (v == -1 && PyErr_Occurred()) {  // beyond a long
+  long v = -1;
+  if (PyLong_Check(o)) {
+    v = PyLong_AsLong(o);
+  } else if (PyObject* i = PyNumber_Index(o)) {
+    v = PyLong_AsLong(i);
+    Py_DECREF(i);
+  }
+  if (v == -1 && PyErr_Occurred()) {  // no integer, or beyond a long
     PyErr_Clear();
     return false;
   }

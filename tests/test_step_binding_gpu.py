@@ -1,4 +1,5 @@
-"""The C++ binding of the per-step calls: streams by their handles, and integers that no length can be."""
+"""The C++ binding of the per-step calls: streams by their handles, and arguments as users hand them
+over (integers of other types, integers that no length can be)."""
 import numpy as np
 import pytest
 import torch
@@ -66,4 +67,25 @@ def test_block_sizes_of_no_pool_are_refused(cuda_lib, name, size):
     with pytest.raises(ValueError, match="block_size"):
         s.call(name, block_size=size)
     assert s.call(name) is not None                     # nothing is left behind for the next call
+    assert cb.get_device_error() == cb.CB_OK
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_integers_of_other_types(cuda_lib, name):
+    s = Step(1002)
+    expect = bits_of(s.call(name))
+    for kind in (np.int32, np.int64, np.uint8):
+        assert np.array_equal(bits_of(s.call(name, block_size=kind(16))), expect)
+    with pytest.raises(ValueError, match="block_size must be an integer"):
+        s.call(name, block_size=16.0)
+    if name == "rope_append":
+        return
+    expect = bits_of(s.call(name, decode_ctas=7))
+    assert np.array_equal(bits_of(s.call(name, decode_ctas=np.int64(7))), expect)
+    for bad in (7.0, 1 << 70, 1 << 31):
+        with pytest.raises(ValueError, match="decode_ctas must be"):
+            s.call(name, decode_ctas=bad)
+    if name == "rope_append_attention":
+        with pytest.raises(ValueError, match="window must be"):
+            s.call(name, window=2.5)
     assert cb.get_device_error() == cb.CB_OK
