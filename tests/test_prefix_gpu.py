@@ -560,3 +560,29 @@ def test_own_scores_that_climb_and_fall(cuda_lib, first, step, decode_ctas):
     lim = 2.0 ** -8 * np.abs(ref) + 1.1 * 2.0 ** -8 * mag
     assert np.all(np.abs(got - ref) <= lim), float((np.abs(got - ref) / lim).max())
     assert np.all(np.abs(lse.cpu().numpy() - ref_lse) <= 3e-4 + 2e-6 * np.abs(ref_lse))
+
+
+@pytest.mark.parametrize("bs", [5, 6, 9, 10, 14])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (1, 1, 64)])
+def test_block_sizes_with_odd_factors(cuda_lib, bs, Hq, Hkv, D):
+    # blocks that a tile of 128 keys is cut into runs of one or two keys for: a group with one tile of
+    # rows, one with two and one with three, keys that end inside a tile and at its border ...
+    rng = np.random.default_rng(bs)
+    n = [9, 130 // (Hq // Hkv) + 3, 2 * 128 // (Hq // Hkv) + 5]
+    group = [g for g in range(3) for _ in range(n[g])] + [-1, -1]
+    own = [1 + int(x) for x in rng.integers(0, 30, len(group))]
+    check(grouped_batch([1] * len(group), own, group, [515, 384, 201], Hq, Hkv, D, bs, seed=1010 + bs))
+    # ... and own keys of several tokens as groups with a causal edge, drafts and chunks
+    b = grouped_batch([8, 3, 1, 40, 130, 8, 2], [300, 700, 4, 90, 400, 200, 8], [0, 0, 0, 0, -1, -1, 0],
+                      [260], Hq, Hkv, D, bs, seed=1020 + bs)
+    check(b)
+    check(b, serial=True)
+
+
+@pytest.mark.parametrize("bs", [5, 6])
+def test_bad_blocks_in_runs_of_one_or_two_keys(cuda_lib, bs):
+    b = grouped_batch(Q11, OWN11, GRP11, [200, 333], 8, 2, 128, bs, seed=1030)
+    b["table"][0, 3], b["table"][1, 20] = 1 << 20, -1
+    Dev(b).attend()
+    assert cb.get_device_error() == cb.CB_ERR_OUT_OF_RANGE
+    assert cb.get_device_error() == cb.CB_OK
