@@ -356,11 +356,12 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
     return fail(CB_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   if (!(scale > 0.f) || scale != scale)
     return fail(CB_ERR_INVALID_ARG, "scale must be a positive finite number");
-  const int R = NG > 0 ? cb::pre_records(dims->num_seqs, dims->num_tokens, dims->num_q_heads)
-                       : dims->num_seqs;
   const int pack = NG > 0 ? cb::pre_pack(dims->num_q_heads / dims->num_kv_heads) : 1;
+  const int R = NG > 0 ? cb::pre_records(dims->num_seqs, dims->num_tokens, pack) : dims->num_seqs;
+  const int LT = NG > 0 ? cb::pre_tokens(dims->num_seqs, dims->num_tokens, dims->num_q_heads) : 0;
+  const int LB = NG > 0 ? LT + cb::pre_second(dims->num_seqs, dims->num_tokens) : 0;
   const size_t need =
-      NG > 0 ? cb::pre_layout(R, dims->num_tokens, dims->num_q_heads, dims->head_dim, NG, pack).total
+      NG > 0 ? cb::pre_layout(R, LT, LB, dims->num_tokens, dims->num_q_heads, dims->head_dim, NG, pack).total
              : cb::ws_layout(R, dims->num_tokens, dims->num_q_heads, dims->head_dim).total;
   if (workspace_bytes < need)
     return fail(CB_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
@@ -408,6 +409,8 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   a.decode_ctas = dctas;
   a.prefill_ctas = a.chunk_ctas = ds->sm_count;
   a.R = R;
+  a.LT = LT;
+  a.LB = LB;
   a.pack = pack;
   a.prefix_group = NG > 0 ? prefix->prefix_group : nullptr;
   a.prefix_lens = NG > 0 ? prefix->prefix_lens : nullptr;
@@ -547,10 +550,11 @@ cb_status cb_append_attention(const void* k_new, const void* v_new, void* k_page
 size_t cb_prefix_workspace_size(const cb_dims* dims, int32_t num_groups) {
   if (num_groups <= 0) return num_groups == 0 ? cb_attention_workspace_size(dims) : 0;
   if (cb_attention_workspace_size(dims) == 0 || dims->num_q_heads / dims->num_kv_heads > 16) return 0;
-  return cb::pre_layout(cb::pre_records(dims->num_seqs, dims->num_tokens, dims->num_q_heads),
-                        dims->num_tokens,
-                        dims->num_q_heads, dims->head_dim, num_groups,
-                        cb::pre_pack(dims->num_q_heads / dims->num_kv_heads)).total;
+  const int S = dims->num_seqs, T = dims->num_tokens, Hq = dims->num_q_heads;
+  const int pack = cb::pre_pack(Hq / dims->num_kv_heads);
+  const int LT = cb::pre_tokens(S, T, Hq);
+  return cb::pre_layout(cb::pre_records(S, T, pack), LT, LT + cb::pre_second(S, T), T, Hq, dims->head_dim,
+                        num_groups, pack).total;
 }
 
 cb_status cb_shared_prefix_attention(const void* q, const void* k_pages, const void* v_pages,

@@ -128,11 +128,26 @@ __host__ __device__ inline int pre_min_steps(long long rows) { return rows <= 51
 
 // Query tokens per tile: all G query heads of a KV head, token by token.
 __host__ __device__ inline int pre_tile_tokens(int G) { return kPrefillTileM / G; }
-// Most query tokens whose prefix is computed apart (and most decode records) of a batch: kPreMaxQ
-// per sequence, and what fewer than kPreChunkItems chunk items hold (an item is 2 x 128 rows).
-__host__ __device__ inline int pre_records(int S, int T, int Hq) {
-  const long long most = (long long)S * kPreMaxQ + kPreChunkItems * 2 * kPrefillTileM / Hq;
-  return most > T ? (T > S ? T : S) : (int)most;
+// What a batch may need at most, whatever its lengths (the host does not know them).
+// Decode records of up to `pack` tokens: those of kPreMaxQ tokens per sequence, and
+// sum ceil(q / pack) <= (T + S (pack - 1)) / pack; at least S, as the lists of sequences are as long.
+__host__ __device__ inline int pre_records(int S, int T, int pack) {
+  const long long by_seq = (long long)S * ((kPreMaxQ + pack - 1) / pack);
+  const long long by_tok = ((long long)T + (long long)S * (pack - 1)) / pack;
+  const long long most = by_seq < by_tok ? by_seq : by_tok;
+  return most > S ? (int)most : S;
+}
+// Query tokens with two chains: those of a prefix's members with a group of their own keys.
+__host__ __device__ inline int pre_second(int S, int T) {
+  const int most = S <= kPrePlanThreads ? S * kPreMaxQ : 0;
+  return most < T ? most : T;
+}
+// Entries of the token list: kPreMaxQ per sequence and, where the planner sees all sequences at once,
+// what fewer than kPreChunkItems chunk items hold (an item is 2 x 128 rows).
+__host__ __device__ inline int pre_tokens(int S, int T, int Hq) {
+  const long long most = (long long)S * kPreMaxQ +
+                         (S <= kPrePlanThreads ? kPreChunkItems * 2 * kPrefillTileM / Hq : 0);
+  return most < T ? (int)most : T;
 }
 
 // One group whose prefix is computed once.  Its query tokens make tiles, two tiles (the last time
@@ -168,11 +183,13 @@ struct PreToken {
   } chain[2];
 };
 
-// Sections of the workspace behind ws_layout's (all 256-byte aligned).
+// Sections of the workspace behind ws_layout's (all 256-byte aligned).  R: pre_records, LT: pre_tokens,
+// LB: LT + pre_second.
 struct PreLayout {
   size_t rec, cnt, first, map, cost, group, tok, base_ml, base_o, cut_ml, cut_o, total;
 };
-__host__ __device__ inline PreLayout pre_layout(int R, int T, int Hq, int D, int NG, int pack) {
+__host__ __device__ inline PreLayout pre_layout(int R, int LT, int LB, int T, int Hq, int D, int NG,
+                                               int pack) {
   PreLayout L;
   size_t off = ws_layout(R, T, Hq, D, pack).total;
   // per decode record: keys of the prefix computed apart and query tokens, or zeros
@@ -184,12 +201,13 @@ __host__ __device__ inline PreLayout pre_layout(int R, int T, int Hq, int D, int
   L.map = off;     off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.cost = off;    off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.group = off;   off = align_up(off + sizeof(PreGroup) * (size_t)(NG + kPrePlanThreads + 1), 256);
-  L.tok = off;     off = align_up(off + sizeof(PreToken) * (size_t)(R + 1), 256);
-  // Partial results of a chain: the part with its first K/V tile in a row per (token list entry,
-  // first or second chain, query head), and a part that a CTA's range begins with in the CTA's own
-  // 2 x 128 rows.
-  L.base_ml = off; off = align_up(off + sizeof(float2) * 2 * (size_t)R * (size_t)Hq, 256);
-  L.base_o = off;  off = align_up(off + sizeof(float) * 2 * (size_t)R * (size_t)Hq * (size_t)D, 256);
+  L.tok = off;     off = align_up(off + sizeof(PreToken) * (size_t)(LT + 1), 256);
+  // Partial results of a chain: the part with its first K/V tile in a row per (token list entry, query
+  // head), for an entry's second chain LT entries further (the groups' members, who have those, are
+  // listed first); and a part that a CTA's range begins with in the CTA's own 2 x 128 rows.
+  const size_t base_rows = (size_t)LB * (size_t)Hq;
+  L.base_ml = off; off = align_up(off + sizeof(float2) * base_rows, 256);
+  L.base_o = off;  off = align_up(off + sizeof(float) * base_rows * (size_t)D, 256);
   const size_t cut_rows = (size_t)kMaxPreCtas * 2 * kPrefillTileM;
   L.cut_ml = off;  off = align_up(off + sizeof(float2) * cut_rows, 256);
   L.cut_o = off;   off = align_up(off + sizeof(float) * cut_rows * (size_t)D, 256);

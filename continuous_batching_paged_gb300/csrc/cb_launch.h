@@ -68,8 +68,10 @@ struct AttnArgs {
   int decode_auto;     // 1: the planner picks how many of them work (decode / chunk balance)
   int prefill_ctas;    // persistent CTAs of the chunk pass (0 when the launch runs decode only)
   int chunk_ctas;      // the same, whatever this launch runs (for the planner)
-  int R;               // decode records the workspace is laid out for (S; pre_records(S, T) with
-                       // shared prefixes)
+  int R;               // decode records the workspace is laid out for (S; pre_records with shared
+                       // prefixes)
+  int LT;              // query tokens whose keys may be computed apart (0; pre_tokens)
+  int LB;              // and their chains' own rows per query head (0; pre_tokens + pre_second)
   int pack;            // most query tokens of a decode record (1; pre_pack(G) with shared prefixes)
   const int32_t* prefix_group;  // [S]: the group whose prefix a sequence shares, or -1
   const int32_t* prefix_lens;   // [NG]: keys of each group's prefix

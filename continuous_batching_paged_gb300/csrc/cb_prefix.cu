@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kMergeThreads, HP * kC > 16 ? 1 : 2)
   allow_dependent_launch();
   const int lane = threadIdx.x & 31;
   const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, a.pack);
-  const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack);
+  const PreLayout PL = pre_layout(a.R, a.LT, a.LB, a.T, a.Hq, a.D, a.NG, a.pack);
   const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.ws + L.header);
   const int4* list = reinterpret_cast<const int4*>(a.ws + PL.tok);
   __nv_bfloat16* outg = static_cast<__nv_bfloat16*>(a.out);
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kMergeThreads, HP * kC > 16 ? 1 : 2)
 #pragma unroll
     for (int k = 0; k < 3; ++k) e[k] = __ldcg(list + 3 * (size_t)i + k);
   };
-  if (i0 < a.R) entry(i0);
+  if (i0 < a.LT) entry(i0);
   const long long jobs = (long long)__ldcg(&hdr->pre_tokens) * per_tok;
   const long long ntiles = __ldcg(&hdr->dec_tiles), Wh = __ldcg(&hdr->pre_cost), W = Wh * a.Hkv;
   const int N = __ldcg(&hdr->decode_ctas), NP = __ldcg(&hdr->pre_ctas);
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kMergeThreads, HP * kC > 16 ? 1 : 2)
         const int j1 = pre_step(x.cs, x.w, x.nt, pre_bound(W, c + 1, NP));
         const bool cut = j0 > 0;
         const size_t at = cut ? ((size_t)c * 2 + (x.tile & 1)) * kPrefillTileM + x.row
-                              : ((size_t)i * 2 + k) * a.Hq + head0;
+                              : ((size_t)i + (size_t)k * a.LT) * a.Hq + head0;
         if (j0 < j1) {  // (a range may end before the step that its last unit of cost lies in)
           pml = reinterpret_cast<const float2*>(a.ws + (cut ? PL.cut_ml : PL.base_ml)) + at;
           po = (unsigned long long)(reinterpret_cast<const float*>(
@@ -244,8 +244,8 @@ cudaError_t launch_prefix_merge(const AttnArgs& a, int sm_count, cudaStream_t st
   // us with one, 30.6 with four; 64 sequences 47.5 and 45.4).  8 parts of four heads in flight take all
   // registers of an SM for 8 warps, so with more blocks than SMs 4 (128 sequences on 4096 keys 57.4 us
   // with 4, 56.0 with 8; 256 on 8192 100.2 and 102.7).
-  const bool four = (long long)a.R * a.Hkv >= (long long)sm_count * 2 && a.G >= 4;
-  const long long warps = (long long)a.R * a.Hkv * (four ? (a.G + 3) / 4 : a.G);
+  const bool four = (long long)a.LT * a.Hkv >= (long long)sm_count * 2 && a.G >= 4;
+  const long long warps = (long long)a.LT * a.Hkv * (four ? (a.G + 3) / 4 : a.G);
   long long blocks = (warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
   const bool one_each = blocks <= sm_count;
   if (blocks > (long long)sm_count * 8) blocks = (long long)sm_count * 8;

@@ -53,7 +53,7 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
   constexpr int NS = SM::kSlots;
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D, a.pack).header);
   const int N = hdr->pre_ctas;
-  const PreLayout PL = pre_layout(a.R, a.T, a.Hq, a.D, a.NG, a.pack);
+  const PreLayout PL = pre_layout(a.R, a.LT, a.LB, a.T, a.Hq, a.D, a.NG, a.pack);
   const PreToken* list = reinterpret_cast<const PreToken*>(a.ws + PL.tok);
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -509,7 +509,7 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
       const int per_tile = pre_tile_tokens(a.G);
       const uint32_t row =  // (the workspace holds far less than 2^32 of them)
           s.cut ? (uint32_t)((c * 2 + (s.two ? t : 0)) * kPrefillTileM + r)
-                : (uint32_t)((s.tok0 + (s.two ? t * per_tile : 0) + i_tok) * 2 + s.second) * (uint32_t)a.Hq +
+                : (uint32_t)(s.tok0 + (s.two ? t * per_tile : 0) + i_tok + s.second * a.LT) * (uint32_t)a.Hq +
                       s.kvh * a.G + (r - i_tok * a.G);
       float2* ml = reinterpret_cast<float2*>(a.ws + (s.cut ? PL.cut_ml : PL.base_ml)) + row;
       float* o = reinterpret_cast<float*>(a.ws + (s.cut ? PL.cut_o : PL.base_o));

@@ -277,9 +277,15 @@ typedef struct {
 /*
  * cb_prefix_workspace_size -- bytes of device scratch for num_groups groups; pure host arithmetic
  * on what cb_attention_workspace_size uses, num_kv_heads and num_groups; 0 when dims is NULL or
- * invalid or num_groups is negative.  Beside the plan and the partial results of the decode pass
- * it holds partial results: two fp32 output rows per query head of up to min(num_tokens,
- * 8 num_seqs + 38912 / num_q_heads) query tokens, and 21 MB (head_dim 128) for split prefixes.
+ * invalid or num_groups is negative.  The lengths are on the device, so it is what any batch of the
+ * shape may need.  Beside the plan it holds partial results, fp32 rows of head_dim + 2 values per query
+ * head, with G = num_q_heads / num_kv_heads and pack = 8 / G (1 where G > 8):
+ *   own keys    pack (512 + min(num_seqs ceil(8 / pack), (num_tokens + num_seqs (pack - 1)) / pack)),
+ *   prefixes    min(num_tokens, 8 num_seqs + 38912 / num_q_heads), and up to 256 sequences once more
+ *               min(num_tokens, 8 num_seqs); beyond 256 sequences min(num_tokens, 8 num_seqs),
+ * and 21 MB (head_dim 128) for split prefixes.  64 decodes (32 / 8 heads of 128) take 43 MB, 256
+ * sequences of 2304 tokens (64 / 8 heads) 252 MB, 1024 sequences of 9000 tokens 586 MB: a workspace
+ * made once and passed to every call saves the allocation.
  */
 size_t cb_prefix_workspace_size(const cb_dims* dims, int32_t num_groups);
 

@@ -123,3 +123,22 @@ def test_output_must_not_overlap_the_queries(lib, out):
                                         ctypes.byref(r), None, out, None, P, 1 << 40,
                                         ctypes.byref(_dims()), None, None) == cb.CB_ERR_INVALID_ARG
     assert b"overlaps the queries" in lib.cb_last_error_message()
+
+
+@pytest.mark.parametrize("S,T,Hq,Hkv,D", [(256, 2048, 32, 32, 128), (512, 4096, 64, 64, 128),
+                                          (1024, 9000, 64, 8, 128), (257, 2304, 64, 8, 128),
+                                          (128, 512, 32, 8, 64), (300, 40000, 16, 1, 64), (64, 64, 32, 8, 128)])
+def test_workspace_holds_what_a_batch_can_need(lib, S, T, Hq, Hkv, D):
+    # partial rows (D + 2 fp32 values a query head): the decode pass's records of up to `pack` tokens,
+    # of sequences with at most 8 tokens, and a slot per decode CTA; the listed tokens (8 a sequence,
+    # and those of fewer than 152 chunk items), twice where a token can have two chains; 160 CTAs' own
+    pack = max(1, 8 // (Hq // Hkv))
+    records = min(S * -(-8 // pack), (T + S * (pack - 1)) // pack)
+    short = min(T, 8 * S)
+    listed = short if S > 256 else min(T, 8 * S + 152 * 256 // Hq) + short
+    rows = (512 + max(records, S)) * pack * Hq + listed * Hq + 160 * 256
+    # the lists: under 128 bytes for a record, a token or a group, and a counter per record and head
+    lists = 128 * (records + S + listed + 300) + 4 * (records + S) * Hq
+    size = lib.cb_prefix_workspace_size(ctypes.byref(_dims(num_seqs=S, num_tokens=T, num_q_heads=Hq,
+                                                           num_kv_heads=Hkv, head_dim=D)), 1)
+    assert rows * (4 * D + 8) <= size <= rows * (4 * D + 8) + lists + 16384

@@ -586,3 +586,22 @@ def test_bad_blocks_in_runs_of_one_or_two_keys(cuda_lib, bs):
     Dev(b).attend()
     assert cb.get_device_error() == cb.CB_ERR_OUT_OF_RANGE
     assert cb.get_device_error() == cb.CB_OK
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (2, 1), (3, 1), (4, 1), (8, 1), (16, 1)])
+@pytest.mark.parametrize("n", [1, 5, 40, 256, 257, 300])
+def test_a_call_stays_inside_its_workspace(cuda_lib, Hq, Hkv, n):
+    # every sequence with 8 tokens, which take as many records or chains as there can be, with the own
+    # keys short (records) and long (groups of their own), and chunks beside them
+    for own, extra in ((9, []), (400, []), (30, [200, 90])):
+        q = [8] * n + extra
+        b = grouped_batch(q, [own + i % 7 for i in range(n)] + [x + 20 for x in extra],
+                          [i % 2 for i in range(n)] + [-1] * len(extra), [140, 260], Hq, Hkv, 64, 16,
+                          seed=1040 + n)
+        d = Dev(b)
+        need = d.workspace().numel()
+        ws = torch.full((need + (1 << 20),), 255, dtype=torch.uint8, device="cuda")
+        out, lse = d.attend(workspace=ws)
+        assert cb.get_device_error() == cb.CB_OK
+        assert (ws[need:] == 255).all()
+        assert_matches(out, lse, b)
