@@ -291,11 +291,9 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
              (my_q <= kPreMaxQ || (few_chunks && my_ctx >= my_q))) {
     own_nt = pre_tiles(0, mine.kv);
   }
-  auto work = [&](int n, int nt) {
-    const PreShape sh = pre_shape(n, nt, a.G);
-    // (of use where one thread has the only group)
+  auto work = [&](int n, int nt) { return pre_shape(n, nt, a.G).per; };
+  auto set_period = [&](const PreShape& sh) {  // by the thread with the first group of the list
     s_period = sh.full == 0 ? 1 : sh.units > sh.full ? kPreCost2 * sh.full + kPreCost1 : sh.full;
-    return sh.per;
   };
   const int own_cost =
       own_nt > 0 ? (int)min((long long)kPreMaxCost + 1, work(my_q, own_nt)) : 0;
@@ -315,16 +313,19 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
     const int keys = g < a.NG ? lens[g] : 0;
     const int n = shared_tokens(g, keys);
     int v[4] = {n > 0, n, 0, 0};
+    PreShape sh = {};
     if (n > 0) {
-      const PreShape sh = pre_shape(n, pre_tiles(0, keys), a.G);
+      sh = pre_shape(n, pre_tiles(0, keys), a.G);
       v[2] = (int)sh.per;
       v[3] = sh.units;
     }
     int ex[4], tot[4];
     block_scan4<kPrePlanThreads>(v, ex, tot, sw);  // (its barriers also part the reads of cnt from the writes)
-    if (n > 0)
+    if (n > 0) {
       groups[carry[0] + ex[0]] =
           {carry[2] + ex[2], n, carry[1] + ex[1], 0, keys, first[g], -1, 0};
+      if (carry[0] + ex[0] == 0) set_period(sh);
+    }
     if (g < a.NG) {
       map[g] = n > 0 ? carry[0] + ex[0] : -1;
       first[g] = carry[1] + ex[1];
@@ -342,8 +343,9 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
       mine.own_first = mine.keys;
     }
     if (any_own) {
+      const PreShape sh = pre_shape(my_q, own_nt, a.G);
       int v[4] = {own_nt > 0, own_nt > 0 && !my_member ? my_q : 0, own_nt > 0 ? own_cost : 0,
-                  own_nt > 0 ? pre_shape(my_q, own_nt, a.G).units : 0};
+                  own_nt > 0 ? sh.units : 0};
       int ex[4], tot[4];
       block_scan4<kPrePlanThreads>(v, ex, tot, sw);
       if (own_nt > 0) {
@@ -354,12 +356,12 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
         }
         groups[carry[0] + ex[0]] = {mine.chain, my_q,   mine.list, mine.own_first,
                                     mine.kv,    tid,    my_ctx,    my_member};
+        if (carry[0] + ex[0] == 0) set_period(sh);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) carry[k] += tot[k];
     }
   }
-  period = carry[0] == 1 ? s_period : 1;
   if (tid == 0) {
     hdr->pre_groups = carry[0];
     hdr->pre_tokens = carry[1];
@@ -367,6 +369,7 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
     hdr->pre_chains = carry[3];
   }
   __syncthreads();
+  period = carry[0] == 1 ? s_period : 1;
   return carry[2];
 }
 
