@@ -539,7 +539,10 @@ def shared_prefix_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_l
     prefix_group int32 [num_seqs]: each sequence's group, or -1; prefix_lens int32 [num_groups]:
     how many leading keys the members of a group have in common (the same blocks in their tables,
     or blocks with the same content), at most each member's prior context.  Results are
-    ragged_paged_attention's within rounding; the other arguments are its.
+    ragged_paged_attention's within rounding; the other arguments are its.  Members with 1 to 8 query
+    tokens share; longer chunks read the prefix themselves.  workspace: prefix_workspace_size bytes
+    (43 MB for 64 decodes of 32 / 8 heads of 128, hundreds for batches of thousands of tokens), made by
+    the call where it is left out.
     """
     if stream is not None:
         with _on_stream(stream):
@@ -567,7 +570,8 @@ def rope_append_attention(q, k_new, v_new, k_pages, v_pages, block_table, cu_seq
                           window: int = 0, stream=None):
     """One layer's attention step (cb_rope_append_attention): rope_append, then
     shared_prefix_attention on the rotated queries (ragged_paged_attention without groups), same
-    results, in two launches.  q_out: where the rotated queries go (default: a temporary)."""
+    results, in two launches (three with groups).  q_out: where the rotated queries go (default: a
+    temporary)."""
     if stream is not None:
         with _on_stream(stream):
             return rope_append_attention(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q,

@@ -105,7 +105,9 @@ __host__ __device__ inline WsLayout ws_layout(int S, int T, int Hq, int D, int p
 // 0.8 us per 16 keys, 8 KV heads and record.  A sequence outside the groups with 2 to kPreMaxQ tokens
 // is such a group, too.  Longer ones (chunks) run the chunk pass, which sharing saves nothing: but
 // where its work items are fewer than kPreChunkItems, so that it would leave SMs idle, a chunk after
-// at least its own length of keys is such a group too, cut to equal shares like the others.
+// at least its own length of keys is such a group too, cut to equal shares like the others.  Groups of one
+// sequence are planned in batches of up to kPrePlanThreads sequences, which the planner sees at once; in
+// larger ones members of several tokens have records, and other sequences of several tokens the chunk pass.
 constexpr int kPreMaxQ = 8;
 constexpr int kPrePlanThreads = 256;  // of the planner (cb_plan.cuh); sequences it sees at once
 constexpr int kPreChunkItems = 152;
