@@ -70,14 +70,15 @@ struct AttnArgs {
   int chunk_ctas;      // the same, whatever this launch runs (for the planner)
   int R;               // decode records the workspace is laid out for (S; pre_records with shared
                        // prefixes)
-  int LT;              // query tokens whose keys may be computed apart (0; pre_tokens)
-  int LB;              // and their chains' own rows per query head (0; pre_tokens + pre_second)
   int pack;            // most query tokens of a decode record (1; pre_pack(G) with shared prefixes)
   const int32_t* prefix_group;  // [S]: the group whose prefix a sequence shares, or -1
   const int32_t* prefix_lens;   // [NG]: keys of each group's prefix
   int NG;                       // groups (0 without shared prefixes)
   int window;          // > 0: query at position p sees keys (p - window, p]; 0: all <= p
   float scale_log2;    // softmax scale * log2(e)
+  // with shared prefixes (behind the others, where they leave the kernels without prefixes as they are):
+  int LT;              // query tokens whose keys may be computed apart (pre_tokens)
+  int LB;              // and their chains' own rows per query head (pre_tokens + pre_second)
 };
 
 // Block moves: copy (pool -> pool), offload (pool -> linear host buffer), restore (host ->
