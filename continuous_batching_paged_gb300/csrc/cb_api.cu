@@ -359,9 +359,9 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   const int pack = NG > 0 ? cb::pre_pack(dims->num_q_heads / dims->num_kv_heads) : 1;
   const int R = NG > 0 ? cb::pre_records(dims->num_seqs, dims->num_tokens, pack) : dims->num_seqs;
   const int LT = NG > 0 ? cb::pre_tokens(dims->num_seqs, dims->num_tokens, dims->num_q_heads) : 0;
-  const int LB = NG > 0 ? LT + cb::pre_second(dims->num_seqs, dims->num_tokens) : 0;
   const size_t need =
-      NG > 0 ? cb::pre_layout(R, LT, LB, dims->num_tokens, dims->num_q_heads, dims->head_dim, NG, pack).total
+      NG > 0 ? cb::pre_layout(dims->num_seqs, R, LT, dims->num_tokens, dims->num_q_heads, dims->head_dim, NG, pack,
+                              cb::pre_second(dims->num_seqs, dims->num_tokens)).total
              : cb::ws_layout(R, dims->num_tokens, dims->num_q_heads, dims->head_dim).total;
   if (workspace_bytes < need)
     return fail(CB_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", workspace_bytes, need);
@@ -410,7 +410,6 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   a.prefill_ctas = a.chunk_ctas = ds->sm_count;
   a.R = R;
   a.LT = LT;
-  a.LB = LB;
   a.pack = pack;
   a.prefix_group = NG > 0 ? prefix->prefix_group : nullptr;
   a.prefix_lens = NG > 0 ? prefix->prefix_lens : nullptr;
@@ -553,8 +552,8 @@ size_t cb_prefix_workspace_size(const cb_dims* dims, int32_t num_groups) {
   const int S = dims->num_seqs, T = dims->num_tokens, Hq = dims->num_q_heads;
   const int pack = cb::pre_pack(Hq / dims->num_kv_heads);
   const int LT = cb::pre_tokens(S, T, Hq);
-  return cb::pre_layout(cb::pre_records(S, T, pack), LT, LT + cb::pre_second(S, T), T, Hq, dims->head_dim,
-                        num_groups, pack).total;
+  return cb::pre_layout(S, cb::pre_records(S, T, pack), LT, T, Hq, dims->head_dim, num_groups, pack,
+                        cb::pre_second(S, T)).total;
 }
 
 cb_status cb_shared_prefix_attention(const void* q, const void* k_pages, const void* v_pages,

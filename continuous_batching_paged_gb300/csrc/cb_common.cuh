@@ -185,13 +185,13 @@ struct PreToken {
   } chain[2];
 };
 
-// Sections of the workspace behind ws_layout's (all 256-byte aligned).  R: pre_records, LT: pre_tokens,
-// LB: LT + pre_second.
+// Sections of the workspace behind ws_layout's (all 256-byte aligned).  R: pre_records, LT: pre_tokens.
+// `second` (pre_second) counts for the total alone, so that the kernels need not know it.
 struct PreLayout {
-  size_t rec, cnt, first, map, cost, group, tok, base_ml, base_o, cut_ml, cut_o, total;
+  size_t rec, cnt, first, map, cost, group, tok, cut_ml, cut_o, base_ml, base_o, total;
 };
-__host__ __device__ inline PreLayout pre_layout(int R, int LT, int LB, int T, int Hq, int D, int NG,
-                                               int pack) {
+__host__ __device__ inline PreLayout pre_layout(int S, int R, int LT, int T, int Hq, int D, int NG,
+                                               int pack, int second = 0) {
   PreLayout L;
   size_t off = ws_layout(R, T, Hq, D, pack).total;
   // per decode record: keys of the prefix computed apart and query tokens, or zeros
@@ -204,15 +204,16 @@ __host__ __device__ inline PreLayout pre_layout(int R, int LT, int LB, int T, in
   L.cost = off;    off = align_up(off + sizeof(int32_t) * (size_t)(NG + 1), 256);
   L.group = off;   off = align_up(off + sizeof(PreGroup) * (size_t)(NG + kPrePlanThreads + 1), 256);
   L.tok = off;     off = align_up(off + sizeof(PreToken) * (size_t)(LT + 1), 256);
-  // Partial results of a chain: the part with its first K/V tile in a row per (token list entry, query
-  // head), for an entry's second chain LT entries further (the groups' members, who have those, are
-  // listed first); and a part that a CTA's range begins with in the CTA's own 2 x 128 rows.
-  const size_t base_rows = (size_t)LB * (size_t)Hq;
-  L.base_ml = off; off = align_up(off + sizeof(float2) * base_rows, 256);
-  L.base_o = off;  off = align_up(off + sizeof(float) * base_rows * (size_t)D, 256);
+  // Partial results of a chain: a part that a CTA's range begins with in the CTA's own 2 x 128 rows, the
+  // part with the chain's first K/V tile in a row per (token list entry, query head), for an entry's
+  // second chain LT entries further (the groups' members, who have those, are listed first).
   const size_t cut_rows = (size_t)kMaxPreCtas * 2 * kPrefillTileM;
   L.cut_ml = off;  off = align_up(off + sizeof(float2) * cut_rows, 256);
   L.cut_o = off;   off = align_up(off + sizeof(float) * cut_rows * (size_t)D, 256);
+  const size_t ml_rows = (size_t)LT * (size_t)(S <= kPrePlanThreads ? 2 : 1) * (size_t)Hq;
+  L.base_ml = off; off = align_up(off + sizeof(float2) * ml_rows, 256);
+  L.base_o = off;
+  off = align_up(off + sizeof(float) * (size_t)(LT + second) * (size_t)Hq * (size_t)D, 256);
   L.total = off;
   return L;
 }

@@ -559,7 +559,7 @@ __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensor
     int2 pre = make_int2(0, 0);
     if constexpr (kPre) {  // and with a prefix computed apart, at the one holding its end
       pre = reinterpret_cast<const int2*>(
-          a.ws + pre_layout(a.R, a.LT, a.LB, a.T, a.Hq, a.D, a.NG, a.pack).rec)[d];
+          a.ws + pre_layout(a.S, a.R, a.LT, a.T, a.Hq, a.D, a.NG, a.pack).rec)[d];
       lo_key = pre.x;
     }
     const int first_tile_key = lo_key / kDecodeTileKeys * kDecodeTileKeys;

@@ -220,7 +220,7 @@ __device__ __forceinline__ int plan_prefixes(const AttnArgs& a, int (*sw)[4], in
                                              int32_t* first, int32_t* map, int32_t* cost,
                                              const int32_t* lens,
                                              PreSeq& mine, int& period) {
-  const PreLayout PL = pre_layout(a.R, a.LT, a.LB, a.T, a.Hq, a.D, a.NG, a.pack);
+  const PreLayout PL = pre_layout(a.S, a.R, a.LT, a.T, a.Hq, a.D, a.NG, a.pack);
   PreGroup* groups = reinterpret_cast<PreGroup*>(a.ws + PL.group);
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D, a.pack).header);
   const int tid = threadIdx.x;
@@ -476,7 +476,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
   float my_keys = 0.f, my_pairs = 0.f;  // work estimates for the decode / chunk balance
   // shared prefixes: their work per KV head, and per group number what plan_prefixes finds
   int pre_cost = 0, period = 1;
-  const PreLayout PL = kPre ? pre_layout(a.R, a.LT, a.LB, a.T, a.Hq, a.D, a.NG, a.pack) : PreLayout{};
+  const PreLayout PL = kPre ? pre_layout(a.S, a.R, a.LT, a.T, a.Hq, a.D, a.NG, a.pack) : PreLayout{};
   const bool few = a.NG <= kPlanSmemGroups;
   int32_t* grp_cnt = few ? s_groups : reinterpret_cast<int32_t*>(a.ws + PL.cnt);
   int32_t* grp_first = few ? s_groups + kPlanSmemGroups : reinterpret_cast<int32_t*>(a.ws + PL.first);

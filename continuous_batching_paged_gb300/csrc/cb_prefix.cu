@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kMergeThreads, HP * kC > 16 ? 1 : 2)
   allow_dependent_launch();
   const int lane = threadIdx.x & 31;
   const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, a.pack);
-  const PreLayout PL = pre_layout(a.R, a.LT, a.LB, a.T, a.Hq, a.D, a.NG, a.pack);
+  const PreLayout PL = pre_layout(a.S, a.R, a.LT, a.T, a.Hq, a.D, a.NG, a.pack);
   const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.ws + L.header);
   const int4* list = reinterpret_cast<const int4*>(a.ws + PL.tok);
   __nv_bfloat16* outg = static_cast<__nv_bfloat16*>(a.out);

@@ -57,7 +57,7 @@ __device__ __forceinline__ void prefix_cta(const AttnArgs& a, const CUtensorMap*
   constexpr int NS = SM::kSlots;
   PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D, a.pack).header);
   const int N = hdr->pre_ctas;
-  const PreLayout PL = pre_layout(a.R, a.LT, a.LB, a.T, a.Hq, a.D, a.NG, a.pack);
+  const PreLayout PL = pre_layout(a.S, a.R, a.LT, a.T, a.Hq, a.D, a.NG, a.pack);
   const PreToken* list = reinterpret_cast<const PreToken*>(a.ws + PL.tok);
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
