@@ -78,8 +78,8 @@ def extension_is_stale() -> bool:
     try:
         with open(_ext_stamp_path()) as f:
             return f.read() != _ext_stamp()
-    except FileNotFoundError:
-        return True
+    except FileNotFoundError:  # (built files that came without the build's folder)
+        return False
 
 
 def is_stale() -> bool:

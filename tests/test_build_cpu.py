@@ -86,3 +86,12 @@ def test_extension_is_rebuilt_for_another_torch_or_python(here, monkeypatch):
     assert not _build.is_stale()
     monkeypatch.setattr(sys, "version", sys.version + " of another build")
     assert _build.is_stale() and not _build.library_is_stale()
+
+
+def test_built_files_are_enough(here):
+    # an installation that has the two libraries and not the build's folder compiles nothing
+    _build.build()
+    for f in (here / "_build").iterdir():
+        f.unlink()
+    (here / "_build").rmdir()
+    assert not _build.is_stale()
