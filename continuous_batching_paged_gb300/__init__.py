@@ -25,6 +25,8 @@ __all__ = [
     "check_device_error", "status_string", "copy_blocks", "kv_offload", "kv_restore",
     "append_attention", "selftest_wait_timeout", "CbRope", "rope_append",
     "CbPrefix", "shared_prefix_attention", "rope_append_attention", "prefix_workspace_size",
+    "CbScore", "scored_attention", "quant_append", "quant_gather", "quant_attention",
+    "quant_append_attention",
 ]
 
 CB_OK = 0
@@ -73,6 +75,12 @@ class CbPrefix(ctypes.Structure):
                 ("reserved", ctypes.c_int64 * 2)]
 
 
+class CbScore(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("reserved32", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("visible_lens", ctypes.c_void_p),
+                ("reserved", ctypes.c_int64 * 2)]
+
+
 class CbError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str = ""):
         self.status = status
@@ -113,6 +121,20 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.cb_rope_append_attention.argtypes = [_P] * 9 + [
         ctypes.c_int32, ctypes.c_float, ctypes.POINTER(CbRope), ctypes.POINTER(CbPrefix)] + attn[8:] + [
         ctypes.POINTER(CbOptions), _P]
+    score, options = ctypes.POINTER(CbScore), ctypes.POINTER(CbOptions)
+    lib.cb_scored_attention.restype = ctypes.c_int
+    lib.cb_scored_attention.argtypes = attn[:8] + [score] + attn[8:] + [options, _P]
+    lib.cb_quant_append.restype = ctypes.c_int
+    lib.cb_quant_append.argtypes = [_P] * 10 + [
+        ctypes.c_int32, ctypes.POINTER(CbRope), ctypes.POINTER(CbDims), _P]
+    lib.cb_quant_gather.restype = ctypes.c_int
+    lib.cb_quant_gather.argtypes = [_P] * 6 + [ctypes.c_int32, _P, _P, ctypes.POINTER(CbDims), _P]
+    lib.cb_quant_attention.restype = ctypes.c_int
+    lib.cb_quant_attention.argtypes = [_P] * 7 + [ctypes.c_int32, ctypes.c_float, score] + attn[8:] + [
+        options, _P]
+    lib.cb_quant_append_attention.restype = ctypes.c_int
+    lib.cb_quant_append_attention.argtypes = [_P] * 10 + [
+        ctypes.c_int32, ctypes.c_float, ctypes.POINTER(CbRope), score] + attn[8:] + [options, _P]
     lib.cb_ragged_paged_attention.restype = ctypes.c_int
     lib.cb_ragged_paged_attention.argtypes = attn + [_P]
     lib.cb_ragged_paged_attention_ex.restype = ctypes.c_int
@@ -326,22 +348,39 @@ def _explain_int(name, x) -> None:
     _require(-2**31 <= operator.index(x) < 2**31, f"{name} must be a 32-bit integer")
 
 
+def _check_codes(name, t):
+    import torch
+    _require(t.dtype == torch.float8_e4m3fn, f"{name} must be float8_e4m3fn")
+    _require(t.is_cuda and t.is_contiguous(), f"{name} must be a contiguous CUDA tensor")
+    _require(t.dim() == 4, f"{name} must have 4 dimensions")
+
+
+def _check_scales(kv_scales, k_pages):
+    import torch
+    _require(kv_scales.dtype == torch.uint8 and kv_scales.is_cuda and kv_scales.is_contiguous()
+             and tuple(kv_scales.shape) == (*k_pages.shape[:3], 2)
+             and kv_scales.get_device() == k_pages.get_device(),
+             "kv_scales must be a contiguous uint8 CUDA tensor [P, block_size, Hkv, 2] beside the pages")
+
+
 def _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
-                  cos_sin) -> None:
+                  cos_sin, kv_scales=None) -> None:
     """Raise the error of a step's inputs that failed their check (k_new, v_new and cos_sin: None
-    where the call takes none; q: None where it may be left out)."""
+    where the call takes none; q: None where it may be left out; kv_scales: a quantised cache's)."""
     import torch
     if cos_sin is not None:
         _require(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_cuda
                  and cos_sin.is_contiguous(),
                  "cos_sin must be a contiguous fp32 CUDA tensor [max_positions, rot_dim]")
-        for name, t in (("q", q), ("k_new", k_new), ("v_new", v_new)):
+    if cos_sin is not None or (kv_scales is not None and k_new is not None):
+        for name, t in (("q", q if cos_sin is not None else None), ("k_new", k_new), ("v_new", v_new)):
             if t is not None:
                 _explain_rows(name, t)
-    else:
+    if cos_sin is None and (q is not None or kv_scales is None):
         _check_bf16("q", q, 3)
-    _check_bf16("k_pages", k_pages, 4)
-    _check_bf16("v_pages", v_pages, 4)
+    check_pages = _check_codes if kv_scales is not None else lambda name, t: _check_bf16(name, t, 4)
+    check_pages("k_pages", k_pages)
+    check_pages("v_pages", v_pages)
     _check_meta(block_table, cu_seqlens_q, kv_lens)
     P, bs, Hkv, D = k_pages.shape
     _explain_int("block_size", block_size)
@@ -356,6 +395,8 @@ def _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, 
     dev = torch.cuda.current_device()
     for t in (q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, cos_sin):
         _require(t is None or t.get_device() == dev, "every tensor must be on the current CUDA device")
+    if kv_scales is not None:
+        _check_scales(kv_scales, k_pages)
 
 
 def _on_stream(stream):
@@ -593,6 +634,185 @@ def rope_append_attention(q, k_new, v_new, k_pages, v_pages, block_table, cu_seq
         raise ValueError("rope_append_attention: bad argument")
     if r.__class__ is int:
         _check(r, "cb_rope_append_attention")
+    return r
+
+
+def _explain_score(q, num_seqs, softcap, slopes, visible_lens) -> None:
+    """Raise the error of the arguments that change the scores."""
+    import torch
+    _require(isinstance(softcap, (int, float)) or hasattr(softcap, "__float__"),
+             "softcap must be a number")
+    dev = q.get_device()
+    if slopes is not None:
+        _require(slopes.dtype == torch.float32 and slopes.is_cuda and slopes.is_contiguous()
+                 and tuple(slopes.shape) == (q.shape[1],) and slopes.get_device() == dev,
+                 "slopes must be a contiguous fp32 CUDA tensor [Hq]")
+    if visible_lens is not None:
+        _check_ids("visible_lens", visible_lens)
+        _require(tuple(visible_lens.shape) == (num_seqs,) and visible_lens.get_device() == dev,
+                 "visible_lens must be [num_seqs], on q's device")
+
+
+def scored_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, scale,
+                     softcap: float = 0.0, slopes=None, visible_lens=None, out=None, lse=None,
+                     workspace=None, decode_ctas: int = 0, phase_events=None, serial: bool = False,
+                     window: int = 0, stream=None):
+    """ragged_paged_attention with changed scores and masks (cb_scored_attention): capped,
+    ``softcap * tanh(score / softcap)`` (softcap 0: not); biased by distance, ``slopes[h] * (key -
+    position)`` with slopes fp32 [Hq]; and with a prefix that is read both ways, the first
+    ``visible_lens[s]`` keys (int32 [num_seqs]) of sequence s seen by all its queries.  ``window``
+    goes with the first two, not with visible_lens; the other arguments are
+    ragged_paged_attention's."""
+    if stream is not None:
+        with _on_stream(stream):
+            return scored_attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                                    block_size, scale, softcap, slopes, visible_lens, out, lse,
+                                    workspace, decode_ctas, phase_events, serial, window)
+    r = (_ext or _native()).scored_attention(
+        k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, None, q, scale, softcap,
+        slopes, visible_lens, None, None, out, lse, workspace, decode_ctas, serial, window,
+        _event_handles(phase_events))
+    if r is NotImplemented:
+        _explain_step(q, None, None, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
+                      None)
+        _explain_score(q, kv_lens.numel(), softcap, slopes, visible_lens)
+        _explain_tail(q, kv_lens.numel(), None, None, out, lse, workspace, decode_ctas, window)
+        raise ValueError("scored_attention: bad argument")
+    if r.__class__ is int:
+        _check(r, "cb_scored_attention")
+    return r
+
+
+def quant_append(q, k_new, v_new, k_pages, v_pages, kv_scales, block_table, cu_seqlens_q, kv_lens,
+                 block_size, cos_sin=None, interleaved: bool = False, q_out=None, stream=None):
+    """rope_append into a quantised cache (cb_quant_append): the keys, rotated, and the values are
+    stored as e4m3 codes with a power-of-two scale per token and KV head; returns q rotated, in bf16.
+    Without cos_sin nothing is rotated, and q must be None.  The cache, three tensors:
+
+        k_pages = torch.zeros(P, block_size, Hkv, D, device="cuda").to(torch.float8_e4m3fn)
+        v_pages = k_pages.clone()
+        kv_scales = torch.zeros(P, block_size, Hkv, 2, dtype=torch.uint8, device="cuda")
+    """
+    if stream is not None:
+        with _on_stream(stream):
+            return quant_append(q, k_new, v_new, k_pages, v_pages, kv_scales, block_table, cu_seqlens_q,
+                                kv_lens, block_size, cos_sin, interleaved, q_out)
+    r = (_ext or _native()).quant_append(k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
+                                         kv_scales, q, k_new, v_new, cos_sin, interleaved, q_out)
+    if r is NotImplemented:
+        _require(kv_scales is not None, "kv_scales must be given")
+        _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                      block_size, cos_sin, kv_scales)
+        _require(q is not None or q_out is None, "q_out without q")
+        if q_out is not None:
+            _check_output(q_out, "q_out", tuple(q.shape), q.get_device())
+        raise ValueError("quant_append: bad argument")
+    if r.__class__ is int:
+        _check(r, "cb_quant_append")
+    return r
+
+
+def quant_gather(k_pages, v_pages, kv_scales, block_table, cu_seqlens_k, block_size, num_rows,
+                 key_starts=None, k_out=None, v_out=None, stream=None):
+    """Read ranges of a quantised cache back as bf16 (cb_quant_gather): rows cu_seqlens_k[s] ..
+    cu_seqlens_k[s + 1] - 1 of the two results [num_rows, Hkv, D] are the keys (values) of sequence s
+    from key_starts[s] (default 0) on; rows behind the last sequence's are not written.  num_rows: a
+    Python integer, at least cu_seqlens_k[-1]."""
+    if stream is not None:
+        with _on_stream(stream):
+            return quant_gather(k_pages, v_pages, kv_scales, block_table, cu_seqlens_k, block_size,
+                                num_rows, key_starts, k_out, v_out)
+    r = (_ext or _native()).quant_gather(k_pages, v_pages, block_table, cu_seqlens_k, block_size,
+                                         kv_scales, key_starts, num_rows, k_out, v_out)
+    if r is NotImplemented:
+        import torch
+        _check_codes("k_pages", k_pages)
+        _check_codes("v_pages", v_pages)
+        _require(k_pages.shape == v_pages.shape, "v_pages must match k_pages")
+        _check_scales(kv_scales, k_pages)
+        for name, t in (("block_table", block_table), ("cu_seqlens_k", cu_seqlens_k),
+                        ("key_starts", key_starts)):
+            if t is not None:
+                _check_ids(name, t)
+        _require(block_table.dim() == 2, "block_table must be [num_seqs, max_blocks]")
+        S = block_table.shape[0]
+        _require(cu_seqlens_k.numel() == S + 1, "cu_seqlens_k must have num_seqs + 1 entries")
+        _require(key_starts is None or key_starts.numel() == S, "key_starts must have num_seqs entries")
+        _explain_int("block_size", block_size)
+        _require(k_pages.shape[1] == block_size, "k_pages must be [P, block_size, Hkv, D]")
+        _explain_int("num_rows", num_rows)
+        _require(operator.index(num_rows) >= 0, "num_rows must not be negative")
+        dev = torch.cuda.current_device()
+        for t in (k_pages, v_pages, block_table, cu_seqlens_k, key_starts):
+            _require(t is None or t.get_device() == dev, "every tensor must be on the current CUDA device")
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is not None:
+                _check_output(t, name, (num_rows, *k_pages.shape[2:]), dev)
+        raise ValueError("quant_gather: bad argument")
+    if r.__class__ is int:
+        _check(r, "cb_quant_gather")
+    return r
+
+
+def quant_attention(q, k_pages, v_pages, kv_scales, block_table, cu_seqlens_q, kv_lens, block_size,
+                    scale, softcap: float = 0.0, slopes=None, visible_lens=None, out=None, lse=None,
+                    workspace=None, decode_ctas: int = 0, phase_events=None, serial: bool = False,
+                    window: int = 0, stream=None):
+    """ragged_paged_attention over a quantised cache (cb_quant_attention); softcap, slopes and
+    visible_lens as in scored_attention, the other arguments as in ragged_paged_attention."""
+    if stream is not None:
+        with _on_stream(stream):
+            return quant_attention(q, k_pages, v_pages, kv_scales, block_table, cu_seqlens_q, kv_lens,
+                                   block_size, scale, softcap, slopes, visible_lens, out, lse,
+                                   workspace, decode_ctas, phase_events, serial, window)
+    _require(kv_scales is not None, "kv_scales must be given")
+    r = (_ext or _native()).scored_attention(
+        k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, kv_scales, q, scale, softcap,
+        slopes, visible_lens, None, None, out, lse, workspace, decode_ctas, serial, window,
+        _event_handles(phase_events))
+    if r is NotImplemented:
+        _require(q is not None, "q must be given")
+        _explain_step(q, None, None, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,
+                      None, kv_scales)
+        _explain_score(q, kv_lens.numel(), softcap, slopes, visible_lens)
+        _explain_tail(q, kv_lens.numel(), None, None, out, lse, workspace, decode_ctas, window)
+        raise ValueError("quant_attention: bad argument")
+    if r.__class__ is int:
+        _check(r, "cb_quant_attention")
+    return r
+
+
+def quant_append_attention(q, k_new, v_new, k_pages, v_pages, kv_scales, block_table, cu_seqlens_q,
+                           kv_lens, block_size, scale, cos_sin=None, interleaved: bool = False,
+                           softcap: float = 0.0, slopes=None, visible_lens=None, q_out=None, out=None,
+                           lse=None, workspace=None, decode_ctas: int = 0, phase_events=None,
+                           serial: bool = False, window: int = 0, stream=None):
+    """One layer's attention step on a quantised cache (cb_quant_append_attention): quant_append,
+    then quant_attention on the rotated queries (without cos_sin: on q, [T, Hq, D] contiguous), same
+    results, in two launches.  q_out: where the rotated queries go (default: a temporary)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return quant_append_attention(q, k_new, v_new, k_pages, v_pages, kv_scales, block_table,
+                                          cu_seqlens_q, kv_lens, block_size, scale, cos_sin, interleaved,
+                                          softcap, slopes, visible_lens, q_out, out, lse, workspace,
+                                          decode_ctas, phase_events, serial, window)
+    r = (_ext or _native()).quant_append_attention(
+        k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, kv_scales, q, k_new, v_new,
+        cos_sin, interleaved, q_out, scale, softcap, slopes, visible_lens, None, None, out, lse, workspace,
+        decode_ctas, serial, window, _event_handles(phase_events))
+    if r is NotImplemented:
+        _require(q is not None, "q must be given")
+        _require(kv_scales is not None, "kv_scales must be given")
+        _explain_step(q, k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                      block_size, cos_sin, kv_scales)
+        _require(cos_sin is not None or q_out is None, "q_out without cos_sin")
+        if q_out is not None:
+            _check_output(q_out, "q_out", tuple(q.shape), q.get_device())
+        _explain_score(q, kv_lens.numel(), softcap, slopes, visible_lens)
+        _explain_tail(q, kv_lens.numel(), None, None, out, lse, workspace, decode_ctas, window)
+        raise ValueError("quant_append_attention: bad argument")
+    if r.__class__ is int:
+        _check(r, "cb_quant_append_attention")
     return r
 
 

@@ -10,6 +10,7 @@
 
 #include "cb_common.cuh"
 #include "cb_launch.h"
+#include "cb_quant_shape.h"
 
 namespace {
 
@@ -177,17 +178,29 @@ bool overlap(const void* a, long long na, const void* b, long long nb) {
 }
 
 // Checks of cb_rope and of the tensors it applies to (non-empty batch), and the kernel's arguments.
+// optional: rope may be NULL, or without a table (keys are stored as they are; no q).
 cb_status rope_args(const void* q, void* q_out, const cb_rope* rope, const cb::AppendArgs& ap,
-                    int Hq, cb::RopeArgs* out) {
-  if (rope == nullptr) return fail(CB_ERR_INVALID_ARG, "rope is NULL");
+                    int Hq, cb::RopeArgs* out, bool optional = false) {
+  const cb_rope none = {};
+  if (rope == nullptr) {
+    if (!optional) return fail(CB_ERR_INVALID_ARG, "rope is NULL");
+    rope = &none;
+  }
+  const bool rotates = !optional || rope->cos_sin != nullptr;
   if ((q == nullptr) != (q_out == nullptr) || !ap.k_new || !ap.v_new || !ap.k_pages ||
-      !ap.v_pages || !ap.block_table || !ap.cu_seqlens_q || !ap.kv_lens || !rope->cos_sin)
+      !ap.v_pages || !ap.block_table || !ap.cu_seqlens_q || !ap.kv_lens ||
+      (rotates && !rope->cos_sin))
     return fail(CB_ERR_INVALID_ARG, "null pointer argument");
+  if (!rotates && q != nullptr)
+    return fail(CB_ERR_INVALID_ARG, "q is rotated or left out: q without cos_sin");
+  if (!rotates && (rope->rot_dim != 0 || rope->interleaved != 0))
+    return fail(CB_ERR_INVALID_ARG, "rot_dim and interleaved must be 0 without cos_sin");
   if (!aligned16(q) || !aligned16(q_out) || !aligned16(ap.k_new) || !aligned16(ap.v_new) ||
       !aligned16(ap.k_pages) || !aligned16(ap.v_pages) || !aligned16(rope->cos_sin))
     return fail(CB_ERR_INVALID_ARG, "q, K/V tensors and cos_sin must be 16-byte aligned");
-  if (rope->max_positions < 1) return fail(CB_ERR_INVALID_ARG, "max_positions must be >= 1");
-  if (rope->rot_dim < 16 || rope->rot_dim > ap.D || rope->rot_dim % 16 != 0)
+  if (rotates && rope->max_positions < 1)
+    return fail(CB_ERR_INVALID_ARG, "max_positions must be >= 1");
+  if (rotates && (rope->rot_dim < 16 || rope->rot_dim > ap.D || rope->rot_dim % 16 != 0))
     return fail(CB_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [16, %d], got %d", ap.D,
                 rope->rot_dim);
   if (rope->interleaved != 0 && rope->interleaved != 1)
@@ -235,6 +248,61 @@ cb_status encode_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1,
   if (r != CUDA_SUCCESS) return fail(CB_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return CB_OK;
 }
+
+// 3-D map of a pool of codes, one byte each: boxes of whole head rows, box1 x box2 of them, with the
+// swizzle of the row's width (128 or 64 bytes).
+cb_status encode_code_map(CUtensorMap* m, const void* base, uint64_t D, uint64_t rows, uint64_t heads,
+                          uint32_t box1, uint32_t box2) {
+  const cuuint64_t dims[3] = {D, rows, heads};
+  const cuuint64_t strides[2] = {D * heads, D};
+  const cuuint32_t box[3] = {(cuuint32_t)D, box1, box2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(CB_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return CB_OK;
+}
+
+// Checks of cb_score, and the kernels' arguments.  *on: something is to be changed.
+cb_status score_args(const cb_score* score, const cb_options* options, float scale,
+                     cb::ScoreArgs* out, bool* on) {
+  *out = cb::ScoreArgs{};
+  *on = options != nullptr && options->window > 0;
+  if (score == nullptr) return CB_OK;
+  const float cap = score->softcap;
+  if (!(cap >= 0.f) || cap > 1e30f)
+    return fail(CB_ERR_INVALID_ARG, "softcap must be 0 (none) or a positive finite number");
+  if ((reinterpret_cast<uintptr_t>(score->slopes) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(score->visible_lens) & 3u) != 0)
+    return fail(CB_ERR_INVALID_ARG, "slopes and visible_lens must be 4-byte aligned");
+  if (score->visible_lens != nullptr && *on)
+    return fail(CB_ERR_UNSUPPORTED, "visible_lens with a sliding window");
+  if (cap > 0.f) {
+    out->cap_in = (float)(2.0 * 1.4426950408889634 * (double)scale / (double)cap);
+    out->cap_out = cap * 1.4426950408889634f;
+    if (!(out->cap_in > 0.f) || out->cap_in > 1e30f)
+      return fail(CB_ERR_INVALID_ARG, "scale / softcap is out of range");
+  }
+  out->slopes = score->slopes;
+  out->visible = score->visible_lens;
+  *on = *on || cap > 0.f || score->slopes != nullptr || score->visible_lens != nullptr;
+  return CB_OK;
+}
+
+cb_status check_scales(const void* kv_scales) {
+  if (kv_scales == nullptr) return fail(CB_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned16(kv_scales)) return fail(CB_ERR_INVALID_ARG, "kv_scales must be 16-byte aligned");
+  return CB_OK;
+}
+
+// What an attention call has beside the plain one's arguments.
+struct Extra {
+  const cb::ScoreArgs* score = nullptr;        // changed scores and masks
+  const void* kv_scales = nullptr;             // the quantised cache's
+  const cb::QuantAppendArgs* append = nullptr; // and the append of the same step
+};
 
 }  // namespace
 
@@ -335,7 +403,8 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
                            float* lse, void* workspace, size_t workspace_bytes,
                            const cb_dims* dims, const cb_options* options,
                            const cb::AppendArgs* app, const cb::RopeArgs* rope,
-                           const cb_prefix* prefix, void* stream) {
+                           const cb_prefix* prefix, void* stream, const Extra& extra = Extra{}) {
+  const bool quant = extra.kv_scales != nullptr;
   cb_status st = check_dims(dims, block_size);
   if (st != CB_OK) return st;
   if (dims->num_tokens == 0) return CB_OK;
@@ -374,7 +443,8 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
     return fail(CB_ERR_UNSUPPORTED, "num_kv_heads > %d must be a multiple of %d", dec_heads,
                 dec_heads);
   const long long n_q = (long long)dims->num_tokens * Hq * dims->head_dim;
-  if ((rope != nullptr || prefix != nullptr) && overlap(q, n_q, out, n_q))
+  if ((rope != nullptr || prefix != nullptr || quant || extra.score != nullptr) &&
+      overlap(q, n_q, out, n_q))
     return fail(CB_ERR_INVALID_ARG, "out overlaps the queries that the attention reads");
   DeviceState* ds = nullptr;
   st = device_state(&ds);
@@ -421,14 +491,26 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   cb::AttnMaps maps;
   const uint64_t D = (uint64_t)a.D;
   const uint64_t rows = (uint64_t)a.P * (uint64_t)block_size;
+  cb::QuantArgs qa = {};
+  cb::QuantMaps qmaps;
   // Decode pass: dims (d, token, head) so one box {64, KB tokens, up to 8 heads} lands in shared
   // memory as [head][token] rows; chunk pass: dims (d, head, token), box {64, 1 head, KBp tokens}.
   const uint32_t HB = (uint32_t)(Hkv < dec_heads ? Hkv : dec_heads);
-  if ((st = encode_map(&maps.k_dec, k_pages, D, rows, Hkv, D * 2 * Hkv, D * 2, a.KB, HB)) != CB_OK) return st;
-  if ((st = encode_map(&maps.v_dec, v_pages, D, rows, Hkv, D * 2 * Hkv, D * 2, a.KB, HB)) != CB_OK) return st;
-  if ((st = encode_map(&maps.k_chunk, k_pages, D, Hkv, rows, D * 2, D * 2 * Hkv, 1, a.KBp)) != CB_OK) return st;
-  if ((st = encode_map(&maps.v_chunk, v_pages, D, Hkv, rows, D * 2, D * 2 * Hkv, 1, a.KBp)) != CB_OK) return st;
   if ((st = encode_map(&maps.q, q, D, Hq, (uint64_t)a.T, D * 2, D * 2 * Hq, 1, 128)) != CB_OK) return st;
+  if (quant) {
+    qa = cb::quant_shape(block_size, Hkv, G, a.D);
+    qa.k_pages = static_cast<const uint8_t*>(k_pages);
+    qa.v_pages = static_cast<const uint8_t*>(v_pages);
+    qa.scales = static_cast<const uint8_t*>(extra.kv_scales);
+    qmaps.q = maps.q;
+    if ((st = encode_code_map(&qmaps.k, k_pages, D, rows, Hkv, qa.KB, HB)) != CB_OK) return st;
+    if ((st = encode_code_map(&qmaps.v, v_pages, D, rows, Hkv, qa.KB, HB)) != CB_OK) return st;
+  } else {
+    if ((st = encode_map(&maps.k_dec, k_pages, D, rows, Hkv, D * 2 * Hkv, D * 2, a.KB, HB)) != CB_OK) return st;
+    if ((st = encode_map(&maps.v_dec, v_pages, D, rows, Hkv, D * 2 * Hkv, D * 2, a.KB, HB)) != CB_OK) return st;
+    if ((st = encode_map(&maps.k_chunk, k_pages, D, Hkv, rows, D * 2, D * 2 * Hkv, 1, a.KBp)) != CB_OK) return st;
+    if ((st = encode_map(&maps.v_chunk, v_pages, D, Hkv, rows, D * 2, D * 2 * Hkv, 1, a.KBp)) != CB_OK) return st;
+  }
   cb::PrefixMaps pm;
   if (NG > 0) {
     const uint64_t T = (uint64_t)a.T, tok = D * 2 * Hq;
@@ -436,6 +518,8 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
     if ((st = encode_map(&pm.q_run, q, D, Hq, T, D * 2, tok, G, cb::pre_tile_tokens(G))) != CB_OK) return st;
   }
   auto launch_pass = [&](const cb::AttnArgs& x, cudaStream_t on) {
+    if (quant) return cb::launch_quant_attention(x, qa, extra.score, qmaps, on);
+    if (extra.score != nullptr) return cb::launch_scored_attention(x, *extra.score, maps, on);
     return NG > 0 ? cb::launch_prefix_attention(x, maps, pm, on) : cb::launch_attention(x, maps, on);
   };
 
@@ -456,7 +540,22 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
     ra = *rope;
     ra.ap.err = ds->err;
   }
-  if (rope != nullptr && !serial) {
+  cb::QuantAppendArgs xa;
+  if (extra.append != nullptr) {
+    xa = *extra.append;
+    xa.r.ap.err = ds->err;
+  }
+  if (extra.append != nullptr && !serial) {
+    // One launch quantises, appends and plans, as below.
+    if ((e = mark(0)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord(phase event)");
+    if ((e = cb::launch_quant_append_plan(xa, a, qa, ds->sm_count, s)) != cudaSuccess)
+      return cuda_fail(e, "quantising append + plan launch");
+  } else if (quant) {
+    if (extra.append != nullptr && (e = cb::launch_quant_append(xa, ds->sm_count, s)) != cudaSuccess)
+      return cuda_fail(e, "quant_append launch");
+    if ((e = mark(0)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord(phase event)");
+    if ((e = cb::launch_quant_plan(a, qa, s)) != cudaSuccess) return cuda_fail(e, "plan launch");
+  } else if (rope != nullptr && !serial) {
     // One launch rotates, appends and plans, as below.
     if ((e = mark(0)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord(phase event)");
     if ((e = cb::launch_rope_plan(ra, a, ds->sm_count, s)) != cudaSuccess)
@@ -589,6 +688,147 @@ cb_status cb_rope_append_attention(const void* q, const void* k_new, const void*
   if (st != CB_OK) return st;
   return attention(q_out, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, scale,
                    out, lse, workspace, workspace_bytes, dims, options, nullptr, &r, prefix, stream);
+}
+
+cb_status cb_scored_attention(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* block_table, const int32_t* cu_seqlens_q,
+                              const int32_t* kv_lens, int32_t block_size, float scale,
+                              const cb_score* score, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, const cb_dims* dims,
+                              const cb_options* options, void* stream) {
+  t_last_error.clear();
+  if (score == nullptr) return fail(CB_ERR_INVALID_ARG, "score is NULL");
+  cb::ScoreArgs sc;
+  bool on;
+  cb_status st = score_args(score, options, scale, &sc, &on);
+  if (st != CB_OK) return st;
+  Extra x;
+  x.score = &sc;
+  return attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, scale, out,
+                   lse, workspace, workspace_bytes, dims, options, nullptr, nullptr, nullptr, stream,
+                   x);
+}
+
+cb_status cb_quant_append(const void* q, const void* k_new, const void* v_new, void* q_out,
+                          void* k_pages, void* v_pages, void* kv_scales, const int32_t* block_table,
+                          const int32_t* cu_seqlens_q, const int32_t* kv_lens, int32_t block_size,
+                          const cb_rope* rope, const cb_dims* dims, void* stream) {
+  t_last_error.clear();
+  cb_status st = check_dims(dims, block_size);
+  if (st != CB_OK) return st;
+  if (dims->num_tokens == 0 || dims->num_seqs == 0) return CB_OK;  // no token but padding rows
+  cb::QuantAppendArgs x;
+  st = rope_args(q, q_out, rope,
+                 append_args(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                             block_size, dims),
+                 dims->num_q_heads, &x.r, true);
+  if (st != CB_OK) return st;
+  if ((st = check_scales(kv_scales)) != CB_OK) return st;
+  x.scales = static_cast<uint8_t*>(kv_scales);
+  DeviceState* ds = nullptr;
+  st = device_state(&ds);
+  if (st != CB_OK) return st;
+  x.r.ap.err = ds->err;
+  cudaError_t e = cb::launch_quant_append(x, ds->sm_count, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "quant_append launch");
+  return CB_OK;
+}
+
+cb_status cb_quant_gather(const void* k_pages, const void* v_pages, const void* kv_scales,
+                          const int32_t* block_table, const int32_t* cu_seqlens_k,
+                          const int32_t* key_starts, int32_t block_size, void* k_out, void* v_out,
+                          const cb_dims* dims, void* stream) {
+  t_last_error.clear();
+  cb_status st = check_dims(dims, block_size);
+  if (st != CB_OK) return st;
+  if (dims->num_tokens == 0 || dims->num_seqs == 0) return CB_OK;
+  if (!k_pages || !v_pages || !block_table || !cu_seqlens_k || !k_out || !v_out)
+    return fail(CB_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_out) || !aligned16(v_out))
+    return fail(CB_ERR_INVALID_ARG, "pages and outputs must be 16-byte aligned");
+  if ((st = check_scales(kv_scales)) != CB_OK) return st;
+  const long long n = (long long)dims->num_tokens * dims->num_kv_heads * dims->head_dim;
+  if (overlap(k_out, n, v_out, n)) return fail(CB_ERR_INVALID_ARG, "k_out overlaps v_out");
+  DeviceState* ds = nullptr;
+  st = device_state(&ds);
+  if (st != CB_OK) return st;
+  cb::GatherArgs g;
+  g.k_pages = static_cast<const uint8_t*>(k_pages);
+  g.v_pages = static_cast<const uint8_t*>(v_pages);
+  g.scales = static_cast<const uint8_t*>(kv_scales);
+  g.block_table = block_table;
+  g.cu_seqlens_k = cu_seqlens_k;
+  g.key_starts = key_starts;
+  g.k_out = k_out;
+  g.v_out = v_out;
+  g.S = dims->num_seqs;
+  g.T = dims->num_tokens;
+  g.Hkv = dims->num_kv_heads;
+  g.D = dims->head_dim;
+  g.bs = block_size;
+  g.max_blocks = dims->max_blocks_per_seq;
+  g.P = dims->num_pages;
+  g.rows = 1;
+  g.err = ds->err;
+  cudaError_t e = cb::launch_quant_gather(g, ds->sm_count, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "quant_gather launch");
+  return CB_OK;
+}
+
+cb_status cb_quant_attention(const void* q, const void* k_pages, const void* v_pages,
+                             const void* kv_scales, const int32_t* block_table,
+                             const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                             int32_t block_size, float scale, const cb_score* score, void* out,
+                             float* lse, void* workspace, size_t workspace_bytes,
+                             const cb_dims* dims, const cb_options* options, void* stream) {
+  t_last_error.clear();
+  cb::ScoreArgs sc;
+  bool on;
+  cb_status st = score_args(score, options, scale, &sc, &on);
+  if (st != CB_OK) return st;
+  if ((st = check_dims(dims, block_size)) != CB_OK) return st;
+  if (dims->num_tokens == 0 || dims->num_seqs == 0) return CB_OK;
+  if ((st = check_scales(kv_scales)) != CB_OK) return st;
+  Extra x;
+  x.score = on ? &sc : nullptr;
+  x.kv_scales = kv_scales;
+  return attention(q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size, scale, out,
+                   lse, workspace, workspace_bytes, dims, options, nullptr, nullptr, nullptr, stream,
+                   x);
+}
+
+cb_status cb_quant_append_attention(const void* q, const void* k_new, const void* v_new, void* q_out,
+                                    void* k_pages, void* v_pages, void* kv_scales,
+                                    const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                    const int32_t* kv_lens, int32_t block_size, float scale,
+                                    const cb_rope* rope, const cb_score* score, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    const cb_dims* dims, const cb_options* options, void* stream) {
+  t_last_error.clear();
+  cb::ScoreArgs sc;
+  bool on;
+  cb_status st = score_args(score, options, scale, &sc, &on);
+  if (st != CB_OK) return st;
+  if ((st = check_dims(dims, block_size)) != CB_OK) return st;
+  if (dims->num_tokens == 0 || dims->num_seqs == 0) return CB_OK;
+  const bool rotates = rope != nullptr && rope->cos_sin != nullptr;
+  if (!q || (rotates && !q_out)) return fail(CB_ERR_INVALID_ARG, "null pointer argument");
+  if (!rotates && q_out != nullptr) return fail(CB_ERR_INVALID_ARG, "q_out without cos_sin");
+  cb::QuantAppendArgs ap;
+  st = rope_args(rotates ? q : nullptr, q_out, rope,
+                 append_args(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                             block_size, dims),
+                 dims->num_q_heads, &ap.r, true);
+  if (st != CB_OK) return st;
+  if ((st = check_scales(kv_scales)) != CB_OK) return st;
+  ap.scales = static_cast<uint8_t*>(kv_scales);
+  Extra x;
+  x.score = on ? &sc : nullptr;
+  x.kv_scales = kv_scales;
+  x.append = &ap;
+  return attention(rotates ? q_out : q, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens,
+                   block_size, scale, out, lse, workspace, workspace_bytes, dims, options, nullptr,
+                   nullptr, nullptr, stream, x);
 }
 
 cb_status cb_ragged_paged_attention(const void* q, const void* k_pages, const void* v_pages,

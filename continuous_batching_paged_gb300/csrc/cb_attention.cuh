@@ -23,14 +23,16 @@ struct AttnSmem {
 // kPre: the batch's shared prefixes are computed once per group (cb_prefix.cu); qmap_tok and
 // qmap_run are the tensor maps of a group's query rows, token by token and a tile of tokens (unused
 // otherwise).
-template <int D, int QS, bool kWin, bool kPre>
+// kMod: changed scores and masks (cb_score.cuh).
+template <int D, int QS, bool kWin, bool kPre, bool kMod = false>
 __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorMap* qmap,
                                               const CUtensorMap* qmap_tok,
                                               const CUtensorMap* qmap_run,
                                               const CUtensorMap* kmap_dec,
                                               const CUtensorMap* vmap_dec,
                                               const CUtensorMap* kmap_chunk,
-                                              const CUtensorMap* vmap_chunk, uint8_t* smem_raw) {
+                                              const CUtensorMap* vmap_chunk, uint8_t* smem_raw,
+                                              const ScoreArgs& sc = ScoreArgs{}) {
   // Launched as a programmatic dependent of the planner: CTAs may start while the planner's
   // launch still runs; everything below reads the plan (and the appended K/V), so wait here
   // for that launch to complete and its writes to be visible.  A no-op without the attribute.
@@ -57,11 +59,12 @@ __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorM
     // chunk role stamps its own span inside prefill_cta).
     const bool busy = hdr->dec_tiles > 0;
     if (threadIdx.x == 0 && busy) atomicMin(&hdr->t_dec_start, global_ns());
-    decode_cta<D, QS, kPre>(a, kmap_dec, vmap_dec, smem_raw, b % a.decode_ctas, b / a.decode_ctas);
+    decode_cta<D, QS, kPre, kMod>(a, kmap_dec, vmap_dec, smem_raw, b % a.decode_ctas,
+                                  b / a.decode_ctas, sc);
     if ((threadIdx.x & 31) == 0 && busy) atomicMax(&hdr->t_dec_end, global_ns());
     return;
   }
-  prefill_cta<D, kWin>(a, qmap, kmap_chunk, vmap_chunk, smem_raw);
+  prefill_cta<D, kWin, kMod>(a, qmap, kmap_chunk, vmap_chunk, smem_raw, sc);
 }
 
 }  // namespace cb

@@ -29,6 +29,7 @@
 
 #include "cb_common.cuh"
 #include "cb_launch.h"
+#include "cb_score.cuh"
 
 namespace cb {
 
@@ -166,12 +167,13 @@ __device__ __forceinline__ void merge_parts(const AttnArgs& a, const float2* par
 //   O^T (16 d x 8 heads)    += V^T (16 d x 16 keys) . P^T (16 keys x 8 heads), over D/16 m-tiles.
 // P^T is moved from the S^T accumulator layout to the B-operand layout with movmatrix.  The warp
 // first loads every K and V fragment of the stage into registers and releases the stage before
-// computing, so the producer refills it sooner.
-template <int D, int QS, bool kPre>
+// computing, so the producer refills it sooner.  kMod: changed scores (cb_score.cuh).
+template <int D, int QS, bool kPre, bool kMod>
 __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase, uint32_t bar_full,
                                                uint32_t bar_empty, const StageInfo<kPre>* info, int c,
                                                int hg, int warp, long long n_my, long long ntiles,
-                                               int N, const WsLayout& L, int lane) {
+                                               int N, const WsLayout& L, int lane,
+                                               const ScoreArgs& sc) {
   using SM = DecodeSmem<D, QS>;
   constexpr int KS = D / 16;  // k-steps of S^T over the head dim
   constexpr int MT = D / 16;  // m-tiles of O^T over the head dim
@@ -186,7 +188,14 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
   int32_t* merge_cnt = reinterpret_cast<int32_t*>(a.ws + L.merge_cnt);
   const uint32_t* q32 = static_cast<const uint32_t*>(a.q);
   __nv_bfloat16* outg = static_cast<__nv_bfloat16*>(a.out);
-  const float sl2 = a.scale_log2;
+  const float sl2 = kMod ? 1.f : a.scale_log2;
+  // kMod: the slopes of this thread's two query heads (columns 2 tq and 2 tq + 1)
+  float slope[2] = {0.f, 0.f};
+  if constexpr (kMod) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (qoff + 2 * tq + j < a.G) slope[j] = slope_of(sc, kvh * a.G + qoff + 2 * tq + j);
+  }
 
   uint32_t qb[NTH][KS][2];
   float o[MT][NTH][4];
@@ -302,6 +311,11 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) mma_bf16_16816(s[ht], kf[ks], qb[ht][ks][0], qb[ht][ks][1]);
       }
+    }
+    if constexpr (kMod) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        s[0][x] = change_score(s[0][x], a.scale_log2, slope[x & 1], si.key0 + g + 8 * (x >> 1), si.kv - 1, sc);
     }
     if constexpr (kPre && QS == 1) {
       if (edge || head) {
@@ -644,10 +658,10 @@ __device__ __forceinline__ void decode_produce(const AttnArgs& a, const CUtensor
 // One CTA of the decode pass: CTA `bx` of the a.decode_ctas CTAs of KV-head group `hg`
 // (decode_kv_heads<QS>() KV heads per group).  Runs in the attention kernel (cb_attention.cu)
 // with that kernel's dynamic shared memory; uses 32 * (QS * HB + 1) of its threads.
-template <int D, int QS, bool kPre>
+template <int D, int QS, bool kPre, bool kMod = false>
 __device__ __forceinline__ void decode_cta(const AttnArgs& a, const CUtensorMap* kmap,
                                            const CUtensorMap* vmap, uint8_t* smem_raw, int bx,
-                                           int hg) {
+                                           int hg, const ScoreArgs& sc = ScoreArgs{}) {
   using SM = DecodeSmem<D, QS>;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -688,8 +702,8 @@ __device__ __forceinline__ void decode_cta(const AttnArgs& a, const CUtensorMap*
                           c, hg, HB, t0, t1, lane);
   };
   auto consume = [&]() {
-    decode_consume<D, QS, kPre>(a, sbase, bar_full, bar_empty, info, c, hg, warp, t1 - t0, ntiles, N,
-                           L, lane);
+    decode_consume<D, QS, kPre, kMod>(a, sbase, bar_full, bar_empty, info, c, hg, warp, t1 - t0, ntiles,
+                                      N, L, lane, sc);
   };
   if (warp == n_cons) produce();
   else if (warp < n_cons) consume();

@@ -50,6 +50,29 @@ struct RopeArgs {
   int parts;         // warps that share one token's heads
 };
 
+// The quantised cache: codes e4m3 [P, bs, Hkv, D] and per (token, KV head) the two exponents of the
+// key's and the value's scale, + 127, [P, bs, Hkv, 2].  The quantising append is the rotary append's
+// arguments (rot_dim 0: nothing is rotated) with these pools.
+struct QuantAppendArgs {
+  RopeArgs r;
+  uint8_t* scales;
+};
+
+// Ranges of cached keys and values read back as bf16 rows.
+struct GatherArgs {
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const uint8_t* scales;
+  const int32_t* block_table;
+  const int32_t* cu_seqlens_k;  // [S + 1]: output rows of each sequence
+  const int32_t* key_starts;    // [S] or NULL (0): the first key of each sequence's range
+  void* k_out;
+  void* v_out;
+  int S, T, Hkv, D, bs, max_blocks, P;
+  int rows;                     // output rows per warp: a power of two up to 32
+  uint32_t* err;
+};
+
 struct AttnArgs {
   const void* q;
   void* out;
@@ -80,6 +103,23 @@ struct AttnArgs {
                        // no other argument: two more in front of the others cost the chunk pass 0.6 %
 };
 
+// Changes of the scores and of the mask (cb_score.cuh).
+struct ScoreArgs {
+  const float* slopes;     // [Hq] or NULL
+  const int32_t* visible;  // [S] or NULL
+  float cap_in, cap_out;   // 2 log2(e) scale / cap, cap log2(e); 0: no cap
+};
+
+// What the attention passes need of the quantised cache beside AttnArgs.
+struct QuantArgs {
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const uint8_t* scales;
+  int tile_log2;  // keys of a decode tile: 2^tile_log2
+  int KB;         // rows per TMA box of the decode pass
+  int copy;       // bytes of a copy of scales: 16, 8, 4, or 2 (plain loads)
+};
+
 // Block moves: copy (pool -> pool), offload (pool -> linear host buffer), restore (host ->
 // pool).  Per pool (K, V) one block is block_bytes contiguous bytes.
 enum BlockMoveMode { kMoveCopy = 0, kMoveOffload = 1, kMoveRestore = 2 };
@@ -99,6 +139,8 @@ unsigned long long launch_context_id();
 
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_rope_append(RopeArgs r, int sm_count, cudaStream_t stream);
+cudaError_t launch_quant_append(QuantAppendArgs x, int sm_count, cudaStream_t stream);
+cudaError_t launch_quant_gather(GatherArgs g, int sm_count, cudaStream_t stream);
 cudaError_t launch_block_move(const BlockMoveArgs& a, int sm_count, cudaStream_t stream);
 cudaError_t launch_wait_selftest(uint32_t* err, uint64_t limit_ns, uint64_t* waited_ns,
                                  cudaStream_t stream);
@@ -123,7 +165,24 @@ struct PrefixMaps {
 cudaError_t launch_prefix_plan(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_prefix_attention(const AttnArgs& a, const AttnMaps& maps,
                                     const PrefixMaps& p, cudaStream_t stream);
-// After it: merges the parts of the shared prefixes' rows.
+// The attention kernel over the quantised cache, its planner (alone, and beside the quantising append);
+// sc: changed scores or masks, or NULL.  Maps of Q for the chunk pass and of the code pools for the decode
+// pass.
+struct QuantMaps {
+  CUtensorMap q, k, v;
+};
+int quant_parts(const RopeArgs& r, int sm_count);
+cudaError_t launch_quant_plan(const AttnArgs& a, const QuantArgs& qa, cudaStream_t stream);
+cudaError_t launch_quant_append_plan(QuantAppendArgs x, const AttnArgs& a, const QuantArgs& qa,
+                                     int sm_count, cudaStream_t stream);
+cudaError_t launch_quant_attention(const AttnArgs& a, const QuantArgs& qa, const ScoreArgs* sc,
+                                   const QuantMaps& m, cudaStream_t stream);
+cudaError_t launch_quant_scored(const AttnArgs& a, const QuantArgs& qa, const ScoreArgs& sc,
+                                const QuantMaps& m, cudaStream_t stream);
+// The attention kernel with changed scores and masks.
+cudaError_t launch_scored_attention(const AttnArgs& a, const ScoreArgs& sc, const AttnMaps& maps,
+                                    cudaStream_t stream);
+// After launch_prefix_attention: merges the parts of the shared prefixes' rows.
 cudaError_t launch_prefix_merge(const AttnArgs& a, int sm_count, cudaStream_t stream);
 
 }  // namespace cb

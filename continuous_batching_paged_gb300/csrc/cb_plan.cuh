@@ -451,9 +451,10 @@ constexpr int kPlanSmemSeqs = 2048;
 template <bool kPre>
 constexpr int plan_smem_seqs() { return kPre ? kPlanSmemSeqs / 2 : kPlanSmemSeqs; }
 
-// kPre: with shared prefixes (a.NG > 0).
-template <bool kPre>
-__device__ __forceinline__ void plan_cta(const AttnArgs& a) {
+// kPre: with shared prefixes (a.NG > 0).  kQuant: the quantised cache, whose decode tiles have
+// 2^tile_log2 keys.
+template <bool kPre, bool kQuant = false>
+__device__ __forceinline__ void plan_cta(const AttnArgs& a, int tile_log2 = 0) {
   constexpr int NT = plan_threads<kPre>();  // threads
   constexpr int kBins = kCostBins / NT;      // histogram bins per thread
   constexpr int kSeqs = plan_smem_seqs<kPre>();
@@ -535,9 +536,10 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       } else if (q_len == 1) {
         grp = -1;
         // tiles from the one holding the window's first key (every key without a window)
-        const int first = window_first_key(kv - 1, a.window) / kDecodeTileKeys * kDecodeTileKeys;
+        const int tile = kQuant ? 1 << tile_log2 : kDecodeTileKeys;
+        const int first = window_first_key(kv - 1, a.window) / tile * tile;
         v[0] = 1;
-        v[1] = (kv - first + kDecodeTileKeys - 1) / kDecodeTileKeys;
+        v[1] = (kv - first + tile - 1) / tile;
         my_keys += (float)(kv - window_first_key(kv - 1, a.window));
       } else if (q_len > 1) {
         grp = -1;
@@ -735,7 +737,8 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a) {
       if (tid == 0)
         hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, items, most, m);
     } else if (a.decode_auto) {
-      n = choose_decode_ctas(keys * (float)(a.Hkv * a.D * 4), pairs * (float)(4 * a.D * a.Hq),
+      n = choose_decode_ctas(keys * (float)(a.Hkv * (kQuant ? 2 * a.D + 2 : 4 * a.D)),
+                             pairs * (float)(4 * a.D * a.Hq),
                              n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq), a.decode_ctas,
                              ntiles);
     }

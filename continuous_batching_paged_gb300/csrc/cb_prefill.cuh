@@ -37,8 +37,11 @@
 // TMEM columns: [0,128) S/P of A, [128,256) S/P of B, [256,256+D) O of A, then O of B.
 #pragma once
 
+#include <type_traits>
+
 #include "cb_common.cuh"
 #include "cb_launch.h"
+#include "cb_score.cuh"
 
 namespace cb {
 
@@ -97,7 +100,32 @@ struct PfItem {
   int j0;                                      // first K/V tile (a sliding window skips older)
   int hasB;
 };
-static_assert(sizeof(PfItem) <= 128, "a decoded item fits its shared-memory slot");
+struct PfItemSeen : PfItem {  // with changed scores
+  int seen;  // keys that every query sees (ScoreArgs::visible; 0: the causal mask alone)
+};
+template <bool kMod>
+using PfItemOf = std::conditional_t<kMod, PfItemSeen, PfItem>;
+static_assert(sizeof(PfItemSeen) <= 128, "a decoded item fits its shared-memory slot");
+
+// The chunk pass over the quantised cache: warps 12-15 make the K and V tiles (quant_convert), warp 0
+// finds their rows.
+constexpr int kQuantPrefillThreads = 512;
+constexpr int kRegsQuantIssue = 64, kRegsQuantSoftmax = 176, kRegsQuantConvert = 96;
+static_assert(kRegsQuantIssue + 2 * kRegsQuantSoftmax + kRegsQuantConvert <= 4 * 128,
+              "register split exceeds the launch");
+constexpr int kRowSlots = 4;  // K/V tiles whose rows are known ahead
+struct RowSlot {
+  int2 row[kChunkKeys];  // per key: its token in the pool (-1: none), its two scale bytes
+  int kvh, flags;
+};
+constexpr int kRowFirst = 1, kRowLast = 2, kRowEnd = 4;  // an item's first and last tile; no more tiles
+template <int D>
+struct QuantPrefillSmem {
+  static constexpr int kRows = (PrefillSmem<D>::kTotal - 1024 + 15) / 16 * 16;
+  static constexpr int kBar = kRows + kRowSlots * (int)sizeof(RowSlot);  // full, empty per slot
+  static constexpr int kTotal = kBar + 2 * kRowSlots * 8 + 1024;
+  static_assert(sizeof(RowSlot) % 8 == 0, "alignment of shared-memory regions");
+};
 
 // Query heads (pairs) per unit: items are unit-major with the head (pair) fastest, so the
 // CTAs on the heads of one KV group at the same time share its K/V tiles through L2.
@@ -105,11 +133,12 @@ __device__ __forceinline__ int pf_heads_per_unit(const AttnArgs& a) {
   return pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq;
 }
 
-template <bool kWin>
-__device__ __forceinline__ PfItem pf_decode_item(int item, const AttnArgs& a,
-                                                 const int32_t* pf_seq, const int32_t* pf_prefix,
-                                                 const int32_t* pf_order, int n_pf) {
-  PfItem it;
+template <bool kWin, bool kMod>
+__device__ __forceinline__ PfItemOf<kMod> pf_decode_item(int item, const AttnArgs& a,
+                                                 const ScoreArgs& sc, const int32_t* pf_seq,
+                                                 const int32_t* pf_prefix, const int32_t* pf_order,
+                                                 int n_pf) {
+  PfItemOf<kMod> it;
   it.item = item;
   const int hu_n = pf_heads_per_unit(a);
   const int pos = item / hu_n;  // position in the longest-first unit order
@@ -125,6 +154,8 @@ __device__ __forceinline__ PfItem pf_decode_item(int item, const AttnArgs& a,
   const int c0 = a.cu_seqlens_q[it.s];
   const int q_len = a.cu_seqlens_q[it.s + 1] - c0;
   it.ctx = a.kv_lens[it.s] - q_len;
+  if constexpr (kMod)
+    it.seen = sc.visible != nullptr ? min(__ldg(sc.visible + it.s), it.ctx + q_len) : 0;
   int qt[2];
   if (pf_pair_heads(a.G)) {  // one query tile, heads 2hu and 2hu+1 of one KV group
     qt[0] = qt[1] = u;
@@ -145,6 +176,7 @@ __device__ __forceinline__ PfItem pf_decode_item(int item, const AttnArgs& a,
     it.tok[t] = c0 + qt[t] * kPrefillTileM;
     it.rows[t] = on ? min(kPrefillTileM, q_len - qt[t] * kPrefillTileM) : 0;
     it.nk[t] = on ? it.ctx + qt[t] * kPrefillTileM + it.rows[t] : 0;
+    if constexpr (kMod) it.nk[t] = on ? max(it.nk[t], it.seen) : 0;
     it.nt[t] = (it.nk[t] + kChunkKeys - 1) / kChunkKeys;
   }
   it.nk_all = max(it.nk[0], it.nk[1]);
@@ -154,14 +186,26 @@ __device__ __forceinline__ PfItem pf_decode_item(int item, const AttnArgs& a,
   return it;
 }
 
+// The quantised pass's producers (cb_quant_prefill.cuh).
+template <int D, bool kMod>
+__device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& qa, const CUtensorMap* qmap,
+                           uint8_t* smem, uint32_t sbase, int lane);
+template <int D>
+__device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs& qa, uint8_t* smem,
+                                              uint32_t sbase);
+
 // kWin: sliding-window attention (a.window > 0).  The full causal pass is compiled without
 // the window's bookkeeping, so it runs exactly the code it ran before windows existed.
-// One persistent CTA of the chunk pass (all kPrefillThreads threads).  Runs in the attention
-// kernel (cb_attention.cu) with that kernel's dynamic shared memory.
-template <int D, bool kWin>
+// kMod: changed scores and masks (cb_score.cuh); with it kWin only allows a window (a.window may be 0).
+// kQuant: K and V come from the quantised cache (kmap and vmap are unused).
+// One persistent CTA of the chunk pass (all kPrefillThreads threads; kQuantPrefillThreads with
+// kQuant).  Runs in the attention kernel (cb_attention.cu) with that kernel's dynamic shared memory.
+template <int D, bool kWin, bool kMod = false, bool kQuant = false>
 __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap* qmap,
                                             const CUtensorMap* kmap, const CUtensorMap* vmap,
-                                            uint8_t* smem_raw) {
+                                            uint8_t* smem_raw, const ScoreArgs& sc = ScoreArgs{},
+                                            const QuantArgs& qa = QuantArgs{}) {
+  static_assert(!kMod || kWin, "the changed-score pass is compiled with a window's bookkeeping");
   using SM = PrefillSmem<D>;
   constexpr int NS = SM::kStages;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -171,7 +215,8 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + SM::kMisc);
   // Decoded items, two slots: the scheduler warp claims and decodes the next item while the
   // current one runs; every role reads it from here (no global-memory chain at an item's start).
-  auto item_slot = [&](int slot) { return reinterpret_cast<PfItem*>(smem + SM::kItems + slot * SM::kItemSlot); };
+  using Item = PfItemOf<kMod>;
+  auto item_slot = [&](int slot) { return reinterpret_cast<Item*>(smem + SM::kItems + slot * SM::kItemSlot); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, a.pack);
@@ -187,7 +232,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
     mbar_init(bar(SM::bQFull), 1);
     mbar_init(bar(SM::bQEmpty), 1);
     for (int i = 0; i < NS; ++i) {
-      mbar_init(bar(SM::bFull + i), 1);
+      mbar_init(bar(SM::bFull + i), kQuant ? 4 : 1);  // (one arrival per converting warp)
       mbar_init(bar(SM::bEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -199,6 +244,12 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
       mbar_init(bar(SM::bItemEmpty + i), kItemConsumers);
     }
     mbar_init(bar(SM::bClaim), 1);
+    if constexpr (kQuant) {
+      for (int i = 0; i < kRowSlots; ++i) {
+        mbar_init(sbase + QuantPrefillSmem<D>::kBar + 8 * i, 1);
+        mbar_init(sbase + QuantPrefillSmem<D>::kBar + 8 * (kRowSlots + i), 4);
+      }
+    }
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -213,8 +264,10 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
   // Each role runs inside the branch that set its register count (no join in between, so the
   // compiler allocates every role's code under that role's own limit).
   if (warp < 4) {
-    regs_dec<kRegsIssue>();
-    if (warp == 0) {
+    regs_dec<kQuant ? kRegsQuantIssue : kRegsIssue>();
+    if (kQuant && warp == 0) {
+      if constexpr (kQuant) quant_rows<D, kMod>(a, qa, qmap, smem, sbase, lane);
+    } else if (warp == 0) {
       // =================================================================== TMA producer
       if (lane == 0) {
         tma_prefetch_desc(qmap);
@@ -227,7 +280,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
       for (uint32_t k = 0;; ++k) {
         const int slot = k & 1;
         if (!mbar_wait(bar(SM::bItemFull + slot), (k >> 1) & 1)) { report(a.err, kErrTimeout); break; }
-        const PfItem it = *item_slot(slot);
+        const Item it = *item_slot(slot);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
         if (it.item < 0) break;
@@ -343,8 +396,8 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
           if (kc == 0 && item >= 0) atomicMin(&hdr->t_pf_start, global_ns());  // role span
         }
         item = __shfl_sync(0xffffffffu, item, 0);
-        PfItem it;
-        if (item >= 0) it = pf_decode_item<kWin>(item, a, pf_seq, pf_prefix, pf_order, n_pf);
+        Item it;
+        if (item >= 0) it = pf_decode_item<kWin, kMod>(item, a, sc, pf_seq, pf_prefix, pf_order, n_pf);
         it.item = item;
         if (lane == 0) {
           *item_slot(slot) = it;
@@ -424,7 +477,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         const int slot = k & 1;
         wait(bar(SM::bItemFull + slot), (k >> 1) & 1);
         if (!ok) break;
-        const PfItem it = *item_slot(slot);
+        const Item it = *item_slot(slot);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
         if (it.item < 0) break;
@@ -472,8 +525,13 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         }
       }
     }
+  } else if (kQuant && warp >= 12) {
+    if constexpr (kQuant) {
+      regs_dec<kRegsQuantConvert>();
+      quant_convert<D>(a, qa, smem, sbase);
+    }
   } else {
-    regs_inc<kRegsSoftmax>();
+    regs_inc<kQuant ? kRegsQuantSoftmax : kRegsSoftmax>();
     // ===================================================================== softmax groups
     const int t = (warp - 4) >> 2;                // 0: tile A, 1: tile B
     const int quad = warp & 3;                    // TMEM lane quadrant this warp may access
@@ -486,7 +544,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
     for (uint32_t k = 0;; ++k) {
       const int slot = k & 1;
       if (!mbar_wait(bar(SM::bItemFull + slot), (k >> 1) & 1)) { report(a.err, kErrTimeout); break; }
-      const PfItem it = *item_slot(slot);
+      const Item it = *item_slot(slot);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
       if (it.item < 0) break;
@@ -498,7 +556,13 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
       const int rows = t ? it.rows[1] : it.rows[0];
       const int head = t ? it.head[1] : it.head[0];
       const int diag0 = it.ctx + (t ? it.qoff[1] : it.qoff[0]);  // row 0's last key
-      const int limit = diag0 + r;                                     // row r's last key
+      int limit = diag0 + r;                                           // row r's last key
+      int full = diag0;  // every row's last key is this one or a later one
+      if constexpr (kMod) {
+        limit = max(limit, it.seen - 1);
+        full = max(full, it.seen - 1);
+      }
+      const float slope = kMod ? slope_of(sc, head) : 0.f;
       float m_run = -INFINITY, l_run = 0.f;
       bool ok = true;
       const int W = kWin ? a.window : 0;
@@ -513,10 +577,26 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         for (int i = 0; i < 4; ++i) tmem_ld32(t_lane + s_col + i * 32, sr + i * 32);
         tc_wait_ld();
         const int key0 = j * kChunkKeys;
+        if constexpr (kMod) {  // the scores in units of log2
+          if (sc.cap_in > 0.f) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              sr[c] = __float_as_uint(cap_score(__uint_as_float(sr[c]), sc));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * sl2);
+          }
+          if (sc.slopes != nullptr) {
+            const float away = (float)(key0 - (diag0 + r));
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              sr[c] = __float_as_uint(fmaf(slope, away + (float)c, __uint_as_float(sr[c])));
+          }
+        }
         // causal edge (keys past the row's position) and, with a sliding window, its lower
         // edge (keys at or before position - W)
-        const int lo_r = kWin ? limit - W + 1 : 0;
-        if (key0 + kChunkKeys - 1 > diag0 || (kWin && key0 < lo_r)) {
+        const int lo_r = !kWin || (kMod && W == 0) ? 0 : diag0 + r - W + 1;
+        if (key0 + kChunkKeys - 1 > full || (kWin && key0 < lo_r)) {
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (key0 + c > limit || (kWin && key0 + c < lo_r)) sr[c] = __float_as_uint(-INFINITY);
@@ -535,7 +615,8 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(mx8[i], __uint_as_float(sr[120 + i]));
         const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]),
                                fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
-        const float mt = mx * sl2;
+        const float mul = kMod ? 1.f : sl2;
+        const float mt = mx * mul;
         float alpha = 1.f;
         bool resc = false;
         if (j == it.j0) {
@@ -549,7 +630,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         // 0 instead (every p is then 0), so that no -inf - (-inf) appears.
         const float m_sub = (kWin && m_run == -INFINITY) ? 0.f : m_run;
         // exponent arguments and row sums two columns per instruction (paired fp32)
-        const uint64_t scale2 = f2_pack(sl2, sl2), neg_m2 = f2_pack(-m_sub, -m_sub);
+        const uint64_t scale2 = f2_pack(mul, mul), neg_m2 = f2_pack(-m_sub, -m_sub);
         uint64_t sum2[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum2[i] = 0ull;
@@ -567,7 +648,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         for (int i = 0; i < 4; ++i) f2_unpack(sum2[i], sm8[2 * i], sm8[2 * i + 1]);
         const float sum = ((sm8[0] + sm8[1]) + (sm8[2] + sm8[3])) + ((sm8[4] + sm8[5]) + (sm8[6] + sm8[7]));
         l_run = l_run * alpha + sum;
-        if (j == it.nt_all - 1) {
+        if (!kQuant && j == it.nt_all - 1) {
           // Keys at or past the pair's last key in the last K/V tile: their V rows hold stale or
           // poison data and P is 0 there, but 0 * NaN is NaN, so zero them before the PV
           // product reads them (both groups may do it; they write the same zeros).

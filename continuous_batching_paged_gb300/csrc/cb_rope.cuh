@@ -38,11 +38,8 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 }
 
 // A unit's two chunks turned by its eight (c, s): chunk against chunk, or neighbours inside each.
-__device__ __forceinline__ void turn_unit(uint4& va, uint4& vb, const float* c, const float* s,
+__device__ __forceinline__ void turn_unit(float* a, float* b, const float* c, const float* s,
                                           bool interleaved) {
-  float a[8], b[8];
-  unpack8(va, a);
-  unpack8(vb, b);
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -53,6 +50,13 @@ __device__ __forceinline__ void turn_unit(uint4& va, uint4& vb, const float* c, 
 #pragma unroll
     for (int i = 0; i < 8; ++i) turn(a[i], b[i], c[i], s[i]);
   }
+}
+__device__ __forceinline__ void turn_unit(uint4& va, uint4& vb, const float* c, const float* s,
+                                          bool interleaved) {
+  float a[8], b[8];
+  unpack8(va, a);
+  unpack8(vb, b);
+  turn_unit(a, b, c, s, interleaved);
   va = pack8(a);
   vb = pack8(b);
 }

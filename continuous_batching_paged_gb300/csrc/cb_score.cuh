@@ -1,0 +1,30 @@
+// Scores that are changed between the product q.k and the softmax, and masks beside the causal one:
+//   x = cap tanh(scale q.k / cap)            (cap > 0),
+//   x + slope_h (key - position)             (a bias that falls with the distance),
+//   keys below visible_lens[s] are seen by every query of sequence s (a prefix read both ways).
+// The passes work in units of log2: x log2(e).
+#pragma once
+
+#include "cb_common.cuh"
+#include "cb_launch.h"
+
+namespace cb {
+
+// cap tanh(u) log2(e) from the raw product s: with t = 2^(cap_in s), cap_in = 2 log2(e) scale / cap,
+// tanh(u) = 1 - 2 / (1 + t).  Off by 2^-22 of the cap at most (two approximations of 2^-22, and the
+// cancellation near 0, which is absolute as well): 2e-5 of a score at a cap of 50.  t = inf gives 1.
+__device__ __forceinline__ float cap_score(float s, const ScoreArgs& sc) {
+  return fmaf(-2.f * sc.cap_out, __fdividef(1.f, 1.f + fast_exp2(s * sc.cap_in)), sc.cap_out);
+}
+// The raw product s of a query at `pos` and key `key`, in units of log2.
+__device__ __forceinline__ float change_score(float s, float scale_log2, float slope_log2, int key,
+                                              int pos, const ScoreArgs& sc) {
+  const float x = sc.cap_in > 0.f ? cap_score(s, sc) : s * scale_log2;
+  return fmaf(slope_log2, (float)(key - pos), x);
+}
+// Head h's slope in units of log2 (0 without slopes).
+__device__ __forceinline__ float slope_of(const ScoreArgs& sc, int h) {
+  return sc.slopes != nullptr ? __ldg(sc.slopes + h) * 1.4426950408889634f : 0.f;
+}
+
+}  // namespace cb

@@ -321,6 +321,101 @@ cb_status cb_rope_append_attention(const void* q, const void* k_new, const void*
                                    const cb_options* options, void* stream);
 
 /*
+ * Changed scores and masks, for models that cap their scores, bias them by distance instead of
+ * embedding positions, or read a prefix both ways (additions of this library; the pages describe
+ * plain causal attention).  The score of query position p (head h) and key j of a sequence is
+ *     x = scale q.k,   x = softcap * tanh(x / softcap) where softcap > 0,   x += slopes[h] (j - p),
+ * and key j is seen when j <= p or j < visible_lens[s] (never beyond kv_len).  A sliding window
+ * (cb_options) goes with the first two, not with visible_lens (CB_ERR_UNSUPPORTED).
+ */
+typedef struct {
+  float softcap;                /* 0: none                                                       */
+  int32_t reserved32;
+  const float* slopes;          /* device fp32 [Hq], or NULL: none                               */
+  const int32_t* visible_lens;  /* device int32 [num_seqs]: leading keys that every query of the
+                                   sequence sees (0 or less: the causal mask alone); or NULL     */
+  int64_t reserved[2];
+} cb_score;
+
+/*
+ * cb_scored_attention -- cb_ragged_paged_attention_ex with changed scores and masks.  score is
+ * required; its fields may all be off.  out must not overlap q (CB_ERR_INVALID_ARG).  The other
+ * arguments, the workspace and the errors are those of cb_ragged_paged_attention_ex.
+ */
+cb_status cb_scored_attention(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* block_table, const int32_t* cu_seqlens_q,
+                              const int32_t* kv_lens, int32_t block_size, float scale,
+                              const cb_score* score, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, const cb_dims* dims,
+                              const cb_options* options, void* stream);
+
+/*
+ * The quantised cache: keys and values in 8 bits, half the memory and half the bytes of a decode
+ * step.  (An addition of this library; the pages store the cache in the model's type.)
+ *
+ *   k_pages, v_pages  e4m3 [P, bs, Hkv, D]   codes, laid out like the bf16 pools
+ *   kv_scales         uint8 [P, bs, Hkv, 2]  per (token, KV head) the exponent + 127 of the key
+ *                                            row's scale, then of the value row's; 16-byte aligned
+ * A stored value is code * 2^(byte - 127).  A row is stored with the smallest exponent e in
+ * [-32, 31] for which max |x| <= 448 * 2^e, each value rounded once to the nearest code (ties to
+ * even): off by 2^-4 of itself at most, or by 2^-10 * 2^e where that is more.  Values beyond
+ * 448 * 2^31 are clamped to it, values that are not finite stored as NaN (they do not count for
+ * the row's maximum).  Bytes outside [95, 158] are not made by the library, and its attention's
+ * accuracy is not specified for them.
+ *
+ * cb_quant_append -- cb_rope_append into the quantised cache: the keys, rotated (and not rounded
+ * before they are quantised), and the values go to their slots, the rotated queries, in bf16, to
+ * q_out.  Without rotation (rope NULL, or its cos_sin NULL, rot_dim and interleaved 0: then only
+ * its strides count) the keys are quantised as they are, and q and q_out must be NULL.  Other
+ * arguments and errors: cb_rope_append.
+ */
+cb_status cb_quant_append(const void* q, const void* k_new, const void* v_new, void* q_out,
+                          void* k_pages, void* v_pages, void* kv_scales, const int32_t* block_table,
+                          const int32_t* cu_seqlens_q, const int32_t* kv_lens, int32_t block_size,
+                          const cb_rope* rope, const cb_dims* dims, void* stream);
+
+/*
+ * cb_quant_gather -- read ranges of a quantised cache back as bf16 rows (exact), to hand a request
+ * over to a bf16 cache or to other code: row cu_seqlens_k[s] + i of k_out and v_out (bf16
+ * [num_tokens, Hkv, D]) receives key (value) key_starts[s] + i of sequence s; key_starts NULL: from
+ * key 0 on.  cu_seqlens_k int32 [S+1] as cu_seqlens_q; rows from cu_seqlens_k[S] on are left as they
+ * are.  dims: num_tokens is the number of output rows, num_q_heads is ignored but for being a valid
+ * number.  k_out and v_out must not overlap.  Device errors: as cb_kv_append (a negative start, a
+ * position beyond the table, a bad block id); the row is skipped.
+ */
+cb_status cb_quant_gather(const void* k_pages, const void* v_pages, const void* kv_scales,
+                          const int32_t* block_table, const int32_t* cu_seqlens_k,
+                          const int32_t* key_starts, int32_t block_size, void* k_out, void* v_out,
+                          const cb_dims* dims, void* stream);
+
+/*
+ * cb_quant_attention -- cb_ragged_paged_attention_ex on the quantised cache, with changed scores
+ * where score is not NULL (cb_score).  The softmax statistics and sums are fp32; nothing is rounded
+ * to 8 bits but the stored rows.  out must not overlap q (CB_ERR_INVALID_ARG).  Workspace:
+ * cb_attention_workspace_size; options and errors: cb_ragged_paged_attention_ex.
+ */
+cb_status cb_quant_attention(const void* q, const void* k_pages, const void* v_pages,
+                             const void* kv_scales, const int32_t* block_table,
+                             const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                             int32_t block_size, float scale, const cb_score* score, void* out,
+                             float* lse, void* workspace, size_t workspace_bytes,
+                             const cb_dims* dims, const cb_options* options, void* stream);
+
+/*
+ * cb_quant_append_attention -- one layer's attention step on the quantised cache: cb_quant_append,
+ * then cb_quant_attention, with the same results (bit for bit), in two launches.  With rotation
+ * q_out (required) receives the rotated queries, which the attention reads; without, q_out is NULL
+ * and q ([T, Hq, D] contiguous) is read as it is.  Phase events as in cb_append_attention.
+ */
+cb_status cb_quant_append_attention(const void* q, const void* k_new, const void* v_new, void* q_out,
+                                    void* k_pages, void* v_pages, void* kv_scales,
+                                    const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                    const int32_t* kv_lens, int32_t block_size, float scale,
+                                    const cb_rope* rope, const cb_score* score, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes,
+                                    const cb_dims* dims, const cb_options* options, void* stream);
+
+/*
  * cb_pass_timestamps -- device time stamps (%globaltimer, ns) of the two passes of the last
  * attention call that used `workspace`: ts_ns[0] / [1] the first start and the last end of the
  * decode CTAs that had work, ts_ns[2] / [3] the same for the chunk CTAs (the end is the last
