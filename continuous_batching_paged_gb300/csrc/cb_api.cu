@@ -498,6 +498,8 @@ static cb_status attention(const void* q, const void* k_pages, const void* v_pag
   const uint32_t HB = (uint32_t)(Hkv < dec_heads ? Hkv : dec_heads);
   if ((st = encode_map(&maps.q, q, D, Hq, (uint64_t)a.T, D * 2, D * 2 * Hq, 1, 128)) != CB_OK) return st;
   if (quant) {
+    if ((long long)a.P * block_size * Hkv >= 0xffffffffLL)  // (rows of the pool are 32-bit numbers)
+      return fail(CB_ERR_UNSUPPORTED, "num_pages * block_size * num_kv_heads must be < 2^32 - 1");
     qa = cb::quant_shape(block_size, Hkv, G, a.D);
     qa.k_pages = static_cast<const uint8_t*>(k_pages);
     qa.v_pages = static_cast<const uint8_t*>(v_pages);

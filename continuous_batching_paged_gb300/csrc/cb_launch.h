@@ -116,8 +116,8 @@ struct QuantArgs {
   const uint8_t* v_pages;
   const uint8_t* scales;
   int tile_log2;  // keys of a decode tile: 2^tile_log2
-  int KB;         // rows per TMA box of the decode pass
-  int copy;       // bytes of a copy of scales: 16, 8, 4, or 2 (plain loads)
+  int KB;         // rows per TMA box of the decode pass (a page run)
+  int copy;       // bytes of a copy of scales: 16, 8, 4, 2 (plain loads), or 0 (a page run's at once)
 };
 
 // Block moves: copy (pool -> pool), offload (pool -> linear host buffer), restore (host ->

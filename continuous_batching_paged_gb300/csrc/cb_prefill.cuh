@@ -110,15 +110,24 @@ static_assert(sizeof(PfItemSeen) <= 128, "a decoded item fits its shared-memory 
 // The chunk pass over the quantised cache: warps 12-15 make the K and V tiles (quant_convert), warp 0
 // finds their rows.
 constexpr int kQuantPrefillThreads = 512;
-constexpr int kRegsQuantIssue = 64, kRegsQuantSoftmax = 176, kRegsQuantConvert = 96;
-static_assert(kRegsQuantIssue + 2 * kRegsQuantSoftmax + kRegsQuantConvert <= 4 * 128,
-              "register split exceeds the launch");
+// Registers of the issuing, softmax and converting warps: what each role needs without spills.
+template <int D>
+struct QuantRegs {
+  static constexpr int kIssue = D == 128 ? 56 : 64, kSoftmax = D == 128 ? 184 : 176,
+                       kConvert = D == 128 ? 88 : 96;
+  static_assert(kIssue + 2 * kSoftmax + kConvert <= 4 * 128, "register split exceeds the launch");
+};
 constexpr int kRowSlots = 4;  // K/V tiles whose rows are known ahead
 struct RowSlot {
-  int2 row[kChunkKeys];  // per key: its token in the pool (-1: none), its two scale bytes
-  int kvh, flags;
+  // per key: its row in the pool (token x Hkv + KV head; kNoRow: none), and the two factors that make
+  // its codes values (bf16, the key's in the low half; quant_convert)
+  uint2 row[kChunkKeys];
+  uint32_t more[kChunkKeys];  // further factors, with kRowMore
+  int flags, pad;
 };
-constexpr int kRowFirst = 1, kRowLast = 2, kRowEnd = 4;  // an item's first and last tile; no more tiles
+constexpr uint32_t kNoRow = 0xffffffffu;
+// an item's first and last tile; no more tiles; some scale takes two factors
+constexpr int kRowFirst = 1, kRowLast = 2, kRowEnd = 4, kRowMore = 8;
 template <int D>
 struct QuantPrefillSmem {
   static constexpr int kRows = (PrefillSmem<D>::kTotal - 1024 + 15) / 16 * 16;
@@ -264,7 +273,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
   // Each role runs inside the branch that set its register count (no join in between, so the
   // compiler allocates every role's code under that role's own limit).
   if (warp < 4) {
-    regs_dec<kQuant ? kRegsQuantIssue : kRegsIssue>();
+    regs_dec<kQuant ? QuantRegs<D>::kIssue : kRegsIssue>();
     if (kQuant && warp == 0) {
       if constexpr (kQuant) quant_rows<D, kMod>(a, qa, qmap, smem, sbase, lane);
     } else if (warp == 0) {
@@ -527,11 +536,11 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
     }
   } else if (kQuant && warp >= 12) {
     if constexpr (kQuant) {
-      regs_dec<kRegsQuantConvert>();
+      regs_dec<QuantRegs<D>::kConvert>();
       quant_convert<D>(a, qa, smem, sbase);
     }
   } else {
-    regs_inc<kQuant ? kRegsQuantSoftmax : kRegsSoftmax>();
+    regs_inc<kQuant ? QuantRegs<D>::kSoftmax : kRegsSoftmax>();
     // ===================================================================== softmax groups
     const int t = (warp - 4) >> 2;                // 0: tile A, 1: tile B
     const int quad = warp & 3;                    // TMEM lane quadrant this warp may access

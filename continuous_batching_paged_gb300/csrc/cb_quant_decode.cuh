@@ -64,11 +64,19 @@ struct QDecodeSmem {
   static constexpr int kMergeWarp = 32 * (D / 4 + 4) * 4;
   static constexpr int kMerge = kScales + kStages * kScaleBytes;
   static constexpr int kBar = kMerge + 4 * kMergeWarp;      // full, empty per stage; 4 merge barriers
-  static constexpr int kInfo = kBar + (2 * kStages + 4) * 8;
-  static constexpr int kTokens = kInfo + kStages * (int)sizeof(StageInfoBase);  // of a tile's page runs
+  static constexpr int kInfo = (kBar + (2 * kStages + 4) * 8 + 15) / 16 * 16;  // QuantStage per stage
+  static constexpr int kTokens = kInfo + kStages * 32;  // of a tile's page runs, where they are many
   static constexpr int kTotal = kTokens + 256 * 4 + 1024;
   static_assert(kMerge % 16 == 0 && kBar % 8 == 0, "alignment of shared-memory regions");
 };
+
+// `bytes` (a multiple of 16) from global to shared memory (both 16-byte aligned), counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
 
 // Bytes between the page runs of a tile (a run: [HB heads][KB keys] rows of D bytes); TMA writes to
 // multiples of 128 bytes.
@@ -81,16 +89,32 @@ __device__ __forceinline__ uint32_t quant_swizzle(uint32_t off) {
   return off ^ ((off >> 3) & (D == 128 ? 0x70u : 0x30u));
 }
 
-// The producer warp: walks the CTA's tiles [t0, t1), copies each tile's page runs by TMA and its
-// scales by small asynchronous copies of every lane, which count on the same barrier.  The block table's
-// entries of a tile are loaded while the tile before it is issued, a sequence's record one sequence
-// ahead.
+// A stage's record, two 16-byte pieces in shared memory: its query's token, keys, index among the decode
+// sequences and first key; flags, first key of the window, the sequence's tiles [p0, p1).
+struct QuantStage {
+  int tok, kv, dec, key0, flags, lo, p0, p1;
+};
+__device__ __forceinline__ QuantStage quant_stage(uint32_t addr) {
+  const uint4 a = lds128(addr), b = lds128(addr + 16);
+  return {(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+__device__ __forceinline__ void sts128(uint32_t addr, int x, int y, int z, int w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+// The producer warp: walks the CTA's tiles [t0, t1) and copies each tile's page runs by TMA and its scales
+// beside them: a run's in one bulk copy where the CTA has all KV heads (qa.copy 0), else in small copies
+// of every lane, which count on the same barrier.  Block-table entries are loaded for up to 32 runs at a
+// time (several tiles), one such batch ahead, and a sequence's record one sequence ahead.  What this warp
+// does per tile is on the path from a freed stage to its next bytes: 27949 tiles of 64 KB on 152 CTAs
+// took 399 us with the entries and their divisions made per tile and all scales copied by lanes.
 template <int D, int QS>
 __device__ __forceinline__ void quant_produce(const AttnArgs& a, const QuantArgs& qa,
                                               const CUtensorMap* kmap, const CUtensorMap* vmap,
-                                              uint32_t sbase, StageInfoBase* info, int* tokens,
-                                              int n_dec, const int4* dec_rec, int d, int hg, int HB,
-                                              long long t0, long long t1, int lane) {
+                                              uint32_t sbase, int* tokens, int n_dec,
+                                              const int4* dec_rec, int d, int hg, int HB, long long t0,
+                                              long long t1, int lane) {
   using SM = QDecodeSmem<D, QS>;
   if (lane == 0) {
     tma_prefetch_desc(kmap);
@@ -98,124 +122,159 @@ __device__ __forceinline__ void quant_produce(const AttnArgs& a, const QuantArgs
   }
   const uint32_t bar_full = sbase + SM::kBar, bar_empty = bar_full + 8 * SM::kStages;
   const int KB = qa.KB, tile_keys = 1 << qa.tile_log2, runs = tile_keys / KB;  // (at most 256)
-  const int run_stride = quant_run_stride<D>(HB, KB);
-  const uint32_t run_bytes = (uint32_t)(2 * KB * HB * D);
+  const int run_stride = quant_run_stride<D>(HB, KB), scale_run = 2 * HB * KB;
+  const uint32_t run_bytes = (uint32_t)(2 * KB * HB * D + (qa.copy == 0 ? scale_run : 0));
   const uint64_t policy = l2_policy_evict_first();  // each K/V row is read once
-  const int row_bytes = 2 * HB, copies = tile_keys * row_bytes / qa.copy;
   const int head0 = hg * (8 / QS);
+  // this lane's first small copy of scales: its run, and where it is in the run's source
+  const int row_bytes = 2 * HB, copies = qa.copy == 0 ? 0 : tile_keys * row_bytes / qa.copy;
+  auto copy_at = [&](int u, int& run) -> long long {
+    const int key = u * qa.copy / row_bytes;
+    run = key / KB;
+    return (long long)(key - run * KB) * a.Hkv * 2 + (u * qa.copy - key * row_bytes) + 2 * head0;
+  };
+  int copy_run;
+  const long long copy_src = copies > 0 ? copy_at(lane, copy_run) : 0;
+  if (copies == 0) copy_run = 0;
 
   int4 rec = dec_rec[d], next = dec_rec[min(d + 1, n_dec)], after = dec_rec[min(d + 2, n_dec)];
   auto first_key = [&](const int4& r) {  // of the sequence's first tile
     return window_first_key(r.z - 1, a.window) / tile_keys * tile_keys;
   };
-  // Block ids of tile t's page runs, run 32 i + lane in e[i] (-1: no keys there, or a bad id).
-  auto entries = [&](const int4& r, long long t, int (&e)[8]) {
-    const int key0 = first_key(r) + (int)(t - r.w) * tile_keys;
-    const int32_t* row = a.block_table + (size_t)r.x * a.max_blocks;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      e[i] = -1;
-      if (32 * i < runs) {
-        const int run = 32 * i + lane, pos = key0 + run * KB;
-        if (run < runs && pos < r.z) {
-          const int lb = pos / a.bs;
-          e[i] = lb < a.max_blocks ? __ldg(row + lb) : -2;
-        }
-      }
-    }
+  // Tiles per batch of entries (a tile of more than 32 runs -- small blocks, few KV heads -- takes them
+  // one by one below), and this lane's place in one.
+  const int per_batch = runs <= 32 ? 32 / runs : 1;
+  const int my_tile = runs <= 32 ? lane / runs : 0, my_key = runs <= 32 ? lane % runs * KB : 0;
+  // The block id of this lane's run in the batch of tiles [t, hi) of r, and the offset in the block (-1:
+  // no such run, -2: beyond the table)
+  auto fetch = [&](const int4& r, long long t, int& off) -> int {
+    const int pos = first_key(r) + (int)(t + my_tile - r.w) * tile_keys + my_key;
+    off = 0;
+    if (runs > 32 || my_tile >= per_batch || pos >= r.z) return -1;
+    const int lb = pos / a.bs;
+    off = pos - lb * a.bs;
+    return lb < a.max_blocks ? __ldg(a.block_table + (size_t)r.x * a.max_blocks + lb) : -2;
   };
-  int e[8];
-  entries(rec, t0, e);
-  long long it = 0;
-  for (long long t = t0; t < t1; ++t, ++it) {
+  int off, e = fetch(rec, t0, off);
+  uint32_t stage = 0, phase = 1;
+  bool begins = true;  // the next tile is this CTA's first of its sequence
+  for (long long t = t0; t < t1;) {
     const long long p0 = rec.w, p1 = next.w;
-    const long long lo = t0 > p0 ? t0 : p0, hi = t1 < p1 ? t1 : p1;
-    // the tile after this one: of this sequence, or the next one's first
-    const bool moves = t + 1 >= p1;
-    int en[8];
-    if (t + 1 < t1) entries(moves ? next : rec, t + 1, en);
-    if (t == lo && lane == 0)  // the consumers read the query rows a few stages from now
+    const long long hi = t1 < p1 ? t1 : p1;
+    const int nb = (int)(hi - t < per_batch ? hi - t : per_batch);
+    int off_n = 0, e_n = -1;
+    if (t + nb < t1) e_n = fetch(t + nb < p1 ? rec : next, t + nb, off_n);
+    if (begins && lane == 0)  // the consumers read the query rows a few stages from now
       l2_prefetch_bulk(static_cast<const __nv_bfloat16*>(a.q) + ((size_t)rec.y * a.Hq + (size_t)head0 * a.G) * D,
                        (uint32_t)(HB * a.G * D * 2));
-    const int stage = (int)(it % SM::kStages);
-    const uint32_t phase = (uint32_t)((it / SM::kStages) & 1);
+    // (runs of this lane's tile count only where the tile is the sequence's and the CTA's)
+    const bool want = e != -1 && t + my_tile < hi, good = want && e >= 0 && e < a.P;
+    if (want && !good) report(a.err, kErrOutOfRange);
+    const int token = good ? e * a.bs + off : -1;
+    const int key_t = first_key(rec) + (int)(t - p0) * tile_keys;
     bool ok = true;
-    if (lane == 0) ok = mbar_wait(bar_empty + 8 * stage, phase ^ 1);
-    if (!__shfl_sync(0xffffffffu, ok, 0)) {
+    for (int i = 0; i < nb; ++i) {
+      if (lane == 0) ok = mbar_wait(bar_empty + 8 * stage, phase);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      const int key0 = key_t + i * tile_keys;
+      uint32_t n_runs;
+      int tok = -1;
+      if (runs <= 32) {
+        tok = __shfl_sync(0xffffffffu, token, i * runs + (lane < runs ? lane : 0));
+        if (lane >= runs) tok = -1;
+        n_runs = __popc(__ballot_sync(0xffffffffu, tok >= 0));
+      } else {
+        n_runs = 0;
+        __syncwarp();  // (the last tile's tokens are read)
+        for (int run = lane; run < runs; run += 32) {  // (runs is a multiple of 32)
+          const int pos = key0 + run * KB;
+          int id = -1;
+          if (pos < rec.z) {
+            const int lb = pos / a.bs;
+            const int block = lb < a.max_blocks ? __ldg(a.block_table + (size_t)rec.x * a.max_blocks + lb) : -1;
+            if (block >= 0 && block < a.P)
+              id = block * a.bs + (pos - lb * a.bs);
+            else
+              report(a.err, kErrOutOfRange);
+          }
+          tokens[run] = id;
+          n_runs += __popc(__ballot_sync(0xffffffffu, id >= 0));
+        }
+      }
+      const uint32_t full = bar_full + 8 * stage;
+      if (lane == 0) {
+        const uint32_t info = sbase + SM::kInfo + stage * (uint32_t)sizeof(QuantStage);
+        const bool first = begins && i == 0, last = t + i == hi - 1;
+        sts128(info, rec.y, rec.z, d, key0);
+        sts128(info + 16,
+               (first ? kInfoFirst : 0u) | (last ? kInfoLast : 0u) |
+                   (p0 >= t0 && p1 <= t1 ? kInfoComplete : 0u),
+               window_first_key(rec.z - 1, a.window), (int)p0, (int)p1);
+        mbar_arrive_expect_tx(full, n_runs * run_bytes);
+      }
+      __syncwarp();
+      const uint32_t kst = sbase + stage * SM::kStageBytes, vst = kst + SM::kKVBytes;
+      const uint32_t sst = sbase + SM::kScales + stage * SM::kScaleBytes;
+      auto copy_run_of = [&](int run, int token) {
+        tma_load_3d_hint(kst + run * run_stride, kmap, full, 0, token, head0, policy);
+        tma_load_3d_hint(vst + run * run_stride, vmap, full, 0, token, head0, policy);
+        if (qa.copy == 0)
+          bulk_load(sst + run * scale_run, qa.scales + (size_t)token * row_bytes, scale_run, full);
+      };
+      if (runs <= 32) {
+        if (tok >= 0) copy_run_of(lane, tok);
+      } else {
+        for (int run = lane; run < runs; run += 32)
+          if (tokens[run] >= 0) copy_run_of(run, tokens[run]);
+      }
+      if (qa.copy > 0) {
+        int run = copy_run;
+        long long from = copy_src;
+        for (int u0 = 0; u0 < copies; u0 += 32) {
+          const int u = u0 + lane;
+          if (u0 > 0) from = copy_at(u < copies ? u : 0, run);
+          const int tk = runs <= 32 ? __shfl_sync(0xffffffffu, tok, run & 31) : u < copies ? tokens[run] : -1;
+          if (u >= copies || tk < 0) continue;
+          const uint8_t* src = qa.scales + (size_t)tk * a.Hkv * 2 + from;
+          const uint32_t dst = sst + u * qa.copy;
+          if (qa.copy == 16) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+          } else if (qa.copy == 8) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+          } else if (qa.copy == 4) {
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+          } else {
+            const unsigned short v = __ldg(reinterpret_cast<const unsigned short*>(src));
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"(v) : "memory");
+          }
+        }
+        // one arrival per lane, once its copies are there
+        if (qa.copy == 2)
+          mbar_arrive(full);
+        else
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+        __syncwarp();
+      }
+      if (++stage == SM::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok) {
       if (lane == 0) report(a.err, kErrTimeout);
       break;
     }
-    const int key0 = first_key(rec) + (int)(t - p0) * tile_keys;
-    uint32_t nvalid = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (32 * i < runs) {
-        const int run = 32 * i + lane, pos = key0 + run * KB;
-        const bool want = run < runs && pos < rec.z;
-        const bool valid = want && e[i] >= 0 && e[i] < a.P;
-        if (want && !valid) report(a.err, kErrOutOfRange);
-        nvalid += __popc(__ballot_sync(0xffffffffu, valid));
-        if (run < runs) tokens[run] = valid ? e[i] * a.bs + pos % a.bs : -1;
-      }
-    }
-    const uint32_t full = bar_full + 8 * stage;
-    if (lane == 0) {
-      StageInfoBase& si = info[stage];
-      si.seq = rec.x;
-      si.dec = d;
-      si.tok = rec.y;
-      si.kv = rec.z;
-      si.lo = window_first_key(rec.z - 1, a.window);
-      si.key0 = key0;
-      si.p0 = (int)p0;
-      si.p1 = (int)p1;
-      si.flags = (t == lo ? kInfoFirst : 0u) | (t == hi - 1 ? kInfoLast : 0u) |
-                 (p0 >= t0 && p1 <= t1 ? kInfoComplete : 0u);
-      mbar_arrive_expect_tx(full, nvalid * run_bytes);
-    }
-    __syncwarp();
-    const uint32_t kst = sbase + stage * SM::kStageBytes, vst = kst + SM::kKVBytes;
-    for (int run = lane; run < runs; run += 32) {
-      const int token = tokens[run];
-      if (token >= 0) {
-        tma_load_3d_hint(kst + run * run_stride, kmap, full, 0, token, head0, policy);
-        tma_load_3d_hint(vst + run * run_stride, vmap, full, 0, token, head0, policy);
-      }
-    }
-    // The scales: [key][HB][2] bytes, in copies that stay inside a page run.
-    const uint32_t sst = sbase + SM::kScales + stage * SM::kScaleBytes;
-    for (int u = lane; u < copies; u += 32) {
-      const int b = u * qa.copy, key = b / row_bytes, rest = b - key * row_bytes;
-      const int run = key / KB, token = tokens[run];
-      if (token >= 0) {
-        const uint8_t* src =
-            qa.scales + ((size_t)(token + key - run * KB) * a.Hkv + head0) * 2 + rest;
-        if (qa.copy == 16) {
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(sst + b), "l"(src) : "memory");
-        } else if (qa.copy == 8) {
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(sst + b), "l"(src) : "memory");
-        } else if (qa.copy == 4) {
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sst + b), "l"(src) : "memory");
-        } else {
-          const unsigned short v = __ldg(reinterpret_cast<const unsigned short*>(src));
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(sst + b), "h"(v) : "memory");
-        }
-      }
-    }
-    // one arrival per lane, once its copies are there
-    if (qa.copy == 2)
-      mbar_arrive(full);
-    else
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = en[i];
-    if (moves) {
+    t += nb;
+    begins = t >= p1;
+    if (begins) {
       ++d;
       rec = next;
       next = after;
       after = dec_rec[min(d + 2, n_dec)];
     }
+    e = e_n;
+    off = off_n;
   }
 }
 
@@ -229,9 +288,9 @@ __device__ __forceinline__ void quant_produce(const AttnArgs& a, const QuantArgs
 template <int D, int QS, bool kMod>
 __device__ __forceinline__ void quant_consume(const AttnArgs& a, const QuantArgs& qa,
                                               const ScoreArgs& sc, uint32_t sbase,
-                                              const StageInfoBase* info, int c, int hg, int HB,
-                                              int slices, int warp, long long n_my, long long ntiles,
-                                              int N, const WsLayout& L, int lane) {
+                                              int c, int hg, int HB, int slices, int warp,
+                                              long long n_my, long long ntiles, int N,
+                                              const WsLayout& L, int lane) {
   using SM = QDecodeSmem<D, QS>;
   constexpr int KS = D / 16, MT = D / 16;   // steps over the head dim
   constexpr int W = D / 32;                 // 32-bit words of a lane's part of a V row
@@ -269,14 +328,17 @@ __device__ __forceinline__ void quant_consume(const AttnArgs& a, const QuantArgs
   float m[2], l[2];
   uint32_t sync_phase = 0;
 
+  uint32_t stage = SM::kStages - 1, phase = 1;
   for (long long it = 0; it < n_my; ++it) {
-    const int stage = (int)(it % SM::kStages);
-    const uint32_t phase = (uint32_t)((it / SM::kStages) & 1);
+    if (++stage == SM::kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
     if (!mbar_wait(bar_full + 8 * stage, phase)) {
       if (lane == 0) report(a.err, kErrTimeout);
       break;
     }
-    const StageInfoBase si = info[stage];
+    const QuantStage si = quant_stage(sbase + SM::kInfo + stage * (uint32_t)sizeof(QuantStage));
     if (si.flags & kInfoFirst) {
       // the query row of column g, scaled so that its largest value is in [1, 2) (exact in fp16 but
       // for values 2^-14 smaller, which are off by 2^-25 at most)
@@ -579,7 +641,6 @@ __device__ __forceinline__ void quant_decode_cta(const AttnArgs& a, const QuantA
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  StageInfoBase* info = reinterpret_cast<StageInfoBase*>(smem + SM::kInfo);
   const int HB = a.Hkv < 8 / QS ? a.Hkv : 8 / QS;
   const int slices = 1 << (qa.tile_log2 - 5);
   const int n_cons = QS * HB * slices;
@@ -597,7 +658,8 @@ __device__ __forceinline__ void quant_decode_cta(const AttnArgs& a, const QuantA
   if (threadIdx.x == 0) {
     const uint32_t bars = sbase + SM::kBar;
     for (int i = 0; i < SM::kStages; ++i) {
-      mbar_init(bars + 8 * i, 1 + 32);  // the bytes announced, and each producer lane's small copies
+      // the bytes announced, and each producer lane's small copies
+      mbar_init(bars + 8 * i, qa.copy == 0 ? 1 : 1 + 32);
       mbar_init(bars + 8 * (SM::kStages + i), n_cons);
     }
     for (int i = 0; i < 4; ++i) mbar_init(bars + 8 * (2 * SM::kStages + i), slices);
@@ -605,7 +667,7 @@ __device__ __forceinline__ void quant_decode_cta(const AttnArgs& a, const QuantA
   }
   __syncthreads();
   auto produce = [&]() {
-    quant_produce<D, QS>(a, qa, kmap, vmap, sbase, info, reinterpret_cast<int*>(smem + SM::kTokens),
+    quant_produce<D, QS>(a, qa, kmap, vmap, sbase, reinterpret_cast<int*>(smem + SM::kTokens),
                          n_dec, dec_rec, d_first, hg, HB, t0, t1, lane);
   };
   // The consumers hold a whole stage in registers: they take what the warps behind them (at most one
@@ -615,7 +677,7 @@ __device__ __forceinline__ void quant_decode_cta(const AttnArgs& a, const QuantA
     if (warp == n_cons)
       produce();
     else if (warp < n_cons)
-      quant_consume<D, QS, kMod>(a, qa, sc, sbase, info, c, hg, HB, slices, warp, t1 - t0, ntiles, N, L,
+      quant_consume<D, QS, kMod>(a, qa, sc, sbase, c, hg, HB, slices, warp, t1 - t0, ntiles, N, L,
                                  lane);
   } else {
     regs_dec<kRegsQuantRest>();

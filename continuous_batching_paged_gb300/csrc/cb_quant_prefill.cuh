@@ -10,6 +10,8 @@
 // the converting warps, beside the softmax warps of the same schedulers.
 #pragma once
 
+#include <cstddef>
+
 #include "cb_prefill.cuh"
 #include "cb_quant.cuh"
 
@@ -85,11 +87,21 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
           sc[i] = __ldg(reinterpret_cast<const unsigned short*>(qa.scales) + (size_t)tok[i] * a.Hkv + it.kvh);
       RowSlot& rs = ring[n % kRowSlots];
       wait(row_empty + 8 * (n % kRowSlots), ((n / kRowSlots) & 1) ^ 1);
+      // The factors: 2^120 (codes_to_bf16x4) times the scale, which bf16 holds for scales up to 2^7; the
+      // rest of a larger one is a second factor.
+      bool more = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) rs.row[32 * i + lane] = make_int2(tok[i], sc[i]);
+      for (int i = 0; i < 4; ++i) {
+        const int ek = (int)(sc[i] & 255) - kQuantBias, ev = (int)(sc[i] >> 8) - kQuantBias;
+        const uint32_t f = (uint32_t)(247 + min(ek, 7)) << 7 | (uint32_t)(247 + min(ev, 7)) << 23;
+        rs.row[32 * i + lane] =
+            make_uint2(tok[i] < 0 ? kNoRow : (uint32_t)tok[i] * a.Hkv + it.kvh, tok[i] < 0 ? 0u : f);
+        rs.more[32 * i + lane] = (uint32_t)(127 + max(ek - 7, 0)) << 7 | (uint32_t)(127 + max(ev - 7, 0)) << 23;
+        more = more || (tok[i] >= 0 && max(ek, ev) > 7);
+      }
+      more = __any_sync(0xffffffffu, more);
       if (lane == 0) {
-        rs.kvh = it.kvh;
-        rs.flags = (j == it.j0 ? kRowFirst : 0) | (j == it.nt_all - 1 ? kRowLast : 0);
+        rs.flags = (j == it.j0 ? kRowFirst : 0) | (j == it.nt_all - 1 ? kRowLast : 0) | (more ? kRowMore : 0);
       }
       __syncwarp();
       if (lane == 0) {
@@ -128,8 +140,12 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t f) {
 }
 
 // Warps 12-15: K and V tiles of the ring's stages.  Stage m of an item holds K tile m and V tile m - 1,
-// as in cb_prefill.cuh.  A thread makes the same 16 columns of D / 16 rows of every tile; the codes of
-// the next tile are loaded while this one's are converted, each into the register that just became free.
+// as in cb_prefill.cuh, so an item's order is K(0) | K(1) V(0) | ... | K(n-1) V(n-2) | V(n-1), stages
+// between the bars.  A thread makes the same 16 columns of D / 16 rows of every tile; the codes of the
+// next tile in that order are loaded while this one's are converted, each into the register that just
+// became free.  One copy of the conversion, in a loop over tiles: written out for each place in the order
+// the four warps' code did not stay in the instruction cache beside the softmax warps' (8 chunks of 512
+// tokens: 804 us).
 template <int D>
 __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs& qa, uint8_t* smem,
                                               uint32_t sbase) {
@@ -138,13 +154,16 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
   constexpr int NS = SM::kStages, NR = D / 16;  // rows per thread
   auto bar = [&](int i) -> uint32_t { return sbase + SM::kBar + 8 * i; };
   const uint32_t row_full = sbase + QM::kBar, row_empty = row_full + 8 * kRowSlots;
-  const RowSlot* ring = reinterpret_cast<const RowSlot*>(smem + QM::kRows);
+  const uint32_t rings = sbase + QM::kRows;
   const int t = threadIdx.x - 384, lane = threadIdx.x & 31;
   // Columns 16 c .. 16 c + 15 of rows r0 + 128 / NR * i.  Eight neighbouring threads (one pass of a
   // 16-byte access) have four columns of two rows, so that their swizzled stores meet no bank twice.
   const int c = D == 128 ? (t & 3) + 4 * ((t >> 3) & 1) : t & 3;
   const int r0 = D == 128 ? ((t >> 2) & 1) + 2 * (t >> 4) : t >> 2;
-  constexpr int kStep = 128 / NR;
+  constexpr int kStep = 128 / NR;  // (a multiple of 8: all rows of a thread have one swizzle)
+  static_assert(kStep % 8 == 0, "rows of a thread share their swizzle");
+  const uint32_t at0 = sw128((c >> 2) * SM::kKVHalf, r0, 2 * (c & 3));
+  const uint32_t at1 = sw128((c >> 2) * SM::kKVHalf, r0, 2 * (c & 3) + 1);
   bool ok = true;
   auto wait = [&](uint32_t b, uint32_t parity) {
     if (ok && !mbar_wait(b, parity)) {
@@ -152,111 +171,115 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
       ok = false;
     }
   };
-  uint4 raw[NR];
-  auto load = [&](const uint8_t* pages, const RowSlot& rs, int i) {
-    const int token = rs.row[r0 + kStep * i].x;
-    raw[i] = make_uint4(0, 0, 0, 0);
-    if (token >= 0)
-      raw[i] = __ldg(reinterpret_cast<const uint4*>(pages + ((size_t)token * a.Hkv + rs.kvh) * D) + c);
+  auto slot = [&](uint32_t i) -> uint32_t { return rings + (i % kRowSlots) * (uint32_t)sizeof(RowSlot); };
+  auto ready = [&](uint32_t i) { wait(row_full + 8 * (i % kRowSlots), (i / kRowSlots) & 1); };
+  auto flags_of = [&](uint32_t i) -> int {
+    int f;
+    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(f) : "r"(slot(i) + (uint32_t)offsetof(RowSlot, flags)));
+    return f;
   };
-  // Converts the codes in raw (rows of rs; v: values) into the tile at dst, and loads the next ones.
-  auto convert = [&](const RowSlot& rs, bool v, uint32_t dst, const uint8_t* next, const RowSlot& nrs) {
+  uint4 raw[NR];
+  auto load = [&](const uint8_t* pages, uint32_t rows, int i) {
+    uint32_t row;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(row) : "r"(rows + 8 * (r0 + kStep * i)));
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (row != kNoRow)
+      raw[i] = __ldg(reinterpret_cast<const uint4*>(pages + (size_t)row * D) + c);
+  };
+
+  uint32_t g = 0;              // stages so far
+  uint32_t n = 0;              // the tile at hand, of all tiles so far
+  bool v = false;              // its values
+  int flags = 0, flags1 = 0;   // of tile n; v: of tile n + 1, where that is the same item's
+  uint32_t kst = 0;
+  bool loaded = false;         // raw holds its codes
+  while (true) {
+    if (!loaded) {             // an item begins
+      ready(n);
+      if (!ok) break;
+      flags = flags_of(n);
+      if (flags & kRowEnd) break;
+#pragma unroll
+      for (int i = 0; i < NR; ++i) load(qa.k_pages, slot(n), i);
+    }
+    // The next tile in the order.
+    uint32_t nn;
+    bool nv;
+    loaded = true;
+    if (!v) {
+      const bool first = flags & kRowFirst, last = flags & kRowLast;
+      nv = !first || last;
+      nn = first ? (last ? n : n + 1) : n - 1;
+    } else if (!(flags & kRowLast)) {
+      nv = flags1 & kRowLast;
+      nn = nv ? n + 1 : n + 2;
+    } else {  // the next item's first keys, where its rows are known already
+      nv = false;
+      nn = n + 1;
+      loaded = __all_sync(0xffffffffu, mbar_test(row_full + 8 * (nn % kRowSlots), (nn / kRowSlots) & 1)) &&
+               !(flags_of(nn) & kRowEnd);
+    }
+    if (!nv && loaded) ready(nn);
+    // A stage begins with keys, or with an item's last values.
+    if (!v || (flags & kRowLast)) {
+      wait(bar(SM::bEmpty + g % NS), ((g / NS) & 1) ^ 1);
+      kst = sbase + SM::kStage0 + (g % NS) * SM::kStageBytes;
+    }
+    if (!ok) break;
+    const uint32_t rows = slot(n), nrows = slot(nn), dst = kst + (v ? SM::kKVTile : 0);
+    const uint8_t* next = nv ? qa.v_pages : qa.k_pages;
+    const uint32_t pick = v ? 0x3232u : 0x1010u;
+    const bool more = flags & kRowMore;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      const int row = r0 + kStep * i;
-      const int e = (rs.row[row].y >> (v ? 8 : 0) & 255) - kQuantBias;
+      uint32_t f;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(f) : "r"(rows + 8 * (r0 + kStep * i) + 4));
+      f = __byte_perm(f, 0, pick);
       const uint4 x = raw[i];
-      if (next != nullptr) load(next, nrs, i);
+      if (loaded) load(next, nrows, i);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t y[8];
-      // bf16's exponent ends at 127: a scale above 2^7 is applied in two steps
-      const uint32_t f1 = (uint32_t)(127 + 120 + min(e, 7)) << 7, f = f1 | f1 << 16;
-      uint32_t nan = 0;
+      uint32_t y[8], nan = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         codes_to_bf16x4(w[k], f, y[2 * k], y[2 * k + 1]);
         nan |= (w[k] & 0x7f7f7f7fu) + 0x01010101u;
       }
-      if (e > 7) {
-        const uint32_t g1 = (uint32_t)(127 + e - 7) << 7, g = g1 | g1 << 16;
+      if (__builtin_expect((nan & 0x80808080u) != 0 || more, 0)) {
+        if (more) {
+          uint32_t m;
+          asm volatile("ld.shared.u32 %0, [%1];"
+                       : "=r"(m)
+                       : "r"(rows + (uint32_t)offsetof(RowSlot, more) + 4 * (r0 + kStep * i)));
+          m = __byte_perm(m, 0, pick);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = mul_bf16x2(y[k], g);
-      }
-      if (nan & 0x80808080u) {  // a NaN code (0x7f with either sign) among them
+          for (int k = 0; k < 8; ++k) y[k] = mul_bf16x2(y[k], m);
+        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 8; ++k) {  // NaN codes: 0x7f with either sign
           const uint32_t pair = w[k >> 1] >> (16 * (k & 1));
           if ((pair & 0x7fu) == 0x7fu) y[k] |= 0x7fffu;
           if ((pair & 0x7f00u) == 0x7f00u) y[k] |= 0x7fff0000u;
         }
       }
-      const uint32_t tile = dst + (c >> 2) * SM::kKVHalf;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t addr = sw128(tile, row, 2 * (c & 3) + k);
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(y[4 * k]),
-                     "r"(y[4 * k + 1]), "r"(y[4 * k + 2]), "r"(y[4 * k + 3]) : "memory");
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + at0 + kStep * 128 * i), "r"(y[0]),
+                   "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + at1 + kStep * 128 * i), "r"(y[4]),
+                   "r"(y[5]), "r"(y[6]), "r"(y[7]) : "memory");
+    }
+    if (v || (flags & kRowFirst)) {  // the stage is complete
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(SM::bFull + g % NS));
+        if (v) mbar_arrive(row_empty + 8 * (n % kRowSlots));
       }
+      ++g;
     }
-  };
-  uint32_t g = 0;  // stages so far
-  auto begin = [&]() -> uint32_t {  // the next stage, once it is free
-    wait(bar(SM::bEmpty + g % NS), ((g / NS) & 1) ^ 1);
-    return sbase + SM::kStage0 + (g % NS) * SM::kStageBytes;
-  };
-  auto finish = [&]() {  // the stage is written
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(SM::bFull + g % NS));
-    ++g;
-  };
-  uint32_t n = 0;       // tiles so far
-  bool loaded = false;  // raw holds tile n's keys
-  auto tile_ready = [&](uint32_t i) { wait(row_full + 8 * (i % kRowSlots), (i / kRowSlots) & 1); };
-  auto release = [&](uint32_t i) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(row_empty + 8 * (i % kRowSlots));
-  };
-  while (ok) {
-    tile_ready(n);
-    if (!ok || (ring[n % kRowSlots].flags & kRowEnd)) break;
-    // ---- an item: K of its first tile, then per tile K and the V before it, then the last V
-    if (!loaded) {
-#pragma unroll
-      for (int i = 0; i < NR; ++i) load(qa.k_pages, ring[n % kRowSlots], i);
-    }
-    loaded = false;
-    bool last = ring[n % kRowSlots].flags & kRowLast;
-    uint32_t kst = begin();
-    if (!last) tile_ready(n + 1);
-    if (!ok) break;
-    convert(ring[n % kRowSlots], false, kst, last ? qa.v_pages : qa.k_pages, ring[(n + (last ? 0 : 1)) % kRowSlots]);
-    finish();
-    while (!last && ok) {
-      ++n;  // this stage: K of tile n, V of tile n - 1
-      const RowSlot &cur = ring[n % kRowSlots], &prev = ring[(n - 1) % kRowSlots];
-      last = cur.flags & kRowLast;
-      kst = begin();
-      if (!ok) break;
-      convert(cur, false, kst, qa.v_pages, prev);
-      if (!last) tile_ready(n + 1);
-      if (!ok) break;
-      convert(prev, true, kst + SM::kKVTile, last ? qa.v_pages : qa.k_pages,
-              ring[(n + (last ? 0 : 1)) % kRowSlots]);
-      finish();
-      release(n - 1);
-    }
-    if (!ok) break;
-    kst = begin();
-    if (!ok) break;
-    // the next item's first keys, where its rows are known already
-    const uint32_t i = (n + 1) % kRowSlots;
-    loaded = __all_sync(0xffffffffu, mbar_test(row_full + 8 * i, ((n + 1) / kRowSlots) & 1)) &&
-             !(ring[i].flags & kRowEnd);
-    convert(ring[n % kRowSlots], true, kst + SM::kKVTile, loaded ? qa.k_pages : nullptr, ring[i]);
-    finish();
-    release(n);
-    ++n;
+    const int flags_n = loaded ? (nn == n ? flags : flags_of(nn)) : 0;
+    if (!v && nv && nn + 1 == n) flags1 = flags;  // (the values before these keys)
+    flags = flags_n;
+    n = nn;
+    v = nv;
   }
 }
 

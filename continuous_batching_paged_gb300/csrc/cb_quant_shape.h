@@ -25,10 +25,10 @@ inline QuantArgs quant_shape(int bs, int Hkv, int G, int D) {
   if (q.KB * HB * D % 128 != 0) slices = 1;
   q.tile_log2 = 5;
   while (1 << (q.tile_log2 - 5) < slices) ++q.tile_log2;
-  // Scales are copied in pieces that stay inside a box's rows: consecutive keys' where the CTA has all
-  // heads, else one key's.
+  // Scales are copied in pieces that stay inside a box's rows: where the CTA has all heads, consecutive
+  // keys', in one bulk copy if they are a multiple of 16 bytes; else one key's.
   const int run = 2 * HB * (Hkv == HB ? q.KB : 1);
-  q.copy = run % 16 == 0 ? 16 : run % 8 == 0 ? 8 : run % 4 == 0 ? 4 : 2;
+  q.copy = run % 16 == 0 ? (Hkv == HB ? 0 : 16) : run % 8 == 0 ? 8 : run % 4 == 0 ? 4 : 2;
   return q;
 }
 
