@@ -6,8 +6,9 @@
 // 448 being the largest e4m3 value.  Scaling by a power of two is exact, so each value is rounded once
 // (to 4 significant bits: off by 2^-4 of its own size at most, or by 2^-10 * 2^e where that is more),
 // and c * 2^e is exact in bf16.  The type's own exponent covers what the scale leaves out, so a finer
-// scale than a power of two would gain nothing but the last bit of the range.  A value that is not
-// finite is stored as NaN and does not count for the row's scale; values above 448 * 2^31 are clamped.
+// scale than a power of two would gain nothing but the last bit of the range.  Values above 448 * 2^31
+// are clamped.  A row with a value that is not finite is stored as NaN: its exponent byte is 255, and all
+// its values read back as NaN.  (Single NaN codes would cost the chunk pass a test of every code.)
 #pragma once
 
 #include "cb_rope.cuh"
@@ -16,6 +17,7 @@ namespace cb {
 
 constexpr int kQuantLow = -32, kQuantHigh = 31;  // exponents of the scales
 constexpr int kQuantBias = 127;                  // a stored exponent byte is e + 127
+constexpr int kQuantNan = 255;                   // that of a row that is NaN
 
 // Four values to four e4m3 codes, the first in the lowest byte (round to nearest even, clamped; NaN
 // stays NaN).
@@ -124,20 +126,23 @@ __device__ __forceinline__ void quant_tokens(const QuantAppendArgs& x, long long
         if ((g + 1) * per_warp <= n_q) continue;  // (queries only)
         const bool key = h < n_q + a.Hkv;
         float y[16], top = 0.f;
+        bool nan = false;
         unpack8(v[i][0], y);
         unpack8(v[i][1], y + 8);
         if (rotates && key) turn_unit(y, y + 8, c, s, r.interleaved != 0);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          if (!(fabsf(y[j]) < INFINITY)) y[j] = __int_as_float(0x7fffffff);
-          top = fmaxf(top, fabsf(y[j]));  // (NaN is never the larger one)
+          nan = nan || !(fabsf(y[j]) < INFINITY);
+          top = fmaxf(top, fabsf(y[j]));
         }
-        // the head's lanes together
+        // the head's lanes together (what is not finite as the largest value)
+        if (nan) top = INFINITY;
         for (int o = 1; o < units; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        nan = top == INFINITY;
         if (h >= n_q && h < heads) {
           const long long row = slot * a.Hkv + (h - n_q - (key ? 0 : a.Hkv));
-          const int e = quant_exponent(top);
-          const float inv = __int_as_float((2 * kQuantBias - e) << 23);  // 2^-(e - 127)
+          const int e = nan ? kQuantNan : quant_exponent(top);
+          const float inv = nan ? __int_as_float(0x7fffffff) : __int_as_float((2 * kQuantBias - e) << 23);
 #pragma unroll
           for (int j = 0; j < 16; ++j) y[j] *= inv;
           const uint2 lo = make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]),
@@ -158,9 +163,9 @@ __device__ __forceinline__ void quant_tokens(const QuantAppendArgs& x, long long
   }
 }
 
-// Eight codes times 2^(e - 127) as bf16 (exact).
+// Eight codes times 2^(e - 127) as bf16 (exact; NaN for kQuantNan).
 __device__ __forceinline__ uint4 codes_to_bf16(uint2 codes, int e) {
-  const float f = __int_as_float(e << 23);
+  const float f = e == kQuantNan ? __int_as_float(0x7fffffff) : __int_as_float(e << 23);
   uint32_t h[4];
   e4m3x4_to_f16(codes.x, h[0], h[1]);
   e4m3x4_to_f16(codes.y, h[2], h[3]);

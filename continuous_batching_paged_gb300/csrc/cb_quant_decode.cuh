@@ -433,6 +433,28 @@ __device__ __forceinline__ void quant_consume(const AttnArgs& a, const QuantArgs
 #pragma unroll
       for (int x = 0; x < 4; ++x) s[j][x] += s1[x];
     }
+    // Rows that are NaN: a key's scores, and all of a value's codes (its p is that of a finite row).
+    if (__any_sync(0xffffffffu, max(max(ex[0] & 255u, ex[0] >> 8), max(ex[1] & 255u, ex[1] >> 8)) == kQuantNan ||
+                                    max(max(ex[2] & 255u, ex[2] >> 8), max(ex[3] & 255u, ex[3] >> 8)) == kQuantNan)) {
+      uint32_t vn = 0;  // bit i: the value of key 8 i + g is NaN
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if ((ex[i] & 255u) == kQuantNan) s[i >> 1][2 * (i & 1)] = s[i >> 1][2 * (i & 1) + 1] = __int_as_float(0x7fffffff);
+        if ((ex[i] >> 8) == kQuantNan) {
+          vn |= 1u << i;
+          ex[i] = (ex[i] & 255u) | (uint32_t)kQuantBias << 8;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int key = 16 * (i >> 2) + 2 * tq + 8 * ((i >> 1) & 1) + (i & 1);
+        const uint32_t bits = __shfl_sync(0xffffffffu, vn, 4 * (key & 7));
+        if (bits >> (key >> 3) & 1) {
+#pragma unroll
+          for (int w = 0; w < W; ++w) vr[i][w] = 0x7f7f7f7fu;
+        }
+      }
+    }
     // y = x + ev; the weights of l
     float wl[4];
 #pragma unroll

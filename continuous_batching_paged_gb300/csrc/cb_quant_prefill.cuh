@@ -93,7 +93,9 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int ek = (int)(sc[i] & 255) - kQuantBias, ev = (int)(sc[i] >> 8) - kQuantBias;
-        const uint32_t f = (uint32_t)(247 + min(ek, 7)) << 7 | (uint32_t)(247 + min(ev, 7)) << 23;
+        const uint32_t fk = ek == kQuantNan - kQuantBias ? 0x7fffu : (uint32_t)(247 + min(ek, 7)) << 7;
+        const uint32_t fv = ev == kQuantNan - kQuantBias ? 0x7fffu : (uint32_t)(247 + min(ev, 7)) << 7;
+        const uint32_t f = fk | fv << 16;
         rs.row[32 * i + lane] =
             make_uint2(tok[i] < 0 ? kNoRow : (uint32_t)tok[i] * a.Hkv + it.kvh, tok[i] < 0 ? 0u : f);
         rs.more[32 * i + lane] = (uint32_t)(127 + max(ek - 7, 0)) << 7 | (uint32_t)(127 + max(ev - 7, 0)) << 23;
@@ -122,7 +124,6 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
 // Four codes to bf16 (two words), times f (2^120 times a row's scale, as bf16 twice).  A code's bits
 // s eeee mmm moved to bf16's sign, low exponent and high mantissa bits are its value times 2^-120 (its
 // exponent's bias is 7, bf16's 127), subnormal codes included, so one product makes it the stored value.
-// Not for NaN codes.
 __device__ __forceinline__ void codes_to_bf16x4(uint32_t w, uint32_t f, uint32_t& lo, uint32_t& hi) {
   uint32_t x, y;
   // each code as 16 bits with its sign above it
@@ -179,12 +180,16 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
     return f;
   };
   uint4 raw[NR];
-  auto load = [&](const uint8_t* pages, uint32_t rows, int i) {
-    uint32_t row;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(row) : "r"(rows + 8 * (r0 + kStep * i)));
+  auto load = [&](const uint8_t* pages, uint32_t row, int i) {
     raw[i] = make_uint4(0, 0, 0, 0);
     if (row != kNoRow)
       raw[i] = __ldg(reinterpret_cast<const uint4*>(pages + (size_t)row * D) + c);
+  };
+  // A tile's rows (or factors, at = 4) of this thread.
+  auto rows_of = [&](uint32_t i, uint32_t at, uint32_t (&r)[NR]) {
+#pragma unroll
+    for (int k = 0; k < NR; ++k)
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[k]) : "r"(slot(i) + 8 * (r0 + kStep * k) + at));
   };
 
   uint32_t g = 0;              // stages so far
@@ -199,8 +204,10 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
       if (!ok) break;
       flags = flags_of(n);
       if (flags & kRowEnd) break;
+      uint32_t row[NR];
+      rows_of(n, 0, row);
 #pragma unroll
-      for (int i = 0; i < NR; ++i) load(qa.k_pages, slot(n), i);
+      for (int i = 0; i < NR; ++i) load(qa.k_pages, row[i], i);
     }
     // The next tile in the order.
     uint32_t nn;
@@ -220,51 +227,43 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
                !(flags_of(nn) & kRowEnd);
     }
     if (!nv && loaded) ready(nn);
+    const int flags_n = loaded ? (nn == n ? flags : flags_of(nn)) : 0;
     // A stage begins with keys, or with an item's last values.
     if (!v || (flags & kRowLast)) {
       wait(bar(SM::bEmpty + g % NS), ((g / NS) & 1) ^ 1);
       kst = sbase + SM::kStage0 + (g % NS) * SM::kStageBytes;
     }
     if (!ok) break;
-    const uint32_t rows = slot(n), nrows = slot(nn), dst = kst + (v ? SM::kKVTile : 0);
+    const uint32_t dst = kst + (v ? SM::kKVTile : 0);
+    // (all shared-memory loads ahead of the stores, which the compiler keeps in order with them)
+    uint32_t fs[NR], row[NR];
+    rows_of(n, 4, fs);
+    rows_of(nn, 0, row);
     const uint8_t* next = nv ? qa.v_pages : qa.k_pages;
     const uint32_t pick = v ? 0x3232u : 0x1010u;
     const bool more = flags & kRowMore;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      uint32_t f;
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(f) : "r"(rows + 8 * (r0 + kStep * i) + 4));
-      f = __byte_perm(f, 0, pick);
+      const uint32_t f = __byte_perm(fs[i], 0, pick);
       const uint4 x = raw[i];
-      if (loaded) load(next, nrows, i);
+      if (loaded) load(next, row[i], i);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t y[8], nan = 0;
+      uint32_t y[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        codes_to_bf16x4(w[k], f, y[2 * k], y[2 * k + 1]);
-        nan |= (w[k] & 0x7f7f7f7fu) + 0x01010101u;
-      }
-      if (__builtin_expect((nan & 0x80808080u) != 0 || more, 0)) {
-        if (more) {
-          uint32_t m;
-          asm volatile("ld.shared.u32 %0, [%1];"
-                       : "=r"(m)
-                       : "r"(rows + (uint32_t)offsetof(RowSlot, more) + 4 * (r0 + kStep * i)));
-          m = __byte_perm(m, 0, pick);
+      for (int k = 0; k < 4; ++k) codes_to_bf16x4(w[k], f, y[2 * k], y[2 * k + 1]);
+      if (__builtin_expect(more, 0)) {
+        uint32_t m;
+        asm volatile("ld.shared.u32 %0, [%1];"
+                     : "=r"(m)
+                     : "r"(slot(n) + (uint32_t)offsetof(RowSlot, more) + 4 * (r0 + kStep * i)));
+        m = __byte_perm(m, 0, pick);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] = mul_bf16x2(y[k], m);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {  // NaN codes: 0x7f with either sign
-          const uint32_t pair = w[k >> 1] >> (16 * (k & 1));
-          if ((pair & 0x7fu) == 0x7fu) y[k] |= 0x7fffu;
-          if ((pair & 0x7f00u) == 0x7f00u) y[k] |= 0x7fff0000u;
-        }
+        for (int k = 0; k < 8; ++k) y[k] = mul_bf16x2(y[k], m);
       }
       asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + at0 + kStep * 128 * i), "r"(y[0]),
-                   "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+                   "r"(y[1]), "r"(y[2]), "r"(y[3]));
       asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + at1 + kStep * 128 * i), "r"(y[4]),
-                   "r"(y[5]), "r"(y[6]), "r"(y[7]) : "memory");
+                   "r"(y[5]), "r"(y[6]), "r"(y[7]));
     }
     if (v || (flags & kRowFirst)) {  // the stage is complete
       fence_proxy_async_smem();
@@ -275,7 +274,6 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
       }
       ++g;
     }
-    const int flags_n = loaded ? (nn == n ? flags : flags_of(nn)) : 0;
     if (!v && nv && nn + 1 == n) flags1 = flags;  // (the values before these keys)
     flags = flags_n;
     n = nn;

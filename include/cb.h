@@ -359,9 +359,10 @@ cb_status cb_scored_attention(const void* q, const void* k_pages, const void* v_
  * A stored value is code * 2^(byte - 127).  A row is stored with the smallest exponent e in
  * [-32, 31] for which max |x| <= 448 * 2^e, each value rounded once to the nearest code (ties to
  * even): off by 2^-4 of itself at most, or by 2^-10 * 2^e where that is more.  Values beyond
- * 448 * 2^31 are clamped to it, values that are not finite stored as NaN (they do not count for
- * the row's maximum).  Bytes outside [95, 158] are not made by the library, and its attention's
- * accuracy is not specified for them.
+ * 448 * 2^31 are clamped to it.  A row with a value that is not finite is stored as NaN: its byte is
+ * 255, and all its values count as NaN.  Other bytes outside [95, 158], and the codes 0x7f and 0xff in
+ * rows whose byte is not 255, are not made by the library, and what its attention makes of them is not
+ * specified.
  *
  * cb_quant_append -- cb_rope_append into the quantised cache: the keys, rotated (and not rounded
  * before they are quantised), and the values go to their slots, the rotated queries, in bf16, to

@@ -3,8 +3,8 @@
 TEST INFRASTRUCTURE (see the package docstring): nothing in the CUDA library uses this file.
 
 A row is stored as e4m3 codes times a power of two: the smallest exponent e in [-32, 31] with
-max |x| <= 448 * 2^e, each x * 2^-e rounded to the nearest e4m3 value (ties to the even code).  The
-256 values are spelled out from the format: sign, 4 exponent bits with bias 7, 3 fraction bits, no
+max |x| <= 448 * 2^e, each x * 2^-e rounded to the nearest e4m3 value (ties to the even code).  A row
+with a value that is not finite is NaN as a whole: exponent byte 255, codes 0x7f.  The 256 values are spelled out from the format: sign, 4 exponent bits with bias 7, 3 fraction bits, no
 infinities, 0x7f and 0xff NaN.
 """
 from __future__ import annotations
@@ -13,7 +13,7 @@ import math
 
 import numpy as np
 
-LOW, HIGH, BIAS = -32, 31, 127
+LOW, HIGH, BIAS, NAN = -32, 31, 127, 255
 
 
 def e4m3_table() -> np.ndarray:
@@ -45,8 +45,8 @@ def to_code(x: np.ndarray) -> np.ndarray:
 
 
 def exponents(rows: np.ndarray) -> np.ndarray:
-    """The exponent of each row's scale: from LOW on, one more for every power that is too small."""
-    top = np.max(np.where(np.isfinite(rows), np.abs(rows), 0.0), axis=-1, initial=0.0)
+    """The exponent of each finite row's scale: from LOW on, one more for every power that is too small."""
+    top = np.max(np.abs(rows), axis=-1, initial=0.0)
     e = np.full(top.shape, LOW)
     for k in range(LOW, HIGH):
         e = e + (top > 448.0 * 2.0 ** k)
@@ -56,14 +56,18 @@ def exponents(rows: np.ndarray) -> np.ndarray:
 def quantise(x: np.ndarray):
     """x float64 [..., D]: codes uint8 [..., D] and stored exponent bytes uint8 [...]."""
     x = np.asarray(x, dtype=np.float64)
+    dead = ~np.isfinite(x).all(-1)
+    x = np.where(dead[..., None], 0.0, x)
     e = exponents(x)
-    codes = to_code(np.where(np.isfinite(x), x, math.nan) * 2.0 ** -e.astype(np.float64)[..., None])
-    return codes, (e + BIAS).astype(np.uint8)
+    codes = to_code(x * 2.0 ** -e.astype(np.float64)[..., None])
+    codes[dead] = 0x7F
+    return codes, np.where(dead, NAN, e + BIAS).astype(np.uint8)
 
 
 def values(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
     """The values that codes [..., D] with exponent bytes [...] stand for."""
-    return _TABLE[codes] * 2.0 ** (scales.astype(np.float64) - BIAS)[..., None]
+    f = np.where(scales == NAN, np.nan, 2.0 ** (scales.astype(np.float64) - BIAS))
+    return _TABLE[codes] * f[..., None]
 
 
 def scored_attention(q, K, V, ctx: int, scale: float, softcap: float = 0.0, slopes=None,

@@ -306,24 +306,38 @@ def test_chunks_long_context_and_serial(cuda_lib):
     assert torch.equal(out[-64:].view(torch.int16), out2[-64:].view(torch.int16))
 
 
-def test_nan_codes(cuda_lib):
-    """A NaN in a visible key or value makes its rows NaN and no others; elsewhere it does nothing (the
-    pools hold NaN codes in every slot that no sequence owns)."""
+def test_nan_rows(cuda_lib):
+    """A key or value row with a value that is not finite is NaN as a whole; it makes the rows NaN that see
+    it and no others (and the pools hold NaN rows in every slot that no sequence owns)."""
     b = workloads.build_batch([1, 140, 1, 1], [90, 200, 90, 40], 4, 2, 128, 16, seed=942)
     d = QuantBatch(b)
     d.append_new()
-    for s, p, pool, h in ((0, 50, d.k, 1), (1, 130, d.k, 0), (1, 40, d.v, 1), (2, 89, d.v, 1)):
-        pool[b.block_table[s, p // 16], p % 16, h, 7] = 0xFF
+    for s, p, h, w in ((0, 50, 1, 0), (1, 130, 0, 0), (1, 40, 1, 1), (2, 89, 1, 1)):
+        (d.v if w else d.k)[b.block_table[s, p // 16], p % 16, h] = 0x7F
+        d.sc[b.block_table[s, p // 16], p % 16, h, w] = 255
     d.upload()
-    out = cb.quant_attention(d.q, *d.pools, *d.where, b.scale)
+    out, lse = cb.quant_attention(d.q, *d.pools, *d.where, b.scale, lse=True)
     assert cb.get_device_error() == cb.CB_OK
     nan = torch.isnan(out).cpu().numpy()
     want = np.zeros_like(nan)
-    want[0, 2:] = True                       # a key: the whole row of the heads that read it
+    want[0, 2:] = True                       # a key
     want[1 + 70:141, :2] = True              # of the queries that see it (the first is at position 60)
-    want[1:141, 2:, 7] = True                # a value: its column
-    want[141, 2:, 7] = True
+    want[1:141, 2:] = True                   # a value
+    want[141, 2:] = True
     assert np.array_equal(nan, want)
+    keys = want[..., 0].copy()
+    keys[1:142, 2:] = False                  # (a value does not count for lse)
+    assert np.array_equal(torch.isnan(lse).cpu().numpy(), keys)
+    # stored by the append, read back
+    x = opa.bf16_bits_to_f64(b.k_new).astype(np.float32)
+    x[3, 0, 5], x[4, 1, 7] = np.inf, np.nan
+    kn = bf16_tensor(workloads.f32_to_bf16_bits(x))
+    cb.quant_append(None, kn, d.v_new, *d.pools, *d.where)
+    ko, vo = cb.quant_gather(*d.pools, d.table, d.cu, 16, 143, key_starts=i32(b.kv_lens - b.q_lens))
+    bad = np.zeros((143, 2), dtype=bool)
+    bad[3, 0] = bad[4, 1] = True
+    assert np.array_equal(torch.isnan(ko).all(-1).cpu().numpy(), bad)
+    assert np.array_equal(torch.isnan(ko).any(-1).cpu().numpy(), bad) and not torch.isnan(vo).any()
 
 
 # the changed scores
