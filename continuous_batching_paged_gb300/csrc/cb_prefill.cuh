@@ -113,8 +113,8 @@ constexpr int kQuantPrefillThreads = 512;
 // Registers of the issuing, softmax and converting warps: what each role needs without spills.
 template <int D>
 struct QuantRegs {
-  static constexpr int kIssue = D == 128 ? 56 : 64, kSoftmax = 176,
-                       kConvert = D == 128 ? 104 : 96;
+  static constexpr int kIssue = D == 128 ? 80 : 64, kSoftmax = D == 128 ? 168 : 176,
+                       kConvert = 96;
   static_assert(kIssue + 2 * kSoftmax + kConvert <= 4 * 128, "register split exceeds the launch");
 };
 constexpr int kRowSlots = 4;  // K/V tiles whose rows are known ahead

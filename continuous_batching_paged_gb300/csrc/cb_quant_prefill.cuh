@@ -179,11 +179,18 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
     asm volatile("ld.shared.s32 %0, [%1];" : "=r"(f) : "r"(slot(i) + (uint32_t)offsetof(RowSlot, flags)));
     return f;
   };
+  // (Predicated, not branched around: a branch per load, and its reconvergence, took as long as the
+  // conversion.)
   uint4 raw[NR];
   auto load = [&](const uint8_t* pages, uint32_t row, int i) {
-    raw[i] = make_uint4(0, 0, 0, 0);
-    if (row != kNoRow)
-      raw[i] = __ldg(reinterpret_cast<const uint4*>(pages + (size_t)row * D) + c);
+    const uint8_t* src = pages + (size_t)row * D + 16 * c;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %5, %6;\n\t"
+        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=&r"(raw[i].x), "=&r"(raw[i].y), "=&r"(raw[i].z), "=&r"(raw[i].w)
+        : "l"(src), "r"(row), "n"(kNoRow));
   };
   // A tile's rows (or factors, at = 4) of this thread.
   auto rows_of = [&](uint32_t i, uint32_t at, uint32_t (&r)[NR]) {
@@ -239,31 +246,43 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
     uint32_t fs[NR], row[NR];
     rows_of(n, 4, fs);
     rows_of(nn, 0, row);
+    if (!loaded) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i) row[i] = kNoRow;
+    }
     const uint8_t* next = nv ? qa.v_pages : qa.k_pages;
     const uint32_t pick = v ? 0x3232u : 0x1010u;
-    const bool more = flags & kRowMore;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       const uint32_t f = __byte_perm(fs[i], 0, pick);
       const uint4 x = raw[i];
-      if (loaded) load(next, row[i], i);
+      load(next, row[i], i);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
       uint32_t y[8];
 #pragma unroll
       for (int k = 0; k < 4; ++k) codes_to_bf16x4(w[k], f, y[2 * k], y[2 * k + 1]);
-      if (__builtin_expect(more, 0)) {
-        uint32_t m;
-        asm volatile("ld.shared.u32 %0, [%1];"
-                     : "=r"(m)
-                     : "r"(slot(n) + (uint32_t)offsetof(RowSlot, more) + 4 * (r0 + kStep * i)));
-        m = __byte_perm(m, 0, pick);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = mul_bf16x2(y[k], m);
-      }
       asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + at0 + kStep * 128 * i), "r"(y[0]),
                    "r"(y[1]), "r"(y[2]), "r"(y[3]));
       asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + at1 + kStep * 128 * i), "r"(y[4]),
                    "r"(y[5]), "r"(y[6]), "r"(y[7]));
+    }
+    if (flags & kRowMore) {  // the second factors: over what this thread has just written
+#pragma unroll 1
+      for (int i = 0; i < 2 * NR; ++i) {
+        const uint32_t at = dst + (i & 1 ? at1 : at0) + kStep * 128 * (i >> 1);
+        uint32_t m;
+        asm volatile("ld.shared.u32 %0, [%1];"
+                     : "=r"(m)
+                     : "r"(slot(n) + (uint32_t)offsetof(RowSlot, more) + 4 * (r0 + kStep * (i >> 1))));
+        m = __byte_perm(m, 0, pick);
+        uint32_t y[4];
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]) : "r"(at));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = mul_bf16x2(y[k], m);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+                     "r"(y[3]));
+      }
     }
     if (v || (flags & kRowFirst)) {  // the stage is complete
       fence_proxy_async_smem();
