@@ -60,6 +60,8 @@ struct PlanHeader {
   int32_t pre_cost;         // their work per KV head, in cost units (PreGroup),
   int32_t pre_tokens;       // entries of the groups' token list,
   int32_t pre_chains;       // and their chains per KV head
+  // counters of claim_range (cb_place.cuh), reset by the planner
+  int32_t dec_claims, dec_arrivals;
 };
 
 // Byte offsets of the workspace sections (all 256-byte aligned).
@@ -373,6 +375,9 @@ __device__ __forceinline__ void mma_bf16_16816(float* c, const uint32_t* a, uint
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mbar_inval(uint32_t bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 // Transpose an 8x8 matrix of 16-bit elements held in the mma fragment layout (thread i: row
 // i / 4, columns 2 (i % 4) and 2 (i % 4) + 1) across the warp.

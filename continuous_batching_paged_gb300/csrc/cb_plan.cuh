@@ -77,14 +77,16 @@ __device__ __forceinline__ void block_scan4(int v[4], int ex[4], int tot[4], int
 // takes at most a quarter of the step.  Without chunk work all CTAs decode.  Called by one
 // full warp; candidates
 // N = 4, 8, ... are spread over the lanes, in fp32 (the fp64 rate of this part is far too low
-// for even this much arithmetic on one thread).
+// for even this much arithmetic on one thread).  kQuant: over the 8-bit cache a decode CTA streams 0.062
+// TB/s (its arithmetic bounds it) and the chunk pass runs at 5.4 TFLOP/s per SM.
+template <bool kQuant = false>
 __device__ __forceinline__ int choose_decode_ctas(float dec_bytes, float chunk_flops, int chunk_items,
                                   int max_ctas, long long tiles) {
   const int lane = threadIdx.x & 31;
   if (tiles <= 0) return 1;
   const int cap = (int)(tiles < max_ctas ? tiles : max_ctas);
   if (chunk_flops <= 0.f || chunk_items <= 0) return cap;
-  const float w_us = chunk_flops * (1.f / 6.4e6f);  // chunk work in SM-microseconds
+  const float w_us = chunk_flops * (kQuant ? 1.f / 5.4e6f : 1.f / 6.4e6f);  // chunk work in SM-microseconds
   const float item_us = w_us / (float)chunk_items;
   const float b_mb = dec_bytes * 1e-6f;             // decode bytes / 1e6: MB / (TB/s) = us
   const int n_cand = (cap + 3) / 4;
@@ -99,7 +101,7 @@ __device__ __forceinline__ int choose_decode_ctas(float dec_bytes, float chunk_f
     td[k] = 0.f;
     chunk_bound[k] = false;
     if (i < n_cand) {
-      const float lin = 0.11f * n[k], sat = 6.8f;
+      const float lin = (kQuant ? 0.062f : 0.11f) * n[k], sat = 6.8f;
       const float bw = rcbrtf(1.f / (lin * lin * lin) + 1.f / (sat * sat * sat));
       td[k] = b_mb / bw;
       const int m = max_ctas - n[k];
@@ -659,6 +661,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a, int tile_log2 = 0) {
     hdr->pf_counter = 0;
     hdr->t_dec_start = hdr->t_pf_start = ~0ull;
     hdr->t_dec_end = hdr->t_pf_end = 0ull;
+    if constexpr (!kPre) hdr->dec_claims = hdr->dec_arrivals = 0;
   }
   __syncthreads();
   // Chunk units longest first (a counting sort on the K/V tiles each streams, descending), so
@@ -737,10 +740,10 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a, int tile_log2 = 0) {
       if (tid == 0)
         hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, items, most, m);
     } else if (a.decode_auto) {
-      n = choose_decode_ctas(keys * (float)(a.Hkv * (kQuant ? 2 * a.D + 2 : 4 * a.D)),
-                             pairs * (float)(4 * a.D * a.Hq),
-                             n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq), a.decode_ctas,
-                             ntiles);
+      n = choose_decode_ctas<kQuant>(keys * (float)(a.Hkv * (kQuant ? 2 * a.D + 2 : 4 * a.D)),
+                                     pairs * (float)(4 * a.D * a.Hq),
+                                     n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq),
+                                     a.decode_ctas, ntiles);
     }
     if (kPre && pre_cost == 0 && tid == 0) hdr->pre_ctas = 0;
     if (tid == 0) {
@@ -758,8 +761,9 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a, int tile_log2 = 0) {
   // Indexed by the grid's decode CTA, so that a CTA reads its first sequence in the same round
   // trip as the plan header.
   const int32_t* dp = n_dec <= kSeqs ? s_dec_prefix : dec_prefix;
+  // (kQuant: by the range itself)
   for (int bx = tid; bx < a.decode_ctas; bx += NT) {
-    const int c = decode_cta_index(bx, N, a.decode_ctas);
+    const int c = kQuant ? bx : decode_cta_index(bx, N, a.decode_ctas);
     int lo = -1;
     if (c >= 0 && c < N) {
       const long long t0 = ntiles * c / N;

@@ -28,8 +28,7 @@ __global__ void __launch_bounds__(kQuantPrefillThreads, 1)
     PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + ws_layout(a.R, a.T, a.Hq, a.D, a.pack).header);
     const bool busy = hdr->dec_tiles > 0;
     if (threadIdx.x == 0 && busy) atomicMin(&hdr->t_dec_start, global_ns());
-    quant_decode_cta<D, QS, kMod>(a, qa, sc, &kmap, &vmap, smem_raw, b % a.decode_ctas,
-                                  b / a.decode_ctas);
+    quant_decode_cta<D, QS, kMod>(a, qa, sc, &kmap, &vmap, smem_raw, b);
     if ((threadIdx.x & 31) == 0 && busy) atomicMax(&hdr->t_dec_end, global_ns());
     return;
   }

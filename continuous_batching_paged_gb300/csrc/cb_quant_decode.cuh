@@ -23,6 +23,7 @@
 #pragma once
 
 #include "cb_decode.cuh"
+#include "cb_place.cuh"
 #include "cb_quant.cuh"
 #include "cb_quant_shape.h"
 #include "cb_score.cuh"
@@ -66,7 +67,8 @@ struct QDecodeSmem {
   static constexpr int kBar = kMerge + 4 * kMergeWarp;      // full, empty per stage; 4 merge barriers
   static constexpr int kInfo = (kBar + (2 * kStages + 4) * 8 + 15) / 16 * 16;  // QuantStage per stage
   static constexpr int kTokens = kInfo + kStages * 32;  // of a tile's page runs, where they are many
-  static constexpr int kTotal = kTokens + 256 * 4 + 1024;
+  static constexpr int kRange = kTokens + 256 * 4;
+  static constexpr int kTotal = kRange + 16 + 1024;
   static_assert(kMerge % 16 == 0 && kBar % 8 == 0, "alignment of shared-memory regions");
 };
 
@@ -651,14 +653,15 @@ __device__ __forceinline__ void quant_consume(const AttnArgs& a, const QuantArgs
 
 // The kernel's 512 threads are launched with 128 registers each.
 constexpr int kRegsQuantConsume = 176, kRegsQuantRest = 80;
+constexpr int kQuantProducer = 8;  // the producer warp (consumers are warps 0 .. 7 at most)
 static_assert(2 * kRegsQuantConsume + 2 * kRegsQuantRest <= 4 * 128, "register split exceeds the launch");
 
-// One CTA of the pass: CTA `bx` of the a.decode_ctas of KV-head group `hg` (decode_cta's counterpart).
+// One CTA of the pass, number b of a.decode_grid: one of the N ranges of each KV-head group; beside chunk
+// items the one that it takes by its SM, and where it arrived last those that are left (cb_place.cuh).
 template <int D, int QS, bool kMod>
 __device__ __forceinline__ void quant_decode_cta(const AttnArgs& a, const QuantArgs& qa,
                                                  const ScoreArgs& sc, const CUtensorMap* kmap,
-                                                 const CUtensorMap* vmap, uint8_t* smem_raw, int bx,
-                                                 int hg) {
+                                                 const CUtensorMap* vmap, uint8_t* smem_raw, int b) {
   using SM = QDecodeSmem<D, QS>;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -668,17 +671,27 @@ __device__ __forceinline__ void quant_decode_cta(const AttnArgs& a, const QuantA
   const int n_cons = QS * HB * slices;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WsLayout L = ws_layout(a.R, a.T, a.Hq, a.D, a.pack);
-  const PlanHeader* hdr = reinterpret_cast<const PlanHeader*>(a.ws + L.header);
+  PlanHeader* hdr = reinterpret_cast<PlanHeader*>(a.ws + L.header);
   const int4* dec_rec = reinterpret_cast<const int4*>(a.ws + L.dec_rec);
-  const int d_first = reinterpret_cast<const int32_t*>(a.ws + L.cta_first)[bx];
+  const int32_t* cta_first = reinterpret_cast<const int32_t*>(a.ws + L.cta_first);
   const long long ntiles = hdr->dec_tiles;
   const int N = hdr->decode_ctas, n_dec = hdr->n_dec;
-  const int c = decode_cta_index(bx, N, a.decode_ctas);
-  if (c < 0 || d_first < 0 || d_first >= n_dec) return;
-  const long long t0 = ntiles * c / N, t1 = ntiles * (c + 1) / N;
-  if (t0 >= t1) return;
+  if (ntiles == 0) return;
+  const int total = N * (a.decode_grid / a.decode_ctas);
+  int* shared = reinterpret_cast<int*>(smem + SM::kRange);  // the range at hand, whether to look for more
   if (threadIdx.x == 0) {
-    const uint32_t bars = sbase + SM::kBar;
+    bool last = false;
+    const int c = decode_cta_index(b % a.decode_ctas, N, a.decode_ctas);
+    int range = c < 0 ? -1 : b / a.decode_ctas * N + c;
+    if (total < a.decode_grid && hdr->pf_qtiles > 0 && a.prefill_ctas > 0) {
+      range = claim_range(hdr, total, a.decode_grid, a.chunk_ctas, &last);
+      if (range < 0 && last) range = next_range(hdr, total);
+    }
+    shared[0] = range;
+    shared[1] = last;
+  }
+  const uint32_t bars = sbase + SM::kBar;
+  auto init = [&]() {
     for (int i = 0; i < SM::kStages; ++i) {
       // the bytes announced, and each producer lane's small copies
       mbar_init(bars + 8 * i, qa.copy == 0 ? 1 : 1 + 32);
@@ -686,24 +699,52 @@ __device__ __forceinline__ void quant_decode_cta(const AttnArgs& a, const QuantA
     }
     for (int i = 0; i < 4; ++i) mbar_init(bars + 8 * (2 * SM::kStages + i), slices);
     fence_barrier_init();
-  }
-  __syncthreads();
-  auto produce = [&]() {
-    quant_produce<D, QS>(a, qa, kmap, vmap, sbase, reinterpret_cast<int*>(smem + SM::kTokens),
-                         n_dec, dec_rec, d_first, hg, HB, t0, t1, lane);
   };
-  // The consumers hold a whole stage in registers: they take what the warps behind them (at most one
-  // of which works, the producer of 8 consumers) leave.
+  if (threadIdx.x == 0) init();
+  __syncthreads();
+  if (shared[0] < 0) return;
+  const bool more = shared[1] != 0;
+  // A role's work on every range of this CTA.
+  auto ranges = [&](auto&& work) {
+    int range = shared[0];
+    while (true) {
+      const int hg = range / N, c = range - hg * N;
+      const long long t0 = ntiles * c / N, t1 = ntiles * (c + 1) / N;
+      const int d_first = cta_first[c];
+      if (t0 < t1 && d_first >= 0 && d_first < n_dec) work(c, hg, d_first, t0, t1);
+      if (!more) break;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        shared[0] = next_range(hdr, total);
+        for (int i = 0; i < 2 * SM::kStages + 4; ++i) mbar_inval(bars + 8 * i);
+        init();
+      }
+      __syncthreads();
+      range = shared[0];
+      if (range < 0) break;
+    }
+  };
+  auto produce = [&](int c, int hg, int d_first, long long t0, long long t1) {
+    quant_produce<D, QS>(a, qa, kmap, vmap, sbase, reinterpret_cast<int*>(smem + SM::kTokens), n_dec,
+                         dec_rec, d_first, hg, HB, t0, t1, lane);
+  };
+  auto consume = [&](int c, int hg, int, long long t0, long long t1) {
+    quant_consume<D, QS, kMod>(a, qa, sc, sbase, c, hg, HB, slices, warp, t1 - t0, ntiles, N, L, lane);
+  };
+  // The consumers hold a whole stage in registers: they take what the warps behind them leave, of which
+  // one works: the producer.
   if (warp < 8) {
     regs_inc<kRegsQuantConsume>();
-    if (warp == n_cons)
-      produce();
-    else if (warp < n_cons)
-      quant_consume<D, QS, kMod>(a, qa, sc, sbase, c, hg, HB, slices, warp, t1 - t0, ntiles, N, L,
-                                 lane);
+    if (warp < n_cons)
+      ranges(consume);
+    else
+      ranges([](int, int, int, long long, long long) {});
   } else {
     regs_dec<kRegsQuantRest>();
-    if (warp == n_cons) produce();
+    if (warp == kQuantProducer)
+      ranges(produce);
+    else
+      ranges([](int, int, int, long long, long long) {});
   }
 }
 

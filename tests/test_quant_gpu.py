@@ -248,6 +248,17 @@ def test_decode_split_and_merged(cuda_lib):
         check_attention(b, decode_ctas=n)
 
 
+def test_decode_ranges_left_to_the_last_cta(cuda_lib):
+    """Beside chunk work the decode CTAs take their ranges by the SM they are on; where too few are on the
+    chosen ones (here 2 to 7 of 152), the last one takes what is left."""
+    for n, kv in ((2, [20, 35]), (4, [70, 30, 35]), (7, [90, 65, 20, 35])):
+        b = workloads.build_batch([1] * (len(kv) - 1) + [30], kv, 8, 8, 128, 16, seed=919 + n)
+        for _ in range(3):
+            check_attention(b, decode_ctas=n)
+    check_attention(workloads.build_batch([1, 1, 40], [3000, 500, 300], 32, 16, 64, 16, seed=929), decode_ctas=5)
+    check_attention(workloads.build_batch([1, 1, 40], [3000, 500, 300], 32, 16, 64, 16, seed=929), decode_ctas=400)
+
+
 def test_decode_many_short_sequences(cuda_lib):
     rng = np.random.default_rng(5)
     kv = rng.integers(1, 70, 700).tolist()
