@@ -282,6 +282,15 @@ cb_status score_args(const cb_score* score, const cb_options* options, float sca
   if (cap > 0.f) {
     out->cap_in = (float)(2.0 * 1.4426950408889634 * (double)scale / (double)cap);
     out->cap_out = cap * 1.4426950408889634f;
+    // tanh(u) = u (c0 + c1 u^2 + ... + c4 u^8) for |u| <= 0.6 (cb_score.cuh)
+    const double c[5] = {0.9999999403953552, -0.33332324028015137, 0.13310357928276062,
+                         -0.052109625190496445, 0.01548669021576643};
+    const double u = (double)scale / (double)cap;
+    if (u > 1e-4 && u < 1e4) {  // (beyond, powers of u and of q.k leave fp32)
+      double f = (double)scale * 1.4426950408889634;
+      for (int i = 0; i < 5; ++i, f *= u * u) out->near[i] = (float)(c[i] * f);
+      out->near_max = (float)(0.6 / u);
+    }
     if (!(out->cap_in > 0.f) || out->cap_in > 1e30f)
       return fail(CB_ERR_INVALID_ARG, "scale / softcap is out of range");
   }

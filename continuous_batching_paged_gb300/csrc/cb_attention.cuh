@@ -3,6 +3,7 @@
 #pragma once
 
 #include "cb_decode.cuh"
+#include "cb_place.cuh"
 #include "cb_prefill.cuh"
 #include "cb_prefix.cuh"
 
@@ -59,7 +60,33 @@ __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorM
     // chunk role stamps its own span inside prefill_cta).
     const bool busy = hdr->dec_tiles > 0;
     if (threadIdx.x == 0 && busy) atomicMin(&hdr->t_dec_start, global_ns());
-    decode_cta<D, QS, kPre, kMod>(a, kmap_dec, vmap_dec, smem_raw, b % a.decode_ctas,
+    const int N = hdr->decode_ctas, total = N * (a.decode_grid / a.decode_ctas);
+    if (kMod && busy && total < a.decode_grid && hdr->pf_qtiles > 0 && a.prefill_ctas > 0) {
+      // beside chunk items: the ranges by the SMs (cb_place.cuh)
+      __shared__ int s_range[2];
+      if (threadIdx.x == 0) {
+        bool last;
+        s_range[0] = claim_range(hdr, total, a.decode_grid, a.chunk_ctas, &last);
+        s_range[1] = last;
+        if (s_range[0] < 0 && last) s_range[0] = next_range(hdr, total);
+      }
+      __syncthreads();
+      while (s_range[0] >= 0) {
+        const int hg = s_range[0] / N, c = s_range[0] - hg * N;
+        decode_cta<D, QS, kPre, kMod>(a, kmap_dec, vmap_dec, smem_raw, decode_cta_of(c, N, a.decode_ctas),
+                                      hg, sc);
+        if (!s_range[1]) break;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          using DS = DecodeSmem<D, QS>;
+          const uint32_t bars = ((smem_u32(smem_raw) + 1023) & ~1023u) + DS::kBarOffset;
+          for (int i = 0; i < 2 * DS::kStages; ++i) mbar_inval(bars + 8 * i);
+          s_range[0] = next_range(hdr, total);
+        }
+        __syncthreads();
+      }
+    } else
+      decode_cta<D, QS, kPre, kMod>(a, kmap_dec, vmap_dec, smem_raw, b % a.decode_ctas,
                                   b / a.decode_ctas, sc);
     if ((threadIdx.x & 31) == 0 && busy) atomicMax(&hdr->t_dec_end, global_ns());
     return;

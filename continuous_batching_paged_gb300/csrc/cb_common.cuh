@@ -240,6 +240,15 @@ __device__ __forceinline__ int decode_cta_index(int bx, int N, int grid) {
   return pairs ? 2 * cu + (bx & 1) : cu;
 }
 
+// A decode CTA of the grid with working index c.
+__device__ __forceinline__ int decode_cta_of(int c, int N, int grid) {
+  if (N >= grid) return c;
+  const bool pairs = ((N | grid) & 1) == 0;
+  const int units = pairs ? grid / 2 : grid, wanted = pairs ? N / 2 : N, cu = pairs ? c >> 1 : c;
+  const int u = (cu * units + wanted - 1) / wanted;
+  return pairs ? 2 * u + (c & 1) : u;
+}
+
 __device__ __forceinline__ void report(uint32_t* err, uint32_t bit) { atomicOr(err, bit); }
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {

@@ -586,20 +586,41 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         for (int i = 0; i < 4; ++i) tmem_ld32(t_lane + s_col + i * 32, sr + i * 32);
         tc_wait_ld();
         const int key0 = j * kChunkKeys;
-        if constexpr (kMod) {  // the scores in units of log2
+        if constexpr (kMod) {  // the scores in units of log2 (where nothing changes them, below)
           if (sc.cap_in > 0.f) {
+            float big = 0.f;
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              sr[c] = __float_as_uint(cap_score(__uint_as_float(sr[c]), sc));
-          } else {
+            for (int c = 0; c < 128; c += 2)
+              big = fmax3(big, fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
+            if (__all_sync(0xffffffffu, big <= sc.near_max)) {
+              uint64_t near[5];
 #pragma unroll
-            for (int c = 0; c < 128; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * sl2);
+              for (int i = 0; i < 5; ++i) near[i] = f2_pack(sc.near[i], sc.near[i]);
+#pragma unroll
+              for (int c = 0; c < 128; c += 2) {
+                float x0, x1;
+                f2_unpack(cap_near(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), near), x0, x1);
+                sr[c] = __float_as_uint(x0);
+                sr[c + 1] = __float_as_uint(x1);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                sr[c] = __float_as_uint(cap_score(__uint_as_float(sr[c]), sc));
+            }
           }
           if (sc.slopes != nullptr) {
-            const float away = (float)(key0 - (diag0 + r));
+            const float first = slope * (float)(key0 - (diag0 + r)), by = sc.cap_in > 0.f ? 1.f : sl2;
+            const uint64_t first2 = f2_pack(first, first), slope2 = f2_pack(slope, slope), by2 = f2_pack(by, by);
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              sr[c] = __float_as_uint(fmaf(slope, away + (float)c, __uint_as_float(sr[c])));
+            for (int c = 0; c < 128; c += 2) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), by2,
+                               f2_fma(f2_pack((float)c, (float)(c + 1)), slope2, first2)),
+                        x0, x1);
+              sr[c] = __float_as_uint(x0);
+              sr[c + 1] = __float_as_uint(x1);
+            }
           }
         }
         // causal edge (keys past the row's position) and, with a sliding window, its lower
@@ -624,7 +645,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(mx8[i], __uint_as_float(sr[120 + i]));
         const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]),
                                fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
-        const float mul = kMod ? 1.f : sl2;
+        const float mul = kMod && (sc.cap_in > 0.f || sc.slopes != nullptr) ? 1.f : sl2;
         const float mt = mx * mul;
         float alpha = 1.f;
         bool resc = false;

@@ -10,11 +10,27 @@
 
 namespace cb {
 
-// cap tanh(u) log2(e) from the raw product s: with t = 2^(cap_in s), cap_in = 2 log2(e) scale / cap,
-// tanh(u) = 1 - 2 / (1 + t).  Off by 2^-22 of the cap at most (two approximations of 2^-22, and the
-// cancellation near 0, which is absolute as well): 2e-5 of a score at a cap of 50.  t = inf gives 1.
+// cap tanh(u) log2(e) from the raw product s, u = s scale / cap: with t = 2^(cap_in s),
+// cap_in = 2 log2(e) scale / cap, tanh(u) = 1 - 2 / (1 + t).  Off by 2^-22 of the cap at most (two
+// approximations of 2^-22, and the cancellation near 0, which is absolute as well): 2e-5 of a score at a
+// cap of 50.  t = inf gives 1.
 __device__ __forceinline__ float cap_score(float s, const ScoreArgs& sc) {
-  return fmaf(-2.f * sc.cap_out, __fdividef(1.f, 1.f + fast_exp2(s * sc.cap_in)), sc.cap_out);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(s * sc.cap_in)));
+  return fmaf(-2.f * sc.cap_out, r, sc.cap_out);
+}
+// The same for two scores with |u| <= 0.6 each, without the two special-function instructions per
+// score: tanh(u) / u is a polynomial in u^2, here the interpolation of degree 4 at Chebyshev's points of
+// [0, 0.36], off by 4e-8 in tanh.  The host multiplies scale log2(e) and the powers of scale / cap into
+// the coefficients (ScoreArgs::near), so it takes six instructions on the raw products s.
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t cap_near(uint64_t s, const uint64_t (&k)[5]) {
+  const uint64_t z = f2_mul(s, s);
+  return f2_mul(s, f2_fma(f2_fma(f2_fma(f2_fma(k[4], z, k[3]), z, k[2]), z, k[1]), z, k[0]));
 }
 // The raw product s of a query at `pos` and key `key`, in units of log2.
 __device__ __forceinline__ float change_score(float s, float scale_log2, float slope_log2, int key,
