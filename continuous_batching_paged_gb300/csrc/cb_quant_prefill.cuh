@@ -30,6 +30,7 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
   const uint32_t row_full = sbase + QM::kBar, row_empty = row_full + 8 * kRowSlots;
   RowSlot* ring = reinterpret_cast<RowSlot*>(smem + QM::kRows);
   if (lane == 0) tma_prefetch_desc(qmap);
+  const int whole = kChunkKeys / a.bs, rest = kChunkKeys - whole * a.bs;  // a tile in blocks
   uint32_t n = 0;  // tiles so far
   bool ok = true;
   auto wait = [&](uint32_t b, uint32_t parity) {
@@ -64,27 +65,68 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
       }
     }
     const int32_t* table = a.block_table + (size_t)it.s * a.max_blocks;
-    for (int j = it.j0; j < it.nt_all && ok; ++j, ++n) {
-      int tok[4];
-      unsigned short sc[4];
+    // Three tiles are in work: one's factors are written, the next one's scales and the block ids of the
+    // one behind it are on their way (with the chain of both loads per tile, the pass waited for this warp:
+    // 8 chunks of 512 tokens 169 us, now 148).
+    int lb[4], off[4];  // the block and the offset in it of this lane's keys, in the tile of `ent`
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int pos = it.j0 * kChunkKeys + 32 * i + lane;
+      lb[i] = pos / a.bs;
+      off[i] = pos - lb[i] * a.bs;
+    }
+    int ent[4], tok[4];
+    unsigned short sc[4];
+    auto fetch = [&](int j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int pos = j * kChunkKeys + 32 * i + lane;
+        ent[i] = -1;  // no key
+        if (j * kChunkKeys + 32 * i + lane < it.nk_all)
+          ent[i] = lb[i] < a.max_blocks ? __ldg(table + lb[i]) : -2;
+      }
+    };
+    auto resolve = [&]() {  // ent's tokens, and their scales
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         tok[i] = -1;
-        sc[i] = 0;
-        if (pos < it.nk_all) {
-          const int lb = pos / a.bs;
-          const int e = lb < a.max_blocks ? __ldg(table + lb) : -1;
-          if (e >= 0 && e < a.P)
-            tok[i] = e * a.bs + (pos - lb * a.bs);
-          else
-            report(a.err, kErrOutOfRange);
-        }
+        if (ent[i] >= 0 && ent[i] < a.P)
+          tok[i] = ent[i] * a.bs + off[i];
+        else if (ent[i] != -1)
+          report(a.err, kErrOutOfRange);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        sc[i] = 0;
         if (tok[i] >= 0)
           sc[i] = __ldg(reinterpret_cast<const unsigned short*>(qa.scales) + (size_t)tok[i] * a.Hkv + it.kvh);
+      }
+    };
+    auto advance = [&]() {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        off[i] += rest;
+        lb[i] += whole;
+        if (off[i] >= a.bs) {
+          off[i] -= a.bs;
+          ++lb[i];
+        }
+      }
+    };
+    fetch(it.j0);
+    resolve();
+    advance();
+    fetch(it.j0 + 1);
+    for (int j = it.j0; j < it.nt_all && ok; ++j, ++n) {
+      int tok_j[4];
+      unsigned short sc_j[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        tok_j[i] = tok[i];
+        sc_j[i] = sc[i];
+      }
+      resolve();
+      advance();
+      fetch(j + 2);
       RowSlot& rs = ring[n % kRowSlots];
       wait(row_empty + 8 * (n % kRowSlots), ((n / kRowSlots) & 1) ^ 1);
       // The factors: 2^120 (codes_to_bf16x4) times the scale, which bf16 holds for scales up to 2^7; the
@@ -92,14 +134,13 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
       bool more = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int ek = (int)(sc[i] & 255) - kQuantBias, ev = (int)(sc[i] >> 8) - kQuantBias;
+        const int ek = (int)(sc_j[i] & 255) - kQuantBias, ev = (int)(sc_j[i] >> 8) - kQuantBias;
         const uint32_t fk = ek == kQuantNan - kQuantBias ? 0x7fffu : (uint32_t)(247 + min(ek, 7)) << 7;
         const uint32_t fv = ev == kQuantNan - kQuantBias ? 0x7fffu : (uint32_t)(247 + min(ev, 7)) << 7;
-        const uint32_t f = fk | fv << 16;
-        rs.row[32 * i + lane] =
-            make_uint2(tok[i] < 0 ? kNoRow : (uint32_t)tok[i] * a.Hkv + it.kvh, tok[i] < 0 ? 0u : f);
+        rs.row[32 * i + lane] = make_uint2(tok_j[i] < 0 ? kNoRow : (uint32_t)tok_j[i] * a.Hkv + it.kvh,
+                                           tok_j[i] < 0 ? 0u : fk | fv << 16);
         rs.more[32 * i + lane] = (uint32_t)(127 + max(ek - 7, 0)) << 7 | (uint32_t)(127 + max(ev - 7, 0)) << 23;
-        more = more || (tok[i] >= 0 && max(ek, ev) > 7);
+        more = more || (tok_j[i] >= 0 && max(ek, ev) > 7);
       }
       more = __any_sync(0xffffffffu, more);
       if (lane == 0) {
