@@ -181,7 +181,9 @@ __device__ __forceinline__ uint4 codes_to_bf16(uint2 codes, int e) {
 // Output rows g.rows * w .. of warp w.  Each lane finds the cache row of one of them (a binary search
 // of its own, so a warp's rows cost one chain of metadata loads together); then the warp takes the rows
 // one after the other, 8 codes of a lane becoming 16 bytes, so that loads and stores are both whole
-// lines.  Bound by bytes: (2 D + 2) Hkv read and 4 D Hkv written per row.
+// lines.  Bound by bytes: (2 D + 2) Hkv read and 4 D Hkv written per row; 95859 rows of 8 heads of 128
+// take 89 us, 6.0 TB/s.  (8 pieces in flight per lane instead of 4 gain nothing there and cost small
+// ranges: 10690 rows of 5 heads of 64 12.9 and 17 us.)
 template <int kUnroll>
 __device__ __forceinline__ void gather_rows(const GatherArgs& g, long long warp) {
   const int lane = threadIdx.x & 31;
