@@ -60,28 +60,28 @@ __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorM
     // chunk role stamps its own span inside prefill_cta).
     const bool busy = hdr->dec_tiles > 0;
     if (threadIdx.x == 0 && busy) atomicMin(&hdr->t_dec_start, global_ns());
-    const int N = hdr->decode_ctas, total = N * (a.decode_grid / a.decode_ctas);
-    if (kMod && busy && total < a.decode_grid && hdr->pf_qtiles > 0 && a.prefill_ctas > 0) {
-      // beside chunk items: the ranges by the SMs (cb_place.cuh)
+    if (kMod && busy) {
+      // Its ranges: one or none, beside chunk items by its SM (cb_place.cuh).
+      const int N = hdr->decode_ctas, total = N * (a.decode_grid / a.decode_ctas);
       __shared__ int s_range[2];
       if (threadIdx.x == 0) {
-        bool last;
-        s_range[0] = claim_range(hdr, total, a.decode_grid, a.chunk_ctas, &last);
-        s_range[1] = last;
-        if (s_range[0] < 0 && last) s_range[0] = next_range(hdr, total);
+        const int c = decode_cta_index(b % a.decode_ctas, N, a.decode_ctas), mine = b / a.decode_ctas * N + c;
+        RangeClaim r = {mine, c < 0 ? mine : mine + 1};
+        if (total < a.decode_grid && hdr->pf_qtiles > 0 && a.prefill_ctas > 0)
+          r = claim_range(hdr, total, a.decode_grid, a.chunk_ctas);
+        s_range[0] = r.first;
+        s_range[1] = r.end;
       }
       __syncthreads();
-      while (s_range[0] >= 0) {
-        const int hg = s_range[0] / N, c = s_range[0] - hg * N;
+      for (int range = s_range[0], end = s_range[1]; range < end; ++range) {
+        const int hg = range / N, c = range - hg * N;
         decode_cta<D, QS, kPre, kMod>(a, kmap_dec, vmap_dec, smem_raw, decode_cta_of(c, N, a.decode_ctas),
                                       hg, sc);
-        if (!s_range[1]) break;
         __syncthreads();
         if (threadIdx.x == 0) {
           using DS = DecodeSmem<D, QS>;
           const uint32_t bars = ((smem_u32(smem_raw) + 1023) & ~1023u) + DS::kBarOffset;
           for (int i = 0; i < 2 * DS::kStages; ++i) mbar_inval(bars + 8 * i);
-          s_range[0] = next_range(hdr, total);
         }
         __syncthreads();
       }
@@ -89,7 +89,10 @@ __device__ __forceinline__ void attention_cta(const AttnArgs& a, const CUtensorM
       decode_cta<D, QS, kPre, kMod>(a, kmap_dec, vmap_dec, smem_raw, b % a.decode_ctas,
                                   b / a.decode_ctas, sc);
     if ((threadIdx.x & 31) == 0 && busy) atomicMax(&hdr->t_dec_end, global_ns());
-    return;
+    if (!kMod || a.prefill_ctas == 0 || hdr->pf_qtiles == 0) return;
+    // kMod: every CTA goes on to chunk items (as in cb_quant_attention.cuh)
+    fence_proxy_async_smem();
+    __syncthreads();
   }
   prefill_cta<D, kWin, kMod>(a, qmap, kmap_chunk, vmap_chunk, smem_raw, sc);
 }

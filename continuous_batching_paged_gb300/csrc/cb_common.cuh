@@ -60,8 +60,9 @@ struct PlanHeader {
   int32_t pre_cost;         // their work per KV head, in cost units (PreGroup),
   int32_t pre_tokens;       // entries of the groups' token list,
   int32_t pre_chains;       // and their chains per KV head
-  // counters of claim_range (cb_place.cuh), reset by the planner
-  int32_t dec_claims, dec_arrivals;
+  // of claim_range (cb_place.cuh), reset by the planner: decode CTAs that have arrived (high half), and
+  // ranges that they took
+  unsigned long long dec_claims;
 };
 
 // Byte offsets of the workspace sections (all 256-byte aligned).

@@ -122,6 +122,12 @@ struct QuantArgs {
   int copy;       // bytes of a copy of scales: 16, 8, 4, 2 (plain loads), or 0 (a page run's at once)
 };
 
+// CTAs of an attention kernel whose decode CTAs go on to chunk items (the 8-bit cache, changed scores): as
+// many more as leave none of prefill_ctas out.
+inline int launch_ctas(const AttnArgs& a) {
+  return a.decode_grid > a.prefill_ctas ? a.decode_grid : a.prefill_ctas;
+}
+
 // Block moves: copy (pool -> pool), offload (pool -> linear host buffer), restore (host ->
 // pool).  Per pool (K, V) one block is block_bytes contiguous bytes.
 enum BlockMoveMode { kMoveCopy = 0, kMoveOffload = 1, kMoveRestore = 2 };

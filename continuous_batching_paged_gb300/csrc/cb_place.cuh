@@ -13,23 +13,23 @@
 
 namespace cb {
 
-// Of one thread of each of the `grid` decode CTAs: the range (of `total` < grid) that it takes, or -1.
-// *last: it arrived last, and has to take the ranges that are left, if any (next_range): the chosen
-// SMs may have had too few CTAs, for instance where another launch holds some.
-__device__ __forceinline__ int claim_range(PlanHeader* hdr, int total, int grid, int sms, bool* last) {
+// Of one thread of each of the `grid` decode CTAs: the ranges (of `total` < grid) that it takes, first to
+// end - 1; most often one or none.  The CTA that arrives last also takes those that are left, if any: the
+// chosen SMs may have had too few CTAs, for instance where another launch holds some.  (One atomic per
+// CTA, for the claim and the arrival: with one for each the step took 4 us longer.)
+struct RangeClaim {
+  int first, end;
+};
+__device__ __forceinline__ RangeClaim claim_range(PlanHeader* hdr, int total, int grid, int sms) {
   unsigned sm;
   asm("mov.u32 %0, %%smid;" : "=r"(sm));
   const int tpcs = (sms + 1) / 2, pairs = (total + 1) / 2, tpc = (int)(sm >> 1) % tpcs;
-  int range = -1;
   // every tpcs / pairs-th TPC, spread evenly
-  if ((tpc + 1) * pairs / tpcs > tpc * pairs / tpcs) range = atomicAdd(&hdr->dec_claims, 1);
-  __threadfence();  // (the claim before the arrival)
-  *last = atomicAdd(&hdr->dec_arrivals, 1) == grid - 1;
-  return range < total ? range : -1;
-}
-__device__ __forceinline__ int next_range(PlanHeader* hdr, int total) {
-  const int range = atomicAdd(&hdr->dec_claims, 1);
-  return range < total ? range : -1;
+  const int chosen = (tpc + 1) * pairs / tpcs > tpc * pairs / tpcs;
+  const unsigned long long old = atomicAdd(&hdr->dec_claims, (1ull << 32) | (unsigned)chosen);
+  const int taken = min((int)(old & 0xffffffffu), total);
+  const bool last = (int)(old >> 32) == grid - 1;
+  return {taken, last ? total : min(taken + chosen, total)};
 }
 
 }  // namespace cb

@@ -77,16 +77,14 @@ __device__ __forceinline__ void block_scan4(int v[4], int ex[4], int tot[4], int
 // takes at most a quarter of the step.  Without chunk work all CTAs decode.  Called by one
 // full warp; candidates
 // N = 4, 8, ... are spread over the lanes, in fp32 (the fp64 rate of this part is far too low
-// for even this much arithmetic on one thread).  kQuant: over the 8-bit cache a decode CTA streams 0.062
-// TB/s (its arithmetic bounds it) and the chunk pass runs at 5.4 TFLOP/s per SM.
-template <bool kQuant = false>
+// for even this much arithmetic on one thread).
 __device__ __forceinline__ int choose_decode_ctas(float dec_bytes, float chunk_flops, int chunk_items,
                                   int max_ctas, long long tiles) {
   const int lane = threadIdx.x & 31;
   if (tiles <= 0) return 1;
   const int cap = (int)(tiles < max_ctas ? tiles : max_ctas);
   if (chunk_flops <= 0.f || chunk_items <= 0) return cap;
-  const float w_us = chunk_flops * (kQuant ? 1.f / 5.4e6f : 1.f / 6.4e6f);  // chunk work in SM-microseconds
+  const float w_us = chunk_flops * (1.f / 6.4e6f);  // chunk work in SM-microseconds
   const float item_us = w_us / (float)chunk_items;
   const float b_mb = dec_bytes * 1e-6f;             // decode bytes / 1e6: MB / (TB/s) = us
   const int n_cand = (cap + 3) / 4;
@@ -101,7 +99,7 @@ __device__ __forceinline__ int choose_decode_ctas(float dec_bytes, float chunk_f
     td[k] = 0.f;
     chunk_bound[k] = false;
     if (i < n_cand) {
-      const float lin = (kQuant ? 0.062f : 0.11f) * n[k], sat = 6.8f;
+      const float lin = 0.11f * n[k], sat = 6.8f;
       const float bw = rcbrtf(1.f / (lin * lin * lin) + 1.f / (sat * sat * sat));
       td[k] = b_mb / bw;
       const int m = max_ctas - n[k];
@@ -131,6 +129,52 @@ __device__ __forceinline__ int choose_decode_ctas(float dec_bytes, float chunk_f
     if (t[k] <= 1.01f * t_min) best = best > n[k] ? best : n[k];
   for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
   return best;
+}
+
+// The same over the 8-bit cache, where a decode CTA's arithmetic bounds it: 1.05 us a tile at head_dim 128
+// and 0.83 at 64 (of all its heads), 4 us for its start and end, and HBM's share beyond; chunk items are
+// taken as equal, each its share of the work at 6.6 or 4.1 TFLOP/s (head_dim 128, 64) and 3 us.  n CTAs for
+// each of the head groups take d us; the other m SMs have begun m ceil(d / item) items by then, and
+// what is left goes to every SM as it becomes free, the former at d, the latter at their item's end.  The
+// choice is the middle of those within 1% of the least time: at both ends the model's steps are least
+// to be relied on.  Called by one full warp.
+__device__ __forceinline__ int choose_quant_ctas(const AttnArgs& a, float dec_bytes, float chunk_flops,
+                                                 int items, long long tiles) {
+  const int lane = threadIdx.x & 31;
+  if (tiles <= 0) return 1;
+  const int cap = (int)(tiles < a.decode_ctas ? tiles : a.decode_ctas);
+  if (chunk_flops <= 0.f || items <= 0) return cap;
+  const int per_cta = a.G > 8 ? kMaxDecodeHeadsPerCta / 2 : kMaxDecodeHeadsPerCta;
+  const int groups = (a.Hkv + per_cta - 1) / per_cta, sms = a.chunk_ctas;
+  const float x1 = (a.D == 128 ? 1.05f : 0.83f) * (float)tiles, y = dec_bytes * (1.f / 6.8e6f);
+  const float item = 3.f + chunk_flops * (a.D == 128 ? 1.f / 6.6e6f : 1.f / 4.1e6f) / (float)items;
+  float t[4], least = 3.4e38f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {  // (at most 256 CTAs: by default an SM each)
+    const int n = min(2 * (lane + 32 * k + 1), cap);
+    const float x = __fdividef(x1, (float)n), d = 4.f + cbrtf(x * x * x + y * y * y);
+    const float m = (float)max(sms - n * groups, 0), dec = (float)sms - m;
+    const float begun = ceilf(__fdividef(d, item)), left = (float)items - m * begun;
+    t[k] = left > 0.f
+               ? fminf(d + item * ceilf(__fdividef(left + m, dec + m)),
+                       fmaxf(d, item * begun) + item * ceilf(__fdividef(left, dec + m)))
+               : fmaxf(d, item * ceilf(__fdividef((float)items, m)));
+    least = fminf(least, t[k]);
+  }
+  for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+  int lo = cap, hi = 1;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (t[k] <= 1.01f * least) {
+      lo = min(lo, 2 * (lane + 32 * k + 1));
+      hi = max(hi, min(2 * (lane + 32 * k + 1), cap));
+    }
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  const int mid = (lo + hi) / 4 * 2;
+  return mid < 1 ? lo : mid;
 }
 
 // Histogram bin of chunk unit g (global index in chunk-sequence order): units that stream
@@ -661,7 +705,7 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a, int tile_log2 = 0) {
     hdr->pf_counter = 0;
     hdr->t_dec_start = hdr->t_pf_start = ~0ull;
     hdr->t_dec_end = hdr->t_pf_end = 0ull;
-    if constexpr (!kPre) hdr->dec_claims = hdr->dec_arrivals = 0;
+    if constexpr (!kPre) hdr->dec_claims = 0ull;
   }
   __syncthreads();
   // Chunk units longest first (a counting sort on the K/V tiles each streams, descending), so
@@ -740,10 +784,10 @@ __device__ __forceinline__ void plan_cta(const AttnArgs& a, int tile_log2 = 0) {
       if (tid == 0)
         hdr->pre_ctas = pre_cta_count(idle > 0 ? idle : a.chunk_ctas / 8, items, most, m);
     } else if (a.decode_auto) {
-      n = choose_decode_ctas<kQuant>(keys * (float)(a.Hkv * (kQuant ? 2 * a.D + 2 : 4 * a.D)),
-                                     pairs * (float)(4 * a.D * a.Hq),
-                                     n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq),
-                                     a.decode_ctas, ntiles);
+      const float flops = pairs * (float)(4 * a.D * a.Hq);
+      const int items = n_units * (pf_pair_heads(a.G) ? a.Hq / 2 : a.Hq);
+      n = kQuant ? choose_quant_ctas(a, keys * (float)(a.Hkv * (2 * a.D + 2)), flops, items, ntiles)
+                 : choose_decode_ctas(keys * (float)(a.Hkv * a.D * 4), flops, items, a.decode_ctas, ntiles);
     }
     if (kPre && pre_cost == 0 && tid == 0) hdr->pre_ctas = 0;
     if (tid == 0) {

@@ -1,6 +1,8 @@
 // The attention kernel over the quantised cache: the decode pass (cb_quant_decode.cuh) and the chunk
-// pass (cb_prefill.cuh, cb_quant_prefill.cuh) in one launch, laid out on the grid like the attention
-// kernel's (cb_attention.cu).
+// pass (cb_prefill.cuh, cb_quant_prefill.cuh) in one launch.  Its first a.decode_grid CTAs take the decode
+// ranges, and every CTA then takes chunk items while there are any: an SM that the planner leaves to the
+// chunk pass begins with it at once, and one whose range is done goes on without another CTA's launch
+// (4 us of a step of 60 beside CTAs that only leave their SM).
 #pragma once
 
 #include "cb_quant_decode.cuh"
@@ -30,7 +32,9 @@ __global__ void __launch_bounds__(kQuantPrefillThreads, 1)
     if (threadIdx.x == 0 && busy) atomicMin(&hdr->t_dec_start, global_ns());
     quant_decode_cta<D, QS, kMod>(a, qa, sc, &kmap, &vmap, smem_raw, b);
     if ((threadIdx.x & 31) == 0 && busy) atomicMax(&hdr->t_dec_end, global_ns());
-    return;
+    if (a.prefill_ctas == 0 || hdr->pf_qtiles == 0) return;
+    fence_proxy_async_smem();  // (the chunk pass's copies into what the decode role wrote)
+    __syncthreads();
   }
   prefill_cta<D, kMod, kMod, true>(a, &qmap, nullptr, nullptr, smem_raw, sc, qa);
 }
@@ -55,7 +59,7 @@ static cudaError_t launch_quant_instance(const AttnArgs& a, const QuantArgs& qa,
     if (f.numRegs < 121) return cudaErrorInvalidConfiguration;  // (allocated in eights: 128)
     configured_ctx = ctx;
   }
-  return launch_dependent(quant_attention_kernel<D, QS, kMod>, (unsigned)(a.decode_grid + a.prefill_ctas),
+  return launch_dependent(quant_attention_kernel<D, QS, kMod>, (unsigned)launch_ctas(a),
                           kQuantPrefillThreads, kSmem, stream, a, qa, sc, m.q, m.k, m.v);
 }
 

@@ -678,17 +678,14 @@ __device__ __forceinline__ void quant_decode_cta(const AttnArgs& a, const QuantA
   const int N = hdr->decode_ctas, n_dec = hdr->n_dec;
   if (ntiles == 0) return;
   const int total = N * (a.decode_grid / a.decode_ctas);
-  int* shared = reinterpret_cast<int*>(smem + SM::kRange);  // the range at hand, whether to look for more
+  int* shared = reinterpret_cast<int*>(smem + SM::kRange);  // this CTA's ranges
   if (threadIdx.x == 0) {
-    bool last = false;
-    const int c = decode_cta_index(b % a.decode_ctas, N, a.decode_ctas);
-    int range = c < 0 ? -1 : b / a.decode_ctas * N + c;
-    if (total < a.decode_grid && hdr->pf_qtiles > 0 && a.prefill_ctas > 0) {
-      range = claim_range(hdr, total, a.decode_grid, a.chunk_ctas, &last);
-      if (range < 0 && last) range = next_range(hdr, total);
-    }
-    shared[0] = range;
-    shared[1] = last;
+    const int c = decode_cta_index(b % a.decode_ctas, N, a.decode_ctas), mine = b / a.decode_ctas * N + c;
+    RangeClaim r = {mine, c < 0 ? mine : mine + 1};
+    if (total < a.decode_grid && hdr->pf_qtiles > 0 && a.prefill_ctas > 0)
+      r = claim_range(hdr, total, a.decode_grid, a.chunk_ctas);
+    shared[0] = r.first;
+    shared[1] = r.end;
   }
   const uint32_t bars = sbase + SM::kBar;
   auto init = [&]() {
@@ -702,26 +699,28 @@ __device__ __forceinline__ void quant_decode_cta(const AttnArgs& a, const QuantA
   };
   if (threadIdx.x == 0) init();
   __syncthreads();
-  if (shared[0] < 0) return;
-  const bool more = shared[1] != 0;
+  const int first = shared[0], end = shared[1];
+  if (first >= end) {
+    __syncthreads();
+    if (threadIdx.x == 0)
+      for (int i = 0; i < 2 * SM::kStages + 4; ++i) mbar_inval(bars + 8 * i);
+    return;
+  }
   // A role's work on every range of this CTA.
   auto ranges = [&](auto&& work) {
-    int range = shared[0];
-    while (true) {
+    for (int range = first;;) {
       const int hg = range / N, c = range - hg * N;
       const long long t0 = ntiles * c / N, t1 = ntiles * (c + 1) / N;
       const int d_first = cta_first[c];
       if (t0 < t1 && d_first >= 0 && d_first < n_dec) work(c, hg, d_first, t0, t1);
+      __syncthreads();
+      const bool more = ++range < end;
+      if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * SM::kStages + 4; ++i) mbar_inval(bars + 8 * i);
+        if (more) init();
+      }
       if (!more) break;
       __syncthreads();
-      if (threadIdx.x == 0) {
-        shared[0] = next_range(hdr, total);
-        for (int i = 0; i < 2 * SM::kStages + 4; ++i) mbar_inval(bars + 8 * i);
-        init();
-      }
-      __syncthreads();
-      range = shared[0];
-      if (range < 0) break;
     }
   };
   auto produce = [&](int c, int hg, int d_first, long long t0, long long t1) {
@@ -739,12 +738,14 @@ __device__ __forceinline__ void quant_decode_cta(const AttnArgs& a, const QuantA
       ranges(consume);
     else
       ranges([](int, int, int, long long, long long) {});
+    regs_dec<128>();  // as launched
   } else {
     regs_dec<kRegsQuantRest>();
     if (warp == kQuantProducer)
       ranges(produce);
     else
       ranges([](int, int, int, long long, long long) {});
+    regs_inc<128>();
   }
 }
 

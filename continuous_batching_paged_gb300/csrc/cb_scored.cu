@@ -30,7 +30,7 @@ static cudaError_t launch_instance(const AttnArgs& a, const ScoreArgs& sc, const
     if (e != cudaSuccess) return e;
     configured_ctx = ctx;
   }
-  return launch_dependent(scored_attention_kernel<D, QS>, (unsigned)(a.decode_grid + a.prefill_ctas),
+  return launch_dependent(scored_attention_kernel<D, QS>, (unsigned)launch_ctas(a),
                           kAttnThreads, kSmem, stream, a, sc, m.q, m.k_dec, m.v_dec, m.k_chunk,
                           m.v_chunk);
 }
