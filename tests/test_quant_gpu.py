@@ -502,3 +502,135 @@ def test_random_batches(cuda_lib, seed):
     if sum(ql) == 0:
         return
     check_attention(b, spread=float(rng.choice([0, 2])), seed=seed, decode_ctas=int(rng.choice([0, 0, 3])))
+
+
+def test_same_bits_on_every_call(cuda_lib):
+    """Which CTA computes what depends on the GPU's state, the results do not."""
+    b = workloads.build_batch([1] * 20 + [200, 1, 77], list(range(100, 2100, 100)) + [900, 5000, 333], 16, 2, 128, 32,
+                              seed=990)
+    d, out, lse = check_attention(b)
+    for _ in range(10):
+        o, l = cb.quant_attention(d.q, *d.pools, *d.where, b.scale, lse=True)
+        assert torch.equal(o.view(torch.int16), out.view(torch.int16)) and torch.equal(l, lse)
+
+
+def test_two_streams_at_once(cuda_lib):
+    """Two batches on two streams, each with its workspace, over and over: as alone."""
+    calls = []
+    for i, (hq, hkv) in enumerate(((8, 2), (32, 8))):
+        b = workloads.build_batch([1] * 8 + [90, 1], [700, 33, 1500, 64, 900, 10, 2000, 128, 400, 77], hq, hkv, 128, 16,
+                                  seed=991 + i)
+        d, out, _ = check_attention(b)
+        calls.append((b, d, out, torch.cuda.Stream(), d.workspace(), torch.empty_like(out)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for b, d, out, stream, ws, o in calls:
+            cb.quant_attention(d.q, *d.pools, *d.where, b.scale, out=o, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for b, d, out, _, _, o in calls:
+        assert torch.equal(o.view(torch.int16), out.view(torch.int16))
+    assert cb.get_device_error() == cb.CB_OK
+
+
+def test_many_sequences_heads_and_keys(cuda_lib):
+    rng = np.random.default_rng(7)
+    ql = rng.choice([0, 1, 1, 2], 2500).tolist()
+    kl = [n + int(x) for n, x in zip(ql, rng.integers(1, 30, 2500))]
+    check_attention(workloads.build_batch(ql, kl, 2, 1, 64, 8, seed=993))
+    check_attention(workloads.build_batch([1, 1, 20], [300, 40, 60], 80, 40, 64, 16, seed=994))
+    check_attention(workloads.build_batch([1, 3], [70000, 66000], 2, 1, 64, 128, seed=995))
+
+
+def test_served_by_the_scheduler(cuda_lib):
+    """Requests served step by step over the 8-bit cache (the scheduler's lengths and block tables): every
+    step's rows against the oracle's cache."""
+    from continuous_batching_paged_gb300.runtime import BlockAllocator, Scheduler
+    P, bs, hq, hkv, D, mb = 64, 16, 8, 2, 128, 12
+    sched = Scheduler(BlockAllocator(P, bs, mb), max_batch_tokens=64, max_requests_per_batch=8)
+    for i, (n, m) in enumerate(((70, 4), (5, 6), (33, 3))):
+        sched.add_request(i, prompt_len=n, max_new_tokens=m)
+    k = np.full((P, bs, hkv, D), 0x7F, dtype=np.uint8)
+    v, sc = k.copy(), np.full((P, bs, hkv, 2), 255, dtype=np.uint8)
+    dk, dv, dsc = (torch.from_numpy(x).cuda() for x in (k, v, sc))
+    pools = dk.view(torch.float8_e4m3fn), dv.view(torch.float8_e4m3fn), dsc
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    steps = 0
+    while sched.num_active():
+        step = sched.step()
+        S = len(step["seq_ids"])
+        if S == 0:
+            continue
+        T, cu, kv, table = int(step["num_tokens"]), step["cu_seqlens_q"], step["kv_lens"], step["block_table"]
+        q, kn, vn = (torch.randn(T, h, D, generator=gen, device="cuda").bfloat16() for h in (hq, hkv, hkv))
+        out, lse = cb.quant_append_attention(q, kn, vn, *pools, i32(table.copy()), i32(cu.copy()), i32(kv.copy()), bs,
+                                             D ** -0.5, lse=True)
+        assert cb.get_device_error() == cb.CB_OK
+        codes = [oq.quantise(f64(x)) for x in (kn, vn)]
+        for s in range(S):
+            for t in range(int(cu[s]), int(cu[s + 1])):
+                p = int(kv[s]) - int(cu[s + 1]) + t
+                at = int(table[s, p // bs]), p % bs
+                for w, pool in ((0, k), (1, v)):
+                    pool[at], sc[at + (slice(None), w)] = codes[w][0][t], codes[w][1][t]
+        for s in range(S):
+            c0, c1 = int(cu[s]), int(cu[s + 1])
+            if c1 > c0:
+                pos = np.arange(int(kv[s]))
+                blk, off = table[s, pos // bs], pos % bs
+                K, V = oq.values(k[blk, off], sc[blk, off, :, 0]), oq.values(v[blk, off], sc[blk, off, :, 1])
+                check_rows(f64(out[c0:c1]), f64(lse[c0:c1]), f64(q[c0:c1]), K, V, int(kv[s]) - (c1 - c0), D ** -0.5,
+                           P16 if c1 - c0 == 1 else P8, f"step {steps}, sequence {s}")
+        steps += 1
+    assert steps >= 5
+    assert np.array_equal(dk.cpu().numpy(), k) and np.array_equal(dsc.cpu().numpy(), sc)
+
+
+def test_binding_refusals(cuda_lib):
+    b = workloads.build_batch([1, 3], [40, 30], 4, 2, 64, 16, seed=996)
+    d = QuantBatch(b)
+    ok = dict(q=d.q, pools=d.pools, where=d.where)
+    bad_sc = d.dsc[..., 0].contiguous()
+    f = torch.float32
+    attend = lambda q=d.q, pools=d.pools, where=d.where, **kw: cb.quant_attention(q, *pools, *where, 0.125, **kw)
+    for match, call in [
+            ("kv_scales must be", lambda: attend(pools=(d.dk, d.dv, bad_sc))),
+            ("float8_e4m3fn", lambda: attend(pools=(d.dk.view(torch.uint8), d.dv, d.dsc))),
+            ("match k_pages", lambda: attend(pools=(d.dk, d.dv[:3].contiguous(), d.dsc))),
+            ("block_size", lambda: attend(where=(d.table, d.cu, d.kv, 8))),
+            ("num_seqs \\+ 1", lambda: attend(where=(d.table, d.cu[:-1].contiguous(), d.kv, 16))),
+            ("bfloat16", lambda: attend(q=d.q.float())),
+            ("contiguous", lambda: attend(q=d.q.transpose(0, 1))),
+            ("slopes must be", lambda: attend(slopes=torch.zeros(3, device="cuda"))),
+            ("slopes must be", lambda: attend(slopes=torch.zeros(4, device="cuda", dtype=torch.float64))),
+            ("visible_lens", lambda: attend(visible_lens=torch.zeros(3, device="cuda", dtype=torch.int32))),
+            ("visible_lens", lambda: attend(visible_lens=torch.zeros(2, device="cuda"))),
+            ("softcap", lambda: attend(softcap="5")),
+            ("out must be", lambda: attend(out=torch.empty(4, 4, 128, device="cuda", dtype=torch.bfloat16))),
+            ("lse must be", lambda: attend(lse=torch.empty(3, 4, device="cuda"))),
+            ("workspace must be", lambda: attend(workspace=torch.empty(9, device="cuda"))),
+            ("window", lambda: attend(window=2 ** 40)),
+            ("q_out without q", lambda: cb.quant_append(None, d.k_new, d.v_new, *d.pools, *d.where, q_out=d.q)),
+            ("k_new must be", lambda: cb.quant_append(None, d.k_new[:, :1], d.v_new[:, :1], *d.pools, *d.where)),
+            ("v_new must match", lambda: cb.quant_append(None, d.k_new, d.v_new[:2], *d.pools, *d.where)),
+            ("contiguous token rows", lambda: cb.quant_append(None, d.k_new[:1].expand(4, 2, 64), d.v_new, *d.pools, *d.where)),
+            ("cos_sin must be", lambda: cb.quant_append(d.q, d.k_new, d.v_new, *d.pools, *d.where, cos_sin=torch.zeros(64, 64, device="cuda").double())),
+            ("q_out without cos_sin", lambda: cb.quant_append_attention(d.q, d.k_new, d.v_new, *d.pools, *d.where, 0.125, q_out=d.q)),
+            ("num_rows", lambda: cb.quant_gather(*d.pools, d.table, d.cu, 16, -1)),
+            ("num_rows", lambda: cb.quant_gather(*d.pools, d.table, d.cu, 16, 2.5)),
+            ("key_starts", lambda: cb.quant_gather(*d.pools, d.table, d.cu, 16, 4, key_starts=d.cu)),
+            ("k_out must be", lambda: cb.quant_gather(*d.pools, d.table, d.cu, 16, 4, k_out=torch.empty(3, 2, 64, device="cuda", dtype=torch.bfloat16))),
+            ("block_size", lambda: cb.quant_gather(*d.pools, d.table, d.cu, 8, 4))]:
+        with pytest.raises(ValueError, match=match):
+            call()
+    for call in (lambda: cb.quant_append(d.q, d.k_new, d.v_new, *d.pools, *d.where),       # a q that nothing turns
+                 lambda: attend(softcap=-1.0), lambda: attend(out=d.q),
+                 lambda: attend(visible_lens=d.kv, window=4), lambda: attend(window=-3)):
+        with pytest.raises(cb.CbError):
+            call()
+    assert cb.get_device_error() == cb.CB_OK
+    # accepted: numpy integers, a view of wider rows, given outputs
+    d.append_new()
+    d.upload()
+    out = torch.empty_like(d.q)
+    assert attend(out=out, decode_ctas=np.int64(4), softcap=np.float32(0)) is out
+    cb.quant_gather(*d.pools, d.table, d.cu, np.int32(16), np.int64(4))
