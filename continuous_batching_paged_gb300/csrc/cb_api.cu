@@ -2,6 +2,7 @@
 // and the per-device error word.
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -286,7 +287,8 @@ cb_status score_args(const cb_score* score, const cb_options* options, float sca
     const double c[5] = {0.9999999403953552, -0.33332324028015137, 0.13310357928276062,
                          -0.052109625190496445, 0.01548669021576643};
     const double u = (double)scale / (double)cap;
-    if (u > 1e-4 && u < 1e4) {  // (beyond, powers of u and of q.k leave fp32)
+    // (beyond these, powers of u and of q.k leave fp32, and the coefficients themselves do)
+    if (u > 1e-4 && u < 1e4 && (double)scale * std::pow(std::fmax(u, 1.0), 8.0) < 1e37) {
       double f = (double)scale * 1.4426950408889634;
       for (int i = 0; i < 5; ++i, f *= u * u) out->near[i] = (float)(c[i] * f);
       out->near_max = (float)(0.6 / u);

@@ -326,7 +326,9 @@ cb_status cb_rope_append_attention(const void* q, const void* k_new, const void*
  * plain causal attention).  The score of query position p (head h) and key j of a sequence is
  *     x = scale q.k,   x = softcap * tanh(x / softcap) where softcap > 0,   x += slopes[h] (j - p),
  * and key j is seen when j <= p or j < visible_lens[s] (never beyond kv_len).  A sliding window
- * (cb_options) goes with the first two, not with visible_lens (CB_ERR_UNSUPPORTED).
+ * (cb_options) goes with the first two, not with visible_lens (CB_ERR_UNSUPPORTED).  The cap is
+ * computed to within 2^-21 softcap, absolute: a cap is to be chosen as a model's, not as a large
+ * number that stands for none.
  */
 typedef struct {
   float softcap;                /* 0: none                                                       */

@@ -317,6 +317,70 @@ def test_chunks_long_context_and_serial(cuda_lib):
     assert torch.equal(out[-64:].view(torch.int16), out2[-64:].view(torch.int16))
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,bs", [(128, 8, 2, 16), (64, 15, 5, 7), (128, 16, 1, 64)])
+def test_only_decodes_only_chunks_and_one_pass_after_the_other(cuda_lib, D, Hq, Hkv, bs):
+    """Batches without work for one of the passes, and both passes in a row (serial): the same bits."""
+    for ql, kv in (([1] * 5, [700, 1, 64, 2000, 33]), ([70, 2, 300], [70, 900, 1500]), ([1, 200, 1, 1], [4000, 900, 80, 7])):
+        b = workloads.build_batch(ql, kv, Hq, Hkv, D, bs, seed=946)
+        for score in (dict(), dict(window=100, softcap=9.0), dict(visible=[9999] * len(ql))):
+            _, out, lse = check_attention(b, **score)
+            _, out2, lse2 = check_attention(b, serial=True, stream=torch.cuda.Stream(), **score)
+            assert torch.equal(out.view(torch.int16), out2.view(torch.int16)) and torch.equal(lse, lse2)
+            check_attention(b, decode_ctas=1, **score)
+
+
+@pytest.mark.parametrize("scale,cap", [(9e11, 1e8), (3e3, 1e-3)])
+def test_scales_and_caps_far_apart(cuda_lib, scale, cap):
+    """Zero queries: every score is 0, whatever the scale and the cap."""
+    b = workloads.build_batch([1, 130, 3], [90, 300, 3], 4, 2, 64, 16, seed=947)
+    b.q[...] = 0
+    b.scale = scale
+    d, out, _ = check_attention(b, softcap=cap)
+    _, plain, _ = check_attention(b)  # (both off by 2^-8 in p and 2^-8 in the result)
+    top = max(np.abs(d.cached(s)[1]).max() for s in range(3))
+    assert (out.float() - plain.float()).abs().max() <= 4 * 2.0 ** -8 * top
+
+
+def test_order_behind_other_work(cuda_lib):
+    """On a stream whose earlier kernels still write what each call reads (the append's rows, the cache, the
+    queries), calls and the results they leave for later ones, each call's own workspace and outputs new."""
+    b = workloads.build_batch([1, 64, 1], [900, 700, 300], 8, 2, 128, 16, seed=948)
+    d = QuantBatch(b)
+    d.upload()
+    big = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    want = [t.clone() for t in step_of(d, d.q, d.k_new, d.v_new)]
+    torch.cuda.synchronize()
+    for stream in (None, torch.cuda.Stream()):
+        d.upload()
+        src = [d.q.clone(), d.k_new.clone(), d.v_new.clone()]
+        late = [torch.full_like(t, float("nan")) for t in src]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            for _ in range(4):
+                big.add_(1)
+            for t, x in zip(late, src):
+                t.copy_(x)
+            got = step_of(d, *late)
+            keep = [t.clone() for t in got]
+            for t in late:
+                t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        assert cb.get_device_error() == cb.CB_OK
+        for x, y in zip(keep, want):
+            assert torch.equal(x.float(), y.float())
+
+
+def step_of(d, q, k, v):
+    """Append, attention, read-back, and the step over the same rows: their outputs."""
+    b = d.b
+    cb.quant_append(None, k, v, *d.pools, *d.where)
+    o1 = cb.quant_attention(q, *d.pools, *d.where, b.scale)
+    cu = i32([0] + list(np.cumsum(b.kv_lens)))
+    k1, v1 = cb.quant_gather(*d.pools, d.where[0], cu, b.block_size, int(sum(b.kv_lens)))
+    o2 = cb.quant_append_attention(q, k, v, *d.pools, *d.where, b.scale)
+    return o1, k1, v1, o2
+
+
 def test_nan_rows(cuda_lib):
     """A key or value row with a value that is not finite is NaN as a whole; it makes the rows NaN that see
     it and no others (and the pools hold NaN rows in every slot that no sequence owns)."""

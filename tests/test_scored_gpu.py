@@ -20,7 +20,7 @@ def slopes_of(h):
     return [2.0 ** (-8.0 * (i + 1) / h) for i in range(h)]
 
 
-def check(b, stream=None, **score):
+def check(b, stream=None, serial=False, decode_ctas=0, **score):
     d = DeviceBatch(b)
     d.append()
     kw = dict(score)
@@ -34,7 +34,8 @@ def check(b, stream=None, **score):
                                                 b.num_tokens)),), 255, dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     cb.scored_attention(d.q, d.k_pages, d.v_pages, d.block_table, d.cu, d.kv_lens, b.block_size, b.scale,
-                        out=out, lse=lse, workspace=ws, stream=stream, **kw)
+                        out=out, lse=lse, workspace=ws, stream=stream, serial=serial,
+                        decode_ctas=decode_ctas, **kw)
     assert cb.get_device_error(stream) == cb.CB_OK
     kp, vp = oracle_append(b)
     o, l, q = f64(out), f64(lse), opa.bf16_bits_to_f64(b.q)
@@ -78,6 +79,30 @@ def test_large_scores_are_capped(cuda_lib):
     check(b, softcap=10.0)
     check(b, softcap=0.5)
     check(b, softcap=1e6)
+
+
+@pytest.mark.parametrize("scale,cap", [(9e11, 1e8), (1e30, 1e30), (1e-30, 1e-3), (1e-6, 1e20), (3e3, 1e-3)])
+def test_scales_and_caps_far_apart(cuda_lib, scale, cap):
+    """Zero queries: every score is 0, whatever the scale and the cap, and a row is the mean of its values."""
+    b = workloads.build_batch([1, 130, 3], [90, 300, 3], 4, 2, 64, 16, seed=625)
+    b.q[...] = 0
+    b.scale = scale
+    _, out, _ = check(b, softcap=cap)
+    vp = oracle_append(b)[1]
+    top = max(np.abs(opa.gather_kv(vp, b.block_table[s], int(b.kv_lens[s]), 16)).max() for s in range(3))
+    _, plain, _ = check(b, softcap=0.0)  # (both off by 2^-8 in p and 2^-8 in the result)
+    assert (out.float() - plain.float()).abs().max() <= 4 * 2.0 ** -8 * top
+
+
+def test_only_decodes_only_chunks_and_one_pass_after_the_other(cuda_lib):
+    """Batches without work for one of the passes, and both passes in a row (serial): the same bits."""
+    for ql, kv in (([1] * 5, [700, 1, 64, 2000, 33]), ([70, 2, 300], [70, 900, 1500]), ([1, 200, 1, 1], [4000, 900, 80, 7])):
+        b = workloads.build_batch(ql, kv, 8, 2, 128, 16, seed=626)
+        for score in (dict(softcap=3.0), dict(slopes=slopes_of(8), window=100), dict(visible_lens=[9999] * len(ql))):
+            _, out, lse = check(b, **score)
+            _, out2, lse2 = check(b, serial=True, stream=torch.cuda.Stream(), **score)
+            assert torch.equal(out.view(torch.int16), out2.view(torch.int16)) and torch.equal(lse, lse2)
+            check(b, decode_ctas=1, **score)
 
 
 def test_positive_and_zero_slopes(cuda_lib):
