@@ -16,7 +16,7 @@ namespace cb {
 // Of one thread of each of the `grid` decode CTAs: the ranges (of `total` < grid) that it takes, first to
 // end - 1; most often one or none.  The CTA that arrives last also takes those that are left, if any: the
 // chosen SMs may have had too few CTAs, for instance where another launch holds some.  (One atomic per
-// CTA, for the claim and the arrival: with one for each the step took 4 us longer.)
+// CTA, for the claim and the arrival.)
 struct RangeClaim {
   int first, end;
 };

@@ -2,7 +2,8 @@
 // pass (cb_prefill.cuh, cb_quant_prefill.cuh) in one launch.  Its first a.decode_grid CTAs take the decode
 // ranges, and every CTA then takes chunk items while there are any: an SM that the planner leaves to the
 // chunk pass begins with it at once, and one whose range is done goes on without another CTA's launch
-// (4 us of a step of 60 beside CTAs that only leave their SM).
+// (beside CTAs that only leave their SM: 64 decodes on up to 4000 keys 63 us, so 62; those and a chunk
+// 148 us, so 144).
 #pragma once
 
 #include "cb_quant_decode.cuh"
