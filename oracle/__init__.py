@@ -29,6 +29,9 @@ Pins (what each function is checked against, in tests/test_oracle_*.py):
     freed), the 10,000-token / 1,500-token chunking example, the FIFO and PrefillFirst orders
     of the transformers "Scheduler" section, and continuous batching = list scheduling on B
     slots, fewer steps than static batching (tests/test_oracle_scheduler.py).
+  * ``quant``: all 256 codes and roundings (ties too) against torch's conversion, error bounds of
+    rows, changed scores in closed form and, without changes, the plain attention
+    (tests/test_oracle_quant.py).
   * ``blocks``: element-wise brute force on tiny pools (tests/test_oracle_blocks.py).
 No function here is "parity unpinned".
 """
