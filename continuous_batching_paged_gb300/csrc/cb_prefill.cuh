@@ -110,15 +110,10 @@ static_assert(sizeof(PfItemSeen) <= 128, "a decoded item fits its shared-memory 
 // The chunk pass over the quantised cache: warps 12-15 make the K and V tiles (quant_convert), warp 0
 // finds their rows.
 constexpr int kQuantPrefillThreads = 512;
-// Registers of the issuing, softmax and converting warps, as timed on 8 chunks of 512 tokens (D = 128, an
-// earlier state of the pass): 80/168/96 198 us, 64/176/96 201, 56/176/104 210, 72/176/88 222, 88/168/88 222.
-// (The compiler spills some 130 bytes there.)
-template <int D>
-struct QuantRegs {
-  static constexpr int kIssue = D == 128 ? 80 : 64, kSoftmax = D == 128 ? 168 : 176,
-                       kConvert = 96;
-  static_assert(kIssue + 2 * kSoftmax + kConvert <= 4 * 128, "register split exceeds the launch");
-};
+// Registers of the issuing, softmax and converting warps: what each role needs without spills.
+constexpr int kRegsQuantIssue = 96, kRegsQuantSoftmax = 176, kRegsQuantConvert = 64;
+static_assert(kRegsQuantIssue + 2 * kRegsQuantSoftmax + kRegsQuantConvert <= 4 * 128,
+              "register split exceeds the launch");
 constexpr int kRowSlots = 4;  // K/V tiles whose rows are known ahead
 struct RowSlot {
   // per key: its row in the pool (token x Hkv + KV head; kNoRow: none), and the two factors that make
@@ -132,10 +127,15 @@ constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr int kRowFirst = 1, kRowLast = 2, kRowEnd = 4, kRowMore = 8;
 template <int D>
 struct QuantPrefillSmem {
-  static constexpr int kRows = (PrefillSmem<D>::kTotal - 1024 + 15) / 16 * 16;
+  static constexpr int kRowsPerThread = D / 16;  // of a tile (quant_convert)
+  // (the block-table entries of the other cache are not staged here, and the output by 16 rows a warp)
+  static constexpr int kCodes = PrefillSmem<D>::kEntries;  // a tile's codes, in pieces of the threads
+  static constexpr int kOut = kCodes + kRowsPerThread * 128 * 16;
+  static constexpr int kOutWarp = PrefillSmem<D>::kStageOutWarp / 2;
+  static constexpr int kRows = kOut + 8 * kOutWarp;
   static constexpr int kBar = kRows + kRowSlots * (int)sizeof(RowSlot);  // full, empty per slot
   static constexpr int kTotal = kBar + 2 * kRowSlots * 8 + 1024;
-  static_assert(sizeof(RowSlot) % 8 == 0, "alignment of shared-memory regions");
+  static_assert(kRows % 16 == 0 && sizeof(RowSlot) % 8 == 0, "alignment of shared-memory regions");
 };
 
 // Query heads (pairs) per unit: items are unit-major with the head (pair) fastest, so the
@@ -275,7 +275,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
   // Each role runs inside the branch that set its register count (no join in between, so the
   // compiler allocates every role's code under that role's own limit).
   if (warp < 4) {
-    regs_dec<kQuant ? QuantRegs<D>::kIssue : kRegsIssue>();
+    regs_dec<kQuant ? kRegsQuantIssue : kRegsIssue>();
     if (kQuant && warp == 0) {
       if constexpr (kQuant) quant_rows<D, kMod>(a, qa, qmap, smem, sbase, lane);
     } else if (warp == 0) {
@@ -538,11 +538,11 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
     }
   } else if (kQuant && warp >= 12) {
     if constexpr (kQuant) {
-      regs_dec<QuantRegs<D>::kConvert>();
+      regs_dec<kRegsQuantConvert>();
       quant_convert<D>(a, qa, smem, sbase);
     }
   } else {
-    regs_inc<kQuant ? QuantRegs<D>::kSoftmax : kRegsSoftmax>();
+    regs_inc<kQuant ? kRegsQuantSoftmax : kRegsSoftmax>();
     // ===================================================================== softmax groups
     const int t = (warp - 4) >> 2;                // 0: tile A, 1: tile B
     const int quad = warp & 3;                    // TMEM lane quadrant this warp may access
@@ -557,15 +557,19 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
       if (!mbar_wait(bar(SM::bItemFull + slot), (k >> 1) & 1)) { report(a.err, kErrTimeout); break; }
       const Item it = *item_slot(slot);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
+      // (Over the quantised cache, with fewer registers, the epilogue reads the slot again.)
+      if (!kQuant && lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
       if (it.item < 0) break;
       const uint32_t g_item = g;
       g += it.nt_all - it.j0 + 1;  // ring stages of the item
-      if (t == 1 && !it.hasB) continue;
+      if (t == 1 && !it.hasB) {
+        if (kQuant && lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
+        continue;
+      }
       const int nt = t ? it.nt[1] : it.nt[0];
-      const int tok = t ? it.tok[1] : it.tok[0];
-      const int rows = t ? it.rows[1] : it.rows[0];
-      const int head = t ? it.head[1] : it.head[0];
+      int tok = t ? it.tok[1] : it.tok[0];
+      int rows = t ? it.rows[1] : it.rows[0];
+      int head = t ? it.head[1] : it.head[0];
       const int diag0 = it.ctx + (t ? it.qoff[1] : it.qoff[0]);  // row 0's last key
       int limit = diag0 + r;                                           // row r's last key
       int full = diag0;  // every row's last key is this one or a later one
@@ -727,13 +731,24 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
       if (!mbar_wait(bar(SM::bOFinal + t), kx & 1)) { report(a.err, kErrTimeout); break; }
       __syncwarp();
       tc_fence_after();
+      if (kQuant) {
+        const Item* again = item_slot(slot);
+        tok = again->tok[t];
+        rows = again->rows[t];
+        head = again->head[t];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(SM::bItemEmpty + slot));
+      }
       const float inv = 1.f / l_run;
       const bool store = r < rows;
       // Each 32-column slice of the warp's 32 rows goes through shared memory: lane = row on
       // the way in (TMEM lane), four lanes per row on the way out, so that every store
       // instruction writes 64 contiguous bytes of 8 rows.  The 16-byte chunks of a row are
       // XOR-swizzled by the row pair so that neither side has bank conflicts.
-      const uint32_t stg = sbase + SM::kStageOut + (warp - 4) * SM::kStageOutWarp;
+      // (Over the quantised cache 16 rows at a time, whose staging leaves room for codes.)
+      constexpr int kParts = kQuant ? 2 : 1, kPartRows = 32 / kParts;
+      const uint32_t stg = kQuant ? sbase + QuantPrefillSmem<D>::kOut + (warp - 4) * QuantPrefillSmem<D>::kOutWarp
+                                  : sbase + SM::kStageOut + (warp - 4) * SM::kStageOutWarp;
       const int orow_base = quad * 32;
 #pragma unroll
       for (int ch = 0; ch < D / 32; ++ch) {
@@ -741,29 +756,34 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         tmem_ld32(t_lane + o_col + ch * 32, ov);
         tc_wait_ld();
 #pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          uint32_t pk[4];
+        for (int part = 0; part < kParts; ++part) {
+          if (kParts == 1 || lane / kPartRows == part) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            pk[i] = pack_bf16x2(__uint_as_float(ov[8 * c4 + 2 * i]) * inv,
-                                __uint_as_float(ov[8 * c4 + 2 * i + 1]) * inv);
-          const uint32_t addr = stg + lane * 64 + ((c4 ^ ((lane >> 1) & 3)) << 4);
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(pk[0]), "r"(pk[1]),
-                       "r"(pk[2]), "r"(pk[3]) : "memory");
-        }
-        __syncwarp();
+            for (int c4 = 0; c4 < 4; ++c4) {
+              uint32_t pk[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = (lane >> 2) + 8 * i, c4 = lane & 3;
-          uint4 v;
-          const uint32_t addr = stg + row * 64 + ((c4 ^ ((row >> 1) & 3)) << 4);
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-          if (orow_base + row < rows)
-            *reinterpret_cast<uint4*>(outg + ((size_t)(tok + orow_base + row) * a.Hq + head) * D +
-                                      ch * 32 + c4 * 8) = v;
+              for (int i = 0; i < 4; ++i)
+                pk[i] = pack_bf16x2(__uint_as_float(ov[8 * c4 + 2 * i]) * inv,
+                                    __uint_as_float(ov[8 * c4 + 2 * i + 1]) * inv);
+              const uint32_t addr = stg + (lane & (kPartRows - 1)) * 64 + ((c4 ^ ((lane >> 1) & 3)) << 4);
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(pk[0]), "r"(pk[1]),
+                           "r"(pk[2]), "r"(pk[3]) : "memory");
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < kPartRows / 8; ++i) {
+            const int row = (lane >> 2) + 8 * i, c4 = lane & 3;
+            uint4 v;
+            const uint32_t addr = stg + row * 64 + ((c4 ^ ((row >> 1) & 3)) << 4);
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+            const int orow = orow_base + part * kPartRows + row;
+            if (orow < rows)
+              *reinterpret_cast<uint4*>(outg + ((size_t)(tok + orow) * a.Hq + head) * D + ch * 32 + c4 * 8) = v;
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       if (store && a.lse != nullptr)
         a.lse[(size_t)(tok + r) * a.Hq + head] = (m_run + __log2f(l_run)) * 0.6931471805599453f;

@@ -41,6 +41,13 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t
       : "r"(x));
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
 // The biased exponent of a row's scale, from the largest finite |x| of the row.
 __device__ __forceinline__ int quant_exponent(float top) {
   const uint32_t b = __float_as_uint(top);  // 448 = 1.75 * 2^8

@@ -187,17 +187,19 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t f) {
 
 // Warps 12-15: K and V tiles of the ring's stages.  Stage m of an item holds K tile m and V tile m - 1,
 // as in cb_prefill.cuh, so an item's order is K(0) | K(1) V(0) | ... | K(n-1) V(n-2) | V(n-1), stages
-// between the bars.  A thread makes the same 16 columns of D / 16 rows of every tile; the codes of the
-// next tile in that order are loaded while this one's are converted, each into the register that just
-// became free.  One copy of the conversion, in a loop over tiles: written out for each place in the order
-// the four warps' code did not stay in the instruction cache beside the softmax warps' (8 chunks of 512
-// tokens: 804 us).
+// between the bars.  A thread makes the same 16 columns of D / 16 rows of every tile.  Its codes wait in
+// shared memory (pieces of 16 bytes that only this thread copies and reads); the next tile's in that order
+// are copied behind the conversion of this one's.  In registers they would be taken from the softmax
+// warps: those spilled, and as the pass leaves L1 some 20 KB, through which the codes pass, a part of the
+// spilled values came from L2, in the chain of every K/V step (4 chunks of 2048 tokens on up to 16384 keys:
+// 1262 us, so FIGURE).  One copy of the conversion, in a loop over tiles: written out for each place in the
+// order the four warps' code did not stay in the instruction cache beside the softmax warps'.
 template <int D>
 __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs& qa, uint8_t* smem,
                                               uint32_t sbase) {
   using SM = PrefillSmem<D>;
   using QM = QuantPrefillSmem<D>;
-  constexpr int NS = SM::kStages, NR = D / 16;  // rows per thread
+  constexpr int NS = SM::kStages, NR = QM::kRowsPerThread;
   auto bar = [&](int i) -> uint32_t { return sbase + SM::kBar + 8 * i; };
   const uint32_t row_full = sbase + QM::kBar, row_empty = row_full + 8 * kRowSlots;
   const uint32_t rings = sbase + QM::kRows;
@@ -210,6 +212,7 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
   static_assert(kStep % 8 == 0, "rows of a thread share their swizzle");
   const uint32_t at0 = sw128((c >> 2) * SM::kKVHalf, r0, 2 * (c & 3));
   const uint32_t at1 = sw128((c >> 2) * SM::kKVHalf, r0, 2 * (c & 3) + 1);
+  const uint32_t codes = sbase + QM::kCodes + t * 16;  // this thread's pieces of a V tile, 2 KB apart
   bool ok = true;
   auto wait = [&](uint32_t b, uint32_t parity) {
     if (ok && !mbar_wait(b, parity)) {
@@ -224,32 +227,36 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
     asm volatile("ld.shared.s32 %0, [%1];" : "=r"(f) : "r"(slot(i) + (uint32_t)offsetof(RowSlot, flags)));
     return f;
   };
-  // (Predicated, not branched around: a branch per load, and its reconvergence, took as long as the
-  // conversion.)
-  uint4 raw[NR];
-  auto load = [&](const uint8_t* pages, uint32_t row, int i) {
-    const uint8_t* src = pages + (size_t)row * D + 16 * c;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %5, %6;\n\t"
-        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-        : "=&r"(raw[i].x), "=&r"(raw[i].y), "=&r"(raw[i].z), "=&r"(raw[i].w)
-        : "l"(src), "r"(row), "n"(kNoRow));
-  };
   // A tile's rows (or factors, at = 4) of this thread.
   auto rows_of = [&](uint32_t i, uint32_t at, uint32_t (&r)[NR]) {
 #pragma unroll
     for (int k = 0; k < NR; ++k)
       asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[k]) : "r"(slot(i) + 8 * (r0 + kStep * k) + at));
   };
-
+  // One row's piece to shared memory (zeros where there is no row).
+  auto copy = [&](const uint8_t* pages, uint32_t row, int k) {
+    const bool none = row == kNoRow;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(codes + 2048 * k),
+                 "l"(pages + (none ? 0 : (size_t)row * D + 16 * c)), "r"(none ? 0 : 16)
+                 : "memory");
+  };
+  auto commit = [&]() { asm volatile("cp.async.commit_group;" ::: "memory"); };
+  auto convert = [&](const uint4& x, uint32_t f, uint32_t dst, int k) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) codes_to_bf16x4(w[i], f, y[2 * i], y[2 * i + 1]);
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + at0 + kStep * 128 * k), "r"(y[0]),
+                 "r"(y[1]), "r"(y[2]), "r"(y[3]));
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + at1 + kStep * 128 * k), "r"(y[4]),
+                 "r"(y[5]), "r"(y[6]), "r"(y[7]));
+  };
   uint32_t g = 0;              // stages so far
   uint32_t n = 0;              // the tile at hand, of all tiles so far
   bool v = false;              // its values
   int flags = 0, flags1 = 0;   // of tile n; v: of tile n + 1, where that is the same item's
   uint32_t kst = 0;
-  bool loaded = false;         // raw holds its codes
+  bool loaded = false;         // its codes are on their way
   while (true) {
     if (!loaded) {             // an item begins
       ready(n);
@@ -259,7 +266,10 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
       uint32_t row[NR];
       rows_of(n, 0, row);
 #pragma unroll
-      for (int i = 0; i < NR; ++i) load(qa.k_pages, row[i], i);
+      for (int k = 0; k < NR; ++k) {
+        copy(qa.k_pages, row[k], k);
+        if (k % 4 == 3) commit();
+      }
     }
     // The next tile in the order.
     uint32_t nn;
@@ -287,29 +297,26 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
     }
     if (!ok) break;
     const uint32_t dst = kst + (v ? SM::kKVTile : 0);
-    // (all shared-memory loads ahead of the stores, which the compiler keeps in order with them)
+    // (all loads of rows and factors ahead of the stores, which the compiler keeps in order with them)
     uint32_t fs[NR], row[NR];
     rows_of(n, 4, fs);
     rows_of(nn, 0, row);
-    if (!loaded) {
-#pragma unroll
-      for (int i = 0; i < NR; ++i) row[i] = kNoRow;
-    }
     const uint8_t* next = nv ? qa.v_pages : qa.k_pages;
     const uint32_t pick = v ? 0x3232u : 0x1010u;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const uint32_t f = __byte_perm(fs[i], 0, pick);
-      const uint4 x = raw[i];
-      load(next, row[i], i);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t y[8];
+    for (int k0 = 0; k0 < NR; k0 += 4) {
+      // (this tile's later pieces may still be on their way)
+      asm volatile("cp.async.wait_group %0;" ::"n"(NR / 4 - 1) : "memory");
+      uint4 x[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) codes_to_bf16x4(w[k], f, y[2 * k], y[2 * k + 1]);
-      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + at0 + kStep * 128 * i), "r"(y[0]),
-                   "r"(y[1]), "r"(y[2]), "r"(y[3]));
-      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + at1 + kStep * 128 * i), "r"(y[4]),
-                   "r"(y[5]), "r"(y[6]), "r"(y[7]));
+      for (int k = 0; k < 4; ++k) x[k] = lds128(codes + 2048 * (k0 + k));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) convert(x[k], __byte_perm(fs[k0 + k], 0, pick), dst, k0 + k);
+      if (loaded) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) copy(next, row[k0 + k], k0 + k);
+      }
+      commit();
     }
     if (flags & kRowMore) {  // the second factors: over what this thread has just written
 #pragma unroll 1
@@ -343,6 +350,7 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
     n = nn;
     v = nv;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 }  // namespace cb
