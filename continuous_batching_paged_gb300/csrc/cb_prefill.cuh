@@ -116,13 +116,12 @@ static_assert(kRegsQuantIssue + 2 * kRegsQuantSoftmax + kRegsQuantConvert <= 4 *
               "register split exceeds the launch");
 constexpr int kRowSlots = 4;  // K/V tiles whose rows are known ahead
 struct RowSlot {
-  // per key: its row in the pool (token x Hkv + KV head; kNoRow: none), and the two factors that make
+  // per key: its row in the pool (token x Hkv + KV head), and the two factors that make
   // its codes values (bf16, the key's in the low half; quant_convert)
   uint2 row[kChunkKeys];
   uint32_t more[kChunkKeys];  // further factors, with kRowMore
   int flags, pad;
 };
-constexpr uint32_t kNoRow = 0xffffffffu;
 // an item's first and last tile; no more tiles; some scale takes two factors
 constexpr int kRowFirst = 1, kRowLast = 2, kRowEnd = 4, kRowMore = 8;
 template <int D>

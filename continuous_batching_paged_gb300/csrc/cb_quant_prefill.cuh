@@ -6,12 +6,9 @@
 // shared memory: c * 2^e is exact in bf16, so nothing is lost and no scale is left to the products.
 // (The tensor cores' own 8-bit products would take the codes as they are, but need the queries and the
 // probabilities in 8 bits too, which costs either accuracy or a second product and more work in the
-// softmax warps, which bound the pass.)  What bounds this part is the latency of the codes' loads -- a
-// thread has one tile's 16 x D / 16 of them in flight, its registers hold no more -- and four instructions
-// per two values on the converting warps, beside the softmax warps of the same schedulers: 8 chunks of 512
-// tokens on up to 4096 keys (32 query, 8 KV heads of 128) take 166 us, 690 TFLOP/s, without the loads 141,
-// on a bf16 cache 146 to 150.  Codes copied by TMA into a ring of their own, which costs the tiles' ring a
-// stage and another pass over shared memory: 174 us.
+// softmax warps, which bound the pass.)  What bounds the pass is this part's
+// instructions, four per two values on the converting warps: 8 chunks of 512 tokens on up to 4096 keys (32
+// query, 8 KV heads of 128) take 156 us, 734 TFLOP/s, on a bf16 cache 150.
 #pragma once
 
 #include <cstddef>
@@ -141,7 +138,8 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
         const int ek = (int)(sc_j[i] & 255) - kQuantBias, ev = (int)(sc_j[i] >> 8) - kQuantBias;
         const uint32_t fk = ek == kQuantNan - kQuantBias ? 0x7fffu : (uint32_t)(247 + min(ek, 7)) << 7;
         const uint32_t fv = ev == kQuantNan - kQuantBias ? 0x7fffu : (uint32_t)(247 + min(ev, 7)) << 7;
-        rs.row[32 * i + lane] = make_uint2(tok_j[i] < 0 ? kNoRow : (uint32_t)tok_j[i] * a.Hkv + it.kvh,
+        // (where there is no key: the pool's first row, times 0)
+        rs.row[32 * i + lane] = make_uint2(tok_j[i] < 0 ? 0u : (uint32_t)tok_j[i] * a.Hkv + it.kvh,
                                            tok_j[i] < 0 ? 0u : fk | fv << 16);
         rs.more[32 * i + lane] = (uint32_t)(127 + max(ek - 7, 0)) << 7 | (uint32_t)(127 + max(ev - 7, 0)) << 23;
         more = more || (tok_j[i] >= 0 && max(ek, ev) > 7);
@@ -188,18 +186,22 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t f) {
 // Warps 12-15: K and V tiles of the ring's stages.  Stage m of an item holds K tile m and V tile m - 1,
 // as in cb_prefill.cuh, so an item's order is K(0) | K(1) V(0) | ... | K(n-1) V(n-2) | V(n-1), stages
 // between the bars.  A thread makes the same 16 columns of D / 16 rows of every tile.  Its codes wait in
-// shared memory (pieces of 16 bytes that only this thread copies and reads); the next tile's in that order
-// are copied behind the conversion of this one's.  In registers they would be taken from the softmax
-// warps: those spilled, and as the pass leaves L1 some 20 KB, through which the codes pass, a part of the
-// spilled values came from L2, in the chain of every K/V step (4 chunks of 2048 tokens on up to 16384 keys:
-// 1262 us, so FIGURE).  One copy of the conversion, in a loop over tiles: written out for each place in the
-// order the four warps' code did not stay in the instruction cache beside the softmax warps'.
+// shared memory, in pieces of 16 bytes that only this thread copies and reads; the next tile's in that
+// order are copied behind the conversion of this one's.
+//   What one warp per scheduler executes for a stage is what bounds the pass (its copies are there in
+// time), beside softmax warps whose code displaces its own from the nearest instruction cache: so few
+// instructions in one small loop count for more than few loads or dependences.  4 chunks of 2048 tokens on
+// up to 16384 keys (32 query, 8 KV heads of 128) took 1262 us with the next tile's codes in registers,
+// loaded between the conversions, all unrolled; 1072 with the codes here; 1024 with a loop over four rows;
+// 967 with the order's decisions once a stage and rows without a predicate.  (Two rows at a time 993, eight
+// 1020, one 1326.  On a bf16 cache 855.)
 template <int D>
 __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs& qa, uint8_t* smem,
                                               uint32_t sbase) {
   using SM = PrefillSmem<D>;
   using QM = QuantPrefillSmem<D>;
   constexpr int NS = SM::kStages, NR = QM::kRowsPerThread;
+  constexpr int kGroup = 4;  // rows at a time
   auto bar = [&](int i) -> uint32_t { return sbase + SM::kBar + 8 * i; };
   const uint32_t row_full = sbase + QM::kBar, row_empty = row_full + 8 * kRowSlots;
   const uint32_t rings = sbase + QM::kRows;
@@ -212,7 +214,7 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
   static_assert(kStep % 8 == 0, "rows of a thread share their swizzle");
   const uint32_t at0 = sw128((c >> 2) * SM::kKVHalf, r0, 2 * (c & 3));
   const uint32_t at1 = sw128((c >> 2) * SM::kKVHalf, r0, 2 * (c & 3) + 1);
-  const uint32_t codes = sbase + QM::kCodes + t * 16;  // this thread's pieces of a V tile, 2 KB apart
+  const uint32_t codes = sbase + QM::kCodes + t * 16;  // this thread's pieces of a tile, 2 KB apart
   bool ok = true;
   auto wait = [&](uint32_t b, uint32_t parity) {
     if (ok && !mbar_wait(b, parity)) {
@@ -227,18 +229,17 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
     asm volatile("ld.shared.s32 %0, [%1];" : "=r"(f) : "r"(slot(i) + (uint32_t)offsetof(RowSlot, flags)));
     return f;
   };
-  // A tile's rows (or factors, at = 4) of this thread.
-  auto rows_of = [&](uint32_t i, uint32_t at, uint32_t (&r)[NR]) {
+  const uint8_t* kp = qa.k_pages + 16 * c;
+  const uint8_t* vp = qa.v_pages + 16 * c;
+  // This thread's rows k0 .. k0 + kGroup - 1 of a tile, its first row's address in the slot given.
+  auto copy = [&](const uint8_t* pages, uint32_t at, int k0) {
 #pragma unroll
-    for (int k = 0; k < NR; ++k)
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[k]) : "r"(slot(i) + 8 * (r0 + kStep * k) + at));
-  };
-  // One row's piece to shared memory (zeros where there is no row).
-  auto copy = [&](const uint8_t* pages, uint32_t row, int k) {
-    const bool none = row == kNoRow;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(codes + 2048 * k),
-                 "l"(pages + (none ? 0 : (size_t)row * D + 16 * c)), "r"(none ? 0 : 16)
-                 : "memory");
+    for (int k = 0; k < kGroup; ++k) {
+      uint32_t row;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(row) : "r"(at + 8 * kStep * (k0 + k)));
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(codes + 2048 * (k0 + k)),
+                   "l"(pages + (size_t)row * D) : "memory");
+    }
   };
   auto commit = [&]() { asm volatile("cp.async.commit_group;" ::: "memory"); };
   auto convert = [&](const uint4& x, uint32_t f, uint32_t dst, int k) {
@@ -251,104 +252,104 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + at1 + kStep * 128 * k), "r"(y[4]),
                  "r"(y[5]), "r"(y[6]), "r"(y[7]));
   };
-  uint32_t g = 0;              // stages so far
-  uint32_t n = 0;              // the tile at hand, of all tiles so far
-  bool v = false;              // its values
-  int flags = 0, flags1 = 0;   // of tile n; v: of tile n + 1, where that is the same item's
-  uint32_t kst = 0;
-  bool loaded = false;         // its codes are on their way
-  while (true) {
-    if (!loaded) {             // an item begins
+  uint32_t n = 0;        // the tile of this stage's keys, of all tiles so far; its values are tile n - 1
+  bool has_v = false;    // not an item's first stage
+  int flags = 0, before = 0;  // of tiles n and n - 1
+  bool loaded = false;   // the codes of tile n's keys are on their way although its item has not begun
+  for (uint32_t g = 0;; ++g) {
+    uint32_t at = slot(n) + 8 * r0;  // this thread's first row in tile n's slot
+    if (!has_v) {          // an item begins
       ready(n);
       if (!ok) break;
       flags = flags_of(n);
       if (flags & kRowEnd) break;
-      uint32_t row[NR];
-      rows_of(n, 0, row);
-#pragma unroll
-      for (int k = 0; k < NR; ++k) {
-        copy(qa.k_pages, row[k], k);
-        if (k % 4 == 3) commit();
-      }
-    }
-    // The next tile in the order.
-    uint32_t nn;
-    bool nv;
-    loaded = true;
-    if (!v) {
-      const bool first = flags & kRowFirst, last = flags & kRowLast;
-      nv = !first || last;
-      nn = first ? (last ? n : n + 1) : n - 1;
-    } else if (!(flags & kRowLast)) {
-      nv = flags1 & kRowLast;
-      nn = nv ? n + 1 : n + 2;
-    } else {  // the next item's first keys, where its rows are known already
-      nv = false;
-      nn = n + 1;
-      loaded = __all_sync(0xffffffffu, mbar_test(row_full + 8 * (nn % kRowSlots), (nn / kRowSlots) & 1)) &&
-               !(flags_of(nn) & kRowEnd);
-    }
-    if (!nv && loaded) ready(nn);
-    const int flags_n = loaded ? (nn == n ? flags : flags_of(nn)) : 0;
-    // A stage begins with keys, or with an item's last values.
-    if (!v || (flags & kRowLast)) {
-      wait(bar(SM::bEmpty + g % NS), ((g / NS) & 1) ^ 1);
-      kst = sbase + SM::kStage0 + (g % NS) * SM::kStageBytes;
-    }
-    if (!ok) break;
-    const uint32_t dst = kst + (v ? SM::kKVTile : 0);
-    // (all loads of rows and factors ahead of the stores, which the compiler keeps in order with them)
-    uint32_t fs[NR], row[NR];
-    rows_of(n, 4, fs);
-    rows_of(nn, 0, row);
-    const uint8_t* next = nv ? qa.v_pages : qa.k_pages;
-    const uint32_t pick = v ? 0x3232u : 0x1010u;
-#pragma unroll
-    for (int k0 = 0; k0 < NR; k0 += 4) {
-      // (this tile's later pieces may still be on their way)
-      asm volatile("cp.async.wait_group %0;" ::"n"(NR / 4 - 1) : "memory");
-      uint4 x[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = lds128(codes + 2048 * (k0 + k));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) convert(x[k], __byte_perm(fs[k0 + k], 0, pick), dst, k0 + k);
-      if (loaded) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) copy(next, row[k0 + k], k0 + k);
-      }
-      commit();
-    }
-    if (flags & kRowMore) {  // the second factors: over what this thread has just written
+      if (!loaded) {
 #pragma unroll 1
-      for (int i = 0; i < 2 * NR; ++i) {
-        const uint32_t at = dst + (i & 1 ? at1 : at0) + kStep * 128 * (i >> 1);
-        uint32_t m;
-        asm volatile("ld.shared.u32 %0, [%1];"
-                     : "=r"(m)
-                     : "r"(slot(n) + (uint32_t)offsetof(RowSlot, more) + 4 * (r0 + kStep * (i >> 1))));
-        m = __byte_perm(m, 0, pick);
-        uint32_t y[4];
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]) : "r"(at));
+        for (int k0 = 0; k0 < NR; k0 += kGroup) {
+          copy(kp, at, k0);
+          commit();
+        }
+      }
+    }
+    const bool has_k = !has_v || !(before & kRowLast);
+    // The tile that the next stage begins with: keys, an item's last values, or the next item's first
+    // keys where its rows are known already.
+    const bool nv = has_k && (flags & kRowLast);
+    uint32_t nn = n;
+    loaded = true;
+    if (has_k && !nv)
+      ready(++nn);
+    else if (!has_k)
+      loaded = __all_sync(0xffffffffu, mbar_test(row_full + 8 * (n % kRowSlots), (n / kRowSlots) & 1)) &&
+               !(flags_of(n) & kRowEnd);
+    const int flags_n = flags_of(nn);
+    wait(bar(SM::bEmpty + g % NS), ((g / NS) & 1) ^ 1);
+    if (!ok) break;
+    const uint32_t at_n = slot(nn) + 8 * r0, at_v = slot(n - 1) + 8 * r0;
+    uint32_t dst = sbase + SM::kStage0 + (g % NS) * SM::kStageBytes, pick = 0x1010u;
+    if (!has_k) {
+      dst += SM::kKVTile;
+      pick = 0x3232u;
+      at = at_v;
+    }
+    // keys, then values; copies of what comes behind each
+#pragma unroll 1
+    for (int tiles = has_k && has_v ? 2 : 1; tiles > 0; --tiles) {
+      const bool more = (has_k && tiles == (has_v ? 2 : 1) ? flags : before) & kRowMore;
+      const bool values_next = tiles == 2 || nv;
+      const uint8_t* next = values_next ? vp : kp;
+      const uint32_t at_next = tiles == 2 ? at_v : at_n;
+#pragma unroll 1
+      for (int k0 = 0; k0 < NR; k0 += kGroup) {
+        // (this tile's later pieces may still be on their way)
+        asm volatile("cp.async.wait_group %0;" ::"n"(NR / kGroup - 1) : "memory");
+        uint4 x[kGroup];
+        uint32_t fs[kGroup];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = mul_bf16x2(y[k], m);
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
-                     "r"(y[3]));
+        for (int k = 0; k < kGroup; ++k) {
+          x[k] = lds128(codes + 2048 * (k0 + k));
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(fs[k]) : "r"(at + 8 * kStep * (k0 + k) + 4));
+        }
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k) convert(x[k], __byte_perm(fs[k], 0, pick), dst, k0 + k);
+        if (loaded || tiles == 2) copy(next, at_next, k0);
+        commit();
       }
-    }
-    if (v || (flags & kRowFirst)) {  // the stage is complete
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(SM::bFull + g % NS));
-        if (v) mbar_arrive(row_empty + 8 * (n % kRowSlots));
+      if (more) {  // the second factors: over what this thread has just written
+#pragma unroll 1
+        for (int i = 0; i < 2 * NR; ++i) {
+          const uint32_t to = dst + (i & 1 ? at1 : at0) + kStep * 128 * (i >> 1);
+          uint32_t m;
+          asm volatile("ld.shared.u32 %0, [%1];"
+                       : "=r"(m)
+                       : "r"(at - 8 * r0 + (uint32_t)offsetof(RowSlot, more) + 4 * (r0 + kStep * (i >> 1))));
+          m = __byte_perm(m, 0, pick);
+          uint32_t y[4];
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]) : "r"(to));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = mul_bf16x2(y[k], m);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+                       "r"(y[3]));
+        }
       }
-      ++g;
+      dst += SM::kKVTile;
+      pick = 0x3232u;
+      at = at_v;
     }
-    if (!v && nv && nn + 1 == n) flags1 = flags;  // (the values before these keys)
-    flags = flags_n;
-    n = nn;
-    v = nv;
+    // the stage is complete
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(bar(SM::bFull + g % NS));
+      if (has_v) mbar_arrive(row_empty + 8 * ((n - 1) % kRowSlots));
+    }
+    has_v = has_k;
+    if (has_k) {
+      before = flags;
+      flags = flags_n;
+      ++n;
+    }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
