@@ -6,9 +6,9 @@
 // shared memory: c * 2^e is exact in bf16, so nothing is lost and no scale is left to the products.
 // (The tensor cores' own 8-bit products would take the codes as they are, but need the queries and the
 // probabilities in 8 bits too, which costs either accuracy or a second product and more work in the
-// softmax warps, which bound the pass.)  What bounds the pass is this part's
-// instructions, four per two values on the converting warps: 8 chunks of 512 tokens on up to 4096 keys (32
-// query, 8 KV heads of 128) take 156 us, 734 TFLOP/s, on a bf16 cache 150.
+// softmax warps.)  What bounds the pass is this part's instructions, four per two values on the
+// converting warps: 8 chunks of 512 tokens on up to 4096 keys (32 query, 8 KV heads of 128) take 153 us,
+// 749 TFLOP/s, on a bf16 cache 150; on up to 8192 keys 231 and 218.
 #pragma once
 
 #include <cstddef>
@@ -193,8 +193,8 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t f) {
 // instructions in one small loop count for more than few loads or dependences.  4 chunks of 2048 tokens on
 // up to 16384 keys (32 query, 8 KV heads of 128) took 1262 us with the next tile's codes in registers,
 // loaded between the conversions, all unrolled; 1072 with the codes here; 1024 with a loop over four rows;
-// 967 with the order's decisions once a stage and rows without a predicate.  (Two rows at a time 993, eight
-// 1020, one 1326.  On a bf16 cache 855.)
+// 967 with the order's decisions once a stage and rows without a predicate; 956 with the next rows read
+// beside the codes.  (Two rows at a time 993, eight 1020, one 1326.  On a bf16 cache 855.)
 template <int D>
 __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs& qa, uint8_t* smem,
                                               uint32_t sbase) {
@@ -231,15 +231,15 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
   };
   const uint8_t* kp = qa.k_pages + 16 * c;
   const uint8_t* vp = qa.v_pages + 16 * c;
-  // This thread's rows k0 .. k0 + kGroup - 1 of a tile, its first row's address in the slot given.
-  auto copy = [&](const uint8_t* pages, uint32_t at, int k0) {
-#pragma unroll
-    for (int k = 0; k < kGroup; ++k) {
-      uint32_t row;
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(row) : "r"(at + 8 * kStep * (k0 + k)));
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(codes + 2048 * (k0 + k)),
-                   "l"(pages + (size_t)row * D) : "memory");
-    }
+  // This thread's piece of a row to shared memory.
+  auto copy = [&](const uint8_t* pages, uint32_t row, int k) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(codes + 2048 * k), "l"(pages + (size_t)row * D)
+                 : "memory");
+  };
+  auto row_at = [&](uint32_t at, int k) -> uint32_t {  // its k-th row (or factors, 4 bytes behind)
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(at + 8 * kStep * k));
+    return r;
   };
   auto commit = [&]() { asm volatile("cp.async.commit_group;" ::: "memory"); };
   auto convert = [&](const uint4& x, uint32_t f, uint32_t dst, int k) {
@@ -266,7 +266,8 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
       if (!loaded) {
 #pragma unroll 1
         for (int k0 = 0; k0 < NR; k0 += kGroup) {
-          copy(kp, at, k0);
+#pragma unroll
+          for (int k = k0; k < k0 + kGroup; ++k) copy(kp, row_at(at, k), k);
           commit();
         }
       }
@@ -304,15 +305,19 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
         // (this tile's later pieces may still be on their way)
         asm volatile("cp.async.wait_group %0;" ::"n"(NR / kGroup - 1) : "memory");
         uint4 x[kGroup];
-        uint32_t fs[kGroup];
+        uint32_t fs[kGroup], row[kGroup];
 #pragma unroll
         for (int k = 0; k < kGroup; ++k) {
+          row[k] = row_at(at_next, k0 + k);
           x[k] = lds128(codes + 2048 * (k0 + k));
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(fs[k]) : "r"(at + 8 * kStep * (k0 + k) + 4));
+          fs[k] = row_at(at + 4, k0 + k);
         }
 #pragma unroll
         for (int k = 0; k < kGroup; ++k) convert(x[k], __byte_perm(fs[k], 0, pick), dst, k0 + k);
-        if (loaded || tiles == 2) copy(next, at_next, k0);
+        if (loaded || tiles == 2) {
+#pragma unroll
+          for (int k = 0; k < kGroup; ++k) copy(next, row[k], k0 + k);
+        }
         commit();
       }
       if (more) {  // the second factors: over what this thread has just written
