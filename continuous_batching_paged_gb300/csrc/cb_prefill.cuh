@@ -116,12 +116,18 @@ static_assert(kRegsQuantIssue + 2 * kRegsQuantSoftmax + kRegsQuantConvert <= 4 *
               "register split exceeds the launch");
 constexpr int kRowSlots = 4;  // K/V tiles whose rows are known ahead
 struct RowSlot {
-  // per key: its row in the pool (token x Hkv + KV head), and the two factors that make
-  // its codes values (bf16, the key's in the low half; quant_convert)
-  uint2 row[kChunkKeys];
-  uint32_t more[kChunkKeys];  // further factors, with kRowMore
-  int flags, pad;
+  // per key, in the order row_place: its row in the pool (token x Hkv + KV head), the two factors that make
+  // its codes values (bf16, the key's in the low half; quant_convert), and further ones, with kRowMore
+  uint32_t row[kChunkKeys], factor[kChunkKeys], more[kChunkKeys];
+  int flags, pad[3];
 };
+// Where key 0 .. 127 of a tile stands: the rows r0, r0 + 128 / NR, ... of a converting thread (NR = D / 16)
+// follow one another.
+template <int D>
+__device__ __forceinline__ int row_place(int key) {
+  constexpr int NR = D / 16, kStep = kChunkKeys / NR;
+  return key % kStep * NR + key / kStep;
+}
 // an item's first and last tile; no more tiles; some scale takes two factors
 constexpr int kRowFirst = 1, kRowLast = 2, kRowEnd = 4, kRowMore = 8;
 template <int D>
@@ -134,7 +140,7 @@ struct QuantPrefillSmem {
   static constexpr int kRows = kOut + 8 * kOutWarp;
   static constexpr int kBar = kRows + kRowSlots * (int)sizeof(RowSlot);  // full, empty per slot
   static constexpr int kTotal = kBar + 2 * kRowSlots * 8 + 1024;
-  static_assert(kRows % 16 == 0 && sizeof(RowSlot) % 8 == 0, "alignment of shared-memory regions");
+  static_assert(kRows % 16 == 0 && sizeof(RowSlot) % 16 == 0, "alignment of shared-memory regions");
 };
 
 // Query heads (pairs) per unit: items are unit-major with the head (pair) fastest, so the

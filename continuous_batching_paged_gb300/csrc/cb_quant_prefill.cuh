@@ -7,8 +7,8 @@
 // (The tensor cores' own 8-bit products would take the codes as they are, but need the queries and the
 // probabilities in 8 bits too, which costs either accuracy or a second product and more work in the
 // softmax warps.)  What bounds the pass is this part's instructions, four per two values on the
-// converting warps: 8 chunks of 512 tokens on up to 4096 keys (32 query, 8 KV heads of 128) take 153 us,
-// 749 TFLOP/s, on a bf16 cache 150; on up to 8192 keys 231 and 218.
+// converting warps: 8 chunks of 512 tokens on up to 4096 keys (32 query, 8 KV heads of 128) take 152 us,
+// 754 TFLOP/s, on a bf16 cache 150; on up to 8192 keys 230 and 218.
 #pragma once
 
 #include <cstddef>
@@ -139,9 +139,10 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
         const uint32_t fk = ek == kQuantNan - kQuantBias ? 0x7fffu : (uint32_t)(247 + min(ek, 7)) << 7;
         const uint32_t fv = ev == kQuantNan - kQuantBias ? 0x7fffu : (uint32_t)(247 + min(ev, 7)) << 7;
         // (where there is no key: the pool's first row, times 0)
-        rs.row[32 * i + lane] = make_uint2(tok_j[i] < 0 ? 0u : (uint32_t)tok_j[i] * a.Hkv + it.kvh,
-                                           tok_j[i] < 0 ? 0u : fk | fv << 16);
-        rs.more[32 * i + lane] = (uint32_t)(127 + max(ek - 7, 0)) << 7 | (uint32_t)(127 + max(ev - 7, 0)) << 23;
+        const int at = row_place<D>(32 * i + lane);
+        rs.row[at] = tok_j[i] < 0 ? 0u : (uint32_t)tok_j[i] * a.Hkv + it.kvh;
+        rs.factor[at] = tok_j[i] < 0 ? 0u : fk | fv << 16;
+        rs.more[at] = (uint32_t)(127 + max(ek - 7, 0)) << 7 | (uint32_t)(127 + max(ev - 7, 0)) << 23;
         more = more || (tok_j[i] >= 0 && max(ek, ev) > 7);
       }
       more = __any_sync(0xffffffffu, more);
@@ -194,7 +195,8 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t f) {
 // up to 16384 keys (32 query, 8 KV heads of 128) took 1262 us with the next tile's codes in registers,
 // loaded between the conversions, all unrolled; 1072 with the codes here; 1024 with a loop over four rows;
 // 967 with the order's decisions once a stage and rows without a predicate; 956 with the next rows read
-// beside the codes.  (Two rows at a time 993, eight 1020, one 1326.  On a bf16 cache 855.)
+// beside the codes; 947 with a thread's rows and factors side by side.  (Two rows at a time 993, eight 1020,
+// one 1326.  On a bf16 cache 855.)
 template <int D>
 __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs& qa, uint8_t* smem,
                                               uint32_t sbase) {
@@ -202,6 +204,7 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
   using QM = QuantPrefillSmem<D>;
   constexpr int NS = SM::kStages, NR = QM::kRowsPerThread;
   constexpr int kGroup = 4;  // rows at a time
+  constexpr uint32_t kFactors = offsetof(RowSlot, factor), kMore = offsetof(RowSlot, more);
   auto bar = [&](int i) -> uint32_t { return sbase + SM::kBar + 8 * i; };
   const uint32_t row_full = sbase + QM::kBar, row_empty = row_full + 8 * kRowSlots;
   const uint32_t rings = sbase + QM::kRows;
@@ -236,10 +239,11 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(codes + 2048 * k), "l"(pages + (size_t)row * D)
                  : "memory");
   };
-  auto row_at = [&](uint32_t at, int k) -> uint32_t {  // its k-th row (or factors, 4 bytes behind)
-    uint32_t r;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(at + 8 * kStep * k));
-    return r;
+  auto copy4 = [&](const uint8_t* pages, const uint4& row, int k0) {
+    copy(pages, row.x, k0);
+    copy(pages, row.y, k0 + 1);
+    copy(pages, row.z, k0 + 2);
+    copy(pages, row.w, k0 + 3);
   };
   auto commit = [&]() { asm volatile("cp.async.commit_group;" ::: "memory"); };
   auto convert = [&](const uint4& x, uint32_t f, uint32_t dst, int k) {
@@ -257,7 +261,7 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
   int flags = 0, before = 0;  // of tiles n and n - 1
   bool loaded = false;   // the codes of tile n's keys are on their way although its item has not begun
   for (uint32_t g = 0;; ++g) {
-    uint32_t at = slot(n) + 8 * r0;  // this thread's first row in tile n's slot
+    uint32_t at = slot(n) + 4 * NR * r0;  // this thread's first row in tile n's slot
     if (!has_v) {          // an item begins
       ready(n);
       if (!ok) break;
@@ -266,8 +270,8 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
       if (!loaded) {
 #pragma unroll 1
         for (int k0 = 0; k0 < NR; k0 += kGroup) {
-#pragma unroll
-          for (int k = k0; k < k0 + kGroup; ++k) copy(kp, row_at(at, k), k);
+          const uint4 row = lds128(at + 4 * k0);
+          copy4(kp, row, k0);
           commit();
         }
       }
@@ -286,7 +290,7 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
     const int flags_n = flags_of(nn);
     wait(bar(SM::bEmpty + g % NS), ((g / NS) & 1) ^ 1);
     if (!ok) break;
-    const uint32_t at_n = slot(nn) + 8 * r0, at_v = slot(n - 1) + 8 * r0;
+    const uint32_t at_n = slot(nn) + 4 * NR * r0, at_v = slot(n - 1) + 4 * NR * r0;
     uint32_t dst = sbase + SM::kStage0 + (g % NS) * SM::kStageBytes, pick = 0x1010u;
     if (!has_k) {
       dst += SM::kKVTile;
@@ -304,20 +308,15 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
       for (int k0 = 0; k0 < NR; k0 += kGroup) {
         // (this tile's later pieces may still be on their way)
         asm volatile("cp.async.wait_group %0;" ::"n"(NR / kGroup - 1) : "memory");
+        const uint4 row = lds128(at_next + 4 * k0), fs = lds128(at + kFactors + 4 * k0);
         uint4 x[kGroup];
-        uint32_t fs[kGroup], row[kGroup];
 #pragma unroll
-        for (int k = 0; k < kGroup; ++k) {
-          row[k] = row_at(at_next, k0 + k);
-          x[k] = lds128(codes + 2048 * (k0 + k));
-          fs[k] = row_at(at + 4, k0 + k);
-        }
-#pragma unroll
-        for (int k = 0; k < kGroup; ++k) convert(x[k], __byte_perm(fs[k], 0, pick), dst, k0 + k);
-        if (loaded || tiles == 2) {
-#pragma unroll
-          for (int k = 0; k < kGroup; ++k) copy(next, row[k], k0 + k);
-        }
+        for (int k = 0; k < kGroup; ++k) x[k] = lds128(codes + 2048 * (k0 + k));
+        convert(x[0], __byte_perm(fs.x, 0, pick), dst, k0);
+        convert(x[1], __byte_perm(fs.y, 0, pick), dst, k0 + 1);
+        convert(x[2], __byte_perm(fs.z, 0, pick), dst, k0 + 2);
+        convert(x[3], __byte_perm(fs.w, 0, pick), dst, k0 + 3);
+        if (loaded || tiles == 2) copy4(next, row, k0);
         commit();
       }
       if (more) {  // the second factors: over what this thread has just written
@@ -327,7 +326,7 @@ __device__ __forceinline__ void quant_convert(const AttnArgs& a, const QuantArgs
           uint32_t m;
           asm volatile("ld.shared.u32 %0, [%1];"
                        : "=r"(m)
-                       : "r"(at - 8 * r0 + (uint32_t)offsetof(RowSlot, more) + 4 * (r0 + kStep * (i >> 1))));
+                       : "r"(at + kMore + 4 * (i >> 1)));
           m = __byte_perm(m, 0, pick);
           uint32_t y[4];
           asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
