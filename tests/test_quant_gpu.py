@@ -317,6 +317,17 @@ def test_chunks_long_context_and_serial(cuda_lib):
     assert torch.equal(out[-64:].view(torch.int16), out2[-64:].view(torch.int16))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("score", [dict(), dict(window=40, softcap=20.0)], ids=str)
+def test_chunks_of_one_to_three_tiles(cuda_lib, D, score):
+    """Many short items in a row on every CTA: one tile, two, three, and ends at and beside a tile's."""
+    rng = np.random.default_rng(949)
+    ql = [int(x) for x in rng.integers(2, 70, 90)]
+    kv = [q + int(x) for q, x in zip(ql, rng.choice([0, 0, 1, 58, 60, 128, 186, 250], 90))]
+    ql[:4], kv[:4] = [128, 129, 64, 2], [128, 129, 128, 257]
+    check_attention(workloads.build_batch(ql, kv, 16, 8, D, 16, seed=949), **score)
+
+
 @pytest.mark.parametrize("D,Hq,Hkv,bs", [(128, 8, 2, 16), (64, 15, 5, 7), (128, 16, 1, 64)])
 def test_only_decodes_only_chunks_and_one_pass_after_the_other(cuda_lib, D, Hq, Hkv, bs):
     """Batches without work for one of the passes, and both passes in a row (serial): the same bits."""
