@@ -141,15 +141,22 @@ __device__ __forceinline__ void quant_produce(const AttnArgs& a, const QuantArgs
   // one by one below), and this lane's place in one.
   const int per_batch = runs <= 32 ? 32 / runs : 1;
   const int my_tile = runs <= 32 ? lane / runs : 0, my_key = runs <= 32 ? lane % runs * KB : 0;
-  // The block id of this lane's run in the batch of tiles [t, hi) of r, and the offset in the block (-1:
-  // no such run, -2: beyond the table)
+  // Has a run that begins at key pos of r keys that are seen?  (Of those before a sliding window the table's
+  // entries may name no block any more.)
+  auto seen = [&](const int4& r, int pos) {
+    return pos < r.z && pos + KB > window_first_key(r.z - 1, a.window);
+  };
+  // The block id of this lane's run in the batch of tiles [t, hi) of r, and the offset in the block
+  // (kNoRun: no such run; kNoBlock: beyond the table, or an entry that is no block id, -1 among them)
+  constexpr int kNoRun = -1, kNoBlock = -2;
   auto fetch = [&](const int4& r, long long t, int& off) -> int {
     const int pos = first_key(r) + (int)(t + my_tile - r.w) * tile_keys + my_key;
     off = 0;
-    if (runs > 32 || my_tile >= per_batch || pos >= r.z) return -1;
+    if (runs > 32 || my_tile >= per_batch || !seen(r, pos)) return kNoRun;
     const int lb = pos / a.bs;
     off = pos - lb * a.bs;
-    return lb < a.max_blocks ? __ldg(a.block_table + (size_t)r.x * a.max_blocks + lb) : -2;
+    const int block = lb < a.max_blocks ? __ldg(a.block_table + (size_t)r.x * a.max_blocks + lb) : kNoBlock;
+    return block < 0 ? kNoBlock : block;
   };
   int off, e = fetch(rec, t0, off);
   uint32_t stage = 0, phase = 1;
@@ -158,13 +165,13 @@ __device__ __forceinline__ void quant_produce(const AttnArgs& a, const QuantArgs
     const long long p0 = rec.w, p1 = next.w;
     const long long hi = t1 < p1 ? t1 : p1;
     const int nb = (int)(hi - t < per_batch ? hi - t : per_batch);
-    int off_n = 0, e_n = -1;
+    int off_n = 0, e_n = kNoRun;
     if (t + nb < t1) e_n = fetch(t + nb < p1 ? rec : next, t + nb, off_n);
     if (begins && lane == 0)  // the consumers read the query rows a few stages from now
       l2_prefetch_bulk(static_cast<const __nv_bfloat16*>(a.q) + ((size_t)rec.y * a.Hq + (size_t)head0 * a.G) * D,
                        (uint32_t)(HB * a.G * D * 2));
     // (runs of this lane's tile count only where the tile is the sequence's and the CTA's)
-    const bool want = e != -1 && t + my_tile < hi, good = want && e >= 0 && e < a.P;
+    const bool want = e != kNoRun && t + my_tile < hi, good = want && e >= 0 && e < a.P;
     if (want && !good) report(a.err, kErrOutOfRange);
     const int token = good ? e * a.bs + off : -1;
     const int key_t = first_key(rec) + (int)(t - p0) * tile_keys;
@@ -186,7 +193,7 @@ __device__ __forceinline__ void quant_produce(const AttnArgs& a, const QuantArgs
         for (int run = lane; run < runs; run += 32) {  // (runs is a multiple of 32)
           const int pos = key0 + run * KB;
           int id = -1;
-          if (pos < rec.z) {
+          if (seen(rec, pos)) {
             const int lb = pos / a.bs;
             const int block = lb < a.max_blocks ? __ldg(a.block_table + (size_t)rec.x * a.max_blocks + lb) : -1;
             if (block >= 0 && block < a.P)

@@ -78,12 +78,18 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
     }
     int ent[4], tok[4];
     unsigned short sc[4];
+    // keys before the earliest query's window are not read: the table's entries may name no block any more
+    const int lo = kMod ? window_first_key(it.ctx + it.qoff[0], a.window) : 0;
+    constexpr int kNoKey = -1, kNoBlock = -2;  // (beyond the table, or an entry that is no block id, -1 among them)
     auto fetch = [&](int j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        ent[i] = -1;  // no key
-        if (j * kChunkKeys + 32 * i + lane < it.nk_all)
-          ent[i] = lb[i] < a.max_blocks ? __ldg(table + lb[i]) : -2;
+        const int pos = j * kChunkKeys + 32 * i + lane;
+        ent[i] = kNoKey;
+        if (pos < it.nk_all && (!kMod || pos >= lo)) {
+          ent[i] = lb[i] < a.max_blocks ? __ldg(table + lb[i]) : kNoBlock;
+          if (ent[i] < 0) ent[i] = kNoBlock;
+        }
       }
     };
     auto resolve = [&]() {  // ent's tokens, and their scales
@@ -92,7 +98,7 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
         tok[i] = -1;
         if (ent[i] >= 0 && ent[i] < a.P)
           tok[i] = ent[i] * a.bs + off[i];
-        else if (ent[i] != -1)
+        else if (ent[i] != kNoKey)
           report(a.err, kErrOutOfRange);
       }
 #pragma unroll
