@@ -146,17 +146,20 @@ __device__ __forceinline__ void quant_produce(const AttnArgs& a, const QuantArgs
   auto seen = [&](const int4& r, int pos) {
     return pos < r.z && pos + KB > window_first_key(r.z - 1, a.window);
   };
-  // The block id of this lane's run in the batch of tiles [t, hi) of r, and the offset in the block
-  // (kNoRun: no such run; kNoBlock: beyond the table, or an entry that is no block id, -1 among them)
-  constexpr int kNoRun = -1, kNoBlock = -2;
+  // The key with which this lane's run in the batch of tiles [t, hi) of r begins, and whether there is one
+  auto run_key = [&](const int4& r, long long t) {
+    return first_key(r) + (int)(t + my_tile - r.w) * tile_keys + my_key;
+  };
+  auto has_run = [&](const int4& r, int pos) { return runs <= 32 && my_tile < per_batch && seen(r, pos); };
+  // Its entry of the block table (-1 beyond the table; looked at only when the batch's turn has come), and
+  // the offset in the block
   auto fetch = [&](const int4& r, long long t, int& off) -> int {
-    const int pos = first_key(r) + (int)(t + my_tile - r.w) * tile_keys + my_key;
+    const int pos = run_key(r, t);
     off = 0;
-    if (runs > 32 || my_tile >= per_batch || !seen(r, pos)) return kNoRun;
+    if (!has_run(r, pos)) return -1;
     const int lb = pos / a.bs;
     off = pos - lb * a.bs;
-    const int block = lb < a.max_blocks ? __ldg(a.block_table + (size_t)r.x * a.max_blocks + lb) : kNoBlock;
-    return block < 0 ? kNoBlock : block;
+    return lb < a.max_blocks ? __ldg(a.block_table + (size_t)r.x * a.max_blocks + lb) : -1;
   };
   int off, e = fetch(rec, t0, off);
   uint32_t stage = 0, phase = 1;
@@ -165,13 +168,13 @@ __device__ __forceinline__ void quant_produce(const AttnArgs& a, const QuantArgs
     const long long p0 = rec.w, p1 = next.w;
     const long long hi = t1 < p1 ? t1 : p1;
     const int nb = (int)(hi - t < per_batch ? hi - t : per_batch);
-    int off_n = 0, e_n = kNoRun;
+    int off_n = 0, e_n = -1;
     if (t + nb < t1) e_n = fetch(t + nb < p1 ? rec : next, t + nb, off_n);
     if (begins && lane == 0)  // the consumers read the query rows a few stages from now
       l2_prefetch_bulk(static_cast<const __nv_bfloat16*>(a.q) + ((size_t)rec.y * a.Hq + (size_t)head0 * a.G) * D,
                        (uint32_t)(HB * a.G * D * 2));
     // (runs of this lane's tile count only where the tile is the sequence's and the CTA's)
-    const bool want = e != kNoRun && t + my_tile < hi, good = want && e >= 0 && e < a.P;
+    const bool want = t + my_tile < hi && has_run(rec, run_key(rec, t)), good = want && e >= 0 && e < a.P;
     if (want && !good) report(a.err, kErrOutOfRange);
     const int token = good ? e * a.bs + off : -1;
     const int key_t = first_key(rec) + (int)(t - p0) * tile_keys;

@@ -80,25 +80,24 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
     unsigned short sc[4];
     // keys before the earliest query's window are not read: the table's entries may name no block any more
     const int lo = kMod ? window_first_key(it.ctx + it.qoff[0], a.window) : 0;
-    constexpr int kNoKey = -1, kNoBlock = -2;  // (beyond the table, or an entry that is no block id, -1 among them)
+    auto has_key = [&](int j, int i) {
+      const int pos = j * kChunkKeys + 32 * i + lane;
+      return pos < it.nk_all && (!kMod || pos >= lo);
+    };
     auto fetch = [&](int j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int pos = j * kChunkKeys + 32 * i + lane;
-        ent[i] = kNoKey;
-        if (pos < it.nk_all && (!kMod || pos >= lo)) {
-          ent[i] = lb[i] < a.max_blocks ? __ldg(table + lb[i]) : kNoBlock;
-          if (ent[i] < 0) ent[i] = kNoBlock;
-        }
+        ent[i] = -1;
+        if (has_key(j, i) && lb[i] < a.max_blocks) ent[i] = __ldg(table + lb[i]);
       }
     };
-    auto resolve = [&]() {  // ent's tokens, and their scales
+    auto resolve = [&](int j) {  // ent's tokens, of tile j, and their scales
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         tok[i] = -1;
         if (ent[i] >= 0 && ent[i] < a.P)
           tok[i] = ent[i] * a.bs + off[i];
-        else if (ent[i] != kNoKey)
+        else if (has_key(j, i))
           report(a.err, kErrOutOfRange);
       }
 #pragma unroll
@@ -120,7 +119,7 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
       }
     };
     fetch(it.j0);
-    resolve();
+    resolve(it.j0);
     advance();
     fetch(it.j0 + 1);
     for (int j = it.j0; j < it.nt_all && ok; ++j, ++n) {
@@ -131,7 +130,7 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
         tok_j[i] = tok[i];
         sc_j[i] = sc[i];
       }
-      resolve();
+      resolve(j + 1);
       advance();
       fetch(j + 2);
       RowSlot& rs = ring[n % kRowSlots];
