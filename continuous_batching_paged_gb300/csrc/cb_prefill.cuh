@@ -603,21 +603,31 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
 #pragma unroll
             for (int c = 0; c < 128; c += 2)
               big = fmax3(big, fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
-            if (__all_sync(0xffffffffu, big <= sc.near_max)) {
-              uint64_t near[5];
+            uint64_t near[5];
 #pragma unroll
-              for (int i = 0; i < 5; ++i) near[i] = f2_pack(sc.near[i], sc.near[i]);
+            for (int i = 0; i < 5; ++i) near[i] = f2_pack(sc.near[i], sc.near[i]);
 #pragma unroll
-              for (int c = 0; c < 128; c += 2) {
-                float x0, x1;
-                f2_unpack(cap_near(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), near), x0, x1);
-                sr[c] = __float_as_uint(x0);
-                sr[c + 1] = __float_as_uint(x1);
+            for (int c = 0; c < 128; c += 2) {
+              float x0, x1;
+              f2_unpack(cap_near(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), near), x0, x1);
+              sr[c] = __float_as_uint(x0);
+              sr[c + 1] = __float_as_uint(x1);
+            }
+            // Then the scores beyond its range, S being still in TMEM.  Both forms are per score, so that a row's
+            // bits depend on nothing beside it (the choice between them for a warp's tile as a whole looked at
+            // masked keys, at keys' rows that an earlier item had left and at other sequences' queries too).
+            if (!__all_sync(0xffffffffu, big <= sc.near_max)) {
+#pragma unroll
+              for (int c0 = 0; c0 < 128; c0 += 16) {
+                uint32_t raw[16];
+                tmem_ld16(t_lane + s_col + c0, raw);
+                tc_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                  const float s = __uint_as_float(raw[c]), far = cap_score(s, sc);
+                  if (!(fabsf(s) <= sc.near_max)) sr[c0 + c] = __float_as_uint(far);
+                }
               }
-            } else {
-#pragma unroll
-              for (int c = 0; c < 128; ++c)
-                sr[c] = __float_as_uint(cap_score(__uint_as_float(sr[c]), sc));
             }
           }
           if (sc.slopes != nullptr) {

@@ -22,10 +22,13 @@ __device__ __forceinline__ float cap_score(float s, const ScoreArgs& sc) {
 // The same for two scores with |u| <= 0.6 each, without the two special-function instructions per
 // score: tanh(u) / u is a polynomial in u^2, here the interpolation of degree 4 at Chebyshev's points of
 // [0, 0.36], off by 4e-8 in tanh.  The host multiplies scale log2(e) and the powers of scale / cap into
-// the coefficients (ScoreArgs::near), so it takes six instructions on pairs of the raw products s.
-// (8 chunks of 512 tokens on up to 4096 keys, 32 query, 8 KV heads of 128: without a cap 145 us, so 217, by
-// the special functions 244.  A shorter polynomial for smaller scores beside this one, degree 2 to 0.3 caps:
-// 208 where it applied, 250 where it did not.)
+// the coefficients (ScoreArgs::near), so it takes six instructions on pairs of the raw products s.  The chunk
+// pass computes it for all scores and cap_score for those beyond its range, in tiles that have any.
+// (8 chunks of 512 tokens on up to 4096 keys, 32 query, 8 KV heads of 128, the whole call: with slopes instead
+// 204 us, capped at 50 237, at 2, where a quarter of the scores is beyond, 343; with one form for a warp's tile
+// as a whole, by its largest product, 239 and 282, but then a row's bits depend on what stands beside it.  A
+// shorter polynomial for smaller scores beside this one, degree 2 to 0.3 caps, made the pass 4 % faster where
+// it applied and 15 % slower where it did not.)
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
