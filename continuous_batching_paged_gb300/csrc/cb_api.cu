@@ -2,6 +2,7 @@
 // and the per-device error word.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -281,20 +282,26 @@ cb_status score_args(const cb_score* score, const cb_options* options, float sca
   if (score->visible_lens != nullptr && *on)
     return fail(CB_ERR_UNSUPPORTED, "visible_lens with a sliding window");
   if (cap > 0.f) {
-    out->cap_in = (float)(2.0 * 1.4426950408889634 * (double)scale / (double)cap);
-    out->cap_out = cap * 1.4426950408889634f;
     // tanh(u) = u (c0 + c1 u^2 + ... + c4 u^8) for |u| <= 0.6 (cb_score.cuh)
     const double c[5] = {0.9999999403953552, -0.33332324028015137, 0.13310357928276062,
                          -0.052109625190496445, 0.01548669021576643};
-    const double u = (double)scale / (double)cap;
-    // (beyond these, powers of u and of q.k leave fp32, and the coefficients themselves do)
-    if (u > 1e-4 && u < 1e4 && (double)scale * std::pow(std::fmax(u, 1.0), 8.0) < 1e37) {
-      double f = (double)scale * 1.4426950408889634;
-      for (int i = 0; i < 5; ++i, f *= u * u) out->near[i] = (float)(c[i] * f);
-      out->near_max = (float)(0.6 / u);
-    }
-    if (!(out->cap_in > 0.f) || out->cap_in > 1e30f)
+    double u = (double)scale / (double)cap, f = (double)scale * 1.4426950408889634;
+    const float cap_in = (float)(2.0 * 1.4426950408889634 * u);
+    if (!(cap_in > 0.f) || cap_in > 1e30f)
       return fail(CB_ERR_INVALID_ARG, "scale / softcap is out of range");
+    // The coefficients hold powers of u, which leave fp32 where scale and cap are far apart: the products are
+    // brought near 1 / u then.
+    out->near_in = 1.f;
+    if (!(u > 1e-4 && u < 1e4 && f * std::pow(std::fmax(u, 1.0), 8.0) < 1e37 &&
+          f * std::pow(std::fmin(u, 1.0), 8.0) > 1e-35)) {
+      out->near_in = (float)std::ldexp(1.0, std::max(std::min(std::ilogb(u), 126), -126));
+      u /= out->near_in;
+      f /= out->near_in;
+    }
+    out->cap_in = (float)(2.0 * 1.4426950408889634 * u);
+    out->cap_out = cap * 1.4426950408889634f;
+    out->near_max = (float)(0.6 / u);
+    for (int i = 0; i < 5; ++i, f *= u * u) out->near[i] = (float)(c[i] * f);
   }
   out->slopes = score->slopes;
   out->visible = score->visible_lens;

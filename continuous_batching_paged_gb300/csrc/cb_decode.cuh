@@ -312,11 +312,7 @@ __device__ __forceinline__ void decode_consume(const AttnArgs& a, uint32_t sbase
         for (int ks = 0; ks < KS; ++ks) mma_bf16_16816(s[ht], kf[ks], qb[ht][ks][0], qb[ht][ks][1]);
       }
     }
-    if constexpr (kMod) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        s[0][x] = change_score(s[0][x], a.scale_log2, slope[x & 1], si.key0 + g + 8 * (x >> 1), si.kv - 1, sc);
-    }
+    if constexpr (kMod) change_scores<4>(s[0], a.scale_log2, slope, si.key0 + g - (si.kv - 1), sc);
     if constexpr (kPre && QS == 1) {
       if (edge || head) {
         const int k0 = si.key0 + g, k1 = k0 + 8;

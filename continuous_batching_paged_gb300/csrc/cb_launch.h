@@ -108,8 +108,9 @@ struct ScoreArgs {
   const float* slopes;     // [Hq] or NULL
   const int32_t* visible;  // [S] or NULL
   float cap_in, cap_out;   // 2 log2(e) scale / cap, cap log2(e); 0: no cap
-  float near[5];           // the polynomial of cap_near, and the largest |q.k| it is for (0: none)
+  float near[5];           // the polynomial of cap_near, and the largest |q.k| it is for
   float near_max;
+  float near_in;           // with a cap, a power of two, most often 1: q.k stands for this times it, here and there
 };
 
 // What the attention passes need of the quantised cache beside AttnArgs.

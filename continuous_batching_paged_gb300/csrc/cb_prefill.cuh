@@ -592,6 +592,18 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         if (!mbar_wait(bar(SM::bSFull + t), tt & 1)) { report(a.err, kErrTimeout); ok = false; break; }
         __syncwarp();
         tc_fence_after();
+        if (kMod && sc.cap_in > 0.f && sc.near_in != 1.f) {  // (rare: S in TMEM, times near_in)
+#pragma unroll 1
+          for (int c0 = 0; c0 < 128; c0 += 8) {
+            uint32_t x[8];
+            tmem_ld8(t_lane + s_col + c0, x);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * sc.near_in);
+            tmem_st8(t_lane + s_col + c0, x);
+          }
+          tc_wait_st();
+        }
         uint32_t sr[128];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(t_lane + s_col + i * 32, sr + i * 32);
@@ -624,7 +636,7 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
                 tc_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
-                  const float s = __uint_as_float(raw[c]), far = cap_score(s, sc);
+                  const float s = __uint_as_float(raw[c]), far = cap_far(s, sc);
                   if (!(fabsf(s) <= sc.near_max)) sr[c0 + c] = __float_as_uint(far);
                 }
               }

@@ -462,19 +462,22 @@ __device__ __forceinline__ void quant_consume(const AttnArgs& a, const QuantArgs
       }
     }
     // y = x + ev; the weights of l
-    float wl[4];
+    float wl[4], ev[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float fk = __uint_as_float((ex[i] & 255u) << 23), ev = (float)(int)(ex[i] >> 8) - 127.f;
+      const float fk = __uint_as_float((ex[i] & 255u) << 23);
+      ev[i] = (float)(int)(ex[i] >> 8) - 127.f;
       wl[i] = __uint_as_float((254u - (ex[i] >> 8)) << 23);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float& x = s[i >> 1][2 * (i & 1) + j];
-        if constexpr (kMod)
-          x = change_score(x * fk * cq[j], sl2, slope[j], key0 + 8 * i + g, si.kv - 1, sc) + ev;
-        else
-          x = fmaf(x * fk, cq[j], ev);
+        x = kMod ? x * fk * cq[j] : fmaf(x * fk, cq[j], ev[i]);
       }
+    }
+    if constexpr (kMod) {
+      change_scores<8>(&s[0][0], sl2, slope, key0 + g - (si.kv - 1), sc);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) s[x >> 2][x & 3] += ev[x >> 1];
     }
     if (edge) {
 #pragma unroll

@@ -327,8 +327,7 @@ cb_status cb_rope_append_attention(const void* q, const void* k_new, const void*
  *     x = scale q.k,   x = softcap * tanh(x / softcap) where softcap > 0,   x += slopes[h] (j - p),
  * and key j is seen when j <= p or j < visible_lens[s] (never beyond kv_len).  A sliding window
  * (cb_options) goes with the first two, not with visible_lens (CB_ERR_UNSUPPORTED).  The cap is
- * computed to within 2^-21 softcap, absolute: a cap is to be chosen as a model's, not as a large
- * number that stands for none.
+ * computed to within 2^-20 of the capped score.
  */
 typedef struct {
   float softcap;                /* 0: none                                                       */

@@ -1,4 +1,5 @@
-"""Capped scores: a row's result is a function of its own sequence alone."""
+"""Capped scores: as exact as uncapped ones whatever the cap's size, and a row's result a function of its own
+sequence alone."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +8,8 @@ import continuous_batching_paged_gb300 as cb
 import workloads
 from gpu_util import DeviceBatch, oracle_append
 from oracle import paged_attention as opa
-from quant_util import QuantBatch
+from oracle import quant as oq
+from quant_util import P8, P16, QuantBatch, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -41,6 +43,71 @@ class Cache:
         if self.quant:
             return self.d.cached(s)
         return [opa.gather_kv(p, b.block_table[s], int(b.kv_lens[s]), b.block_size) for p in self.pools]
+
+
+def check_capped(c, softcap):
+    """Every row against the oracle.  A score x is off by 2^-20 |x| by the cap (tanh by a polynomial or from
+    exp2 and a reciprocal: 2^-21 of itself, and the roundings of its factors), and by its products' rounding: D of them summed in fp32, 2^-24 each of the sum of |q_d k_d|, which the cap, of slope 1
+    at most, does not enlarge.  The quantised decode pass has its query row in fp16, off by 2^-25 of its largest
+    power of two.  That moves a probability by e (and an exponential's 2^-21) and the output by 2 e times the
+    weighted |v|; a probability is rounded once to p_step, the result to bf16."""
+    b = c.b
+    out, lse = c.attend(softcap=softcap)
+    o, l, q = f64(out), f64(lse), opa.bf16_bits_to_f64(b.q)
+    g = b.num_q_heads // b.num_kv_heads
+    for s in range(b.num_seqs):
+        c0, c1, kv = int(b.cu_seqlens_q[s]), int(b.cu_seqlens_q[s + 1]), int(b.kv_lens[s])
+        n = c1 - c0
+        if n == 0:
+            continue
+        K, V = c.cached(s)
+        ref, ref_lse, size = oq.scored_attention(q[c0:c1], K, V, kv - n, b.scale, softcap)
+        Kr = np.repeat(np.abs(K), g, axis=1)
+        mag = np.einsum("nhd,khd->nhk", np.abs(q[c0:c1]), Kr).max(-1) * b.scale
+        x = np.abs(np.einsum("nhd,khd->nhk", q[c0:c1], np.repeat(K, g, axis=1))).max(-1) * b.scale
+        x = softcap * np.tanh(x / softcap)
+        fp16 = b.scale * np.abs(q[c0:c1]).max(-1) * Kr.sum(-1).max(0)[None] * 2.0 ** -25 if c.quant else 0.0
+        e = 2.0 ** -20 * x + 2.0 ** -24 * (b.head_dim + 8) * mag + fp16 + 2.0 ** -21
+        p_step = P16 if c.quant and n == 1 else P8
+        assert np.isfinite(o[c0:c1]).all()
+        tol = 2.0 ** -8 * np.abs(ref) + (p_step + 2 * e)[..., None] * size * (1 + 2.0 ** -8) + 1e-30
+        err = np.abs(o[c0:c1] - ref)
+        assert np.all(err <= tol), f"cap {softcap}, sequence {s}: worst {(err / tol).max():.3g}"
+        lerr = np.abs(l[c0:c1] - ref_lse)
+        assert np.all(lerr <= e + 2.0 ** -20 * (1 + np.abs(ref_lse))), f"cap {softcap}, sequence {s}: lse off by " \
+                                                                       f"{lerr.max():.3g}"
+
+
+CAPS = [0.3, 5.0, 50.0, 300.0, 1e3, 1e4, 1e6, 1e9, 1e15, 1e30]
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 3, 1), (128, 8, 2), (128, 16, 1)])
+@pytest.mark.parametrize("cap", CAPS)
+def test_caps_of_all_sizes(cuda_lib, cap, D, Hq, Hkv, quant):
+    check_capped(Cache(workloads.build_batch([1, 37, 1, 130, 5], [1, 37, 513, 700, 70], Hq, Hkv, D, 16,
+                                             seed=670 + D + Hq), quant), cap)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("scale,cap", [(1e-4, 1e-4), (1e-4, 1e-1), (3e-3, 1e-5), (5.0, 1e-3), (40.0, 4e3), (2.0, 1e20)])
+def test_scales_beside_the_usual(cuda_lib, scale, cap, quant):
+    b = workloads.build_batch([1, 37, 1, 130], [1, 37, 513, 300], 4, 2, 64, 16, seed=680)
+    b.scale = scale
+    check_capped(Cache(b, quant), cap)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("cap", [2.0, 30.0, 1e6])
+def test_small_scores_beside_large_ones(cuda_lib, cap, quant):
+    """Rows and heads of one tile whose scores are 2^12 apart."""
+    b = workloads.build_batch([1, 150, 1, 40], [300, 400, 65, 40], 8, 2, 128, 16, seed=690)
+    q = opa.bf16_bits_to_f64(b.q).astype(np.float32)
+    q[::3] *= np.float32(64.0)
+    q[1::3] *= np.float32(2.0 ** -6)
+    q[:, 3] *= np.float32(16.0)
+    b = workloads.Batch(**{**b.__dict__, "q": workloads.f32_to_bf16_bits(q)})
+    check_capped(Cache(b, quant), cap)
 
 
 @pytest.mark.parametrize("quant", [False, True])
