@@ -642,6 +642,8 @@ def _explain_score(q, num_seqs, softcap, slopes, visible_lens) -> None:
     import torch
     _require(isinstance(softcap, (int, float)) or hasattr(softcap, "__float__"),
              "softcap must be a number")
+    _require(float(softcap) == 0 or ctypes.c_float(softcap).value != 0,
+             "softcap must be 0 (none) or a number that fp32 holds")
     dev = q.get_device()
     if slopes is not None:
         _require(slopes.dtype == torch.float32 and slopes.is_cuda and slopes.is_contiguous()

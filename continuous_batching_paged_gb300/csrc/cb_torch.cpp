@@ -78,7 +78,8 @@ struct Step {
 bool read_step(PyObject* const* args, int dev, Step* s, at::ScalarType type = at::kBFloat16) {
   const at::Tensor* t[5];
   for (int i = 0; i < 5; ++i) t[i] = tensor(args[i]);
-  if (dev != c10::cuda::current_device() || !plain(t[0], type, 4, dev) || !plain(t[1], type, 4, dev) || !plain(t[2], at::kInt, 2, dev) ||
+  if (dev != c10::cuda::current_device() || !plain(t[0], type, 4, dev) ||
+      !plain(t[1], type, 4, dev) || !plain(t[2], at::kInt, 2, dev) ||
       !plain(t[3], at::kInt, t[3] ? t[3]->dim() : 0, dev) ||
       !plain(t[4], at::kInt, t[4] ? t[4]->dim() : 0, dev) || !read_int(args[5], &s->block_size))
     return false;
@@ -396,6 +397,7 @@ bool read_score(PyObject* const* args, const Step& s, cb_score* out) {
     return false;
   }
   out->softcap = (float)cap;
+  if (cap != 0 && out->softcap == 0.f) return false;  // (0 is no cap)
   if (args[1] != Py_None) {
     const at::Tensor* t = tensor(args[1]);
     if (!plain(t, at::kFloat, 1, s.dev) || t->numel() != s.dims.num_q_heads) return false;

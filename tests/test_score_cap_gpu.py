@@ -153,3 +153,17 @@ def test_same_bits_on_every_call(cuda_lib, quant):
     for _ in range(30):
         o, l = c.attend(softcap=4.0)
         assert torch.equal(o.view(torch.int16), out.view(torch.int16)) and torch.equal(l, lse)
+
+
+def test_caps_that_fp32_does_not_hold(cuda_lib):
+    """A cap that rounds to 0 (none) or to infinity is refused, not taken for none."""
+    b = workloads.build_batch([1, 3], [40, 30], 4, 2, 64, 16, seed=699)
+    for quant in (False, True):
+        c = Cache(b, quant)
+        with pytest.raises(ValueError, match="softcap"):
+            c.attend(softcap=1e-50)
+        with pytest.raises((ValueError, cb.CbError), match="softcap"):
+            c.attend(softcap=1e39)
+        with pytest.raises(ValueError, match="softcap"):
+            c.attend(softcap=-1e-50)
+        c.attend(softcap=0)
