@@ -17,9 +17,12 @@
 //     to fp16 range by 2^eq,
 //       x_j = scale log2(e) 2^(eq + ek_j) (qc . kc_j),   y_j = x_j + ev_j,   p_j = 2^(y_j - m),
 //       o = sum_j p_j vc_j,   l = sum_j p_j 2^-ev_j,   out = o / l,
-//     with m the running maximum of y: so p is at most 2^8 (the maximum is followed lazily) and its
-//     rounding to fp16 (2^-11 relative, 2^-25 absolute) is small against the largest contribution to
-//     o, whatever the sizes of the values.  l is summed in fp32, where 2^-ev (ev in [-32, 31]) is safe.
+//     with m the running maximum of y less 7, kept at the end of a sequence too: so p is at most 2^15 (the
+//     maximum is followed lazily, 2^8) and its rounding to fp16 -- 2^-11 relative, and 2^-32 of the largest
+//     where p is less than 2^-21 of that -- is small against the largest contribution to o, whatever the
+//     sizes of the values.  (With the largest p at 1, keys with less than 2^-25 of it were lost from o but
+//     not from l: 2^19 of them beside one that takes all are 1 / 65 of the result.)  l is summed in fp32,
+//     where 2^-ev (ev in [-32, 31]) is safe.
 #pragma once
 
 #include "cb_decode.cuh"
@@ -284,6 +287,8 @@ __device__ __forceinline__ void quant_produce(const AttnArgs& a, const QuantArgs
   }
 }
 
+constexpr float kFp16Room = 7.f;  // log2 of the largest p where the running maximum is up to date
+
 // Consumer warp: KV head h of the CTA's HB, query heads qoff .. qoff + 7 of its G, keys
 // 32 slice .. 32 slice + 31 of every tile.  As in the decode pass the keys are the M side of the score
 // product and the head dim that of the output product, 8 query heads the N side.  Lane (g, tq):
@@ -528,7 +533,7 @@ __device__ __forceinline__ void quant_consume(const AttnArgs& a, const QuantArgs
       }
     }
     // (a warp whose keys so far are all masked has m = -inf: 0 is subtracted instead)
-    const float sa = m[0] == -INFINITY ? 0.f : m[0], sb = m[1] == -INFINITY ? 0.f : m[1];
+    const float sa = m[0] == -INFINITY ? 0.f : m[0] - kFp16Room, sb = m[1] == -INFINITY ? 0.f : m[1] - kFp16Room;
     uint32_t pb[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -553,6 +558,8 @@ __device__ __forceinline__ void quant_consume(const AttnArgs& a, const QuantArgs
       }
 
     if (!(si.flags & kInfoLast)) continue;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) m[j] -= kFp16Room;  // what was subtracted
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
