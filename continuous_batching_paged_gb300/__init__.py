@@ -163,6 +163,12 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.cb_kv_restore.restype = ctypes.c_int
     lib.cb_kv_restore.argtypes = [_P, _P, _P, ctypes.c_int32, ctypes.c_int32,
                                   ctypes.POINTER(CbDims), _P, _P, _P]
+    lib.cb_quant_copy_blocks.restype = ctypes.c_int
+    lib.cb_quant_copy_blocks.argtypes = [_P] * 5 + [ctypes.c_int32, ctypes.c_int32,
+                                                    ctypes.POINTER(CbDims), _P]
+    for f in (lib.cb_quant_offload, lib.cb_quant_restore):
+        f.restype = ctypes.c_int
+        f.argtypes = [_P] * 4 + [ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(CbDims)] + [_P] * 4
 
 
 def library(build_if_missing: bool = True) -> ctypes.CDLL:
@@ -232,12 +238,26 @@ def _check_bf16(name, t, ndim):
     _require(t.dim() == ndim, f"{name} must have {ndim} dimensions")
 
 
-def _pool_dims(k_pages, v_pages, block_size) -> CbDims:
-    _check_bf16("k_pages", k_pages, 4)
+def _pool_dims(k_pages, v_pages, block_size, kv_scales=None) -> CbDims:
+    import torch
+    codes = kv_scales is not None
+    _require(codes or k_pages.dtype != torch.float8_e4m3fn, "kv_scales must be given with pools of codes")
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _check_codes(name, t) if codes else _check_bf16(name, t, 4)
     _require(k_pages.shape == v_pages.shape, "v_pages must match k_pages")
+    if codes:
+        _check_scales(kv_scales, k_pages)
     P, bs, Hkv, D = k_pages.shape
     _require(bs == block_size, "k_pages.shape[1] must be block_size")
     return _dims(0, 0, Hkv, Hkv, D, P, 1)
+
+
+def _check_host(n, *buffers) -> None:
+    """Pinned host buffers (name, tensor, the pool whose n blocks it holds)."""
+    for name, h, pool in buffers:
+        _require(h is not None and h.is_pinned() and h.is_contiguous()
+                 and h.numel() * h.element_size() >= n * pool[0].numel() * pool.element_size(),
+                 f"{name} must be pinned, contiguous, large enough")
 
 
 def _check_ids(name, t):
@@ -253,41 +273,51 @@ def selftest_wait_timeout(limit_us: int, waited_ns=None, stream=None) -> None:
            "cb_selftest_wait_timeout")
 
 
-def copy_blocks(k_pages, v_pages, src, dst, block_size, stream=None) -> None:
-    """Block dst[i] of both pools receives block src[i] (cb_copy_blocks: copy-on-write data)."""
-    dims = _pool_dims(k_pages, v_pages, block_size)
+def copy_blocks(k_pages, v_pages, src, dst, block_size, stream=None, kv_scales=None) -> None:
+    """Block dst[i] of both pools receives block src[i] (cb_copy_blocks: copy-on-write data).
+    kv_scales: a quantised cache's, copied with its codes (cb_quant_copy_blocks)."""
+    dims = _pool_dims(k_pages, v_pages, block_size, kv_scales)
     _check_ids("src", src)
     _check_ids("dst", dst)
     _require(src.numel() == dst.numel(), "src and dst must have the same length")
-    _check(library().cb_copy_blocks(_ptr(k_pages), _ptr(v_pages), _ptr(src), _ptr(dst),
-                                    src.numel(), int(block_size), ctypes.byref(dims),
-                                    _stream(stream)), "cb_copy_blocks")
+    rest = (_ptr(src), _ptr(dst), src.numel(), int(block_size), ctypes.byref(dims), _stream(stream))
+    if kv_scales is not None:
+        _check(library().cb_quant_copy_blocks(_ptr(k_pages), _ptr(v_pages), _ptr(kv_scales), *rest),
+               "cb_quant_copy_blocks")
+    else:
+        _check(library().cb_copy_blocks(_ptr(k_pages), _ptr(v_pages), *rest), "cb_copy_blocks")
 
 
-def kv_offload(k_pages, v_pages, blocks, block_size, host_k, host_v, stream=None) -> None:
-    """Gather blocks of both pools into pinned host tensors [n, bs, Hkv, D] (cb_kv_offload)."""
-    dims = _pool_dims(k_pages, v_pages, block_size)
+def _host_move(name, quant_name, k_pages, v_pages, blocks, block_size, host_k, host_v, stream, kv_scales,
+               host_scales) -> None:
+    dims = _pool_dims(k_pages, v_pages, block_size, kv_scales)
     _check_ids("blocks", blocks)
     n = blocks.numel()
-    for name, h in (("host_k", host_k), ("host_v", host_v)):
-        _require(h.is_pinned() and h.is_contiguous() and h.numel() * h.element_size()
-                 >= n * k_pages[0].numel() * 2, f"{name} must be pinned, contiguous, large enough")
-    _check(library().cb_kv_offload(_ptr(k_pages), _ptr(v_pages), _ptr(blocks), n,
-                                   int(block_size), ctypes.byref(dims), _ptr(host_k),
-                                   _ptr(host_v), _stream(stream)), "cb_kv_offload")
+    _check_host(n, ("host_k", host_k, k_pages), ("host_v", host_v, v_pages))
+    where = (_ptr(blocks), n, int(block_size), ctypes.byref(dims), _ptr(host_k), _ptr(host_v))
+    if kv_scales is not None:
+        _check_host(n, ("host_scales", host_scales, kv_scales))
+        _check(getattr(library(), quant_name)(_ptr(k_pages), _ptr(v_pages), _ptr(kv_scales), *where,
+                                              _ptr(host_scales), _stream(stream)), quant_name)
+    else:
+        _require(host_scales is None, "host_scales without kv_scales")
+        _check(getattr(library(), name)(_ptr(k_pages), _ptr(v_pages), *where, _stream(stream)), name)
 
 
-def kv_restore(k_pages, v_pages, blocks, block_size, host_k, host_v, stream=None) -> None:
-    """Scatter pinned host tensors [n, bs, Hkv, D] into blocks of both pools (cb_kv_restore)."""
-    dims = _pool_dims(k_pages, v_pages, block_size)
-    _check_ids("blocks", blocks)
-    n = blocks.numel()
-    for name, h in (("host_k", host_k), ("host_v", host_v)):
-        _require(h.is_pinned() and h.is_contiguous() and h.numel() * h.element_size()
-                 >= n * k_pages[0].numel() * 2, f"{name} must be pinned, contiguous, large enough")
-    _check(library().cb_kv_restore(_ptr(k_pages), _ptr(v_pages), _ptr(blocks), n,
-                                   int(block_size), ctypes.byref(dims), _ptr(host_k),
-                                   _ptr(host_v), _stream(stream)), "cb_kv_restore")
+def kv_offload(k_pages, v_pages, blocks, block_size, host_k, host_v, stream=None, kv_scales=None,
+               host_scales=None) -> None:
+    """Gather blocks of both pools into pinned host tensors [n, bs, Hkv, D] (cb_kv_offload); a quantised
+    cache's with kv_scales into host_scales, uint8 [n, bs, Hkv, 2] (cb_quant_offload)."""
+    _host_move("cb_kv_offload", "cb_quant_offload", k_pages, v_pages, blocks, block_size, host_k, host_v,
+               stream, kv_scales, host_scales)
+
+
+def kv_restore(k_pages, v_pages, blocks, block_size, host_k, host_v, stream=None, kv_scales=None,
+               host_scales=None) -> None:
+    """Scatter pinned host tensors [n, bs, Hkv, D] into blocks of both pools (cb_kv_restore); a quantised
+    cache's with host_scales into kv_scales (cb_quant_restore)."""
+    _host_move("cb_kv_restore", "cb_quant_restore", k_pages, v_pages, blocks, block_size, host_k, host_v,
+               stream, kv_scales, host_scales)
 
 
 def kv_append(k_new, v_new, k_pages, v_pages, block_table, cu_seqlens_q, kv_lens, block_size,

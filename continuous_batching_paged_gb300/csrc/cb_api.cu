@@ -861,10 +861,11 @@ cb_status cb_ragged_paged_attention(const void* q, const void* k_pages, const vo
                                       dims, nullptr, stream);
 }
 
-// Shared host half of the three block-move entry points.
+// Shared host half of the block-move entry points (quant: of the quantised cache, with its scales ps and pd).
 static cb_status block_move(const void* pk, const void* pv, void* dk, void* dv,
                             const int32_t* src_idx, const int32_t* dst_idx, int32_t n,
-                            int32_t block_size, const cb_dims* dims, int mode, void* stream) {
+                            int32_t block_size, const cb_dims* dims, int mode, void* stream,
+                            bool quant = false, const void* ps = nullptr, void* pd = nullptr) {
   t_last_error.clear();
   if (dims == nullptr) return fail(CB_ERR_INVALID_ARG, "dims is NULL");
   if (block_size < 4)
@@ -878,8 +879,11 @@ static cb_status block_move(const void* pk, const void* pv, void* dk, void* dv,
   if (!pk || !pv || !dk || !dv || (mode != cb::kMoveRestore && !src_idx) ||
       (mode != cb::kMoveOffload && !dst_idx))
     return fail(CB_ERR_INVALID_ARG, "null pointer argument");
-  if (!aligned16(pk) || !aligned16(pv) || !aligned16(dk) || !aligned16(dv))
+  if (quant && (!ps || !pd)) return fail(CB_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned16(pk) || !aligned16(pv) || !aligned16(dk) || !aligned16(dv) || !aligned16(ps) || !aligned16(pd))
     return fail(CB_ERR_INVALID_ARG, "pools and host buffers must be 16-byte aligned");
+  if (quant && (long long)block_size * dims->num_kv_heads >= (1LL << 30))
+    return fail(CB_ERR_UNSUPPORTED, "block_size * num_kv_heads must be < 2^30");
   DeviceState* ds = nullptr;
   cb_status st = device_state(&ds);
   if (st != CB_OK) return st;
@@ -893,8 +897,11 @@ static cb_status block_move(const void* pk, const void* pv, void* dk, void* dv,
   a.n = n;
   a.P = dims->num_pages;
   a.mode = mode;
-  a.block_bytes = (long long)block_size * dims->num_kv_heads * dims->head_dim * 2;
+  a.block_bytes = (long long)block_size * dims->num_kv_heads * dims->head_dim * (quant ? 1 : 2);
   a.err = ds->err;
+  a.src_scales = static_cast<const char*>(ps);
+  a.dst_scales = static_cast<char*>(pd);
+  a.scale_bytes = quant ? block_size * dims->num_kv_heads * 2 : 0;
   cudaError_t e = cb::launch_block_move(a, ds->sm_count, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "block move launch");
   return CB_OK;
@@ -918,6 +925,28 @@ cb_status cb_kv_restore(void* k_pages, void* v_pages, const int32_t* blocks, int
                         const void* host_v, void* stream) {
   return block_move(host_k, host_v, k_pages, v_pages, nullptr, blocks, n, block_size, dims,
                     cb::kMoveRestore, stream);
+}
+
+cb_status cb_quant_copy_blocks(void* k_pages, void* v_pages, void* kv_scales, const int32_t* src,
+                               const int32_t* dst, int32_t n, int32_t block_size,
+                               const cb_dims* dims, void* stream) {
+  return block_move(k_pages, v_pages, k_pages, v_pages, src, dst, n, block_size, dims,
+                    cb::kMoveCopy, stream, true, kv_scales, kv_scales);
+}
+
+cb_status cb_quant_offload(const void* k_pages, const void* v_pages, const void* kv_scales,
+                           const int32_t* blocks, int32_t n, int32_t block_size,
+                           const cb_dims* dims, void* host_k, void* host_v, void* host_scales,
+                           void* stream) {
+  return block_move(k_pages, v_pages, host_k, host_v, blocks, nullptr, n, block_size, dims,
+                    cb::kMoveOffload, stream, true, kv_scales, host_scales);
+}
+
+cb_status cb_quant_restore(void* k_pages, void* v_pages, void* kv_scales, const int32_t* blocks,
+                           int32_t n, int32_t block_size, const cb_dims* dims, const void* host_k,
+                           const void* host_v, const void* host_scales, void* stream) {
+  return block_move(host_k, host_v, k_pages, v_pages, nullptr, blocks, n, block_size, dims,
+                    cb::kMoveRestore, stream, true, host_scales, kv_scales);
 }
 
 cb_status cb_selftest_wait_timeout(int32_t limit_us, unsigned long long* waited_ns, void* stream) {

@@ -140,6 +140,10 @@ struct BlockMoveArgs {
   int n, P, mode;
   long long block_bytes;
   uint32_t* err;
+  // the quantised cache's scales, which move with the codes (scale_bytes per block; 0: none)
+  const char* src_scales;
+  char* dst_scales;
+  int scale_bytes;
 };
 
 // Id of the CUDA context the calling thread's next launch goes to (set by every API entry

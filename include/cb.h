@@ -493,6 +493,22 @@ cb_status cb_kv_restore(void* k_pages, void* v_pages, const int32_t* blocks, int
                         const void* host_v, void* stream);
 
 /*
+ * The block moves of a quantised cache: as the three above, with the scales beside the codes.  The
+ * host buffers: host_k and host_v e4m3 [n, bs, Hkv, D], host_scales uint8 [n, bs, Hkv, 2], each
+ * 16-byte aligned.
+ */
+cb_status cb_quant_copy_blocks(void* k_pages, void* v_pages, void* kv_scales, const int32_t* src,
+                               const int32_t* dst, int32_t n, int32_t block_size,
+                               const cb_dims* dims, void* stream);
+cb_status cb_quant_offload(const void* k_pages, const void* v_pages, const void* kv_scales,
+                           const int32_t* blocks, int32_t n, int32_t block_size,
+                           const cb_dims* dims, void* host_k, void* host_v, void* host_scales,
+                           void* stream);
+cb_status cb_quant_restore(void* k_pages, void* v_pages, void* kv_scales, const int32_t* blocks,
+                           int32_t n, int32_t block_size, const cb_dims* dims, const void* host_k,
+                           const void* host_v, const void* host_scales, void* stream);
+
+/*
  * cb_get_device_error -- synchronise `stream`, then read and clear the current device's error
  * word.  Returns CB_OK, CB_ERR_OUT_OF_RANGE, CB_ERR_TIMEOUT (reported first when both were
  * seen) or CB_ERR_CUDA if the synchronisation itself failed.
