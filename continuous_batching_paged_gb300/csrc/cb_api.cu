@@ -769,6 +769,11 @@ cb_status cb_quant_gather(const void* k_pages, const void* v_pages, const void* 
   if ((st = check_scales(kv_scales)) != CB_OK) return st;
   const long long n = (long long)dims->num_tokens * dims->num_kv_heads * dims->head_dim;
   if (overlap(k_out, n, v_out, n)) return fail(CB_ERR_INVALID_ARG, "k_out overlaps v_out");
+  const long long rows = (long long)dims->num_pages * block_size * dims->num_kv_heads;  // of the pools
+  for (const void* o : {k_out, v_out})
+    if (overlap(o, n, k_pages, rows * dims->head_dim / 2) || overlap(o, n, v_pages, rows * dims->head_dim / 2) ||
+        overlap(o, n, kv_scales, rows))
+      return fail(CB_ERR_INVALID_ARG, "k_out or v_out overlaps the cache");
   DeviceState* ds = nullptr;
   st = device_state(&ds);
   if (st != CB_OK) return st;

@@ -382,8 +382,8 @@ cb_status cb_quant_append(const void* q, const void* k_new, const void* v_new, v
  * [num_tokens, Hkv, D]) receives key (value) key_starts[s] + i of sequence s; key_starts NULL: from
  * key 0 on.  cu_seqlens_k int32 [S+1] as cu_seqlens_q; rows from cu_seqlens_k[S] on are left as they
  * are.  dims: num_tokens is the number of output rows, num_q_heads is ignored but for being a valid
- * number.  k_out and v_out must not overlap.  Device errors: as cb_kv_append (a negative start, a
- * position beyond the table, a bad block id); the row is skipped.
+ * number.  k_out and v_out must overlap neither each other nor the cache.  Device errors: as
+ * cb_kv_append (a negative start, a position beyond the table, a bad block id); the row is skipped.
  */
 cb_status cb_quant_gather(const void* k_pages, const void* v_pages, const void* kv_scales,
                           const int32_t* block_table, const int32_t* cu_seqlens_k,
