@@ -57,7 +57,7 @@ cudaError_t launch_quant_gather(GatherArgs g, int sm_count, cudaStream_t stream)
   while (g.rows < 32 && (long long)g.rows * 2 * sm_count * 32 <= g.T && g.rows * 2 * per_row <= 512)
     g.rows *= 2;
   const int per_block = kGatherThreads / 32 * g.rows;
-  const unsigned blocks = (unsigned)((g.T + per_block - 1) / per_block);
+  const unsigned blocks = (unsigned)(((long long)g.T + per_block - 1) / per_block);
   return launch_dependent(quant_gather_kernel, blocks, kGatherThreads, 0, stream, g);
 }
 
