@@ -110,7 +110,8 @@ static_assert(sizeof(PfItemSeen) <= 128, "a decoded item fits its shared-memory 
 // The chunk pass over the quantised cache: warps 12-15 make the K and V tiles (quant_convert), warp 0
 // finds their rows.
 constexpr int kQuantPrefillThreads = 512;
-// Registers of the issuing, softmax and converting warps: what each role needs without spills.
+// Registers of the issuing, softmax and converting warps: all that the launch has.  With the decode role's 176
+// and 80 a few values are spilled: 16 to 56 bytes a thread, 48 to 76 with changed scores (-Xptxas -v).
 constexpr int kRegsQuantIssue = 96, kRegsQuantSoftmax = 176, kRegsQuantConvert = 64;
 static_assert(kRegsQuantIssue + 2 * kRegsQuantSoftmax + kRegsQuantConvert <= 4 * 128,
               "register split exceeds the launch");
@@ -128,8 +129,8 @@ __device__ __forceinline__ int row_place(int key) {
   constexpr int NR = D / 16, kStep = kChunkKeys / NR;
   return key % kStep * NR + key / kStep;
 }
-// an item's first and last tile; no more tiles; some scale takes two factors
-constexpr int kRowFirst = 1, kRowLast = 2, kRowEnd = 4, kRowMore = 8;
+// an item's last tile; no more tiles; some scale takes two factors
+constexpr int kRowLast = 1, kRowEnd = 2, kRowMore = 4;
 template <int D>
 struct QuantPrefillSmem {
   static constexpr int kRowsPerThread = D / 16;  // of a tile (quant_convert)

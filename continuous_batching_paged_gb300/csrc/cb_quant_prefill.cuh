@@ -152,7 +152,7 @@ __device__ __forceinline__ void quant_rows(const AttnArgs& a, const QuantArgs& q
       }
       more = __any_sync(0xffffffffu, more);
       if (lane == 0) {
-        rs.flags = (j == it.j0 ? kRowFirst : 0) | (j == it.nt_all - 1 ? kRowLast : 0) | (more ? kRowMore : 0);
+        rs.flags = (j == it.nt_all - 1 ? kRowLast : 0) | (more ? kRowMore : 0);
       }
       __syncwarp();
       if (lane == 0) {
