@@ -534,14 +534,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : CB_R8(0), CB_R8(8), CB_R8(16), CB_R8(24)
       : "r"(taddr));
 }
-// 16 columns -> r[0..15].
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15}, [%16];"
-      : CB_R8(0), CB_R8(8)
-      : "r"(taddr));
-}
 // r[0..31] -> 32 consecutive 32-bit TMEM columns of this thread's lane.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -550,15 +542,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
           taddr),
       CB_W8(0), CB_W8(8), CB_W8(16), CB_W8(24)
       : "memory");
-}
-
-// 8 columns -> r[0..7], and back.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : CB_R8(0) : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), CB_W8(0)
-               : "memory");
 }
 
 // Shared-memory matrix descriptor of the 5th-generation tensor core: start address, leading

@@ -111,7 +111,7 @@ static_assert(sizeof(PfItemSeen) <= 128, "a decoded item fits its shared-memory 
 // finds their rows.
 constexpr int kQuantPrefillThreads = 512;
 // Registers of the issuing, softmax and converting warps: all that the launch has.  With the decode role's 176
-// and 80 a few values are spilled: 16 to 56 bytes a thread, 48 to 76 with changed scores (-Xptxas -v).
+// and 80 a few values are spilled: 16 to 56 bytes a thread, 36 to 80 with changed scores (-Xptxas -v).
 constexpr int kRegsQuantIssue = 96, kRegsQuantSoftmax = 176, kRegsQuantConvert = 64;
 static_assert(kRegsQuantIssue + 2 * kRegsQuantSoftmax + kRegsQuantConvert <= 4 * 128,
               "register split exceeds the launch");
@@ -593,18 +593,6 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
         if (!mbar_wait(bar(SM::bSFull + t), tt & 1)) { report(a.err, kErrTimeout); ok = false; break; }
         __syncwarp();
         tc_fence_after();
-        if (kMod && sc.cap_in > 0.f && sc.near_in != 1.f) {  // (rare: S in TMEM, times near_in)
-#pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 8) {
-            uint32_t x[8];
-            tmem_ld8(t_lane + s_col + c0, x);
-            tc_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 8; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * sc.near_in);
-            tmem_st8(t_lane + s_col + c0, x);
-          }
-          tc_wait_st();
-        }
         uint32_t sr[128];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(t_lane + s_col + i * 32, sr + i * 32);
@@ -619,28 +607,39 @@ __device__ __forceinline__ void prefill_cta(const AttnArgs& a, const CUtensorMap
             uint64_t near[5];
 #pragma unroll
             for (int i = 0; i < 5; ++i) near[i] = f2_pack(sc.near[i], sc.near[i]);
+            // Both forms are per score, so that a row's bits depend on nothing beside it.  Which loop a warp takes
+            // does depend on all that is in its tile, masked keys, keys' rows that an earlier item has left and
+            // other sequences' queries among it, but the bits do not: the loop of both forms, which is small (S
+            // goes from TMEM to TMEM), has the other's arithmetic for the scores that are near.
+            if (__all_sync(0xffffffffu, big <= sc.near_max) && sc.near_in == 1.f) {
 #pragma unroll
-            for (int c = 0; c < 128; c += 2) {
-              float x0, x1;
-              f2_unpack(cap_near(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), near), x0, x1);
-              sr[c] = __float_as_uint(x0);
-              sr[c + 1] = __float_as_uint(x1);
-            }
-            // Then the scores beyond its range, S being still in TMEM.  Both forms are per score, so that a row's
-            // bits depend on nothing beside it (the choice between them for a warp's tile as a whole looked at
-            // masked keys, at keys' rows that an earlier item had left and at other sequences' queries too).
-            if (!__all_sync(0xffffffffu, big <= sc.near_max)) {
-#pragma unroll
-              for (int c0 = 0; c0 < 128; c0 += 16) {
-                uint32_t raw[16];
-                tmem_ld16(t_lane + s_col + c0, raw);
+              for (int c = 0; c < 128; c += 2) {
+                float x0, x1;
+                f2_unpack(cap_near(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), near), x0, x1);
+                sr[c] = __float_as_uint(x0);
+                sr[c + 1] = __float_as_uint(x1);
+              }
+            } else {
+#pragma unroll 1
+              for (int c0 = 0; c0 < 128; c0 += 32) {
+                uint32_t x[32];
+                tmem_ld32(t_lane + s_col + c0, x);
                 tc_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                  const float s = __uint_as_float(raw[c]), far = cap_far(s, sc);
-                  if (!(fabsf(s) <= sc.near_max)) sr[c0 + c] = __float_as_uint(far);
+                for (int c = 0; c < 32; c += 2) {
+                  const float s0 = __uint_as_float(x[c]) * sc.near_in, s1 = __uint_as_float(x[c + 1]) * sc.near_in;
+                  const float f0 = cap_far(s0, sc), f1 = cap_far(s1, sc);
+                  float n0, n1;
+                  f2_unpack(cap_near(f2_pack(s0, s1), near), n0, n1);
+                  x[c] = __float_as_uint(fabsf(s0) <= sc.near_max ? n0 : f0);
+                  x[c + 1] = __float_as_uint(fabsf(s1) <= sc.near_max ? n1 : f1);
                 }
+                tmem_st32(t_lane + s_col + c0, x);
               }
+              tc_wait_st();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) tmem_ld32(t_lane + s_col + i * 32, sr + i * 32);
+              tc_wait_ld();
             }
           }
           if (sc.slopes != nullptr) {

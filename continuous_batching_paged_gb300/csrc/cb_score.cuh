@@ -27,13 +27,14 @@ __device__ __forceinline__ float cap_far(float s, const ScoreArgs& sc) {
 // The same where |u| <= 0.6, for two scores, without special functions: tanh(u) / u is a polynomial in u^2, here
 // the interpolation of degree 4 at Chebyshev's points of [0, 0.36], off by 6e-8 of itself.  The host multiplies
 // scale log2(e) and the powers of scale / cap into the coefficients (ScoreArgs::near), so it takes six
-// instructions on pairs of the raw products s.  Both passes compute it for all scores, and cap_far for those
-// beyond its range in tiles that have any.
+// instructions on pairs of the raw products s.  Tiles of a warp that have scores beyond its range take both forms
+// for all scores.
 // (8 chunks of 512 tokens on up to 4096 keys, 32 query, 8 KV heads of 128, bf16 cache, the whole call: with slopes
-// instead 206 us, capped at 50 238, at 2, where a quarter of the scores is beyond, 344; with one form for a
-// warp's tile as a whole, by its largest product, 239 and 282, but then a row's bits depend on what stands beside
-// it.  A shorter polynomial for smaller scores beside this one, degree 2 to 0.3 caps, made the pass 4 % faster
-// where it applied and 15 % slower where it did not.  Over the 8-bit cache, where the decode pass is bound by its
+// instead 200 us, capped at 50 233, at 2, where a quarter of the scores is beyond, 303, with the scores beyond
+// replaced in the unrolled registers instead of the small loop over TMEM 238 and 344.  With one form for a warp's
+// tile as a whole, by its largest product, 240 and 283, but then a row's bits depend on what stands beside it.  A
+// shorter polynomial for smaller scores beside this one, degree 2 to 0.3 caps, made the pass 4 % faster where it
+// applied and 15 % slower where it did not.  Over the 8-bit cache, where the decode pass is bound by its
 // instructions, 100 decodes of head_dim 64 take 73 us, capped at 50 82, at 2 91.)
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t d;
