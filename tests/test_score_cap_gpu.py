@@ -47,10 +47,11 @@ class Cache:
 
 def check_capped(c, softcap):
     """Every row against the oracle.  A score x is off by 2^-20 |x| by the cap (tanh by a polynomial or from
-    exp2 and a reciprocal: 2^-21 of itself, and the roundings of its factors), and by its products' rounding: D of them summed in fp32, 2^-24 each of the sum of |q_d k_d|, which the cap, of slope 1
-    at most, does not enlarge.  The quantised decode pass has its query row in fp16, off by 2^-25 of its largest
-    power of two.  That moves a probability by e (and an exponential's 2^-21) and the output by 2 e times the
-    weighted |v|; a probability is rounded once to p_step, the result to bf16."""
+    exp2 and a reciprocal: 2^-21 of itself, and the roundings of its factors), and by its products' rounding: D of
+    them summed in fp32, 2^-24 each of the sum of |q_d k_d|, times the slope that the cap has there.  The quantised
+    decode pass has its query row in fp16, off by 2^-25 of its largest power of two.  That moves a probability by e
+    (and an exponential's 2^-21) and the output by 2 e times the weighted |v|; a probability is rounded once to
+    p_step, the result to bf16."""
     b = c.b
     out, lse = c.attend(softcap=softcap)
     o, l, q = f64(out), f64(lse), opa.bf16_bits_to_f64(b.q)
@@ -62,12 +63,14 @@ def check_capped(c, softcap):
             continue
         K, V = c.cached(s)
         ref, ref_lse, size = oq.scored_attention(q[c0:c1], K, V, kv - n, b.scale, softcap)
-        Kr = np.repeat(np.abs(K), g, axis=1)
-        mag = np.einsum("nhd,khd->nhk", np.abs(q[c0:c1]), Kr).max(-1) * b.scale
-        x = np.abs(np.einsum("nhd,khd->nhk", q[c0:c1], np.repeat(K, g, axis=1))).max(-1) * b.scale
-        x = softcap * np.tanh(x / softcap)
-        fp16 = b.scale * np.abs(q[c0:c1]).max(-1) * Kr.sum(-1).max(0)[None] * 2.0 ** -25 if c.quant else 0.0
-        e = 2.0 ** -20 * x + 2.0 ** -24 * (b.head_dim + 8) * mag + fp16 + 2.0 ** -21
+        Kr = np.repeat(K, g, axis=1)
+        mag = np.einsum("nhd,khd->nhk", np.abs(q[c0:c1]), np.abs(Kr)) * b.scale
+        x = np.abs(np.einsum("nhd,khd->nhk", q[c0:c1], Kr)) * b.scale
+        off = 2.0 ** -24 * (b.head_dim + 8) * mag
+        if c.quant:
+            off = off + b.scale * np.abs(q[c0:c1]).max(-1)[..., None] * np.abs(Kr).sum(-1).T[None] * 2.0 ** -25
+        slope = np.cosh(np.minimum(np.maximum(x - off, 0.0) / softcap, 300.0)) ** -2.0  # the steepest within `off`
+        e = 2.0 ** -21 + (2.0 ** -20 * softcap * np.tanh(x / softcap) + off * slope).max(-1)
         p_step = P16 if c.quant and n == 1 else P8
         assert np.isfinite(o[c0:c1]).all()
         tol = 2.0 ** -8 * np.abs(ref) + (p_step + 2 * e)[..., None] * size * (1 + 2.0 ** -8) + 1e-30
@@ -167,3 +170,34 @@ def test_caps_that_fp32_does_not_hold(cuda_lib):
         with pytest.raises(ValueError, match="softcap"):
             c.attend(softcap=-1e-50)
         c.attend(softcap=0)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("cap", [3.0, 1e7])
+def test_products_beyond_fp32_and_keys_that_are_nan(cuda_lib, cap, quant):
+    """Products that overflow are capped like any large one; a key that is NaN makes the rows NaN that see it, and
+    no others.  (Keys are multiples of one unit vector, so that no sum of infinities is NaN.)"""
+    b = workloads.build_batch([1, 70, 1], [90, 200, 40], 4, 2, 64, 16, seed=698)
+    q = np.zeros(b.q.shape, dtype=np.float32)
+    q[..., 5] = np.where(np.arange(q.shape[0]) % 2 == 0, 2.0 ** 100, 2.0 ** -3)[:, None]
+    pool = np.zeros(b.k_pages.shape, dtype=np.float32)
+    rng = np.random.default_rng(1)
+    pool[..., 5] = rng.choice([-1.0, 1.0, 0.25], pool.shape[:-1]) * np.float32(2.0 ** 30)
+    new = np.zeros(b.k_new.shape, dtype=np.float32)
+    new[..., 5] = np.float32(2.0 ** 30)
+    b = workloads.Batch(**{**b.__dict__, "q": workloads.f32_to_bf16_bits(q), "k_new": workloads.f32_to_bf16_bits(new),
+                           "k_pages": workloads.f32_to_bf16_bits(pool)})
+    c = Cache(b, quant)
+    check_capped(c, cap)
+    want, _ = c.attend(softcap=cap)
+    s, p = 1, 160  # a key in the chunk: queries 30 .. 69 of it see it
+    where = int(b.block_table[s, p // 16]), p % 16
+    if quant:
+        c.d.dk.view(torch.uint8)[where] = 0x7F
+        c.d.dsc[where + (slice(None), 0)] = 255
+    else:
+        c.d.k_pages[where] = float("nan")
+    got, _ = c.attend(softcap=cap)
+    seen = torch.zeros(72, dtype=torch.bool, device="cuda")
+    seen[1 + 30:1 + 70] = True
+    assert torch.isnan(got[seen]).all() and torch.equal(got[~seen].view(torch.int16), want[~seen].view(torch.int16))
